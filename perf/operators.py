@@ -23,36 +23,36 @@ MAX_CODE, MAX_NV_SCALE = 6.0, 448.0     # largest 4-bit value, largest e4m3 scal
 def listed():
     return [
         # one generated token: a row of a GPT-2-width table and its position's row, where latency is all
-        {"name": "lookup, one token", "op": "lookup", "n": 1, "vocab": 50257, "dim": 1280, "table": "f32", "out": "bf16",
+        {"name": "lookup one token", "op": "lookup", "n": 1, "vocab": 50257, "dim": 1280, "table": "f32", "out": "bf16",
          "scale": 1.0, "positions": 1024, "p": 0.0},
         # a training batch into the Llama-style 8B table, scaled by sqrt(dim), with embedding dropout
-        {"name": "lookup, 8B batch", "op": "lookup", "n": 16384, "vocab": 128256, "dim": 4096, "table": "f32", "out": "bf16",
+        {"name": "lookup 8B batch", "op": "lookup", "n": 16384, "vocab": 128256, "dim": 4096, "table": "f32", "out": "bf16",
          "scale": 64.0, "positions": 0, "p": 0.1},
         # the embedding gradient of eight 1024-token sequences, under the embedding dropout
-        {"name": "grad, GPT-2 batch", "op": "grad", "n": 8192, "vocab": 50257, "dim": 1280, "dout": "bf16", "scale": 1.0,
+        {"name": "grad GPT-2 batch", "op": "grad", "n": 8192, "vocab": 50257, "dim": 1280, "dout": "bf16", "scale": 1.0,
          "p": 0.1, "padding": 0.0, "accumulate": False},
         # the gradient of the 8B table: 2.1 GB written for the AdamW tail
-        {"name": "grad, 8B batch", "op": "grad", "n": 16384, "vocab": 128256, "dim": 4096, "dout": "bf16", "scale": 64.0,
+        {"name": "grad 8B batch", "op": "grad", "n": 16384, "vocab": 128256, "dim": 4096, "dout": "bf16", "scale": 64.0,
          "p": 0.0, "padding": 0.0, "accumulate": False},
         # gradient accumulation with padded sequences, few rows that many tokens share, an odd width
-        {"name": "grad, accumulated, odd", "op": "grad", "n": 3001, "vocab": 1003, "dim": 257, "dout": "f32", "scale": 1.0,
+        {"name": "grad accumulated odd", "op": "grad", "n": 3001, "vocab": 1003, "dim": 257, "dout": "f32", "scale": 1.0,
          "p": 0.25, "padding": 0.3, "accumulate": True},
         # residual dropout of an 8B-width activation
-        {"name": "dropout, residual", "op": "dropout", "n": 16384 * 4096, "dtype": "bf16", "residual": True, "p": 0.1},
+        {"name": "dropout residual", "op": "dropout", "n": 16384 * 4096, "dtype": "bf16", "residual": True, "p": 0.1},
         # the backward pass of a small odd tensor
-        {"name": "dropout, odd", "op": "dropout", "n": 1023 * 257, "dtype": "f32", "residual": False, "p": 0.5},
+        {"name": "dropout odd", "op": "dropout", "n": 1023 * 257, "dtype": "f32", "residual": False, "p": 0.5},
         # an 8B feed-forward weight after its update, in the orientations of the forward and the backward product
-        {"name": "quantize, weight mx", "op": "quantize", "rows": 14336, "cols": 4096, "dtype": "f32", "format": "mx",
+        {"name": "quantize weight mx", "op": "quantize", "rows": 14336, "cols": 4096, "dtype": "f32", "format": "mx",
          "stochastic": False},
         # an output gradient, rounded stochastically
-        {"name": "quantize, gradient nv", "op": "quantize", "rows": 4096, "cols": 5120, "dtype": "bf16", "format": "nv",
+        {"name": "quantize gradient nv", "op": "quantize", "rows": 4096, "cols": 5120, "dtype": "bf16", "format": "nv",
          "stochastic": True},
         # one token through an 8B feed-forward weight
-        {"name": "product, one token nv", "op": "product", "m": 1, "n": 14336, "k": 4096, "format": "nv"},
+        {"name": "product one token nv", "op": "product", "m": 1, "n": 14336, "k": 4096, "format": "nv"},
         # a batch through the same
-        {"name": "product, 8B batch mx", "op": "product", "m": 8192, "n": 14336, "k": 4096, "format": "mx"},
+        {"name": "product 8B batch mx", "op": "product", "m": 8192, "n": 14336, "k": 4096, "format": "mx"},
         # forward and backward of a GPT-2 Large feed-forward weight: the output, and the gradients of input and weight
-        {"name": "linear, GPT-2 step nv", "op": "linear", "tokens": 8192, "cols": 1280, "rows": 5120, "format": "nv"},
+        {"name": "linear GPT-2 step nv", "op": "linear", "tokens": 8192, "cols": 1280, "rows": 5120, "format": "nv"},
     ]
 
 
