@@ -49,7 +49,8 @@ enum mo_status {
   MO_ERR_CUDA = -7,              /* a CUDA runtime call failed; see mo_last_cuda_error() */
   MO_ERR_DEVICE_TIMEOUT = -8,    /* a bounded device-side wait expired (see mo_last_device_error) */
   MO_ERR_UNSUPPORTED_DEVICE = -9, /* the current device is not sm_103 */
-  MO_ERR_SCRATCH_LIMIT = -10      /* muon_owner_step_noalloc: table too large for the built-in scratch */
+  MO_ERR_SCRATCH_LIMIT = -10,     /* muon_owner_step_noalloc: table too large for the built-in scratch */
+  MO_ERR_BAD_TOKEN = -11          /* a token index outside the embedding table (see mo_last_device_error) */
 };
 
 /* One 2D matrix of an owner's shape table ("MatrixFSDP", section 4.1: one
@@ -275,9 +276,80 @@ size_t mo_rmnp_colcut_workspace_bytes(const mo_matrix* shards, int32_t n);
 int rmnp_colcut_step(const mo_matrix* shards, const int32_t* group, const float* scales, int32_t n,
                      const mo_rmnp_params* params, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---- training-step operators around the optimizer (no counterpart on the
+ * pages): what makes the gradients the optimizers read and consumes the
+ * weights they write. Activations and tables are fp32 or bf16, dense
+ * row-major with 16-byte aligned bases; arithmetic is fp32, rounded once. */
+
+enum mo_dtype { MO_F32 = 0, MO_BF16 = 1 };
+
+/* Counter-based random numbers (Philox4x32-10): element i of a tensor takes
+ * the 16-bit number i % 8 (low half of each word first) of the call with
+ * counter (i / 8, offset) under the key `seed`. A caller advances `offset`
+ * from step to step and from layer to layer. *d_offset (device memory, 8-byte
+ * aligned, may be NULL) is added to `offset` when the kernel runs, so a
+ * captured step can advance it between replays. */
+typedef struct {
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* d_offset;
+} mo_random;
+
+/* Dropout with probability p in [0, 1], in steps of 2^-16: with
+ * T = round(65536 p), an element is kept, times 65536 / (65536 - T), where its
+ * number is at least T, and becomes 0 elsewhere, whatever its value. The mask
+ * is never stored: the backward pass is given the same seed and offset and
+ * draws it again. */
+typedef struct {
+  float p;
+  mo_random random;
+} mo_dropout;
+
+/* Token indexes: int32 or int64 (bits 32 or 64), n of them (up to 2^30).
+ * padding_idx: the index whose row gets no gradient, or -1. An index outside
+ * the table is reported through mo_last_device_error (MO_ERR_BAD_TOKEN); its
+ * embedding reads as zeros and it gets no gradient. */
+typedef struct {
+  const void* ids;
+  int64_t n;
+  int64_t padding_idx;
+  int32_t bits;
+} mo_tokens;
+
+/* y = drop(x), or drop(x) + residual with a residual. x, residual and y have n
+ * elements of `dtype`; y may be x or residual itself, but not overlap either
+ * otherwise. With the same `dropout` and dy for x it is the backward pass. */
+int dropout_apply(const void* x, const void* residual, void* y, int64_t n, int32_t dtype, const mo_dropout* dropout,
+                  cudaStream_t stream);
+
+/* out[t] = drop(scale table[ids[t]] + add[t mod add_rows]) for every token.
+ * table [vocab, dim] and add [add_rows, dim] (learned positions of sequences
+ * of add_rows tokens, or NULL) have table_dtype, out [n, dim] has out_dtype.
+ * dropout may be NULL; its element index is that of out. vocab up to 2^31 - 2,
+ * dim up to 2^22. */
+int embed_lookup(const void* table, int32_t table_dtype, int64_t vocab, int64_t dim, const mo_tokens* tokens, float scale,
+                 const void* add, int64_t add_rows, const mo_dropout* dropout, void* out, int32_t out_dtype,
+                 cudaStream_t stream);
+
+/* Gradient of embed_lookup in its table, as the fp32 g that adamw_tail_step
+ * reads: grad[v] = scale times the sum over the tokens t with ids[t] = v of
+ * dout[t] under the forward pass's dropout; rows no token names become 0. With
+ * accumulate = 1 the sums are added to grad and other rows are left alone.
+ * (The gradient in `add` is embed_grad with the positions as tokens and
+ * scale 1.) The tokens are sorted and each row's sum is taken in position
+ * order, split and joined at fixed places: results do not depend on
+ * scheduling. ws: device scratch of mo_embed_grad_workspace_bytes() bytes
+ * (host-only computation; 0 for invalid sizes), 256-byte aligned. Two
+ * launches. */
+size_t mo_embed_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
+int embed_grad(const void* dout, int32_t dout_dtype, const mo_tokens* tokens, int64_t vocab, int64_t dim, float scale,
+               const mo_dropout* dropout, float* grad, int32_t accumulate, void* ws, size_t ws_bytes,
+               cudaStream_t stream);
+
 /* Synchronises `stream`, then returns and clears the device-side status word:
- * MO_OK, or MO_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel expired
- * (the kernel then skipped its remaining work and released its resources). */
+ * MO_OK, MO_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel expired
+ * (the kernel then skipped its remaining work and released its resources), or
+ * MO_ERR_BAD_TOKEN if an embedding call met an index outside its table. */
 int mo_last_device_error(cudaStream_t stream);
 
 /* cudaError_t of the most recent MO_ERR_CUDA on this thread (0 if none). */

@@ -37,6 +37,8 @@ __all__ = [
     "mo_status_string", "mo_selftest_bounded_wait", "mo_muon_tile_schedule", "MuonTable",
     "TailTable", "RmnpTable", "muon_owner_step_noalloc", "mo_static_scratch_bytes", "mo_plan_owners",
     "rmnp_colcut_step", "muon_owner_step_coverage",
+    "Random", "Dropout", "dropout_apply", "embed_lookup", "embed_grad", "embed_grad_workspace",
+    "mo_embed_grad_workspace_bytes",
 ]
 
 MO_OK = 0
@@ -147,6 +149,10 @@ def load_library() -> ctypes.CDLL:
         "mo_muon_plan_step": (ctypes.c_int, [P, P]),
         "mo_muon_plan_lr_ptr": (P, [P]),
         "mo_muon_plan_destroy": (ctypes.c_int, [P]),
+        "dropout_apply": (ctypes.c_int, [P, P, P, I64, I32, P, P]),
+        "embed_lookup": (ctypes.c_int, [P, I32, I64, I64, P, ctypes.c_float, P, I64, P, P, I32, P]),
+        "mo_embed_grad_workspace_bytes": (SZ, [I64, I64, I64]),
+        "embed_grad": (ctypes.c_int, [P, I32, P, I64, I64, ctypes.c_float, P, P, I32, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -471,3 +477,7 @@ def mo_plan_owners(roles: Sequence[Tuple[int, int, int]], world: int, strategy: 
                                          ctypes.cast(loads, ctypes.c_void_p), ctypes.byref(chosen)),
            "mo_plan_owners")
     return list(owners[:n]), list(loads[:world]), int(chosen.value)
+
+
+from .train_ops import (  # noqa: E402  (uses the binding above)
+    Dropout, Random, dropout_apply, embed_grad, embed_grad_workspace, embed_lookup, mo_embed_grad_workspace_bytes)

@@ -15,6 +15,7 @@
 #include "mo.h"
 #include "mo_internal.h"
 #include "plan.h"
+#include "train_kernels.h"
 
 namespace {
 
@@ -176,6 +177,17 @@ int insert_plan(PlanEntry* e, const mo_matrix* tbl, int32_t n, void* ws, bool wa
 }  // namespace
 
 namespace mo {
+
+int current_device(int* sms, int** status) {
+  DeviceInfo* d = nullptr;
+  const int st = device_info(&d);
+  if (st != MO_OK) return st;
+  *sms = d->sms;
+  *status = d->status;
+  return MO_OK;
+}
+
+int report_cuda(cudaError_t e) { return cuda_fail(e); }
 
 int enqueue_muon(const mo::MuonLayout& L, uint8_t* wsb, const mo_muon_params* prm, const float* lr_dev,
                  DeviceInfo* dev, cudaStream_t stream, cudaEvent_t ev_begin, cudaEvent_t ev_end,
@@ -696,6 +708,7 @@ const char* mo_status_string(int status) {
     case MO_ERR_DEVICE_TIMEOUT: return "bounded device-side wait expired";
     case MO_ERR_UNSUPPORTED_DEVICE: return "current device is not sm_103";
     case MO_ERR_SCRATCH_LIMIT: return "table needs more scratch than the built-in array holds (mo_static_scratch_bytes)";
+    case MO_ERR_BAD_TOKEN: return "token index outside the embedding table";
     default: return "unknown status";
   }
 }

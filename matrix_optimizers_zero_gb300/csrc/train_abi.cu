@@ -1,0 +1,217 @@
+// extern "C" entry points of the training-step operators around the
+// optimizer (include/mo.h): argument checks, workspace layout, launches. No
+// entry point allocates device memory or synchronises.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "mo.h"
+#include "train_kernels.h"
+
+namespace {
+
+using mo::report_cuda;
+
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxVocab = (int64_t(1) << 31) - 2;
+constexpr int64_t kMaxDim = int64_t(1) << 22;
+constexpr int64_t kMaxElems = int64_t(1) << 42;
+
+bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+bool dtype_ok(int32_t d) { return d == MO_F32 || d == MO_BF16; }
+size_t dtype_bytes(int32_t d) { return d == MO_BF16 ? 2 : 4; }
+
+int random_args(const mo_random& r, mo::RandomArgs* out) {
+  if (misaligned(r.d_offset, 8)) return MO_ERR_MISALIGNED;
+  out->seed = r.seed;
+  out->offset = r.offset;
+  out->offset_dev = r.d_offset;
+  return MO_OK;
+}
+
+int drop_args(const mo_dropout* d, mo::DropArgs* out) {
+  *out = mo::DropArgs();
+  if (d == nullptr) return MO_OK;
+  if (!(d->p >= 0.0f && d->p <= 1.0f)) return MO_ERR_BAD_PARAM;
+  const int st = random_args(d->random, &out->rnd);
+  if (st != MO_OK) return st;
+  out->threshold = uint32_t(std::lrint(65536.0 * double(d->p)));
+  out->factor = out->threshold < 65536u ? 65536.0f / float(65536u - out->threshold) : 0.0f;
+  return MO_OK;
+}
+
+int token_args(const mo_tokens* t, mo::TokenArgs* out) {
+  if (t == nullptr) return MO_ERR_NULL_POINTER;
+  if (t->n < 0 || t->n > kMaxTokens) return MO_ERR_BAD_SHAPE;
+  if (t->bits != 32 && t->bits != 64) return MO_ERR_BAD_PARAM;
+  if (t->n > 0 && t->ids == nullptr) return MO_ERR_NULL_POINTER;
+  if (misaligned(t->ids, uintptr_t(t->bits / 8))) return MO_ERR_MISALIGNED;
+  out->ids = t->ids;
+  out->n = t->n;
+  out->padding = t->padding_idx;
+  out->wide = t->bits == 64 ? 1 : 0;
+  return MO_OK;
+}
+
+size_t token_bytes(const mo_tokens* t) { return size_t(t->n) * size_t(t->bits / 8); }
+
+int table_shape(int64_t vocab, int64_t dim) {
+  return vocab <= 0 || vocab > kMaxVocab || dim <= 0 || dim > kMaxDim ? MO_ERR_BAD_SHAPE : MO_OK;
+}
+
+size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Workspace of embed_grad: two buffers of keys and of positions, the join's
+// counters, the sums of tokens that cross chunks.
+struct GradLayout {
+  size_t key[2], pos[2], counter, partial, bytes;
+  int64_t counters, dim_pad;
+};
+GradLayout grad_layout(int64_t n, int64_t dim) {
+  GradLayout L;
+  const mo::GradGrid g = mo::grad_grid(n, dim);
+  size_t at = 0;
+  for (int i = 0; i < 2; ++i) {
+    L.key[i] = at;
+    at += align256(size_t(n) * 4);
+    L.pos[i] = at;
+    at += align256(size_t(n) * 4);
+  }
+  L.counters = 4 * g.chunks * g.col_blocks;
+  L.counter = at;
+  at += align256(size_t(L.counters) * 4);
+  L.dim_pad = (dim + 7) / 8 * 8;
+  L.partial = at;
+  at += align256(size_t(2 * g.chunks) * size_t(L.dim_pad) * 4);
+  L.bytes = at;
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+int dropout_apply(const void* x, const void* residual, void* y, int64_t n, int32_t dtype, const mo_dropout* dropout,
+                  cudaStream_t stream) {
+  if (dropout == nullptr) return MO_ERR_NULL_POINTER;
+  mo::DropoutParams p = {};
+  int st = drop_args(dropout, &p.drop);
+  if (st != MO_OK) return st;
+  if (!dtype_ok(dtype)) return MO_ERR_BAD_PARAM;
+  if (n < 0 || n > kMaxElems) return MO_ERR_BAD_SHAPE;
+  if (n == 0) return MO_OK;
+  if (x == nullptr || y == nullptr) return MO_ERR_NULL_POINTER;
+  if (misaligned(x, 16) || misaligned(residual, 16) || misaligned(y, 16)) return MO_ERR_MISALIGNED;
+  const size_t bytes = size_t(n) * dtype_bytes(dtype);
+  // in place is fine (an element is read before it is written, by one thread); a shifted overlap is not
+  if ((y != x && overlap(y, bytes, x, bytes)) || (y != residual && overlap(y, bytes, residual, bytes)))
+    return MO_ERR_OVERLAP;
+  int sms = 0;
+  int* status = nullptr;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  p.x = x;
+  p.residual = residual;
+  p.y = y;
+  p.n = n;
+  const cudaError_t e = mo::launch_dropout(p, dtype == MO_BF16, stream);
+  return e != cudaSuccess ? report_cuda(e) : MO_OK;
+}
+
+int embed_lookup(const void* table, int32_t table_dtype, int64_t vocab, int64_t dim, const mo_tokens* tokens, float scale,
+                 const void* add, int64_t add_rows, const mo_dropout* dropout, void* out, int32_t out_dtype,
+                 cudaStream_t stream) {
+  mo::LookupParams p = {};
+  int st = token_args(tokens, &p.tokens);
+  if (st != MO_OK) return st;
+  if ((st = table_shape(vocab, dim)) != MO_OK) return st;
+  if (!dtype_ok(table_dtype) || !dtype_ok(out_dtype) || !std::isfinite(scale)) return MO_ERR_BAD_PARAM;
+  if ((st = drop_args(dropout, &p.drop)) != MO_OK) return st;
+  if (add != nullptr && (add_rows <= 0 || add_rows > kMaxVocab)) return MO_ERR_BAD_SHAPE;
+  if (tokens->n == 0) return MO_OK;
+  if (table == nullptr || out == nullptr) return MO_ERR_NULL_POINTER;
+  if (misaligned(table, 16) || misaligned(add, 16) || misaligned(out, 16)) return MO_ERR_MISALIGNED;
+  const size_t out_bytes = size_t(tokens->n) * size_t(dim) * dtype_bytes(out_dtype);
+  if (overlap(out, out_bytes, table, size_t(vocab) * size_t(dim) * dtype_bytes(table_dtype)) ||
+      overlap(out, out_bytes, add, size_t(add ? add_rows : 0) * size_t(dim) * dtype_bytes(table_dtype)) ||
+      overlap(out, out_bytes, tokens->ids, token_bytes(tokens)))
+    return MO_ERR_OVERLAP;
+  int sms = 0;
+  if ((st = mo::current_device(&sms, &p.status)) != MO_OK) return st;
+  p.table = table;
+  p.add = add;
+  p.out = out;
+  p.vocab = vocab;
+  p.dim = dim;
+  p.add_rows = add_rows;
+  p.scale = scale;
+  const cudaError_t e = mo::launch_embed_lookup(p, table_dtype == MO_BF16, out_dtype == MO_BF16, stream);
+  return e != cudaSuccess ? report_cuda(e) : MO_OK;
+}
+
+size_t mo_embed_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
+  if (n < 0 || n > kMaxTokens || table_shape(vocab, dim) != MO_OK) return 0;
+  return n == 0 ? 256 : grad_layout(n, dim).bytes;
+}
+
+int embed_grad(const void* dout, int32_t dout_dtype, const mo_tokens* tokens, int64_t vocab, int64_t dim, float scale,
+               const mo_dropout* dropout, float* grad, int32_t accumulate, void* ws, size_t ws_bytes,
+               cudaStream_t stream) {
+  mo::GradParams p = {};
+  int st = token_args(tokens, &p.tokens);
+  if (st != MO_OK) return st;
+  if ((st = table_shape(vocab, dim)) != MO_OK) return st;
+  if (!dtype_ok(dout_dtype) || !std::isfinite(scale) || (accumulate != 0 && accumulate != 1)) return MO_ERR_BAD_PARAM;
+  if ((st = drop_args(dropout, &p.drop)) != MO_OK) return st;
+  if (grad == nullptr) return MO_ERR_NULL_POINTER;
+  if (misaligned(grad, 16)) return MO_ERR_MISALIGNED;
+  const int64_t n = tokens->n;
+  const size_t grad_bytes = size_t(vocab) * size_t(dim) * 4;
+  if (n == 0) {   // the sum over no tokens
+    if (accumulate) return MO_OK;
+    int sms = 0;
+    if ((st = mo::current_device(&sms, &p.status)) != MO_OK) return st;
+    const cudaError_t e = cudaMemsetAsync(grad, 0, grad_bytes, stream);
+    return e != cudaSuccess ? report_cuda(e) : MO_OK;
+  }
+  if (dout == nullptr || ws == nullptr) return MO_ERR_NULL_POINTER;
+  if (misaligned(dout, 16) || misaligned(ws, 256)) return MO_ERR_MISALIGNED;
+  const GradLayout L = grad_layout(n, dim);
+  if (ws_bytes < L.bytes) return MO_ERR_WORKSPACE_TOO_SMALL;
+  const size_t dout_bytes = size_t(n) * size_t(dim) * dtype_bytes(dout_dtype);
+  if (overlap(grad, grad_bytes, dout, dout_bytes) || overlap(grad, grad_bytes, tokens->ids, token_bytes(tokens)) ||
+      overlap(grad, grad_bytes, ws, L.bytes) || overlap(ws, L.bytes, dout, dout_bytes) ||
+      overlap(ws, L.bytes, tokens->ids, token_bytes(tokens)))
+    return MO_ERR_OVERLAP;
+  int sms = 0;
+  if ((st = mo::current_device(&sms, &p.status)) != MO_OK) return st;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  for (int i = 0; i < 2; ++i) {
+    p.key[i] = reinterpret_cast<uint32_t*>(w + L.key[i]);
+    p.pos[i] = reinterpret_cast<uint32_t*>(w + L.pos[i]);
+  }
+  p.counter = reinterpret_cast<uint32_t*>(w + L.counter);
+  p.partial = reinterpret_cast<float*>(w + L.partial);
+  p.counters = L.counters;
+  p.dim_pad = L.dim_pad;
+  p.chunk = mo::grad_grid(n, dim).chunk;
+  p.dout = dout;
+  p.grad = grad;
+  p.vocab = vocab;
+  p.dim = dim;
+  p.factor = scale * p.drop.factor;
+  p.accumulate = accumulate;
+  int bits = 1;
+  while ((int64_t(1) << bits) <= vocab) ++bits;   // the keys run from 0 to vocab
+  p.passes = (bits + 8) / 9;
+  const cudaError_t e = mo::launch_embed_grad(p, dout_dtype == MO_BF16, sms, stream);
+  return e != cudaSuccess ? report_cuda(e) : MO_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,87 @@
+// Launch interface between the entry points of the training-step operators
+// (train_abi.cu) and their kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "mo.h"
+#include "philox.cuh"
+
+namespace mo {
+
+// ---------------------------------------------------------------- shared with abi.cu
+// The current device's SM count and status word; MO_OK or an error status.
+int current_device(int* sms, int** status);
+// Records a failing runtime call for mo_last_cuda_error; MO_ERR_CUDA.
+int report_cuda(cudaError_t e);
+
+// ---------------------------------------------------------------- dropout, embedding
+struct DropoutParams {
+  const void* x;
+  const void* residual;   // or null
+  void* y;
+  int64_t n;
+  DropArgs drop;
+};
+cudaError_t launch_dropout(const DropoutParams& p, bool bf16, cudaStream_t stream);
+
+struct TokenArgs {
+  const void* ids;
+  int64_t n;
+  int64_t padding;   // index without a gradient, or -1
+  int32_t wide;      // 64-bit indexes
+};
+
+struct LookupParams {
+  const void* table;
+  const void* add;       // rows added to token t's: t mod add_rows; or null
+  void* out;
+  int* status;
+  int64_t vocab, dim, add_rows;
+  TokenArgs tokens;
+  DropArgs drop;
+  float scale;
+};
+cudaError_t launch_embed_lookup(const LookupParams& p, bool table_bf16, bool out_bf16, cudaStream_t stream);
+
+// Launch shape of the gradient's sums: chunks of sorted positions by blocks of
+// columns (eight a thread, or one where dim is not a multiple of 8). A chunk
+// is 64 positions, fewer where that leaves too few blocks to fill the GPU.
+struct GradGrid {
+  int64_t chunk, chunks, col_blocks;
+  int threads;
+};
+inline GradGrid grad_grid(int64_t n, int64_t dim) {
+  GradGrid g;
+  const int64_t items = (dim & 7) == 0 ? dim / 8 : dim;
+  g.col_blocks = (items + 255) / 256;
+  const int64_t per = (items + g.col_blocks - 1) / g.col_blocks;
+  g.threads = int((per + 31) / 32 * 32);
+  g.chunk = 64;
+  while (g.chunk > 8 && (n + g.chunk - 1) / g.chunk * g.col_blocks < 608) g.chunk /= 2;
+  g.chunks = (n + g.chunk - 1) / g.chunk;
+  return g;
+}
+
+struct GradParams {
+  const void* dout;
+  float* grad;
+  int* status;
+  uint32_t* key[2];       // [n] each; the sorted keys are in key[(passes - 1) & 1]
+  uint32_t* pos[2];
+  uint32_t* counter;      // arrivals of the join: two per slot and column block
+  float* partial;         // [2 chunks, dim_pad] sums of tokens that cross chunks
+  int64_t counters;
+  int64_t vocab, dim, dim_pad, chunk;
+  TokenArgs tokens;
+  DropArgs drop;
+  float factor;           // scale times the dropout's factor
+  int32_t passes;         // of the sort
+  int32_t accumulate;
+};
+cudaError_t launch_embed_grad(const GradParams& p, bool dout_bf16, int sms, cudaStream_t stream);
+
+}  // namespace mo

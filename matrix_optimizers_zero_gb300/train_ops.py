@@ -1,0 +1,145 @@
+"""Binding of the training-step operators around the optimizer (include/mo.h):
+embedding lookup and its gradient, and counter-based dropout.
+
+Tensors are contiguous CUDA tensors on the current device, fp32 or bf16;
+outputs are written in place, on the current stream unless one is given:
+
+    drop = mo.Dropout(0.1, seed=seed, offset=step)         # drawn again in the backward pass
+    mo.embed_lookup(table, tokens, x, scale=1.0, add=positions, dropout=drop)
+    ws = mo.embed_grad_workspace(tokens.numel(), *table.shape)   # reuse it every step
+    mo.embed_grad(dx, tokens, g, ws, scale=1.0, dropout=drop)    # g: the fp32 gradient adamw_tail_step reads
+    mo.dropout_apply(h, y, drop, residual=x)               # forward; with dy for h the backward pass
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+from . import _check, _stream_ptr, load_library
+
+MO_F32, MO_BF16 = 0, 1
+
+
+class Random(ctypes.Structure):
+    """mo_random: seed and offset of the counter-based generator. offset_dev, a
+    one-element int64 CUDA tensor, is added to offset when the kernel runs."""
+    _fields_ = [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("d_offset", ctypes.c_void_p)]
+
+    def __init__(self, seed=0, offset=0, offset_dev=None):
+        super().__init__(int(seed), int(offset), _offset_ptr(offset_dev))
+        self.keep = offset_dev
+
+
+class Dropout(ctypes.Structure):
+    """mo_dropout: probability p and the random numbers of the mask."""
+    _fields_ = [("p", ctypes.c_float), ("random", Random)]
+
+    def __init__(self, p, seed=0, offset=0, offset_dev=None):
+        super().__init__(p, Random(seed, offset, offset_dev))
+        self.keep = offset_dev
+
+
+class MoTokens(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("n", ctypes.c_int64), ("padding_idx", ctypes.c_int64),
+                ("bits", ctypes.c_int32)]
+
+
+def _offset_ptr(t):
+    if t is None:
+        return None
+    import torch
+    if t.dtype != torch.int64 or t.numel() != 1 or not t.is_cuda:
+        raise TypeError("offset_dev must be a one-element int64 CUDA tensor")
+    return t.data_ptr()
+
+
+def _dtype(t, name: str) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        code = MO_F32
+    elif t.dtype == torch.bfloat16:
+        code = MO_BF16
+    else:
+        raise TypeError(f"{name} must be fp32 or bf16")
+    _dense(t, name)
+    return code
+
+
+def _dense(t, name: str) -> None:
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+
+
+def _tokens(tokens, padding_idx: int = -1) -> MoTokens:
+    import torch
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError("tokens must be int32 or int64")
+    _dense(tokens, "tokens")
+    return MoTokens(tokens.data_ptr(), tokens.numel(), padding_idx, 64 if tokens.dtype == torch.int64 else 32)
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def dropout_apply(x, out, dropout: Dropout, residual=None, stream=None) -> None:
+    """out = drop(x) (+ residual); out may be x or residual. With dy for x and
+    no residual it is the backward pass."""
+    code = _dtype(x, "x")
+    if _dtype(out, "out") != code or out.numel() != x.numel():
+        raise ValueError("x and out must have equal types and sizes")
+    if residual is not None and (_dtype(residual, "residual") != code or residual.numel() != x.numel()):
+        raise ValueError("x and residual must have equal types and sizes")
+    st = load_library().dropout_apply(x.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(),
+                                      x.numel(), code, ctypes.byref(dropout), _stream_ptr(stream))
+    _check(st, "dropout_apply")
+
+
+def embed_lookup(table, tokens, out, scale: float = 1.0, add=None, dropout: Optional[Dropout] = None,
+                 stream=None) -> None:
+    """out[t] = drop(scale * table[tokens[t]] + add[t % len(add)]) for every
+    token, in the order of the flattened tokens."""
+    code, out_code = _dtype(table, "table"), _dtype(out, "out")
+    if table.dim() != 2:
+        raise ValueError("table must be [vocab, dim]")
+    vocab, dim = table.shape
+    if out.numel() != tokens.numel() * dim:
+        raise ValueError("out must have dim elements for every token")
+    if add is not None and (_dtype(add, "add") != code or add.dim() != 2 or add.shape[1] != dim):
+        raise ValueError("add must be [rows, dim] of the table's type")
+    tk = _tokens(tokens)
+    st = load_library().embed_lookup(table.data_ptr(), code, vocab, dim, ctypes.byref(tk), scale,
+                                     None if add is None else add.data_ptr(), 0 if add is None else add.shape[0],
+                                     _ref(dropout), out.data_ptr(), out_code, _stream_ptr(stream))
+    _check(st, "embed_lookup")
+
+
+def mo_embed_grad_workspace_bytes(n: int, vocab: int, dim: int) -> int:
+    return int(load_library().mo_embed_grad_workspace_bytes(n, vocab, dim))
+
+
+def embed_grad_workspace(n: int, vocab: int, dim: int, device=None):
+    """A torch uint8 device tensor large enough for embed_grad of n tokens."""
+    import torch
+    return torch.empty(max(mo_embed_grad_workspace_bytes(n, vocab, dim), 256), dtype=torch.uint8,
+                       device=device or torch.device("cuda"))
+
+
+def embed_grad(dout, tokens, grad, workspace, scale: float = 1.0, padding_idx: int = -1, accumulate: bool = False,
+               dropout: Optional[Dropout] = None, stream=None) -> None:
+    """grad[v] (+)= scale * sum of dout[t] over the tokens t = v, under the
+    forward pass's dropout; grad is fp32 [vocab, dim]. Without accumulate the
+    rows no token names become 0."""
+    import torch
+    code = _dtype(dout, "dout")
+    if grad.dtype != torch.float32 or grad.dim() != 2:
+        raise TypeError("grad must be fp32 [vocab, dim]")
+    _dense(grad, "grad")
+    vocab, dim = grad.shape
+    if dout.numel() != tokens.numel() * dim:
+        raise ValueError("dout must have dim elements for every token")
+    tk = _tokens(tokens, padding_idx)
+    st = load_library().embed_grad(dout.data_ptr(), code, ctypes.byref(tk), vocab, dim, scale, _ref(dropout),
+                                   grad.data_ptr(), int(accumulate), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(st, "embed_grad")
