@@ -346,6 +346,63 @@ int embed_grad(const void* dout, int32_t dout_dtype, const mo_tokens* tokens, in
                const mo_dropout* dropout, float* grad, int32_t accumulate, void* ws, size_t ws_bytes,
                cudaStream_t stream);
 
+/* Microscaled 4-bit tensors: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign)
+ * with a scale for each block of consecutive elements of a row.
+ *   MO_FP4_MX   blocks of 32, scale a power of two (e8m0, 2^-127 .. 2^127)
+ *   MO_FP4_NV   blocks of 16, scale e4m3 times g, a power of two for the whole
+ *               tensor: the smallest g with amax <= 6 * 448 g (at least 2^-126;
+ *               1 for a tensor of zeros)
+ * A block's scale is the smallest of its type with which no element exceeds
+ * 6, so nothing saturates (with a caller's amax that is too small, elements
+ * beyond 6 * 448 g do). A block that holds a NaN or an infinity has a NaN
+ * scale: all its values are NaN.
+ * Storage, owned by the caller, 16-byte aligned:
+ *   codes   mo_fp4_codes_bytes(): two a byte, the even element in the low half;
+ *           rows of 16 ceil(k / 32) bytes
+ *   scales  mo_fp4_scales_bytes(): tiles of 128 rows by 4 blocks, the tiles of
+ *           128 rows one after the other along k; row r, block b of a tile at
+ *           byte (r % 32) 16 + (r / 32) 4 + b
+ *   amax    MO_FP4_NV: one fp32, the magnitude that g comes from
+ * rows and k up to 2^22, and up to 2^37 elements. */
+enum mo_fp4_format { MO_FP4_MX = 0, MO_FP4_NV = 1 };
+typedef struct {
+  void* codes;
+  void* scales;
+  float* amax;
+  int64_t rows;
+  int64_t k;
+  int32_t format;   /* enum mo_fp4_format */
+} mo_fp4;
+
+/* Bytes of a 4-bit tensor's codes and scales (host only; 0 for invalid sizes). */
+size_t mo_fp4_codes_bytes(int64_t rows, int64_t k);
+size_t mo_fp4_scales_bytes(int64_t rows, int64_t k, int32_t format);
+
+/* Quantises x [rows, cols] in one pass over it: into by_row [rows, cols], with
+ * blocks along its rows, and into by_col [cols, rows], its transpose with
+ * blocks along its columns; either may be NULL. (A linear layer's forward
+ * product needs x and w by row; its backward products dy by row and w by
+ * column, dy and x by column.)
+ * stochastic NULL: to the nearest code, ties to the even one. Otherwise up or
+ * down with the probabilities of the remainder in steps of 2^-16 (unbiased but
+ * for that step): element (r, c) of by_row takes random number
+ * r 32 ceil(cols / 32) + c, element (c, r) of by_col number
+ * c 32 ceil(rows / 32) + r of the next offset (offset + 1).
+ * amax (device, MO_FP4_NV): the magnitude that g comes from, for example the
+ * last step's; NULL: the call takes the largest finite magnitude of x, which
+ * reads x once more. The tensors' amax receive it. */
+int fp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, const mo_fp4* by_row, const mo_fp4* by_col,
+                 const float* amax, const mo_random* stochastic, cudaStream_t stream);
+
+/* The values q stands for, [rows, k] of `dtype` (exact in both types but at
+ * the ends of their ranges). */
+int fp4_dequantize(const mo_fp4* q, void* out, int32_t dtype, cudaStream_t stream);
+
+/* out [a->rows, b->rows] = A B^T over k, which a and b share along with their
+ * format, on the tensor cores; sums in fp32, rounded once to `dtype`. One
+ * launch. */
+int fp4_product(const mo_fp4* a, const mo_fp4* b, void* out, int32_t dtype, cudaStream_t stream);
+
 /* Synchronises `stream`, then returns and clears the device-side status word:
  * MO_OK, MO_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel expired
  * (the kernel then skipped its remaining work and released its resources), or

@@ -38,7 +38,8 @@ __all__ = [
     "TailTable", "RmnpTable", "muon_owner_step_noalloc", "mo_static_scratch_bytes", "mo_plan_owners",
     "rmnp_colcut_step", "muon_owner_step_coverage",
     "Random", "Dropout", "dropout_apply", "embed_lookup", "embed_grad", "embed_grad_workspace",
-    "mo_embed_grad_workspace_bytes",
+    "mo_embed_grad_workspace_bytes", "Fp4Tensor", "fp4_quantize", "fp4_dequantize", "fp4_product",
+    "mo_fp4_codes_bytes", "mo_fp4_scales_bytes",
 ]
 
 MO_OK = 0
@@ -152,6 +153,11 @@ def load_library() -> ctypes.CDLL:
         "dropout_apply": (ctypes.c_int, [P, P, P, I64, I32, P, P]),
         "embed_lookup": (ctypes.c_int, [P, I32, I64, I64, P, ctypes.c_float, P, I64, P, P, I32, P]),
         "mo_embed_grad_workspace_bytes": (SZ, [I64, I64, I64]),
+        "mo_fp4_codes_bytes": (SZ, [I64, I64]),
+        "mo_fp4_scales_bytes": (SZ, [I64, I64, I32]),
+        "fp4_quantize": (ctypes.c_int, [P, I32, I64, I64, P, P, P, P, P]),
+        "fp4_dequantize": (ctypes.c_int, [P, P, I32, P]),
+        "fp4_product": (ctypes.c_int, [P, P, P, I32, P]),
         "embed_grad": (ctypes.c_int, [P, I32, P, I64, I64, ctypes.c_float, P, P, I32, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
@@ -480,4 +486,5 @@ def mo_plan_owners(roles: Sequence[Tuple[int, int, int]], world: int, strategy: 
 
 
 from .train_ops import (  # noqa: E402  (uses the binding above)
-    Dropout, Random, dropout_apply, embed_grad, embed_grad_workspace, embed_lookup, mo_embed_grad_workspace_bytes)
+    Dropout, Fp4Tensor, Random, dropout_apply, embed_grad, embed_grad_workspace, embed_lookup, fp4_dequantize, fp4_product,
+    fp4_quantize, mo_embed_grad_workspace_bytes, mo_fp4_codes_bytes, mo_fp4_scales_bytes)

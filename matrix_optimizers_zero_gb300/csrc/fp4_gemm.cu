@@ -1,0 +1,671 @@
+// Products of 4-bit block-scaled tensors on the 5th-generation tensor cores:
+// D[m, n] = gA gB sum_k A[m, k] B[n, k], with A and B as e2m1 codes under a
+// scale for each block of their rows, accumulated in fp32 in TMEM, rounded
+// once to the output's type.
+//
+// Scales reach the tensor core through TMEM: their 512-byte tiles arrive by
+// TMA beside the codes and are copied to TMEM columns (tcgen05.cp) in front
+// of the instructions that use them, in issue order.
+//
+//   fp4_pair_kernel    256 x 256 tiles on CTA pairs, persistent: the large products
+//   fp4_narrow_kernel  128 (rows of B) x NT (rows of A) tiles on single CTAs, K
+//                      split over a cluster whose CTAs add their sums through
+//                      distributed shared memory in rank order: few rows
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "device_common.cuh"
+#include "ptx_fp4.cuh"
+#include "train_kernels.h"
+
+namespace mo {
+namespace {
+
+constexpr int kStageK = 256;                         // elements of K a stage: 128 bytes of codes, one swizzle row
+constexpr uint32_t kPanelBytes = 128 * kStageK / 2;  // 128 rows of codes
+// 512-byte scale tiles of 128 rows in a stage, and K = 64 instructions a tile serves
+template <bool MX>
+constexpr int kSfTiles = MX ? 2 : 4;
+template <bool MX>
+constexpr int kStepsPerTile = MX ? 2 : 1;
+template <bool MX>
+constexpr uint32_t kSfBytes = 512u * kSfTiles<MX>;
+
+struct alignas(64) ProductParams {
+  CUtensorMap a, b, sa, sb;   // codes (128-byte swizzle) and scale tiles of both operands
+  void* out;
+  const float* amax_a;
+  const float* amax_b;
+  int* status;
+  int64_t m, n;
+  int32_t steps;              // K = 64 instructions: ceil(k / 64)
+  int32_t stages;             // ceil(k / 256)
+  int32_t tiles_k;            // scale tiles along K
+  int32_t tiles_m, tiles_n;   // output tiles
+  int32_t align;              // of D's rows: 32, 16 or 0 (element stores)
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ float scale_of(const float* amax) {
+  if (amax == nullptr) return 1.0f;
+  const uint32_t b = __float_as_uint(*amax) & 0x7FFFFFFFu;
+  if (b == 0u || b >= 0x7F800000u) return 1.0f;
+  const int e = int(b >> 23) - 138 + ((b & 0x7FFFFFu) > 0x280000u ? 1 : 0);
+  return __uint_as_float(uint32_t(max(e, -126) + 127) << 23);
+}
+
+// 32 consecutive outputs of one row.
+template <typename O>
+__device__ __forceinline__ void store32(O* row, int64_t col, int64_t n, int align, const float (&v)[32]);
+
+template <>
+__device__ __forceinline__ void store32<uint16_t>(uint16_t* row, int64_t col, int64_t n, int align, const float (&v)[32]) {
+  uint16_t* o = row + col;
+  if (col + 32 <= n && align != 0) {
+    uint32_t w[2][8];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j >> 3][j & 7] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+    if (align == 32) {
+      ptx::st_global_v8(o, w[0]);
+      ptx::st_global_v8(o + 16, w[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        reinterpret_cast<uint4*>(o)[j] = make_uint4(w[j >> 1][4 * (j & 1)], w[j >> 1][4 * (j & 1) + 1],
+                                                    w[j >> 1][4 * (j & 1) + 2], w[j >> 1][4 * (j & 1) + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col + i < n) o[i] = float_to_bf16_bits(v[i]);
+  }
+}
+
+template <>
+__device__ __forceinline__ void store32<float>(float* row, int64_t col, int64_t n, int align, const float (&v)[32]) {
+  float* o = row + col;
+  if (col + 32 <= n && align != 0) {
+    if (align == 32) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * q + j]);
+        ptx::st_global_v8(o + 8 * q, w);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        reinterpret_cast<float4*>(o)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col + i < n) o[i] = v[i];
+  }
+}
+
+// ------------------------------------------------------------------ pairs
+//
+// Warp 0 of each CTA loads its 128-row halves of A and B, its A scales and all
+// 256 rows' B scales; the even CTA's warp 1 copies scales and issues the
+// instructions; eight warps drain 128 lanes x 256 columns.
+//
+// TMEM: a 256 x 256 accumulator takes 256 columns and a stage's scales up to
+// 48, so two whole accumulators do not fit. They overlap in 48 columns,
+// [208, 256): the epilogue drains those first, and the next tile starts as
+// soon as they are free.
+constexpr int kEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kEpiWarps;
+constexpr int kPairStages = 5;
+constexpr uint32_t kAccStep = 208;
+constexpr uint32_t kSfCol = 464;
+constexpr uint32_t kSfColStep = 12;   // A 4 columns, B 8, a scale tile
+template <bool MX>
+constexpr uint32_t kPairStageBytes = 2 * kPanelBytes + 3 * kSfBytes<MX>;
+constexpr uint32_t kPairBars = 2 * kPairStages + 7;
+template <bool MX>
+constexpr size_t kPairSmem = 1024 + size_t(kPairStages) * kPairStageBytes<MX> + 256;
+static_assert(kAccStep + 256 <= kSfCol && kSfCol + 4 * kSfColStep <= 512, "TMEM columns");
+static_assert(8 * kPairBars + 32 <= 256, "control block");
+static_assert(kPairSmem<false> <= 227 * 1024, "shared memory");
+
+// Output tiles in groups of 8 tile rows, column by column: the tiles in
+// flight share operand panels.
+__device__ __forceinline__ void tile_at(int32_t t, int32_t tiles_m, int32_t tiles_n, int32_t& tm, int32_t& tn) {
+  const int32_t group = t / (8 * tiles_n), first = group * 8;
+  const int32_t height = min(8, tiles_m - first), in = t - group * 8 * tiles_n;
+  tm = first + in % height;
+  tn = in / height;
+}
+
+template <bool MX, typename O>
+__global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_constant__ ProductParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  constexpr uint32_t kStage = kPairStageBytes<MX>;
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  // panels first (1024-byte aligned), then the scale tiles of every stage, then control
+  const uint32_t sf_base = base + uint32_t(kPairStages) * 2u * kPanelBytes;
+  const uint32_t bars = sf_base + uint32_t(kPairStages) * 3u * kSfBytes<MX>;
+  uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kPairBars);
+  uint32_t* tmem_slot = ctrl;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 1);
+  volatile uint32_t* peer_report = ctrl + 2;   // [0] the peer gave up, [1] stages its producer issued
+  auto full_bar = [&](int s) { return bars + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(kPairStages + s); };
+  auto tfull_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + s); };
+  auto tempty_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + 2 + s); };
+  auto over_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + 4 + s); };
+  const uint32_t drain_bar = bars + 8u * uint32_t(2 * kPairStages + 6);
+
+  const int warp = int(threadIdx.x >> 5);
+  const int lane = int(threadIdx.x & 31);
+  const uint32_t rank = ptx::cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(tfull_bar(s), 1);
+      ptx::mbar_init(tempty_bar(s), 2 * kEpiWarps);
+      ptx::mbar_init(over_bar(s), kEpiWarps);   // four warps of each CTA
+    }
+    ptx::mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    peer_report[0] = 0u;
+    peer_report[1] = 0u;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int32_t ntiles = p.tiles_m * p.tiles_n;
+  const int32_t first = int32_t(ptx::cluster_id_x()), step = int32_t(ptx::nclusters_x());
+  uint32_t n_issued = 0;
+  bool mma_issued = false;
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer (both CTAs)
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int32_t t = first; ok && t < ntiles; t += step) {
+        int32_t tm, tn;
+        tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
+        const int32_t ra = tm * 2 + int32_t(rank), rb = tn * 2 + int32_t(rank);   // 128-row panels
+        for (int32_t kb = 0; kb < p.stages; ++kb) {
+          if (!mbar_wait_bounded(empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb_local = full_bar(stage);
+          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * kStage);
+          const uint32_t fb = ptx::mapa_shared(fb_local, 0);
+          const uint32_t sa = base + uint32_t(stage) * 2u * kPanelBytes;
+          const uint32_t sf = sf_base + uint32_t(stage) * 3u * kSfBytes<MX>;
+          ptx::tma_load_2d_pair(sa, &p.a, fb, kb * 128, ra * 128);
+          ptx::tma_load_2d_pair(sa + kPanelBytes, &p.b, fb, kb * 128, rb * 128);
+          const int32_t at = kb * kSfTiles<MX>;
+          ptx::tma_load_2d_pair(sf, &p.sa, fb, 0, (ra * p.tiles_k + at) * 2);
+          ptx::tma_load_2d_pair(sf + kSfBytes<MX>, &p.sb, fb, 0, (tn * 2 * p.tiles_k + at) * 2);
+          ptx::tma_load_2d_pair(sf + 2 * kSfBytes<MX>, &p.sb, fb, 0, ((tn * 2 + 1) * p.tiles_k + at) * 2);
+          ++n_issued;
+          if (++stage == kPairStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------ MMA issuer (even CTA)
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int32_t i = 0;
+      for (int32_t t = first; ok && t < ntiles; t += step, ++i) {
+        const int acc = i & 1;
+        // the accumulator's previous tile is drained, and the columns shared with the last one
+        if (!mbar_wait_bounded(tempty_bar(acc), (uint32_t(i >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
+        if (i > 0 && !mbar_wait_bounded(over_bar(acc ^ 1), uint32_t((i - 1) >> 1) & 1u, abort_flag, p.status, p.timeout_ns))
+          break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + uint32_t(acc) * kAccStep;
+        int32_t left = p.steps;
+        for (int32_t kb = 0; kb < p.stages; ++kb) {
+          if (!mbar_wait_bounded(full_bar(stage), ph, abort_flag, p.status, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sa = base + uint32_t(stage) * 2u * kPanelBytes;
+          const uint32_t sb = sa + kPanelBytes;
+          const uint32_t sf = sf_base + uint32_t(stage) * 3u * kSfBytes<MX>;
+#pragma unroll
+          for (int a = 0; a < kSfTiles<MX>; ++a) {
+            const uint32_t c = tmem + kSfCol + uint32_t(a) * kSfColStep;
+            if (left > a * kStepsPerTile<MX>) {
+              ptx::tmem_copy_scales<true>(c, ptx::smem_desc_scales(sf + 512u * uint32_t(a)));
+              ptx::tmem_copy_scales<true>(c + 4, ptx::smem_desc_scales(sf + kSfBytes<MX> + 512u * uint32_t(a)));
+              ptx::tmem_copy_scales<true>(c + 8, ptx::smem_desc_scales(sf + 2 * kSfBytes<MX> + 512u * uint32_t(a)));
+            }
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk < left) {
+              constexpr uint32_t idesc0 = ptx::idesc_fp4(256, 256, MX, 0);
+              constexpr uint32_t idesc2 = ptx::idesc_fp4(256, 256, MX, 2);
+              const int a = kk / kStepsPerTile<MX>;
+              const uint32_t c = tmem + kSfCol + uint32_t(a) * kSfColStep;
+              ptx::umma_fp4<true, MX>(d, ptx::smem_desc_sw128(sa + uint32_t(kk) * 32u, 16u, 1024u),
+                                      ptx::smem_desc_sw128(sb + uint32_t(kk) * 32u, 16u, 1024u),
+                                      MX && (kk & 1) ? idesc2 : idesc0, c, c + 4, (kb | kk) != 0 ? 1u : 0u);
+            }
+          }
+          left -= 4;
+          ptx::umma_commit_pair(empty_bar(stage), 0x3);
+          mma_issued = true;
+          if (++stage == kPairStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::umma_commit_pair(tfull_bar(acc), 0x3);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue (both CTAs)
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const float factor = scale_of(p.amax_a) * scale_of(p.amax_b);
+    int32_t i = 0;
+    for (int32_t t = first; t < ntiles; t += step, ++i) {
+      const int acc = i & 1;
+      int32_t tm, tn;
+      tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
+      bool ok = mbar_wait_bounded(tfull_bar(acc), uint32_t(i >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const int64_t row = int64_t(tm) * 256 + int64_t(rank) * 128 + quarter * 32 + lane;
+      const int64_t col = int64_t(tn) * 256 + half * 128;
+      O* out = static_cast<O*>(p.out) + (row < p.m ? row : 0) * p.n;
+      const uint32_t tb = tmem + uint32_t(acc) * kAccStep + uint32_t(half * 128) + (uint32_t(quarter * 32) << 16);
+      // accumulator 0 ends in the shared columns, accumulator 1 begins with them
+#pragma unroll 1
+      for (int s = 0; s < 4; ++s) {
+        const int ch = acc == 0 ? 3 - s : s;
+        uint32_t r[32];
+        __syncwarp();
+        ptx::tmem_ld_32x32b_x32(tb + uint32_t(ch * 32), r);
+        ptx::tmem_ld_wait();
+        if ((s == 1 && half == (acc ^ 1)) || s == 3) {   // the shared columns, or all, are in registers
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (s == 1) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(over_bar(acc), 0));
+            if (s == 3) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(tempty_bar(acc), 0));
+          }
+        }
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * factor;
+        if (row < p.m && col + ch * 32 < p.n) store32<O>(out, col + ch * 32, p.n, p.align, v);
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  // Both CTAs learn whether either gave up and how many stages its producer issued.
+  if (threadIdx.x == 0)
+    ptx::st_shared_cluster_v2(ptx::mapa_shared(ptx::smem_addr(const_cast<uint32_t*>(peer_report)), rank ^ 1u),
+                              *abort_flag != 0 ? 1u : 0u, n_issued);
+  ptx::cluster_sync();
+  if (*abort_flag != 0 || peer_report[0] != 0u) {
+    // Nothing may still write into either CTA's memory when they exit: the even CTA waits for its
+    // instructions, then settles every stage that either producer left in flight (all copies of both
+    // CTAs count their bytes on its full barriers; at most the last kPairStages can be in flight).
+    if (leader && warp == 1 && lane == 0 && mma_issued) {
+      ptx::umma_commit_pair(drain_bar, 0x1);
+      mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
+    }
+    if (leader && threadIdx.x == 0) {
+      const uint32_t L = n_issued, P = peer_report[1];
+      const uint32_t most = L > P ? L : P;
+      for (uint32_t j = most > uint32_t(kPairStages) ? most - uint32_t(kPairStages) : 0u; j < most; ++j) {
+        const int s = int(j % uint32_t(kPairStages));
+        if (j >= L)
+          ptx::mbar_arrive_expect_tx(full_bar(s), kStage);   // only the peer's half is coming
+        else if (j >= P)
+          ptx::mbar_complete_tx(full_bar(s), kStage);        // the peer's half never will
+        mbar_wait_drain(full_bar(s), (j / uint32_t(kPairStages)) & 1u, p.timeout_ns);
+      }
+    }
+    ptx::cluster_sync();
+  }
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc_pair(tmem, 512);
+}
+
+// ------------------------------------------------------------------ few rows
+//
+// A CTA multiplies 128 rows of B by NT rows of A over its part of K; the
+// accumulator's lanes are the output's columns, so stores of a row of D are
+// contiguous across lanes. The CTAs of a cluster hold the parts of one tile.
+constexpr int kNarrowThreads = 192;
+constexpr int kNarrowStages = 4;
+constexpr uint32_t kNarrowPitch = 129;   // of the fp32 sums [NT][128] in shared memory
+template <bool MX, int NT>
+constexpr uint32_t kNarrowStageBytes = kPanelBytes + NT * (kStageK / 2) + 2 * kSfBytes<MX>;
+template <bool MX, int NT>
+constexpr size_t kNarrowSmem = 1024 + size_t(kNarrowStages) * kNarrowStageBytes<MX, NT> + 128;
+template <int NT>
+constexpr uint32_t kNarrowCols = NT <= 32 ? 64 : 2 * NT;   // TMEM: sums, then 8 columns of scales a tile
+static_assert(kNarrowStages * kPanelBytes >= 32 * kNarrowPitch * 4, "sums in the stages' memory (NT <= 32)");
+static_assert(kNarrowStages * (kPanelBytes + 128 * 128) >= 128 * kNarrowPitch * 4, "sums in the stages' memory (NT 128)");
+
+template <bool MX, int NT, typename O>
+__global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid_constant__ ProductParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  constexpr uint32_t kStage = kNarrowStageBytes<MX, NT>;
+  constexpr uint32_t kQBytes = NT * (kStageK / 2);
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t sf_base = base + uint32_t(kNarrowStages) * (kPanelBytes + kQBytes);
+  const uint32_t bars = sf_base + uint32_t(kNarrowStages) * 2u * kSfBytes<MX>;
+  constexpr uint32_t kBars = 2 * kNarrowStages + 2;
+  uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kBars);
+  uint32_t* tmem_slot = ctrl;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 1);
+  float* sums = reinterpret_cast<float*>(smem_raw + (base - raw));
+  auto full_bar = [&](int s) { return bars + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(kNarrowStages + s); };
+  const uint32_t done_bar = bars + 8u * uint32_t(2 * kNarrowStages);
+  const uint32_t drain_bar = bars + 8u * uint32_t(2 * kNarrowStages + 1);
+
+  const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+  const uint32_t parts = gridDim.x / uint32_t(p.tiles_m * p.tiles_n);   // CTAs of a cluster
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int32_t t = int32_t(blockIdx.x / parts);
+  const int32_t tn = t / p.tiles_m, tm = t - tn * p.tiles_m;            // 128 columns of D, NT rows
+  const int32_t k0 = int32_t(int64_t(p.stages) * rank / parts), k1 = int32_t(int64_t(p.stages) * (rank + 1) / parts);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kNarrowStages; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    ptx::mbar_init(done_bar, 1);
+    ptx::mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_one(ptx::smem_addr(tmem_slot), kNarrowCols<NT>);
+    ptx::tmem_relinquish_one();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  uint32_t n_issued = 0;
+  bool mma_issued = false;
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 0;
+      for (int32_t kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait_bounded(empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
+        const uint32_t fb = full_bar(stage);
+        ptx::mbar_arrive_expect_tx(fb, kStage);
+        const uint32_t sp = base + uint32_t(stage) * (kPanelBytes + kQBytes);
+        const uint32_t sf = sf_base + uint32_t(stage) * 2u * kSfBytes<MX>;
+        ptx::tma_load_2d(sp, &p.b, fb, kb * 128, tn * 128);
+        ptx::tma_load_2d(sp + kPanelBytes, &p.a, fb, kb * 128, tm * NT);
+        const int32_t at = kb * kSfTiles<MX>;
+        ptx::tma_load_2d(sf, &p.sb, fb, 0, (tn * p.tiles_k + at) * 2);
+        ptx::tma_load_2d(sf + kSfBytes<MX>, &p.sa, fb, 0, (tm * p.tiles_k + at) * 2);
+        ++n_issued;
+        if (++stage == kNarrowStages) {
+          stage = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int32_t left = p.steps - 4 * k0;
+      for (int32_t kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait_bounded(full_bar(stage), ph, abort_flag, p.status, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t sp = base + uint32_t(stage) * (kPanelBytes + kQBytes);
+        const uint32_t sq = sp + kPanelBytes;
+        const uint32_t sf = sf_base + uint32_t(stage) * 2u * kSfBytes<MX>;
+#pragma unroll
+        for (int a = 0; a < kSfTiles<MX>; ++a) {
+          const uint32_t c = tmem + uint32_t(kNarrowCols<NT> == 64 ? 32 : NT) + uint32_t(a) * 8u;
+          if (left > a * kStepsPerTile<MX>) {
+            ptx::tmem_copy_scales<false>(c, ptx::smem_desc_scales(sf + 512u * uint32_t(a)));
+            ptx::tmem_copy_scales<false>(c + 4, ptx::smem_desc_scales(sf + kSfBytes<MX> + 512u * uint32_t(a)));
+          }
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk < left) {
+            constexpr uint32_t idesc0 = ptx::idesc_fp4(128, NT, MX, 0);
+            constexpr uint32_t idesc2 = ptx::idesc_fp4(128, NT, MX, 2);
+            const int a = kk / kStepsPerTile<MX>;
+            const uint32_t c = tmem + uint32_t(kNarrowCols<NT> == 64 ? 32 : NT) + uint32_t(a) * 8u;
+            ptx::umma_fp4<false, MX>(tmem, ptx::smem_desc_sw128(sp + uint32_t(kk) * 32u, 16u, 1024u),
+                                     ptx::smem_desc_sw128(sq + uint32_t(kk) * 32u, 16u, 1024u),
+                                     MX && (kk & 1) ? idesc2 : idesc0, c, c + 4, (kb > k0 || kk > 0) ? 1u : 0u);
+          }
+        }
+        left -= 4;
+        ptx::umma_commit_one(empty_bar(stage));
+        mma_issued = true;
+        if (++stage == kNarrowStages) {
+          stage = 0;
+          ph ^= 1u;
+        }
+      }
+      if (ok) ptx::umma_commit_one(done_bar);
+    }
+  } else {
+    const int quarter = warp & 3;
+    bool ok = mbar_wait_bounded(done_bar, 0u, abort_flag, p.status, p.timeout_ns);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (ok) {
+      ptx::tc_fence_after();
+      // every instruction has completed, so every stage has been read: its memory takes the sums
+#pragma unroll 1
+      for (int c = 0; c < NT; c += 16) {
+        uint32_t r[16];
+        __syncwarp();
+        ptx::tmem_ld_32x32b_x16(tmem + uint32_t(c) + (uint32_t(quarter * 32) << 16), r);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          sums[uint32_t(c + j) * kNarrowPitch + uint32_t(quarter * 32 + lane)] = __uint_as_float(r[j]);
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (*abort_flag != 0) {   // settle what is in flight before the memory is given back
+    if (warp == 1 && lane == 0 && mma_issued) {
+      ptx::umma_commit_one(drain_bar);
+      mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
+    }
+    if (threadIdx.x == 0)
+      for (uint32_t j = n_issued > uint32_t(kNarrowStages) ? n_issued - uint32_t(kNarrowStages) : 0u; j < n_issued; ++j)
+        mbar_wait_drain(full_bar(int(j % uint32_t(kNarrowStages))), (j / uint32_t(kNarrowStages)) & 1u, p.timeout_ns);
+    __syncthreads();
+  }
+  ptx::cluster_sync();   // every part's sums are in place
+  const float factor = scale_of(p.amax_a) * scale_of(p.amax_b);
+  const uint32_t sums_addr = ptx::smem_addr(sums);
+  const int64_t row0 = int64_t(tm) * NT, col0 = int64_t(tn) * 128;
+  O* out = static_cast<O*>(p.out);
+  // this CTA's share of the tile's rows, parts added in rank order
+  for (uint32_t i = threadIdx.x + rank * (NT * 128u / parts); i < (rank + 1) * (NT * 128u / parts); i += kNarrowThreads) {
+    const uint32_t j = i >> 7, l = i & 127u;
+    if (row0 + j < p.m && col0 + l < p.n) {
+      float v = 0.0f;
+      for (uint32_t s = 0; s < parts; ++s)
+        v += ptx::ld_shared_cluster_f32(ptx::mapa_shared(sums_addr + 4u * (j * kNarrowPitch + l), s));
+      v *= factor;
+      if constexpr (sizeof(O) == 2)
+        out[(row0 + j) * p.n + col0 + l] = float_to_bf16_bits(v);
+      else
+        out[(row0 + j) * p.n + col0 + l] = v;
+    }
+  }
+  ptx::cluster_sync();   // the peers have read this CTA's sums
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc_one(tmem, kNarrowCols<NT>);
+}
+
+// ------------------------------------------------------------------ launches
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn tensor_map_encoder() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// Codes as bytes [rows, pitch], boxes of 128 bytes (256 elements) by box_rows.
+bool encode_codes(EncodeTiledFn enc, CUtensorMap* map, const Fp4In& q, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {cuuint64_t(q.pitch), cuuint64_t(q.rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(q.pitch)};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(q.codes), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scale tiles as lines of 256 bytes, two a tile; a box is a stage's tiles of
+// one 128-row panel. A box may run into the next panel's tiles (not used) or
+// past the end (zeros).
+bool encode_scales(EncodeTiledFn enc, CUtensorMap* map, const Fp4In& q, uint32_t tiles) {
+  const cuuint64_t dims[2] = {64, cuuint64_t(q.tiles_r * q.tiles_k * 2)};
+  const cuuint64_t strides[1] = {256};
+  const cuuint32_t box[2] = {64, 2 * tiles};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(q.scales), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename K>
+cudaError_t launch(K kern, const ProductParams& p, unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                   cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// A has more than one tile of rows only with NT = 128, so a tile's scales begin a scale tile; every
+// CTA of a cluster has at least two stages.
+template <bool MX, int NT, typename O>
+cudaError_t narrow_as(ProductParams& p, int sms, cudaStream_t stream) {
+  p.tiles_m = int32_t((p.m + NT - 1) / NT);
+  p.tiles_n = int32_t((p.n + 127) / 128);
+  const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
+  unsigned parts = 1;
+  while (parts < 8 && tiles * parts * 2 <= 2 * sms && p.stages >= int32_t(parts) * 4) parts *= 2;
+  return launch(fp4_narrow_kernel<MX, NT, O>, p, unsigned(tiles * parts), kNarrowThreads, kNarrowSmem<MX, NT>, parts, stream);
+}
+
+template <bool MX, typename O>
+cudaError_t product_as(ProductParams& p, const Fp4In& a, const Fp4In& b, int sms, cudaStream_t stream) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const int64_t pairs = sms / 2;
+  const int64_t pair_tiles = ((p.m + 255) / 256) * ((p.n + 255) / 256);
+  const bool narrow = p.m <= 128 || pair_tiles * 2 < pairs;
+  const uint32_t nt = !narrow ? 128 : p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : 128;
+  if (!encode_codes(enc, &p.a, a, nt) || !encode_codes(enc, &p.b, b, 128) ||
+      !encode_scales(enc, &p.sa, a, kSfTiles<MX>) || !encode_scales(enc, &p.sb, b, kSfTiles<MX>))
+    return cudaErrorInvalidValue;
+  if (narrow) {
+    if (nt == 16) return narrow_as<MX, 16, O>(p, sms, stream);
+    if (nt == 32) return narrow_as<MX, 32, O>(p, sms, stream);
+    if (nt == 64) return narrow_as<MX, 64, O>(p, sms, stream);
+    return narrow_as<MX, 128, O>(p, sms, stream);
+  }
+  p.tiles_m = int32_t((p.m + 255) / 256);
+  p.tiles_n = int32_t((p.n + 255) / 256);
+  const unsigned grid = unsigned(2 * std::min(pairs, pair_tiles));
+  return launch(fp4_pair_kernel<MX, O>, p, grid, kPairThreads, kPairSmem<MX>, 2, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_product(const Fp4In& a, const Fp4In& b, bool mx, void* out, bool out_bf16, int sms, int* status,
+                               cudaStream_t stream) {
+  ProductParams p = {};
+  p.out = out;
+  p.amax_a = a.amax;
+  p.amax_b = b.amax;
+  p.status = status;
+  p.m = a.rows;
+  p.n = b.rows;
+  p.steps = int32_t((a.k + 63) / 64);
+  p.stages = int32_t((a.k + kStageK - 1) / kStageK);
+  p.tiles_k = int32_t(a.tiles_k);
+  p.timeout_ns = kDefaultTimeoutNs;
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(out) | uintptr_t(p.n * (out_bf16 ? 2 : 4));
+  p.align = (mis & 31) == 0 ? 32 : (mis & 15) == 0 ? 16 : 0;
+  if (out_bf16) return mx ? product_as<true, uint16_t>(p, a, b, sms, stream) : product_as<false, uint16_t>(p, a, b, sms, stream);
+  return mx ? product_as<true, float>(p, a, b, sms, stream) : product_as<false, float>(p, a, b, sms, stream);
+}
+
+}  // namespace mo

@@ -1,0 +1,356 @@
+// Microscaled 4-bit quantisation: e2m1 codes with a scale for each block of
+// consecutive elements (mx: 32 elements, e8m0; nv: 16 elements, e4m3, times a
+// power of two g for the whole tensor).
+//
+// A block's scale is the smallest of its type, s, with which no element
+// exceeds the largest code: max |x| <= 6 s g. Nothing saturates, so stochastic
+// rounding stays unbiased. Both roundings are exact functions of the input:
+// with mx (and g) a power of two the quotient x / (s g) is exact, with nv it
+// is rounded once (see `quotient`).
+#include <cuda_runtime.h>
+
+#include "device_common.cuh"
+#include "philox.cuh"
+#include "ptx_fp4.cuh"
+#include "train_kernels.h"
+
+namespace mo {
+namespace {
+
+// A 128 x 128 tile of x goes through shared memory, from which both
+// orientations are quantised: x is read once for the operands of a forward and
+// a backward product. Row pitch in elements: 16 bytes more than the row, so
+// that 32 threads reading 16 bytes of 32 rows meet all banks.
+constexpr int kTile = 128;
+constexpr int kThreads = 256;
+template <typename T>
+constexpr int kPitch = kTile + 16 / int(sizeof(T));
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Value of e4m3 bits (0 - 126).
+__device__ __forceinline__ float e4m3_value(uint32_t c) {
+  const uint32_t e = c >> 3, f = c & 7u;
+  return e == 0 ? float(f) * (1.0f / 512.0f) : __uint_as_float(((e + 120u) << 23) | (f << 20));
+}
+
+// The tensor's own scale of nv: the smallest power of two g with
+// amax <= 6 * 448 g = 1.3125 * 2^11 g, from 2^-126; 1 for zeros (and for an
+// amax that is not finite). Returns its exponent.
+__device__ __forceinline__ int tensor_exponent(const float* amax) {
+  if (amax == nullptr) return 0;
+  const uint32_t b = abs_bits(*amax);
+  if (b == 0u || b >= 0x7F800000u) return 0;
+  int e = int(b >> 23) - 127 - 11 + ((b & 0x7FFFFFu) > 0x280000u ? 1 : 0);
+  return e < -126 ? -126 : e;
+}
+__device__ __forceinline__ float pow2(int e) {   // -149 <= e <= 127
+  return e >= -126 ? __uint_as_float(uint32_t(e + 127) << 23) : __uint_as_float(1u << (e + 149));
+}
+
+// x / s for x = v[i] in fp32, correctly rounded: y = RN(1 / s), q = RN(x y), one
+// correction with the exact remainder (Markstein, 1990). A plain product with
+// the reciprocal would put exact ties on the wrong side.
+__device__ __forceinline__ float quotient(float x, float s, float y) {
+  const float q = x * y;
+  return fmaf(fmaf(-q, s, x), y, q);
+}
+
+// Eight codes of |y| <= 6 rounded up with the probability of the remainder:
+// y in fixed point with 16 bits below the grid's step, plus a 16-bit number.
+__device__ __forceinline__ uint32_t stochastic_e2m1x8(const float (&y)[8], const uint4& g) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fminf(fabsf(y[i]), 6.0f);
+    const uint32_t f = uint32_t(a * 131072.0f);   // floor; steps of 0.5 below 2, 1 below 4, 2 above
+    const uint32_t sh = (a >= 2.0f ? 1u : 0u) + (a >= 4.0f ? 1u : 0u);
+    const uint32_t m = ((f + (philox_half(g, i) << sh)) >> (16u + sh)) + 2u * sh;
+    r |= (m | ((__float_as_uint(y[i]) >> 28) & 8u)) << (4 * i);
+  }
+  return r;
+}
+
+// Quantises 32 consecutive elements (one block of mx, two of nv): codes in four
+// words, scale bits in the returned value (one byte a block). i0: index of the
+// first element for the random numbers.
+template <bool MX, bool STOCH>
+__device__ __forceinline__ uint32_t quantize32(const float (&v)[32], int gexp, const Philox& rng, uint64_t i0,
+                                               uint32_t (&codes)[4]) {
+  uint32_t bits = 0;
+  constexpr int kBlock = MX ? 32 : 16;
+#pragma unroll
+  for (int b = 0; b < 32 / kBlock; ++b) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kBlock; ++i) top = max(top, abs_bits(v[b * kBlock + i]));
+    float down, s = 1.0f, inv = 1.0f;
+    uint32_t sc;
+    if (MX) {
+      // 6 = 1.5 * 2^2: the exponent of the maximum less two, one more where its mantissa exceeds 1.5
+      const int e = int(top >> 23) - 2 + ((top & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+      sc = top >= 0x7F800000u ? 0xFFu : uint32_t(max(e, 0));
+      down = __uint_as_float((254u - min(sc, 253u)) << 23);
+    } else {
+      down = pow2(-gexp);
+      const float a = __uint_as_float(top) * down;
+      if (top >= 0x7F800000u) {
+        sc = 0x7Fu;
+      } else {
+        // nearest e4m3 of a / 6 from below or above, then up or down to the smallest with 6 s >= a
+        const float t = fminf(a * (1.0f / 6.0f), 448.0f);
+        uint16_t c16;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c16) : "f"(0.0f), "f"(t));
+        sc = c16 & 0x7Fu;
+        if (6.0f * e4m3_value(sc) < a && sc < 126u) ++sc;
+        if (sc > 0u && 6.0f * e4m3_value(sc - 1u) >= a) --sc;
+        if (sc == 0u && top != 0u) sc = 1u;   // a underflowed
+      }
+      s = e4m3_value(min(sc, 126u));
+      inv = sc != 0u ? 1.0f / s : 0.0f;
+    }
+    bits |= sc << (8 * b);
+    const bool bad = top >= 0x7F800000u;   // the scale says NaN; codes 0
+#pragma unroll
+    for (int w = 0; w < kBlock / 8; ++w) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x = v[b * kBlock + 8 * w + i] * down;
+        if (!MX) x = fminf(fmaxf(x, -2688.0f), 2688.0f);   // 6 * 448: only a caller's too small amax reaches it
+        y[i] = bad ? 0.0f : MX ? x : quotient(x, s, inv);
+      }
+      const int k = b * (kBlock / 8) + w;
+      codes[k] = STOCH ? stochastic_e2m1x8(y, rng.group((i0 >> 3) + uint64_t(k))) : ptx::cvt_e2m1x8(y);
+    }
+  }
+  return bits;
+}
+
+__device__ __forceinline__ float as_float(uint16_t x) { return bf16_bits_to_float(x); }
+__device__ __forceinline__ float as_float(float x) { return x; }
+
+// Writes the codes and scales of 64 elements of row `row` (two 32-element parts
+// from element k0, a multiple of 64, on): 32 bytes of codes and 2 (mx) or 4 (nv) scales.
+template <bool MX>
+__device__ __forceinline__ void put64(const Fp4Out& q, int64_t row, int64_t k0, const uint32_t (&c0)[4],
+                                      const uint32_t (&c1)[4], uint32_t s0, uint32_t s1) {
+  if (row < q.rows) {
+    uint8_t* o = q.codes + row * q.pitch + (k0 >> 1);
+    if (k0 < q.k) *reinterpret_cast<uint4*>(o) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
+    if (k0 + 32 < q.k) *reinterpret_cast<uint4*>(o + 16) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+  }
+  // rows and blocks outside the tensor have zeros in its last tiles (values and scale 0)
+  const int64_t blk = MX ? k0 >> 5 : k0 >> 4;
+  if ((blk >> 2) < q.tiles_k && (row >> 7) < q.tiles_r) {
+    uint8_t* o = q.scales + ((row >> 7) * q.tiles_k + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
+    if (MX)
+      *reinterpret_cast<uint16_t*>(o) = uint16_t(s0 | (s1 << 8));
+    else
+      *reinterpret_cast<uint32_t*>(o) = s0 | (s1 << 16);
+  }
+}
+
+template <typename T, bool MX, bool STOCH>
+__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const QuantParams p) {
+  extern __shared__ __align__(16) uint8_t tile_smem[];
+  T* tile = reinterpret_cast<T*>(tile_smem);
+  constexpr int P = kPitch<T>;
+  constexpr int E = 16 / int(sizeof(T));        // elements of a 16-byte access
+  constexpr int kVecs = kTile / E;              // accesses a row
+  const int tid = int(threadIdx.x);
+  const int64_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x - tr * p.tiles_c;
+  const int64_t r0 = tr * kTile, c0 = tc * kTile;
+  const T* x = static_cast<const T*>(p.x);
+  const bool full = r0 + kTile <= p.rows && c0 + kTile <= p.cols && p.vec;
+  if (full) {
+#pragma unroll 8
+    for (int i = tid; i < kTile * kVecs; i += kThreads) {
+      const int r = i / kVecs, c = (i - r * kVecs) * E;
+      *reinterpret_cast<uint4*>(tile + r * P + c) = __ldg(reinterpret_cast<const uint4*>(x + (r0 + r) * p.cols + c0 + c));
+    }
+  } else {
+    for (int i = tid; i < kTile * kTile; i += kThreads) {
+      const int r = i / kTile, c = i - r * kTile;
+      tile[r * P + c] = r0 + r < p.rows && c0 + c < p.cols ? x[(r0 + r) * p.cols + c0 + c] : T(0);
+    }
+  }
+  const int gexp = MX ? 0 : tensor_exponent(p.amax);
+  if (!MX && blockIdx.x == 0 && tid == 0) {
+    if (p.row.amax != nullptr) *p.row.amax = *p.amax;
+    if (p.col.amax != nullptr) *p.col.amax = *p.amax;
+  }
+  __syncthreads();
+  const int line = tid & (kTile - 1), half = tid >> 7;   // a row (a column) of the tile, 64 elements of it
+  if (p.row.codes != nullptr) {
+    const Philox rng(p.rnd, 0);
+    uint32_t codes[2][4], s[2];
+    const uint64_t kpad = uint64_t((p.cols + 31) / 32 * 32);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[32];
+      const T* src = tile + line * P + half * 64 + h * 32;
+#pragma unroll
+      for (int i = 0; i < 32 / E; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(src + i * E);
+        const T* t = reinterpret_cast<const T*>(&w);
+#pragma unroll
+        for (int j = 0; j < E; ++j) v[i * E + j] = as_float(t[j]);
+      }
+      s[h] = quantize32<MX, STOCH>(v, gexp, rng, uint64_t(r0 + line) * kpad + uint64_t(c0 + half * 64 + h * 32), codes[h]);
+    }
+    put64<MX>(p.row, r0 + line, c0 + half * 64, codes[0], codes[1], s[0], s[1]);
+  }
+  if (p.col.codes != nullptr) {
+    const Philox rng(p.rnd, 1);   // the transposed tensor draws from the next offset
+    uint32_t codes[2][4], s[2];
+    const uint64_t kpad = uint64_t((p.rows + 31) / 32 * 32);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[32];
+      const T* src = tile + (half * 64 + h * 32) * P + line;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = as_float(src[i * P]);
+      s[h] = quantize32<MX, STOCH>(v, gexp, rng, uint64_t(c0 + line) * kpad + uint64_t(r0 + half * 64 + h * 32), codes[h]);
+    }
+    put64<MX>(p.col, c0 + line, r0 + half * 64, codes[0], codes[1], s[0], s[1]);
+  }
+}
+
+// Largest finite magnitude of x: an unsigned maximum of the bit patterns, so
+// the order of the atomics does not matter. *amax is 0 on entry.
+template <typename T>
+__global__ void __launch_bounds__(256) fp4_amax_kernel(const T* x, int64_t n, uint32_t* amax) {
+  constexpr int E = 16 / int(sizeof(T));
+  constexpr int U = 4;
+  uint32_t top = 0;
+  auto take = [&](float v) {
+    const uint32_t b = abs_bits(v);
+    top = max(top, b < 0x7F800000u ? b : 0u);
+  };
+  const int64_t full = n / E, stride = int64_t(gridDim.x) * blockDim.x;
+  const int64_t i0 = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+  for (int64_t i = i0; i < full; i += U * stride) {
+    uint4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      w[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (i + u * stride < full) w[u] = __ldg(reinterpret_cast<const uint4*>(x) + i + u * stride);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const T* t = reinterpret_cast<const T*>(&w[u]);
+#pragma unroll
+      for (int j = 0; j < E; ++j) take(as_float(t[j]));
+    }
+  }
+  if (i0 < n - full * E) take(as_float(x[full * E + i0]));
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  __shared__ uint32_t warp_top[8];
+  if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = max(top, warp_top[i]);
+    atomicMax(amax, top);
+  }
+}
+
+// Values of a quantised tensor: a thread takes eight consecutive elements.
+template <typename O, bool MX>
+__global__ void __launch_bounds__(256) fp4_dequantize_kernel(const Fp4In q, O* out) {
+  const int64_t per_row = (q.k + 7) >> 3;
+  const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= q.rows * per_row) return;
+  const int64_t row = i / per_row, k0 = (i - row * per_row) * 8;
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(q.codes + row * q.pitch + (k0 >> 1));
+  const int64_t blk = MX ? k0 >> 5 : k0 >> 4;
+  const uint32_t sc = q.scales[((row >> 7) * q.tiles_k + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3)];
+  float s;
+  if (MX)
+    s = sc == 0xFFu ? __uint_as_float(0x7FC00000u) : pow2(int(sc) - 127);
+  else
+    s = sc == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_value(sc) * pow2(tensor_exponent(q.amax));
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t c = w >> (4 * j);
+    // the three magnitude bits are a tiny float: exponent field and first mantissa bit
+    const float m = __uint_as_float((c & 7u) << 22) * __uint_as_float(253u << 23);   // 2^126
+    v[j] = s * ((c & 8u) ? -m : m);
+  }
+  O* o = out + row * q.k + k0;
+  if ((q.k & 7) == 0) {
+    if constexpr (sizeof(O) == 2) {
+      *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else {
+      reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k0 + j < q.k) {
+        if constexpr (sizeof(O) == 2)
+          o[j] = float_to_bf16_bits(v[j]);
+        else
+          o[j] = v[j];
+      }
+  }
+}
+
+template <typename T, bool MX, bool STOCH>
+cudaError_t quantize_as(const QuantParams& p, cudaStream_t stream) {
+  constexpr size_t smem = size_t(kTile) * kPitch<T> * sizeof(T);
+  auto kern = fp4_quantize_kernel<T, MX, STOCH>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (p.rows + kTile - 1) / kTile * p.tiles_c;
+  kern<<<unsigned(tiles), kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_quantize(const QuantParams& p, bool bf16, bool mx, bool stochastic, cudaStream_t stream) {
+  if (bf16) {
+    if (mx) return stochastic ? quantize_as<uint16_t, true, true>(p, stream) : quantize_as<uint16_t, true, false>(p, stream);
+    return stochastic ? quantize_as<uint16_t, false, true>(p, stream) : quantize_as<uint16_t, false, false>(p, stream);
+  }
+  if (mx) return stochastic ? quantize_as<float, true, true>(p, stream) : quantize_as<float, true, false>(p, stream);
+  return stochastic ? quantize_as<float, false, true>(p, stream) : quantize_as<float, false, false>(p, stream);
+}
+
+cudaError_t launch_fp4_amax(const void* x, bool bf16, int64_t n, float* amax, int sms, cudaStream_t stream) {
+  cudaError_t e = cudaMemsetAsync(amax, 0, sizeof(float), stream);
+  if (e != cudaSuccess) return e;
+  const int64_t want = (n / (bf16 ? 8 : 4) + 1023) / 1024;
+  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(want, int64_t(sms) * 8)));
+  if (bf16)
+    fp4_amax_kernel<uint16_t><<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(x), n, reinterpret_cast<uint32_t*>(amax));
+  else
+    fp4_amax_kernel<float><<<grid, 256, 0, stream>>>(static_cast<const float*>(x), n, reinterpret_cast<uint32_t*>(amax));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp4_dequantize(const Fp4In& q, bool mx, void* out, bool out_bf16, cudaStream_t stream) {
+  const int64_t items = q.rows * ((q.k + 7) / 8);
+  const unsigned grid = unsigned((items + 255) / 256);
+  if (out_bf16) {
+    uint16_t* o = static_cast<uint16_t*>(out);
+    if (mx)
+      fp4_dequantize_kernel<uint16_t, true><<<grid, 256, 0, stream>>>(q, o);
+    else
+      fp4_dequantize_kernel<uint16_t, false><<<grid, 256, 0, stream>>>(q, o);
+  } else {
+    float* o = static_cast<float*>(out);
+    if (mx)
+      fp4_dequantize_kernel<float, true><<<grid, 256, 0, stream>>>(q, o);
+    else
+      fp4_dequantize_kernel<float, false><<<grid, 256, 0, stream>>>(q, o);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace mo

@@ -1,0 +1,116 @@
+// PTX wrappers for 4-bit block-scaled tensor-core products (sm_103a), beside
+// those of ptx.cuh. Written from the PTX ISA descriptions.
+#pragma once
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace mo {
+namespace ptx {
+
+// Instruction descriptor of kind::mxf4 / kind::mxf4nvf4 (e2m1 operands, both
+// K-major, fp32 accumulator).
+//   bits 4-5 B scale id, 7-9 A format (1 = e2m1), 10-12 B format, 17-22 N >> 3,
+//   bit 23 scale type (0 = e4m3, 1 = e8m0), bits 27-28 M >> 7, 29-30 A scale id
+// The scale id is the first byte, of the four in each 32-bit scale column,
+// that the instruction uses (0 or 2; always 0 with four scales a row).
+__host__ __device__ constexpr uint32_t idesc_fp4(uint32_t M, uint32_t N, bool e8m0, uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((e8m0 ? 1u : 0u) << 23) | ((M >> 7) << 27) |
+         (sf_id << 29);
+}
+
+// Shared-memory descriptor of a 512-byte scale tile (32 rows of 16 bytes, no
+// swizzle): 8-row groups of 128 bytes, one after the other.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(128u >> 4) << 32) | (uint64_t(1) << 46);
+}
+
+// Copies a 512-byte scale tile from shared memory to four TMEM columns,
+// repeated in the four lane quarters. kPair: each CTA of the pair copies from
+// its own shared memory to its own TMEM; issued by the even CTA.
+template <bool kPair>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
+  if (kPair)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D (+)= (A sA)(B sB)^T over K = 64. kMx: a scale for 32 elements (e8m0),
+// otherwise for 16 (e4m3). The accumulator, and the A scales, are those of
+// each CTA's own rows; each CTA holds the B scales of all N columns.
+template <bool kPair, bool kMx>
+__device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+#define MO_UMMA_FP4(GROUP, KIND, VEC)                                                                    \
+  asm volatile(                                                                                          \
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                                  \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" KIND ".block_scale.scale_vec::" VEC                      \
+      " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc),        \
+      "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)                                                      \
+      : "memory")
+  if (kPair && kMx) MO_UMMA_FP4("2", "mxf4", "2X");
+  if (kPair && !kMx) MO_UMMA_FP4("2", "mxf4nvf4", "4X");
+  if (!kPair && kMx) MO_UMMA_FP4("1", "mxf4", "2X");
+  if (!kPair && !kMx) MO_UMMA_FP4("1", "mxf4nvf4", "4X");
+#undef MO_UMMA_FP4
+}
+
+// ---------------------------------------------------------------- one CTA by itself
+__device__ __forceinline__ void tmem_alloc_one(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_one() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_one(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void umma_commit_one(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// TMA load into this CTA's shared memory, completion on its own mbarrier.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// ---------------------------------------------------------------- conversions
+// Eight fp32 values to e2m1 (to nearest, ties to even, saturating at 6), the
+// first in the lowest four bits.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+}  // namespace ptx
+}  // namespace mo

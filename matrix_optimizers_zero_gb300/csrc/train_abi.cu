@@ -94,6 +94,50 @@ GradLayout grad_layout(int64_t n, int64_t dim) {
   return L;
 }
 
+// ---------------------------------------------------------------- 4-bit tensors
+constexpr int64_t kMaxFp4Dim = int64_t(1) << 22;
+constexpr int64_t kMaxFp4Elems = int64_t(1) << 37;   // scale tiles and their lines count in 31 bits
+
+int fp4_shape(int64_t rows, int64_t k, int32_t format) {
+  if (format != MO_FP4_MX && format != MO_FP4_NV) return MO_ERR_BAD_PARAM;
+  if (rows < 0 || k < 0 || rows > kMaxFp4Dim || k > kMaxFp4Dim) return MO_ERR_BAD_SHAPE;
+  return (rows + 127) / 128 * 128 * ((k + 127) / 128 * 128) > kMaxFp4Elems ? MO_ERR_BAD_SHAPE : MO_OK;
+}
+
+size_t fp4_codes_bytes(int64_t rows, int64_t k) { return size_t(rows) * size_t((k + 31) / 32 * 16); }
+int64_t fp4_tiles_k(int64_t k, int32_t format) { return format == MO_FP4_MX ? (k + 127) / 128 : (k + 63) / 64; }
+size_t fp4_scales_bytes(int64_t rows, int64_t k, int32_t format) {
+  return size_t((rows + 127) / 128) * size_t(fp4_tiles_k(k, format)) * 512;
+}
+
+// A tensor that is written (or read): its storage's pointers.
+int fp4_storage(const mo_fp4* q, bool need_amax) {
+  const int st = fp4_shape(q->rows, q->k, q->format);
+  if (st != MO_OK) return st;
+  if (q->rows == 0 || q->k == 0) return MO_OK;
+  if (q->codes == nullptr || q->scales == nullptr || (need_amax && q->format == MO_FP4_NV && q->amax == nullptr))
+    return MO_ERR_NULL_POINTER;
+  if (misaligned(q->codes, 16) || misaligned(q->scales, 16) || misaligned(q->amax, 4)) return MO_ERR_MISALIGNED;
+  return MO_OK;
+}
+
+bool fp4_overlaps(const mo_fp4* q, const void* p, size_t bytes) {
+  return overlap(q->codes, fp4_codes_bytes(q->rows, q->k), p, bytes) ||
+         overlap(q->scales, fp4_scales_bytes(q->rows, q->k, q->format), p, bytes) ||
+         (q->format == MO_FP4_NV && overlap(q->amax, 4, p, bytes));
+}
+
+mo::Fp4In fp4_in(const mo_fp4* q) {
+  return {static_cast<const uint8_t*>(q->codes), static_cast<const uint8_t*>(q->scales),
+          q->format == MO_FP4_NV ? q->amax : nullptr, q->rows, q->k, (q->k + 31) / 32 * 16, (q->rows + 127) / 128,
+          fp4_tiles_k(q->k, q->format)};
+}
+
+mo::Fp4Out fp4_out(const mo_fp4* q) {
+  return {static_cast<uint8_t*>(q->codes), static_cast<uint8_t*>(q->scales), q->format == MO_FP4_NV ? q->amax : nullptr,
+          q->rows, q->k, (q->k + 31) / 32 * 16, (q->rows + 127) / 128, fp4_tiles_k(q->k, q->format)};
+}
+
 }  // namespace
 
 extern "C" {
@@ -211,6 +255,103 @@ int embed_grad(const void* dout, int32_t dout_dtype, const mo_tokens* tokens, in
   while ((int64_t(1) << bits) <= vocab) ++bits;   // the keys run from 0 to vocab
   p.passes = (bits + 8) / 9;
   const cudaError_t e = mo::launch_embed_grad(p, dout_dtype == MO_BF16, sms, stream);
+  return e != cudaSuccess ? report_cuda(e) : MO_OK;
+}
+
+size_t mo_fp4_codes_bytes(int64_t rows, int64_t k) {
+  return fp4_shape(rows, k, MO_FP4_MX) == MO_OK ? fp4_codes_bytes(rows, k) : 0;
+}
+
+size_t mo_fp4_scales_bytes(int64_t rows, int64_t k, int32_t format) {
+  return fp4_shape(rows, k, format) == MO_OK ? fp4_scales_bytes(rows, k, format) : 0;
+}
+
+int fp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, const mo_fp4* by_row, const mo_fp4* by_col,
+                 const float* amax, const mo_random* stochastic, cudaStream_t stream) {
+  if (by_row == nullptr && by_col == nullptr) return MO_ERR_NULL_POINTER;
+  if (!dtype_ok(dtype)) return MO_ERR_BAD_PARAM;
+  const int32_t format = by_row != nullptr ? by_row->format : by_col->format;
+  int st = fp4_shape(rows, cols, format);
+  if (st != MO_OK) return st;
+  for (const mo_fp4* q : {by_row, by_col}) {
+    if (q == nullptr) continue;
+    if (q->format != format) return MO_ERR_BAD_PARAM;
+    if (q->rows != (q == by_row ? rows : cols) || q->k != (q == by_row ? cols : rows)) return MO_ERR_BAD_SHAPE;
+    if ((st = fp4_storage(q, true)) != MO_OK) return st;
+  }
+  mo::QuantParams p = {};
+  if (stochastic != nullptr && (st = random_args(*stochastic, &p.rnd)) != MO_OK) return st;
+  if (misaligned(amax, 4)) return MO_ERR_MISALIGNED;
+  if (rows == 0 || cols == 0) return MO_OK;
+  if (x == nullptr) return MO_ERR_NULL_POINTER;
+  if (misaligned(x, 16)) return MO_ERR_MISALIGNED;
+  const size_t x_bytes = size_t(rows) * size_t(cols) * dtype_bytes(dtype);
+  for (const mo_fp4* q : {by_row, by_col})
+    if (q != nullptr && (fp4_overlaps(q, x, x_bytes) ||
+                         overlap(q->codes, fp4_codes_bytes(q->rows, q->k), q->scales, fp4_scales_bytes(q->rows, q->k, format))))
+      return MO_ERR_OVERLAP;
+  if (by_row != nullptr && by_col != nullptr &&
+      (fp4_overlaps(by_row, by_col->codes, fp4_codes_bytes(cols, rows)) ||
+       fp4_overlaps(by_row, by_col->scales, fp4_scales_bytes(cols, rows, format))))
+    return MO_ERR_OVERLAP;
+  int sms = 0;
+  int* status = nullptr;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  p.x = x;
+  p.rows = rows;
+  p.cols = cols;
+  p.tiles_c = (cols + 127) / 128;
+  p.vec = cols % (16 / int64_t(dtype_bytes(dtype))) == 0 ? 1 : 0;
+  if (by_row != nullptr) p.row = fp4_out(by_row);
+  if (by_col != nullptr) p.col = fp4_out(by_col);
+  cudaError_t e = cudaSuccess;
+  if (format == MO_FP4_NV) {
+    p.amax = amax;
+    if (amax == nullptr) {
+      float* top = p.row.amax != nullptr ? p.row.amax : p.col.amax;
+      if ((e = mo::launch_fp4_amax(x, dtype == MO_BF16, rows * cols, top, sms, stream)) != cudaSuccess) return report_cuda(e);
+      p.amax = top;
+    }
+  }
+  e = mo::launch_fp4_quantize(p, dtype == MO_BF16, format == MO_FP4_MX, stochastic != nullptr, stream);
+  return e != cudaSuccess ? report_cuda(e) : MO_OK;
+}
+
+int fp4_dequantize(const mo_fp4* q, void* out, int32_t dtype, cudaStream_t stream) {
+  if (q == nullptr) return MO_ERR_NULL_POINTER;
+  if (!dtype_ok(dtype)) return MO_ERR_BAD_PARAM;
+  int st = fp4_storage(q, true);
+  if (st != MO_OK) return st;
+  if (q->rows == 0 || q->k == 0) return MO_OK;
+  if (out == nullptr) return MO_ERR_NULL_POINTER;
+  if (misaligned(out, 16)) return MO_ERR_MISALIGNED;
+  if (fp4_overlaps(q, out, size_t(q->rows) * size_t(q->k) * dtype_bytes(dtype))) return MO_ERR_OVERLAP;
+  int sms = 0;
+  int* status = nullptr;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  const cudaError_t e = mo::launch_fp4_dequantize(fp4_in(q), q->format == MO_FP4_MX, out, dtype == MO_BF16, stream);
+  return e != cudaSuccess ? report_cuda(e) : MO_OK;
+}
+
+int fp4_product(const mo_fp4* a, const mo_fp4* b, void* out, int32_t dtype, cudaStream_t stream) {
+  if (a == nullptr || b == nullptr) return MO_ERR_NULL_POINTER;
+  if (!dtype_ok(dtype)) return MO_ERR_BAD_PARAM;
+  int st = fp4_storage(a, true);
+  if (st != MO_OK) return st;
+  if ((st = fp4_storage(b, true)) != MO_OK) return st;
+  if (a->format != b->format) return MO_ERR_BAD_PARAM;
+  if (a->k != b->k) return MO_ERR_BAD_SHAPE;
+  if (a->rows == 0 || b->rows == 0) return MO_OK;
+  if (out == nullptr) return MO_ERR_NULL_POINTER;
+  if (misaligned(out, 16)) return MO_ERR_MISALIGNED;
+  const size_t out_bytes = size_t(a->rows) * size_t(b->rows) * dtype_bytes(dtype);
+  if (fp4_overlaps(a, out, out_bytes) || fp4_overlaps(b, out, out_bytes)) return MO_ERR_OVERLAP;
+  int sms = 0;
+  int* status = nullptr;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  const cudaError_t e =
+      a->k == 0 ? cudaMemsetAsync(out, 0, out_bytes, stream)   // the sum over nothing
+                : mo::launch_fp4_product(fp4_in(a), fp4_in(b), a->format == MO_FP4_MX, out, dtype == MO_BF16, sms, status, stream);
   return e != cudaSuccess ? report_cuda(e) : MO_OK;
 }
 

@@ -84,4 +84,39 @@ struct GradParams {
 };
 cudaError_t launch_embed_grad(const GradParams& p, bool dout_bf16, int sms, cudaStream_t stream);
 
+// ---------------------------------------------------------------- 4-bit tensors
+// Storage of a 4-bit tensor [rows, k]: codes, two a byte (the even element in
+// the low half), rows of `pitch` = 16 ceil(k / 32) bytes; scales in tiles of
+// 128 rows by 4 blocks, the 512-byte order that the tensor core's scale copy
+// takes: row r, block b of a tile at byte (r % 32) 16 + (r / 32) 4 + b.
+struct Fp4Out {
+  uint8_t* codes;          // null: this orientation is not wanted
+  uint8_t* scales;
+  float* amax;             // nv: receives the magnitude that fixes the tensor's scale
+  int64_t rows, k, pitch;
+  int64_t tiles_r, tiles_k;
+};
+struct Fp4In {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* amax;       // or null: the tensor's own scale is 1
+  int64_t rows, k, pitch;
+  int64_t tiles_r, tiles_k;
+};
+
+struct QuantParams {
+  const void* x;           // [rows, cols]
+  const float* amax;       // nv: its largest magnitude
+  int64_t rows, cols, tiles_c;
+  Fp4Out row, col;         // blocks along the rows of x, and along its columns (transposed)
+  RandomArgs rnd;          // of stochastic rounding
+  int32_t vec;             // rows are 16-byte aligned
+};
+cudaError_t launch_fp4_quantize(const QuantParams& p, bool bf16, bool mx, bool stochastic, cudaStream_t stream);
+cudaError_t launch_fp4_amax(const void* x, bool bf16, int64_t n, float* amax, int sms, cudaStream_t stream);
+cudaError_t launch_fp4_dequantize(const Fp4In& q, bool mx, void* out, bool out_bf16, cudaStream_t stream);
+// out [a.rows, b.rows] = A B^T; a.k == b.k.
+cudaError_t launch_fp4_product(const Fp4In& a, const Fp4In& b, bool mx, void* out, bool out_bf16, int sms, int* status,
+                               cudaStream_t stream);
+
 }  // namespace mo

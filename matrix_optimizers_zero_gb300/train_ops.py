@@ -1,5 +1,6 @@
 """Binding of the training-step operators around the optimizer (include/mo.h):
-embedding lookup and its gradient, and counter-based dropout.
+embedding lookup and its gradient, counter-based dropout, and microscaled 4-bit
+quantisation with its product.
 
 Tensors are contiguous CUDA tensors on the current device, fp32 or bf16;
 outputs are written in place, on the current stream unless one is given:
@@ -9,6 +10,12 @@ outputs are written in place, on the current stream unless one is given:
     ws = mo.embed_grad_workspace(tokens.numel(), *table.shape)   # reuse it every step
     mo.embed_grad(dx, tokens, g, ws, scale=1.0, dropout=drop)    # g: the fp32 gradient adamw_tail_step reads
     mo.dropout_apply(h, y, drop, residual=x)               # forward; with dy for h the backward pass
+
+    wq, wt = mo.Fp4Tensor(n, k, "mx"), mo.Fp4Tensor(k, n, "mx")   # "mx": 32-element blocks; "nv": 16
+    mo.fp4_quantize(w, wq, wt)                             # both orientations from one pass over w
+    mo.fp4_quantize(dy, dyq, dyt, stochastic=mo.Random(seed, step))
+    mo.fp4_product(xq, wq, y)                              # y = x w^T
+    mo.fp4_product(dyt, xt, dw)                            # dw = dy^T x: the bf16 gradient muon_owner_step reads
 """
 from __future__ import annotations
 
@@ -143,3 +150,90 @@ def embed_grad(dout, tokens, grad, workspace, scale: float = 1.0, padding_idx: i
                                    grad.data_ptr(), int(accumulate), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), _stream_ptr(stream))
     _check(st, "embed_grad")
+
+
+# ---------------------------------------------------------------- 4-bit tensors
+
+FP4_FORMATS = {"mx": 0, "nv": 1}   # mo_fp4_format
+
+
+class MoFp4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("amax", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("k", ctypes.c_int64), ("format", ctypes.c_int32)]
+
+
+def mo_fp4_codes_bytes(rows: int, k: int) -> int:
+    return int(load_library().mo_fp4_codes_bytes(rows, k))
+
+
+def mo_fp4_scales_bytes(rows: int, k: int, fmt: str = "mx") -> int:
+    return int(load_library().mo_fp4_scales_bytes(rows, k, FP4_FORMATS[fmt]))
+
+
+class Fp4Tensor:
+    """Storage of a microscaled 4-bit tensor [rows, k] (mo_fp4): uint8 `codes`
+    and `scales` and, for "nv", a one-element fp32 `amax`. Allocated when not
+    given; reuse it every step."""
+
+    def __init__(self, rows: int, k: int, fmt: str = "mx", codes=None, scales=None, amax=None, device=None):
+        import torch
+        if fmt not in FP4_FORMATS:
+            raise ValueError('format must be "mx" or "nv"')
+        device = device or torch.device("cuda")
+        sizes = mo_fp4_codes_bytes(rows, k), mo_fp4_scales_bytes(rows, k, fmt)
+        if rows and k and not all(sizes):
+            raise ValueError("rows and k must be 0 to 2^22, with at most 2^37 elements")
+        got = []
+        for t, nbytes, name in ((codes, sizes[0], "codes"), (scales, sizes[1], "scales")):
+            if t is None:
+                t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            if t.dtype != torch.uint8 or t.numel() != nbytes:
+                raise ValueError(f"{name} must be {nbytes} uint8 elements")
+            _dense(t, name)
+            got.append(t)
+        self.codes, self.scales = got
+        if amax is None and fmt == "nv":
+            amax = torch.ones(1, dtype=torch.float32, device=device)
+        self.amax = _amax(amax)
+        self.rows, self.k, self.format = rows, k, fmt
+        self.arg = MoFp4(self.codes.data_ptr(), self.scales.data_ptr(), None if amax is None else amax.data_ptr(), rows, k,
+                         FP4_FORMATS[fmt])
+
+
+def _amax(t):
+    import torch
+    if t is not None and (t.dtype != torch.float32 or t.numel() != 1 or not t.is_cuda):
+        raise TypeError("amax must be a one-element fp32 CUDA tensor")
+    return t
+
+
+def fp4_quantize(x, by_row: Optional[Fp4Tensor] = None, by_col: Optional[Fp4Tensor] = None, amax=None,
+                 stochastic: Optional[Random] = None, stream=None) -> None:
+    """Quantises x [rows, cols] into by_row [rows, cols] and, transposed, into
+    by_col [cols, rows]. "nv" tensors take their scale from amax (a one-element
+    fp32 CUDA tensor) or from x itself."""
+    code = _dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2D")
+    st = load_library().fp4_quantize(x.data_ptr(), code, x.shape[0], x.shape[1],
+                                     None if by_row is None else ctypes.byref(by_row.arg),
+                                     None if by_col is None else ctypes.byref(by_col.arg),
+                                     None if amax is None else _amax(amax).data_ptr(), _ref(stochastic), _stream_ptr(stream))
+    _check(st, "fp4_quantize")
+
+
+def fp4_dequantize(q: Fp4Tensor, out, stream=None) -> None:
+    """out [rows, k] = the values q stands for."""
+    code = _dtype(out, "out")
+    if out.numel() != q.rows * q.k:
+        raise ValueError("out must be [rows, k]")
+    _check(load_library().fp4_dequantize(ctypes.byref(q.arg), out.data_ptr(), code, _stream_ptr(stream)), "fp4_dequantize")
+
+
+def fp4_product(a: Fp4Tensor, b: Fp4Tensor, out, stream=None) -> None:
+    """out [a.rows, b.rows] = a b^T over k; out is bf16 or fp32."""
+    code = _dtype(out, "out")
+    if out.numel() != a.rows * b.rows:
+        raise ValueError("out must be [a.rows, b.rows]")
+    _check(load_library().fp4_product(ctypes.byref(a.arg), ctypes.byref(b.arg), out.data_ptr(), code, _stream_ptr(stream)),
+           "fp4_product")

@@ -66,3 +66,81 @@ def embed_grad(dout, tokens, vocab, scale=1.0, padding_idx=-1, drop=None, so_far
         if 0 <= v < vocab and v != padding_idx:
             g[v] += scale * d[t]
     return g
+
+
+# ---------------------------------------------------------------- 4-bit tensors
+
+FP4_BLOCK = {"mx": 32, "nv": 16}
+FP4_GRID = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+
+def fp4_scale_values(fmt):
+    """Value of every scale byte, increasing: e8m0, or the finite e4m3 from 0."""
+    if fmt == "mx":
+        return np.ldexp(1.0, np.arange(-127, 128))
+    i = np.arange(127)
+    return np.where(i < 8, i / 512.0, np.ldexp(8.0 + i % 8, i // 8 - 10))
+
+
+def fp4_tensor_scale(amax):
+    """Smallest power of two g (from 2^-126) with amax <= 2688 g; 1 for 0."""
+    if not (0 < amax < np.inf):
+        return 1.0
+    e = -126
+    while 2688.0 * 2.0 ** e < amax:
+        e += 1
+    return 2.0 ** e
+
+
+def fp4_quantize(x, fmt, stochastic=None, amax=None):
+    """(codes [rows, k] 0-15, scale bytes [rows, blocks], values) of x (64 bits),
+    blocks along its rows. stochastic: (seed, offset) or None."""
+    x = np.asarray(x, np.float64)
+    rows, k = x.shape
+    B = FP4_BLOCK[fmt]
+    kp = (k + 31) // 32 * 32
+    pad = np.zeros((rows, kp))
+    pad[:, :k] = x
+    v = pad.reshape(rows, kp // B, B)
+    finite = np.isfinite(v)
+    if amax is None:
+        amax = np.abs(v[finite]).max() if finite.any() else 0.0
+    g = fp4_tensor_scale(amax) if fmt == "nv" else 1.0
+    sv = fp4_scale_values(fmt) * g
+    bad = ~finite.all(axis=2)
+    w = np.where(bad[..., None], 0.0, v)
+    bits = np.minimum(np.searchsorted(6 * sv, np.abs(w).max(axis=2)), len(sv) - 1)
+    s = sv[bits][..., None]
+    y = np.minimum(np.where(s > 0, np.abs(w) / np.where(s > 0, s, 1), 0.0), 6.0)
+    lo = np.searchsorted(FP4_GRID, y, side="right") - 1
+    hi = np.minimum(lo + 1, 7)
+    gap = np.where(hi > lo, FP4_GRID[hi] - FP4_GRID[lo], 1.0)
+    if stochastic is None:
+        part = (y - FP4_GRID[lo]) / gap
+        up = (part > 0.5) | ((part == 0.5) & (lo % 2 == 1))
+    else:
+        u = random16(rows * kp, *stochastic).reshape(v.shape)
+        up = np.floor(np.floor((y - FP4_GRID[lo]) * 131072) / (gap * 2)) + u >= 65536
+    c = np.where(up, hi, lo)
+    values = FP4_GRID[c] * s * np.where(np.signbit(w), -1.0, 1.0)
+    codes = c + 8 * np.signbit(w)
+    nb = (k + B - 1) // B
+    bits = np.where(bad, 255 if fmt == "mx" else 127, bits)
+    values = np.where(bad[..., None], np.nan, values)
+    return codes.reshape(rows, kp)[:, :k], bits[:, :nb], values.reshape(rows, kp)[:, :k]
+
+
+def fp4_pack(codes, bits, fmt):
+    """(codes, scales) bytes in the library's storage order."""
+    rows, k = codes.shape
+    kp = (k + 31) // 32 * 32
+    c = np.zeros((rows, kp), np.uint8)
+    c[:, :k] = codes
+    packed = (c[:, 0::2] | (c[:, 1::2] << 4)).astype(np.uint8).reshape(-1)
+    per_tile = 4 * FP4_BLOCK[fmt]
+    tk = (k + per_tile - 1) // per_tile
+    s = np.zeros((rows + 127) // 128 * tk * 512, np.uint8)
+    for r in range(rows):
+        for b in range(bits.shape[1]):
+            s[(r // 128 * tk + b // 4) * 512 + r % 32 * 16 + r % 128 // 32 * 4 + b % 4] = bits[r, b]
+    return packed, s

@@ -146,3 +146,115 @@ def test_grad_workspace_bytes(lib):
 
 def test_status_names_the_bad_token(lib):
     assert "token" in mo.mo_status_string(-11)
+
+
+# ---------------------------------------------------------------- 4-bit tensors
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_fp4_oracle_rounds_to_nearest_and_never_saturates(fmt):
+    rng = np.random.default_rng(1)
+    x = rng.normal(size=(40, 100)) * np.exp(2 * rng.normal(size=(40, 1)))
+    codes, bits, values = ot.fp4_quantize(x, fmt)
+    s = ot.fp4_scale_values(fmt)[bits] * (ot.fp4_tensor_scale(np.abs(x).max()) if fmt == "nv" else 1.0)
+    B = ot.FP4_BLOCK[fmt]
+    for r in range(40):
+        for k in range(100):
+            grid = np.concatenate([-ot.FP4_GRID, ot.FP4_GRID]) * s[r, k // B]
+            assert abs(values[r, k] - x[r, k]) <= np.abs(grid - x[r, k]).min() * (1 + 1e-12)
+            assert abs(x[r, k]) <= 6 * s[r, k // B]
+    # the next smaller scale would not do
+    for r in range(40):
+        for b in range(bits.shape[1]):
+            if bits[r, b] > 0:
+                smaller = s[r, b] * ot.fp4_scale_values(fmt)[bits[r, b] - 1] / ot.fp4_scale_values(fmt)[bits[r, b]]
+                assert np.abs(x[r, b * B:(b + 1) * B]).max() > 6 * smaller * (1 - 1e-15)
+
+
+def test_fp4_oracle_ties_go_to_the_even_code():
+    # scale 1 (the block's maximum is 6): the midpoints of the grid
+    x = np.zeros((1, 32))
+    x[0, :8] = [6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5]
+    codes, bits, values = ot.fp4_quantize(x, "mx")
+    assert bits[0, 0] == 127
+    assert list(values[0, :8]) == [6, 0, 1, 1, 2, 2, 4, 4]
+
+
+def test_fp4_oracle_stochastic_rounding_is_unbiased():
+    n = 32 * 4000
+    x = np.tile(np.linspace(-6, 6, 32), 4000).reshape(4000, 32)
+    _, _, values = ot.fp4_quantize(x, "mx", (5, 6))
+    mean = values.mean(axis=0)
+    # the widest step is 2: a standard deviation of at most 1 an element
+    assert np.all(np.abs(mean - x[0]) < 5 / np.sqrt(4000) + 2 ** -15)
+
+
+@pytest.mark.parametrize("amax,g", [(2688.0, 1.0), (2688.1, 2.0), (1344.0, 0.5), (0.0, 1.0), (1e-45, 2.0 ** -126)])
+def test_fp4_oracle_tensor_scale(amax, g):
+    assert ot.fp4_tensor_scale(amax) == g
+
+
+class Fp4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("amax", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("k", ctypes.c_int64), ("format", ctypes.c_int32)]
+
+
+def q4(rows=64, k=96, fmt=0, codes=C, scales=D_, amax=E_):
+    return Fp4(codes, scales, amax, rows, k, fmt)
+
+
+def ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+def call_quantize(lib, x=A, dt=0, rows=64, cols=96, row=q4(), col=None, amax=None, rnd=None):
+    return lib.fp4_quantize(x, dt, rows, cols, ref(row), ref(col), amax, ref(rnd), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(row=None), NULL), (dict(x=None), NULL), (dict(row=q4(codes=None)), NULL), (dict(row=q4(scales=None)), NULL),
+    (dict(row=q4(fmt=1, amax=None)), NULL), (dict(dt=5), PARAM), (dict(row=q4(fmt=2)), PARAM),
+    (dict(col=q4(96, 64, 1, B, B + 65536)), PARAM), (dict(rows=-1), SHAPE), (dict(row=q4(63)), SHAPE),
+    (dict(col=q4(64, 96, 0, B, B + 65536)), SHAPE), (dict(cols=2 ** 22 + 1), SHAPE), (dict(x=A + 8), ALIGN),
+    (dict(row=q4(codes=C + 8)), ALIGN), (dict(row=q4(scales=D_ + 4)), ALIGN), (dict(amax=E_ + 2), ALIGN),
+    (dict(rnd=mo.Random(1), row=q4(fmt=1, amax=E_ + 1)), ALIGN), (dict(row=q4(codes=A + 64)), OVERLAP),
+    (dict(row=q4(scales=C + 16)), OVERLAP), (dict(col=q4(96, 64, 0, C + 16, B)), OVERLAP),
+])
+def test_quantize_refusals(lib, kw, status):
+    assert call_quantize(lib, **kw) == status
+
+
+def call_product(lib, a=None, b=None, out=B, dt=1):
+    a = a if a is not None else q4()
+    b = b if b is not None else q4(32, 96, 0, A, A + 65536)
+    return lib.fp4_product(ref(a), ref(b), out, dt, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(a=q4(codes=None)), NULL), (dict(out=None), NULL), (dict(a=q4(fmt=1)), PARAM), (dict(dt=9), PARAM),
+    (dict(a=q4(k=64)), SHAPE), (dict(a=q4(rows=-3)), SHAPE), (dict(a=q4(2 ** 22, 2 ** 22)), SHAPE), (dict(out=B + 8), ALIGN),
+    (dict(out=C), OVERLAP), (dict(out=A + 65536), OVERLAP),
+])
+def test_product_refusals(lib, kw, status):
+    assert call_product(lib, **kw) == status
+
+
+def test_dequantize_refusals(lib):
+    assert lib.fp4_dequantize(None, B, 0, None) == NULL
+    assert lib.fp4_dequantize(ref(q4()), None, 0, None) == NULL
+    assert lib.fp4_dequantize(ref(q4()), B, 3, None) == PARAM
+    assert lib.fp4_dequantize(ref(q4()), B + 4, 0, None) == ALIGN
+    assert lib.fp4_dequantize(ref(q4()), C, 0, None) == OVERLAP
+    assert lib.fp4_dequantize(ref(q4(k=-1)), B, 0, None) == SHAPE
+
+
+def test_fp4_empty_calls_are_no_ops(lib):
+    assert call_quantize(lib, rows=0, row=q4(0, 96)) == 0
+    assert call_product(lib, a=q4(0)) == 0
+    assert lib.fp4_dequantize(ref(q4(0, 96)), None, 0, None) == 0
+
+
+def test_fp4_storage_sizes(lib):
+    assert mo.mo_fp4_codes_bytes(3, 33) == 3 * 32
+    assert mo.mo_fp4_scales_bytes(129, 129, "mx") == 2 * 2 * 512
+    assert mo.mo_fp4_scales_bytes(1, 65, "nv") == 2 * 512
+    assert mo.mo_fp4_codes_bytes(-1, 4) == 0 and mo.mo_fp4_scales_bytes(4, 2 ** 23, "nv") == 0
