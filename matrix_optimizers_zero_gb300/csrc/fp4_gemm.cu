@@ -110,25 +110,34 @@ __device__ __forceinline__ void store32<float>(float* row, int64_t col, int64_t 
 // ------------------------------------------------------------------ pairs
 //
 // Warp 0 of each CTA loads its 128-row halves of A and B, its A scales and all
-// 256 rows' B scales; the even CTA's warp 1 copies scales and issues the
-// instructions; eight warps drain 128 lanes x 256 columns.
+// 256 rows' B scales; warps 10-13 put the scales into TMEM; the even CTA's
+// warp 1 issues the instructions; warps 2-9 drain 128 lanes x 256 columns.
 //
-// TMEM: a 256 x 256 accumulator takes 256 columns and a stage's scales up to
-// 48, so two whole accumulators do not fit. They overlap in 48 columns,
-// [208, 256): the epilogue drains those first, and the next tile starts as
-// soon as they are free.
+// Scales: the tensor core's own copy (tcgen05.cp) runs in its instruction
+// stream, about 30 cycles a 512-byte tile beside 200 for an instruction (six to
+// twelve tiles for four instructions). Stores from registers (tcgen05.st) run
+// beside it: 8192^3 with mx 266 -> see the table in the documentation.
+//
+// TMEM: an accumulator takes 256 columns and a stage's scales 24 (mx) or 48
+// (nv), and a stage's scales are written while the last one's are in use. So
+// the two accumulators overlap in 96 columns, [160, 256): the epilogue drains
+// those first, and the next tile starts as soon as they are free.
 constexpr int kEpiWarps = 8;
-constexpr int kPairThreads = 64 + 32 * kEpiWarps;
+constexpr int kSfWarps = 4;
+constexpr int kPairThreads = 64 + 32 * (kEpiWarps + kSfWarps);
 constexpr int kPairStages = 5;
-constexpr uint32_t kAccStep = 208;
-constexpr uint32_t kSfCol = 464;
-constexpr uint32_t kSfColStep = 12;   // A 4 columns, B 8, a scale tile
+constexpr uint32_t kAccStep = 160;
+constexpr uint32_t kSfCol = 416;
+template <bool MX>
+constexpr uint32_t kSfCols = 12 * kSfTiles<MX>;    // A 4 columns, B 8, for every scale tile of a stage
+template <bool MX>
+constexpr int kSfSlots = int(96 / kSfCols<MX>);    // stages whose scales TMEM holds
 template <bool MX>
 constexpr uint32_t kPairStageBytes = 2 * kPanelBytes + 3 * kSfBytes<MX>;
-constexpr uint32_t kPairBars = 2 * kPairStages + 7;
+constexpr uint32_t kPairBars = 3 * kPairStages + 7 + 4;
 template <bool MX>
 constexpr size_t kPairSmem = 1024 + size_t(kPairStages) * kPairStageBytes<MX> + 256;
-static_assert(kAccStep + 256 <= kSfCol && kSfCol + 4 * kSfColStep <= 512, "TMEM columns");
+static_assert(kAccStep + 256 <= kSfCol && kSfCol + 96 <= 512, "TMEM columns");
 static_assert(8 * kPairBars + 32 <= 256, "control block");
 static_assert(kPairSmem<false> <= 227 * 1024, "shared memory");
 
@@ -144,7 +153,8 @@ __device__ __forceinline__ void tile_at(int32_t t, int32_t tiles_m, int32_t tile
 template <bool MX, typename O>
 __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr uint32_t kStage = kPairStageBytes<MX>;
+  constexpr uint32_t kStage = 2 * kPanelBytes;   // codes; their bytes count on the even CTA's barriers
+  constexpr int kSlots = kSfSlots<MX>;
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   // panels first (1024-byte aligned), then the scale tiles of every stage, then control
@@ -160,6 +170,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   auto tempty_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + 2 + s); };
   auto over_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + 4 + s); };
   const uint32_t drain_bar = bars + 8u * uint32_t(2 * kPairStages + 6);
+  auto sf_full_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + 7 + s); };    // scales in shared memory
+  auto sf_ready_bar = [&](int s) { return bars + 8u * uint32_t(3 * kPairStages + 7 + s); };   // scales in TMEM, both CTAs
 
   const int warp = int(threadIdx.x >> 5);
   const int lane = int(threadIdx.x & 31);
@@ -170,12 +182,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     for (int s = 0; s < kPairStages; ++s) {
       ptx::mbar_init(full_bar(s), 1);
       ptx::mbar_init(empty_bar(s), 1);
+      ptx::mbar_init(sf_full_bar(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(tfull_bar(s), 1);
       ptx::mbar_init(tempty_bar(s), 2 * kEpiWarps);
-      ptx::mbar_init(over_bar(s), kEpiWarps);   // four warps of each CTA
+      ptx::mbar_init(over_bar(s), 2 * kEpiWarps);
     }
+    for (int s = 0; s < kSlots; ++s) ptx::mbar_init(sf_ready_bar(s), 2 * kSfWarps);
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0;
     peer_report[0] = 0u;
@@ -219,9 +233,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           ptx::tma_load_2d_pair(sa, &p.a, fb, kb * 128, ra * 128);
           ptx::tma_load_2d_pair(sa + kPanelBytes, &p.b, fb, kb * 128, rb * 128);
           const int32_t at = kb * kSfTiles<MX>;
-          ptx::tma_load_2d_pair(sf, &p.sa, fb, 0, (ra * p.tiles_k + at) * 2);
-          ptx::tma_load_2d_pair(sf + kSfBytes<MX>, &p.sb, fb, 0, (tn * 2 * p.tiles_k + at) * 2);
-          ptx::tma_load_2d_pair(sf + 2 * kSfBytes<MX>, &p.sb, fb, 0, ((tn * 2 + 1) * p.tiles_k + at) * 2);
+          const uint32_t sfb = sf_full_bar(stage);
+          ptx::mbar_arrive_expect_tx(sfb, 3 * kSfBytes<MX>);
+          ptx::tma_load_2d(sf, &p.sa, sfb, 0, (ra * p.tiles_k + at) * 2);
+          ptx::tma_load_2d(sf + kSfBytes<MX>, &p.sb, sfb, 0, (tn * 2 * p.tiles_k + at) * 2);
+          ptx::tma_load_2d(sf + 2 * kSfBytes<MX>, &p.sb, sfb, 0, ((tn * 2 + 1) * p.tiles_k + at) * 2);
           ++n_issued;
           if (++stage == kPairStages) {
             stage = 0;
@@ -233,8 +249,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ MMA issuer (even CTA)
-      int stage = 0;
-      uint32_t ph = 0;
+      int stage = 0, slot = 0;
+      uint32_t ph = 0, sph = 0;
       bool ok = true;
       int32_t i = 0;
       for (int32_t t = first; ok && t < ntiles; t += step, ++i) {
@@ -247,34 +263,28 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         const uint32_t d = tmem + uint32_t(acc) * kAccStep;
         int32_t left = p.steps;
         for (int32_t kb = 0; kb < p.stages; ++kb) {
-          if (!mbar_wait_bounded(full_bar(stage), ph, abort_flag, p.status, p.timeout_ns)) {
+          if (!mbar_wait_bounded(sf_ready_bar(slot), sph, abort_flag, p.status, p.timeout_ns) ||
+              !mbar_wait_bounded(full_bar(stage), ph, abort_flag, p.status, p.timeout_ns)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
           const uint32_t sa = base + uint32_t(stage) * 2u * kPanelBytes;
           const uint32_t sb = sa + kPanelBytes;
-          const uint32_t sf = sf_base + uint32_t(stage) * 3u * kSfBytes<MX>;
-#pragma unroll
-          for (int a = 0; a < kSfTiles<MX>; ++a) {
-            const uint32_t c = tmem + kSfCol + uint32_t(a) * kSfColStep;
-            if (left > a * kStepsPerTile<MX>) {
-              ptx::tmem_copy_scales<true>(c, ptx::smem_desc_scales(sf + 512u * uint32_t(a)));
-              ptx::tmem_copy_scales<true>(c + 4, ptx::smem_desc_scales(sf + kSfBytes<MX> + 512u * uint32_t(a)));
-              ptx::tmem_copy_scales<true>(c + 8, ptx::smem_desc_scales(sf + 2 * kSfBytes<MX> + 512u * uint32_t(a)));
-            }
-          }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk < left) {
               constexpr uint32_t idesc0 = ptx::idesc_fp4(256, 256, MX, 0);
               constexpr uint32_t idesc2 = ptx::idesc_fp4(256, 256, MX, 2);
-              const int a = kk / kStepsPerTile<MX>;
-              const uint32_t c = tmem + kSfCol + uint32_t(a) * kSfColStep;
+              const uint32_t c = tmem + kSfCol + uint32_t(slot) * kSfCols<MX> + 12u * uint32_t(kk / kStepsPerTile<MX>);
               ptx::umma_fp4<true, MX>(d, ptx::smem_desc_sw128(sa + uint32_t(kk) * 32u, 16u, 1024u),
                                       ptx::smem_desc_sw128(sb + uint32_t(kk) * 32u, 16u, 1024u),
                                       MX && (kk & 1) ? idesc2 : idesc0, c, c + 4, (kb | kk) != 0 ? 1u : 0u);
             }
+          }
+          if (++slot == kSlots) {
+            slot = 0;
+            sph ^= 1u;
           }
           left -= 4;
           ptx::umma_commit_pair(empty_bar(stage), 0x3);
@@ -286,6 +296,54 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         }
         if (!ok) break;
         ptx::umma_commit_pair(tfull_bar(acc), 0x3);
+      }
+    }
+  } else if (warp >= 2 + kEpiWarps) {
+    // -------------------------------------------------------------- scales (both CTAs)
+    // Lane l of every quarter holds, column by column, the scales of rows l, 32 + l, 64 + l, 96 + l
+    // of a 512-byte tile: 16 consecutive bytes of it.
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    int stage = 0, slot = 0;
+    uint32_t ph = 0;
+    uint32_t j = 0;   // stages so far
+    bool ok = true;
+    for (int32_t t = first; ok && t < ntiles; t += step) {
+      for (int32_t kb = 0; kb < p.stages; ++kb, ++j) {
+        // the slot's last stage has been multiplied (and its shared memory may be refilled)
+        if (j >= uint32_t(kSlots)) {
+          const uint32_t u = j - uint32_t(kSlots);
+          ok = mbar_wait_bounded(empty_bar(int(u % kPairStages)), (u / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
+        }
+        ok = ok && mbar_wait_bounded(sf_full_bar(stage), ph, abort_flag, p.status, p.timeout_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        const uint8_t* src = smem_raw + (sf_base - raw) + uint32_t(stage) * 3u * kSfBytes<MX> + 16 * lane;
+        uint32_t w[kSfCols<MX>];
+#pragma unroll
+        for (int a = 0; a < kSfTiles<MX>; ++a)
+#pragma unroll
+          for (int o = 0; o < 3; ++o)
+            *reinterpret_cast<uint4*>(w + 12 * a + 4 * o) = *reinterpret_cast<const uint4*>(src + o * kSfBytes<MX> + 512 * a);
+        const uint32_t c = tmem + kSfCol + uint32_t(slot) * kSfCols<MX> + lanes;
+        ptx::tc_fence_after();
+        ptx::tmem_st_32x32b_x16(c, w);
+        if constexpr (MX) {
+          ptx::tmem_st_32x32b_x8(c + 16, w + 16);
+        } else {
+          ptx::tmem_st_32x32b_x16(c + 16, w + 16);
+          ptx::tmem_st_32x32b_x16(c + 32, w + 32);
+        }
+        // The stores have completed before the arrive, which therefore needs no wider release than its
+        // own CTA's (a cluster-scope one in every stage: 8192^3 214 -> 402 us).
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(sf_ready_bar(slot), 0));
+        if (++slot == kSlots) slot = 0;
+        if (++stage == kPairStages) {
+          stage = 0;
+          ph ^= 1u;
+        }
       }
     }
   } else {
@@ -303,24 +361,23 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       if (!ok) break;
       ptx::tc_fence_after();
       const int64_t row = int64_t(tm) * 256 + int64_t(rank) * 128 + quarter * 32 + lane;
-      const int64_t col = int64_t(tn) * 256 + half * 128;
+      const int64_t col = int64_t(tn) * 256;
       O* out = static_cast<O*>(p.out) + (row < p.m ? row : 0) * p.n;
-      const uint32_t tb = tmem + uint32_t(acc) * kAccStep + uint32_t(half * 128) + (uint32_t(quarter * 32) << 16);
-      // accumulator 0 ends in the shared columns, accumulator 1 begins with them
+      const uint32_t tb = tmem + uint32_t(acc) * kAccStep + (uint32_t(quarter * 32) << 16);
+      // Chunks of 32 columns, every other one each half's. Accumulator 0 ends in the shared columns
+      // (its chunks 7, 6, 5 go first), accumulator 1 begins with them (0, 1, 2).
 #pragma unroll 1
       for (int s = 0; s < 4; ++s) {
-        const int ch = acc == 0 ? 3 - s : s;
+        const int ch = acc == 0 ? 6 - 2 * s + half : 2 * s + half;
         uint32_t r[32];
         __syncwarp();
         ptx::tmem_ld_32x32b_x32(tb + uint32_t(ch * 32), r);
         ptx::tmem_ld_wait();
-        if ((s == 1 && half == (acc ^ 1)) || s == 3) {   // the shared columns, or all, are in registers
+        const bool shared_done = s == (half ^ acc);   // this warp's last chunk in the shared columns is in registers
+        if (shared_done || s == 3) {
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            if (s == 1) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(over_bar(acc), 0));
-            if (s == 3) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(tempty_bar(acc), 0));
-          }
+          if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(shared_done ? over_bar(acc) : tempty_bar(acc), 0));
         }
         float v[32];
 #pragma unroll
@@ -357,6 +414,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         mbar_wait_drain(full_bar(s), (j / uint32_t(kPairStages)) & 1u, p.timeout_ns);
       }
     }
+    if (threadIdx.x == 0)   // this CTA's scales count on its own barriers
+      for (uint32_t j = n_issued > uint32_t(kPairStages) ? n_issued - uint32_t(kPairStages) : 0u; j < n_issued; ++j)
+        mbar_wait_drain(sf_full_bar(int(j % uint32_t(kPairStages))), (j / uint32_t(kPairStages)) & 1u, p.timeout_ns);
     ptx::cluster_sync();
   }
   ptx::tc_fence_after();

@@ -56,17 +56,22 @@ __device__ __forceinline__ float quotient(float x, float s, float y) {
   return fmaf(fmaf(-q, s, x), y, q);
 }
 
-// Eight codes of |y| <= 6 rounded up with the probability of the remainder:
-// y in fixed point with 16 bits below the grid's step, plus a 16-bit number.
-__device__ __forceinline__ uint32_t stochastic_e2m1x8(const float (&y)[8], const uint4& g) {
+// Eight codes rounded up with the probability of the remainder: |y| <= 6 in
+// fixed point, 17 bits after the point, plus the 16-bit number times the
+// grid's step (1/2 below 2, 1 below 4, 2 above), cut off to the grid. All in
+// floats, whose units are those of [64, 128): 2^-17. Exact: every sum has at
+// most 20 bits. y = v down, where its rounding towards zero is part of the
+// fixed point (down a power of two).
+__device__ __forceinline__ uint32_t stochastic_e2m1x8(const float (&v)[8], const float (&sign)[8], float down, const uint4& g) {
   uint32_t r = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fminf(fabsf(y[i]), 6.0f);
-    const uint32_t f = uint32_t(a * 131072.0f);   // floor; steps of 0.5 below 2, 1 below 4, 2 above
-    const uint32_t sh = (a >= 2.0f ? 1u : 0u) + (a >= 4.0f ? 1u : 0u);
-    const uint32_t m = ((f + (philox_half(g, i) << sh)) >> (16u + sh)) + 2u * sh;
-    r |= (m | ((__float_as_uint(y[i]) >> 28) & 8u)) << (4 * i);
+  for (int i = 7; i >= 0; --i) {
+    const float y = __fmaf_rz(fabsf(v[i]), down, 64.0f) - 64.0f;
+    const float u = __uint_as_float(0x42800000u | philox_half(g, i)) - 64.0f;                        // u 2^-17
+    const float step2 = fmaxf(__uint_as_float(__float_as_uint(y) & 0x7F800000u), 1.0f);              // twice the step
+    // in units of 2^-126 the grid's numbers are those of the float's two exponent bits and first mantissa bit
+    const float t = __fmul_rz(fmaf(u, step2, y), __uint_as_float(1u << 23));
+    r = r * 16u + ((__float_as_uint(t) >> 22) | ((__float_as_uint(sign[i]) >> 28) & 8u));
   }
   return r;
 }
@@ -111,17 +116,24 @@ __device__ __forceinline__ uint32_t quantize32(const float (&v)[32], int gexp, c
     }
     bits |= sc << (8 * b);
     const bool bad = top >= 0x7F800000u;   // the scale says NaN; codes 0
+    // only a caller's too small amax lets elements exceed 6 s g: they saturate, however far they are
+    const bool beyond = !MX && __uint_as_float(top) * down > 2688.0f;
 #pragma unroll
     for (int w = 0; w < kBlock / 8; ++w) {
-      float y[8];
+      float x[8], y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float x = v[b * kBlock + 8 * w + i] * down;
-        if (!MX) x = fminf(fmaxf(x, -2688.0f), 2688.0f);   // 6 * 448: only a caller's too small amax reaches it
-        y[i] = bad ? 0.0f : MX ? x : quotient(x, s, inv);
+        x[i] = y[i] = bad ? 0.0f : v[b * kBlock + 8 * w + i];
+        if (!MX) {
+          const float t = y[i] * down;
+          y[i] = quotient(beyond ? fminf(fmaxf(t, -2688.0f), 2688.0f) : t, s, inv);
+          if (STOCH) y[i] = fminf(fabsf(y[i]), 6.0f);
+        } else if (!STOCH) {
+          y[i] *= down;
+        }
       }
       const int k = b * (kBlock / 8) + w;
-      codes[k] = STOCH ? stochastic_e2m1x8(y, rng.group((i0 >> 3) + uint64_t(k))) : ptx::cvt_e2m1x8(y);
+      codes[k] = STOCH ? stochastic_e2m1x8(y, x, MX ? down : 1.0f, rng.group((i0 >> 3) + uint64_t(k))) : ptx::cvt_e2m1x8(y);
     }
   }
   return bits;
@@ -167,8 +179,9 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const QuantParam
 #pragma unroll 8
     for (int i = tid; i < kTile * kVecs; i += kThreads) {
       const int r = i / kVecs, c = (i - r * kVecs) * E;
-      *reinterpret_cast<uint4*>(tile + r * P + c) = __ldg(reinterpret_cast<const uint4*>(x + (r0 + r) * p.cols + c0 + c));
+      ptx::cp_async16(ptx::smem_addr(tile + r * P + c), x + (r0 + r) * p.cols + c0 + c);
     }
+    ptx::cp_async_wait();
   } else {
     for (int i = tid; i < kTile * kTile; i += kThreads) {
       const int r = i / kTile, c = i - r * kTile;
@@ -256,47 +269,70 @@ __global__ void __launch_bounds__(256) fp4_amax_kernel(const T* x, int64_t n, ui
   }
 }
 
-// Values of a quantised tensor: a thread takes eight consecutive elements.
+// Values of a quantised tensor: a thread takes kDequantU groups of 16
+// consecutive elements of a row (8 bytes of codes, one scale), 32 groups
+// apart; 32 lanes by 8 rows a block, blocks down the rows first.
+constexpr int kDequantU = 2;
+
 template <typename O, bool MX>
-__global__ void __launch_bounds__(256) fp4_dequantize_kernel(const Fp4In q, O* out) {
-  const int64_t per_row = (q.k + 7) >> 3;
-  const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= q.rows * per_row) return;
-  const int64_t row = i / per_row, k0 = (i - row * per_row) * 8;
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(q.codes + row * q.pitch + (k0 >> 1));
-  const int64_t blk = MX ? k0 >> 5 : k0 >> 4;
-  const uint32_t sc = q.scales[((row >> 7) * q.tiles_k + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3)];
-  float s;
-  if (MX)
-    s = sc == 0xFFu ? __uint_as_float(0x7FC00000u) : pow2(int(sc) - 127);
-  else
-    s = sc == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_value(sc) * pow2(tensor_exponent(q.amax));
-  float v[8];
+__global__ void __launch_bounds__(256) fp4_dequantize_kernel(const Fp4In q, O* out, int vec) {
+  const int row = int(blockIdx.x) * 8 + int(threadIdx.y);
+  if (row >= q.rows) return;
+  const int k = int(q.k), g0 = int(blockIdx.y) * (32 * kDequantU) + int(threadIdx.x);
+  const uint8_t* codes = q.codes + int64_t(row) * q.pitch;
+  const uint8_t* scales = q.scales + int64_t(row >> 7) * q.tiles_k * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+  O* o_row = out + int64_t(row) * k;
+  const float g = MX ? 1.0f : pow2(tensor_exponent(q.amax));
+  uint2 w[kDequantU];
+  uint32_t sc[kDequantU];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t c = w >> (4 * j);
-    // the three magnitude bits are a tiny float: exponent field and first mantissa bit
-    const float m = __uint_as_float((c & 7u) << 22) * __uint_as_float(253u << 23);   // 2^126
-    v[j] = s * ((c & 8u) ? -m : m);
-  }
-  O* o = out + row * q.k + k0;
-  if ((q.k & 7) == 0) {
-    if constexpr (sizeof(O) == 2) {
-      *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    } else {
-      reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  for (int u = 0; u < kDequantU; ++u) {
+    const int at = g0 + 32 * u;
+    if (16 * at < k) {
+      w[u] = *reinterpret_cast<const uint2*>(codes + 8 * at);
+      const int blk = MX ? at >> 1 : at;
+      sc[u] = scales[(blk >> 2) * 512 + (blk & 3)];
     }
-  } else {
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (k0 + j < q.k) {
-        if constexpr (sizeof(O) == 2)
-          o[j] = float_to_bf16_bits(v[j]);
-        else
-          o[j] = v[j];
+  for (int u = 0; u < kDequantU; ++u) {
+    const int k0 = 16 * (g0 + 32 * u);
+    if (k0 >= k) break;
+    const float s = sc[u] == (MX ? 0xFFu : 0x7Fu) ? __uint_as_float(0x7FC00000u) : MX ? pow2(int(sc[u]) - 127) : e4m3_value(sc[u]) * g;
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t c = (j < 8 ? w[u].x : w[u].y) >> (4 * (j & 7));
+      // the three magnitude bits are a tiny float: exponent field and first mantissa bit
+      const float m = __uint_as_float((c & 7u) << 22) * __uint_as_float(253u << 23);   // 2^126
+      v[j] = s * __uint_as_float(__float_as_uint(m) | (c & 8u) << 28);
+    }
+    O* o = o_row + k0;
+    if (vec) {   // k is a multiple of 16 and the rows are 32-byte aligned
+      if constexpr (sizeof(O) == 2) {
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        ptx::st_global_v8(o, r);
+      } else {
+        uint32_t r[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[8 * h + j]);
+          ptx::st_global_v8(o + 8 * h, r);
+        }
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (k0 + j < k) {
+          if constexpr (sizeof(O) == 2)
+            o[j] = float_to_bf16_bits(v[j]);
+          else
+            o[j] = v[j];
+        }
+    }
   }
 }
 
@@ -335,20 +371,21 @@ cudaError_t launch_fp4_amax(const void* x, bool bf16, int64_t n, float* amax, in
 }
 
 cudaError_t launch_fp4_dequantize(const Fp4In& q, bool mx, void* out, bool out_bf16, cudaStream_t stream) {
-  const int64_t items = q.rows * ((q.k + 7) / 8);
-  const unsigned grid = unsigned((items + 255) / 256);
+  const dim3 grid(unsigned((q.rows + 7) / 8), unsigned((q.k + 16 * 32 * kDequantU - 1) / (16 * 32 * kDequantU)));
+  const dim3 block(32, 8);
+  const int vec = q.k % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   if (out_bf16) {
     uint16_t* o = static_cast<uint16_t*>(out);
     if (mx)
-      fp4_dequantize_kernel<uint16_t, true><<<grid, 256, 0, stream>>>(q, o);
+      fp4_dequantize_kernel<uint16_t, true><<<grid, block, 0, stream>>>(q, o, vec);
     else
-      fp4_dequantize_kernel<uint16_t, false><<<grid, 256, 0, stream>>>(q, o);
+      fp4_dequantize_kernel<uint16_t, false><<<grid, block, 0, stream>>>(q, o, vec);
   } else {
     float* o = static_cast<float*>(out);
     if (mx)
-      fp4_dequantize_kernel<float, true><<<grid, 256, 0, stream>>>(q, o);
+      fp4_dequantize_kernel<float, true><<<grid, block, 0, stream>>>(q, o, vec);
     else
-      fp4_dequantize_kernel<float, false><<<grid, 256, 0, stream>>>(q, o);
+      fp4_dequantize_kernel<float, false><<<grid, block, 0, stream>>>(q, o, vec);
   }
   return cudaGetLastError();
 }
