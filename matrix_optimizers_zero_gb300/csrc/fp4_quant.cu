@@ -7,6 +7,7 @@
 // rounding stays unbiased. Both roundings are exact functions of the input:
 // with mx (and g) a power of two the quotient x / (s g) is exact, with nv it
 // is rounded once (see `quotient`).
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "device_common.cuh"
@@ -26,12 +27,20 @@ constexpr int kThreads = 256;
 template <typename T>
 constexpr int kPitch = kTile + 16 / int(sizeof(T));
 
+// max(|a|, |b|, |c|), NaN if any is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // Value of e4m3 bits (0 - 126).
 __device__ __forceinline__ float e4m3_value(uint32_t c) {
-  const uint32_t e = c >> 3, f = c & 7u;
-  return e == 0 ? float(f) * (1.0f / 512.0f) : __uint_as_float(((e + 120u) << 23) | (f << 20));
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(c)));
+  return __half2float(__ushort_as_half(uint16_t(h)));
 }
 
 // The tensor's own scale of nv: the smallest power of two g with
@@ -67,7 +76,8 @@ __device__ __forceinline__ uint32_t stochastic_e2m1x8(const float (&v)[8], const
 #pragma unroll
   for (int i = 7; i >= 0; --i) {
     const float y = __fmaf_rz(fabsf(v[i]), down, 64.0f) - 64.0f;
-    const float u = __uint_as_float(0x42800000u | philox_half(g, i)) - 64.0f;                        // u 2^-17
+    const uint32_t w = i < 4 ? (i < 2 ? g.x : g.y) : (i < 6 ? g.z : g.w);
+    const float u = __uint_as_float(__byte_perm(w, 0x4280u, (i & 1) ? 0x5432 : 0x5410)) - 64.0f;     // u 2^-17
     const float step2 = fmaxf(__uint_as_float(__float_as_uint(y) & 0x7F800000u), 1.0f);              // twice the step
     // in units of 2^-126 the grid's numbers are those of the float's two exponent bits and first mantissa bit
     const float t = __fmul_rz(fmaf(u, step2, y), __uint_as_float(1u << 23));
@@ -80,15 +90,16 @@ __device__ __forceinline__ uint32_t stochastic_e2m1x8(const float (&v)[8], const
 // words, scale bits in the returned value (one byte a block). i0: index of the
 // first element for the random numbers.
 template <bool MX, bool STOCH>
-__device__ __forceinline__ uint32_t quantize32(const float (&v)[32], int gexp, const Philox& rng, uint64_t i0,
+__device__ __forceinline__ uint32_t quantize32(float (&v)[32], int gexp, const Philox& rng, uint64_t i0,
                                                uint32_t (&codes)[4]) {
   uint32_t bits = 0;
   constexpr int kBlock = MX ? 32 : 16;
 #pragma unroll
   for (int b = 0; b < 32 / kBlock; ++b) {
-    uint32_t top = 0;
+    float most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kBlock; ++i) top = max(top, abs_bits(v[b * kBlock + i]));
+    for (int i = 0; i < kBlock; i += 2) most = max_abs(most, v[b * kBlock + i], v[b * kBlock + i + 1]);
+    const uint32_t top = __float_as_uint(most);
     float down, s = 1.0f, inv = 1.0f;
     uint32_t sc;
     if (MX) {
@@ -102,35 +113,43 @@ __device__ __forceinline__ uint32_t quantize32(const float (&v)[32], int gexp, c
       if (top >= 0x7F800000u) {
         sc = 0x7Fu;
       } else {
-        // nearest e4m3 of a / 6 from below or above, then up or down to the smallest with 6 s >= a
-        const float t = fminf(a * (1.0f / 6.0f), 448.0f);
+        // the e4m3 nearest to a / 6, and the next one where it is too small (448 s: saturated)
         uint16_t c16;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c16) : "f"(0.0f), "f"(t));
-        sc = c16 & 0x7Fu;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c16) : "f"(0.0f), "f"(a * (1.0f / 6.0f)));
+        sc = c16;
         if (6.0f * e4m3_value(sc) < a && sc < 126u) ++sc;
-        if (sc > 0u && 6.0f * e4m3_value(sc - 1u) >= a) --sc;
         if (sc == 0u && top != 0u) sc = 1u;   // a underflowed
       }
+      // x / (s g): with a tiny g the elements are scaled up first, so that no divisor is subnormal
       s = e4m3_value(min(sc, 126u));
+      if (gexp < -100) {
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) v[b * kBlock + i] *= down;
+      } else {
+        s *= pow2(gexp);
+      }
       inv = sc != 0u ? 1.0f / s : 0.0f;
     }
     bits |= sc << (8 * b);
-    const bool bad = top >= 0x7F800000u;   // the scale says NaN; codes 0
-    // only a caller's too small amax lets elements exceed 6 s g: they saturate, however far they are
-    const bool beyond = !MX && __uint_as_float(top) * down > 2688.0f;
+    if (top >= 0x7F800000u) {   // the scale says NaN; codes 0
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) v[b * kBlock + i] = 0.0f;
+    } else if (!MX && __uint_as_float(top) * down > 2688.0f) {
+      // only a caller's too small amax lets elements exceed 6 s g: they saturate, however far they are
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i)
+        v[b * kBlock + i] = copysignf(fminf(fabsf(v[b * kBlock + i]), 6.0f * s), v[b * kBlock + i]);
+    }
 #pragma unroll
     for (int w = 0; w < kBlock / 8; ++w) {
       float x[8], y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[i] = y[i] = bad ? 0.0f : v[b * kBlock + 8 * w + i];
-        if (!MX) {
-          const float t = y[i] * down;
-          y[i] = quotient(beyond ? fminf(fmaxf(t, -2688.0f), 2688.0f) : t, s, inv);
-          if (STOCH) y[i] = fminf(fabsf(y[i]), 6.0f);
-        } else if (!STOCH) {
+        x[i] = y[i] = v[b * kBlock + 8 * w + i];
+        if (!MX)
+          y[i] = quotient(y[i], s, inv);
+        else if (!STOCH)
           y[i] *= down;
-        }
       }
       const int k = b * (kBlock / 8) + w;
       codes[k] = STOCH ? stochastic_e2m1x8(y, x, MX ? down : 1.0f, rng.group((i0 >> 3) + uint64_t(k))) : ptx::cvt_e2m1x8(y);
@@ -142,29 +161,25 @@ __device__ __forceinline__ uint32_t quantize32(const float (&v)[32], int gexp, c
 __device__ __forceinline__ float as_float(uint16_t x) { return bf16_bits_to_float(x); }
 __device__ __forceinline__ float as_float(float x) { return x; }
 
-// Writes the codes and scales of 64 elements of row `row` (two 32-element parts
-// from element k0, a multiple of 64, on): 32 bytes of codes and 2 (mx) or 4 (nv) scales.
+// Writes the codes (16 bytes) and the scale (mx) or scales (nv) of 32 elements of row `row` from
+// element k0, a multiple of 32, on.
 template <bool MX>
-__device__ __forceinline__ void put64(const Fp4Out& q, int64_t row, int64_t k0, const uint32_t (&c0)[4],
-                                      const uint32_t (&c1)[4], uint32_t s0, uint32_t s1) {
-  if (row < q.rows) {
-    uint8_t* o = q.codes + row * q.pitch + (k0 >> 1);
-    if (k0 < q.k) *reinterpret_cast<uint4*>(o) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
-    if (k0 + 32 < q.k) *reinterpret_cast<uint4*>(o + 16) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
-  }
+__device__ __forceinline__ void put32(const Fp4Out& q, int64_t row, int64_t k0, const uint32_t (&c)[4], uint32_t bits) {
+  if (row < q.rows && k0 < q.k)
+    *reinterpret_cast<uint4*>(q.codes + row * q.pitch + (k0 >> 1)) = make_uint4(c[0], c[1], c[2], c[3]);
   // rows and blocks outside the tensor have zeros in its last tiles (values and scale 0)
   const int64_t blk = MX ? k0 >> 5 : k0 >> 4;
   if ((blk >> 2) < q.tiles_k && (row >> 7) < q.tiles_r) {
     uint8_t* o = q.scales + ((row >> 7) * q.tiles_k + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
     if (MX)
-      *reinterpret_cast<uint16_t*>(o) = uint16_t(s0 | (s1 << 8));
+      *o = uint8_t(bits);
     else
-      *reinterpret_cast<uint32_t*>(o) = s0 | (s1 << 16);
+      *reinterpret_cast<uint16_t*>(o) = uint16_t(bits);
   }
 }
 
 template <typename T, bool MX, bool STOCH>
-__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const QuantParams p) {
   extern __shared__ __align__(16) uint8_t tile_smem[];
   T* tile = reinterpret_cast<T*>(tile_smem);
   constexpr int P = kPitch<T>;
@@ -195,14 +210,18 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const QuantParam
   }
   __syncthreads();
   const int line = tid & (kTile - 1), half = tid >> 7;   // a row (a column) of the tile, 64 elements of it
-  if (p.row.codes != nullptr) {
-    const Philox rng(p.rnd, 0);
-    uint32_t codes[2][4], s[2];
-    const uint64_t kpad = uint64_t((p.cols + 31) / 32 * 32);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[32];
-      const T* src = tile + line * P + half * 64 + h * 32;
+  // With stochastic rounding one copy of the code serves both orientations and both 32-element
+  // parts: unrolled four times it no longer fits the instruction cache.
+  constexpr int kUnroll = STOCH ? 1 : 2;
+  const int begin = p.row.codes != nullptr ? 0 : 2, end = p.col.codes != nullptr ? 4 : 2;
+#pragma unroll kUnroll
+  for (int it = begin; it < end; ++it) {
+    const bool by_row = it < 2;
+    const Fp4Out& q = by_row ? p.row : p.col;
+    const int at = half * 64 + (it & 1) * 32;
+    float v[32];
+    if (by_row) {
+      const T* src = tile + line * P + at;
 #pragma unroll
       for (int i = 0; i < 32 / E; ++i) {
         const uint4 w = *reinterpret_cast<const uint4*>(src + i * E);
@@ -210,23 +229,16 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const QuantParam
 #pragma unroll
         for (int j = 0; j < E; ++j) v[i * E + j] = as_float(t[j]);
       }
-      s[h] = quantize32<MX, STOCH>(v, gexp, rng, uint64_t(r0 + line) * kpad + uint64_t(c0 + half * 64 + h * 32), codes[h]);
-    }
-    put64<MX>(p.row, r0 + line, c0 + half * 64, codes[0], codes[1], s[0], s[1]);
-  }
-  if (p.col.codes != nullptr) {
-    const Philox rng(p.rnd, 1);   // the transposed tensor draws from the next offset
-    uint32_t codes[2][4], s[2];
-    const uint64_t kpad = uint64_t((p.rows + 31) / 32 * 32);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[32];
-      const T* src = tile + (half * 64 + h * 32) * P + line;
+    } else {
+      const T* src = tile + at * P + line;
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = as_float(src[i * P]);
-      s[h] = quantize32<MX, STOCH>(v, gexp, rng, uint64_t(c0 + line) * kpad + uint64_t(r0 + half * 64 + h * 32), codes[h]);
     }
-    put64<MX>(p.col, c0 + line, r0 + half * 64, codes[0], codes[1], s[0], s[1]);
+    const int64_t row = (by_row ? r0 : c0) + line, k0 = (by_row ? c0 : r0) + at;
+    const Philox rng(p.rnd, by_row ? 0 : 1);   // the transposed tensor draws from the next offset
+    uint32_t codes[4];
+    const uint32_t bits = quantize32<MX, STOCH>(v, gexp, rng, uint64_t(row) * uint64_t(2 * q.pitch) + uint64_t(k0), codes);
+    put32<MX>(q, row, k0, codes, bits);
   }
 }
 
