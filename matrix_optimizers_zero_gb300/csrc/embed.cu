@@ -12,6 +12,7 @@
 
 #include "device_common.cuh"
 #include "philox.cuh"
+#include "ptx_train.cuh"
 #include "train_kernels.h"
 
 namespace mo {
@@ -63,9 +64,17 @@ __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = float_to_bf1
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
 // Zeroes the dropped ones of a group's eight values and scales the others.
+// (A word's high half compares as the word itself; threshold 65536, which
+// shifts out, drops everything through a factor of 0 and a last select.)
 __device__ __forceinline__ void drop8(float (&v)[8], const uint4& g, uint32_t threshold, float factor) {
+  const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+  const uint32_t high = threshold << 16;
+  const bool none = threshold > 0xFFFFu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = philox_half(g, i) >= threshold ? v[i] * factor : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = (w[i] << 16) >= high && !none ? v[2 * i] * factor : 0.0f;
+    v[2 * i + 1] = w[i] >= high && !none ? v[2 * i + 1] * factor : 0.0f;
+  }
 }
 
 __device__ __forceinline__ int64_t token_at(const TokenArgs& t, int64_t i) {
@@ -122,47 +131,53 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutPara
 
 // ------------------------------------------------------------------ lookup
 // dim % 8 == 0: blockDim.x threads cover a row in groups of eight columns,
-// blockDim.y tokens a block.
+// blockDim.y tokens at a time; the next token's index is loaded before this
+// one's row is used, so the row's address is known when its turn comes.
 template <typename T, typename O>
 __global__ void __launch_bounds__(256) embed_lookup_kernel(const LookupParams p) {
-  const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-  if (t >= p.tokens.n) return;
   const Philox rng(p.drop.rnd);
-  const int64_t tok = token_at(p.tokens, t);
-  const bool valid = tok >= 0 && tok < p.vocab;
-  if (!valid && threadIdx.x == 0) atomicExch(p.status, MO_ERR_BAD_TOKEN);
-  const int64_t groups = p.dim >> 3;
-  const T* row = static_cast<const T*>(p.table) + (valid ? tok : 0) * p.dim;
-  const T* add = p.add != nullptr ? static_cast<const T*>(p.add) + (t % p.add_rows) * p.dim : nullptr;
-  O* out = static_cast<O*>(p.out) + t * p.dim;
-  constexpr int U = 2;
-  for (int64_t g0 = threadIdx.x; g0 < groups; g0 += int64_t(U) * blockDim.x) {
-    Vec8<T> a[U], b[U];
+  const int groups = int(p.dim >> 3);
+  const int64_t stride = int64_t(gridDim.x) * blockDim.y;
+  int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (t >= p.tokens.n) return;
+  int64_t next = token_at(p.tokens, t);
+  for (; t < p.tokens.n; t += stride) {
+    const int64_t tok = next;
+    if (t + stride < p.tokens.n) next = token_at(p.tokens, t + stride);
+    const bool valid = tok >= 0 && tok < p.vocab;
+    if (!valid && threadIdx.x == 0) atomicExch(p.status, MO_ERR_BAD_TOKEN);
+    const T* row = static_cast<const T*>(p.table) + (valid ? tok : 0) * p.dim;
+    const T* add = p.add != nullptr ? static_cast<const T*>(p.add) + (t % p.add_rows) * p.dim : nullptr;
+    O* out = static_cast<O*>(p.out) + t * p.dim;
+    constexpr int U = 2;
+    for (int g0 = int(threadIdx.x); g0 < groups; g0 += U * int(blockDim.x)) {
+      Vec8<T> a[U], b[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t g = g0 + u * int64_t(blockDim.x);
-      a[u].zero();
-      if (g < groups) {
-        if (valid) a[u].load(row + 8 * g);
-        if (add != nullptr) b[u].load(add + 8 * g);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t g = g0 + u * int64_t(blockDim.x);
-      if (g < groups) {
-        float v[8];
-        a[u].unpack(v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= p.scale;
-        if (add != nullptr) {
-          float w[8];
-          b[u].unpack(w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += w[i];
+      for (int u = 0; u < U; ++u) {
+        const int g = g0 + u * int(blockDim.x);
+        a[u].zero();
+        if (g < groups) {
+          if (valid) a[u].load(row + 8 * g);
+          if (add != nullptr) b[u].load(add + 8 * g);
         }
-        if (p.drop.threshold != 0) drop8(v, rng.group(uint64_t(t * groups + g)), p.drop.threshold, p.drop.factor);
-        store8(out + 8 * g, v);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int g = g0 + u * int(blockDim.x);
+        if (g < groups) {
+          float v[8];
+          a[u].unpack(v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= p.scale;
+          if (add != nullptr) {
+            float w[8];
+            b[u].unpack(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += w[i];
+          }
+          if (p.drop.threshold != 0) drop8(v, rng.group(uint64_t(t) * uint64_t(groups) + uint64_t(g)), p.drop.threshold, p.drop.factor);
+          store8(out + 8 * g, v);
+        }
       }
     }
   }
@@ -213,22 +228,24 @@ __global__ void __launch_bounds__(256) embed_lookup_flat_kernel(const LookupPara
 
 // ------------------------------------------------------------------ gradient: sort
 //
-// Launch 1 of the gradient. Cluster 0 (eight CTAs) sorts the tokens with their
-// positions by a stable radix sort, 9 bits a pass (two passes for vocabularies
-// up to 2^18); the other clusters meanwhile write the zeros of the rows that
-// no token names. Every warp owns a contiguous part of the positions, so its
-// histogram, its offsets and its scatter need no atomics and keep the order:
-// the sums of launch 2 have one order whatever the scheduling. The CTAs'
-// histograms meet through distributed shared memory; keys ping-pong through
-// the workspace, which L2 holds.
+// Launch 1 of the gradient. Cluster 0 (eight CTAs; one for few tokens) sorts
+// the tokens with their positions by a stable radix sort, up to 9 bits a pass
+// (two passes for vocabularies up to 2^18). The other clusters meanwhile write
+// zeros: to every row, since leaving out the rows that tokens name would need
+// to know them first, and writing the table front to back by many short-lived
+// CTAs is what reaches the memory's write rate (2.1 GB: 7.4 TB/s; row by row
+// from resident CTAs, touched rows skipped, 4.4).
+//
+// Every warp owns a contiguous part of the positions, so its histogram, its
+// offsets and its scatter keep the order: the sums of launch 2 have one order
+// whatever the scheduling. The CTAs' histograms meet through distributed
+// shared memory; keys ping-pong through the workspace, which L2 holds.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCtas = 8;
-constexpr int kDigitBits = 9;
-constexpr int kBins = 1 << kDigitBits;
-constexpr uint32_t kMaskWords = 8192;   // rows a zeroing CTA marks at a time: 32 a word
-constexpr size_t kSortSmem = sizeof(uint32_t) * (size_t(kSortWarps) * kBins + kBins + kSortWarps);
-static_assert(sizeof(uint32_t) * kMaskWords <= kSortSmem, "the row mask shares the histograms' memory");
+constexpr int64_t kOneCtaTokens = 4096;
+constexpr int kMaxBins = 1 << kMaxDigitBits;
+constexpr size_t kSortSmem = sizeof(uint32_t) * (size_t(kSortWarps) * (kMaxBins + 1) + 2 * kMaxBins + kSortWarps);
+constexpr int64_t kZeroBytes = int64_t(kSortThreads) * 16 * 16;   // a zeroing CTA's share: 256 KB
 
 // The sort key of a token: itself, or `vocab` (sorted last, ignored) for the
 // padding index and for an index outside the table.
@@ -239,51 +256,54 @@ __device__ __forceinline__ uint32_t sort_key(const GradParams& p, int64_t i, boo
   return valid && tok != p.tokens.padding ? uint32_t(tok) : uint32_t(p.vocab);
 }
 
-__device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank) {
-  uint32_t* hist = sm;                                 // [warp][bin]
-  uint32_t* total = sm + size_t(kSortWarps) * kBins;   // this CTA's bin counts, read by the cluster
-  uint32_t* wsum = total + kBins;
+__device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank, uint32_t ctas) {
+  const int bins = 1 << p.digit_bits, stride = bins + 1;   // the odd stride serves a bin's counts from 32 banks
+  uint32_t* hist = sm;                                     // [warp][bin]
+  uint32_t* total = sm + size_t(kSortWarps) * stride;      // this CTA's bin counts, read by the cluster
+  uint32_t* start = total + bins;                          // where this CTA's part of each bin begins
+  uint32_t* wsum = start + bins;
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int64_t n = p.tokens.n;
   // positions a warp: a multiple of 32
-  const int64_t per_warp = (n + int64_t(kSortCtas) * kSortThreads - 1) / (int64_t(kSortCtas) * kSortThreads) * 32;
+  const int64_t per_warp = (n + int64_t(ctas) * kSortThreads - 1) / (int64_t(ctas) * kSortThreads) * 32;
   const int64_t begin = (int64_t(rank) * kSortWarps + warp) * per_warp;
   const int64_t end = min(n, begin + per_warp);
-  uint32_t* my = hist + size_t(warp) * kBins;
+  uint32_t* my = hist + size_t(warp) * stride;
 
   // the join's arrival counters, for launch 2
-  for (int64_t i = int64_t(rank) * kSortThreads + tid; i < p.counters; i += int64_t(kSortCtas) * kSortThreads)
+  for (int64_t i = int64_t(rank) * kSortThreads + tid; i < p.counters; i += int64_t(ctas) * kSortThreads)
     p.counter[i] = 0u;
 
   for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = pass * kDigitBits;
+    const int shift = pass * p.digit_bits;
     const uint32_t* src_key = p.key[(pass + 1) & 1];   // pass k writes buffer k & 1
     const uint32_t* src_pos = p.pos[(pass + 1) & 1];
     uint32_t* dst_key = p.key[pass & 1];
     uint32_t* dst_pos = p.pos[pass & 1];
-    for (int i = tid; i < kSortWarps * kBins; i += kSortThreads) hist[i] = 0u;
+    for (int i = tid; i < kSortWarps * stride; i += kSortThreads) hist[i] = 0u;
     __syncthreads();
     for (int64_t i = begin + lane; i < end; i += 32) {
       const uint32_t k = pass == 0 ? sort_key(p, i, true) : __ldcg(src_key + i);
-      atomicAdd(my + ((k >> shift) & (kBins - 1)), 1u);
+      atomicAdd(my + ((k >> shift) & (bins - 1)), 1u);
     }
     __syncthreads();
-    // exclusive offsets over (bin, CTA, warp)
-    uint32_t sum = 0;
-    if (tid < kBins) {
-#pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = hist[size_t(w) * kBins + tid];
-        hist[size_t(w) * kBins + tid] = sum;
-        sum += c;
+    // offsets over (bin, CTA, warp): within the CTA a warp scans a bin's counts, one a lane
+    for (int b = warp; b < bins; b += kSortWarps) {
+      const uint32_t c = hist[size_t(lane) * stride + b];
+      uint32_t inc = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+        if (lane >= d) inc += v;
       }
-      total[tid] = sum;
+      hist[size_t(lane) * stride + b] = inc - c;
+      if (lane == 31) total[b] = inc;
     }
     ptx::cluster_sync();
-    uint32_t before = 0, all = 0;
-    if (tid < kBins) {
-#pragma unroll
-      for (uint32_t c = 0; c < uint32_t(kSortCtas); ++c) {
+    uint32_t before = 0, inc = 0;
+    if (tid < bins) {
+      uint32_t all = 0;
+      for (uint32_t c = 0; c < ctas; ++c) {
         uint32_t v;
         asm volatile("ld.shared::cluster.u32 %0, [%1];"
                      : "=r"(v)
@@ -292,20 +312,19 @@ __device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank) {
         before += c < rank ? v : 0u;
         all += v;
       }
-      uint32_t inc = all;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-        if (lane >= d) inc += v;
-      }
-      if (lane == 31) wsum[warp] = inc;
-      before += inc - all;   // plus the bins before this one in the warp
+      inc = all;
+      before -= all;
     }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      if (lane >= d) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    if (tid < kBins) {
+    if (tid < bins) {
       for (int w = 0; w < warp; ++w) before += wsum[w];
-#pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) hist[size_t(w) * kBins + tid] += before;
+      start[tid] = before + inc;   // bins before this one, and this one's part in the CTAs before
     }
     __syncthreads();
     for (int64_t base = begin; base < end; base += 32) {
@@ -316,7 +335,7 @@ __device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank) {
         k = pass == 0 ? sort_key(p, i, false) : __ldcg(src_key + i);
         at = pass == 0 ? uint32_t(i) : __ldcg(src_pos + i);
       }
-      const uint32_t bin = live ? (k >> shift) & (kBins - 1) : uint32_t(kBins);
+      const uint32_t bin = live ? (k >> shift) & uint32_t(bins - 1) : uint32_t(bins);
       const uint32_t peers = __match_any_sync(0xFFFFFFFFu, bin);
       const uint32_t below = peers & ((1u << lane) - 1u);
       const uint32_t off = live ? my[bin] : 0u;
@@ -324,7 +343,7 @@ __device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank) {
       if (live && below == 0u) my[bin] = off + uint32_t(__popc(peers));
       __syncwarp();
       if (live) {
-        const uint32_t to = off + uint32_t(__popc(below));
+        const uint32_t to = start[bin] + off + uint32_t(__popc(below));
         dst_key[to] = k;
         dst_pos[to] = at;
       }
@@ -333,42 +352,21 @@ __device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank) {
   }
 }
 
-// CTA z of `ctas` zeroes the untouched ones of the rows z, z + ctas, ...
-__device__ void zero_rows(const GradParams& p, uint32_t* mask, uint32_t z, uint32_t ctas) {
-  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  const int64_t mine = z < p.vocab ? (p.vocab - z + ctas - 1) / ctas : 0;
-  for (int64_t r0 = 0; r0 < mine; r0 += int64_t(kMaskWords) * 32) {
-    const int64_t rows = min(mine - r0, int64_t(kMaskWords) * 32);
-    for (int i = tid; i < (rows + 31) / 32; i += kSortThreads) mask[i] = 0u;
-    __syncthreads();
-    for (int64_t i = tid; i < p.tokens.n; i += kSortThreads) {
-      const uint32_t k = sort_key(p, i, false);
-      const uint32_t q = k / ctas;
-      if (k < uint32_t(p.vocab) && k - q * ctas == z && q >= r0 && q < r0 + rows)
-        atomicOr(mask + ((q - r0) >> 5), 1u << ((q - r0) & 31));
-    }
-    __syncthreads();
-    for (int64_t r = warp; r < rows; r += kSortWarps) {
-      if ((mask[r >> 5] >> (r & 31)) & 1u) continue;
-      float* row = p.grad + (int64_t(z) + (r0 + r) * ctas) * p.dim;
-      if ((p.dim & 3) == 0) {
-        for (int64_t c = lane * 4; c < p.dim; c += 128)
-          *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-      } else {
-        for (int64_t c = lane; c < p.dim; c += 32) row[c] = 0.0f;
-      }
-    }
-    __syncthreads();
-  }
-}
-
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ GradParams p) {
   extern __shared__ uint32_t sort_smem[];
-  const uint32_t cluster = ptx::cluster_id_x();
-  if (cluster == 0)
-    sort_tokens(p, sort_smem, ptx::cluster_ctarank());
-  else
-    zero_rows(p, sort_smem, blockIdx.x - kSortCtas, gridDim.x - kSortCtas);
+  ptx::griddep_launch_dependents();   // launch 2 waits for this grid's end by itself
+  const uint32_t ctas = ptx::cluster_nctarank();
+  if (ptx::cluster_id_x() == 0) {
+    sort_tokens(p, sort_smem, ptx::cluster_ctarank(), ctas);
+    return;
+  }
+  const int64_t floats = p.vocab * p.dim, begin = int64_t(blockIdx.x - ctas) * (kZeroBytes / 4);
+  float* g = p.grad + begin;
+  const int64_t mine = min(floats - begin, kZeroBytes / 4);
+#pragma unroll 4
+  for (int64_t i = int64_t(threadIdx.x) * 4; i + 4 <= mine; i += kSortThreads * 4)
+    *reinterpret_cast<float4*>(g + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (int64_t(threadIdx.x) < (mine > 0 ? (mine & 3) : 0)) g[(mine & ~int64_t(3)) + threadIdx.x] = 0.0f;
 }
 
 // ------------------------------------------------------------------ gradient: sums
@@ -382,24 +380,30 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
 // aligned groups of kJoin chunks, then over the groups, so that a token that
 // fills the batch is not summed by one block alone.
 constexpr int kJoin = 32;
-constexpr int kMaxChunk = 64;
 
-// First index in [lo, hi) of the sorted keys whose key is at least k, hi if
-// none: each step of the warp cuts the range by 32.
-__device__ int64_t lower_bound_warp(const uint32_t* key, int64_t lo, int64_t hi, uint32_t k) {
+// First and last chunk of a token that crosses chunks. A chunk after this one
+// holds it if its first key is the token's, one before if its last key is;
+// `near` is that key of the 32 chunks next to this one, a lane each, loaded
+// before the token was known. Farther ones are searched for, 32 at a time.
+__device__ __forceinline__ int64_t reach(const GradParams& p, const uint32_t* key, uint32_t token, int64_t chunk,
+                                         uint32_t near, int dir) {
+  const uint32_t votes = __ballot_sync(0xFFFFFFFFu, near == token);   // a run of ones from lane 0
+  if (votes != 0xFFFFFFFFu) return chunk + dir * int64_t(__ffs(int(~votes)) - 1);
   const int lane = int(threadIdx.x & 31);
-  while (hi > lo) {
-    const int64_t step = (hi - lo + 31) / 32;
-    const int64_t at = lo + lane * step;
-    const bool less = at < hi && __ldcg(key + at) < k;
-    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, less);   // a run of ones from lane 0
-    const int ones = __popc(votes);
-    if (ones == 0) return lo;
-    const int64_t next = lo + int64_t(ones - 1) * step + 1;
-    hi = min(hi, lo + int64_t(ones) * step);
-    lo = next;
+  // chunk + dir lo holds the token, chunk + dir hi does not (or is none)
+  int64_t lo = 32, hi = dir > 0 ? (p.tokens.n - 1) / p.chunk - chunk + 1 : chunk + 1;
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 31) / 32, d = lo + (lane + 1) * step;
+    bool holds = false;
+    if (d < hi) {
+      const int64_t c = chunk + dir * d;
+      holds = __ldcg(key + (dir > 0 ? c * p.chunk : c * p.chunk + p.chunk - 1)) == token;
+    }
+    const int ones = __popc(__ballot_sync(0xFFFFFFFFu, holds));
+    hi = min(hi, lo + (ones + 1) * step);
+    lo += ones * step;
   }
-  return lo;
+  return chunk + dir * lo;
 }
 
 template <int V>
@@ -474,13 +478,11 @@ __device__ void join(const GradParams& p, uint32_t token, int64_t chunk, int64_t
   const int64_t cb = blockIdx.x;
   auto slot_of = [&](int64_t c) { return 2 * c + (c == c0 ? 1 : 0); };
   auto arrive = [&](int64_t counter, int64_t count) {
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(p.counter + counter * gridDim.x + cb, 1u) == uint32_t(count - 1);
+    __syncthreads();   // the block's sums are written; thread 0 releases them
+    if (threadIdx.x == 0) last = ptx::atomic_add_acq_rel(p.counter + counter * gridDim.x + cb, 1u) == uint32_t(count - 1);
     __syncthreads();
     const bool mine = last != 0;
     __syncthreads();   // `last` may be set again
-    __threadfence();
     return mine;
   };
   const int64_t g = chunk / kJoin, g0 = c0 / kJoin, g1 = c1 / kJoin;
@@ -490,7 +492,7 @@ __device__ void join(const GradParams& p, uint32_t token, int64_t chunk, int64_t
 #pragma unroll
   for (int i = 0; i < V; ++i) a.v[i] = 0.0f;
   if (live)
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t c = lo; c <= hi; ++c) add_slot<V>(p, slot_of(c), col, a);
   if (g0 == g1) {
     if (live) write_row<V>(p, token, col, a);
@@ -501,7 +503,7 @@ __device__ void join(const GradParams& p, uint32_t token, int64_t chunk, int64_t
 #pragma unroll
   for (int i = 0; i < V; ++i) a.v[i] = 0.0f;
   if (live) {
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t h = g0; h <= g1; ++h) add_slot<V>(p, slot_of(max(c0, h * kJoin)), col, a);
     write_row<V>(p, token, col, a);
   }
@@ -511,7 +513,8 @@ template <typename T, int V, bool DROP>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ GradParams p) {
   __shared__ uint32_t s_key[kMaxChunk + 2];   // the chunk's keys between its neighbours'
   __shared__ uint32_t s_pos[kMaxChunk];
-  __shared__ int64_t s_bound[3];
+  __shared__ int64_t s_bound[2];
+  ptx::griddep_wait();
   const uint32_t* key = p.key[(p.passes + 1) & 1];
   const uint32_t* pos = p.pos[(p.passes + 1) & 1];
   const int64_t n = p.tokens.n;
@@ -523,6 +526,12 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
     const int64_t at = s - 1 + i;
     s_key[i] = at < 0 || at >= n ? none : __ldcg(key + at);
     if (i >= 1 && i <= int(e - s)) s_pos[i - 1] = __ldcg(pos + at);
+  }
+  uint32_t key_after = none, key_before = none;   // see `reach`
+  if (threadIdx.x < 32) {
+    const int64_t after = (chunk + 1 + threadIdx.x) * p.chunk, prev = (chunk - int64_t(threadIdx.x)) * p.chunk - 1;
+    if (after < n) key_after = __ldcg(key + after);
+    if (prev >= 0) key_before = __ldcg(key + prev);
   }
   __syncthreads();
   if (s_key[1] == none) return;   // ignored positions only
@@ -594,22 +603,20 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
       write_row<V>(p, cur, col, a);
   }
   if (!from_before && !goes_on) return;
-  // the positions of the tokens that cross this chunk's ends
+  // the chunks of the tokens that cross this chunk's ends
   const uint32_t head_key = s_key[1], tail_key = s_key[count];
   if (threadIdx.x < 32) {
-    int64_t b0 = 0, b1 = e, b2 = e;
-    if (from_before) b0 = lower_bound_warp(key, 0, s, head_key);
-    if (from_before && head && goes_on) b1 = lower_bound_warp(key, e, n, head_key + 1u);
-    if (goes_on && !head) b2 = lower_bound_warp(key, e, n, tail_key + 1u);
+    const int64_t c0 = from_before ? reach(p, key, head_key, chunk, key_before, -1) : chunk;
+    const int64_t c1 = goes_on ? reach(p, key, tail_key, chunk, key_after, 1) : chunk;
     if (threadIdx.x == 0) {
-      s_bound[0] = b0;
-      s_bound[1] = b1;
-      s_bound[2] = b2;
+      s_bound[0] = c0;
+      s_bound[1] = c1;
     }
   }
   __syncthreads();
-  if (from_before) join<V>(p, head_key, chunk, s_bound[0] / p.chunk, head && goes_on ? (s_bound[1] - 1) / p.chunk : chunk, col, live);
-  if (goes_on && !head) join<V>(p, tail_key, chunk, chunk, (s_bound[2] - 1) / p.chunk, col, live);
+  const int64_t c0 = s_bound[0], c1 = s_bound[1];
+  if (from_before) join<V>(p, head_key, chunk, c0, head ? c1 : chunk, col, live);   // (head: one token fills the chunk)
+  if (goes_on && !head) join<V>(p, tail_key, chunk, chunk, c1, col, live);
 }
 
 template <typename T>
@@ -625,13 +632,14 @@ cudaError_t dropout_as(const DropoutParams& p, cudaStream_t stream) {
 }
 
 template <typename T, typename O>
-cudaError_t lookup_as(const LookupParams& p, cudaStream_t stream) {
+cudaError_t lookup_as(const LookupParams& p, int sms, cudaStream_t stream) {
   if ((p.dim & 7) == 0) {
     const int64_t groups = p.dim / 8;
     unsigned x = 32;
     while (x < 256 && x < groups) x <<= 1;
     const unsigned y = 256 / x;
-    embed_lookup_kernel<T, O><<<unsigned((p.tokens.n + y - 1) / y), dim3(x, y), 0, stream>>>(p);
+    const int64_t blocks = std::min<int64_t>((p.tokens.n + y - 1) / y, int64_t(sms) * 8);
+    embed_lookup_kernel<T, O><<<unsigned(blocks), dim3(x, y), 0, stream>>>(p);
   } else {
     const int64_t groups = (p.tokens.n * p.dim + 7) / 8;
     embed_lookup_flat_kernel<T, O><<<unsigned((groups + 255) / 256), 256, 0, stream>>>(p);
@@ -643,12 +651,17 @@ template <typename T, int V>
 cudaError_t sum_as(const GradParams& p, cudaStream_t stream) {
   const GradGrid g = grad_grid(p.tokens.n, p.dim);
   const int64_t y = g.chunks < 32768 ? g.chunks : 32768;
-  const dim3 grid(unsigned(g.col_blocks), unsigned(y), unsigned((g.chunks + y - 1) / y));
-  if (p.drop.threshold != 0)
-    embed_sum_kernel<T, V, true><<<grid, unsigned(g.threads), 0, stream>>>(p);
-  else
-    embed_sum_kernel<T, V, false><<<grid, unsigned(g.threads), 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(g.col_blocks), unsigned(y), unsigned((g.chunks + y - 1) / y));
+  cfg.blockDim = dim3(unsigned(g.threads), 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // the launch overlaps the sort's end
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return p.drop.threshold != 0 ? cudaLaunchKernelEx(&cfg, embed_sum_kernel<T, V, true>, p)
+                               : cudaLaunchKernelEx(&cfg, embed_sum_kernel<T, V, false>, p);
 }
 
 }  // namespace
@@ -657,25 +670,27 @@ cudaError_t launch_dropout(const DropoutParams& p, bool bf16, cudaStream_t strea
   return bf16 ? dropout_as<uint16_t>(p, stream) : dropout_as<float>(p, stream);
 }
 
-cudaError_t launch_embed_lookup(const LookupParams& p, bool table_bf16, bool out_bf16, cudaStream_t stream) {
-  if (table_bf16) return out_bf16 ? lookup_as<uint16_t, uint16_t>(p, stream) : lookup_as<uint16_t, float>(p, stream);
-  return out_bf16 ? lookup_as<float, uint16_t>(p, stream) : lookup_as<float, float>(p, stream);
+cudaError_t launch_embed_lookup(const LookupParams& p, bool table_bf16, bool out_bf16, int sms, cudaStream_t stream) {
+  if (table_bf16) return out_bf16 ? lookup_as<uint16_t, uint16_t>(p, sms, stream) : lookup_as<uint16_t, float>(p, sms, stream);
+  return out_bf16 ? lookup_as<float, uint16_t>(p, sms, stream) : lookup_as<float, float>(p, sms, stream);
 }
 
-cudaError_t launch_embed_grad(const GradParams& p, bool dout_bf16, int sms, cudaStream_t stream) {
+cudaError_t launch_embed_grad(const GradParams& p, bool dout_bf16, cudaStream_t stream) {
   static_assert(kSortSmem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSortSmem));
   if (e != cudaSuccess) return e;
+  // few tokens sort faster without the cluster's barriers
+  const int64_t ctas = p.tokens.n <= kOneCtaTokens ? 1 : 8;
+  const int64_t zeros = p.accumulate ? 0 : (p.vocab * p.dim * 4 + kZeroBytes - 1) / kZeroBytes;
+  const int bins = 1 << p.digit_bits;
   cudaLaunchConfig_t cfg = {};
-  // one cluster sorts; with zeros to write, one CTA an SM for them
-  const int clusters = 1 + (p.accumulate ? 0 : (sms > 2 * kSortCtas ? sms / kSortCtas - 1 : 1));
-  cfg.gridDim = dim3(unsigned(kSortCtas * clusters), 1, 1);
+  cfg.gridDim = dim3(unsigned(ctas + (zeros + ctas - 1) / ctas * ctas), 1, 1);
   cfg.blockDim = dim3(kSortThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSortSmem;
+  cfg.dynamicSmemBytes = sizeof(uint32_t) * (size_t(kSortWarps) * size_t(bins + 1) + 2 * size_t(bins) + kSortWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kSortCtas;
+  attr[0].val.clusterDim.x = unsigned(ctas);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;

@@ -17,7 +17,7 @@
 #include <mutex>
 
 #include "device_common.cuh"
-#include "ptx_fp4.cuh"
+#include "ptx_train.cuh"
 #include "train_kernels.h"
 
 namespace mo {

@@ -12,7 +12,7 @@
 
 #include "device_common.cuh"
 #include "philox.cuh"
-#include "ptx_fp4.cuh"
+#include "ptx_train.cuh"
 #include "train_kernels.h"
 
 namespace mo {

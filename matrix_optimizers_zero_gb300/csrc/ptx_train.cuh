@@ -1,5 +1,5 @@
-// PTX wrappers for 4-bit block-scaled tensor-core products (sm_103a), beside
-// those of ptx.cuh. Written from the PTX ISA descriptions.
+// PTX wrappers of the training-step operators (sm_103a), beside those of
+// ptx.cuh: 4-bit block-scaled tensor-core products and a few others. Written from the PTX ISA descriptions.
 #pragma once
 
 #include <cstdint>
@@ -55,6 +55,20 @@ __device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint64_t adesc, uint64
   if (!kPair && kMx) MO_UMMA_FP4("1", "mxf4", "2X");
   if (!kPair && !kMx) MO_UMMA_FP4("1", "mxf4nvf4", "4X");
 #undef MO_UMMA_FP4
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// Adds to a counter in global memory, releasing the block's earlier writes
+// (after a block barrier) and acquiring those of the blocks that added before.
+__device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v) {
+  uint32_t r;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(v) : "memory");
+  return r;
 }
 
 // ---------------------------------------------------------------- one CTA by itself

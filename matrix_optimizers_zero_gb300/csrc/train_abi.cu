@@ -195,7 +195,7 @@ int embed_lookup(const void* table, int32_t table_dtype, int64_t vocab, int64_t 
   p.dim = dim;
   p.add_rows = add_rows;
   p.scale = scale;
-  const cudaError_t e = mo::launch_embed_lookup(p, table_dtype == MO_BF16, out_dtype == MO_BF16, stream);
+  const cudaError_t e = mo::launch_embed_lookup(p, table_dtype == MO_BF16, out_dtype == MO_BF16, sms, stream);
   return e != cudaSuccess ? report_cuda(e) : MO_OK;
 }
 
@@ -253,8 +253,10 @@ int embed_grad(const void* dout, int32_t dout_dtype, const mo_tokens* tokens, in
   p.accumulate = accumulate;
   int bits = 1;
   while ((int64_t(1) << bits) <= vocab) ++bits;   // the keys run from 0 to vocab
-  p.passes = (bits + 8) / 9;
-  const cudaError_t e = mo::launch_embed_grad(p, dout_dtype == MO_BF16, sms, stream);
+  p.passes = (bits + mo::kMaxDigitBits - 1) / mo::kMaxDigitBits;
+  p.digit_bits = (bits + p.passes - 1) / p.passes;
+  if (p.digit_bits < 5) p.digit_bits = 5;   // a whole warp of bins
+  const cudaError_t e = mo::launch_embed_grad(p, dout_dtype == MO_BF16, stream);
   return e != cudaSuccess ? report_cuda(e) : MO_OK;
 }
 

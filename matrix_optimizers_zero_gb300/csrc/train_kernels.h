@@ -45,7 +45,12 @@ struct LookupParams {
   DropArgs drop;
   float scale;
 };
-cudaError_t launch_embed_lookup(const LookupParams& p, bool table_bf16, bool out_bf16, cudaStream_t stream);
+cudaError_t launch_embed_lookup(const LookupParams& p, bool table_bf16, bool out_bf16, int sms, cudaStream_t stream);
+
+// Bits a pass of the gradient's radix sort: the fewest passes of at most
+// kMaxDigitBits, then the fewest bits.
+constexpr int kMaxDigitBits = 9;
+constexpr int kMaxChunk = 64;
 
 // Launch shape of the gradient's sums: chunks of sorted positions by blocks of
 // columns (eight a thread, or one where dim is not a multiple of 8). A chunk
@@ -60,7 +65,7 @@ inline GradGrid grad_grid(int64_t n, int64_t dim) {
   g.col_blocks = (items + 255) / 256;
   const int64_t per = (items + g.col_blocks - 1) / g.col_blocks;
   g.threads = int((per + 31) / 32 * 32);
-  g.chunk = 64;
+  g.chunk = kMaxChunk;
   while (g.chunk > 8 && (n + g.chunk - 1) / g.chunk * g.col_blocks < 608) g.chunk /= 2;
   g.chunks = (n + g.chunk - 1) / g.chunk;
   return g;
@@ -80,9 +85,10 @@ struct GradParams {
   DropArgs drop;
   float factor;           // scale times the dropout's factor
   int32_t passes;         // of the sort
+  int32_t digit_bits;
   int32_t accumulate;
 };
-cudaError_t launch_embed_grad(const GradParams& p, bool dout_bf16, int sms, cudaStream_t stream);
+cudaError_t launch_embed_grad(const GradParams& p, bool dout_bf16, cudaStream_t stream);
 
 // ---------------------------------------------------------------- 4-bit tensors
 // Storage of a 4-bit tensor [rows, k]: codes, two a byte (the even element in
