@@ -64,16 +64,15 @@ __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = float_to_bf1
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
 // Zeroes the dropped ones of a group's eight values and scales the others.
-// (A word's high half compares as the word itself; threshold 65536, which
-// shifts out, drops everything through a factor of 0 and a last select.)
+// Halves compare in the upper half of a word: at least T << 16, or above
+// (T << 16) - 1, which for T = 65536 is the largest word and drops all.
 __device__ __forceinline__ void drop8(float (&v)[8], const uint4& g, uint32_t threshold, float factor) {
   const uint32_t w[4] = {g.x, g.y, g.z, g.w};
-  const uint32_t high = threshold << 16;
-  const bool none = threshold > 0xFFFFu;
+  const uint32_t below = (threshold << 16) - 1u;   // threshold >= 1
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = (w[i] << 16) >= high && !none ? v[2 * i] * factor : 0.0f;
-    v[2 * i + 1] = w[i] >= high && !none ? v[2 * i + 1] * factor : 0.0f;
+    v[2 * i] = (w[i] << 16) > below ? v[2 * i] * factor : 0.0f;
+    v[2 * i + 1] = w[i] > below ? v[2 * i + 1] * factor : 0.0f;
   }
 }
 
@@ -110,7 +109,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutPara
     if (g < full) {
       float v[8];
       a[u].unpack(v);
-      drop8(v, rng.group(uint64_t(g)), p.drop.threshold, p.drop.factor);
+      if (p.drop.threshold != 0) drop8(v, rng.group(uint64_t(g)), p.drop.threshold, p.drop.factor);
       if (RES) {
         float w[8];
         r[u].unpack(w);
@@ -133,10 +132,11 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutPara
 // dim % 8 == 0: blockDim.x threads cover a row in groups of eight columns,
 // blockDim.y tokens at a time; the next token's index is loaded before this
 // one's row is used, so the row's address is known when its turn comes.
-template <typename T, typename O>
-__global__ void __launch_bounds__(256) embed_lookup_kernel(const LookupParams p) {
+template <typename T, typename O, bool ADD, bool DROP>
+__global__ void __launch_bounds__(256, ADD ? 4 : 5) embed_lookup_kernel(const LookupParams p) {
   const Philox rng(p.drop.rnd);
   const int groups = int(p.dim >> 3);
+  const float scale = ADD ? p.scale : p.scale * p.drop.factor;
   const int64_t stride = int64_t(gridDim.x) * blockDim.y;
   int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
   if (t >= p.tokens.n) return;
@@ -147,18 +147,18 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(const LookupParams p)
     const bool valid = tok >= 0 && tok < p.vocab;
     if (!valid && threadIdx.x == 0) atomicExch(p.status, MO_ERR_BAD_TOKEN);
     const T* row = static_cast<const T*>(p.table) + (valid ? tok : 0) * p.dim;
-    const T* add = p.add != nullptr ? static_cast<const T*>(p.add) + (t % p.add_rows) * p.dim : nullptr;
+    const T* add = ADD ? static_cast<const T*>(p.add) + (t % p.add_rows) * p.dim : nullptr;
     O* out = static_cast<O*>(p.out) + t * p.dim;
     constexpr int U = 2;
     for (int g0 = int(threadIdx.x); g0 < groups; g0 += U * int(blockDim.x)) {
-      Vec8<T> a[U], b[U];
+      Vec8<T> a[U], b[ADD ? U : 1];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int g = g0 + u * int(blockDim.x);
         a[u].zero();
         if (g < groups) {
           if (valid) a[u].load(row + 8 * g);
-          if (add != nullptr) b[u].load(add + 8 * g);
+          if (ADD) b[ADD ? u : 0].load(add + 8 * g);
         }
       }
 #pragma unroll
@@ -168,14 +168,14 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(const LookupParams p)
           float v[8];
           a[u].unpack(v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= p.scale;
-          if (add != nullptr) {
+          for (int i = 0; i < 8; ++i) v[i] *= scale;
+          if (ADD) {
             float w[8];
-            b[u].unpack(w);
+            b[ADD ? u : 0].unpack(w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += w[i];
           }
-          if (p.drop.threshold != 0) drop8(v, rng.group(uint64_t(t) * uint64_t(groups) + uint64_t(g)), p.drop.threshold, p.drop.factor);
+          if (DROP) drop8(v, rng.group(uint64_t(t) * uint64_t(groups) + uint64_t(g)), p.drop.threshold, ADD ? p.drop.factor : 1.0f);
           store8(out + 8 * g, v);
         }
       }
@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(256) embed_lookup_flat_kernel(const LookupPara
 // shared memory; keys ping-pong through the workspace, which L2 holds.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int64_t kOneCtaTokens = 4096;
+constexpr int kBatch = 4;
+constexpr int64_t kOneCtaTokens = 1024;
 constexpr int kMaxBins = 1 << kMaxDigitBits;
 constexpr size_t kSortSmem = sizeof(uint32_t) * (size_t(kSortWarps) * (kMaxBins + 1) + 2 * kMaxBins + kSortWarps);
 constexpr int64_t kZeroBytes = int64_t(kSortThreads) * 16 * 16;   // a zeroing CTA's share: 256 KB
@@ -282,9 +283,23 @@ __device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank, ui
     uint32_t* dst_pos = p.pos[pass & 1];
     for (int i = tid; i < kSortWarps * stride; i += kSortThreads) hist[i] = 0u;
     __syncthreads();
-    for (int64_t i = begin + lane; i < end; i += 32) {
-      const uint32_t k = pass == 0 ? sort_key(p, i, true) : __ldcg(src_key + i);
-      atomicAdd(my + ((k >> shift) & (bins - 1)), 1u);
+    // kBatch loads at a time; a part of one batch stays in registers for the scatter
+    uint32_t k[kBatch], at[kBatch];
+    auto load = [&](int64_t base, bool report) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t i = base + 32 * u + lane;
+        if (i < end) {
+          k[u] = pass == 0 ? sort_key(p, i, report) : __ldcg(src_key + i);
+          at[u] = pass == 0 ? uint32_t(i) : __ldcg(src_pos + i);
+        }
+      }
+    };
+    for (int64_t base = begin; base < end; base += 32 * kBatch) {
+      load(base, true);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (base + 32 * u + lane < end) atomicAdd(my + ((k[u] >> shift) & uint32_t(bins - 1)), 1u);
     }
     __syncthreads();
     // offsets over (bin, CTA, warp): within the CTA a warp scans a bin's counts, one a lane
@@ -327,25 +342,24 @@ __device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank, ui
       start[tid] = before + inc;   // bins before this one, and this one's part in the CTAs before
     }
     __syncthreads();
-    for (int64_t base = begin; base < end; base += 32) {
-      const int64_t i = base + lane;
-      const bool live = i < end;
-      uint32_t k = 0, at = 0;
-      if (live) {
-        k = pass == 0 ? sort_key(p, i, false) : __ldcg(src_key + i);
-        at = pass == 0 ? uint32_t(i) : __ldcg(src_pos + i);
-      }
-      const uint32_t bin = live ? (k >> shift) & uint32_t(bins - 1) : uint32_t(bins);
-      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, bin);
-      const uint32_t below = peers & ((1u << lane) - 1u);
-      const uint32_t off = live ? my[bin] : 0u;
-      __syncwarp();
-      if (live && below == 0u) my[bin] = off + uint32_t(__popc(peers));
-      __syncwarp();
-      if (live) {
-        const uint32_t to = start[bin] + off + uint32_t(__popc(below));
-        dst_key[to] = k;
-        dst_pos[to] = at;
+    for (int64_t base = begin; base < end; base += 32 * kBatch) {
+      if (per_warp > 32 * kBatch) load(base, false);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (base + 32 * u >= end) break;   // the same for the whole warp
+        const bool live = base + 32 * u + lane < end;
+        const uint32_t bin = live ? (k[u] >> shift) & uint32_t(bins - 1) : uint32_t(bins);
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, bin);
+        const uint32_t below = peers & ((1u << lane) - 1u);
+        const uint32_t off = live ? my[bin] : 0u;
+        __syncwarp();
+        if (live && below == 0u) my[bin] = off + uint32_t(__popc(peers));
+        __syncwarp();
+        if (live) {
+          const uint32_t to = start[bin] + off + uint32_t(__popc(below));
+          dst_key[to] = k[u];
+          dst_pos[to] = at[u];
+        }
       }
     }
     ptx::cluster_sync();   // the pass is complete and visible to the cluster
@@ -510,7 +524,7 @@ __device__ void join(const GradParams& p, uint32_t token, int64_t chunk, int64_t
 }
 
 template <typename T, int V, bool DROP>
-__global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ GradParams p) {
+__global__ void __launch_bounds__(256, 4) embed_sum_kernel(const __grid_constant__ GradParams p) {
   __shared__ uint32_t s_key[kMaxChunk + 2];   // the chunk's keys between its neighbours'
   __shared__ uint32_t s_pos[kMaxChunk];
   __shared__ int64_t s_bound[2];
@@ -549,7 +563,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
   for (int i = 0; i < V; ++i) a.v[i] = 0.0f;
   uint32_t cur = s_key[1];
   bool first = true;
-  constexpr int U = V == 8 ? 8 : 8;
+  constexpr int U = 4;
   for (int i0 = 0; i0 < count; i0 += U) {
     Vec8<T> q[V == 8 ? U : 1];
     float sc[V == 8 ? 1 : U];
@@ -639,7 +653,10 @@ cudaError_t lookup_as(const LookupParams& p, int sms, cudaStream_t stream) {
     while (x < 256 && x < groups) x <<= 1;
     const unsigned y = 256 / x;
     const int64_t blocks = std::min<int64_t>((p.tokens.n + y - 1) / y, int64_t(sms) * 8);
-    embed_lookup_kernel<T, O><<<unsigned(blocks), dim3(x, y), 0, stream>>>(p);
+    const bool add = p.add != nullptr, drop = p.drop.threshold != 0;
+    auto kern = add ? (drop ? embed_lookup_kernel<T, O, true, true> : embed_lookup_kernel<T, O, true, false>)
+                    : (drop ? embed_lookup_kernel<T, O, false, true> : embed_lookup_kernel<T, O, false, false>);
+    kern<<<unsigned(blocks), dim3(x, y), 0, stream>>>(p);
   } else {
     const int64_t groups = (p.tokens.n * p.dim + 7) / 8;
     embed_lookup_flat_kernel<T, O><<<unsigned((groups + 255) / 256), 256, 0, stream>>>(p);
