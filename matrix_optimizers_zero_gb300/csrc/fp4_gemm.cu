@@ -110,7 +110,7 @@ __device__ __forceinline__ void store32<float>(float* row, int64_t col, int64_t 
 // ------------------------------------------------------------------ pairs
 //
 // Warp 0 of each CTA loads its 128-row halves of A and B, its A scales and all
-// 256 rows' B scales; warps 10-13 put the scales into TMEM; the even CTA's
+// 256 rows' B scales; warps 10-17 put the scales into TMEM; the even CTA's
 // warp 1 issues the instructions; warps 2-9 drain 128 lanes x 256 columns.
 //
 // Scales: the tensor core's own copy (tcgen05.cp) runs in its instruction
@@ -123,8 +123,9 @@ __device__ __forceinline__ void store32<float>(float* row, int64_t col, int64_t 
 // the two accumulators overlap in 96 columns, [160, 256): the epilogue drains
 // those first, and the next tile starts as soon as they are free.
 constexpr int kEpiWarps = 8;
-constexpr int kSfWarps = 4;
-constexpr int kPairThreads = 64 + 32 * (kEpiWarps + kSfWarps);
+constexpr int kSfWarps = 4;    // a stage's: one a lane quarter
+constexpr int kSfGroups = 2;
+constexpr int kPairThreads = 64 + 32 * (kEpiWarps + kSfGroups * kSfWarps);
 constexpr int kPairStages = 5;
 constexpr uint32_t kAccStep = 160;
 constexpr uint32_t kSfCol = 416;
@@ -302,49 +303,43 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     // -------------------------------------------------------------- scales (both CTAs)
     // Lane l of every quarter holds, column by column, the scales of rows l, 32 + l, 64 + l, 96 + l
     // of a 512-byte tile: 16 consecutive bytes of it.
+    // Warps 10-13 take every other stage, 14-17 the ones between: a stage's chain of waits, loads,
+    // stores and the arrive is longer than its instructions.
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    int stage = 0, slot = 0;
-    uint32_t ph = 0;
-    uint32_t j = 0;   // stages so far
-    bool ok = true;
-    for (int32_t t = first; ok && t < ntiles; t += step) {
-      for (int32_t kb = 0; kb < p.stages; ++kb, ++j) {
-        // the slot's last stage has been multiplied (and its shared memory may be refilled)
-        if (j >= uint32_t(kSlots)) {
-          const uint32_t u = j - uint32_t(kSlots);
-          ok = mbar_wait_bounded(empty_bar(int(u % kPairStages)), (u / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
-        }
-        ok = ok && mbar_wait_bounded(sf_full_bar(stage), ph, abort_flag, p.status, p.timeout_ns);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        const uint8_t* src = smem_raw + (sf_base - raw) + uint32_t(stage) * 3u * kSfBytes<MX> + 16 * lane;
-        uint32_t w[kSfCols<MX>];
-#pragma unroll
-        for (int a = 0; a < kSfTiles<MX>; ++a)
-#pragma unroll
-          for (int o = 0; o < 3; ++o)
-            *reinterpret_cast<uint4*>(w + 12 * a + 4 * o) = *reinterpret_cast<const uint4*>(src + o * kSfBytes<MX> + 512 * a);
-        const uint32_t c = tmem + kSfCol + uint32_t(slot) * kSfCols<MX> + lanes;
-        ptx::tc_fence_after();
-        ptx::tmem_st_32x32b_x16(c, w);
-        if constexpr (MX) {
-          ptx::tmem_st_32x32b_x8(c + 16, w + 16);
-        } else {
-          ptx::tmem_st_32x32b_x16(c + 16, w + 16);
-          ptx::tmem_st_32x32b_x16(c + 32, w + 32);
-        }
-        // The stores have completed before the arrive, which therefore needs no wider release than its
-        // own CTA's (a cluster-scope one in every stage: 8192^3 214 -> 402 us).
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(sf_ready_bar(slot), 0));
-        if (++slot == kSlots) slot = 0;
-        if (++stage == kPairStages) {
-          stage = 0;
-          ph ^= 1u;
-        }
+    const uint32_t total = first < ntiles ? uint32_t((ntiles - first + step - 1) / step) * uint32_t(p.stages) : 0u;
+    for (uint32_t j = uint32_t(warp - 2 - kEpiWarps) >> 2; j < total; j += kSfGroups) {
+      const uint32_t stage = j % kPairStages, slot = j % kSlots;
+      // the slot's last stage has been multiplied
+      bool ok = true;
+      if (j >= uint32_t(kSlots)) {
+        const uint32_t u = j - uint32_t(kSlots);
+        ok = mbar_wait_bounded(empty_bar(int(u % kPairStages)), (u / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
       }
+      ok = ok && mbar_wait_bounded(sf_full_bar(int(stage)), (j / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      const uint8_t* src = smem_raw + (sf_base - raw) + stage * 3u * kSfBytes<MX> + 16 * lane;
+      uint32_t w[kSfCols<MX>];
+#pragma unroll
+      for (int a = 0; a < kSfTiles<MX>; ++a)
+#pragma unroll
+        for (int o = 0; o < 3; ++o)
+          *reinterpret_cast<uint4*>(w + 12 * a + 4 * o) = *reinterpret_cast<const uint4*>(src + o * kSfBytes<MX> + 512 * a);
+      const uint32_t c = tmem + kSfCol + slot * kSfCols<MX> + lanes;
+      ptx::tc_fence_after();
+      ptx::tmem_st_32x32b_x16(c, w);
+      if constexpr (MX) {
+        ptx::tmem_st_32x32b_x8(c + 16, w + 16);
+      } else {
+        ptx::tmem_st_32x32b_x16(c + 16, w + 16);
+        ptx::tmem_st_32x32b_x16(c + 32, w + 32);
+      }
+      // The stores have completed before the arrive, which therefore needs no wider release than its
+      // own CTA's (a cluster-scope one in every stage: 8192^3 214 -> 402 us).
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(sf_ready_bar(int(slot)), 0));
     }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
@@ -365,24 +360,27 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       O* out = static_cast<O*>(p.out) + (row < p.m ? row : 0) * p.n;
       const uint32_t tb = tmem + uint32_t(acc) * kAccStep + (uint32_t(quarter * 32) << 16);
       // Chunks of 32 columns, every other one each half's. Accumulator 0 ends in the shared columns
-      // (its chunks 7, 6, 5 go first), accumulator 1 begins with them (0, 1, 2).
+      // (chunks 7, 6, 5), accumulator 1 begins with them (0, 1, 2): each warp takes two chunks to
+      // registers before it stores the first.
+      auto chunk = [&](int s) { return acc == 0 ? 6 - 2 * s + half : 2 * s + half; };
 #pragma unroll 1
-      for (int s = 0; s < 4; ++s) {
-        const int ch = acc == 0 ? 6 - 2 * s + half : 2 * s + half;
-        uint32_t r[32];
+      for (int s = 0; s < 4; s += 2) {
+        uint32_t r[2][32];
         __syncwarp();
-        ptx::tmem_ld_32x32b_x32(tb + uint32_t(ch * 32), r);
+        ptx::tmem_ld_32x32b_x32(tb + uint32_t(chunk(s) * 32), r[0]);
+        ptx::tmem_ld_32x32b_x32(tb + uint32_t(chunk(s + 1) * 32), r[1]);
         ptx::tmem_ld_wait();
-        const bool shared_done = s == (half ^ acc);   // this warp's last chunk in the shared columns is in registers
-        if (shared_done || s == 3) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(shared_done ? over_bar(acc) : tempty_bar(acc), 0));
-        }
-        float v[32];
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(s == 0 ? over_bar(acc) : tempty_bar(acc), 0));
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * factor;
-        if (row < p.m && col + ch * 32 < p.n) store32<O>(out, col + ch * 32, p.n, p.align, v);
+        for (int q = 0; q < 2; ++q) {
+          const int64_t at = col + chunk(s + q) * 32;
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[q][j]) * factor;
+          if (row < p.m && at < p.n) store32<O>(out, at, p.n, p.align, v);
+        }
       }
     }
   }
