@@ -109,14 +109,14 @@ __device__ __forceinline__ void store32<float>(float* row, int64_t col, int64_t 
 
 // ------------------------------------------------------------------ pairs
 //
-// Warp 0 of each CTA loads its 128-row halves of A and B, its A scales and all
-// 256 rows' B scales; warps 10-17 put the scales into TMEM; the even CTA's
+// Warp 0 of each CTA loads its 128-row halves of A and B, warp 18 its A scales
+// and all 256 rows' B scales; warps 10-17 put the scales into TMEM; the even CTA's
 // warp 1 issues the instructions; warps 2-9 drain 128 lanes x 256 columns.
 //
 // Scales: the tensor core's own copy (tcgen05.cp) runs in its instruction
-// stream, about 30 cycles a 512-byte tile beside 200 for an instruction (six to
-// twelve tiles for four instructions). Stores from registers (tcgen05.st) run
-// beside it: 8192^3 with mx 266 -> see the table in the documentation.
+// stream, about 30 cycles for each of the six to twelve 512-byte tiles of a
+// stage beside 125 for each of its four instructions. Stores from registers
+// (tcgen05.st) run beside it (8192^3: mx 267 -> 201 us, nv 357 -> 211 us).
 //
 // TMEM: an accumulator takes 256 columns and a stage's scales 24 (mx) or 48
 // (nv), and a stage's scales are written while the last one's are in use. So
@@ -125,21 +125,22 @@ __device__ __forceinline__ void store32<float>(float* row, int64_t col, int64_t 
 constexpr int kEpiWarps = 8;
 constexpr int kSfWarps = 4;    // a stage's: one a lane quarter
 constexpr int kSfGroups = 2;
-constexpr int kPairThreads = 64 + 32 * (kEpiWarps + kSfGroups * kSfWarps);
+constexpr int kSfWarp0 = 2 + kEpiWarps;
+constexpr int kSfLoader = kSfWarp0 + kSfGroups * kSfWarps;
+constexpr int kPairThreads = 32 * (kSfLoader + 1);
 constexpr int kPairStages = 5;
+constexpr int kSfStages = 8;   // scales run farther ahead: they have one step more to go
 constexpr uint32_t kAccStep = 160;
 constexpr uint32_t kSfCol = 416;
 template <bool MX>
 constexpr uint32_t kSfCols = 12 * kSfTiles<MX>;    // A 4 columns, B 8, for every scale tile of a stage
 template <bool MX>
 constexpr int kSfSlots = int(96 / kSfCols<MX>);    // stages whose scales TMEM holds
+constexpr uint32_t kPairBars = 2 * kPairStages + 7 + 2 * kSfStages + 4;
 template <bool MX>
-constexpr uint32_t kPairStageBytes = 2 * kPanelBytes + 3 * kSfBytes<MX>;
-constexpr uint32_t kPairBars = 3 * kPairStages + 7 + 4;
-template <bool MX>
-constexpr size_t kPairSmem = 1024 + size_t(kPairStages) * kPairStageBytes<MX> + 256;
+constexpr size_t kPairSmem = 1024 + size_t(kPairStages) * 2 * kPanelBytes + size_t(kSfStages) * 3 * kSfBytes<MX> + 384;
 static_assert(kAccStep + 256 <= kSfCol && kSfCol + 96 <= 512, "TMEM columns");
-static_assert(8 * kPairBars + 32 <= 256, "control block");
+static_assert(8 * kPairBars + 32 <= 384, "control block");
 static_assert(kPairSmem<false> <= 227 * 1024, "shared memory");
 
 // Output tiles in groups of 8 tile rows, column by column: the tiles in
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   const uint32_t base = (raw + 1023u) & ~1023u;
   // panels first (1024-byte aligned), then the scale tiles of every stage, then control
   const uint32_t sf_base = base + uint32_t(kPairStages) * 2u * kPanelBytes;
-  const uint32_t bars = sf_base + uint32_t(kPairStages) * 3u * kSfBytes<MX>;
+  const uint32_t bars = sf_base + uint32_t(kSfStages) * 3u * kSfBytes<MX>;
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kPairBars);
   uint32_t* tmem_slot = ctrl;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 1);
@@ -172,7 +173,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   auto over_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + 4 + s); };
   const uint32_t drain_bar = bars + 8u * uint32_t(2 * kPairStages + 6);
   auto sf_full_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + 7 + s); };    // scales in shared memory
-  auto sf_ready_bar = [&](int s) { return bars + 8u * uint32_t(3 * kPairStages + 7 + s); };   // scales in TMEM, both CTAs
+  auto sf_empty_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + 7 + kSfStages + s); };
+  auto sf_ready_bar = [&](int s) { return bars + 8u * uint32_t(2 * kPairStages + 7 + 2 * kSfStages + s); };   // in TMEM, both CTAs
 
   const int warp = int(threadIdx.x >> 5);
   const int lane = int(threadIdx.x & 31);
@@ -183,7 +185,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     for (int s = 0; s < kPairStages; ++s) {
       ptx::mbar_init(full_bar(s), 1);
       ptx::mbar_init(empty_bar(s), 1);
+    }
+    for (int s = 0; s < kSfStages; ++s) {
       ptx::mbar_init(sf_full_bar(s), 1);
+      ptx::mbar_init(sf_empty_bar(s), kSfWarps);
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(tfull_bar(s), 1);
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
 
   const int32_t ntiles = p.tiles_m * p.tiles_n;
   const int32_t first = int32_t(ptx::cluster_id_x()), step = int32_t(ptx::nclusters_x());
-  uint32_t n_issued = 0;
+  uint32_t n_issued = 0, sf_issued = 0;
   bool mma_issued = false;
   if (warp == 0) {
     if (lane == 0) {
@@ -230,15 +235,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * kStage);
           const uint32_t fb = ptx::mapa_shared(fb_local, 0);
           const uint32_t sa = base + uint32_t(stage) * 2u * kPanelBytes;
-          const uint32_t sf = sf_base + uint32_t(stage) * 3u * kSfBytes<MX>;
           ptx::tma_load_2d_pair(sa, &p.a, fb, kb * 128, ra * 128);
           ptx::tma_load_2d_pair(sa + kPanelBytes, &p.b, fb, kb * 128, rb * 128);
-          const int32_t at = kb * kSfTiles<MX>;
-          const uint32_t sfb = sf_full_bar(stage);
-          ptx::mbar_arrive_expect_tx(sfb, 3 * kSfBytes<MX>);
-          ptx::tma_load_2d(sf, &p.sa, sfb, 0, (ra * p.tiles_k + at) * 2);
-          ptx::tma_load_2d(sf + kSfBytes<MX>, &p.sb, sfb, 0, (tn * 2 * p.tiles_k + at) * 2);
-          ptx::tma_load_2d(sf + 2 * kSfBytes<MX>, &p.sb, sfb, 0, ((tn * 2 + 1) * p.tiles_k + at) * 2);
           ++n_issued;
           if (++stage == kPairStages) {
             stage = 0;
@@ -252,7 +250,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       // ------------------------------------------------------------ MMA issuer (even CTA)
       int stage = 0, slot = 0;
       uint32_t ph = 0, sph = 0;
-      bool ok = true;
+      bool ok = true, seen = false;   // seen: the stage is known to be complete
       int32_t i = 0;
       for (int32_t t = first; ok && t < ntiles; t += step, ++i) {
         const int acc = i & 1;
@@ -264,42 +262,75 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         const uint32_t d = tmem + uint32_t(acc) * kAccStep;
         int32_t left = p.steps;
         for (int32_t kb = 0; kb < p.stages; ++kb) {
-          if (!mbar_wait_bounded(sf_ready_bar(slot), sph, abort_flag, p.status, p.timeout_ns) ||
-              !mbar_wait_bounded(full_bar(stage), ph, abort_flag, p.status, p.timeout_ns)) {
+          if (!seen && (!mbar_wait_bounded(sf_ready_bar(slot), sph, abort_flag, p.status, p.timeout_ns) ||
+                        !mbar_wait_bounded(full_bar(stage), ph, abort_flag, p.status, p.timeout_ns))) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
           const uint32_t sa = base + uint32_t(stage) * 2u * kPanelBytes;
-          const uint32_t sb = sa + kPanelBytes;
+          const uint32_t sb = sa + kPanelBytes, sf = tmem + kSfCol + uint32_t(slot) * kSfCols<MX>;
+          const uint32_t bar = empty_bar(stage);
+          if (++slot == kSlots) {
+            slot = 0;
+            sph ^= 1u;
+          }
+          if (++stage == kPairStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk < left) {
               constexpr uint32_t idesc0 = ptx::idesc_fp4(256, 256, MX, 0);
               constexpr uint32_t idesc2 = ptx::idesc_fp4(256, 256, MX, 2);
-              const uint32_t c = tmem + kSfCol + uint32_t(slot) * kSfCols<MX> + 12u * uint32_t(kk / kStepsPerTile<MX>);
+              const uint32_t c = sf + 12u * uint32_t(kk / kStepsPerTile<MX>);
               ptx::umma_fp4<true, MX>(d, ptx::smem_desc_sw128(sa + uint32_t(kk) * 32u, 16u, 1024u),
                                       ptx::smem_desc_sw128(sb + uint32_t(kk) * 32u, 16u, 1024u),
                                       MX && (kk & 1) ? idesc2 : idesc0, c, c + 4, (kb | kk) != 0 ? 1u : 0u);
             }
-          }
-          if (++slot == kSlots) {
-            slot = 0;
-            sph ^= 1u;
+            // the next stage is looked at while this one's instructions are under way
+            if (kk == 1) seen = ptx::mbar_peek(sf_ready_bar(slot), sph) && ptx::mbar_peek(full_bar(stage), ph);
           }
           left -= 4;
-          ptx::umma_commit_pair(empty_bar(stage), 0x3);
+          ptx::umma_commit_pair(bar, 0x3);
           mma_issued = true;
-          if (++stage == kPairStages) {
-            stage = 0;
-            ph ^= 1u;
-          }
         }
         if (!ok) break;
         ptx::umma_commit_pair(tfull_bar(acc), 0x3);
       }
     }
-  } else if (warp >= 2 + kEpiWarps) {
+  } else if (warp == kSfLoader) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ scale loads (both CTAs)
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int32_t t = first; ok && t < ntiles; t += step) {
+        int32_t tm, tn;
+        tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
+        const int32_t ra = tm * 2 + int32_t(rank);
+        for (int32_t kb = 0; kb < p.stages; ++kb) {
+          if (!mbar_wait_bounded(sf_empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sf = sf_base + uint32_t(stage) * 3u * kSfBytes<MX>;
+          const uint32_t sfb = sf_full_bar(stage);
+          const int32_t at = kb * kSfTiles<MX>;
+          ptx::mbar_arrive_expect_tx(sfb, 3 * kSfBytes<MX>);
+          ptx::tma_load_2d(sf, &p.sa, sfb, 0, (ra * p.tiles_k + at) * 2);
+          ptx::tma_load_2d(sf + kSfBytes<MX>, &p.sb, sfb, 0, (tn * 2 * p.tiles_k + at) * 2);
+          ptx::tma_load_2d(sf + 2 * kSfBytes<MX>, &p.sb, sfb, 0, ((tn * 2 + 1) * p.tiles_k + at) * 2);
+          ++sf_issued;
+          if (++stage == kSfStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp >= kSfWarp0) {
     // -------------------------------------------------------------- scales (both CTAs)
     // Lane l of every quarter holds, column by column, the scales of rows l, 32 + l, 64 + l, 96 + l
     // of a 512-byte tile: 16 consecutive bytes of it.
@@ -307,17 +338,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     // stores and the arrive is longer than its instructions.
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t total = first < ntiles ? uint32_t((ntiles - first + step - 1) / step) * uint32_t(p.stages) : 0u;
-    for (uint32_t j = uint32_t(warp - 2 - kEpiWarps) >> 2; j < total; j += kSfGroups) {
-      const uint32_t stage = j % kPairStages, slot = j % kSlots;
-      // the slot's last stage has been multiplied
-      bool ok = true;
-      if (j >= uint32_t(kSlots)) {
-        const uint32_t u = j - uint32_t(kSlots);
-        ok = mbar_wait_bounded(empty_bar(int(u % kPairStages)), (u / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
-      }
-      ok = ok && mbar_wait_bounded(sf_full_bar(int(stage)), (j / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
+    for (uint32_t j = uint32_t(warp - kSfWarp0) >> 2; j < total; j += kSfGroups) {
+      const uint32_t stage = j % kSfStages, slot = j % kSlots;
+      bool ok = mbar_wait_bounded(sf_full_bar(int(stage)), (j / kSfStages) & 1u, abort_flag, p.status, p.timeout_ns);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
       const uint8_t* src = smem_raw + (sf_base - raw) + stage * 3u * kSfBytes<MX> + 16 * lane;
       uint32_t w[kSfCols<MX>];
 #pragma unroll
@@ -325,6 +349,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
 #pragma unroll
         for (int o = 0; o < 3; ++o)
           *reinterpret_cast<uint4*>(w + 12 * a + 4 * o) = *reinterpret_cast<const uint4*>(src + o * kSfBytes<MX> + 512 * a);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(sf_empty_bar(int(stage)));
+      if (j >= uint32_t(kSlots)) {   // the slot's last stage has been multiplied
+        const uint32_t u = j - uint32_t(kSlots);
+        ok = mbar_wait_bounded(empty_bar(int(u % kPairStages)), (u / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      }
       const uint32_t c = tmem + kSfCol + slot * kSfCols<MX> + lanes;
       ptx::tc_fence_after();
       ptx::tmem_st_32x32b_x16(c, w);
@@ -412,9 +443,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         mbar_wait_drain(full_bar(s), (j / uint32_t(kPairStages)) & 1u, p.timeout_ns);
       }
     }
-    if (threadIdx.x == 0)   // this CTA's scales count on its own barriers
-      for (uint32_t j = n_issued > uint32_t(kPairStages) ? n_issued - uint32_t(kPairStages) : 0u; j < n_issued; ++j)
-        mbar_wait_drain(sf_full_bar(int(j % uint32_t(kPairStages))), (j / uint32_t(kPairStages)) & 1u, p.timeout_ns);
+    // (each CTA's scales count on its own barriers)
+    if (warp == kSfLoader && lane == 0)
+      for (uint32_t j = sf_issued > uint32_t(kSfStages) ? sf_issued - uint32_t(kSfStages) : 0u; j < sf_issued; ++j)
+        mbar_wait_drain(sf_full_bar(int(j % uint32_t(kSfStages))), (j / uint32_t(kSfStages)) & 1u, p.timeout_ns);
     ptx::cluster_sync();
   }
   ptx::tc_fence_after();
