@@ -349,8 +349,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
 #pragma unroll
         for (int o = 0; o < 3; ++o)
           *reinterpret_cast<uint4*>(w + 12 * a + 4 * o) = *reinterpret_cast<const uint4*>(src + o * kSfBytes<MX> + 512 * a);
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(sf_empty_bar(int(stage)));
       if (j >= uint32_t(kSlots)) {   // the slot's last stage has been multiplied
         const uint32_t u = j - uint32_t(kSlots);
         ok = mbar_wait_bounded(empty_bar(int(u % kPairStages)), (u / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
@@ -366,11 +364,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         ptx::tmem_st_32x32b_x16(c + 32, w + 32);
       }
       // The stores have completed before the arrive, which therefore needs no wider release than its
-      // own CTA's (a cluster-scope one in every stage: 8192^3 214 -> 402 us).
+      // own CTA's (a cluster-scope one in every stage: 8192^3 214 -> 402 us). The shared memory goes
+      // back only now too: an arrive in front of the stores can pass loads whose values nothing has
+      // used yet, and the next copy then overwrites what they read.
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(sf_ready_bar(int(slot)), 0));
+      if (lane == 0) {
+        ptx::mbar_arrive_remote_cta(ptx::mapa_shared(sf_ready_bar(int(slot)), 0));
+        ptx::mbar_arrive(sf_empty_bar(int(stage)));
+      }
     }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)

@@ -189,6 +189,23 @@ def test_product(fmt, odt, m, n, k):
     check_product((a, b), (va, vb), out)
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("m,n,k", [(2048, 8192, 1280), (1000, 7000, 4000), (5000, 2500, 2304)])
+def test_product_many_tiles_and_stages(fmt, m, n, k):
+    # every CTA pair takes several tiles of many stages: all rings go round
+    a, b = mo.Fp4Tensor(m, k, fmt), mo.Fp4Tensor(n, k, fmt)
+    mo.fp4_quantize(data(m, k, torch.bfloat16, 1), a)
+    mo.fp4_quantize(data(n, k, torch.bfloat16, 2), b)
+    va, vb = torch.empty((m, k), device=dev()), torch.empty((n, k), device=dev())
+    mo.fp4_dequantize(a, va)
+    mo.fp4_dequantize(b, vb)
+    for odt in (torch.float32, torch.bfloat16):
+        out = torch.full((m, n), 9.0, dtype=odt, device=dev())
+        mo.fp4_product(a, b, out)
+        assert mo.mo_last_device_error() == 0
+        check_product((a, b), (va.double(), vb.double()), out)
+
+
 @pytest.mark.parametrize("m,n,k", [(40, 200, 2048), (300, 5120, 512)])
 def test_product_repeats_bit_for_bit_and_on_a_side_stream(m, n, k):
     a, _ = operand(m, k, "nv", 1)
