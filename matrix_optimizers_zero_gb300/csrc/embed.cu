@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "device_common.cuh"
+#include "launch.cuh"
 #include "philox.cuh"
 #include "ptx_train.cuh"
 #include "train_kernels.h"
@@ -668,17 +669,10 @@ template <typename T, int V>
 cudaError_t sum_as(const GradParams& p, cudaStream_t stream) {
   const GradGrid g = grad_grid(p.tokens.n, p.dim);
   const int64_t y = g.chunks < 32768 ? g.chunks : 32768;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(g.col_blocks), unsigned(y), unsigned((g.chunks + y - 1) / y));
-  cfg.blockDim = dim3(unsigned(g.threads), 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // the launch overlaps the sort's end
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return p.drop.threshold != 0 ? cudaLaunchKernelEx(&cfg, embed_sum_kernel<T, V, true>, p)
-                               : cudaLaunchKernelEx(&cfg, embed_sum_kernel<T, V, false>, p);
+  // the launch overlaps the sort's end
+  return launch_kernel(p.drop.threshold != 0 ? embed_sum_kernel<T, V, true> : embed_sum_kernel<T, V, false>,
+                       dim3(unsigned(g.col_blocks), unsigned(y), unsigned((g.chunks + y - 1) / y)), dim3(unsigned(g.threads)), 0, 1,
+                       true, stream, p);
 }
 
 }  // namespace
@@ -694,25 +688,16 @@ cudaError_t launch_embed_lookup(const LookupParams& p, bool table_bf16, bool out
 
 cudaError_t launch_embed_grad(const GradParams& p, bool dout_bf16, cudaStream_t stream) {
   static_assert(kSortSmem <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSortSmem));
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(embed_sort_kernel), kSortSmem);
   if (e != cudaSuccess) return e;
   // few tokens sort faster without the cluster's barriers
   const int64_t ctas = p.tokens.n <= kOneCtaTokens ? 1 : 8;
   const int64_t zeros = p.accumulate ? 0 : (p.vocab * p.dim * 4 + kZeroBytes - 1) / kZeroBytes;
-  const int bins = 1 << p.digit_bits;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ctas + (zeros + ctas - 1) / ctas * ctas), 1, 1);
-  cfg.blockDim = dim3(kSortThreads, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(uint32_t) * (size_t(kSortWarps) * size_t(bins + 1) + 2 * size_t(bins) + kSortWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(ctas);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, p)) != cudaSuccess) return e;
+  const size_t bins = size_t(1) << p.digit_bits;
+  const size_t smem = sizeof(uint32_t) * (size_t(kSortWarps) * (bins + 1) + 2 * bins + kSortWarps);
+  e = launch_kernel(embed_sort_kernel, dim3(unsigned(ctas + (zeros + ctas - 1) / ctas * ctas)), dim3(kSortThreads), smem,
+                    unsigned(ctas), false, stream, p);
+  if (e != cudaSuccess) return e;
   const bool vec = (p.dim & 7) == 0;
   if (dout_bf16) return vec ? sum_as<uint16_t, 8>(p, stream) : sum_as<uint16_t, 1>(p, stream);
   return vec ? sum_as<float, 8>(p, stream) : sum_as<float, 1>(p, stream);

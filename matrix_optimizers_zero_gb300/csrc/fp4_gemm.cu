@@ -17,6 +17,7 @@
 #include <mutex>
 
 #include "device_common.cuh"
+#include "launch.cuh"
 #include "ptx_train.cuh"
 #include "train_kernels.h"
 
@@ -211,6 +212,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // All of the above overlaps the previous kernel's end. The next one may come only now: its blocks
+  // take their TMEM before they wait for this grid, and this block has its own.
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
 
   const int32_t ntiles = p.tiles_m * p.tiles_n;
   const int32_t first = int32_t(ptx::cluster_id_x()), step = int32_t(ptx::nclusters_x());
@@ -517,6 +522,8 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  ptx::griddep_launch_dependents();   // after the TMEM is held, as above
+  ptx::griddep_wait();
 
   uint32_t n_issued = 0;
   bool mma_issued = false;
@@ -685,26 +692,6 @@ bool encode_scales(EncodeTiledFn enc, CUtensorMap* map, const Fp4In& q, uint32_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename K>
-cudaError_t launch(K kern, const ProductParams& p, unsigned grid, unsigned threads, size_t smem, unsigned cluster,
-                   cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
 // A has more than one tile of rows only with NT = 128, so a tile's scales begin a scale tile; every
 // CTA of a cluster has at least two stages.
 template <bool MX, int NT, typename O>
@@ -714,7 +701,10 @@ cudaError_t narrow_as(ProductParams& p, int sms, cudaStream_t stream) {
   const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
   unsigned parts = 1;
   while (parts < 8 && tiles * parts * 2 <= 2 * sms && p.stages >= int32_t(parts) * 4) parts *= 2;
-  return launch(fp4_narrow_kernel<MX, NT, O>, p, unsigned(tiles * parts), kNarrowThreads, kNarrowSmem<MX, NT>, parts, stream);
+  auto kern = fp4_narrow_kernel<MX, NT, O>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kNarrowSmem<MX, NT>);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(unsigned(tiles * parts)), dim3(kNarrowThreads), kNarrowSmem<MX, NT>, parts, true, stream, p);
 }
 
 template <bool MX, typename O>
@@ -737,7 +727,10 @@ cudaError_t product_as(ProductParams& p, const Fp4In& a, const Fp4In& b, int sms
   p.tiles_m = int32_t((p.m + 255) / 256);
   p.tiles_n = int32_t((p.n + 255) / 256);
   const unsigned grid = unsigned(2 * std::min(pairs, pair_tiles));
-  return launch(fp4_pair_kernel<MX, O>, p, grid, kPairThreads, kPairSmem<MX>, 2, stream);
+  auto kern = fp4_pair_kernel<MX, O>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kPairSmem<MX>);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(grid), dim3(kPairThreads), kPairSmem<MX>, 2, true, stream, p);
 }
 
 }  // namespace

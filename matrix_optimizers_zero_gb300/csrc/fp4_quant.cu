@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "device_common.cuh"
+#include "launch.cuh"
 #include "philox.cuh"
 #include "ptx_train.cuh"
 #include "train_kernels.h"
@@ -189,6 +190,9 @@ __global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const QuantPa
   const int64_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x - tr * p.tiles_c;
   const int64_t r0 = tr * kTile, c0 = tc * kTile;
   const T* x = static_cast<const T*>(p.x);
+  ptx::griddep_launch_dependents();
+  // after the launch that measured amax, which waited for whatever wrote x, x can be loaded at once
+  if (!p.measured) ptx::griddep_wait();
   const bool full = r0 + kTile <= p.rows && c0 + kTile <= p.cols && p.vec;
   if (full) {
 #pragma unroll 8
@@ -203,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const QuantPa
       tile[r * P + c] = r0 + r < p.rows && c0 + c < p.cols ? x[(r0 + r) * p.cols + c0 + c] : T(0);
     }
   }
+  if (p.measured) ptx::griddep_wait();
   const int gexp = MX ? 0 : tensor_exponent(p.amax);
   if (!MX && blockIdx.x == 0 && tid == 0) {
     if (p.row.amax != nullptr) *p.row.amax = *p.amax;
@@ -248,6 +253,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) fp4_amax_kernel(const T* x, int64_t n, uint32_t* amax) {
   constexpr int E = 16 / int(sizeof(T));
   constexpr int U = 4;
+  ptx::griddep_launch_dependents();
   uint32_t top = 0;
   auto take = [&](float v) {
     const uint32_t b = abs_bits(v);
@@ -288,6 +294,8 @@ constexpr int kDequantU = 2;
 
 template <typename O, bool MX>
 __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const Fp4In q, O* out, int vec) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const int row = int(blockIdx.x) * 8 + int(threadIdx.y);
   if (row >= q.rows) return;
   const int k = int(q.k), g0 = int(blockIdx.y) * (32 * kDequantU) + int(threadIdx.x);
@@ -352,11 +360,10 @@ template <typename T, bool MX, bool STOCH>
 cudaError_t quantize_as(const QuantParams& p, cudaStream_t stream) {
   constexpr size_t smem = size_t(kTile) * kPitch<T> * sizeof(T);
   auto kern = fp4_quantize_kernel<T, MX, STOCH>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (p.rows + kTile - 1) / kTile * p.tiles_c;
-  kern<<<unsigned(tiles), kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(kern, dim3(unsigned(tiles)), dim3(kThreads), smem, 1, true, stream, p);
 }
 
 }  // namespace
@@ -388,18 +395,12 @@ cudaError_t launch_fp4_dequantize(const Fp4In& q, bool mx, void* out, bool out_b
   const int vec = q.k % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   if (out_bf16) {
     uint16_t* o = static_cast<uint16_t*>(out);
-    if (mx)
-      fp4_dequantize_kernel<uint16_t, true><<<grid, block, 0, stream>>>(q, o, vec);
-    else
-      fp4_dequantize_kernel<uint16_t, false><<<grid, block, 0, stream>>>(q, o, vec);
-  } else {
-    float* o = static_cast<float*>(out);
-    if (mx)
-      fp4_dequantize_kernel<float, true><<<grid, block, 0, stream>>>(q, o, vec);
-    else
-      fp4_dequantize_kernel<float, false><<<grid, block, 0, stream>>>(q, o, vec);
+    return launch_kernel(mx ? fp4_dequantize_kernel<uint16_t, true> : fp4_dequantize_kernel<uint16_t, false>, grid, block, 0, 1,
+                         true, stream, q, o, vec);
   }
-  return cudaGetLastError();
+  float* o = static_cast<float*>(out);
+  return launch_kernel(mx ? fp4_dequantize_kernel<float, true> : fp4_dequantize_kernel<float, false>, grid, block, 0, 1, true,
+                       stream, q, o, vec);
 }
 
 }  // namespace mo

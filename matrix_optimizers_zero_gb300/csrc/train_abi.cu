@@ -313,6 +313,7 @@ int fp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, const
       float* top = p.row.amax != nullptr ? p.row.amax : p.col.amax;
       if ((e = mo::launch_fp4_amax(x, dtype == MO_BF16, rows * cols, top, sms, stream)) != cudaSuccess) return report_cuda(e);
       p.amax = top;
+      p.measured = 1;
     }
   }
   e = mo::launch_fp4_quantize(p, dtype == MO_BF16, format == MO_FP4_MX, stochastic != nullptr, stream);

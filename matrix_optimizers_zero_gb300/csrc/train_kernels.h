@@ -117,6 +117,7 @@ struct QuantParams {
   Fp4Out row, col;         // blocks along the rows of x, and along its columns (transposed)
   RandomArgs rnd;          // of stochastic rounding
   int32_t vec;             // rows are 16-byte aligned
+  int32_t measured;        // the launch before this one, a normal one, writes *amax
 };
 cudaError_t launch_fp4_quantize(const QuantParams& p, bool bf16, bool mx, bool stochastic, cudaStream_t stream);
 cudaError_t launch_fp4_amax(const void* x, bool bf16, int64_t n, float* amax, int sms, cudaStream_t stream);
