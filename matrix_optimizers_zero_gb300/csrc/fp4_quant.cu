@@ -19,12 +19,12 @@
 namespace mo {
 namespace {
 
-// A 128 x 128 tile of x goes through shared memory, from which both
+// A 64 x 64 tile of x goes through shared memory, from which both
 // orientations are quantised: x is read once for the operands of a forward and
 // a backward product. Row pitch in elements: 16 bytes more than the row, so
 // that 32 threads reading 16 bytes of 32 rows meet all banks.
-constexpr int kTile = 128;
-constexpr int kThreads = 256;
+constexpr int kTile = kQuantTile;
+constexpr int kThreads = 128;
 template <typename T>
 constexpr int kPitch = kTile + 16 / int(sizeof(T));
 
@@ -180,7 +180,7 @@ __device__ __forceinline__ void put32(const Fp4Out& q, int64_t row, int64_t k0, 
 }
 
 template <typename T, bool MX, bool STOCH>
-__global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, 6) fp4_quantize_kernel(const QuantParams p) {
   extern __shared__ __align__(16) uint8_t tile_smem[];
   T* tile = reinterpret_cast<T*>(tile_smem);
   constexpr int P = kPitch<T>;
@@ -214,16 +214,14 @@ __global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const QuantPa
     if (p.col.amax != nullptr) *p.col.amax = *p.amax;
   }
   __syncthreads();
-  const int line = tid & (kTile - 1), half = tid >> 7;   // a row (a column) of the tile, 64 elements of it
-  // With stochastic rounding one copy of the code serves both orientations and both 32-element
-  // parts: unrolled four times it no longer fits the instruction cache.
-  constexpr int kUnroll = STOCH ? 1 : 2;
-  const int begin = p.row.codes != nullptr ? 0 : 2, end = p.col.codes != nullptr ? 4 : 2;
-#pragma unroll kUnroll
+  const int line = tid & (kTile - 1), at = tid / kTile * 32;   // a row (a column) of the tile, 32 elements of it
+  // One copy of the code serves both orientations: twice as long, with stochastic rounding, it no
+  // longer fits the instruction cache.
+  const int begin = p.row.codes != nullptr ? 0 : 1, end = p.col.codes != nullptr ? 2 : 1;
+#pragma unroll 1
   for (int it = begin; it < end; ++it) {
-    const bool by_row = it < 2;
+    const bool by_row = it == 0;
     const Fp4Out& q = by_row ? p.row : p.col;
-    const int at = half * 64 + (it & 1) * 32;
     float v[32];
     if (by_row) {
       const T* src = tile + line * P + at;
@@ -362,7 +360,7 @@ cudaError_t quantize_as(const QuantParams& p, cudaStream_t stream) {
   auto kern = fp4_quantize_kernel<T, MX, STOCH>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (p.rows + kTile - 1) / kTile * p.tiles_c;
+  const int64_t tiles = (p.rows + 127) / 128 * (128 / kTile) * p.tiles_c;   // whole scale tiles
   return launch_kernel(kern, dim3(unsigned(tiles)), dim3(kThreads), smem, 1, true, stream, p);
 }
 

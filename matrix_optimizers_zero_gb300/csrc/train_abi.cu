@@ -302,7 +302,7 @@ int fp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, const
   p.x = x;
   p.rows = rows;
   p.cols = cols;
-  p.tiles_c = (cols + 127) / 128;
+  p.tiles_c = (cols + 127) / 128 * (128 / mo::kQuantTile);   // whole scale tiles
   p.vec = cols % (16 / int64_t(dtype_bytes(dtype))) == 0 ? 1 : 0;
   if (by_row != nullptr) p.row = fp4_out(by_row);
   if (by_col != nullptr) p.col = fp4_out(by_col);

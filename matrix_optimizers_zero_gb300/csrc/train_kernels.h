@@ -110,6 +110,7 @@ struct Fp4In {
   int64_t tiles_r, tiles_k;
 };
 
+constexpr int kQuantTile = 64;   // rows and columns of x a block takes
 struct QuantParams {
   const void* x;           // [rows, cols]
   const float* amax;       // nv: its largest magnitude
