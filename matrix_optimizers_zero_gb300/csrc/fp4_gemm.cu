@@ -34,7 +34,7 @@ constexpr int kStepsPerTile = MX ? 2 : 1;
 template <bool MX>
 constexpr uint32_t kSfBytes = 512u * kSfTiles<MX>;
 
-struct alignas(64) ProductParams {
+struct ProductParams {
   CUtensorMap a, b, sa, sb;   // codes (128-byte swizzle) and scale tiles of both operands
   void* out;
   const float* amax_a;
@@ -119,6 +119,11 @@ __device__ __forceinline__ void store32<float>(float* row, int64_t col, int64_t 
 // stage beside 125 for each of its four instructions. Stores from registers
 // (tcgen05.st) run beside it (8192^3: mx 267 -> 201 us, nv 357 -> 211 us).
 //
+// The issuing thread bounds a stage as much as the tensor core does: with
+// operand descriptors put together for every instruction 8192^3 takes 201 us
+// (mx), with precomputed halves 180. For the same reason tiles 192 wide, whose
+// last round of tiles is fuller, take as long a stage as these.
+//
 // TMEM: an accumulator takes 256 columns and a stage's scales 24 (mx) or 48
 // (nv), and a stage's scales are written while the last one's are in use. So
 // the two accumulators overlap in 96 columns, [160, 256): the epilogue drains
@@ -129,8 +134,9 @@ constexpr int kSfGroups = 2;
 constexpr int kSfWarp0 = 2 + kEpiWarps;
 constexpr int kSfLoader = kSfWarp0 + kSfGroups * kSfWarps;
 constexpr int kPairThreads = 32 * (kSfLoader + 1);
-constexpr int kPairStages = 5;
 constexpr int kSfStages = 8;   // scales run farther ahead: they have one step more to go
+
+constexpr int kPairStages = 5;
 constexpr uint32_t kAccStep = 160;
 constexpr uint32_t kSfCol = 416;
 template <bool MX>
@@ -161,7 +167,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   // panels first (1024-byte aligned), then the scale tiles of every stage, then control
-  const uint32_t sf_base = base + uint32_t(kPairStages) * 2u * kPanelBytes;
+  const uint32_t sf_base = base + uint32_t(kPairStages) * kStage;
   const uint32_t bars = sf_base + uint32_t(kSfStages) * 3u * kSfBytes<MX>;
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kPairBars);
   uint32_t* tmem_slot = ctrl;
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       for (int32_t t = first; ok && t < ntiles; t += step) {
         int32_t tm, tn;
         tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
-        const int32_t ra = tm * 2 + int32_t(rank), rb = tn * 2 + int32_t(rank);   // 128-row panels
+        const int32_t ra = tm * 256 + int32_t(rank) * 128, rb = tn * 256 + int32_t(rank) * 128;
         for (int32_t kb = 0; kb < p.stages; ++kb) {
           if (!mbar_wait_bounded(empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) {
             ok = false;
@@ -239,9 +245,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           const uint32_t fb_local = full_bar(stage);
           if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * kStage);
           const uint32_t fb = ptx::mapa_shared(fb_local, 0);
-          const uint32_t sa = base + uint32_t(stage) * 2u * kPanelBytes;
-          ptx::tma_load_2d_pair(sa, &p.a, fb, kb * 128, ra * 128);
-          ptx::tma_load_2d_pair(sa + kPanelBytes, &p.b, fb, kb * 128, rb * 128);
+          const uint32_t sa = base + uint32_t(stage) * kStage;
+          ptx::tma_load_2d_pair(sa, &p.a, fb, kb * 128, ra);
+          ptx::tma_load_2d_pair(sa + kPanelBytes, &p.b, fb, kb * 128, rb);
           ++n_issued;
           if (++stage == kPairStages) {
             stage = 0;
@@ -256,6 +262,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       int stage = 0, slot = 0;
       uint32_t ph = 0, sph = 0;
       bool ok = true, seen = false;   // seen: the stage is known to be complete
+      const uint32_t desc_lo = ptx::desc_lo_sw128(base);
       int32_t i = 0;
       for (int32_t t = first; ok && t < ntiles; t += step, ++i) {
         const int acc = i & 1;
@@ -273,8 +280,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sa = base + uint32_t(stage) * 2u * kPanelBytes;
-          const uint32_t sb = sa + kPanelBytes, sf = tmem + kSfCol + uint32_t(slot) * kSfCols<MX>;
+          const uint32_t a_lo = desc_lo + uint32_t(stage) * (kStage / 16), b_lo = a_lo + kPanelBytes / 16;
+          const uint32_t sf = tmem + kSfCol + uint32_t(slot) * kSfCols<MX>;
           const uint32_t bar = empty_bar(stage);
           if (++slot == kSlots) {
             slot = 0;
@@ -284,19 +291,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
             stage = 0;
             ph ^= 1u;
           }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk < left) {
-              constexpr uint32_t idesc0 = ptx::idesc_fp4(256, 256, MX, 0);
-              constexpr uint32_t idesc2 = ptx::idesc_fp4(256, 256, MX, 2);
-              const uint32_t c = sf + 12u * uint32_t(kk / kStepsPerTile<MX>);
-              ptx::umma_fp4<true, MX>(d, ptx::smem_desc_sw128(sa + uint32_t(kk) * 32u, 16u, 1024u),
-                                      ptx::smem_desc_sw128(sb + uint32_t(kk) * 32u, 16u, 1024u),
-                                      MX && (kk & 1) ? idesc2 : idesc0, c, c + 4, (kb | kk) != 0 ? 1u : 0u);
-            }
-            // the next stage is looked at while this one's instructions are under way
-            if (kk == 1) seen = ptx::mbar_peek(sf_ready_bar(slot), sph) && ptx::mbar_peek(full_bar(stage), ph);
+          // instruction kk: 32 bytes of codes, its scales
+          auto issue = [&](int kk) {
+            const uint32_t c = sf + 12u * uint32_t(kk / kStepsPerTile<MX>);
+            ptx::umma_fp4<true, MX>(d, a_lo + 2u * uint32_t(kk), b_lo + 2u * uint32_t(kk), ptx::kDescHiSw128,
+                                    ptx::idesc_fp4(256, 256, MX, MX && (kk & 1) ? 2 : 0), c, c + 4, kk > 0 || kb > 0);
+          };
+          issue(0);
+          if (left >= 4) {
+            issue(1);
+            issue(2);
+            issue(3);
+          } else {
+            for (int kk = 1; kk < left; ++kk) issue(kk);
           }
+          // the next stage is looked at while these are under way
+          seen = ptx::mbar_peek(sf_ready_bar(slot), sph) && ptx::mbar_peek(full_bar(stage), ph);
           left -= 4;
           ptx::umma_commit_pair(bar, 0x3);
           mma_issued = true;
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       for (int32_t t = first; ok && t < ntiles; t += step) {
         int32_t tm, tn;
         tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
-        const int32_t ra = tm * 2 + int32_t(rank);
+        const int32_t ra = tm * 2 + int32_t(rank), rb = tn * 2;
         for (int32_t kb = 0; kb < p.stages; ++kb) {
           if (!mbar_wait_bounded(sf_empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) {
             ok = false;
@@ -325,8 +335,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           const int32_t at = kb * kSfTiles<MX>;
           ptx::mbar_arrive_expect_tx(sfb, 3 * kSfBytes<MX>);
           ptx::tma_load_2d(sf, &p.sa, sfb, 0, (ra * p.tiles_k + at) * 2);
-          ptx::tma_load_2d(sf + kSfBytes<MX>, &p.sb, sfb, 0, (tn * 2 * p.tiles_k + at) * 2);
-          ptx::tma_load_2d(sf + 2 * kSfBytes<MX>, &p.sb, sfb, 0, ((tn * 2 + 1) * p.tiles_k + at) * 2);
+          ptx::tma_load_2d(sf + kSfBytes<MX>, &p.sb, sfb, 0, (rb * p.tiles_k + at) * 2);
+          ptx::tma_load_2d(sf + 2 * kSfBytes<MX>, &p.sb, sfb, 0, ((rb + 1) * p.tiles_k + at) * 2);
           ++sf_issued;
           if (++stage == kSfStages) {
             stage = 0;
@@ -575,13 +585,11 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if (kk < left) {
-            constexpr uint32_t idesc0 = ptx::idesc_fp4(128, NT, MX, 0);
-            constexpr uint32_t idesc2 = ptx::idesc_fp4(128, NT, MX, 2);
             const int a = kk / kStepsPerTile<MX>;
             const uint32_t c = tmem + uint32_t(kNarrowCols<NT> == 64 ? 32 : NT) + uint32_t(a) * 8u;
-            ptx::umma_fp4<false, MX>(tmem, ptx::smem_desc_sw128(sp + uint32_t(kk) * 32u, 16u, 1024u),
-                                     ptx::smem_desc_sw128(sq + uint32_t(kk) * 32u, 16u, 1024u),
-                                     MX && (kk & 1) ? idesc2 : idesc0, c, c + 4, (kb > k0 || kk > 0) ? 1u : 0u);
+            ptx::umma_fp4<false, MX>(tmem, ptx::desc_lo_sw128(sp) + 2u * uint32_t(kk), ptx::desc_lo_sw128(sq) + 2u * uint32_t(kk),
+                                     ptx::kDescHiSw128, ptx::idesc_fp4(128, NT, MX, MX && (kk & 1) ? 2 : 0), c, c + 4,
+                                     kb > k0 || kk > 0);
           }
         }
         left -= 4;

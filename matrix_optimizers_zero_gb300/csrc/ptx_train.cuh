@@ -39,16 +39,19 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) 
 
 // D (+)= (A sA)(B sB)^T over K = 64. kMx: a scale for 32 elements (e8m0),
 // otherwise for 16 (e4m3). The accumulator, and the A scales, are those of
-// each CTA's own rows; each CTA holds the B scales of all N columns.
+// each CTA's own rows; each CTA holds the B scales of all N columns. The
+// descriptors share their upper halves (desc_hi): one thread issues these, and
+// every instruction it spends on an operand delays the tensor core.
 template <bool kPair, bool kMx>
-__device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+__device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t desc_hi, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, bool accumulate) {
 #define MO_UMMA_FP4(GROUP, KIND, VEC)                                                                    \
   asm volatile(                                                                                          \
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                                  \
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"                              \
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"                                                 \
       "tcgen05.mma.cta_group::" GROUP ".kind::" KIND ".block_scale.scale_vec::" VEC                      \
-      " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc),        \
-      "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)                                                      \
+      " [%0], a, b, %4, [%6], [%7], p;\n\t}" ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), \
+      "r"(accumulate ? 1u : 0u), "r"(sfa_tmem), "r"(sfb_tmem)                                            \
       : "memory")
   if (kPair && kMx) MO_UMMA_FP4("2", "mxf4", "2X");
   if (kPair && !kMx) MO_UMMA_FP4("2", "mxf4nvf4", "4X");
@@ -56,6 +59,12 @@ __device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint64_t adesc, uint64
   if (!kPair && !kMx) MO_UMMA_FP4("1", "mxf4nvf4", "4X");
 #undef MO_UMMA_FP4
 }
+
+// Upper half of the descriptor of a K-major operand of 128-byte rows
+// (smem_desc_sw128 with 1024 bytes between 8-row groups); the lower half is
+// the address / 16 with the unused leading dimension (1) above it.
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_sw128(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 
 __device__ __forceinline__ uint32_t cluster_nctarank() {
   uint32_t r;
