@@ -57,17 +57,25 @@ __device__ __forceinline__ float scale_of(const float* amax) {
   return __uint_as_float(uint32_t(max(e, -126) + 127) << 23);
 }
 
-// 32 consecutive outputs of one row.
-template <typename O>
-__device__ __forceinline__ void store32(O* row, int64_t col, int64_t n, int align, const float (&v)[32]);
+__device__ __forceinline__ void put(uint16_t* o, float v) { *o = float_to_bf16_bits(v); }
+__device__ __forceinline__ void put(float* o, float v) { *o = v; }
 
-template <>
-__device__ __forceinline__ void store32<uint16_t>(uint16_t* row, int64_t col, int64_t n, int align, const float (&v)[32]) {
-  uint16_t* o = row + col;
-  if (col + 32 <= n && align != 0) {
-    uint32_t w[2][8];
+// Stores a chunk of 32 columns, a row a lane, of the 32 rows from `row0` on.
+// Rows that are 16-byte aligned and a whole chunk: vectors, 32 bytes wide
+// where the rows allow it. Others (an odd n, the last columns) would store
+// element by element into 32 rows at a time, so the chunk is turned in shared
+// memory, and a warp stores one row after the other.
+constexpr uint32_t kTurnWords = 17 * 32;   // a warp's: 32 rows of 16 words, each a word apart from the next
+
+__device__ __forceinline__ void store_chunk(uint16_t* out, int64_t row0, int64_t m, int64_t col, int64_t n, int align,
+                                            const float (&v)[32], uint32_t* turn) {
+  const int lane = int(threadIdx.x & 31);
+  uint32_t w[2][8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) w[j >> 3][j & 7] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  for (int j = 0; j < 16; ++j) w[j >> 3][j & 7] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  if (align != 0 && col + 32 <= n) {
+    if (row0 + lane >= m) return;
+    uint16_t* o = out + (row0 + lane) * n + col;
     if (align == 32) {
       ptx::st_global_v8(o, w[0]);
       ptx::st_global_v8(o + 16, w[1]);
@@ -77,17 +85,26 @@ __device__ __forceinline__ void store32<uint16_t>(uint16_t* row, int64_t col, in
         reinterpret_cast<uint4*>(o)[j] = make_uint4(w[j >> 1][4 * (j & 1)], w[j >> 1][4 * (j & 1) + 1],
                                                     w[j >> 1][4 * (j & 1) + 2], w[j >> 1][4 * (j & 1) + 3]);
     }
-  } else {
+    return;
+  }
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i < n) o[i] = float_to_bf16_bits(v[i]);
+  for (int j = 0; j < 16; ++j) turn[lane * 17 + j] = w[j >> 3][j & 7];
+  __syncwarp();
+  const int rows = int(min(int64_t(32), m - row0));
+  if (col + lane < n) {
+    uint16_t* o = out + row0 * n + col + lane;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) o[r * n] = uint16_t(turn[r * 17 + (lane >> 1)] >> (16 * (lane & 1)));
   }
 }
 
-template <>
-__device__ __forceinline__ void store32<float>(float* row, int64_t col, int64_t n, int align, const float (&v)[32]) {
-  float* o = row + col;
-  if (col + 32 <= n && align != 0) {
+__device__ __forceinline__ void store_chunk(float* out, int64_t row0, int64_t m, int64_t col, int64_t n, int align,
+                                            const float (&v)[32], uint32_t* turn) {
+  const int lane = int(threadIdx.x & 31);
+  if (align != 0 && col + 32 <= n) {
+    if (row0 + lane >= m) return;
+    float* o = out + (row0 + lane) * n + col;
     if (align == 32) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -101,10 +118,19 @@ __device__ __forceinline__ void store32<float>(float* row, int64_t col, int64_t 
       for (int j = 0; j < 8; ++j)
         reinterpret_cast<float4*>(o)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     }
-  } else {
+    return;
+  }
+  const int rows = int(min(int64_t(32), m - row0));
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i < n) o[i] = v[i];
+  for (int h = 0; h < 2; ++h) {   // 16 columns at a time: two rows a store
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) turn[lane * 17 + j] = __float_as_uint(v[16 * h + j]);
+    __syncwarp();
+    const int64_t c = col + 16 * h + (lane & 15);
+    if (c < n)
+#pragma unroll 8
+      for (int r = lane >> 4; r < rows; r += 2) out[(row0 + r) * n + c] = __uint_as_float(turn[r * 17 + (lane & 15)]);
   }
 }
 
@@ -145,7 +171,8 @@ template <bool MX>
 constexpr int kSfSlots = int(96 / kSfCols<MX>);    // stages whose scales TMEM holds
 constexpr uint32_t kPairBars = 2 * kPairStages + 7 + 2 * kSfStages + 4;
 template <bool MX>
-constexpr size_t kPairSmem = 1024 + size_t(kPairStages) * 2 * kPanelBytes + size_t(kSfStages) * 3 * kSfBytes<MX> + 384;
+constexpr size_t kPairSmem = 1024 + size_t(kPairStages) * 2 * kPanelBytes + size_t(kSfStages) * 3 * kSfBytes<MX> + 384 +
+                             kEpiWarps * 4 * kTurnWords;
 static_assert(kAccStep + 256 <= kSfCol && kSfCol + 96 <= 512, "TMEM columns");
 static_assert(8 * kPairBars + 32 <= 384, "control block");
 static_assert(kPairSmem<false> <= 227 * 1024, "shared memory");
@@ -305,10 +332,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           } else {
             for (int kk = 1; kk < left; ++kk) issue(kk);
           }
-          // the next stage is looked at while these are under way
-          seen = ptx::mbar_peek(sf_ready_bar(slot), sph) && ptx::mbar_peek(full_bar(stage), ph);
           left -= 4;
           ptx::umma_commit_pair(bar, 0x3);
+          // the next stage is looked at while these are under way
+          seen = ptx::mbar_peek(sf_ready_bar(slot), sph) && ptx::mbar_peek(full_bar(stage), ph);
           mma_issued = true;
         }
         if (!ok) break;
@@ -395,6 +422,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     const int quarter = warp & 3;
     const int half = (warp - 2) >> 2;
     const float factor = scale_of(p.amax_a) * scale_of(p.amax_b);
+    uint32_t* turn = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 384) + (warp - 2) * kTurnWords;
     int32_t i = 0;
     for (int32_t t = first; t < ntiles; t += step, ++i) {
       const int acc = i & 1;
@@ -404,9 +432,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       ptx::tc_fence_after();
-      const int64_t row = int64_t(tm) * 256 + int64_t(rank) * 128 + quarter * 32 + lane;
+      const int64_t row0 = int64_t(tm) * 256 + int64_t(rank) * 128 + quarter * 32;
       const int64_t col = int64_t(tn) * 256;
-      O* out = static_cast<O*>(p.out) + (row < p.m ? row : 0) * p.n;
       const uint32_t tb = tmem + uint32_t(acc) * kAccStep + (uint32_t(quarter * 32) << 16);
       // Chunks of 32 columns, every other one each half's. Accumulator 0 ends in the shared columns
       // (chunks 7, 6, 5), accumulator 1 begins with them (0, 1, 2): each warp takes two chunks to
@@ -428,7 +455,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[q][j]) * factor;
-          if (row < p.m && at < p.n) store32<O>(out, at, p.n, p.align, v);
+          if (row0 < p.m && at < p.n) store_chunk(static_cast<O*>(p.out), row0, p.m, at, p.n, p.align, v, turn);
         }
       }
     }
@@ -477,35 +504,38 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
 // accumulator's lanes are the output's columns, so stores of a row of D are
 // contiguous across lanes. The CTAs of a cluster hold the parts of one tile.
 constexpr int kNarrowThreads = 192;
-constexpr int kNarrowStages = 4;
-constexpr uint32_t kNarrowPitch = 129;   // of the fp32 sums [NT][128] in shared memory
+constexpr uint32_t kNarrowPitch = 132;   // of the fp32 sums [NT][128] in shared memory
+template <int NT>
+constexpr int kNarrowStages = NT <= 32 ? 4 : 3;   // two CTAs an SM
 template <bool MX, int NT>
 constexpr uint32_t kNarrowStageBytes = kPanelBytes + NT * (kStageK / 2) + 2 * kSfBytes<MX>;
 template <bool MX, int NT>
-constexpr size_t kNarrowSmem = 1024 + size_t(kNarrowStages) * kNarrowStageBytes<MX, NT> + 128;
+constexpr size_t kNarrowSmem = 1024 + size_t(kNarrowStages<NT>) * kNarrowStageBytes<MX, NT> + 128;
 template <int NT>
 constexpr uint32_t kNarrowCols = NT <= 32 ? 64 : 2 * NT;   // TMEM: sums, then 8 columns of scales a tile
-static_assert(kNarrowStages * kPanelBytes >= 32 * kNarrowPitch * 4, "sums in the stages' memory (NT <= 32)");
-static_assert(kNarrowStages * (kPanelBytes + 128 * 128) >= 128 * kNarrowPitch * 4, "sums in the stages' memory (NT 128)");
+static_assert(2 * (kNarrowSmem<false, 128> + 1024) <= 228 * 1024 && 2 * kNarrowCols<128> <= 512, "two CTAs an SM");
+static_assert(4 * kPanelBytes >= 32 * kNarrowPitch * 4 && 3 * (kPanelBytes + 64 * 128) >= 64 * kNarrowPitch * 4 &&
+              3 * (kPanelBytes + 128 * 128) >= 128 * kNarrowPitch * 4, "sums in the stages' memory");
 
 template <bool MX, int NT, typename O>
 __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t smem_raw[];
   constexpr uint32_t kStage = kNarrowStageBytes<MX, NT>;
+  constexpr int kStages = kNarrowStages<NT>;
   constexpr uint32_t kQBytes = NT * (kStageK / 2);
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  const uint32_t sf_base = base + uint32_t(kNarrowStages) * (kPanelBytes + kQBytes);
-  const uint32_t bars = sf_base + uint32_t(kNarrowStages) * 2u * kSfBytes<MX>;
-  constexpr uint32_t kBars = 2 * kNarrowStages + 2;
+  const uint32_t sf_base = base + uint32_t(kStages) * (kPanelBytes + kQBytes);
+  const uint32_t bars = sf_base + uint32_t(kStages) * 2u * kSfBytes<MX>;
+  constexpr uint32_t kBars = 2 * kStages + 2;
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kBars);
   uint32_t* tmem_slot = ctrl;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 1);
   float* sums = reinterpret_cast<float*>(smem_raw + (base - raw));
   auto full_bar = [&](int s) { return bars + 8u * uint32_t(s); };
-  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(kNarrowStages + s); };
-  const uint32_t done_bar = bars + 8u * uint32_t(2 * kNarrowStages);
-  const uint32_t drain_bar = bars + 8u * uint32_t(2 * kNarrowStages + 1);
+  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(kStages + s); };
+  const uint32_t done_bar = bars + 8u * uint32_t(2 * kStages);
+  const uint32_t drain_bar = bars + 8u * uint32_t(2 * kStages + 1);
 
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
   const uint32_t parts = gridDim.x / uint32_t(p.tiles_m * p.tiles_n);   // CTAs of a cluster
@@ -515,7 +545,7 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
   const int32_t k0 = int32_t(int64_t(p.stages) * rank / parts), k1 = int32_t(int64_t(p.stages) * (rank + 1) / parts);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kNarrowStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(full_bar(s), 1);
       ptx::mbar_init(empty_bar(s), 1);
     }
@@ -534,6 +564,7 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
   const uint32_t tmem = *tmem_slot;
   ptx::griddep_launch_dependents();   // after the TMEM is held, as above
   ptx::griddep_wait();
+  const float factor = scale_of(p.amax_a) * scale_of(p.amax_b);
 
   uint32_t n_issued = 0;
   bool mma_issued = false;
@@ -553,7 +584,7 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
         ptx::tma_load_2d(sf, &p.sb, fb, 0, (tn * p.tiles_k + at) * 2);
         ptx::tma_load_2d(sf + kSfBytes<MX>, &p.sa, fb, 0, (tm * p.tiles_k + at) * 2);
         ++n_issued;
-        if (++stage == kNarrowStages) {
+        if (++stage == kStages) {
           stage = 0;
           ph ^= 1u;
         }
@@ -595,7 +626,7 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
         left -= 4;
         ptx::umma_commit_one(empty_bar(stage));
         mma_issued = true;
-        if (++stage == kNarrowStages) {
+        if (++stage == kStages) {
           stage = 0;
           ph ^= 1u;
         }
@@ -608,16 +639,24 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (ok) {
       ptx::tc_fence_after();
-      // every instruction has completed, so every stage has been read: its memory takes the sums
+      // lane l of a quarter holds column quarter 32 + l of the output. A CTA by itself stores it at
+      // once; the parts of a cluster's tile go to the memory of the stages, which have all been read.
+      const int64_t n_at = int64_t(tn) * 128 + quarter * 32 + lane;
+      O* out = static_cast<O*>(p.out) + int64_t(tm) * NT * p.n + n_at;
+      const int rows = int(min(int64_t(NT), p.m - int64_t(tm) * NT));
 #pragma unroll 1
-      for (int c = 0; c < NT; c += 16) {
+      for (int c = 0; c < rows; c += 16) {
         uint32_t r[16];
         __syncwarp();
         ptx::tmem_ld_32x32b_x16(tmem + uint32_t(c) + (uint32_t(quarter * 32) << 16), r);
         ptx::tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          sums[uint32_t(c + j) * kNarrowPitch + uint32_t(quarter * 32 + lane)] = __uint_as_float(r[j]);
+        for (int j = 0; j < 16; ++j) {
+          if (parts > 1)
+            sums[uint32_t(c + j) * kNarrowPitch + uint32_t(quarter * 32 + lane)] = __uint_as_float(r[j]);
+          else if (c + j < rows && n_at < p.n)
+            put(out + int64_t(c + j) * p.n, __uint_as_float(r[j]) * factor);
+        }
       }
     }
   }
@@ -629,30 +668,48 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
       mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
     }
     if (threadIdx.x == 0)
-      for (uint32_t j = n_issued > uint32_t(kNarrowStages) ? n_issued - uint32_t(kNarrowStages) : 0u; j < n_issued; ++j)
-        mbar_wait_drain(full_bar(int(j % uint32_t(kNarrowStages))), (j / uint32_t(kNarrowStages)) & 1u, p.timeout_ns);
+      for (uint32_t j = n_issued > uint32_t(kStages) ? n_issued - uint32_t(kStages) : 0u; j < n_issued; ++j)
+        mbar_wait_drain(full_bar(int(j % uint32_t(kStages))), (j / uint32_t(kStages)) & 1u, p.timeout_ns);
     __syncthreads();
   }
-  ptx::cluster_sync();   // every part's sums are in place
-  const float factor = scale_of(p.amax_a) * scale_of(p.amax_b);
-  const uint32_t sums_addr = ptx::smem_addr(sums);
-  const int64_t row0 = int64_t(tm) * NT, col0 = int64_t(tn) * 128;
-  O* out = static_cast<O*>(p.out);
-  // this CTA's share of the tile's rows, parts added in rank order
-  for (uint32_t i = threadIdx.x + rank * (NT * 128u / parts); i < (rank + 1) * (NT * 128u / parts); i += kNarrowThreads) {
-    const uint32_t j = i >> 7, l = i & 127u;
-    if (row0 + j < p.m && col0 + l < p.n) {
-      float v = 0.0f;
-      for (uint32_t s = 0; s < parts; ++s)
-        v += ptx::ld_shared_cluster_f32(ptx::mapa_shared(sums_addr + 4u * (j * kNarrowPitch + l), s));
-      v *= factor;
-      if constexpr (sizeof(O) == 2)
-        out[(row0 + j) * p.n + col0 + l] = float_to_bf16_bits(v);
-      else
-        out[(row0 + j) * p.n + col0 + l] = v;
+  if (parts > 1) {
+    ptx::cluster_sync();   // every part's sums are in place
+    const uint32_t sums_addr = ptx::smem_addr(sums);
+    const int64_t row0 = int64_t(tm) * NT, col0 = int64_t(tn) * 128;
+    const bool vec = (p.n & 3) == 0;
+    // this CTA's share of the tile, four columns a thread, parts added in rank order
+    const uint32_t rows = uint32_t(min(int64_t(NT), p.m - row0)), share = (rows * 32u + parts - 1u) / parts;
+    const uint32_t end = min(rows * 32u, (rank + 1u) * share);
+    for (uint32_t i = rank * share + threadIdx.x; i < end; i += kNarrowThreads) {
+      const uint32_t j = i >> 5, l = 4u * (i & 31u);
+      float4 v[8];
+#pragma unroll
+      for (uint32_t s = 0; s < 8; ++s)
+        if (s < parts) v[s] = ptx::ld_shared_cluster_v4(ptx::mapa_shared(sums_addr + 4u * (j * kNarrowPitch + l), s));
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (uint32_t s = 0; s < 8; ++s)
+        if (s < parts) {
+          t.x += v[s].x;
+          t.y += v[s].y;
+          t.z += v[s].z;
+          t.w += v[s].w;
+        }
+      O* o = static_cast<O*>(p.out) + (row0 + j) * p.n + col0 + l;
+      const float f[4] = {t.x * factor, t.y * factor, t.z * factor, t.w * factor};
+      if (vec && col0 + l + 4 <= p.n) {
+        if constexpr (sizeof(O) == 2)
+          *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+        else
+          *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (col0 + l + q < p.n) put(o + q, f[q]);
+      }
     }
+    ptx::cluster_sync();   // the peers have read this CTA's sums
   }
-  ptx::cluster_sync();   // the peers have read this CTA's sums
   ptx::tc_fence_after();
   if (warp == 1) ptx::tmem_dealloc_one(tmem, kNarrowCols<NT>);
 }
@@ -707,8 +764,11 @@ cudaError_t narrow_as(ProductParams& p, int sms, cudaStream_t stream) {
   p.tiles_m = int32_t((p.m + NT - 1) / NT);
   p.tiles_n = int32_t((p.n + 127) / 128);
   const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
+  // K in as many parts as leave all clusters resident (two CTAs an SM; clusters of 4 and 8 do not
+  // fill the GPU's parts evenly: 72 of 76 and 30 of 38 fit on 152 SMs) and two stages for each CTA
+  const int64_t most[4] = {0, sms, int64_t(sms) * 45 / 100, int64_t(sms) * 18 / 100};
   unsigned parts = 1;
-  while (parts < 8 && tiles * parts * 2 <= 2 * sms && p.stages >= int32_t(parts) * 4) parts *= 2;
+  for (int i = 1; i < 4 && tiles <= most[i] && p.stages >= (2 << i); ++i) parts = 1u << i;
   auto kern = fp4_narrow_kernel<MX, NT, O>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kNarrowSmem<MX, NT>);
   if (e != cudaSuccess) return e;
@@ -721,7 +781,10 @@ cudaError_t product_as(ProductParams& p, const Fp4In& a, const Fp4In& b, int sms
   if (!enc) return cudaErrorNotSupported;
   const int64_t pairs = sms / 2;
   const int64_t pair_tiles = ((p.m + 255) / 256) * ((p.n + 255) / 256);
-  const bool narrow = p.m <= 128 || pair_tiles * 2 < pairs;
+  // Few rows of A, or a long K and fewer tiles than half of the pairs: splitting K beats wider tiles
+  // (1 x 4096 x 14336: 12 against 26 us, 128 x 4096 x 14336: 17 against 26; 1024 x 1024 x 1024, not
+  // split: 11 against 8).
+  const bool narrow = p.m <= 64 || (pair_tiles * 2 < pairs && p.stages >= 24);
   const uint32_t nt = !narrow ? 128 : p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : 128;
   if (!encode_codes(enc, &p.a, a, nt) || !encode_codes(enc, &p.b, b, 128) ||
       !encode_scales(enc, &p.sa, a, kSfTiles<MX>) || !encode_scales(enc, &p.sb, b, kSfTiles<MX>))

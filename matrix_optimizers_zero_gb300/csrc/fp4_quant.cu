@@ -66,25 +66,28 @@ __device__ __forceinline__ float quotient(float x, float s, float y) {
   return fmaf(fmaf(-q, s, x), y, q);
 }
 
-// Eight codes rounded up with the probability of the remainder: |y| <= 6 in
-// fixed point, 17 bits after the point, plus the 16-bit number times the
-// grid's step (1/2 below 2, 1 below 4, 2 above), cut off to the grid. All in
-// floats, whose units are those of [64, 128): 2^-17. Exact: every sum has at
-// most 20 bits. y = v down, where its rounding towards zero is part of the
-// fixed point (down a power of two).
-__device__ __forceinline__ uint32_t stochastic_e2m1x8(const float (&v)[8], const float (&sign)[8], float down, const uint4& g) {
-  uint32_t r = 0;
+// Byte 3 of four words.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+// Eight codes rounded up with the probability of the remainder in steps of
+// 2^-16, |y| <= 6, signs from `sign`. In units of 2^-126 the numbers below 1 are
+// subnormal, and the float's bits are the position on the grid (0, 0.5, 1,
+// 1.5, 2, 3, 4, 6) in units of 2^22: the exponent's two low bits and the first
+// mantissa bit are the code, linear in between. So the 16-bit number is added
+// right below the code and the sum cut off: floor(position 2^16) + u, exactly.
+__device__ __forceinline__ uint32_t stochastic_e2m1x8(const float (&y)[8], const float (&sign)[8], const uint4& g) {
+  uint32_t t[8], s[8];
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float y = __fmaf_rz(fabsf(v[i]), down, 64.0f) - 64.0f;
+  for (int i = 0; i < 8; ++i) {
     const uint32_t w = i < 4 ? (i < 2 ? g.x : g.y) : (i < 6 ? g.z : g.w);
-    const float u = __uint_as_float(__byte_perm(w, 0x4280u, (i & 1) ? 0x5432 : 0x5410)) - 64.0f;     // u 2^-17
-    const float step2 = fmaxf(__uint_as_float(__float_as_uint(y) & 0x7F800000u), 1.0f);              // twice the step
-    // in units of 2^-126 the grid's numbers are those of the float's two exponent bits and first mantissa bit
-    const float t = __fmul_rz(fmaf(u, step2, y), __uint_as_float(1u << 23));
-    r = r * 16u + ((__float_as_uint(t) >> 22) | ((__float_as_uint(sign[i]) >> 28) & 8u));
+    const uint32_t u = __byte_perm(w, 0u, (i & 1) ? 0x4324 : 0x4104);   // u 2^8
+    t[i] = __float_as_uint(__fmul_rz(fabsf(y[i]), __uint_as_float(1u << 23))) * 4u + u;   // the code in byte 3
+    s[i] = __float_as_uint(sign[i]);
   }
-  return r;
+  return top_bytes(t[0], t[2], t[4], t[6]) + top_bytes(t[1], t[3], t[5], t[7]) * 16u +
+         (((top_bytes(s[0], s[2], s[4], s[6]) >> 4) & 0x08080808u) | (top_bytes(s[1], s[3], s[5], s[7]) & 0x80808080u));
 }
 
 // Quantises 32 consecutive elements (one block of mx, two of nv): codes in four
@@ -147,13 +150,10 @@ __device__ __forceinline__ uint32_t quantize32(float (&v)[32], int gexp, const P
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[i] = y[i] = v[b * kBlock + 8 * w + i];
-        if (!MX)
-          y[i] = quotient(y[i], s, inv);
-        else if (!STOCH)
-          y[i] *= down;
+        y[i] = MX ? y[i] * down : quotient(y[i], s, inv);
       }
       const int k = b * (kBlock / 8) + w;
-      codes[k] = STOCH ? stochastic_e2m1x8(y, x, MX ? down : 1.0f, rng.group((i0 >> 3) + uint64_t(k))) : ptx::cvt_e2m1x8(y);
+      codes[k] = STOCH ? stochastic_e2m1x8(y, x, rng.group((i0 >> 3) + uint64_t(k))) : ptx::cvt_e2m1x8(y);
     }
   }
   return bits;
@@ -301,8 +301,9 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const Fp4In q, O* o
   const uint8_t* scales = q.scales + int64_t(row >> 7) * q.tiles_k * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
   O* o_row = out + int64_t(row) * k;
   const float g = MX ? 1.0f : pow2(tensor_exponent(q.amax));
-  uint2 w[kDequantU];
-  uint32_t sc[kDequantU];
+  __shared__ O turns[8][32 * (sizeof(O) == 2 ? 18 : 17)];
+  uint2 w[kDequantU] = {};
+  uint32_t sc[kDequantU] = {};
 #pragma unroll
   for (int u = 0; u < kDequantU; ++u) {
     const int at = g0 + 32 * u;
@@ -315,7 +316,8 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const Fp4In q, O* o
 #pragma unroll
   for (int u = 0; u < kDequantU; ++u) {
     const int k0 = 16 * (g0 + 32 * u);
-    if (k0 >= k) break;
+    if (16 * (int(blockIdx.y) * (32 * kDequantU) + 32 * u) >= k) break;   // the whole warp
+    if (vec && k0 >= k) break;
     const float s = sc[u] == (MX ? 0xFFu : 0x7Fu) ? __uint_as_float(0x7FC00000u) : MX ? pow2(int(sc[u]) - 127) : e4m3_value(sc[u]) * g;
     float v[16];
 #pragma unroll
@@ -341,15 +343,19 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(const Fp4In q, O* o
           ptx::st_global_v8(o + 8 * h, r);
         }
       }
-    } else {
+    } else {   // rows that start anywhere: the warp's 512 elements in order, a whole warp a store
+      O* turn = turns[threadIdx.y];
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (k0 + j < k) {
-          if constexpr (sizeof(O) == 2)
-            o[j] = float_to_bf16_bits(v[j]);
-          else
-            o[j] = v[j];
-        }
+      for (int j = 0; j < 16; ++j) {
+        if constexpr (sizeof(O) == 2)
+          turn[threadIdx.x * 18 + j] = float_to_bf16_bits(v[j]);
+        else
+          turn[threadIdx.x * 17 + j] = v[j];
+      }
+      __syncwarp();
+      const int first = 16 * (g0 - int(threadIdx.x) + 32 * u), count = min(512, k - first);
+      for (int j = int(threadIdx.x); j < count; j += 32) o_row[first + j] = turn[(j >> 4) * (sizeof(O) == 2 ? 18 : 17) + (j & 15)];
     }
   }
 }
