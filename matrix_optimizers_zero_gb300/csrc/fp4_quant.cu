@@ -180,7 +180,7 @@ __device__ __forceinline__ void put32(const Fp4Out& q, int64_t row, int64_t k0, 
 }
 
 template <typename T, bool MX, bool STOCH>
-__global__ void __launch_bounds__(kThreads, 6) fp4_quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, 8) fp4_quantize_kernel(const QuantParams p) {
   extern __shared__ __align__(16) uint8_t tile_smem[];
   T* tile = reinterpret_cast<T*>(tile_smem);
   constexpr int P = kPitch<T>;
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 6) fp4_quantize_kernel(const QuantPa
 template <typename T>
 __global__ void __launch_bounds__(256) fp4_amax_kernel(const T* x, int64_t n, uint32_t* amax) {
   constexpr int E = 16 / int(sizeof(T));
-  constexpr int U = 4;
+  constexpr int U = 8;
   ptx::griddep_launch_dependents();
   uint32_t top = 0;
   auto take = [&](float v) {
