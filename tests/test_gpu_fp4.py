@@ -289,3 +289,92 @@ def test_input_gradient_against_differences():
     want = step.double() @ values.double().T      # <step, dx> for dy = each unit vector
     mag = (x.abs() + step.abs()).double() @ values.double().abs().T
     assert bool(((y2.double() - y.double() - want).abs() <= 2 * k * 2.0 ** -23 * mag).all())
+
+
+# ---------------------------------------------------------------- past 32 bits, graphs
+
+def test_quantize_past_32_bit_elements():
+    rows, cols = 2 ** 20 + 3, 4160              # 4.4 G elements
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device=dev())
+    spots = torch.tensor([0, 2 ** 19 + 1, 2 ** 20 - 200, rows - 1], device=dev())
+    x[spots] = data(len(spots), cols, torch.bfloat16, 1)
+    row, col = mo.Fp4Tensor(rows, cols, "mx"), mo.Fp4Tensor(cols, rows, "mx")
+    mo.fp4_quantize(x, row, col)
+    _, _, values = ot.fp4_quantize(f64(x[spots]), "mx")
+    del x
+    out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev())
+    mo.fp4_dequantize(row, out)
+    assert np.array_equal(f64(out[spots]), values)
+    out[spots] = 0
+    assert not any(bool(part.any()) for part in out.split(2 ** 16))
+
+
+@pytest.mark.parametrize("n", [40000, 39999])
+def test_product_past_32_bit_outputs(n):
+    m, k = 120000, 64                            # 4.8 G outputs
+    a, b = mo.Fp4Tensor(m, k, "mx"), mo.Fp4Tensor(n, k, "mx")
+    mo.fp4_quantize(data(m, k, torch.bfloat16, 1), a)
+    mo.fp4_quantize(data(n, k, torch.bfloat16, 2), b)
+    va, vb = torch.empty((m, k), device=dev()), torch.empty((n, k), device=dev())
+    mo.fp4_dequantize(a, va)
+    mo.fp4_dequantize(b, vb)
+    out = torch.empty((m, n), dtype=torch.bfloat16, device=dev())
+    mo.fp4_product(a, b, out)
+    assert mo.mo_last_device_error() == 0
+    for r0 in (0, 53500, 53687, 107374, m - 300):   # around 2^31 and 2^32 outputs
+        part = slice(r0, r0 + 300)
+        check_product((a, b), (va[part].double(), vb.double()), out[part])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_linear_captured_in_a_graph(fmt):
+    t, r, c = 300, 5120, 288
+    x, w = data(t, c, torch.bfloat16, 1), data(r, c, torch.float32, 2)
+    xq, xt, wq = mo.Fp4Tensor(t, c, fmt), mo.Fp4Tensor(c, t, fmt), mo.Fp4Tensor(r, c, fmt)
+    y, off = torch.empty((t, r), device=dev()), torch.zeros(1, dtype=torch.int64, device=dev())
+
+    def step():
+        mo.fp4_quantize(w, wq)
+        mo.fp4_quantize(x, xq, xt, stochastic=mo.Random(3, 4, off))
+        mo.fp4_product(xq, wq, y)
+        off.add_(2)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    x.copy_(data(t, c, torch.bfloat16, 7))
+    off.fill_(40)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = y.clone(), xt.codes.clone()
+    off.fill_(42)
+    step()
+    assert torch.equal(y, got[0]) and torch.equal(xt.codes, got[1])
+
+
+@pytest.mark.parametrize("m,n,k", [(33, 131, 100), (300, 5113, 96)])
+def test_nothing_outside_the_outputs_is_written(m, n, k):
+    guard = 4096
+    def guarded(count, dtype, value):
+        whole = torch.full((count + 2 * guard,), value, dtype=dtype, device=dev())
+        return whole, whole[guard:guard + count], value
+    x, w = data(m, k, torch.float32, 1), data(n, k, torch.float32, 2)
+    sizes = [(m, k), (k, m), (n, k)]
+    keep, q = [], []
+    for r, kk in sizes:
+        c = guarded(mo.mo_fp4_codes_bytes(r, kk), torch.uint8, 0x5C)
+        s = guarded(mo.mo_fp4_scales_bytes(r, kk, "nv"), torch.uint8, 0x5C)
+        keep += [c, s]
+        q.append(mo.Fp4Tensor(r, kk, "nv", codes=c[1], scales=s[1]))
+    mo.fp4_quantize(x, q[0], q[1])
+    mo.fp4_quantize(w, q[2])
+    for dtype in (torch.float32, torch.bfloat16):
+        y = guarded(m * n, dtype, 77.0)
+        v = guarded(k * m, dtype, 77.0)
+        keep += [y, v]
+        mo.fp4_product(q[0], q[2], y[1].view(m, n))
+        mo.fp4_dequantize(q[1], v[1].view(k, m))
+    for whole, part, value in keep:
+        assert bool((whole[:guard] == value).all()) and bool((whole[guard + part.numel():] == value).all())

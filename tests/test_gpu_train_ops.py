@@ -302,3 +302,80 @@ def test_grad_on_a_side_stream():
         got = run_grad(dout, tokens, vocab)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- past 32 bits, graphs
+
+def test_dropout_past_32_bit_elements():
+    n = 2 ** 32 + 4099
+    x = torch.ones(n, dtype=torch.bfloat16, device=dev())
+    mo.dropout_apply(x, x, mo.Dropout(0.5, seed=17, offset=3))
+    for first in (0, 2 ** 31 - 16, 2 ** 32 - 8, n - 4000):
+        part = x[first:first + 4000].float().cpu().numpy()
+        u = ot.random16(len(part), 17, 3, first)
+        assert np.array_equal(part != 0, u >= 32768)
+
+
+def test_lookup_and_grad_past_32_bit_offsets():
+    vocab, dim = 2 ** 20 + 77, 4096            # 4.3 G elements
+    table = torch.zeros((vocab, dim), dtype=torch.bfloat16, device=dev())
+    rows = torch.tensor([0, 2 ** 19 - 1, 2 ** 19, 2 ** 20 - 1, 2 ** 20, vocab - 1], device=dev())
+    table[rows] = randn((len(rows), dim), torch.bfloat16, 1)
+    out = torch.empty((len(rows), dim), dtype=torch.bfloat16, device=dev())
+    mo.embed_lookup(table, rows, out)
+    assert torch.equal(out, table[rows])
+    del table
+    tokens = rows.repeat(40)
+    dout = randn((len(tokens), dim), torch.float32, 2)
+    grad = run_grad(dout, tokens, vocab)       # 17 GB
+    want = dout.double().reshape(40, len(rows), dim).sum(0)
+    mag = dout.double().abs().reshape(40, len(rows), dim).sum(0)
+    assert bool(((grad[rows].double() - want).abs() <= 43 * U * mag).all())
+    grad[rows] = 0
+    assert not any(bool(part.any()) for part in grad.split(2 ** 18))
+
+
+def test_lookup_and_grad_captured_in_a_graph():
+    n, vocab, dim = 3000, 700, 264
+    table, dout = randn((vocab, dim), torch.float32, 1), randn((n, dim), torch.bfloat16, 2)
+    tokens = make_tokens(n, vocab, "hot", 3)
+    out, grad = torch.empty((n, dim), device=dev()), torch.empty((vocab, dim), device=dev())
+    ws = mo.embed_grad_workspace(n, vocab, dim)
+    d = mo.Dropout(0.2, seed=5)
+
+    def step():
+        mo.embed_lookup(table, tokens, out, dropout=d)
+        mo.embed_grad(dout, tokens, grad, ws, dropout=d)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    tokens.copy_(make_tokens(n, vocab, "uniform", 9))
+    graph.replay()
+    torch.cuda.synchronize()
+    got_out, got_grad = out.clone(), grad.clone()
+    step()
+    assert torch.equal(out, got_out) and torch.equal(grad, got_grad)
+
+
+@pytest.mark.parametrize("dim", [24, 25])
+def test_nothing_outside_the_outputs_is_written(dim):
+    n, vocab, guard = 1500, 333, 4096
+    def guarded(count, dtype):
+        t = torch.full((count + 2 * guard,), 77.0, dtype=dtype, device=dev())
+        return t, t[guard:guard + count]
+    dout, table = randn((n, dim), torch.float32, 1), randn((vocab, dim), torch.float32, 2)
+    tokens = make_tokens(n, vocab, "hot", 3)
+    whole_g, grad = guarded(vocab * dim, torch.float32)
+    whole_o, out = guarded(n * dim, torch.bfloat16)
+    whole_y, y = guarded(n * dim, torch.float32)
+    ws_bytes = mo.mo_embed_grad_workspace_bytes(n, vocab, dim)
+    whole_w = torch.full((ws_bytes + 2 * guard,), 0x5C, dtype=torch.uint8, device=dev())
+    drop = mo.Dropout(0.3, seed=1)
+    mo.embed_grad(dout, tokens, grad.view(vocab, dim), whole_w[guard:guard + ws_bytes], dropout=drop)
+    mo.embed_lookup(table, tokens, out.view(n, dim), dropout=drop)
+    mo.dropout_apply(dout.view(-1), y, drop)
+    for whole, count in ((whole_g, vocab * dim), (whole_o, n * dim), (whole_y, n * dim)):
+        assert bool((whole[:guard] == 77).all()) and bool((whole[guard + count:] == 77).all())
+    assert bool((whole_w[:guard] == 0x5C).all()) and bool((whole_w[guard + ws_bytes:] == 0x5C).all())
