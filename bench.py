@@ -46,10 +46,10 @@ UNIT = "TFLOP/s"
 # mo_internal.h); the profiles directory holds the capture summaries with their
 # commands.
 NS_TRAFFIC = {
-    "llama8b": {"source_sha256_16": "4e806d95c73f9fef", "bytes_per_ns_segment": 469.903e9,
+    "llama8b": {"source_sha256_16": "9cc98018ce5e65be", "bytes_per_ns_segment": 469.903e9,
                 "how": "ncu dram__bytes_read.sum + dram__bytes_write.sum (one pass) over the 15 NS launches of the "
                        "fourth step on the full table (tiles from the per-launch counter; 470-495 GB over captures)"},
-    "gpt2l": {"source_sha256_16": "4e806d95c73f9fef", "bytes_per_ns_segment": 34.910e9,
+    "gpt2l": {"source_sha256_16": "9cc98018ce5e65be", "bytes_per_ns_segment": 34.910e9,
               "how": "ncu dram__bytes_read.sum + dram__bytes_write.sum (one pass) over the 15 NS launches of the "
                      "fourth step on the full table (static tile assignment; the last launch from the counter)"},
 }
