@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ MMA issuer (even CTA)
       int stage = 0, slot = 0;
-      uint32_t ph = 0, sph = 0;
+      uint32_t sph = 0;
       bool ok = true, seen = false;   // seen: the stage is known to be complete
       const uint32_t desc_lo = ptx::desc_lo_sw128(base);
       int32_t i = 0;
@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         const uint32_t d = tmem + uint32_t(acc) * kAccStep;
         int32_t left = p.steps;
         for (int32_t kb = 0; kb < p.stages; ++kb) {
-          if (!seen && (!mbar_wait_bounded(sf_ready_bar(slot), sph, abort_flag, p.status, p.timeout_ns) ||
-                        !mbar_wait_bounded(full_bar(stage), ph, abort_flag, p.status, p.timeout_ns))) {
+          // (a stage's scales are reported only once its codes have landed too)
+          if (!seen && !mbar_wait_bounded(sf_ready_bar(slot), sph, abort_flag, p.status, p.timeout_ns)) {
             ok = false;
             break;
           }
@@ -314,10 +314,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
             slot = 0;
             sph ^= 1u;
           }
-          if (++stage == kPairStages) {
-            stage = 0;
-            ph ^= 1u;
-          }
+          if (++stage == kPairStages) stage = 0;
           // instruction kk: 32 bytes of codes, its scales
           auto issue = [&](int kk) {
             const uint32_t c = sf + 12u * uint32_t(kk / kStepsPerTile<MX>);
@@ -335,7 +332,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           left -= 4;
           ptx::umma_commit_pair(bar, 0x3);
           // the next stage is looked at while these are under way
-          seen = ptx::mbar_peek(sf_ready_bar(slot), sph) && ptx::mbar_peek(full_bar(stage), ph);
+          seen = ptx::mbar_peek(sf_ready_bar(slot), sph);
           mma_issued = true;
         }
         if (!ok) break;
@@ -412,10 +409,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive_remote_cta(ptx::mapa_shared(sf_ready_bar(int(slot)), 0));
-        ptx::mbar_arrive(sf_empty_bar(int(stage)));
+      if (lane == 0) ptx::mbar_arrive(sf_empty_bar(int(stage)));
+      // The even CTA's warps report the stage when both CTAs' codes have landed as well, so that the
+      // issuing thread has one barrier a stage to look at.
+      if (leader) {
+        ok = mbar_wait_bounded(full_bar(int(j % kPairStages)), (j / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
       }
+      if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(sf_ready_bar(int(slot)), 0));
     }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
