@@ -104,13 +104,21 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutPara
       if (RES) r[u].load(res + 8 * g);
     }
   }
+  // The numbers are drawn while the loads are on their way: the empty statement keeps the compiler
+  // from drawing them only where the loaded values are used (bf16 without a residual 52 -> 46 us).
+  uint4 rnd[kDropGroups];
+#pragma unroll
+  for (int u = 0; u < kDropGroups; ++u) {
+    rnd[u] = rng.group(uint64_t(g0 + u * kDropThreads));
+    asm volatile("" : "+r"(rnd[u].x), "+r"(rnd[u].y), "+r"(rnd[u].z), "+r"(rnd[u].w));
+  }
 #pragma unroll
   for (int u = 0; u < kDropGroups; ++u) {
     const int64_t g = g0 + u * kDropThreads;
     if (g < full) {
       float v[8];
       a[u].unpack(v);
-      if (p.drop.threshold != 0) drop8(v, rng.group(uint64_t(g)), p.drop.threshold, p.drop.factor);
+      if (p.drop.threshold != 0) drop8(v, rnd[u], p.drop.threshold, p.drop.factor);
       if (RES) {
         float w[8];
         r[u].unpack(w);
@@ -119,9 +127,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutPara
       }
       store8(y + 8 * g, v);
     } else if (g == full) {   // the last, partial group
-      const uint4 q = rng.group(uint64_t(g));
       for (int64_t i = 8 * g; i < p.n; ++i) {
-        float v = philox_half(q, int(i & 7)) >= p.drop.threshold ? to_float(x[i]) * p.drop.factor : 0.0f;
+        float v = philox_half(rnd[u], int(i & 7)) >= p.drop.threshold ? to_float(x[i]) * p.drop.factor : 0.0f;
         if (RES) v += to_float(res[i]);
         store1(y + i, v);
       }
