@@ -660,7 +660,8 @@ cudaError_t lookup_as(const LookupParams& p, int sms, cudaStream_t stream) {
     unsigned x = 32;
     while (x < 256 && x < groups) x <<= 1;
     const unsigned y = 256 / x;
-    const int64_t blocks = std::min<int64_t>((p.tokens.n + y - 1) / y, int64_t(sms) * 8);
+    // a few tokens a block: enough to load indexes ahead, and blocks that end at different times
+    const int64_t blocks = std::min<int64_t>((p.tokens.n + y - 1) / y, int64_t(sms) * 40);
     const bool add = p.add != nullptr, drop = p.drop.threshold != 0;
     auto kern = add ? (drop ? embed_lookup_kernel<T, O, true, true> : embed_lookup_kernel<T, O, true, false>)
                     : (drop ? embed_lookup_kernel<T, O, false, true> : embed_lookup_kernel<T, O, false, false>);

@@ -246,19 +246,16 @@ __global__ void __launch_bounds__(kThreads, 8) fp4_quantize_kernel(const QuantPa
 }
 
 // Largest finite magnitude of x: an unsigned maximum of the bit patterns, so
-// the order of the atomics does not matter. *amax is 0 on entry.
+// the order of the atomics does not matter. *amax is 0 on entry. A thread that
+// meets a NaN or an infinity looks at its elements once more without them.
 template <typename T>
-__global__ void __launch_bounds__(256) fp4_amax_kernel(const T* x, int64_t n, uint32_t* amax) {
+__global__ void __launch_bounds__(256, 8) fp4_amax_kernel(const T* x, int64_t n, uint32_t* amax) {
   constexpr int E = 16 / int(sizeof(T));
-  constexpr int U = 8;
+  constexpr int U = 4;
   ptx::griddep_launch_dependents();
-  uint32_t top = 0;
-  auto take = [&](float v) {
-    const uint32_t b = abs_bits(v);
-    top = max(top, b < 0x7F800000u ? b : 0u);
-  };
   const int64_t full = n / E, stride = int64_t(gridDim.x) * blockDim.x;
   const int64_t i0 = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+  float most = 0.0f;
   for (int64_t i = i0; i < full; i += U * stride) {
     uint4 w[U];
 #pragma unroll
@@ -268,12 +265,28 @@ __global__ void __launch_bounds__(256) fp4_amax_kernel(const T* x, int64_t n, ui
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const T* t = reinterpret_cast<const T*>(&w[u]);
+      const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      if constexpr (E == 8) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) take(as_float(t[j]));
+        for (int j = 0; j < 4; ++j) most = max_abs(most, __uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xFFFF0000u));
+      } else {
+        most = max_abs(most, __uint_as_float(q[0]), __uint_as_float(q[1]));
+        most = max_abs(most, __uint_as_float(q[2]), __uint_as_float(q[3]));
+      }
     }
   }
-  if (i0 < n - full * E) take(as_float(x[full * E + i0]));
+  if (i0 < n - full * E) most = max_abs(most, as_float(x[full * E + i0]), 0.0f);
+  uint32_t top = __float_as_uint(most);
+  if (top >= 0x7F800000u) {
+    top = 0;
+    auto take = [&](T v) {
+      const uint32_t b = abs_bits(as_float(v));
+      top = max(top, b < 0x7F800000u ? b : 0u);
+    };
+    for (int64_t i = i0; i < full; i += stride)
+      for (int j = 0; j < E; ++j) take(x[i * E + j]);
+    if (i0 < n - full * E) take(x[full * E + i0]);
+  }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   __shared__ uint32_t warp_top[8];
   if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
