@@ -92,7 +92,7 @@ __device__ __forceinline__ uint32_t stochastic_e2m1x8(const float (&y)[8], const
 
 // Quantises 32 consecutive elements (one block of mx, two of nv): codes in four
 // words, scale bits in the returned value (one byte a block). i0: index of the
-// first element for the random numbers.
+// first element for the random numbers, a multiple of 32.
 template <bool MX, bool STOCH>
 __device__ __forceinline__ uint32_t quantize32(float (&v)[32], int gexp, const Philox& rng, uint64_t i0,
                                                uint32_t (&codes)[4]) {
@@ -153,7 +153,7 @@ __device__ __forceinline__ uint32_t quantize32(float (&v)[32], int gexp, const P
         y[i] = MX ? y[i] * down : quotient(y[i], s, inv);
       }
       const int k = b * (kBlock / 8) + w;
-      codes[k] = STOCH ? stochastic_e2m1x8(y, x, rng.group((i0 >> 3) + uint64_t(k))) : ptx::cvt_e2m1x8(y);
+      codes[k] = STOCH ? stochastic_e2m1x8(y, x, rng.group(uint32_t(i0 >> 35), uint32_t(i0 >> 3) + uint32_t(k))) : ptx::cvt_e2m1x8(y);
     }
   }
   return bits;

@@ -46,8 +46,10 @@ struct Philox {
   }
 
   // the eight 16-bit numbers of group j, two a word
-  __device__ __forceinline__ uint4 group(uint64_t j) const {
-    uint32_t a = uint32_t(j), b = uint32_t(j >> 32), c = o0, d = o1, x = k0, y = k1;
+  __device__ __forceinline__ uint4 group(uint64_t j) const { return group(uint32_t(j >> 32), uint32_t(j)); }
+  // (calls that share the upper half share two of the twenty products)
+  __device__ __forceinline__ uint4 group(uint32_t j_hi, uint32_t j_lo) const {
+    uint32_t a = j_lo, b = j_hi, c = o0, d = o1, x = k0, y = k1;
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
       const uint64_t p = uint64_t(a) * 0xD2511F53u;
