@@ -239,10 +239,11 @@ __global__ void __launch_bounds__(256) embed_lookup_flat_kernel(const LookupPara
 // Launch 1 of the gradient. Cluster 0 (eight CTAs; one for few tokens) sorts
 // the tokens with their positions by a stable radix sort, up to 9 bits a pass
 // (two passes for vocabularies up to 2^18). The other clusters meanwhile write
-// zeros: to every row, since leaving out the rows that tokens name would need
-// to know them first, and writing the table front to back by many short-lived
-// CTAs is what reaches the memory's write rate (2.1 GB: 7.4 TB/s; row by row
-// from resident CTAs, touched rows skipped, 4.4).
+// zeros to the first rows of the table, as many as the sort takes the time for;
+// the rest are launch 2's. They write every row, since the rows that tokens
+// name are not known yet. Writing front to back by many short-lived CTAs is
+// what reaches the memory's write rate (2.1 GB: 7.4 TB/s; row by row from
+// resident CTAs 4.4).
 //
 // Every warp owns a contiguous part of the positions, so its histogram, its
 // offsets and its scatter keep the order: the sums of launch 2 have one order
@@ -255,6 +256,7 @@ constexpr int64_t kOneCtaTokens = 1024;
 constexpr int kMaxBins = 1 << kMaxDigitBits;
 constexpr size_t kSortSmem = sizeof(uint32_t) * (size_t(kSortWarps) * (kMaxBins + 1) + 2 * kMaxBins + kSortWarps);
 constexpr int64_t kZeroBytes = int64_t(kSortThreads) * 16 * 16;   // a zeroing CTA's share: 256 KB
+constexpr int kZeroMaskWords = kZeroRowsMost / 32;
 
 // The sort key of a token: itself, or `vocab` (sorted last, ignored) for the
 // padding index and for an index outside the table.
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
     sort_tokens(p, sort_smem, ptx::cluster_ctarank(), ctas);
     return;
   }
-  const int64_t floats = p.vocab * p.dim, begin = int64_t(blockIdx.x - ctas) * (kZeroBytes / 4);
+  const int64_t floats = p.zero_first * p.dim, begin = int64_t(blockIdx.x - ctas) * (kZeroBytes / 4);
   float* g = p.grad + begin;
   const int64_t mine = min(floats - begin, kZeroBytes / 4);
 #pragma unroll 4
@@ -531,6 +533,57 @@ __device__ void join(const GradParams& p, uint32_t token, int64_t chunk, int64_t
   }
 }
 
+// First index in [0, n) of the sorted keys whose key is at least k, n if none:
+// each step of the warp cuts the range by 32.
+__device__ int64_t lower_bound_warp(const uint32_t* key, int64_t n, uint32_t k) {
+  const int lane = int(threadIdx.x & 31);
+  int64_t lo = 0, hi = n;
+  while (hi > lo) {
+    const int64_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const int ones = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && __ldcg(key + at) < k));   // a run from lane 0
+    if (ones == 0) return lo;
+    hi = min(hi, lo + int64_t(ones) * step);
+    lo += int64_t(ones - 1) * step + 1;
+  }
+  return lo;
+}
+
+// Zeroes the rows of [r0, r1) that no token names (launch 2's share of the
+// zeros, written while the sums wait for their rows).
+__device__ void zero_untouched(const GradParams& p, const uint32_t* key, int64_t r0, int64_t r1, uint32_t* mask) {
+  __shared__ int64_t bound[2];
+  if (threadIdx.x < 32) {
+    const int64_t lo = lower_bound_warp(key, p.tokens.n, uint32_t(r0)), hi = lower_bound_warp(key, p.tokens.n, uint32_t(r1));
+    if (threadIdx.x == 0) {
+      bound[0] = lo;
+      bound[1] = hi;
+    }
+  }
+  const int rows = int(r1 - r0);
+  for (int i = int(threadIdx.x); i < (rows + 31) / 32; i += int(blockDim.x)) mask[i] = 0u;
+  __syncthreads();
+  for (int64_t i = bound[0] + threadIdx.x; i < bound[1]; i += blockDim.x) {
+    const uint32_t r = __ldcg(key + i) - uint32_t(r0);
+    atomicOr(mask + (r >> 5), 1u << (r & 31u));
+  }
+  __syncthreads();
+  float* g = p.grad + r0 * p.dim;
+  if ((p.dim & 3) == 0) {
+    const uint32_t per = uint32_t(p.dim >> 2), total = uint32_t(rows) * per;
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < total; i += blockDim.x) {
+      const uint32_t r = i / per;
+      if (!((mask[r >> 5] >> (r & 31u)) & 1u)) reinterpret_cast<float4*>(g)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  } else {
+    const uint32_t per = uint32_t(p.dim), total = uint32_t(rows) * per;
+    for (uint32_t i = threadIdx.x; i < total; i += blockDim.x) {
+      const uint32_t r = i / per;
+      if (!((mask[r >> 5] >> (r & 31u)) & 1u)) g[i] = 0.0f;
+    }
+  }
+}
+
 template <typename T, int V, bool DROP>
 __global__ void __launch_bounds__(256, 4) embed_sum_kernel(const __grid_constant__ GradParams p) {
   __shared__ uint32_t s_key[kMaxChunk + 2];   // the chunk's keys between its neighbours'
@@ -542,7 +595,12 @@ __global__ void __launch_bounds__(256, 4) embed_sum_kernel(const __grid_constant
   const int64_t n = p.tokens.n;
   const int64_t chunk = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
   const int64_t s = chunk * p.chunk, e = min(n, s + p.chunk);
-  if (s >= n) return;
+  if (chunk >= p.chunks) {   // the blocks after the sums'
+    __shared__ uint32_t mask[kZeroMaskWords];
+    const int64_t r0 = p.zero_first + ((chunk - p.chunks) * gridDim.x + blockIdx.x) * p.zero_rows;
+    if (r0 < p.vocab) zero_untouched(p, key, r0, min(p.vocab, r0 + p.zero_rows), mask);
+    return;
+  }
   const uint32_t none = uint32_t(p.vocab);
   for (int i = int(threadIdx.x); i < int(e - s) + 2; i += int(blockDim.x)) {
     const int64_t at = s - 1 + i;
@@ -676,10 +734,11 @@ cudaError_t lookup_as(const LookupParams& p, int sms, cudaStream_t stream) {
 template <typename T, int V>
 cudaError_t sum_as(const GradParams& p, cudaStream_t stream) {
   const GradGrid g = grad_grid(p.tokens.n, p.dim);
-  const int64_t y = g.chunks < 32768 ? g.chunks : 32768;
+  const int64_t zeros = p.accumulate ? 0 : (p.vocab - p.zero_first + p.zero_rows - 1) / p.zero_rows;
+  const int64_t all = g.chunks + (zeros + g.col_blocks - 1) / g.col_blocks, y = all < 32768 ? all : 32768;
   // the launch overlaps the sort's end
   return launch_kernel(p.drop.threshold != 0 ? embed_sum_kernel<T, V, true> : embed_sum_kernel<T, V, false>,
-                       dim3(unsigned(g.col_blocks), unsigned(y), unsigned((g.chunks + y - 1) / y)), dim3(unsigned(g.threads)), 0, 1,
+                       dim3(unsigned(g.col_blocks), unsigned(y), unsigned((all + y - 1) / y)), dim3(unsigned(g.threads)), 0, 1,
                        true, stream, p);
 }
 
@@ -700,7 +759,7 @@ cudaError_t launch_embed_grad(const GradParams& p, bool dout_bf16, cudaStream_t 
   if (e != cudaSuccess) return e;
   // few tokens sort faster without the cluster's barriers
   const int64_t ctas = p.tokens.n <= kOneCtaTokens ? 1 : 8;
-  const int64_t zeros = p.accumulate ? 0 : (p.vocab * p.dim * 4 + kZeroBytes - 1) / kZeroBytes;
+  const int64_t zeros = p.accumulate ? 0 : (p.zero_first * p.dim * 4 + kZeroBytes - 1) / kZeroBytes;
   const size_t bins = size_t(1) << p.digit_bits;
   const size_t smem = sizeof(uint32_t) * (size_t(kSortWarps) * (bins + 1) + 2 * bins + kSortWarps);
   e = launch_kernel(embed_sort_kernel, dim3(unsigned(ctas + (zeros + ctas - 1) / ctas * ctas)), dim3(kSortThreads), smem,

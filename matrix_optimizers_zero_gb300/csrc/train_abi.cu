@@ -244,7 +244,14 @@ int embed_grad(const void* dout, int32_t dout_dtype, const mo_tokens* tokens, in
   p.partial = reinterpret_cast<float*>(w + L.partial);
   p.counters = L.counters;
   p.dim_pad = L.dim_pad;
-  p.chunk = mo::grad_grid(n, dim).chunk;
+  const mo::GradGrid grid = mo::grad_grid(n, dim);
+  p.chunk = grid.chunk;
+  p.chunks = grid.chunks;
+  // launch 1 writes zeros for about as long as its sort takes (at 7 TB/s: 9 us, and 0.34 ns a token);
+  // launch 2 in blocks of 128 KB, or of 256 KB where there are thousands (2.1 GB: 327 -> 317 us)
+  p.zero_first = std::min(vocab, ((int64_t(60) << 20) + 2304 * n) / (4 * dim) + 1);
+  const int64_t block = int64_t(grad_bytes) > (int64_t(1) << 30) ? int64_t(256) << 10 : int64_t(128) << 10;
+  p.zero_rows = std::max(int64_t(1), std::min(mo::kZeroRowsMost, block / (4 * dim)));
   p.dout = dout;
   p.grad = grad;
   p.vocab = vocab;

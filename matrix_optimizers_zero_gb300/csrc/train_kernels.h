@@ -51,6 +51,7 @@ cudaError_t launch_embed_lookup(const LookupParams& p, bool table_bf16, bool out
 // kMaxDigitBits, then the fewest bits.
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxChunk = 64;
+constexpr int64_t kZeroRowsMost = 4096;   // rows a block of launch 2 zeroes, at most
 
 // Launch shape of the gradient's sums: chunks of sorted positions by blocks of
 // columns (eight a thread, or one where dim is not a multiple of 8). A chunk
@@ -80,7 +81,9 @@ struct GradParams {
   uint32_t* counter;      // arrivals of the join: two per slot and column block
   float* partial;         // [2 chunks, dim_pad] sums of tokens that cross chunks
   int64_t counters;
-  int64_t vocab, dim, dim_pad, chunk;
+  int64_t vocab, dim, dim_pad, chunk, chunks;
+  int64_t zero_first;     // rows that launch 1 zeroes; launch 2 zeroes those of the others that no token names,
+  int64_t zero_rows;      // so many a block
   TokenArgs tokens;
   DropArgs drop;
   float factor;           // scale times the dropout's factor

@@ -274,6 +274,20 @@ def test_grad_wide_vocabulary_takes_three_passes():
     assert not grad[untouched].any()
 
 
+@pytest.mark.parametrize("n,vocab,dim", [(3000, 70001, 401), (20000, 300007, 96), (5, 2 ** 25 + 3, 1), (9000, 2 ** 23 + 1, 5),
+                                         (700, 40000, 1024)])
+def test_grad_tables_whose_zeros_both_launches_write(n, vocab, dim):
+    dout = randn((n, dim), torch.float32, 1)
+    tokens = make_tokens(n, vocab, "uniform", 5)
+    tokens[::3] = vocab - 1 - tokens[::3] % 50          # touched rows beside each other at the end
+    tokens[:4] = torch.tensor([0, vocab - 1, vocab // 2, 1], device=dev())
+    grad = run_grad(dout, tokens, vocab)
+    rows, remap = torch.unique(tokens, return_inverse=True)
+    check_grad(grad[rows], dout, remap, len(rows), 1.0, -1, None, None)
+    grad[rows] = 0
+    assert not grad.any()
+
+
 def test_grad_against_differences_of_the_lookup():
     # the lookup is linear in its table: <lookup(E + D) - lookup(E), dout> = <grad, D>
     n, vocab, dim = 400, 60, 48
