@@ -83,7 +83,10 @@ __device__ __forceinline__ int64_t token_at(const TokenArgs& t, int64_t i) {
 
 // ------------------------------------------------------------------ dropout
 // A thread takes kDropGroups groups of eight elements, kDropThreads groups
-// apart, and issues all their loads before the first use.
+// apart, and issues all their loads before the first use. Bound by memory
+// with a residual (16384 x 4096 bf16: 59 us, 6.8 TB/s), nearly so without
+// (44 us, 6.2 TB/s): the random numbers' 20 wide products a group take about
+// 18 us of the SMs' time there.
 constexpr int kDropThreads = 256;
 constexpr int kDropGroups = 4;
 
@@ -140,6 +143,10 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutPara
 // dim % 8 == 0: blockDim.x threads cover a row in groups of eight columns,
 // blockDim.y tokens at a time; the next token's index is loaded before this
 // one's row is used, so the row's address is known when its turn comes.
+// 16384 tokens of 128256 x 4096 fp32, to bf16: 63 us with distinct rows (402
+// MB, 6.4 TB/s), 46 us with the frequencies of text (254 MB), 58 us with
+// dropout, then bound by the random numbers' arithmetic. (The next row's loads
+// a step ahead in registers: 70 us, for the occupancy they cost.)
 template <typename T, typename O, bool ADD, bool DROP>
 __global__ void __launch_bounds__(256, ADD ? 4 : 5) embed_lookup_kernel(const LookupParams p) {
   const Philox rng(p.drop.rnd);
@@ -244,6 +251,9 @@ __global__ void __launch_bounds__(256) embed_lookup_flat_kernel(const LookupPara
 // name are not known yet. Writing front to back by many short-lived CTAs is
 // what reaches the memory's write rate (2.1 GB: 7.4 TB/s; row by row from
 // resident CTAs 4.4).
+//
+// The sort is bound by latencies: 14 us for 8192 tokens in two passes, 10 us for
+// 1024 on one CTA.
 //
 // Every warp owns a contiguous part of the positions, so its histogram, its
 // offsets and its scatter keep the order: the sums of launch 2 have one order
@@ -402,7 +412,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
 // before chunk c, 2 c + 1 for one that begins in it and goes on) and are
 // joined, in chunk order, by whichever block arrives last: first within
 // aligned groups of kJoin chunks, then over the groups, so that a token that
-// fills the batch is not summed by one block alone.
+// fills the batch is not summed by one block alone. With the zeros beside them
+// the sums are bound by memory at 8B size (both launches: 316 us for 2.24 GB,
+// 7.1 TB/s); alone they take 14 us for 8192 x 1280, most of it the chain of
+// loading positions, rows and partial sums.
 constexpr int kJoin = 32;
 
 // First and last chunk of a token that crosses chunks. A chunk after this one

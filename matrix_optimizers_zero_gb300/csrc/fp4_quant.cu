@@ -21,7 +21,11 @@ namespace {
 
 // A 64 x 64 tile of x goes through shared memory, from which both
 // orientations are quantised: x is read once for the operands of a forward and
-// a backward product. Row pitch in elements: 16 bytes more than the row, so
+// a backward product. (128 x 128 tiles, 256 threads: a tenth slower, as their
+// last ones leave SMs idle.) 14336 x 4096 fp32 to mx, both orientations: 51 us for
+// 297 MB, 5.8 TB/s. Others are bound by arithmetic, 8192 x 5120 bf16: mx 32 us,
+// nv 41 us (quotients and a scale search for every 16 elements), stochastic 62
+// and 81 us (the random numbers: 20 wide products for 8 elements). Row pitch in elements: 16 bytes more than the row, so
 // that 32 threads reading 16 bytes of 32 rows meet all banks.
 constexpr int kTile = kQuantTile;
 constexpr int kThreads = 128;
@@ -248,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 8) fp4_quantize_kernel(const QuantPa
 // Largest finite magnitude of x: an unsigned maximum of the bit patterns, so
 // the order of the atomics does not matter. *amax is 0 on entry. A thread that
 // meets a NaN or an infinity looks at its elements once more without them.
+// 8192 x 5120 bf16: 16 us, 5.2 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(256, 8) fp4_amax_kernel(const T* x, int64_t n, uint32_t* amax) {
   constexpr int E = 16 / int(sizeof(T));
@@ -300,7 +305,8 @@ __global__ void __launch_bounds__(256, 8) fp4_amax_kernel(const T* x, int64_t n,
 
 // Values of a quantised tensor: a thread takes kDequantU groups of 16
 // consecutive elements of a row (8 bytes of codes, one scale), 32 groups
-// apart; 32 lanes by 8 rows a block, blocks down the rows first.
+// apart; 32 lanes by 8 rows a block, blocks down the rows first. Bound by
+// memory: 14336 x 4096 to bf16 22 us for 148 MB, 6.7 TB/s.
 constexpr int kDequantU = 2;
 
 template <typename O, bool MX>
