@@ -575,9 +575,24 @@ __device__ void zero_untouched(const GradParams& p, const uint32_t* key, int64_t
   const int rows = int(r1 - r0);
   for (int i = int(threadIdx.x); i < (rows + 31) / 32; i += int(blockDim.x)) mask[i] = 0u;
   __syncthreads();
-  for (int64_t i = bound[0] + threadIdx.x; i < bound[1]; i += blockDim.x) {
-    const uint32_t r = __ldcg(key + i) - uint32_t(r0);
-    atomicOr(mask + (r >> 5), 1u << (r & 31u));
+  if (bound[1] - bound[0] <= 16 * int64_t(max(rows, int(blockDim.x)))) {
+    for (int64_t i = bound[0] + threadIdx.x; i < bound[1]; i += blockDim.x) {
+      const uint32_t r = __ldcg(key + i) - uint32_t(r0);
+      atomicOr(mask + (r >> 5), 1u << (r & 31u));
+    }
+  } else {   // a frequent token among them: look the rows up instead of walking its keys
+             // (16384 x 768, all the last of 50257 rows: 69 -> 46 us)
+    for (int r = int(threadIdx.x); r < rows; r += int(blockDim.x)) {
+      int64_t lo = bound[0], hi = bound[1];
+      while (lo < hi) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (__ldcg(key + mid) < uint32_t(r0 + r))
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      if (lo < bound[1] && __ldcg(key + lo) == uint32_t(r0 + r)) atomicOr(mask + (r >> 5), 1u << (r & 31));
+    }
   }
   __syncthreads();
   float* g = p.grad + r0 * p.dim;

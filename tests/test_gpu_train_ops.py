@@ -288,6 +288,20 @@ def test_grad_tables_whose_zeros_both_launches_write(n, vocab, dim):
     assert not grad.any()
 
 
+@pytest.mark.parametrize("n,vocab,dim,row", [(20000, 50257, 64, 50256), (20000, 50257, 65, 40000), (60000, 128256, 16, 128000),
+                                             (5000, 40000, 1024, 39999)])
+def test_grad_frequent_token_among_the_rows_zeroed_last(n, vocab, dim, row):
+    dout = randn((n, dim), torch.float32, 1)
+    tokens = torch.full((n,), row, device=dev())
+    tokens[7::1000] = row - 1
+    tokens[5::1001] = row - 77
+    grad = run_grad(dout, tokens, vocab)
+    rows, remap = torch.unique(tokens, return_inverse=True)
+    check_grad(grad[rows], dout, remap, len(rows), 1.0, -1, None, None)
+    grad[rows] = 0
+    assert not grad.any()
+
+
 def test_grad_against_differences_of_the_lookup():
     # the lookup is linear in its table: <lookup(E + D) - lookup(E), dout> = <grad, D>
     n, vocab, dim = 400, 60, 48
