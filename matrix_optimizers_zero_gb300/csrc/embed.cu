@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(256) embed_lookup_flat_kernel(const LookupPara
 
 // ------------------------------------------------------------------ gradient: sort
 //
-// Launch 1 of the gradient. Cluster 0 (eight CTAs; one for few tokens) sorts
+// Launch 1 of the gradient, below 65536 tokens. Cluster 0 (eight CTAs; one for few) sorts
 // the tokens with their positions by a stable radix sort, up to 9 bits a pass
 // (two passes for vocabularies up to 2^18). The other clusters meanwhile write
 // zeros to the first rows of the table, as many as the sort takes the time for;
@@ -277,113 +277,195 @@ __device__ __forceinline__ uint32_t sort_key(const GradParams& p, int64_t i, boo
   return valid && tok != p.tokens.padding ? uint32_t(tok) : uint32_t(p.vocab);
 }
 
-__device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank, uint32_t ctas) {
-  const int bins = 1 << p.digit_bits, stride = bins + 1;   // the odd stride serves a bin's counts from 32 banks
-  uint32_t* hist = sm;                                     // [warp][bin]
-  uint32_t* total = sm + size_t(kSortWarps) * stride;      // this CTA's bin counts, read by the cluster
-  uint32_t* start = total + bins;                          // where this CTA's part of each bin begins
-  uint32_t* wsum = start + bins;
-  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  const int64_t n = p.tokens.n;
-  // positions a warp: a multiple of 32
-  const int64_t per_warp = (n + int64_t(ctas) * kSortThreads - 1) / (int64_t(ctas) * kSortThreads) * 32;
-  const int64_t begin = (int64_t(rank) * kSortWarps + warp) * per_warp;
-  const int64_t end = min(n, begin + per_warp);
-  uint32_t* my = hist + size_t(warp) * stride;
+// The parts of a pass. A warp's positions are [begin, end), per_warp a warp; hist
+// is [warp][bin] with a stride of bins + 1 words, so that a bin's counts lie in
+// 32 banks.
+struct Pass {
+  int index, shift, bins, stride;
+  const uint32_t* src_key;   // pass k writes buffer k & 1
+  const uint32_t* src_pos;
+  uint32_t* dst_key;
+  uint32_t* dst_pos;
+  __device__ __forceinline__ Pass(const GradParams& p, int pass)
+      : index(pass), shift(pass * p.digit_bits), bins(1 << p.digit_bits), stride(bins + 1), src_key(p.key[(pass + 1) & 1]),
+        src_pos(p.pos[(pass + 1) & 1]), dst_key(p.key[pass & 1]), dst_pos(p.pos[pass & 1]) {}
+  __device__ __forceinline__ uint32_t bin(uint32_t key) const { return (key >> shift) & uint32_t(bins - 1); }
+  // kBatch loads at a time
+  __device__ __forceinline__ void load(const GradParams& p, int64_t base, int64_t end, bool report, uint32_t (&k)[kBatch],
+                                       uint32_t (&at)[kBatch]) const {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = base + 32 * u + (threadIdx.x & 31);
+      if (i < end) {
+        k[u] = index == 0 ? sort_key(p, i, report) : __ldcg(src_key + i);
+        at[u] = index == 0 ? uint32_t(i) : __ldcg(src_pos + i);
+      }
+    }
+  }
+};
 
-  // the join's arrival counters, for launch 2
-  for (int64_t i = int64_t(rank) * kSortThreads + tid; i < p.counters; i += int64_t(ctas) * kSortThreads)
-    p.counter[i] = 0u;
+// Counts the digits of a warp's positions into `my`; the last batch stays in k and at.
+__device__ __forceinline__ void count_digits(const GradParams& p, const Pass& q, int64_t begin, int64_t end, uint32_t* my,
+                                             bool report, uint32_t (&k)[kBatch], uint32_t (&at)[kBatch]) {
+  for (int64_t base = begin; base < end; base += 32 * kBatch) {
+    q.load(p, base, end, report, k, at);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (base + 32 * u + (threadIdx.x & 31) < end) atomicAdd(my + q.bin(k[u]), 1u);
+  }
+}
 
-  for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = pass * p.digit_bits;
-    const uint32_t* src_key = p.key[(pass + 1) & 1];   // pass k writes buffer k & 1
-    const uint32_t* src_pos = p.pos[(pass + 1) & 1];
-    uint32_t* dst_key = p.key[pass & 1];
-    uint32_t* dst_pos = p.pos[pass & 1];
-    for (int i = tid; i < kSortWarps * stride; i += kSortThreads) hist[i] = 0u;
-    __syncthreads();
-    // kBatch loads at a time; a part of one batch stays in registers for the scatter
-    uint32_t k[kBatch], at[kBatch];
-    auto load = [&](int64_t base, bool report) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int64_t i = base + 32 * u + lane;
-        if (i < end) {
-          k[u] = pass == 0 ? sort_key(p, i, report) : __ldcg(src_key + i);
-          at[u] = pass == 0 ? uint32_t(i) : __ldcg(src_pos + i);
-        }
-      }
-    };
-    for (int64_t base = begin; base < end; base += 32 * kBatch) {
-      load(base, true);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (base + 32 * u + lane < end) atomicAdd(my + ((k[u] >> shift) & uint32_t(bins - 1)), 1u);
-    }
-    __syncthreads();
-    // offsets over (bin, CTA, warp): within the CTA a warp scans a bin's counts, one a lane
-    for (int b = warp; b < bins; b += kSortWarps) {
-      const uint32_t c = hist[size_t(lane) * stride + b];
-      uint32_t inc = c;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-        if (lane >= d) inc += v;
-      }
-      hist[size_t(lane) * stride + b] = inc - c;
-      if (lane == 31) total[b] = inc;
-    }
-    ptx::cluster_sync();
-    uint32_t before = 0, inc = 0;
-    if (tid < bins) {
-      uint32_t all = 0;
-      for (uint32_t c = 0; c < ctas; ++c) {
-        uint32_t v;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                     : "=r"(v)
-                     : "r"(ptx::mapa_shared(ptx::smem_addr(total + tid), c))
-                     : "memory");
-        before += c < rank ? v : 0u;
-        all += v;
-      }
-      inc = all;
-      before -= all;
-    }
+// Turns the warps' counts of each bin into offsets, and writes the bins' totals: a warp
+// scans a bin, one count a lane.
+__device__ __forceinline__ void scan_warps(const Pass& q, uint32_t* hist, uint32_t* total) {
+  const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+  for (int b = warp; b < q.bins; b += kSortWarps) {
+    const uint32_t c = hist[size_t(lane) * q.stride + b];
+    uint32_t inc = c;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
       if (lane >= d) inc += v;
     }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    if (tid < bins) {
-      for (int w = 0; w < warp; ++w) before += wsum[w];
-      start[tid] = before + inc;   // bins before this one, and this one's part in the CTAs before
-    }
-    __syncthreads();
-    for (int64_t base = begin; base < end; base += 32 * kBatch) {
-      if (per_warp > 32 * kBatch) load(base, false);
+    hist[size_t(lane) * q.stride + b] = inc - c;
+    if (lane == 31) total[b] = inc;
+  }
+}
+
+// Sum of `value` over the threads before this one (those with a value come first).
+__device__ __forceinline__ uint32_t scan_block(uint32_t value, uint32_t* wsum) {
+  const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+  uint32_t inc = value;
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (base + 32 * u >= end) break;   // the same for the whole warp
-        const bool live = base + 32 * u + lane < end;
-        const uint32_t bin = live ? (k[u] >> shift) & uint32_t(bins - 1) : uint32_t(bins);
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, bin);
-        const uint32_t below = peers & ((1u << lane) - 1u);
-        const uint32_t off = live ? my[bin] : 0u;
-        __syncwarp();
-        if (live && below == 0u) my[bin] = off + uint32_t(__popc(peers));
-        __syncwarp();
-        if (live) {
-          const uint32_t to = start[bin] + off + uint32_t(__popc(below));
-          dst_key[to] = k[u];
-          dst_pos[to] = at[u];
-        }
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    if (lane >= d) inc += v;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  return inc - value + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wsum[lane] : 0u);
+}
+
+// Writes a warp's keys and positions where start[bin] and its offsets `my` say, in order.
+__device__ __forceinline__ void scatter(const GradParams& p, const Pass& q, int64_t begin, int64_t end, int64_t per_warp,
+                                        uint32_t* my, const uint32_t* start, uint32_t (&k)[kBatch], uint32_t (&at)[kBatch]) {
+  const int lane = int(threadIdx.x & 31);
+  for (int64_t base = begin; base < end; base += 32 * kBatch) {
+    if (per_warp > 32 * kBatch) q.load(p, base, end, false, k, at);   // one batch is still there
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (base + 32 * u >= end) break;   // the same for the whole warp
+      const bool live = base + 32 * u + lane < end;
+      const uint32_t bin = live ? q.bin(k[u]) : uint32_t(q.bins);
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, bin);
+      const uint32_t below = peers & ((1u << lane) - 1u);
+      const uint32_t off = live ? my[bin] : 0u;
+      __syncwarp();
+      if (live && below == 0u) my[bin] = off + uint32_t(__popc(peers));
+      __syncwarp();
+      if (live) {
+        const uint32_t to = start[bin] + off + uint32_t(__popc(below));
+        q.dst_key[to] = k[u];
+        q.dst_pos[to] = at[u];
       }
     }
+  }
+}
+
+// The join's arrival counters, for the sums' launch.
+__device__ __forceinline__ void clear_counters(const GradParams& p, int64_t cta, int64_t ctas) {
+  for (int64_t i = cta * kSortThreads + threadIdx.x; i < p.counters; i += ctas * kSortThreads) p.counter[i] = 0u;
+}
+
+__device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank, uint32_t ctas) {
+  const int tid = int(threadIdx.x), warp = tid >> 5;
+  const int64_t n = p.tokens.n;
+  // positions a warp: a multiple of 32
+  const int64_t per_warp = (n + int64_t(ctas) * kSortThreads - 1) / (int64_t(ctas) * kSortThreads) * 32;
+  const int64_t begin = (int64_t(rank) * kSortWarps + warp) * per_warp;
+  const int64_t end = min(n, begin + per_warp);
+  clear_counters(p, rank, ctas);
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const Pass q(p, pass);
+    uint32_t* hist = sm;
+    uint32_t* total = sm + size_t(kSortWarps) * q.stride;   // this CTA's bin counts, read by the cluster
+    uint32_t* start = total + q.bins;                       // where this CTA's part of each bin begins
+    uint32_t* wsum = start + q.bins;
+    uint32_t* my = hist + size_t(warp) * q.stride;
+    for (int i = tid; i < kSortWarps * q.stride; i += kSortThreads) hist[i] = 0u;
+    __syncthreads();
+    uint32_t k[kBatch], at[kBatch];
+    count_digits(p, q, begin, end, my, true, k, at);
+    __syncthreads();
+    scan_warps(q, hist, total);
+    ptx::cluster_sync();
+    uint32_t before = 0, all = 0;   // this bin in the CTAs before, and in all
+    if (tid < q.bins)
+      for (uint32_t c = 0; c < ctas; ++c) {
+        const uint32_t v = ptx::ld_shared_cluster_u32(ptx::mapa_shared(ptx::smem_addr(total + tid), c));
+        before += c < rank ? v : 0u;
+        all += v;
+      }
+    before += scan_block(all, wsum);
+    if (tid < q.bins) start[tid] = before;
+    __syncthreads();
+    scatter(p, q, begin, end, per_warp, my, start, k, at);
     ptx::cluster_sync();   // the pass is complete and visible to the cluster
   }
+}
+
+// Many tokens: three launches a pass on all SMs instead. A block counts its
+// part's digits, a block a bin scans the parts' counts, and the blocks scatter,
+// in the same order as the cluster would. Launch 2 then writes all the zeros.
+// (The gradient of 2^20 x 64, 1000000 rows, three passes: 572 us with one
+// cluster's sort, 199 so; 2^20 x 1024, 128256 rows: 821 and 508.)
+__global__ void __launch_bounds__(kSortThreads) radix_count_kernel(const __grid_constant__ GradParams p, int pass) {
+  __shared__ uint32_t count[kMaxBins];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const Pass q(p, pass);
+  for (int i = int(threadIdx.x); i < q.bins; i += kSortThreads) count[i] = 0u;
+  if (pass == 0) clear_counters(p, blockIdx.x, gridDim.x);
+  __syncthreads();
+  const int64_t begin = (int64_t(blockIdx.x) * kSortWarps + (threadIdx.x >> 5)) * p.per_warp;
+  uint32_t k[kBatch], at[kBatch];
+  count_digits(p, q, begin, min(p.tokens.n, begin + p.per_warp), count, true, k, at);
+  __syncthreads();
+  for (int i = int(threadIdx.x); i < q.bins; i += kSortThreads) p.part_count[size_t(i) * gridDim.x + blockIdx.x] = count[i];
+}
+
+__global__ void __launch_bounds__(kSortThreads) radix_scan_kernel(const __grid_constant__ GradParams p, int parts) {
+  __shared__ uint32_t wsum[kSortWarps];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  uint32_t* c = p.part_count + size_t(blockIdx.x) * parts;   // at most kSortThreads parts
+  const uint32_t v = int(threadIdx.x) < parts ? c[threadIdx.x] : 0u, before = scan_block(v, wsum);
+  if (int(threadIdx.x) < parts) c[threadIdx.x] = before;
+  if (int(threadIdx.x) == parts - 1) p.bin_count[blockIdx.x] = before + v;
+}
+
+__global__ void __launch_bounds__(kSortThreads) radix_scatter_kernel(const __grid_constant__ GradParams p, int pass) {
+  extern __shared__ uint32_t sort_smem[];
+  ptx::griddep_launch_dependents();
+  const Pass q(p, pass);
+  const int tid = int(threadIdx.x), warp = tid >> 5;
+  uint32_t* hist = sort_smem;
+  uint32_t* total = hist + size_t(kSortWarps) * q.stride;
+  uint32_t* start = total + q.bins;
+  uint32_t* wsum = start + q.bins;
+  uint32_t* my = hist + size_t(warp) * q.stride;
+  for (int i = tid; i < kSortWarps * q.stride; i += kSortThreads) hist[i] = 0u;
+  ptx::griddep_wait();
+  __syncthreads();
+  const int64_t begin = (int64_t(blockIdx.x) * kSortWarps + warp) * p.per_warp, end = min(p.tokens.n, begin + p.per_warp);
+  uint32_t k[kBatch], at[kBatch];
+  count_digits(p, q, begin, end, my, false, k, at);
+  __syncthreads();
+  scan_warps(q, hist, total);
+  const uint32_t base = scan_block(tid < q.bins ? p.bin_count[tid] : 0u, wsum);
+  if (tid < q.bins) start[tid] = base + p.part_count[size_t(tid) * gridDim.x + blockIdx.x];
+  __syncthreads();
+  scatter(p, q, begin, end, p.per_warp, my, start, k, at);
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ GradParams p) {
@@ -770,6 +852,12 @@ cudaError_t sum_as(const GradParams& p, cudaStream_t stream) {
                        true, stream, p);
 }
 
+cudaError_t launch_sums(const GradParams& p, bool dout_bf16, cudaStream_t stream) {
+  const bool vec = (p.dim & 7) == 0;
+  if (dout_bf16) return vec ? sum_as<uint16_t, 8>(p, stream) : sum_as<uint16_t, 1>(p, stream);
+  return vec ? sum_as<float, 8>(p, stream) : sum_as<float, 1>(p, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_dropout(const DropoutParams& p, bool bf16, cudaStream_t stream) {
@@ -783,19 +871,30 @@ cudaError_t launch_embed_lookup(const LookupParams& p, bool table_bf16, bool out
 
 cudaError_t launch_embed_grad(const GradParams& p, bool dout_bf16, cudaStream_t stream) {
   static_assert(kSortSmem <= 227 * 1024, "shared memory");
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(embed_sort_kernel), kSortSmem);
-  if (e != cudaSuccess) return e;
+  const size_t bins = size_t(1) << p.digit_bits;
+  const size_t smem = sizeof(uint32_t) * (size_t(kSortWarps) * (bins + 1) + 2 * bins + kSortWarps);
+  cudaError_t e;
+  if (p.parts > 0) {   // many tokens
+    if ((e = allow_smem(reinterpret_cast<const void*>(radix_scatter_kernel), kSortSmem)) != cudaSuccess) return e;
+    for (int pass = 0; pass < p.passes; ++pass) {
+      if ((e = launch_kernel(radix_count_kernel, dim3(unsigned(p.parts)), dim3(kSortThreads), 0, 1, pass > 0, stream, p, pass)) !=
+              cudaSuccess ||
+          (e = launch_kernel(radix_scan_kernel, dim3(unsigned(bins)), dim3(kSortThreads), 0, 1, true, stream, p, p.parts)) !=
+              cudaSuccess ||
+          (e = launch_kernel(radix_scatter_kernel, dim3(unsigned(p.parts)), dim3(kSortThreads), smem, 1, true, stream, p, pass)) !=
+              cudaSuccess)
+        return e;
+    }
+    return launch_sums(p, dout_bf16, stream);
+  }
+  if ((e = allow_smem(reinterpret_cast<const void*>(embed_sort_kernel), kSortSmem)) != cudaSuccess) return e;
   // few tokens sort faster without the cluster's barriers
   const int64_t ctas = p.tokens.n <= kOneCtaTokens ? 1 : 8;
   const int64_t zeros = p.accumulate ? 0 : (p.zero_first * p.dim * 4 + kZeroBytes - 1) / kZeroBytes;
-  const size_t bins = size_t(1) << p.digit_bits;
-  const size_t smem = sizeof(uint32_t) * (size_t(kSortWarps) * (bins + 1) + 2 * bins + kSortWarps);
   e = launch_kernel(embed_sort_kernel, dim3(unsigned(ctas + (zeros + ctas - 1) / ctas * ctas)), dim3(kSortThreads), smem,
                     unsigned(ctas), false, stream, p);
   if (e != cudaSuccess) return e;
-  const bool vec = (p.dim & 7) == 0;
-  if (dout_bf16) return vec ? sum_as<uint16_t, 8>(p, stream) : sum_as<uint16_t, 1>(p, stream);
-  return vec ? sum_as<float, 8>(p, stream) : sum_as<float, 1>(p, stream);
+  return launch_sums(p, dout_bf16, stream);
 }
 
 }  // namespace mo

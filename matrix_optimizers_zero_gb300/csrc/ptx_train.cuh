@@ -72,6 +72,12 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
   return r;
 }
 
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // Adds to a counter in global memory, releasing the block's earlier writes
 // (after a block barrier) and acquiring those of the blocks that added before.
 __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v) {

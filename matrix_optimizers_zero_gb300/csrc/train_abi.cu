@@ -69,9 +69,9 @@ int table_shape(int64_t vocab, int64_t dim) {
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Workspace of embed_grad: two buffers of keys and of positions, the join's
-// counters, the sums of tokens that cross chunks.
+// counters, the sums of tokens that cross chunks, the sort's digit counts.
 struct GradLayout {
-  size_t key[2], pos[2], counter, partial, bytes;
+  size_t key[2], pos[2], counter, partial, part_count, bin_count, bytes;
   int64_t counters, dim_pad;
 };
 GradLayout grad_layout(int64_t n, int64_t dim) {
@@ -90,6 +90,10 @@ GradLayout grad_layout(int64_t n, int64_t dim) {
   L.dim_pad = (dim + 7) / 8 * 8;
   L.partial = at;
   at += align256(size_t(2 * g.chunks) * size_t(L.dim_pad) * 4);
+  L.part_count = at;
+  at += align256(size_t(mo::sort_parts(n).parts) * (size_t(4) << mo::kMaxDigitBits));
+  L.bin_count = at;
+  at += size_t(4) << mo::kMaxDigitBits;
   L.bytes = at;
   return L;
 }
@@ -242,6 +246,11 @@ int embed_grad(const void* dout, int32_t dout_dtype, const mo_tokens* tokens, in
   }
   p.counter = reinterpret_cast<uint32_t*>(w + L.counter);
   p.partial = reinterpret_cast<float*>(w + L.partial);
+  p.part_count = reinterpret_cast<uint32_t*>(w + L.part_count);
+  p.bin_count = reinterpret_cast<uint32_t*>(w + L.bin_count);
+  const mo::SortParts parts = mo::sort_parts(n);
+  p.parts = parts.parts;
+  p.per_warp = parts.per_warp;
   p.counters = L.counters;
   p.dim_pad = L.dim_pad;
   const mo::GradGrid grid = mo::grad_grid(n, dim);
@@ -249,8 +258,11 @@ int embed_grad(const void* dout, int32_t dout_dtype, const mo_tokens* tokens, in
   p.chunks = grid.chunks;
   // launch 1 writes zeros for about as long as its sort takes (at 7 TB/s: 9 us, and 0.34 ns a token);
   // launch 2 in blocks of 128 KB, or of 256 KB where there are thousands (2.1 GB: 327 -> 317 us)
-  p.zero_first = std::min(vocab, ((int64_t(60) << 20) + 2304 * n) / (4 * dim) + 1);
-  const int64_t block = int64_t(grad_bytes) > (int64_t(1) << 30) ? int64_t(256) << 10 : int64_t(128) << 10;
+  // (all of them with many tokens, whose sort leaves launch 1 no time)
+  p.zero_first = p.parts > 0 ? 0 : std::min(vocab, ((int64_t(60) << 20) + 2304 * n) / (4 * dim) + 1);
+  // but no more than 1 KB a thread, as blocks of narrow rows have few (65536 x 63 of 128256: 88 -> 66 us)
+  const int64_t block =
+      std::min(int64_t(grid.threads) << 10, int64_t(grad_bytes) > (int64_t(1) << 30) ? int64_t(256) << 10 : int64_t(128) << 10);
   p.zero_rows = std::max(int64_t(1), std::min(mo::kZeroRowsMost, block / (4 * dim)));
   p.dout = dout;
   p.grad = grad;

@@ -53,6 +53,22 @@ constexpr int kMaxDigitBits = 9;
 constexpr int kMaxChunk = 64;
 constexpr int64_t kZeroRowsMost = 4096;   // rows a block of launch 2 zeroes, at most
 
+// From kManyTokens on the sort takes all SMs and three launches a pass; fewer
+// are one cluster's in one launch. (65536 x 1024 of 50257 rows: uniform tokens
+// 104 us by the cluster, 87 so, one token for all 80 and 83.) A part is a
+// block of 32 warps, one part an SM: with 1024 small parts 2^20 x 64 takes 247
+// us instead of 199, with 16 large ones 65536 x 1024 takes 94 instead of 85.
+constexpr int64_t kManyTokens = 65536;
+struct SortParts {
+  int64_t per_warp;   // positions, a multiple of 32
+  int32_t parts;
+};
+inline SortParts sort_parts(int64_t n) {
+  if (n < kManyTokens) return {0, 0};
+  const int64_t per_warp = (n + 152 * 1024 - 1) / (152 * 1024) * 32;
+  return {per_warp, int32_t((n + 32 * per_warp - 1) / (32 * per_warp))};
+}
+
 // Launch shape of the gradient's sums: chunks of sorted positions by blocks of
 // columns (eight a thread, or one where dim is not a multiple of 8). A chunk
 // is 64 positions, fewer where that leaves too few blocks to fill the GPU.
@@ -80,6 +96,10 @@ struct GradParams {
   uint32_t* pos[2];
   uint32_t* counter;      // arrivals of the join: two per slot and column block
   float* partial;         // [2 chunks, dim_pad] sums of tokens that cross chunks
+  uint32_t* part_count;   // many tokens: [bins, parts] digit counts, then offsets
+  uint32_t* bin_count;    // [bins]
+  int64_t per_warp;       // positions of a warp of a part
+  int32_t parts;          // 0: one cluster sorts
   int64_t counters;
   int64_t vocab, dim, dim_pad, chunk, chunks;
   int64_t zero_first;     // rows that launch 1 zeroes; launch 2 zeroes those of the others that no token names,

@@ -302,6 +302,49 @@ def test_grad_frequent_token_among_the_rows_zeroed_last(n, vocab, dim, row):
     assert not grad.any()
 
 
+@pytest.mark.parametrize("n", [65535, 65536, 65537, 200003])
+@pytest.mark.parametrize("vocab,dim,kind", [(300, 16, "uniform"), (50257, 9, "hot"), (300007, 8, "uniform"), (130000, 8, "one"),
+                                            (2 ** 18, 64, "distinct")])
+def test_grad_many_tokens(n, vocab, dim, kind):
+    dout = randn((n, dim), torch.bfloat16, 1)
+    tokens = make_tokens(n, vocab, kind, 5)
+    tokens[11] = vocab - 1
+    grad = run_grad(dout, tokens, vocab)
+    assert torch.equal(run_grad(dout, tokens, vocab), grad)
+    rows, remap = torch.unique(tokens, return_inverse=True)
+    check_grad(grad[rows], dout, remap, len(rows), 1.0, -1, None, None)
+    grad[rows] = 0
+    assert not grad.any()
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grad_many_tokens_padding_dropout_bad_tokens(accumulate):
+    n, vocab, dim = 90001, 2003, 24
+    dout = randn((n, dim), torch.float32, 1)
+    tokens = make_tokens(n, vocab, "hot", 3).to(torch.int32)
+    tokens[5], tokens[70000] = -3, vocab
+    so_far = randn((vocab, dim), torch.float32, 2) if accumulate else None
+    grad = run_grad(dout, tokens, vocab, 2.0, 0, (0.3, 5, 9), so_far)
+    assert mo.mo_last_device_error() == -11
+    check_grad(grad, dout, tokens, vocab, 2.0, 0, (0.3, 5, 9), so_far)
+
+
+def test_grad_many_tokens_captured_in_a_graph():
+    n, vocab, dim = 70000, 3001, 16
+    dout, tokens = randn((n, dim), torch.bfloat16, 1), make_tokens(n, vocab, "uniform", 2)
+    grad, ws = torch.empty((vocab, dim), device=dev()), mo.embed_grad_workspace(n, vocab, dim)
+    mo.embed_grad(dout, tokens, grad, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mo.embed_grad(dout, tokens, grad, ws)
+    for seed in (3, 4):
+        tokens.copy_(make_tokens(n, vocab, "uniform", seed))
+        grad.fill_(float("nan"))
+        graph.replay()
+        check_grad(grad, dout, tokens, vocab, 1.0, -1, None, None)
+
+
 def test_grad_against_differences_of_the_lookup():
     # the lookup is linear in its table: <lookup(E + D) - lookup(E), dout> = <grad, D>
     n, vocab, dim = 400, 60, 48
