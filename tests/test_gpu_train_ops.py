@@ -133,6 +133,23 @@ def test_lookup(tdt, odt, n, vocab, dim, p):
     assert mo.mo_last_device_error() == 0
 
 
+@pytest.mark.parametrize("dim", [8, 24, 64])
+@pytest.mark.parametrize("p", [0.0, 0.2])
+def test_lookup_many_narrow_rows(dim, p):
+    n, vocab = 2 ** 21 + 3, 5001                # more tokens than threads that take them
+    table = randn((vocab, dim), torch.float32, 1)
+    tokens = torch.randint(0, vocab, (n,), device=dev(), generator=torch.Generator(dev()).manual_seed(2))
+    out = torch.full((n, dim), float("nan"), device=dev())
+    mo.embed_lookup(table, tokens, out, dropout=mo.Dropout(p, seed=3, offset=7) if p else None)
+    if p == 0:
+        assert torch.equal(out, table[tokens])
+        return
+    for a in (0, n // 2 - 500, n - 1000):
+        keep = (ot.random16(1000 * dim, 3, 7, a * dim) >= round(65536 * p)).reshape(1000, dim)
+        ref = f64(table[tokens[a:a + 1000]]) * keep * (65536 / (65536 - round(65536 * p)))
+        check(out[a:a + 1000], ref, 4 * U * np.abs(ref))
+
+
 @pytest.mark.parametrize("dim", [16, 19])
 def test_lookup_outside_the_table_reads_zeros_and_reports(dim):
     table = randn((10, dim), torch.float32, 0)
