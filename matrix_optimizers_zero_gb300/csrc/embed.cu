@@ -710,7 +710,8 @@ __global__ void __launch_bounds__(256, 4) embed_sum_kernel(const __grid_constant
   if (chunk >= p.chunks) {   // the blocks after the sums'
     __shared__ uint32_t mask[kZeroMaskWords];
     const int64_t r0 = p.zero_first + ((chunk - p.chunks) * gridDim.x + blockIdx.x) * p.zero_rows;
-    if (r0 < p.vocab) zero_untouched(p, key, r0, min(p.vocab, r0 + p.zero_rows), mask);
+    // (a grid of several z layers ends in spare blocks, also where nothing is to be zeroed)
+    if (!p.accumulate && r0 < p.vocab) zero_untouched(p, key, r0, min(p.vocab, r0 + p.zero_rows), mask);
     return;
   }
   const uint32_t none = uint32_t(p.vocab);

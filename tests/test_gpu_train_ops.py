@@ -467,3 +467,26 @@ def test_nothing_outside_the_outputs_is_written(dim):
     for whole, count in ((whole_g, vocab * dim), (whole_o, n * dim), (whole_y, n * dim)):
         assert bool((whole[:guard] == 77).all()) and bool((whole[guard + count:] == 77).all())
     assert bool((whole_w[:guard] == 0x5C).all()) and bool((whole_w[guard + ws_bytes:] == 0x5C).all())
+
+
+@pytest.mark.parametrize("accumulate", [True, False])
+@pytest.mark.parametrize("n", [2 ** 21, 2 ** 21 + 1, 3 * 2 ** 20 + 5])
+def test_grad_past_2_to_21_tokens_leaves_other_rows_alone(n, accumulate):
+    # from 2^21 tokens on the launch's blocks no longer fit one row of its grid
+    vocab, dim, padding = 50257, 8, 4000
+    g = torch.Generator(dev()).manual_seed(n)
+    tokens = 4000 + 3 * torch.randint(0, 500, (n,), generator=g, device=dev())   # 499 rows, and the padding
+    dout = torch.randn((n, dim), generator=g, device=dev())
+    so_far = torch.randn((vocab, dim), generator=g, device=dev()) if accumulate else None
+    grad = run_grad(dout, tokens, vocab, 0.5, padding, None, so_far)
+    named = torch.unique(tokens)
+    named = named[named != padding]
+    base = so_far.double() if accumulate else torch.zeros((vocab, dim), dtype=torch.float64, device=dev())
+    keep = tokens != padding
+    ref = base.index_add(0, tokens[keep], 0.5 * dout[keep].double())
+    mag = base.abs().index_add(0, tokens[keep], 0.5 * dout[keep].double().abs())
+    count = torch.bincount(tokens, minlength=vocab)[:, None]
+    assert bool(((grad.double() - ref).abs() <= (count + 4) * U * mag)[named].all())
+    others = torch.ones(vocab, dtype=torch.bool, device=dev())
+    others[named] = False
+    assert torch.equal(grad[others], so_far[others] if accumulate else torch.zeros_like(grad[others]))
