@@ -54,13 +54,28 @@ struct ProductParams {
   uint64_t timeout_ns;
 };
 
-__device__ __forceinline__ float scale_of(const float* amax) {
-  if (amax == nullptr) return 1.0f;
+// Exponent of a tensor's own scale g (a power of two, 2^-126 to 2^117).
+__device__ __forceinline__ int scale_exponent(const float* amax) {
+  if (amax == nullptr) return 0;
   const uint32_t b = __float_as_uint(*amax) & 0x7FFFFFFFu;
-  if (b == 0u || b >= 0x7F800000u) return 1.0f;
-  const int e = int(b >> 23) - 138 + ((b & 0x7FFFFFu) > 0x280000u ? 1 : 0);
-  return __uint_as_float(uint32_t(max(e, -126) + 127) << 23);
+  if (b == 0u || b >= 0x7F800000u) return 0;
+  return max(int(b >> 23) - 138 + ((b & 0x7FFFFFu) > 0x280000u ? 1 : 0), -126);
 }
+
+// gA gB as two powers of two, applied one after the other: their product, 2^-252
+// to 2^234, is no float at either end, where the sums times it may be (a sum of
+// 0 always is). A sum that is not 0 is at least 2^-20 (the smallest codes and
+// scales), so the first product, with no less than 2^-100, is exact; what the
+// second cuts off below 2^-226 rounds to 0 whatever the sum.
+struct Factor {
+  float first, second;
+  __device__ __forceinline__ Factor(const float* amax_a, const float* amax_b) {
+    const int e = scale_exponent(amax_a) + scale_exponent(amax_b), e1 = min(max(e, -100), 127), e2 = max(e - e1, -126);
+    first = __uint_as_float(uint32_t(e1 + 127) << 23);
+    second = __uint_as_float(uint32_t(e2 + 127) << 23);
+  }
+  __device__ __forceinline__ float operator()(float sum) const { return sum * first * second; }
+};
 
 __device__ __forceinline__ void put(uint16_t* o, float v) { *o = float_to_bf16_bits(v); }
 __device__ __forceinline__ void put(float* o, float v) { *o = v; }
@@ -427,7 +442,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
     // -------------------------------------------------------------- epilogue (both CTAs)
     const int quarter = warp & 3;
     const int half = (warp - 2) >> 2;
-    const float factor = scale_of(p.amax_a) * scale_of(p.amax_b);
+    const Factor scaled(p.amax_a, p.amax_b);
     uint32_t* turn = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 384) + (warp - 2) * kTurnWords;
     int32_t i = 0;
     for (int32_t t = first; t < ntiles; t += step, ++i) {
@@ -460,7 +475,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           const int64_t at = col + chunk(s + q) * 32;
           float v[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[q][j]) * factor;
+          for (int j = 0; j < 32; ++j) v[j] = scaled(__uint_as_float(r[q][j]));
           if (row0 < p.m && at < p.n) store_chunk(static_cast<O*>(p.out), row0, p.m, at, p.n, p.align, v, turn);
         }
       }
@@ -570,7 +585,7 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
   const uint32_t tmem = *tmem_slot;
   ptx::griddep_launch_dependents();   // after the TMEM is held, as above
   ptx::griddep_wait();
-  const float factor = scale_of(p.amax_a) * scale_of(p.amax_b);
+  const Factor scaled(p.amax_a, p.amax_b);
 
   uint32_t n_issued = 0;
   bool mma_issued = false;
@@ -661,7 +676,7 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
           if (parts > 1)
             sums[uint32_t(c + j) * kNarrowPitch + uint32_t(quarter * 32 + lane)] = __uint_as_float(r[j]);
           else if (c + j < rows && n_at < p.n)
-            put(out + int64_t(c + j) * p.n, __uint_as_float(r[j]) * factor);
+            put(out + int64_t(c + j) * p.n, scaled(__uint_as_float(r[j])));
         }
       }
     }
@@ -702,7 +717,7 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
           t.w += v[s].w;
         }
       O* o = static_cast<O*>(p.out) + (row0 + j) * p.n + col0 + l;
-      const float f[4] = {t.x * factor, t.y * factor, t.z * factor, t.w * factor};
+      const float f[4] = {scaled(t.x), scaled(t.y), scaled(t.z), scaled(t.w)};
       if (vec && col0 + l + 4 <= p.n) {
         if constexpr (sizeof(O) == 2)
           *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));

@@ -378,3 +378,38 @@ def test_nothing_outside_the_outputs_is_written(m, n, k):
         mo.fp4_dequantize(q[1], v[1].view(k, m))
     for whole, part, value in keep:
         assert bool((whole[:guard] == value).all()) and bool((whole[guard + part.numel():] == value).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(20, 200, 512), (100, 260, 6208), (300, 5120, 320)])   # few rows, split K, pairs
+@pytest.mark.parametrize("sa,sb", [(90, 90), (115, 20), (30, 70), (-75, -75), (-75, -100), (-126, 110), (117, -126), (40, -30)])
+def test_product_at_the_ends_of_the_tensor_scales(m, n, k, sa, sb):
+    # the tensors' scales 2^sa and 2^sb; their product need not be a float where the result is one
+    rng = np.random.default_rng(1000 + m + sa)
+    qs, vs = [], []
+    for rows, e, zero in ((m, sa, 3), (n, sb, 5)):
+        v = rng.uniform(0.25, 1, size=(rows, k)) * 2688
+        v[zero] = 0                              # a row of zeros stays 0
+        v[zero + 1] *= 2.0 ** -12                # small sums
+        v[0, 0] = 2688
+        codes, bits, values = ot.fp4_quantize(v, "nv")
+        c, s = ot.fp4_pack(codes, bits, "nv")
+        amax = torch.tensor([min(2688 * 2.0 ** e, torch.finfo(torch.float32).max)], device=dev())
+        qs.append(mo.Fp4Tensor(rows, k, "nv", codes=torch.from_numpy(c).to(dev()), scales=torch.from_numpy(s).to(dev()), amax=amax))
+        vs.append(torch.from_numpy(values).to(dev()))
+    sums = vs[0] @ vs[1].T
+    for odt in (torch.float32, torch.bfloat16):
+        out = torch.full((m, n), 9.0, dtype=odt, device=dev())
+        mo.fp4_product(*qs, out)
+        assert mo.mo_last_device_error() == 0
+        assert not out[3].any() and not out[:, 5].any()
+        # the roundings: k 2^-23 of the sum, one to the type, and its smallest step where the result is subnormal
+        rel = k * 2.0 ** -23 + 1.01 * ROUND[odt]
+        step = 2.0 ** (-149 if odt == torch.float32 else -133)
+        most = torch.finfo(odt).max
+        exact = sums * 2.0 ** sa * 2.0 ** sb
+        lo, hi = exact * (1 - rel) - step, exact * (1 + rel) + step
+        got = out.double()
+        assert bool(((got >= lo) | (got == most)).all()) and bool(((got <= hi) | (hi >= most)).all())
+        assert bool(torch.isinf(got)[lo > 1.01 * most].all()) and bool(torch.isfinite(got)[hi < most].all())
+        if odt == torch.float32 and sa + sb == -150:
+            assert bool((exact > 2.0 ** -126).any())   # results of full precision
