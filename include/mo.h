@@ -407,7 +407,8 @@ int fp4_product(const mo_fp4* a, const mo_fp4* b, void* out, int32_t dtype, cuda
 /* Synchronises `stream`, then returns and clears the device-side status word:
  * MO_OK, MO_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel expired
  * (the kernel then skipped its remaining work and released its resources), or
- * MO_ERR_BAD_TOKEN if an embedding call met an index outside its table. */
+ * MO_ERR_BAD_TOKEN if an embedding call met an index outside its table. Where
+ * both happened since the last call, in either order, it is the former. */
 int mo_last_device_error(cudaStream_t stream);
 
 /* cudaError_t of the most recent MO_ERR_CUDA on this thread (0 if none). */

@@ -81,6 +81,10 @@ __device__ __forceinline__ int64_t token_at(const TokenArgs& t, int64_t i) {
   return t.wide ? static_cast<const int64_t*>(t.ids)[i] : int64_t(static_cast<const int32_t*>(t.ids)[i]);
 }
 
+// The status word is shared with the bounded waits: an expired one, after which a
+// result is incomplete, is not replaced.
+__device__ __forceinline__ void report_bad_token(int* status) { atomicCAS(status, MO_OK, MO_ERR_BAD_TOKEN); }
+
 // ------------------------------------------------------------------ dropout
 // A thread takes kDropGroups groups of eight elements, kDropThreads groups
 // apart, and issues all their loads before the first use. Bound by memory
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(256, ADD ? 4 : 5) embed_lookup_kernel(const Lo
     const int64_t tok = next;
     if (t + stride < p.tokens.n) next = token_at(p.tokens, t + stride);
     const bool valid = tok >= 0 && tok < p.vocab;
-    if (!valid && threadIdx.x == 0) atomicExch(p.status, MO_ERR_BAD_TOKEN);
+    if (!valid && threadIdx.x == 0) report_bad_token(p.status);
     const T* row = static_cast<const T*>(p.table) + (valid ? tok : 0) * p.dim;
     const T* add = ADD ? static_cast<const T*>(p.add) + (t % p.add_rows) * p.dim : nullptr;
     O* out = static_cast<O*>(p.out) + t * p.dim;
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(256) embed_lookup_flat_kernel(const LookupPara
       if (fresh) {
         tok = token_at(p.tokens, t);
         valid = tok >= 0 && tok < p.vocab;
-        if (!valid) atomicExch(p.status, MO_ERR_BAD_TOKEN);
+        if (!valid) report_bad_token(p.status);
         fresh = false;
       }
       if (valid) v[i] = to_float(static_cast<const T*>(p.table)[tok * p.dim + c]) * p.scale;
@@ -275,7 +279,7 @@ constexpr int kZeroMaskWords = kZeroRowsMost / 32;
 __device__ __forceinline__ uint32_t sort_key(const GradParams& p, int64_t i, bool report) {
   const int64_t tok = token_at(p.tokens, i);
   const bool valid = tok >= 0 && tok < p.vocab;
-  if (report && !valid) atomicExch(p.status, MO_ERR_BAD_TOKEN);
+  if (report && !valid) report_bad_token(p.status);
   return valid && tok != p.tokens.padding ? uint32_t(tok) : uint32_t(p.vocab);
 }
 

@@ -490,3 +490,28 @@ def test_grad_past_2_to_21_tokens_leaves_other_rows_alone(n, accumulate):
     others = torch.ones(vocab, dtype=torch.bool, device=dev())
     others[named] = False
     assert torch.equal(grad[others], so_far[others] if accumulate else torch.zeros_like(grad[others]))
+
+
+@pytest.mark.parametrize("timeout_first", [True, False])
+@pytest.mark.parametrize("call", ["lookup", "lookup odd", "grad", "grad many"])
+def test_a_bad_token_does_not_hide_an_expired_wait(call, timeout_first):
+    dim, n = (9 if call == "lookup odd" else 8), (70000 if call == "grad many" else 40)
+    tokens = torch.zeros(n, dtype=torch.int64, device=dev())
+    tokens[3] = 10
+    x = torch.zeros((n, dim), device=dev())
+
+    def bad_token():
+        if call.startswith("lookup"):
+            mo.embed_lookup(torch.zeros((10, dim), device=dev()), tokens, x)
+        else:
+            run_grad(x, tokens, 10)
+    assert mo.mo_last_device_error() == 0
+    if not timeout_first:
+        bad_token()
+    mo.mo_selftest_bounded_wait(20_000_000)    # 20 ms
+    if timeout_first:
+        bad_token()
+    assert mo.mo_last_device_error() == -8
+    assert mo.mo_last_device_error() == 0
+    bad_token()
+    assert mo.mo_last_device_error() == -11
