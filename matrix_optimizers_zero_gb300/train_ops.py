@@ -163,6 +163,7 @@ def embed_grad(dout, tokens, grad, workspace, scale: float = 1.0, padding_idx: i
     vocab, dim = grad.shape
     if dout.numel() != tokens.numel() * dim:
         raise ValueError("dout must have dim elements for every token")
+    _dense(workspace, "workspace")
     tk = _tokens(tokens, padding_idx)
     st = load_library().embed_grad(dout.data_ptr(), code, ctypes.byref(tk), vocab, dim, scale, _ref(dropout),
                                    grad.data_ptr(), int(accumulate), workspace.data_ptr(),
