@@ -285,8 +285,10 @@ enum mo_dtype { MO_F32 = 0, MO_BF16 = 1 };
 
 /* Counter-based random numbers (Philox4x32-10): element i of a tensor takes
  * the 16-bit number i % 8 (low half of each word first) of the call with
- * counter (i / 8, offset) under the key `seed`. A caller advances `offset`
- * from step to step and from layer to layer. *d_offset (device memory, 8-byte
+ * counter (i / 8, offset) under the key `seed`. Uses that share seed and
+ * offset draw the same numbers: a caller advances `offset` from step to step,
+ * from layer to layer and from use to use, past the two that fp4_quantize takes
+ * (by_row and by_col). *d_offset (device memory, 8-byte
  * aligned, may be NULL) is added to `offset` when the kernel runs, so a
  * captured step can advance it between replays. */
 typedef struct {

@@ -5,7 +5,7 @@ quantisation with its product.
 Tensors are contiguous CUDA tensors on the current device, fp32 or bf16;
 outputs are written in place, on the current stream unless one is given:
 
-    drop = mo.Dropout(0.1, seed=seed, offset=step)         # drawn again in the backward pass
+    drop = mo.Dropout(0.1, seed=seed, offset=4 * step)     # drawn again in the backward pass
     mo.embed_lookup(table, tokens, x, scale=1.0, add=positions, dropout=drop)
     ws = mo.embed_grad_workspace(tokens.numel(), *table.shape)   # reuse it every step
     mo.embed_grad(dx, tokens, g, ws, scale=1.0, dropout=drop)    # g: the fp32 gradient adamw_tail_step reads
@@ -13,9 +13,13 @@ outputs are written in place, on the current stream unless one is given:
 
     wq, wt = mo.Fp4Tensor(n, k, "mx"), mo.Fp4Tensor(k, n, "mx")   # "mx": 32-element blocks; "nv": 16
     mo.fp4_quantize(w, wq, wt)                             # both orientations from one pass over w
-    mo.fp4_quantize(dy, dyq, dyt, stochastic=mo.Random(seed, step))
+    mo.fp4_quantize(dy, dyq, dyt, stochastic=mo.Random(seed, 4 * step + 1))   # dyt takes 4 * step + 2
     mo.fp4_product(xq, wq, y)                              # y = x w^T
     mo.fp4_product(dyt, xt, dw)                            # dw = dy^T x: the bf16 gradient muon_owner_step reads
+
+Every dropout and every stochastic rounding of a step has an offset of its own,
+and a step's offsets begin behind the last one's: uses that share seed and
+offset draw the same numbers. fp4_quantize takes offset + 1 too, for by_col.
 """
 from __future__ import annotations
 

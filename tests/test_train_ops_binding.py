@@ -1,5 +1,8 @@
 """The binding's own checks of its tensors (no GPU needed: stand-ins for CUDA
 tensors, and a stand-in for the library that records its calls)."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -61,3 +64,26 @@ def test_embed_grad_refuses_other_workspaces(library, kw):
     with pytest.raises(ValueError, match="workspace"):
         call_grad(Tensor((1 << 16,), torch.uint8, **kw))
     assert not library.calls
+
+
+# ---------------------------------------------------------------- the documented use of the generator
+
+def generator_streams(text, step):
+    """(seed, offset) of every stream that the lines of a code sample draw from at a step."""
+    used = []
+    for line in text.splitlines():
+        for cls, args in re.findall(r"mo\.(Dropout|Random)\(([^()]*)\)", line.split("#")[0]):
+            made = eval(f"mo.{cls}({args})", {"mo": mo, "seed": 7, "step": step})
+            r = made.random if cls == "Dropout" else made
+            # a quantisation takes the next offset for the transposed tensor
+            used += [(r.seed, r.offset + i) for i in range(2 if "fp4_quantize" in line else 1)]
+    return used
+
+
+@pytest.mark.parametrize("where", ["docstring", "README.md"])
+def test_documented_offsets_never_repeat(where):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = train_ops.__doc__ if where == "docstring" else open(os.path.join(root, where), encoding="utf-8").read()
+    assert len(generator_streams(text, 1)) == 3      # dropout, both orientations of a gradient
+    used = [s for step in range(1, 9) for s in generator_streams(text, step)]
+    assert len(set(used)) == len(used)
