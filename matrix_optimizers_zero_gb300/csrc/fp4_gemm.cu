@@ -314,15 +314,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       for (int32_t t = first; ok && t < ntiles; t += step, ++i) {
         const int acc = i & 1;
         // the accumulator's previous tile is drained, and the columns shared with the last one
-        if (!mbar_wait_bounded(tempty_bar(acc), (uint32_t(i >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
-        if (i > 0 && !mbar_wait_bounded(over_bar(acc ^ 1), uint32_t((i - 1) >> 1) & 1u, abort_flag, p.status, p.timeout_ns))
+        if (!mbar_wait_bounded<true>(tempty_bar(acc), (uint32_t(i >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
+        if (i > 0 && !mbar_wait_bounded<true>(over_bar(acc ^ 1), uint32_t((i - 1) >> 1) & 1u, abort_flag, p.status, p.timeout_ns))
           break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc) * kAccStep;
         int32_t left = p.steps;
         for (int32_t kb = 0; kb < p.stages; ++kb) {
           // (a stage's scales are reported only once its codes have landed too)
-          if (!seen && !mbar_wait_bounded(sf_ready_bar(slot), sph, abort_flag, p.status, p.timeout_ns)) {
+          if (!seen && !mbar_wait_bounded<true>(sf_ready_bar(slot), sph, abort_flag, p.status, p.timeout_ns)) {
             ok = false;
             break;
           }
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
           left -= 4;
           ptx::umma_commit_pair(bar, 0x3);
           // the next stage is looked at while these are under way
-          seen = ptx::mbar_peek(sf_ready_bar(slot), sph);
+          seen = ptx::mbar_peek_cluster(sf_ready_bar(slot), sph);
           mma_issued = true;
         }
         if (!ok) break;
@@ -422,10 +422,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         ptx::tmem_st_32x32b_x16(c + 16, w + 16);
         ptx::tmem_st_32x32b_x16(c + 32, w + 32);
       }
-      // The stores have completed before the arrive, which therefore needs no wider release than its
-      // own CTA's (a cluster-scope one in every stage: 8192^3 214 -> 402 us). The shared memory goes
-      // back only now too: an arrive in front of the stores can pass loads whose values nothing has
-      // used yet, and the next copy then overwrites what they read.
+      // The shared memory goes back only after the stores: an arrive in front of them can pass loads
+      // whose values nothing has used yet, and the next copy then overwrites what they read.
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
@@ -436,7 +434,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         ok = mbar_wait_bounded(full_bar(int(j % kPairStages)), (j / kPairStages) & 1u, abort_flag, p.status, p.timeout_ns);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
       }
-      if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(sf_ready_bar(int(slot)), 0));
+      // The TMEM stores are ordered by the wait and the fence above and the fence after the issuing
+      // thread's wait, so the odd CTA's arrive is a relaxed one (8192^3 mx: 177 us; a cluster-scope
+      // release in every stage nearly doubled the time). The even CTA's also passes on that the codes
+      // have landed, to a thread of its own CTA. The issuing thread waits at cluster scope, which takes
+      // 2% more than a wait at its own CTA's (173 us).
+      if (lane == 0) {
+        const uint32_t ready = ptx::mapa_shared(sf_ready_bar(int(slot)), 0);
+        if (leader)
+          ptx::mbar_arrive_remote_cta(ready);
+        else
+          ptx::mbar_arrive_remote_relaxed(ready);
+      }
     }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         ptx::tmem_ld_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_remote_cta(ptx::mapa_shared(s == 0 ? over_bar(acc) : tempty_bar(acc), 0));
+        if (lane == 0) ptx::mbar_arrive_remote_relaxed(ptx::mapa_shared(s == 0 ? over_bar(acc) : tempty_bar(acc), 0));
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int64_t at = col + chunk(s + q) * 32;

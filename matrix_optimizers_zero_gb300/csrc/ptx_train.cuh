@@ -86,12 +86,20 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v) 
   return r;
 }
 
-// Whether the phase with the given parity has completed, without waiting.
-__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
+// Arrives on an mbarrier of any CTA of the cluster without releasing memory:
+// hands over accesses to TMEM, which tcgen05.wait and
+// tcgen05.fence::before_thread_sync have ordered.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Whether the phase with the given parity has completed, without waiting; its
+// arrives may be another CTA's.
+__device__ __forceinline__ bool mbar_peek_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)

@@ -413,3 +413,19 @@ def test_product_at_the_ends_of_the_tensor_scales(m, n, k, sa, sb):
         assert bool(torch.isinf(got)[lo > 1.01 * most].all()) and bool(torch.isfinite(got)[hi < most].all())
         if odt == torch.float32 and sa + sb == -150:
             assert bool((exact > 2.0 ** -126).any())   # results of full precision
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_product_of_many_tiles_repeats_bit_for_bit(fmt):
+    # scales and accumulators change hands between the two CTAs of a pair in every stage and tile
+    m, n, k = 2048, 8192, 1280
+    a, b = mo.Fp4Tensor(m, k, fmt), mo.Fp4Tensor(n, k, fmt)
+    mo.fp4_quantize(data(m, k, torch.bfloat16, 1), a)
+    mo.fp4_quantize(data(n, k, torch.bfloat16, 2), b)
+    first, out = torch.empty((m, n), device=dev()), torch.empty((m, n), device=dev())
+    mo.fp4_product(a, b, first)
+    for _ in range(30):
+        out.fill_(float("nan"))
+        mo.fp4_product(a, b, out)
+        assert torch.equal(out, first)
+    assert mo.mo_last_device_error() == 0
