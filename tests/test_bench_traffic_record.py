@@ -51,5 +51,6 @@ def test_the_launches_sources_end_the_record(tree, name, old, new):
 
 
 def test_a_missing_launch_function_ends_the_record(tree):
-    edit(tree / "abi.cu", "\nint enqueue_muon(", "\nint enqueue_muon_step(")
+    text = (tree / "abi.cu").read_text(encoding="utf-8")
+    (tree / "abi.cu").write_text(text.replace("\nint enqueue_muon(", "\nint enqueue_muon_step("), encoding="utf-8")
     assert all(bench.ns_traffic(w)[0] is None for w in bench.NS_TRAFFIC)
