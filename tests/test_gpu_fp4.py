@@ -429,3 +429,31 @@ def test_product_of_many_tiles_repeats_bit_for_bit(fmt):
         mo.fp4_product(a, b, out)
         assert torch.equal(out, first)
     assert mo.mo_last_device_error() == 0
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 33), (130, 257), (257, 40), (64, 1000)])
+def test_quantize_nv_of_full_mantissas(rows, cols):
+    # fp32 weights. The quotient is rounded once to fp32: a value next to a tie differs from it by at least
+    # 1 / 1.875 of the quotient's last place (the scale's mantissa is at most 1.875), so it is not rounded onto it
+    x = data(rows, cols, torch.float32, rows + 3 * cols, 0.02)
+    row, col = storage(rows, cols, "nv"), storage(cols, rows, "nv")
+    mo.fp4_quantize(x, row, col)
+    check_storage(row, f64(x), "nv")
+    check_storage(col, f64(x).T, "nv")
+
+
+@pytest.mark.parametrize("e", [0, 40, 116, -30, -101, -126])   # of the tensor's scale
+def test_quantize_nv_beside_every_tie_of_every_scale(e):
+    ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5])
+    scales = ot.fp4_scale_values("nv")[1:]
+    x = np.zeros((len(scales), 48), np.float32)
+    for i, t in enumerate((ties * 2.0 ** e)[:, None] * scales[None, :]):
+        t = t.astype(np.float32)
+        for j, v in enumerate((np.nextafter(t, np.float32(0)), t, np.nextafter(t, np.float32(np.inf)))):
+            x[:, 16 * j + 1 + i] = v
+            x[:, 16 * j + 9 + i] = -v            # (columns 9 to 15)
+    x[:, ::16] = (6 * scales * 2.0 ** e).astype(np.float32)[:, None]   # fixes the block's scale
+    amax = 2688 * 2.0 ** e
+    q = storage(*x.shape, "nv")
+    mo.fp4_quantize(torch.from_numpy(x).to(dev()), q, amax=torch.tensor([amax], device=dev()))
+    check_storage(q, x.astype(np.float64), "nv", amax=amax)
