@@ -3,9 +3,11 @@
 // scale for each block of their rows, accumulated in fp32 in TMEM, rounded
 // once to the output's type.
 //
-// Scales reach the tensor core through TMEM: their 512-byte tiles arrive by
-// TMA beside the codes and are copied to TMEM columns (tcgen05.cp) in front
-// of the instructions that use them, in issue order.
+// Scales reach the tensor core through TMEM; their 512-byte tiles arrive in
+// shared memory by TMA. The narrow kernel's issuing thread copies them to TMEM
+// columns (tcgen05.cp) in front of the instructions that use them, in issue
+// order. The pair kernel's scale warps store them there from registers
+// (tcgen05.st) and hand them to the issuing thread through a barrier.
 //
 //   fp4_pair_kernel    256 x 256 tiles on CTA pairs, persistent: the large products.
 //                      8192 x 14336 x 4096: mx 165 us = 5.8 PFLOP/s at 1.88 GHz,
@@ -639,8 +641,8 @@ __global__ void __launch_bounds__(kNarrowThreads) fp4_narrow_kernel(const __grid
         for (int a = 0; a < kSfTiles<MX>; ++a) {
           const uint32_t c = tmem + uint32_t(kNarrowCols<NT> == 64 ? 32 : NT) + uint32_t(a) * 8u;
           if (left > a * kStepsPerTile<MX>) {
-            ptx::tmem_copy_scales<false>(c, ptx::smem_desc_scales(sf + 512u * uint32_t(a)));
-            ptx::tmem_copy_scales<false>(c + 4, ptx::smem_desc_scales(sf + kSfBytes<MX> + 512u * uint32_t(a)));
+            ptx::tmem_copy_scales(c, ptx::smem_desc_scales(sf + 512u * uint32_t(a)));
+            ptx::tmem_copy_scales(c + 4, ptx::smem_desc_scales(sf + kSfBytes<MX> + 512u * uint32_t(a)));
           }
         }
 #pragma unroll

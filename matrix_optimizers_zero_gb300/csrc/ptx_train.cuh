@@ -27,14 +27,9 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
 }
 
 // Copies a 512-byte scale tile from shared memory to four TMEM columns,
-// repeated in the four lane quarters. kPair: each CTA of the pair copies from
-// its own shared memory to its own TMEM; issued by the even CTA.
-template <bool kPair>
+// repeated in the four lane quarters.
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
-  if (kPair)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // D (+)= (A sA)(B sB)^T over K = 64. kMx: a scale for 32 elements (e8m0),
