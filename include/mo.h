@@ -366,6 +366,9 @@ int embed_grad(const void* dout, int32_t dout_dtype, const mo_tokens* tokens, in
  *           128 rows one after the other along k; row r, block b of a tile at
  *           byte (r % 32) 16 + (r / 32) 4 + b
  *   amax    MO_FP4_NV: one fp32, the magnitude that g comes from
+ * fp4_quantize fills the padding with zeros. Storage that a caller writes needs
+ * them too, as fp4_product reads it: codes past k, to the end of a row, are 0,
+ * and the scales of blocks past k are 0 (or any value but NaN).
  * rows and k up to 2^22, and up to 2^37 elements. */
 enum mo_fp4_format { MO_FP4_MX = 0, MO_FP4_NV = 1 };
 typedef struct {

@@ -196,7 +196,8 @@ def mo_fp4_scales_bytes(rows: int, k: int, fmt: str = "mx") -> int:
 class Fp4Tensor:
     """Storage of a microscaled 4-bit tensor [rows, k] (mo_fp4): uint8 `codes`
     and `scales` and, for "nv", a one-element fp32 `amax`. Allocated when not
-    given; reuse it every step."""
+    given; reuse it every step. Given codes and scales hold zeros in their
+    padding, as fp4_quantize leaves it: fp4_product reads it."""
 
     def __init__(self, rows: int, k: int, fmt: str = "mx", codes=None, scales=None, amax=None, device=None):
         import torch
