@@ -58,6 +58,9 @@ constexpr int64_t kZeroRowsMost = 4096;   // rows a block of launch 2 zeroes, at
 // 104 us by the cluster, 87 so, one token for all 80 and 83.) A part is a
 // block of 32 warps, one part an SM: with 1024 small parts 2^20 x 64 takes 247
 // us instead of 199, with 16 large ones 65536 x 1024 takes 94 instead of 85.
+// (152 SMs, here and in grad_grid's four blocks for each: the workspace's size is
+// computed on the host alone and results do not depend on the device, so neither
+// asks it for its count.)
 constexpr int64_t kManyTokens = 65536;
 struct SortParts {
   int64_t per_warp;   // positions, a multiple of 32
