@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutPara
 // one's row is used, so the row's address is known when its turn comes.
 // 16384 tokens of 128256 x 4096 fp32, to bf16: 63 us with distinct rows (402
 // MB, 6.4 TB/s), 46 us with the frequencies of text (254 MB), 58 us with
-// dropout, then bound by the random numbers' arithmetic. (The next row's loads
-// a step ahead in registers: 70 us, for the occupancy they cost.) Rows of less
-// than 32 groups share a warp: 2^20 tokens of 64 columns 70 us (distinct rows,
-// 403 MB, 5.8 TB/s; 155 with a warp a row), of 8 columns 12 us (112).
+// dropout, whose numbers are drawn where the loaded row is used. (The next row's
+// loads a step ahead in registers: 70 us, for the occupancy they cost.) Rows of
+// less than 32 groups share a warp: 2^20 tokens of 64 columns 72 us (distinct
+// rows, 398 MB, 5.5 TB/s; 155 with a warp a row), of 8 columns 17 us (112).
 template <typename T, typename O, bool ADD, bool DROP>
 __global__ void __launch_bounds__(256, ADD ? 4 : 5) embed_lookup_kernel(const LookupParams p) {
   const Philox rng(p.drop.rnd);
@@ -423,8 +423,9 @@ __device__ void sort_tokens(const GradParams& p, uint32_t* sm, uint32_t rank, ui
 // Many tokens: three launches a pass on all SMs instead. A block counts its
 // part's digits, a block a bin scans the parts' counts, and the blocks scatter,
 // in the same order as the cluster would. Launch 2 then writes all the zeros.
-// (The gradient of 2^20 x 64, 1000000 rows, three passes: 572 us with one
-// cluster's sort, 199 so; 2^20 x 1024, 128256 rows: 821 and 508.)
+// (The gradient of 2^20 x 64 fp32, 1000000 rows, three passes: 572 us with one
+// cluster's sort, 196 so; 2^20 x 1024 bf16, 128256 rows, two passes: 821 and 504,
+// of which the sort takes 63.)
 __global__ void __launch_bounds__(kSortThreads) radix_count_kernel(const __grid_constant__ GradParams p, int pass) {
   __shared__ uint32_t count[kMaxBins];
   ptx::griddep_launch_dependents();

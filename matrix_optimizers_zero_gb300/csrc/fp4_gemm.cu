@@ -10,14 +10,14 @@
 // (tcgen05.st) and hand them to the issuing thread through a barrier.
 //
 //   fp4_pair_kernel    256 x 256 tiles on CTA pairs, persistent: the large products.
-//                      8192 x 14336 x 4096: mx 165 us = 5.8 PFLOP/s at 1.88 GHz,
-//                      nv 184 us = 5.2 at 1.79, both under the 1.4 kW power cap;
+//                      8192 x 14336 x 4096: mx 168 us = 5.7 PFLOP/s at 1.92 GHz,
+//                      nv 185 us = 5.2 at 1.82, both under the 1.4 kW power cap;
 //                      where the cap does not bind, by the issue of instructions
-//                      (700 cycles a stage of four that take 530)
+//                      (about 720 cycles a stage of four that take 530)
 //   fp4_narrow_kernel  128 (rows of B) x NT (rows of A) tiles on single CTAs, K
 //                      split over a cluster whose CTAs add their sums through
 //                      distributed shared memory in rank order: few rows. Bound by
-//                      latencies: 1 x 14336 x 4096 nv 9 us, 33 MB
+//                      latencies: 1 x 14336 x 4096 nv 10 us, 33 MB
 #include <cuda.h>
 #include <cuda_runtime.h>
 
