@@ -281,7 +281,7 @@ int rmnp_colcut_step(const mo_matrix* shards, const int32_t* group, const float*
  * weights they write. Activations and tables are fp32 or bf16, dense
  * row-major with 16-byte aligned bases; arithmetic is fp32, rounded once. */
 
-enum mo_dtype { MO_F32 = 0, MO_BF16 = 1 };
+enum mo_dtype { MO_F32 = 0, MO_BF16 = 1, MO_MX8 = 2 /* where mo_tensor says so */ };
 
 /* Counter-based random numbers (Philox4x32-10): element i of a tensor takes
  * the 16-bit number i % 8 (low half of each word first) of the call with
@@ -408,6 +408,119 @@ int fp4_dequantize(const mo_fp4* q, void* out, int32_t dtype, cudaStream_t strea
  * format, on the tensor cores; sums in fp32, rounded once to `dtype`. One
  * launch. */
 int fp4_product(const mo_fp4* a, const mo_fp4* b, void* out, int32_t dtype, cudaStream_t stream);
+
+/* ---- the feed-forward half of a transformer layer: norm, products with
+ * everything around them in their epilogues, 8-bit activation checkpoints.
+ * Weights and activations of products are bf16, sums fp32; what is kept for
+ * the backward pass is bf16 or 8 bits. No call needs another's workspace or
+ * state; a workspace may be shared by calls in stream order. */
+
+/* A tensor [rows, k] of a call, in one of
+ *   MO_F32, MO_BF16   data: the elements, dense; scales NULL
+ *   MO_MX8            data: e4m3 codes, mo_mx8_codes_bytes() bytes in rows of
+ *                     32 ceil(k / 32); scales: mo_mx8_scales_bytes() bytes, for
+ *                     each block of 32 elements of a row the exponent + 127 of
+ *                     a power of two, rows of ceil(k / 32)
+ * data is 16-byte aligned. An element is code times scale. A block's scale is
+ * the smallest, from 2^-127 on, with which no element exceeds 448, and its
+ * codes are rounded to nearest, ties to even; a block that holds a NaN or an
+ * infinity has scale 255 and only NaN values. What writes 8-bit tensors fills
+ * the last block of a row with zeros; what reads them does not look past k. */
+typedef struct {
+  void* data;
+  void* scales;
+  int32_t dtype;
+} mo_tensor;
+
+/* Bytes of an 8-bit tensor's codes and scales (host only; 0 for invalid sizes:
+ * rows up to 2^30, k up to 2^22, up to 2^37 elements). */
+size_t mo_mx8_codes_bytes(int64_t rows, int64_t k);
+size_t mo_mx8_scales_bytes(int64_t rows, int64_t k);
+
+/* q = x [rows, k] of `dtype` in 8 bits; and back: out = the values of q (exact
+ * in either type but at the ends of its range: magnitudes from 2^128 on, which
+ * 3.3e38 rounds to, are infinite). */
+int mx8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, const mo_tensor* q, cudaStream_t stream);
+int mx8_dequantize(const mo_tensor* q, int64_t rows, int64_t k, void* out, int32_t dtype, cudaStream_t stream);
+
+/* Root-mean-square norm of the rows of s = x + residual:
+ *   y = s / sqrt(mean(s^2) + eps) * weight
+ * x, residual (or NULL) and sum (s is stored there; or NULL) have `dtype`; y
+ * goes to out (`out_dtype`), to out8 in 8 bits, or to both; either may be NULL.
+ * weight is fp32 [dim], or NULL for ones. s is not rounded in between. sum and
+ * out may each be x or residual itself. rows up to 2^30, dim up to 2^22. */
+int rms_norm(const void* x, const void* residual, int32_t dtype, int64_t rows, int64_t dim, const float* weight, float eps,
+             void* sum, void* out, int32_t out_dtype, const mo_tensor* out8, cudaStream_t stream);
+
+/* Gradients of rms_norm in s and in the weight, from dy and s itself (x: of
+ * dy's type, or 8 bits). With r = 1 / sqrt(mean(s^2) + eps), n = s r, g = dy weight:
+ *   dx = r (g - n mean(g n)) + dresidual,   dweight (+)= sum over rows of dy n
+ * dresidual (the gradient that passes the norm by) and dweight may be NULL; dx
+ * may be dy or dresidual itself. With accumulate = 1 dweight, the fp32 g of
+ * adamw_tail_step, is added to. Sums over rows are taken in a fixed order. ws:
+ * mo_rms_norm_grad_workspace_bytes() bytes, 256-byte aligned (not used without
+ * dweight). */
+size_t mo_rms_norm_grad_workspace_bytes(int64_t rows, int64_t dim);
+int rms_norm_grad(const void* dy, int32_t dtype, const mo_tensor* x, int64_t rows, int64_t dim, const float* weight,
+                  float eps, const void* dresidual, void* dx, float* dweight, int32_t accumulate, void* ws,
+                  size_t ws_bytes, cudaStream_t stream);
+
+/* Activations. GELU: x Phi(x); GELU_TANH: its approximation
+ * 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))). */
+enum mo_activation { MO_ACT_NONE = 0, MO_ACT_RELU = 1, MO_ACT_GELU = 2, MO_ACT_GELU_TANH = 3, MO_ACT_SILU = 4 };
+
+/* z = x w^T + bias, out = act(z) + residual, in one launch.
+ *   x [tokens, cols] bf16 or 8 bits; w bf16 [rows, cols]; bias fp32 [rows] or
+ *   NULL; residual (or NULL) and out [tokens, rows] of `out_dtype`, out may be
+ *   residual itself; pre (or NULL; with an activation only): receives z
+ *   [tokens, rows] for the backward pass, in bf16 or 8 bits
+ * tokens up to 2^30, cols up to 2^16, rows up to 2^22. ws: device scratch of
+ * mo_linear_workspace_bytes(.., 0) bytes, 256-byte aligned: 8-bit operands, and
+ * operands whose rows are no multiple of 8, are laid out there first. */
+size_t mo_linear_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t grad);
+int linear_forward(const mo_tensor* x, const void* w, int64_t tokens, int64_t cols, int64_t rows, const float* bias,
+                   int32_t act, const void* residual, const mo_tensor* pre, void* out, int32_t out_dtype, void* ws,
+                   size_t ws_bytes, cudaStream_t stream);
+
+/* Gradients of linear_forward, from dout bf16 [tokens, rows] and, with an
+ * activation, the kept pre (and x, as it was given or in 8 bits):
+ *   dz = dout act'(pre),  dx = dz w,  dw (+)= dz^T x,  dbias (+)= sum over tokens of dz
+ * dx [tokens, cols], dw [rows, cols] in their types, dbias fp32 [rows]; each
+ * may be NULL, and x and w where nothing needs them. (The residual's gradient
+ * is dout.) dz is rounded to bf16 for the products, not for dbias. With
+ * accumulate = 1 dw and dbias are added to. Sums over more than 32768 tokens
+ * (or, for dx, rows) are taken in slices of as many, joined in fp32. ws:
+ * mo_linear_workspace_bytes(.., 1) bytes, 256-byte aligned. */
+int linear_grad(const void* dout, const mo_tensor* x, const void* w, int64_t tokens, int64_t cols, int64_t rows,
+                int32_t act, const mo_tensor* pre, void* dx, int32_t dx_dtype, void* dw, int32_t dw_dtype, float* dbias,
+                int32_t accumulate, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Gated feed-forward block: g = x w_gate^T, u = x w_up^T, h = act(g) u,
+ * out = h w_down^T + residual, in two launches (g, u and h in one; h, in bf16,
+ * is in the workspace).
+ *   x [tokens, dim] bf16 or 8 bits; w_gate, w_up bf16 [inner, dim], w_down bf16
+ *   [dim, inner]; residual (or NULL) and out [tokens, dim] of `out_dtype`, out
+ *   may be residual itself; gate, up (both or neither, of one type): receive g
+ *   and u [tokens, inner] for the backward pass, in bf16 or 8 bits
+ * tokens up to 2^30, dim up to 2^16, inner up to 2^15. */
+size_t mo_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t inner, int32_t grad);
+int gated_ffn_forward(const mo_tensor* x, const void* w_gate, const void* w_up, const void* w_down, int64_t tokens,
+                      int64_t dim, int64_t inner, int32_t act, const void* residual, const mo_tensor* gate,
+                      const mo_tensor* up, void* out, int32_t out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Its gradients, from dout bf16 [tokens, dim] and the kept gate and up; h is
+ * computed again from them:
+ *   dh = dout w_down,  dg = dh u act'(g),  du = dh act(g)
+ *   dx = dg w_gate + du w_up,  dw_gate (+)= dg^T x,  dw_up (+)= du^T x,
+ *   dw_down (+)= dout^T h
+ * dx and the weights' gradients (of one type, dw_dtype) may each be NULL, x
+ * where no gradient needs it. dg, du and h are rounded to bf16 for the
+ * products. With accumulate = 1 the weights' gradients are added to. ws:
+ * mo_gated_ffn_workspace_bytes(.., 1) bytes, 256-byte aligned. */
+int gated_ffn_grad(const void* dout, const mo_tensor* x, const mo_tensor* gate, const mo_tensor* up, const void* w_gate,
+                   const void* w_up, const void* w_down, int64_t tokens, int64_t dim, int64_t inner, int32_t act,
+                   void* dx, int32_t dx_dtype, void* dw_gate, void* dw_up, void* dw_down, int32_t dw_dtype,
+                   int32_t accumulate, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Synchronises `stream`, then returns and clears the device-side status word:
  * MO_OK, MO_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel expired

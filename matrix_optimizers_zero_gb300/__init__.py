@@ -40,6 +40,10 @@ __all__ = [
     "Random", "Dropout", "dropout_apply", "embed_lookup", "embed_grad", "embed_grad_workspace",
     "mo_embed_grad_workspace_bytes", "Fp4Tensor", "fp4_quantize", "fp4_dequantize", "fp4_product",
     "mo_fp4_codes_bytes", "mo_fp4_scales_bytes",
+    "Mx8Tensor", "mx8_quantize", "mx8_dequantize", "mo_mx8_codes_bytes", "mo_mx8_scales_bytes",
+    "rms_norm", "rms_norm_grad", "rms_norm_grad_workspace", "mo_rms_norm_grad_workspace_bytes",
+    "linear", "linear_grad", "linear_workspace", "mo_linear_workspace_bytes",
+    "gated_ffn", "gated_ffn_grad", "gated_ffn_workspace", "mo_gated_ffn_workspace_bytes",
 ]
 
 MO_OK = 0
@@ -159,6 +163,19 @@ def load_library() -> ctypes.CDLL:
         "fp4_dequantize": (ctypes.c_int, [P, P, I32, P]),
         "fp4_product": (ctypes.c_int, [P, P, P, I32, P]),
         "embed_grad": (ctypes.c_int, [P, I32, P, I64, I64, ctypes.c_float, P, P, I32, P, SZ, P]),
+        "mo_mx8_codes_bytes": (SZ, [I64, I64]),
+        "mo_mx8_scales_bytes": (SZ, [I64, I64]),
+        "mx8_quantize": (ctypes.c_int, [P, I32, I64, I64, P, P]),
+        "mx8_dequantize": (ctypes.c_int, [P, I64, I64, P, I32, P]),
+        "rms_norm": (ctypes.c_int, [P, P, I32, I64, I64, P, ctypes.c_float, P, P, I32, P, P]),
+        "mo_rms_norm_grad_workspace_bytes": (SZ, [I64, I64]),
+        "rms_norm_grad": (ctypes.c_int, [P, I32, P, I64, I64, P, ctypes.c_float, P, P, P, I32, P, SZ, P]),
+        "mo_linear_workspace_bytes": (SZ, [I64, I64, I64, I32]),
+        "linear_forward": (ctypes.c_int, [P, P, I64, I64, I64, P, I32, P, P, P, I32, P, SZ, P]),
+        "linear_grad": (ctypes.c_int, [P, P, P, I64, I64, I64, I32, P, P, I32, P, I32, P, I32, P, SZ, P]),
+        "mo_gated_ffn_workspace_bytes": (SZ, [I64, I64, I64, I32]),
+        "gated_ffn_forward": (ctypes.c_int, [P, P, P, P, I64, I64, I64, I32, P, P, P, P, I32, P, SZ, P]),
+        "gated_ffn_grad": (ctypes.c_int, [P, P, P, P, P, P, P, I64, I64, I64, I32, P, I32, P, P, P, I32, I32, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -488,3 +505,7 @@ def mo_plan_owners(roles: Sequence[Tuple[int, int, int]], world: int, strategy: 
 from .train_ops import (  # noqa: E402  (uses the binding above)
     Dropout, Fp4Tensor, Random, dropout_apply, embed_grad, embed_grad_workspace, embed_lookup, fp4_dequantize, fp4_product,
     fp4_quantize, mo_embed_grad_workspace_bytes, mo_fp4_codes_bytes, mo_fp4_scales_bytes)
+from .layer_ops import (  # noqa: E402
+    Mx8Tensor, gated_ffn, gated_ffn_grad, gated_ffn_workspace, linear, linear_grad, linear_workspace,
+    mo_gated_ffn_workspace_bytes, mo_linear_workspace_bytes, mo_mx8_codes_bytes, mo_mx8_scales_bytes,
+    mo_rms_norm_grad_workspace_bytes, mx8_dequantize, mx8_quantize, rms_norm, rms_norm_grad, rms_norm_grad_workspace)

@@ -1,0 +1,647 @@
+// extern "C" entry points of the feed-forward operators (include/mo.h):
+// argument checks, workspace layout, launches. No entry point allocates device
+// memory or synchronises.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <initializer_list>
+
+#include "layer_kernels.h"
+#include "mo.h"
+
+namespace {
+
+using mo::Kept;
+using mo::Operand;
+using mo::padded;
+using mo::report_cuda;
+
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxWidth = int64_t(1) << 22;
+constexpr int64_t kMaxElems = int64_t(1) << 37;
+constexpr int64_t kMaxReduction = int64_t(1) << 16;   // of one accumulation
+// Longer sums over tokens or rows are taken in slices of as many: over one very
+// long reduction the tensor core's accumulator loses products far below the
+// running sum (as the Newton-Schulz Gram products do).
+constexpr int64_t kSlice = 32768;
+
+bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+bool plain_dtype(int32_t d) { return d == MO_F32 || d == MO_BF16; }
+size_t bytes_of(int32_t d) { return d == MO_BF16 ? 2 : 4; }
+size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+int matrix_shape(int64_t rows, int64_t k) {
+  if (rows < 0 || rows > kMaxTokens || k <= 0 || k > kMaxWidth) return MO_ERR_BAD_SHAPE;
+  return rows > 0 && mo::mx8_blocks(k) * 32 > kMaxElems / rows ? MO_ERR_BAD_SHAPE : MO_OK;
+}
+
+// Memory that a call touches; a range that is written may overlap no other, but
+// be one that it was given to replace.
+struct Range {
+  const void* p;
+  size_t bytes;
+  bool written;
+  const void* in_place[2];   // ranges that may begin at the same place
+};
+struct Ranges {
+  Range r[24];
+  int n = 0;
+  void add(const void* p, size_t bytes, bool written, const void* same0 = nullptr, const void* same1 = nullptr) {
+    if (p != nullptr && bytes > 0) r[n++] = {p, bytes, written, {same0, same1}};
+  }
+  void reads(const void* p, size_t bytes) { add(p, bytes, false); }
+  void writes(const void* p, size_t bytes, const void* same0 = nullptr, const void* same1 = nullptr) { add(p, bytes, true, same0, same1); }
+  void kept(const mo_tensor* t, int64_t rows, int64_t k, bool written) {
+    if (t == nullptr) return;
+    if (t->dtype == MO_MX8) {
+      add(t->data, size_t(rows) * size_t(mo::mx8_blocks(k)) * 32, written);
+      add(t->scales, size_t(rows) * size_t(mo::mx8_blocks(k)), written);
+    } else {
+      add(t->data, size_t(rows) * size_t(k) * bytes_of(t->dtype), written);
+    }
+  }
+  int check() const {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < n; ++j) {
+        if (i == j || !r[i].written) continue;
+        const uintptr_t x = reinterpret_cast<uintptr_t>(r[i].p), y = reinterpret_cast<uintptr_t>(r[j].p);
+        if (!(x < y + r[j].bytes && y < x + r[i].bytes)) continue;
+        const bool same = x == y && r[i].bytes == r[j].bytes && !r[j].written && (r[i].in_place[0] == r[j].p || r[i].in_place[1] == r[j].p);
+        if (!same) return MO_ERR_OVERLAP;
+      }
+    return MO_OK;
+  }
+};
+
+// A tensor of a call, of bf16 or 8 bits (or fp32 where `f32` allows it).
+int kept_args(const mo_tensor* t, bool f32, Kept* out) {
+  if (t->dtype != MO_MX8 && t->dtype != MO_BF16 && !(f32 && t->dtype == MO_F32)) return MO_ERR_BAD_PARAM;
+  if (t->data == nullptr || (t->dtype == MO_MX8 && t->scales == nullptr)) return MO_ERR_NULL_POINTER;
+  if (misaligned(t->data, 16)) return MO_ERR_MISALIGNED;
+  out->data = t->data;
+  out->scales = static_cast<uint8_t*>(t->scales);
+  out->dtype = t->dtype;
+  return MO_OK;
+}
+
+struct Workspace {
+  uint8_t* base;
+  size_t at = 0;
+  void* take(size_t bytes) {
+    void* p = base + at;
+    at += align256(bytes);
+    return p;
+  }
+};
+
+// Runs launches until one fails.
+struct Launches {
+  cudaError_t error = cudaSuccess;
+  void operator()(cudaError_t e) {
+    if (error == cudaSuccess) error = e;
+  }
+  int status() const { return error == cudaSuccess ? MO_OK : report_cuda(error); }
+};
+
+// A bf16 operand [rows, cols] that TMA can read: rows of a multiple of 16
+// bytes, or else (and from 8 bits) laid out in the workspace.
+bool needs_copy(int64_t cols, int32_t dtype) { return dtype == MO_MX8 || cols % 8 != 0; }
+size_t copy_bytes(int64_t rows, int64_t cols) { return align256(size_t(rows) * size_t(padded(cols)) * 2); }
+
+Operand operand(const Kept& t, int64_t rows, int64_t cols, Workspace& ws, Launches& run, cudaStream_t stream) {
+  if (!needs_copy(cols, t.dtype)) return {t.data, rows, cols, cols};
+  void* copy = ws.take(size_t(rows) * size_t(padded(cols)) * 2);
+  if (run.error == cudaSuccess) run(mo::launch_unpack(t, rows, cols, copy, true, padded(cols), stream));
+  return {copy, rows, cols, padded(cols)};
+}
+Operand operand(const void* p, int64_t rows, int64_t cols, Workspace& ws, Launches& run, cudaStream_t stream) {
+  Kept t;
+  t.data = const_cast<void*>(p);
+  return operand(t, rows, cols, ws, run, stream);
+}
+
+// Bytes of the partial sums of a product whose reduction is cut.
+size_t slice_bytes(int64_t k, int64_t m, int64_t n) { return k > kSlice ? align256(size_t(m) * size_t(n) * 4) : 0; }
+
+// A product without activation whose reduction runs over the rows of both
+// operands (or, without a_mn, of the second alone), in slices where it is long:
+// the first slices' sums go to `part` in fp32, each on top of the last one's.
+void sliced_product(const mo::Product& whole, float* part, int sms, int* status, Launches& run, cudaStream_t stream) {
+  const int64_t slices = (whole.k + kSlice - 1) / kSlice;
+  for (int64_t s = 0; s < slices && run.error == cudaSuccess; ++s) {
+    mo::Product q = whole;
+    const int64_t k0 = s * kSlice;
+    q.k = std::min(kSlice, whole.k - k0);
+    float* sums = part;
+    for (int i = 0; i < q.count; ++i) {
+      if (slices > 1) {
+        auto cut_rows = [&](Operand& o) {
+          o.p = static_cast<const uint16_t*>(o.p) + k0 * o.ld;
+          o.rows = q.k;
+        };
+        cut_rows(q.b[i]);
+        if (q.a_mn) {
+          cut_rows(q.a[i]);
+        } else {
+          q.a[i].p = static_cast<const uint16_t*>(q.a[i].p) + k0;
+          q.a[i].cols = q.k;
+        }
+        mo::Target& t = q.t[i];
+        if (s > 0) t.add = sums, t.add_ld = t.n, t.add_bf16 = 0;
+        if (s + 1 < slices) t.out = sums, t.ld = t.n, t.out_bf16 = 0;
+        sums += align256(size_t(t.m) * size_t(t.n) * 4) / 4;
+      }
+    }
+    run(mo::launch_product(q, sms, status, stream));
+  }
+}
+
+mo::Target target(void* out, int32_t dtype, int64_t m, int64_t n, const void* add = nullptr) {
+  return {out, add, m, n, n, n, dtype == MO_BF16, dtype == MO_BF16};
+}
+
+int clear(void* p, size_t bytes, cudaStream_t stream) {
+  const cudaError_t e = cudaMemsetAsync(p, 0, bytes, stream);
+  return e != cudaSuccess ? report_cuda(e) : MO_OK;
+}
+
+bool known_act(int32_t act) { return act >= MO_ACT_NONE && act <= MO_ACT_SILU; }
+
+int linear_shape(int64_t tokens, int64_t cols, int64_t rows) {
+  if (tokens < 0 || tokens > kMaxTokens || cols <= 0 || cols > kMaxReduction || rows <= 0 || rows > kMaxWidth) return MO_ERR_BAD_SHAPE;
+  const int64_t most = std::max(padded(cols), padded(rows));
+  return tokens > 0 && most > kMaxElems / tokens ? MO_ERR_BAD_SHAPE : MO_OK;
+}
+
+int ffn_shape(int64_t tokens, int64_t dim, int64_t inner) {
+  if (tokens < 0 || tokens > kMaxTokens || dim <= 0 || dim > kMaxReduction || inner <= 0 || inner > kMaxReduction / 2)
+    return MO_ERR_BAD_SHAPE;
+  const int64_t most = std::max(padded(dim), padded(inner));
+  return tokens > 0 && most > kMaxElems / tokens ? MO_ERR_BAD_SHAPE : MO_OK;
+}
+
+size_t linear_bytes(int64_t tokens, int64_t cols, int64_t rows, bool grad) {
+  size_t b = copy_bytes(tokens, cols) + (cols % 8 != 0 ? copy_bytes(rows, cols) : 0);
+  if (grad) {
+    b += copy_bytes(tokens, rows);   // dz
+    const int64_t per = mo::act_grad_per(tokens, rows);
+    b += align256(size_t((tokens + per - 1) / per) * size_t(rows) * 4);
+    b += std::max(slice_bytes(tokens, rows, cols), slice_bytes(rows, tokens, cols));
+  }
+  return std::max<size_t>(b, 256);
+}
+
+size_t ffn_bytes(int64_t tokens, int64_t dim, int64_t inner, bool grad) {
+  size_t b = copy_bytes(tokens, dim) + copy_bytes(tokens, inner);   // x, h
+  if (dim % 8 != 0) b += 2 * copy_bytes(inner, dim);
+  if (inner % 8 != 0) b += copy_bytes(dim, inner);
+  if (grad) {
+    b += 2 * copy_bytes(tokens, inner);   // dg, du
+    if (dim % 8 != 0) b += copy_bytes(tokens, dim);   // dout
+    b += 3 * slice_bytes(tokens, inner, dim);
+  }
+  return std::max<size_t>(b, 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mo_mx8_codes_bytes(int64_t rows, int64_t k) {
+  return matrix_shape(rows, k) == MO_OK ? size_t(rows) * size_t(mo::mx8_blocks(k)) * 32 : 0;
+}
+
+size_t mo_mx8_scales_bytes(int64_t rows, int64_t k) {
+  return matrix_shape(rows, k) == MO_OK ? size_t(rows) * size_t(mo::mx8_blocks(k)) : 0;
+}
+
+int mx8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, const mo_tensor* q, cudaStream_t stream) {
+  if (q == nullptr) return MO_ERR_NULL_POINTER;
+  if (!plain_dtype(dtype) || q->dtype != MO_MX8) return MO_ERR_BAD_PARAM;
+  int st = matrix_shape(rows, k);
+  if (st != MO_OK) return st;
+  if (rows == 0) return MO_OK;
+  Kept to;
+  if (x == nullptr) return MO_ERR_NULL_POINTER;
+  if ((st = kept_args(q, false, &to)) != MO_OK) return st;
+  if (misaligned(x, 16)) return MO_ERR_MISALIGNED;
+  Ranges mem;
+  mem.reads(x, size_t(rows) * size_t(k) * bytes_of(dtype));
+  mem.kept(q, rows, k, true);
+  if ((st = mem.check()) != MO_OK) return st;
+  int sms = 0;
+  int* status = nullptr;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  Launches run;
+  run(mo::launch_mx8_quantize(x, dtype == MO_BF16, rows, k, to, stream));
+  return run.status();
+}
+
+int mx8_dequantize(const mo_tensor* q, int64_t rows, int64_t k, void* out, int32_t dtype, cudaStream_t stream) {
+  if (q == nullptr) return MO_ERR_NULL_POINTER;
+  if (!plain_dtype(dtype) || q->dtype != MO_MX8) return MO_ERR_BAD_PARAM;
+  int st = matrix_shape(rows, k);
+  if (st != MO_OK) return st;
+  if (rows == 0) return MO_OK;
+  Kept from;
+  if (out == nullptr) return MO_ERR_NULL_POINTER;
+  if ((st = kept_args(q, false, &from)) != MO_OK) return st;
+  if (misaligned(out, 16)) return MO_ERR_MISALIGNED;
+  Ranges mem;
+  mem.writes(out, size_t(rows) * size_t(k) * bytes_of(dtype));
+  mem.kept(q, rows, k, false);
+  if ((st = mem.check()) != MO_OK) return st;
+  int sms = 0;
+  int* status = nullptr;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  Launches run;
+  run(mo::launch_unpack(from, rows, k, out, dtype == MO_BF16, k, stream));
+  return run.status();
+}
+
+int rms_norm(const void* x, const void* residual, int32_t dtype, int64_t rows, int64_t dim, const float* weight, float eps,
+             void* sum, void* out, int32_t out_dtype, const mo_tensor* out8, cudaStream_t stream) {
+  if (!plain_dtype(dtype) || (out != nullptr && !plain_dtype(out_dtype)) || (out8 != nullptr && out8->dtype != MO_MX8) ||
+      !(eps >= 0.0f) || !std::isfinite(eps))
+    return MO_ERR_BAD_PARAM;
+  int st = matrix_shape(rows, dim);
+  if (st != MO_OK) return st;
+  if (rows == 0) return MO_OK;
+  if (x == nullptr || (out == nullptr && out8 == nullptr)) return MO_ERR_NULL_POINTER;
+  mo::NormParams p = {};
+  if (out8 != nullptr && (st = kept_args(out8, false, &p.out8)) != MO_OK) return st;
+  for (const void* q : {x, residual, static_cast<const void*>(weight), static_cast<const void*>(sum), static_cast<const void*>(out)})
+    if (misaligned(q, 16)) return MO_ERR_MISALIGNED;
+  const size_t n = size_t(rows) * size_t(dim);
+  Ranges mem;
+  mem.reads(x, n * bytes_of(dtype));
+  mem.reads(residual, n * bytes_of(dtype));
+  mem.reads(weight, size_t(dim) * 4);
+  mem.writes(sum, n * bytes_of(dtype), x, residual);
+  mem.writes(out, n * bytes_of(out_dtype), x, residual);
+  mem.kept(out8, rows, dim, true);
+  if ((st = mem.check()) != MO_OK) return st;
+  int sms = 0;
+  int* status = nullptr;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  p.x = x;
+  p.residual = residual;
+  p.weight = weight;
+  p.sum = sum;
+  p.out = out;
+  p.rows = rows;
+  p.dim = dim;
+  p.eps = eps;
+  p.out_bf16 = out_dtype == MO_BF16;
+  Launches run;
+  run(mo::launch_rms_norm(p, dtype == MO_BF16, stream));
+  return run.status();
+}
+
+size_t mo_rms_norm_grad_workspace_bytes(int64_t rows, int64_t dim) {
+  if (matrix_shape(rows, dim) != MO_OK) return 0;
+  return std::max<size_t>(256, rows == 0 ? 0 : align256(size_t(mo::norm_parts(rows, dim)) * size_t(dim) * 4));
+}
+
+int rms_norm_grad(const void* dy, int32_t dtype, const mo_tensor* x, int64_t rows, int64_t dim, const float* weight,
+                  float eps, const void* dresidual, void* dx, float* dweight, int32_t accumulate, void* ws,
+                  size_t ws_bytes, cudaStream_t stream) {
+  if (!plain_dtype(dtype) || !(eps >= 0.0f) || !std::isfinite(eps) || (accumulate != 0 && accumulate != 1)) return MO_ERR_BAD_PARAM;
+  int st = matrix_shape(rows, dim);
+  if (st != MO_OK) return st;
+  if (misaligned(dweight, 16)) return MO_ERR_MISALIGNED;
+  int sms = 0;
+  int* status = nullptr;
+  if (rows == 0) {   // the sum over no rows
+    if (dweight == nullptr || accumulate) return MO_OK;
+    if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+    return clear(dweight, size_t(dim) * 4, stream);
+  }
+  if (dy == nullptr || x == nullptr || dx == nullptr) return MO_ERR_NULL_POINTER;
+  mo::NormGradParams p = {};
+  if ((st = kept_args(x, true, &p.x)) != MO_OK) return st;
+  if (x->dtype != MO_MX8 && x->dtype != dtype) return MO_ERR_BAD_PARAM;
+  for (const void* q : {dy, static_cast<const void*>(weight), dresidual, static_cast<const void*>(dx)})
+    if (misaligned(q, 16)) return MO_ERR_MISALIGNED;
+  const size_t n = size_t(rows) * size_t(dim) * bytes_of(dtype);
+  const size_t need = dweight != nullptr ? mo_rms_norm_grad_workspace_bytes(rows, dim) : 0;
+  if (dweight != nullptr) {
+    if (ws == nullptr) return MO_ERR_NULL_POINTER;
+    if (misaligned(ws, 256)) return MO_ERR_MISALIGNED;
+    if (ws_bytes < need) return MO_ERR_WORKSPACE_TOO_SMALL;
+  }
+  Ranges mem;
+  mem.reads(dy, n);
+  mem.kept(x, rows, dim, false);
+  mem.reads(weight, size_t(dim) * 4);
+  mem.reads(dresidual, n);
+  mem.writes(dx, n, dy, dresidual);
+  mem.writes(dweight, size_t(dim) * 4);
+  mem.writes(ws, need);
+  if ((st = mem.check()) != MO_OK) return st;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  p.dy = dy;
+  p.weight = weight;
+  p.dres = dresidual;
+  p.dx = dx;
+  p.part = dweight != nullptr ? static_cast<float*>(ws) : nullptr;
+  p.rows = rows;
+  p.dim = dim;
+  p.eps = eps;
+  Launches run;
+  run(mo::launch_rms_norm_grad(p, dtype == MO_BF16, stream));
+  if (dweight != nullptr && run.error == cudaSuccess)
+    run(mo::launch_join(p.part, mo::norm_parts(rows, dim), dim, dweight, accumulate != 0, stream));
+  return run.status();
+}
+
+size_t mo_linear_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t grad) {
+  if (linear_shape(tokens, cols, rows) != MO_OK || (grad != 0 && grad != 1)) return 0;
+  return linear_bytes(tokens, cols, rows, grad != 0);
+}
+
+int linear_forward(const mo_tensor* x, const void* w, int64_t tokens, int64_t cols, int64_t rows, const float* bias,
+                   int32_t act, const void* residual, const mo_tensor* pre, void* out, int32_t out_dtype, void* ws,
+                   size_t ws_bytes, cudaStream_t stream) {
+  if (!known_act(act) || !plain_dtype(out_dtype) || (pre != nullptr && act == MO_ACT_NONE)) return MO_ERR_BAD_PARAM;
+  int st = linear_shape(tokens, cols, rows);
+  if (st != MO_OK) return st;
+  if (tokens == 0) return MO_OK;
+  if (x == nullptr || w == nullptr || out == nullptr || ws == nullptr) return MO_ERR_NULL_POINTER;
+  Kept xk;
+  mo::Product q;
+  if ((st = kept_args(x, false, &xk)) != MO_OK) return st;
+  if (pre != nullptr && (st = kept_args(pre, false, &q.pre)) != MO_OK) return st;
+  for (const void* p : {w, static_cast<const void*>(bias), residual, static_cast<const void*>(out)})
+    if (misaligned(p, 16)) return MO_ERR_MISALIGNED;
+  if (misaligned(ws, 256)) return MO_ERR_MISALIGNED;
+  const size_t need = linear_bytes(tokens, cols, rows, false), out_bytes = size_t(tokens) * size_t(rows) * bytes_of(out_dtype);
+  if (ws_bytes < need) return MO_ERR_WORKSPACE_TOO_SMALL;
+  Ranges mem;
+  mem.kept(x, tokens, cols, false);
+  mem.reads(w, size_t(rows) * size_t(cols) * 2);
+  mem.reads(bias, size_t(rows) * 4);
+  mem.reads(residual, out_bytes);
+  mem.kept(pre, tokens, rows, true);
+  mem.writes(out, out_bytes, residual);
+  mem.writes(ws, need);
+  if ((st = mem.check()) != MO_OK) return st;
+  int sms = 0;
+  int* status = nullptr;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  Workspace space{static_cast<uint8_t*>(ws)};
+  Launches run;
+  q.act = act;
+  q.a[0] = operand(xk, tokens, cols, space, run, stream);
+  q.b[0] = operand(w, rows, cols, space, run, stream);
+  q.t[0] = target(out, out_dtype, tokens, rows, residual);
+  q.k = cols;
+  q.bias = bias;
+  if (run.error == cudaSuccess) run(mo::launch_product(q, sms, status, stream));
+  return run.status();
+}
+
+int linear_grad(const void* dout, const mo_tensor* x, const void* w, int64_t tokens, int64_t cols, int64_t rows,
+                int32_t act, const mo_tensor* pre, void* dx, int32_t dx_dtype, void* dw, int32_t dw_dtype, float* dbias,
+                int32_t accumulate, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!known_act(act) || (dx != nullptr && !plain_dtype(dx_dtype)) || (dw != nullptr && !plain_dtype(dw_dtype)) ||
+      (accumulate != 0 && accumulate != 1) || (pre != nullptr && act == MO_ACT_NONE))
+    return MO_ERR_BAD_PARAM;
+  int st = linear_shape(tokens, cols, rows);
+  if (st != MO_OK) return st;
+  if (tokens > 0 && dx == nullptr && dw == nullptr && dbias == nullptr) return MO_ERR_NULL_POINTER;
+  for (const void* p : {static_cast<const void*>(dx), static_cast<const void*>(dw), static_cast<const void*>(dbias)})
+    if (misaligned(p, 16)) return MO_ERR_MISALIGNED;
+  int sms = 0;
+  int* status = nullptr;
+  const size_t dw_bytes = size_t(rows) * size_t(cols) * bytes_of(dw_dtype);
+  if (tokens == 0) {   // sums over no tokens
+    if (accumulate || (dw == nullptr && dbias == nullptr)) return MO_OK;
+    if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+    if (dw != nullptr && (st = clear(dw, dw_bytes, stream)) != MO_OK) return st;
+    return dbias != nullptr ? clear(dbias, size_t(rows) * 4, stream) : MO_OK;
+  }
+  if (dout == nullptr || ws == nullptr || (dw != nullptr && x == nullptr) || (dx != nullptr && w == nullptr) ||
+      (act != MO_ACT_NONE && pre == nullptr))
+    return MO_ERR_NULL_POINTER;
+  Kept xk;
+  mo::ActGradParams g = {};
+  if (dw != nullptr && (st = kept_args(x, false, &xk)) != MO_OK) return st;
+  if (pre != nullptr && (st = kept_args(pre, false, &g.pre)) != MO_OK) return st;
+  if (misaligned(dout, 16) || misaligned(dx != nullptr ? w : nullptr, 16) || misaligned(ws, 256)) return MO_ERR_MISALIGNED;
+  const size_t need = linear_bytes(tokens, cols, rows, true);
+  if (ws_bytes < need) return MO_ERR_WORKSPACE_TOO_SMALL;
+  Ranges mem;
+  mem.reads(dout, size_t(tokens) * size_t(rows) * 2);
+  if (dw != nullptr) mem.kept(x, tokens, cols, false);
+  if (dx != nullptr) mem.reads(w, size_t(rows) * size_t(cols) * 2);
+  mem.kept(pre, tokens, rows, false);
+  mem.writes(dx, size_t(tokens) * size_t(cols) * bytes_of(dx_dtype));
+  mem.writes(dw, dw_bytes);
+  mem.writes(dbias, size_t(rows) * 4);
+  mem.writes(ws, need);
+  if ((st = mem.check()) != MO_OK) return st;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  Workspace space{static_cast<uint8_t*>(ws)};
+  Launches run;
+  // dz, and its sums over tokens
+  Operand dz = {dout, tokens, rows, rows};
+  const bool products = dx != nullptr || dw != nullptr;
+  g.dout = static_cast<const uint16_t*>(dout);
+  g.tokens = tokens;
+  g.rows = rows;
+  g.act = act;
+  g.per = mo::act_grad_per(tokens, rows);
+  if (products && (act != MO_ACT_NONE || rows % 8 != 0)) {
+    g.ld = padded(rows);
+    g.dz = static_cast<uint16_t*>(space.take(size_t(tokens) * size_t(g.ld) * 2));
+    dz = {g.dz, tokens, rows, g.ld};
+  }
+  const int64_t parts = (tokens + g.per - 1) / g.per;
+  if (dbias != nullptr) g.part = static_cast<float*>(space.take(size_t(parts) * size_t(rows) * 4));
+  if (g.dz != nullptr || g.part != nullptr) run(mo::launch_act_grad(g, stream));
+  if (dbias != nullptr && run.error == cudaSuccess) run(mo::launch_join(g.part, parts, rows, dbias, accumulate != 0, stream));
+  const Operand xo = dw != nullptr ? operand(xk, tokens, cols, space, run, stream) : Operand{};
+  const Operand wo = dx != nullptr ? operand(w, rows, cols, space, run, stream) : Operand{};
+  float* part = reinterpret_cast<float*>(space.take(0));
+  if (dx != nullptr) {
+    mo::Product q;
+    q.b_mn = true;
+    q.a[0] = dz;
+    q.b[0] = wo;
+    q.t[0] = target(dx, dx_dtype, tokens, cols);
+    q.k = rows;
+    sliced_product(q, part, sms, status, run, stream);
+  }
+  if (dw != nullptr) {
+    mo::Product q;
+    q.a_mn = q.b_mn = true;
+    q.a[0] = dz;
+    q.b[0] = xo;
+    q.t[0] = target(dw, dw_dtype, rows, cols, accumulate ? dw : nullptr);
+    q.k = tokens;
+    sliced_product(q, part, sms, status, run, stream);
+  }
+  return run.status();
+}
+
+size_t mo_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t inner, int32_t grad) {
+  if (ffn_shape(tokens, dim, inner) != MO_OK || (grad != 0 && grad != 1)) return 0;
+  return ffn_bytes(tokens, dim, inner, grad != 0);
+}
+
+int gated_ffn_forward(const mo_tensor* x, const void* w_gate, const void* w_up, const void* w_down, int64_t tokens,
+                      int64_t dim, int64_t inner, int32_t act, const void* residual, const mo_tensor* gate,
+                      const mo_tensor* up, void* out, int32_t out_dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!known_act(act) || !plain_dtype(out_dtype)) return MO_ERR_BAD_PARAM;
+  int st = ffn_shape(tokens, dim, inner);
+  if (st != MO_OK) return st;
+  if ((gate == nullptr) != (up == nullptr)) return MO_ERR_NULL_POINTER;
+  if (tokens == 0) return MO_OK;
+  if (x == nullptr || w_gate == nullptr || w_up == nullptr || w_down == nullptr || out == nullptr || ws == nullptr)
+    return MO_ERR_NULL_POINTER;
+  Kept xk;
+  mo::Product q;
+  if ((st = kept_args(x, false, &xk)) != MO_OK) return st;
+  if (gate != nullptr) {
+    if ((st = kept_args(gate, false, &q.pre)) != MO_OK || (st = kept_args(up, false, &q.pre2)) != MO_OK) return st;
+    if (gate->dtype != up->dtype) return MO_ERR_BAD_PARAM;
+  }
+  for (const void* p : {w_gate, w_up, w_down, residual, static_cast<const void*>(out)})
+    if (misaligned(p, 16)) return MO_ERR_MISALIGNED;
+  if (misaligned(ws, 256)) return MO_ERR_MISALIGNED;
+  const size_t need = ffn_bytes(tokens, dim, inner, false), out_bytes = size_t(tokens) * size_t(dim) * bytes_of(out_dtype);
+  if (ws_bytes < need) return MO_ERR_WORKSPACE_TOO_SMALL;
+  Ranges mem;
+  mem.kept(x, tokens, dim, false);
+  for (const void* p : {w_gate, w_up, w_down}) mem.reads(p, size_t(inner) * size_t(dim) * 2);
+  mem.reads(residual, out_bytes);
+  mem.kept(gate, tokens, inner, true);
+  mem.kept(up, tokens, inner, true);
+  mem.writes(out, out_bytes, residual);
+  mem.writes(ws, need);
+  if ((st = mem.check()) != MO_OK) return st;
+  int sms = 0;
+  int* status = nullptr;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  Workspace space{static_cast<uint8_t*>(ws)};
+  Launches run;
+  const int64_t ld = padded(inner);
+  void* h = space.take(size_t(tokens) * size_t(ld) * 2);
+  q.epi = mo::kEpiGated;
+  q.act = act;
+  q.a[0] = operand(xk, tokens, dim, space, run, stream);
+  q.b[0] = operand(w_gate, inner, dim, space, run, stream);
+  q.b[1] = operand(w_up, inner, dim, space, run, stream);
+  q.t[0] = {h, nullptr, tokens, inner, ld, 0, 1, 0};
+  q.k = dim;
+  if (run.error == cudaSuccess) run(mo::launch_product(q, sms, status, stream));
+  mo::Product down;
+  down.a[0] = {h, tokens, inner, ld};
+  down.b[0] = operand(w_down, dim, inner, space, run, stream);
+  down.t[0] = target(out, out_dtype, tokens, dim, residual);
+  down.k = inner;
+  if (run.error == cudaSuccess) run(mo::launch_product(down, sms, status, stream));
+  return run.status();
+}
+
+int gated_ffn_grad(const void* dout, const mo_tensor* x, const mo_tensor* gate, const mo_tensor* up, const void* w_gate,
+                   const void* w_up, const void* w_down, int64_t tokens, int64_t dim, int64_t inner, int32_t act,
+                   void* dx, int32_t dx_dtype, void* dw_gate, void* dw_up, void* dw_down, int32_t dw_dtype,
+                   int32_t accumulate, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  void* const dw[3] = {dw_gate, dw_up, dw_down};
+  const bool any_dw = dw_gate != nullptr || dw_up != nullptr || dw_down != nullptr;
+  if (!known_act(act) || (dx != nullptr && !plain_dtype(dx_dtype)) || (any_dw && !plain_dtype(dw_dtype)) ||
+      (accumulate != 0 && accumulate != 1))
+    return MO_ERR_BAD_PARAM;
+  int st = ffn_shape(tokens, dim, inner);
+  if (st != MO_OK) return st;
+  if (tokens > 0 && dx == nullptr && !any_dw) return MO_ERR_NULL_POINTER;
+  for (const void* p : {static_cast<const void*>(dx), static_cast<const void*>(dw_gate), static_cast<const void*>(dw_up),
+                        static_cast<const void*>(dw_down)})
+    if (misaligned(p, 16)) return MO_ERR_MISALIGNED;
+  int sms = 0;
+  int* status = nullptr;
+  const size_t dw_bytes = size_t(inner) * size_t(dim) * bytes_of(dw_dtype);
+  if (tokens == 0) {   // sums over no tokens
+    if (accumulate || !any_dw) return MO_OK;
+    if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+    for (void* p : dw)
+      if (p != nullptr && (st = clear(p, dw_bytes, stream)) != MO_OK) return st;
+    return MO_OK;
+  }
+  const bool need_x = dw_gate != nullptr || dw_up != nullptr;
+  if (dout == nullptr || gate == nullptr || up == nullptr || w_down == nullptr || ws == nullptr || (need_x && x == nullptr) ||
+      (dx != nullptr && (w_gate == nullptr || w_up == nullptr)))
+    return MO_ERR_NULL_POINTER;
+  Kept xk;
+  mo::Product q;
+  if (need_x && (st = kept_args(x, false, &xk)) != MO_OK) return st;
+  if ((st = kept_args(gate, false, &q.pre)) != MO_OK || (st = kept_args(up, false, &q.pre2)) != MO_OK) return st;
+  if (gate->dtype != up->dtype) return MO_ERR_BAD_PARAM;
+  if (misaligned(dout, 16) || misaligned(w_down, 16) || misaligned(ws, 256) ||
+      (dx != nullptr && (misaligned(w_gate, 16) || misaligned(w_up, 16))))
+    return MO_ERR_MISALIGNED;
+  const size_t need = ffn_bytes(tokens, dim, inner, true);
+  if (ws_bytes < need) return MO_ERR_WORKSPACE_TOO_SMALL;
+  Ranges mem;
+  mem.reads(dout, size_t(tokens) * size_t(dim) * 2);
+  if (need_x) mem.kept(x, tokens, dim, false);
+  mem.kept(gate, tokens, inner, false);
+  mem.kept(up, tokens, inner, false);
+  mem.reads(w_down, size_t(inner) * size_t(dim) * 2);
+  if (dx != nullptr)
+    for (const void* p : {w_gate, w_up}) mem.reads(p, size_t(inner) * size_t(dim) * 2);
+  mem.writes(dx, size_t(tokens) * size_t(dim) * bytes_of(dx_dtype));
+  for (void* p : dw) mem.writes(p, dw_bytes);
+  mem.writes(ws, need);
+  if ((st = mem.check()) != MO_OK) return st;
+  if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
+  Workspace space{static_cast<uint8_t*>(ws)};
+  Launches run;
+  const int64_t ld = padded(inner);
+  uint16_t* kept[3];   // dg, du, h
+  for (uint16_t*& p : kept) p = static_cast<uint16_t*>(space.take(size_t(tokens) * size_t(ld) * 2));
+  const Operand d = operand(dout, tokens, dim, space, run, stream);
+  q.epi = mo::kEpiGatedGrad;
+  q.act = act;
+  q.b_mn = true;
+  q.a[0] = d;
+  q.b[0] = operand(w_down, dim, inner, space, run, stream);
+  q.t[0] = {kept[0], nullptr, tokens, inner, ld, 0, 1, 0};
+  q.out2 = kept[1];
+  q.out3 = kept[2];
+  q.k = dim;
+  if (run.error == cudaSuccess) run(mo::launch_product(q, sms, status, stream));
+  if (dx != nullptr) {
+    mo::Product s;
+    s.b_mn = true;
+    s.segments = 2;
+    const void* w[2] = {w_gate, w_up};
+    for (int i = 0; i < 2; ++i) {
+      s.a[i] = {kept[i], tokens, inner, ld};
+      s.b[i] = operand(w[i], inner, dim, space, run, stream);
+    }
+    s.t[0] = target(dx, dx_dtype, tokens, dim);
+    s.k = inner;
+    if (run.error == cudaSuccess) run(mo::launch_product(s, sms, status, stream));
+  }
+  if (any_dw) {   // up to three products over the tokens, one launch
+    const Operand xo = need_x ? operand(xk, tokens, dim, space, run, stream) : Operand{};
+    mo::Product s;
+    s.a_mn = s.b_mn = true;
+    s.count = 0;
+    for (int i = 0; i < 3; ++i) {
+      if (dw[i] == nullptr) continue;
+      s.a[s.count] = i < 2 ? Operand{kept[i], tokens, inner, ld} : d;
+      s.b[s.count] = i < 2 ? xo : Operand{kept[2], tokens, inner, ld};
+      s.t[s.count] = target(dw[i], dw_dtype, i < 2 ? inner : dim, i < 2 ? dim : inner, accumulate ? dw[i] : nullptr);
+      ++s.count;
+    }
+    s.k = tokens;
+    sliced_product(s, reinterpret_cast<float*>(space.take(0)), sms, status, run, stream);
+  }
+  return run.status();
+}
+
+}  // extern "C"

@@ -1,0 +1,278 @@
+// What the two kernels of the bf16 products share: their parameters and the
+// epilogue of a chunk of 32 columns.
+#pragma once
+
+#include <cuda.h>
+
+#include "activation.cuh"
+#include "layer_kernels.h"
+#include "ptx_train.cuh"
+
+namespace mo {
+
+constexpr int kBlockK = 64;   // elements of the reduction a stage: 128 bytes, one swizzle row
+constexpr uint32_t kBox = 64 * 64 * 2;
+
+struct GemmTarget {
+  void* out;
+  const void* add;
+  int64_t m, n, ld, add_ld;
+  int32_t tiles_m, tiles_n, tile0;
+  int32_t align;                 // of the rows of out and add: 32, 16 or 0 (elements)
+  int32_t out_bf16, add_bf16;
+};
+
+struct GemmParams {
+  CUtensorMap a[3], b[3];
+  GemmTarget t[3];
+  int32_t count, segments;
+  int32_t blocks;                // stages a segment
+  int32_t tiles;                 // of all targets
+  int32_t act;
+  const float* bias;
+  Kept pre, pre2;
+  int32_t pre_align;             // of bf16 rows, as above; of 8-bit codes 32 or 16
+  uint16_t* out2;
+  uint16_t* out3;
+  int* status;
+  uint64_t timeout_ns;
+};
+
+// The target of a tile, in order.
+__device__ __forceinline__ int target_of(const GemmParams& p, int32_t tile) {
+  return p.count > 2 && tile >= p.t[2].tile0 ? 2 : p.count > 1 && tile >= p.t[1].tile0 ? 1 : 0;
+}
+
+// Tiles in groups of 8 tile rows, column by column: those in flight share
+// operand panels.
+__device__ __forceinline__ void tile_at(const GemmTarget& t, int32_t tile, int32_t& tm, int32_t& tn) {
+  const int32_t i = tile - t.tile0;
+  const int32_t group = i / (8 * t.tiles_n), first = group * 8;
+  const int32_t height = min(8, t.tiles_m - first), in = i - group * 8 * t.tiles_n;
+  tm = first + in % height;
+  tn = in / height;
+}
+
+// A warp's scratch of 16 columns of fp32: rows of 16 words, each a word apart
+// from the next.
+constexpr uint32_t kTurn = 17 * 32;
+
+__device__ __forceinline__ void load32(const uint16_t* p, int align, float (&v)[32]) {
+  uint32_t w[16];
+  if (align == 32) {
+    ptx::ld_global_v8(p, *reinterpret_cast<uint32_t (*)[8]>(&w[0]));
+    ptx::ld_global_v8(p + 16, *reinterpret_cast<uint32_t (*)[8]>(&w[8]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 q = reinterpret_cast<const uint4*>(p)[j];
+      w[4 * j] = q.x, w[4 * j + 1] = q.y, w[4 * j + 2] = q.z, w[4 * j + 3] = q.w;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ void load32(const float* p, int align, float (&v)[32]) {
+  if (align == 32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[8];
+      ptx::ld_global_v8(p + 8 * q, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * q + j] = __uint_as_float(w[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 q = reinterpret_cast<const float4*>(p)[j];
+      v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
+    }
+  }
+}
+
+__device__ __forceinline__ void store32(uint16_t* p, int align, const float (&v)[32]) {
+  uint32_t w[2][8];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j >> 3][j & 7] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  if (align == 32) {
+    ptx::st_global_v8(p, w[0]);
+    ptx::st_global_v8(p + 16, w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      reinterpret_cast<uint4*>(p)[j] =
+          make_uint4(w[j >> 1][4 * (j & 1)], w[j >> 1][4 * (j & 1) + 1], w[j >> 1][4 * (j & 1) + 2], w[j >> 1][4 * (j & 1) + 3]);
+  }
+}
+
+__device__ __forceinline__ void store32(float* p, int align, const float (&v)[32]) {
+  if (align == 32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * q + j]);
+      ptx::st_global_v8(p + 8 * q, w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      reinterpret_cast<float4*>(p)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  }
+}
+
+__device__ __forceinline__ void put(void* out, bool bf16, int64_t at, float v) {
+  if (bf16)
+    store1(static_cast<uint16_t*>(out) + at, v);
+  else
+    store1(static_cast<float*>(out) + at, v);
+}
+__device__ __forceinline__ float get(const void* p, bool bf16, int64_t at) {
+  return bf16 ? load1(static_cast<const uint16_t*>(p) + at) : load1(static_cast<const float*>(p) + at);
+}
+
+// Stores a chunk of 32 columns, a row a lane, of the 32 rows from `row0` on,
+// plus the chunk of `add`. Rows that are 16-byte aligned and a whole chunk:
+// vectors. Others (an odd n, the last columns) are turned in shared memory, 16
+// columns at a time, and stored two rows an instruction.
+__device__ __forceinline__ void store_chunk(void* out, bool out_bf16, int64_t ld, const void* add, bool add_bf16, int64_t add_ld,
+                                            int align, int64_t row0, int64_t m, int64_t col, int64_t n, float (&v)[32],
+                                            float* turn) {
+  const int lane = int(threadIdx.x & 31);
+  if (align != 0 && col + 32 <= n) {
+    const int64_t row = row0 + lane;
+    if (row >= m) return;
+    if (add != nullptr) {
+      float x[32];
+      if (add_bf16)
+        load32(static_cast<const uint16_t*>(add) + row * add_ld + col, align, x);
+      else
+        load32(static_cast<const float*>(add) + row * add_ld + col, align, x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += x[i];
+    }
+    if (out_bf16)
+      store32(static_cast<uint16_t*>(out) + row * ld + col, align, v);
+    else
+      store32(static_cast<float*>(out) + row * ld + col, align, v);
+    return;
+  }
+  const int rows = int(min(int64_t(32), m - row0));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) turn[lane * 17 + j] = v[16 * h + j];
+    __syncwarp();
+    const int64_t c = col + 16 * h + (lane & 15);
+    if (c < n) {
+#pragma unroll 4
+      for (int r = lane >> 4; r < rows; r += 2) {
+        float x = turn[r * 17 + (lane & 15)];
+        if (add != nullptr) x += get(add, add_bf16, (row0 + r) * add_ld + c);
+        put(out, out_bf16, (row0 + r) * ld + c, x);
+      }
+    }
+  }
+}
+
+// Keeps a chunk, in 8 bits or in bf16.
+__device__ __forceinline__ void keep_chunk(const Kept& q, int align, int64_t row0, int64_t m, int64_t col, int64_t n,
+                                           const float (&v)[32], float* turn) {
+  if (q.dtype != MO_MX8) {
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = v[i];
+    store_chunk(q.data, true, n, nullptr, false, 0, align, row0, m, col, n, x, turn);
+    return;
+  }
+  const int64_t row = row0 + int64_t(threadIdx.x & 31);
+  if (row >= m) return;
+  // (past n the sums are zeros, and so are the codes)
+  float top = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < 31; i += 2) top = top3(top, v[i], v[i + 1]);
+  top = top2(top, fabsf(v[31]));
+  const uint32_t s = mx8_scale(top);
+  const float down = mx8_down(s);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = cvt_e4m3x4(v[4 * i] * down, v[4 * i + 1] * down, v[4 * i + 2] * down, v[4 * i + 3] * down);
+  const int64_t nb = (n + 31) / 32;
+  uint8_t* o = static_cast<uint8_t*>(q.data) + row * nb * 32 + col;
+  if (align == 32) {
+    ptx::st_global_v8(o, w);
+  } else {
+    reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  q.scales[row * nb + (col >> 5)] = uint8_t(s);
+}
+
+// A kept chunk's raw words, loaded ahead of their use: 8-bit codes in the first
+// eight and the scale, or bf16. Chunks of bf16 rows that are not whole or not
+// aligned are read element by element.
+struct RawChunk {
+  uint32_t w[16];
+  uint32_t scale;
+};
+__device__ __forceinline__ void fetch_kept(const Kept& q, int align, int64_t row, int64_t col, int64_t n, RawChunk& raw) {
+  if (q.dtype == MO_MX8) {
+    const int64_t nb = (n + 31) / 32;
+    const uint8_t* o = static_cast<const uint8_t*>(q.data) + row * nb * 32 + col;
+    const uint4 a = reinterpret_cast<const uint4*>(o)[0], b = reinterpret_cast<const uint4*>(o)[1];
+    raw.w[0] = a.x, raw.w[1] = a.y, raw.w[2] = a.z, raw.w[3] = a.w;
+    raw.w[4] = b.x, raw.w[5] = b.y, raw.w[6] = b.z, raw.w[7] = b.w;
+    raw.scale = q.scales[row * nb + (col >> 5)];
+  } else {
+    const uint16_t* o = static_cast<const uint16_t*>(q.data) + row * n + col;
+    if (align != 0 && col + 32 <= n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 a = reinterpret_cast<const uint4*>(o)[j];
+        raw.w[4 * j] = a.x, raw.w[4 * j + 1] = a.y, raw.w[4 * j + 2] = a.z, raw.w[4 * j + 3] = a.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        raw.w[j] = (col + 2 * j < n ? uint32_t(o[2 * j]) : 0u) | (col + 2 * j + 1 < n ? uint32_t(o[2 * j + 1]) << 16 : 0u);
+    }
+  }
+}
+__device__ __forceinline__ void kept_values(const Kept& q, const RawChunk& raw, float (&v)[32]) {
+  if (q.dtype == MO_MX8) {
+    const float up = mx8_up(raw.scale);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float x[4];
+      e4m3x4_values(raw.w[j], x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * j + i] = x[i] * up;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      v[2 * j] = __uint_as_float(raw.w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(raw.w[j] & 0xFFFF0000u);
+    }
+  }
+}
+// One element of a kept tensor of rows of n.
+__device__ __forceinline__ float kept_at(const Kept& q, int64_t row, int64_t col, int64_t n) {
+  if (q.dtype == MO_MX8) {
+    const int64_t nb = (n + 31) / 32;
+    return e4m3_value(static_cast<const uint8_t*>(q.data)[row * nb * 32 + col]) * mx8_up(q.scales[row * nb + (col >> 5)]);
+  }
+  return load1(static_cast<const uint16_t*>(q.data) + row * n + col);
+}
+
+// Few rows: tiles of 128 columns, the reduction split over clusters.
+cudaError_t launch_narrow(const Product& q, GemmParams& p, int sms, cudaStream_t stream);
+bool encode_operand(CUtensorMap* map, const Operand& o, uint32_t box_rows);
+
+}  // namespace mo

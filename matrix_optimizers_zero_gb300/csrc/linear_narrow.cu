@@ -1,0 +1,321 @@
+// bf16 products of few rows (see linear_pair.cu for what they compute): a CTA
+// multiplies 128 columns' operand by NT rows' over its part of the reduction,
+// and the CTAs of a cluster, which hold the parts of one tile, add their sums
+// through distributed shared memory in rank order. Accumulator lanes are
+// columns of the output, so a warp's 32 lanes store 32 neighbours of a row,
+// and are a block of an 8-bit tensor.
+//
+// With few rows a product is the reading of its weights, so K is split until
+// all SMs have loads under way.
+#include <cuda_runtime.h>
+
+#include "launch.cuh"
+#include "linear_gemm.cuh"
+
+namespace mo {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kWarps = kThreads / 32;
+constexpr uint32_t kPanel = 128 * kBlockK * 2;   // 128 columns' operand
+constexpr uint32_t kPitch = 132;                 // of the fp32 sums [NT][128] in shared memory
+
+template <Epilogue EPI>
+constexpr int kPanels = EPI == kEpiGated ? 2 : 1;   // gate and up
+template <Epilogue EPI, int NT>
+constexpr uint32_t kStage = kPanels<EPI> * kPanel + NT * kBlockK * 2;
+// Two CTAs an SM where the sums and enough stages fit.
+template <Epilogue EPI, int NT>
+constexpr int kStages = EPI == kEpiGated ? (NT == 16 ? 3 : NT == 64 ? 5 : 4) : (NT == 16 ? 6 : NT == 64 ? 4 : 3);
+template <Epilogue EPI, int NT>
+constexpr size_t kSmem = 1024 + size_t(kStages<EPI, NT>) * kStage<EPI, NT> + 160;
+template <Epilogue EPI, int NT>
+constexpr uint32_t kCols = kPanels<EPI> * NT < 32 ? 32 : kPanels<EPI> * NT;   // of TMEM
+template <Epilogue EPI, int NT>
+constexpr bool kFits = kStages<EPI, NT> * kStage<EPI, NT> >= kPanels<EPI> * NT * kPitch * 4 && kSmem<EPI, NT> <= 227 * 1024;
+static_assert(kFits<kEpiLinear, 16> && kFits<kEpiLinear, 64> && kFits<kEpiLinear, 128> && kFits<kEpiGated, 16> &&
+                  kFits<kEpiGated, 64> && kFits<kEpiGated, 128>,
+              "sums in the stages' memory");
+
+// What follows the sums of one element; a warp has 32 neighbours of a row.
+template <Epilogue EPI>
+__device__ __forceinline__ void finish(const GemmParams& p, const GemmTarget& t, int64_t row, int64_t col, float x, float y) {
+  const bool in = col < t.n;
+  const int lane = int(threadIdx.x & 31);
+  auto keep = [&](const Kept& q, float v) {
+    if (q.dtype == MO_MX8) {
+      float top = in ? fabsf(v) : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      const int64_t nb = (t.n + 31) / 32;
+      if (col - lane >= t.n) return;
+      const uint32_t s = mx8_scale(top);
+      static_cast<uint8_t*>(q.data)[row * nb * 32 + col] = uint8_t(cvt_e4m3x2(in ? v * mx8_down(s) : 0.0f, 0.0f));
+      if (lane == 0) q.scales[row * nb + (col >> 5)] = uint8_t(s);
+    } else if (in) {
+      store1(static_cast<uint16_t*>(q.data) + row * t.n + col, v);
+    }
+  };
+  if constexpr (EPI == kEpiLinear) {
+    if (p.bias != nullptr && in) x += p.bias[col];
+    if (p.pre.data != nullptr) keep(p.pre, x);
+    with_act(p.act, [&](auto act) { x = act_value<decltype(act)::value>(x); });
+    if (!in) return;
+    if (t.add != nullptr) x += get(t.add, t.add_bf16 != 0, row * t.add_ld + col);
+    put(t.out, t.out_bf16 != 0, row * t.ld + col, x);
+  } else if constexpr (EPI == kEpiGated) {
+    if (p.pre.data != nullptr) {
+      keep(p.pre, x);
+      keep(p.pre2, y);
+    }
+    with_act(p.act, [&](auto act) { x = act_value<decltype(act)::value>(x) * y; });
+    if (in) store1(static_cast<uint16_t*>(t.out) + row * t.ld + col, x);
+  } else {
+    if (!in) return;
+    const float g = kept_at(p.pre, row, col, t.n), u = kept_at(p.pre2, row, col, t.n);
+    float a = 0.0f, slope = 0.0f;
+    with_act(p.act, [&](auto act) { slope = act_slope<decltype(act)::value>(g, &a); });
+    const int64_t at = row * t.ld + col;
+    store1(static_cast<uint16_t*>(t.out) + at, x * u * slope);
+    store1(p.out2 + at, x * a);
+    store1(p.out3 + at, a * u);
+  }
+}
+
+// Q: the rows' operand (A of the product), P: the columns' (B).
+template <Epilogue EPI, bool Q_MN, bool P_MN, int NT>
+__global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_constant__ GemmParams p) {
+  static_assert(!Q_MN || NT == 128, "whole boxes");
+  extern __shared__ uint8_t smem_raw[];
+  constexpr uint32_t kStg = kStage<EPI, NT>;
+  constexpr int kStgs = kStages<EPI, NT>;
+  constexpr uint32_t kQ = kPanels<EPI> * kPanel;   // of the rows' operand in a stage
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t bars = base + uint32_t(kStgs) * kStg;
+  constexpr uint32_t kBars = 2 * kStgs + 2;
+  static_assert(8 * kBars + 8 <= 160, "control block");
+  uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kBars);
+  uint32_t* tmem_slot = ctrl;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 1);
+  float* sums = reinterpret_cast<float*>(smem_raw + (base - raw));
+  auto full_bar = [&](int s) { return bars + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(kStgs + s); };
+  const uint32_t done_bar = bars + 8u * uint32_t(2 * kStgs);
+  const uint32_t drain_bar = bars + 8u * uint32_t(2 * kStgs + 1);
+
+  const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+  const uint32_t parts = gridDim.x / uint32_t(p.tiles);   // CTAs of a cluster
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int32_t tile = int32_t(blockIdx.x / parts);
+  const int q = target_of(p, tile);
+  const GemmTarget& t = p.t[q];
+  const int32_t tn = (tile - t.tile0) / t.tiles_m, tm = (tile - t.tile0) - tn * t.tiles_m;   // 128 columns, NT rows
+  const int64_t blocks = int64_t(p.blocks) * p.segments;
+  const int32_t k0 = int32_t(blocks * rank / parts), k1 = int32_t(blocks * (rank + 1) / parts);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStgs; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    ptx::mbar_init(done_bar, 1);
+    ptx::mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_one(ptx::smem_addr(tmem_slot), kCols<EPI, NT>);
+    ptx::tmem_relinquish_one();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  ptx::griddep_launch_dependents();   // after the TMEM is held: the next kernel's blocks take theirs before they wait
+  ptx::griddep_wait();
+
+  uint32_t n_issued = 0;
+  bool mma_issued = false;
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 0;
+      for (int32_t kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait_bounded(empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
+        const int seg = kb >= p.blocks ? 1 : 0;
+        const int32_t at = (kb - seg * p.blocks) * kBlockK;
+        const int op = p.segments > 1 ? seg : q;
+        const uint32_t fb = full_bar(stage);
+        ptx::mbar_arrive_expect_tx(fb, kStg);
+        const uint32_t sp = base + uint32_t(stage) * kStg, sq = sp + kQ;
+#pragma unroll
+        for (int i = 0; i < kPanels<EPI>; ++i) {
+          const CUtensorMap* mp = &p.b[EPI == kEpiGated ? i : op];
+          const uint32_t s = sp + uint32_t(i) * kPanel;
+          if (P_MN) {
+            ptx::tma_load_2d(s, mp, fb, tn * 128, at);
+            ptx::tma_load_2d(s + kBox, mp, fb, tn * 128 + 64, at);
+          } else {
+            ptx::tma_load_2d(s, mp, fb, at, tn * 128);
+          }
+        }
+        if (Q_MN) {
+          ptx::tma_load_2d(sq, &p.a[op], fb, tm * NT, at);
+          ptx::tma_load_2d(sq + kBox, &p.a[op], fb, tm * NT + 64, at);
+        } else {
+          ptx::tma_load_2d(sq, &p.a[op], fb, at, tm * NT);
+        }
+        ++n_issued;
+        if (++stage == kStgs) {
+          stage = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, NT, P_MN ? 1u : 0u, Q_MN ? 1u : 0u);
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int32_t kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait_bounded(full_bar(stage), ph, abort_flag, p.status, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t sp = base + uint32_t(stage) * kStg, sq = sp + kQ;
+#pragma unroll
+        for (int i = 0; i < kPanels<EPI>; ++i) {
+#pragma unroll
+          for (int kk = 0; kk < kBlockK / 16; ++kk) {
+            const uint32_t s = sp + uint32_t(i) * kPanel;
+            const uint64_t pd = P_MN ? ptx::smem_desc_sw128(s + uint32_t(kk) * 2048u, kBox, 1024u)
+                                     : ptx::smem_desc_sw128(s + uint32_t(kk) * 32u, 16u, 1024u);
+            const uint64_t qd = Q_MN ? ptx::smem_desc_sw128(sq + uint32_t(kk) * 2048u, kBox, 1024u)
+                                     : ptx::smem_desc_sw128(sq + uint32_t(kk) * 32u, 16u, 1024u);
+            ptx::umma_bf16_one(tmem + uint32_t(i) * NT, pd, qd, idesc, kb > k0 || kk > 0 ? 1u : 0u);
+          }
+        }
+        ptx::umma_commit_one(empty_bar(stage));
+        mma_issued = true;
+        if (++stage == kStgs) {
+          stage = 0;
+          ph ^= 1u;
+        }
+      }
+      if (ok) ptx::umma_commit_one(done_bar);
+    }
+  } else {
+    const int quarter = warp & 3;
+    bool ok = mbar_wait_bounded(done_bar, 0u, abort_flag, p.status, p.timeout_ns);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (ok) {
+      ptx::tc_fence_after();
+      // lane l of a quarter holds column quarter 32 + l; the sums go to the memory of the stages, which
+      // have all been read
+      const int rows = int(min(int64_t(NT), t.m - int64_t(tm) * NT));
+#pragma unroll 1
+      for (int i = 0; i < kPanels<EPI>; ++i)
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 16) {
+          uint32_t r[16];
+          __syncwarp();
+          ptx::tmem_ld_32x32b_x16(tmem + uint32_t(i * NT + c) + (uint32_t(quarter * 32) << 16), r);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            sums[uint32_t(i * NT + c + j) * kPitch + uint32_t(quarter * 32 + lane)] = __uint_as_float(r[j]);
+        }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (*abort_flag != 0) {   // settle what is in flight before the memory is given back
+    if (warp == 1 && lane == 0 && mma_issued) {
+      ptx::umma_commit_one(drain_bar);
+      mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
+    }
+    if (threadIdx.x == 0)
+      for (uint32_t j = n_issued > uint32_t(kStgs) ? n_issued - uint32_t(kStgs) : 0u; j < n_issued; ++j)
+        mbar_wait_drain(full_bar(int(j % uint32_t(kStgs))), (j / uint32_t(kStgs)) & 1u, p.timeout_ns);
+    __syncthreads();
+  }
+  if (parts > 1) ptx::cluster_sync();   // every part's sums are in place
+  {
+    // this CTA's share of the tile, 32 columns of a row a warp, parts added in rank order
+    const uint32_t sums_addr = ptx::smem_addr(sums);
+    const int64_t row0 = int64_t(tm) * NT, col0 = int64_t(tn) * 128;
+    const uint32_t units = uint32_t(min(int64_t(NT), t.m - row0)) * 4u;
+    for (uint32_t u = rank * kWarps + uint32_t(warp); u < units; u += parts * kWarps) {
+      const uint32_t j = u >> 2, c = (u & 3u) * 32u + uint32_t(lane);
+      float v[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kPanels<EPI>; ++i) {
+        const uint32_t at = (uint32_t(i) * NT + j) * kPitch + c;
+        if (parts == 1) {
+          v[i] = sums[at];
+        } else {
+          float x[8];
+#pragma unroll
+          for (uint32_t s = 0; s < 8; ++s)
+            if (s < parts) x[s] = ptx::ld_shared_cluster_f32(ptx::mapa_shared(sums_addr + 4u * at, s));
+#pragma unroll
+          for (uint32_t s = 0; s < 8; ++s)
+            if (s < parts) v[i] += x[s];
+        }
+      }
+      finish<EPI>(p, t, row0 + j, col0 + c, v[0], v[1]);
+    }
+  }
+  if (parts > 1) ptx::cluster_sync();   // the peers have read this CTA's sums
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc_one(tmem, kCols<EPI, NT>);
+}
+
+template <Epilogue EPI, bool Q_MN, bool P_MN, int NT>
+cudaError_t narrow_as(const Product& q, GemmParams& p, int sms, cudaStream_t stream) {
+  const int n = std::max(q.count, q.segments);
+  for (int i = 0; i < 3; ++i) {
+    if (i < n && !encode_operand(&p.a[i], q.a[i], Q_MN ? 64 : NT)) return cudaErrorInvalidValue;
+    if (i < (EPI == kEpiGated ? 2 : n) && !encode_operand(&p.b[i], q.b[i], P_MN ? 64 : 128)) return cudaErrorInvalidValue;
+  }
+  int64_t tiles = 0;
+  for (int i = 0; i < q.count; ++i) {
+    GemmTarget& t = p.t[i];
+    t.tile0 = int32_t(tiles);
+    t.tiles_m = int32_t((t.m + NT - 1) / NT);
+    t.tiles_n = int32_t((t.n + 127) / 128);
+    tiles += int64_t(t.tiles_m) * t.tiles_n;
+  }
+  p.tiles = int32_t(tiles);
+  // The reduction in as many parts as leave all clusters resident (clusters of 4 and 8 do not fill the
+  // GPU's parts evenly: 72 of 76 and 30 of 38 fit on 152 SMs, two CTAs an SM) and four stages a CTA.
+  const int64_t per_sm = kSmem<EPI, NT> <= 113 * 1024 ? 2 : 1;
+  const int64_t most[4] = {0, sms * per_sm / 2, sms * per_sm * 45 / 200, sms * per_sm * 18 / 200};
+  unsigned parts = 1;
+  for (int i = 1; i < 4 && tiles <= most[i] && p.blocks * q.segments >= (4 << i); ++i) parts = 1u << i;
+  auto kern = linear_narrow_kernel<EPI, Q_MN, P_MN, NT>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem<EPI, NT>);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(unsigned(tiles * parts)), dim3(kThreads), kSmem<EPI, NT>, parts, true, stream, p);
+}
+
+template <Epilogue EPI, bool P_MN>
+cudaError_t narrow_rows(const Product& q, GemmParams& p, int sms, cudaStream_t stream) {
+  if (q.t[0].m <= 16) return narrow_as<EPI, false, P_MN, 16>(q, p, sms, stream);
+  if (q.t[0].m <= 64) return narrow_as<EPI, false, P_MN, 64>(q, p, sms, stream);
+  return narrow_as<EPI, false, P_MN, 128>(q, p, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_narrow(const Product& q, GemmParams& p, int sms, cudaStream_t stream) {
+  if (q.epi == kEpiGated) return narrow_rows<kEpiGated, false>(q, p, sms, stream);
+  if (q.epi == kEpiGatedGrad) return narrow_rows<kEpiGatedGrad, true>(q, p, sms, stream);
+  if (q.a_mn) return narrow_as<kEpiLinear, true, true, 128>(q, p, sms, stream);
+  return q.b_mn ? narrow_rows<kEpiLinear, true>(q, p, sms, stream) : narrow_rows<kEpiLinear, false>(q, p, sms, stream);
+}
+
+}  // namespace mo

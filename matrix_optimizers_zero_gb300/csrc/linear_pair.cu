@@ -1,0 +1,426 @@
+// bf16 products of the feed-forward operators on the 5th-generation tensor
+// cores, sums in fp32, everything that follows a sum in its epilogue:
+//
+//   out[m, n] = act(sum_k A[m, k] B[n, k] + bias[n]) + add[m, n]      kEpiLinear
+//   out = act(g) u of two sums g and u with the same A                 kEpiGated
+//   out = dh u act'(g), dh act(g) and act(g) u of one sum dh           kEpiGatedGrad
+//
+// 256 x 256 tiles on CTA pairs (cta_group::2), persistent, as the Newton-Schulz
+// products: warp 0 loads this CTA's 128-row halves of both operands by TMA
+// (128-byte swizzle) into six 32 KB stages, the even CTA's warp 1 issues the
+// instructions, warps 2-9 drain 128 lanes x 256 columns; two accumulators let a
+// tile's epilogue run under the next tile's products. Either operand's rows may
+// run along k (K-major) or along its own index (MN-major: the transposed
+// operands of the gradients, as they lie in memory).
+//
+// kEpiGated: the even CTA's half of B is 128 rows of the gate weight, the odd
+// CTA's the same rows of the up weight. Both CTAs' accumulators then hold g in
+// columns 0-127 and u in 128-255 for their own rows of A, and one thread has
+// both.
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "launch.cuh"
+#include "linear_gemm.cuh"
+
+namespace mo {
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kStages = 6;
+constexpr uint32_t kHalf = 128 * kBlockK * 2;   // 16 KB: 128 rows of an operand
+constexpr uint32_t kStage = 2 * kHalf;
+constexpr uint32_t kBars = 2 * kStages + 5;
+constexpr uint32_t kCtrl = 256;
+constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kCtrl + size_t(kEpiWarps) * kTurn * 4;
+static_assert(8 * kBars + 16 <= kCtrl && kSmem <= 227 * 1024, "shared memory");
+
+// A chunk of 32 columns of an accumulator, a row a lane.
+__device__ __forceinline__ void tmem_chunk(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  __syncwarp();
+  ptx::tmem_ld_32x32b_x32(taddr, r);
+  ptx::tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The 32 rows from row0 on (lane l has row0 + l) and this warp's half of the
+// tile's columns, from TMEM column `tb` on.
+template <Epilogue EPI>
+__device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& t, int64_t row0, int32_t tn, int half, uint32_t tb,
+                                         float* turn) {
+  const int lane = int(threadIdx.x & 31);
+  const int64_t row = row0 + lane;
+  if constexpr (EPI == kEpiLinear) {
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+      const int64_t col = int64_t(tn) * 256 + half * 128 + ch * 32;
+      float v[32];
+      tmem_chunk(tb + uint32_t(half * 128 + ch * 32), v);
+      if (row0 >= t.m || col >= t.n) continue;
+      if (p.bias != nullptr) {
+        if (col + 32 <= t.n) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 b = reinterpret_cast<const float4*>(p.bias + col)[j];
+            v[4 * j] += b.x, v[4 * j + 1] += b.y, v[4 * j + 2] += b.z, v[4 * j + 3] += b.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (col + i < t.n) v[i] += p.bias[col + i];
+        }
+      }
+      if (p.pre.data != nullptr) keep_chunk(p.pre, p.pre_align, row0, t.m, col, t.n, v, turn);
+      if (p.act != MO_ACT_NONE)
+        with_act(p.act, [&](auto act) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
+        });
+      store_chunk(t.out, t.out_bf16 != 0, t.ld, t.add, t.add_bf16 != 0, t.add_ld, t.align, row0, t.m, col, t.n, v, turn);
+    }
+  } else if constexpr (EPI == kEpiGated) {
+#pragma unroll 1
+    for (int ch = 0; ch < 2; ++ch) {
+      const int64_t col = int64_t(tn) * 128 + half * 64 + ch * 32;
+      float g[32], u[32];
+      tmem_chunk(tb + uint32_t(half * 64 + ch * 32), g);
+      tmem_chunk(tb + uint32_t(128 + half * 64 + ch * 32), u);
+      if (row0 >= t.m || col >= t.n) continue;
+      if (p.pre.data != nullptr) {
+        keep_chunk(p.pre, p.pre_align, row0, t.m, col, t.n, g, turn);
+        keep_chunk(p.pre2, p.pre_align, row0, t.m, col, t.n, u, turn);
+      }
+      with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) g[i] = act_value<decltype(act)::value>(g[i]) * u[i];
+      });
+      // (a whole chunk: the rows of the workspace are padded)
+      if (row < t.m) store32(static_cast<uint16_t*>(t.out) + row * t.ld + col, 32, g);
+    }
+  } else {
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+      const int64_t col = int64_t(tn) * 256 + half * 128 + ch * 32;
+      const bool in = row < t.m && col < t.n;
+      RawChunk rg, ru;
+      if (in) {
+        fetch_kept(p.pre, p.pre_align, row, col, t.n, rg);
+        fetch_kept(p.pre2, p.pre_align, row, col, t.n, ru);
+      }
+      float dh[32];
+      tmem_chunk(tb + uint32_t(half * 128 + ch * 32), dh);
+      if (!in) continue;
+      float g[32], u[32];
+      kept_values(p.pre, rg, g);
+      kept_values(p.pre2, ru, u);
+      with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float a;
+          const float slope = act_slope<decltype(act)::value>(g[i], &a);
+          g[i] = dh[i] * u[i] * slope;
+          u[i] = a * u[i];
+          dh[i] = dh[i] * a;
+        }
+      });
+      const int64_t at = row * t.ld + col;
+      store32(static_cast<uint16_t*>(t.out) + at, 32, g);
+      store32(p.out2 + at, 32, dh);
+      store32(p.out3 + at, 32, u);
+    }
+  }
+}
+
+template <Epilogue EPI, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_constant__ GemmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t bars = base + uint32_t(kStages) * kStage;
+  uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kBars);
+  uint32_t* tmem_slot = ctrl;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 1);
+  volatile uint32_t* peer_report = ctrl + 2;   // [0] the peer gave up, [1] stages its producer issued
+  auto full_bar = [&](int s) { return bars + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(kStages + s); };
+  auto tfull_bar = [&](int s) { return bars + 8u * uint32_t(2 * kStages + s); };
+  auto tempty_bar = [&](int s) { return bars + 8u * uint32_t(2 * kStages + 2 + s); };
+  const uint32_t drain_bar = bars + 8u * uint32_t(2 * kStages + 4);
+
+  const int warp = int(threadIdx.x >> 5);
+  const int lane = int(threadIdx.x & 31);
+  const uint32_t rank = ptx::cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(tfull_bar(s), 1);
+      ptx::mbar_init(tempty_bar(s), 2 * kEpiWarps);
+    }
+    ptx::mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    peer_report[0] = 0u;
+    peer_report[1] = 0u;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // All of the above overlaps the previous kernel's end. The next one may come only now: its blocks
+  // take their TMEM before they wait for this grid, and this block has its own.
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+
+  const int32_t first = int32_t(ptx::cluster_id_x()), step = int32_t(ptx::nclusters_x());
+  const int32_t blocks = p.blocks * p.segments;
+  uint32_t n_issued = 0;
+  bool mma_issued = false;
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer (both CTAs)
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int32_t tile = first; ok && tile < p.tiles; tile += step) {
+        const int q = target_of(p, tile);
+        int32_t tm, tn;
+        tile_at(p.t[q], tile, tm, tn);
+        const int32_t ra = tm * 256 + int32_t(rank) * 128;
+        const int32_t rb = EPI == kEpiGated ? tn * 128 : tn * 256 + int32_t(rank) * 128;
+        for (int32_t kb = 0; kb < blocks; ++kb) {
+          if (!mbar_wait_bounded(empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          const int seg = kb >= p.blocks ? 1 : 0;
+          const int32_t k0 = (kb - seg * p.blocks) * kBlockK;
+          const CUtensorMap* ma = &p.a[p.segments > 1 ? seg : q];
+          const CUtensorMap* mb = &p.b[EPI == kEpiGated ? int(rank) : p.segments > 1 ? seg : q];
+          const uint32_t fb_local = full_bar(stage);
+          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * kStage);
+          const uint32_t fb = ptx::mapa_shared(fb_local, 0);
+          const uint32_t sa = base + uint32_t(stage) * kStage, sb = sa + kHalf;
+          if (A_MN) {
+            ptx::tma_load_2d_pair(sa, ma, fb, ra, k0);
+            ptx::tma_load_2d_pair(sa + kBox, ma, fb, ra + 64, k0);
+          } else {
+            ptx::tma_load_2d_pair(sa, ma, fb, k0, ra);
+          }
+          if (B_MN) {
+            ptx::tma_load_2d_pair(sb, mb, fb, rb, k0);
+            ptx::tma_load_2d_pair(sb + kBox, mb, fb, rb + 64, k0);
+          } else {
+            ptx::tma_load_2d_pair(sb, mb, fb, k0, rb);
+          }
+          ++n_issued;
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------ MMA issuer (even CTA)
+      constexpr uint32_t idesc = ptx::idesc_bf16_f32(256, 256, A_MN ? 1u : 0u, B_MN ? 1u : 0u);
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int32_t i = 0;
+      for (int32_t tile = first; ok && tile < p.tiles; tile += step, ++i) {
+        const int acc = i & 1;
+        if (!mbar_wait_bounded<true>(tempty_bar(acc), (uint32_t(i >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + uint32_t(acc) * 256u;
+        for (int32_t kb = 0; kb < blocks; ++kb) {
+          // (the odd CTA's copies count on this barrier too)
+          if (!mbar_wait_bounded(full_bar(stage), ph, abort_flag, p.status, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sa = base + uint32_t(stage) * kStage, sb = sa + kHalf;
+#pragma unroll
+          for (int kk = 0; kk < kBlockK / 16; ++kk) {
+            const uint64_t ad = A_MN ? ptx::smem_desc_sw128(sa + uint32_t(kk) * 2048u, kBox, 1024u)
+                                     : ptx::smem_desc_sw128(sa + uint32_t(kk) * 32u, 16u, 1024u);
+            const uint64_t bd = B_MN ? ptx::smem_desc_sw128(sb + uint32_t(kk) * 2048u, kBox, 1024u)
+                                     : ptx::smem_desc_sw128(sb + uint32_t(kk) * 32u, 16u, 1024u);
+            ptx::umma_bf16_pair(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+          }
+          ptx::umma_commit_pair(empty_bar(stage), 0x3);
+          mma_issued = true;
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::umma_commit_pair(tfull_bar(acc), 0x3);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue (both CTAs)
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;
+    float* turn = reinterpret_cast<float*>(smem_raw + (bars - raw) + kCtrl) + (warp - 2) * kTurn;
+    int32_t i = 0;
+    for (int32_t tile = first; tile < p.tiles; tile += step, ++i) {
+      const int acc = i & 1;
+      const GemmTarget& t = p.t[target_of(p, tile)];
+      int32_t tm, tn;
+      tile_at(t, tile, tm, tn);
+      bool ok = mbar_wait_bounded(tfull_bar(acc), uint32_t(i >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const int64_t row0 = int64_t(tm) * 256 + int64_t(rank) * 128 + quarter * 32;
+      epilogue<EPI>(p, t, row0, tn, half, tmem + uint32_t(acc) * 256u + (uint32_t(quarter * 32) << 16), turn);
+      // hand the accumulator back: its reads are complete (tcgen05.wait::ld) and fenced, and nothing
+      // else of the tile has to be ordered inside the launch
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_remote_relaxed(ptx::mapa_shared(tempty_bar(acc), 0));
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  // Both CTAs learn whether either gave up and how many stages its producer issued.
+  if (threadIdx.x == 0)
+    ptx::st_shared_cluster_v2(ptx::mapa_shared(ptx::smem_addr(const_cast<uint32_t*>(peer_report)), rank ^ 1u),
+                              *abort_flag != 0 ? 1u : 0u, n_issued);
+  ptx::cluster_sync();
+  if (*abort_flag != 0 || peer_report[0] != 0u) {
+    // Nothing may still write into either CTA's memory when they exit: the even CTA waits for its
+    // instructions, then settles every stage that either producer left in flight (all copies of both
+    // CTAs count their bytes on its full barriers; at most the last kStages can be in flight).
+    if (leader && warp == 1 && lane == 0 && mma_issued) {
+      ptx::umma_commit_pair(drain_bar, 0x1);
+      mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
+    }
+    if (leader && threadIdx.x == 0) {
+      const uint32_t L = n_issued, P = peer_report[1];
+      const uint32_t most = L > P ? L : P;
+      for (uint32_t j = most > uint32_t(kStages) ? most - uint32_t(kStages) : 0u; j < most; ++j) {
+        const int s = int(j % uint32_t(kStages));
+        if (j >= L)
+          ptx::mbar_arrive_expect_tx(full_bar(s), kStage);   // only the peer's half is coming
+        else if (j >= P)
+          ptx::mbar_complete_tx(full_bar(s), kStage);        // the peer's half never will
+        mbar_wait_drain(full_bar(s), (j / uint32_t(kStages)) & 1u, p.timeout_ns);
+      }
+    }
+    ptx::cluster_sync();
+  }
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc_pair(tmem, 512);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn tensor_map_encoder() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+template <Epilogue EPI, bool A_MN, bool B_MN>
+cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t stream) {
+  const int n = std::max(q.count, q.segments);
+  for (int i = 0; i < 3; ++i) {
+    if (i < n && !encode_operand(&p.a[i], q.a[i], A_MN ? 64 : 128)) return cudaErrorInvalidValue;
+    if (i < (EPI == kEpiGated ? 2 : n) && !encode_operand(&p.b[i], q.b[i], B_MN ? 64 : 128)) return cudaErrorInvalidValue;
+  }
+  int64_t tiles = 0;
+  for (int i = 0; i < q.count; ++i) {
+    GemmTarget& t = p.t[i];
+    t.tile0 = int32_t(tiles);
+    t.tiles_m = int32_t((t.m + 255) / 256);
+    t.tiles_n = int32_t(EPI == kEpiGated ? (t.n + 127) / 128 : (t.n + 255) / 256);
+    tiles += int64_t(t.tiles_m) * t.tiles_n;
+  }
+  if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
+  p.tiles = int32_t(tiles);
+  auto kern = linear_pair_kernel<EPI, A_MN, B_MN>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = unsigned(2 * std::min<int64_t>(sms / 2, tiles));
+  return launch_kernel(kern, dim3(grid), dim3(kThreads), kSmem, 2, true, stream, p);
+}
+
+}  // namespace
+
+bool encode_operand(CUtensorMap* map, const Operand& o, uint32_t box_rows) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(o.cols), cuuint64_t(o.rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(o.ld) * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(o.p), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_product(const Product& q, int sms, int* status, cudaStream_t stream) {
+  GemmParams p = {};
+  p.count = q.count;
+  p.segments = q.segments;
+  p.blocks = int32_t((q.k + kBlockK - 1) / kBlockK);
+  p.act = q.act;
+  p.bias = q.bias;
+  p.pre = q.pre;
+  p.pre2 = q.pre2;
+  p.out2 = q.out2;
+  p.out3 = q.out3;
+  p.status = status;
+  p.timeout_ns = kDefaultTimeoutNs;
+  auto align_of = [](uintptr_t bits) { return (bits & 31) == 0 ? 32 : (bits & 15) == 0 ? 16 : 0; };
+  int64_t pair_tiles = 0, rows = 0;
+  for (int i = 0; i < q.count; ++i) {
+    const Target& t = q.t[i];
+    uintptr_t bits = reinterpret_cast<uintptr_t>(t.out) | uintptr_t(t.ld * (t.out_bf16 ? 2 : 4));
+    if (t.add != nullptr) bits |= reinterpret_cast<uintptr_t>(t.add) | uintptr_t(t.add_ld * (t.add_bf16 ? 2 : 4));
+    p.t[i] = {t.out, t.add, t.m, t.n, t.ld, t.add_ld, 0, 0, 0, align_of(bits), t.out_bf16, t.add_bf16};
+    pair_tiles += ((t.m + 255) / 256) * (q.epi == kEpiGated ? (t.n + 127) / 128 : (t.n + 255) / 256);
+    rows = std::max(rows, t.m);
+  }
+  if (q.pre.data != nullptr) {
+    uintptr_t bits = reinterpret_cast<uintptr_t>(q.pre.data) | reinterpret_cast<uintptr_t>(q.pre2.data);
+    if (q.pre.dtype != MO_MX8) bits |= uintptr_t(q.t[0].n * 2);
+    p.pre_align = align_of(bits);
+  }
+  // Few rows, or a long reduction and fewer tiles than half of the pairs: the reduction is split.
+  if ((rows <= 128 && !q.a_mn) || (pair_tiles * 2 < sms / 2 && p.blocks * q.segments >= 16)) return launch_narrow(q, p, sms, stream);
+  if (q.epi == kEpiGated) return launch_pair<kEpiGated, false, false>(q, p, sms, stream);
+  if (q.epi == kEpiGatedGrad) return launch_pair<kEpiGatedGrad, false, true>(q, p, sms, stream);
+  if (q.a_mn) return launch_pair<kEpiLinear, true, true>(q, p, sms, stream);
+  return q.b_mn ? launch_pair<kEpiLinear, false, true>(q, p, sms, stream) : launch_pair<kEpiLinear, false, false>(q, p, sms, stream);
+}
+
+}  // namespace mo

@@ -1,0 +1,289 @@
+// 8-bit activation checkpoints: e4m3 codes with a power of two for each 32
+// consecutive elements of a row, and what reads them on the way to a product.
+//
+//   code = e4m3(x 2^-e),  e the least with max |x| <= 448 2^e, e >= -127
+//
+// The scaling is exact, so a code is one rounding of x (at most 2^-4 of it, for
+// elements above 2^-14 of the block's largest), and code 2^e is a bf16 number:
+// products read the values without a second rounding.
+#include <cuda_runtime.h>
+
+#include "activation.cuh"
+#include "launch.cuh"
+#include "layer_kernels.h"
+
+namespace mo {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int64_t global_thread() { return int64_t(blockIdx.x) * kThreads + threadIdx.x; }
+
+// Four lanes a block of 32, eight elements a lane.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict__ x, int64_t groups, int64_t k, uint32_t nb,
+                                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t g = global_thread();
+  const uint32_t per_row = nb * 4u;
+  const int64_t row = g / per_row;
+  const int64_t col = int64_t(g - row * per_row) * 8;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  if (g < groups && col < k) load8(x + row * k + col, v);
+  float top = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < 7; i += 2) top = top3(top, v[i], v[i + 1]);
+  top = top2(top, fabsf(v[7]));
+  top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+  if (g >= groups) return;
+  const uint32_t s = mx8_scale(top);
+  const float down = mx8_down(s);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= down;
+  *reinterpret_cast<uint2*>(codes + g * 8) = make_uint2(cvt_e4m3x4(v[0], v[1], v[2], v[3]), cvt_e4m3x4(v[4], v[5], v[6], v[7]));
+  if ((g & 3) == 0) scales[g >> 2] = uint8_t(s);
+}
+
+// Rows that are not 16-byte aligned: a lane an element, a warp a block.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) quantize_odd_kernel(const T* __restrict__ x, int64_t blocks, int64_t k, uint32_t nb,
+                                                                uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = int(threadIdx.x & 31);
+  const int64_t b = global_thread() >> 5;
+  if (b >= blocks) return;
+  const int64_t row = b / nb, col = (b - row * nb) * 32 + lane;
+  const float v = col < k ? load1(x + row * k + col) : 0.0f;
+  float top = fabsf(v);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const uint32_t s = mx8_scale(top);
+  codes[b * 32 + lane] = uint8_t(cvt_e4m3x2(v * mx8_down(s), 0.0f));
+  if (lane == 0) scales[b] = uint8_t(s);
+}
+
+// Values of 8-bit codes, or of bf16 rows, into rows of `ld` elements: eight
+// elements a thread where the output's rows are 16-byte aligned. Elements past
+// k are not written.
+template <bool MX8, typename O>
+__global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restrict__ src, const uint8_t* __restrict__ scales,
+                                                          int64_t groups, int64_t k, uint32_t per_row, O* __restrict__ out, int64_t ld) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t g = global_thread();
+  if (g >= groups) return;
+  const int64_t row = g / per_row, col = (g - row * per_row) * 8;
+  float v[8];
+  if constexpr (MX8) {
+    const uint32_t nb = uint32_t((k + 31) / 32);
+    const uint2 w = *reinterpret_cast<const uint2*>(src + (row * nb * 32 + col));
+    const float up = mx8_up(scales[row * nb + (col >> 5)]);
+    float a[4], b[4];
+    e4m3x4_values(w.x, a);
+    e4m3x4_values(w.y, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i] * up;
+      v[4 + i] = b[i] * up;
+    }
+  } else {
+    const uint16_t* s = reinterpret_cast<const uint16_t*>(src) + row * k + col;
+    const int n = int(min(int64_t(8), k - col));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? load1(s + i) : 0.0f;
+  }
+  O* o = out + row * ld + col;
+  if (col + 8 <= k) {
+    store8(o, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < k) store1(o + i, v[i]);
+  }
+}
+
+// 8-bit codes into rows that are not 16-byte aligned: a lane an element.
+template <typename O>
+__global__ void __launch_bounds__(kThreads) unpack_odd_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                              int64_t blocks, int64_t k, uint32_t nb, O* __restrict__ out) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = int(threadIdx.x & 31);
+  const int64_t b = global_thread() >> 5;
+  if (b >= blocks) return;
+  const int64_t row = b / nb, col = (b - row * nb) * 32 + lane;
+  if (col < k) store1(out + row * k + col, e4m3_value(codes[b * 32 + lane]) * mx8_up(scales[b]));
+}
+
+// dz = dout act'(pre) and its column sums: a block takes 256 columns, eight a
+// thread, and `per` rows, eight at a time (one a warp); its warps' sums are
+// joined in order. A launch of strips x parts blocks.
+template <bool VEC, bool MX8, int ACT>
+__device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t row0, int64_t row1, int64_t col, float (&sum)[8]) {
+  const int64_t n = p.rows;
+  const uint32_t nb = uint32_t((n + 31) / 32);
+  for (int64_t r = row0 + (threadIdx.x >> 5); r < row1; r += 8) {
+    float d[8], z[8];
+    const uint16_t* src = p.dout + r * n;
+    if constexpr (VEC) {
+      if (col >= n) continue;
+      load8(src + col, d);
+      if constexpr (ACT != MO_ACT_NONE) {
+        if constexpr (MX8) {
+          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.pre.data) + r * nb * 32 + col);
+          const float up = mx8_up(p.pre.scales[r * nb + (col >> 5)]);
+          float a[4], b[4];
+          e4m3x4_values(w.x, a);
+          e4m3x4_values(w.y, b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            z[i] = a[i] * up;
+            z[4 + i] = b[i] * up;
+          }
+        } else {
+          load8(static_cast<const uint16_t*>(p.pre.data) + r * n + col, z);
+        }
+      }
+    } else {   // columns a warp apart
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t c = col + 32 * i;
+        d[i] = c < n ? load1(src + c) : 0.0f;
+        if constexpr (ACT != MO_ACT_NONE) {
+          z[i] = 0.0f;
+          if (c < n) {
+            if constexpr (MX8)
+              z[i] = e4m3_value(static_cast<const uint8_t*>(p.pre.data)[r * nb * 32 + c]) * mx8_up(p.pre.scales[r * nb + (c >> 5)]);
+            else
+              z[i] = load1(static_cast<const uint16_t*>(p.pre.data) + r * n + c);
+          }
+        }
+      }
+    }
+    if constexpr (ACT != MO_ACT_NONE) {
+      float value;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] *= act_slope<ACT>(z[i], &value);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += d[i];
+    if (p.dz != nullptr) {
+      uint16_t* o = p.dz + r * p.ld;
+      if constexpr (VEC) {
+        store8(o + col, d);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (col + 32 * i < n) store1(o + col + 32 * i, d[i]);
+      }
+    }
+  }
+}
+
+template <bool VEC, bool MX8>
+__global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams p) {
+  __shared__ float sums[8][256];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
+  const int64_t col = int64_t(blockIdx.x) * 256 + (VEC ? lane * 8 : lane);
+  const int64_t row0 = int64_t(blockIdx.y) * p.per, row1 = min(row0 + p.per, p.tokens);
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+  with_act(p.act, [&](auto act) { act_grad_rows<VEC, MX8, decltype(act)::value>(p, row0, row1, col, sum); });
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[warp][VEC ? lane * 8 + i : lane + 32 * i] = sum[i];
+  __syncthreads();
+  const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (c < p.rows) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
+    p.part[int64_t(blockIdx.y) * p.rows + c] = t;
+  }
+}
+
+// Column sums of part [parts, n]: a block takes 32 columns, a warp every eighth
+// row, and the eight sums are joined in order.
+__global__ void __launch_bounds__(kThreads) join_kernel(const float* __restrict__ part, int64_t parts, int64_t n, float* out,
+                                                        int accumulate) {
+  __shared__ float sums[8][32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
+  const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+  float t = 0.0f;
+  if (c < n)
+    for (int64_t r = warp; r < parts; r += 8) t += part[r * n + c];
+  sums[warp][lane] = t;
+  __syncthreads();
+  if (warp == 0 && c < n) {
+    t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += sums[w][lane];
+    out[c] = accumulate ? out[c] + t : t;
+  }
+}
+
+unsigned blocks_of(int64_t threads) { return unsigned((threads + kThreads - 1) / kThreads); }
+
+template <typename T>
+cudaError_t quantize_as(const T* x, int64_t rows, int64_t k, const Kept& q, cudaStream_t stream) {
+  const int64_t nb = mx8_blocks(k);
+  uint8_t* codes = static_cast<uint8_t*>(q.data);
+  if (k % 8 == 0) {
+    const int64_t groups = rows * nb * 4;
+    return launch_kernel(quantize_kernel<T>, dim3(blocks_of(groups)), dim3(kThreads), 0, 1, true, stream, x, groups, k,
+                         uint32_t(nb), codes, q.scales);
+  }
+  return launch_kernel(quantize_odd_kernel<T>, dim3(blocks_of(rows * nb * 32)), dim3(kThreads), 0, 1, true, stream, x, rows * nb, k,
+                       uint32_t(nb), codes, q.scales);
+}
+
+template <typename O>
+cudaError_t unpack_as(const Kept& src, int64_t rows, int64_t k, O* out, int64_t ld, cudaStream_t stream) {
+  const uint8_t* s = static_cast<const uint8_t*>(src.data);
+  if (ld % 8 == 0) {
+    const int64_t per_row = (k + 7) / 8, groups = rows * per_row;
+    auto kern = src.dtype == MO_MX8 ? unpack_kernel<true, O> : unpack_kernel<false, O>;
+    return launch_kernel(kern, dim3(blocks_of(groups)), dim3(kThreads), 0, 1, true, stream, s, static_cast<const uint8_t*>(src.scales),
+                         groups, k, uint32_t(per_row), out, ld);
+  }
+  const int64_t nb = mx8_blocks(k);
+  return launch_kernel(unpack_odd_kernel<O>, dim3(blocks_of(rows * nb * 32)), dim3(kThreads), 0, 1, true, stream, s,
+                       static_cast<const uint8_t*>(src.scales), rows * nb, k, uint32_t(nb), out);
+}
+
+}  // namespace
+
+cudaError_t launch_mx8_quantize(const void* x, bool bf16, int64_t rows, int64_t k, const Kept& q, cudaStream_t stream) {
+  return bf16 ? quantize_as(static_cast<const uint16_t*>(x), rows, k, q, stream)
+              : quantize_as(static_cast<const float*>(x), rows, k, q, stream);
+}
+
+cudaError_t launch_unpack(const Kept& src, int64_t rows, int64_t k, void* out, bool out_bf16, int64_t ld, cudaStream_t stream) {
+  return out_bf16 ? unpack_as(src, rows, k, static_cast<uint16_t*>(out), ld, stream)
+                  : unpack_as(src, rows, k, static_cast<float*>(out), ld, stream);
+}
+
+cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream) {
+  const dim3 grid(unsigned((p.rows + 255) / 256), unsigned((p.tokens + p.per - 1) / p.per));
+  const bool vec = p.rows % 8 == 0, mx8 = p.act != MO_ACT_NONE && p.pre.dtype == MO_MX8;
+  auto kern = vec ? (mx8 ? act_grad_kernel<true, true> : act_grad_kernel<true, false>)
+                  : (mx8 ? act_grad_kernel<false, true> : act_grad_kernel<false, false>);
+  return launch_kernel(kern, grid, dim3(kThreads), 0, 1, true, stream, p);
+}
+
+cudaError_t launch_join(const float* part, int64_t parts, int64_t n, float* out, bool accumulate, cudaStream_t stream) {
+  return launch_kernel(join_kernel, dim3(unsigned((n + 31) / 32)), dim3(kThreads), 0, 1, true, stream, part, parts, n, out,
+                       accumulate ? 1 : 0);
+}
+
+}  // namespace mo
