@@ -2,10 +2,11 @@
 // (e4m3 codes, a power of two for each 32 elements of a row).
 //
 // Logistic functions go through 2^x and a reciprocal of the special function
-// unit (__expf, __fdividef: a few units of 2^-23, relative, over the range
-// where the result is not 0 or 1 in fp32). gelu_tanh uses
-// 0.5 (1 + tanh(u)) = 1 / (1 + e^(-2u)), which loses nothing where tanh is near
-// -1. gelu's normal distribution function is erfcf's.
+// unit (a few units of 2^-23, relative, over the range where the result is not 0
+// or 1 in fp32), without the scaling that subnormal arguments would need: they
+// give 1 and infinity here. gelu_tanh uses 0.5 (1 + tanh(u)) = 1 / (1 + e^(-2u)),
+// which loses nothing where tanh is near -1. gelu's normal distribution function
+// is erfcf's.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -17,8 +18,27 @@ namespace mo {
 constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// 1 / (1 + e^-x); __fdividef gives 0 for divisors from 2^126 to infinity.
-__device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2E = 1.4426950408889634f;
+
+// 1 / (1 + 2^-x): 0 where 2^-x is infinite
+__device__ __forceinline__ float logistic2(float x) { return reciprocal_fast(1.0f + exp2_fast(-x)); }
+
+// max(x, -3.4e38), NaN if x is: times 0, where it was -infinity, it gives -0
+__device__ __forceinline__ float bounded(float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(-3.402823466e38f));
+  return r;
+}
 
 __device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(x * -0.70710678118654752f); }
 
@@ -26,10 +46,20 @@ __device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(x * -
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
   if constexpr (ACT == MO_ACT_RELU) return x > 0.0f ? x : (x != x ? x : 0.0f);
-  if constexpr (ACT == MO_ACT_GELU) return x == -INFINITY ? 0.0f : x * normal_cdf(x);
-  if constexpr (ACT == MO_ACT_GELU_TANH) return x == -INFINITY ? 0.0f : x * logistic(kGeluA * fmaf(kGeluB * x * x, x, x));
-  if constexpr (ACT == MO_ACT_SILU) return x == -INFINITY ? 0.0f : x * logistic(x);
+  if constexpr (ACT == MO_ACT_GELU) return bounded(x) * normal_cdf(x);
+  // the exponent is x (A + A B x^2) log2(e)
+  if constexpr (ACT == MO_ACT_GELU_TANH)
+    return bounded(x) * logistic2(x * fmaf(kGeluA * kGeluB * kLog2E, x * x, kGeluA * kLog2E));
+  if constexpr (ACT == MO_ACT_SILU) return bounded(x) * logistic2(x * kLog2E);
   return x;
+}
+
+// x between -96 and 96, where what the slopes are made of is 0 or 1 to fp32 (or
+// below 2^-126); NaN if x is
+__device__ __forceinline__ float clamped(float x) {
+  float r;
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(r) : "f"(x), "f"(-96.0f), "f"(96.0f));
+  return r;
 }
 
 // act'(x), and act(x) in *value
@@ -41,22 +71,22 @@ __device__ __forceinline__ float act_slope(float x, float* value) {
   }
   if constexpr (ACT == MO_ACT_GELU) {
     const float c = normal_cdf(x);
-    *value = x == -INFINITY ? 0.0f : x * c;
-    // x e^(-x^2 / 2) is 0 in fp32 from |x| = 15 on (and inf times 0 is not a number)
-    const float t = fabsf(x) < 16.0f ? x * __expf(-0.5f * x * x) : (x != x ? x : 0.0f);
+    *value = bounded(x) * c;
+    // x e^(-x^2 / 2) is 0 in fp32 from |x| = 15 on (and infinity times 0 is not a number)
+    const float t = fabsf(x) < 16.0f ? x * exp2_fast(-0.5f * kLog2E * x * x) : (x != x ? x : 0.0f);
     return fmaf(0.3989422804014327f, t, c);
   }
   if constexpr (ACT == MO_ACT_GELU_TANH) {
-    const float y = fminf(fmaxf(x, -64.0f), 64.0f), y2 = y * y;   // all 0 or 1 beyond
-    const float s = logistic(kGeluA * fmaf(kGeluB * y2, y, y));
-    *value = x == -INFINITY ? 0.0f : x * s;
-    return x != x ? x : fmaf(y * s * (1.0f - s), kGeluA * fmaf(3.0f * kGeluB, y2, 1.0f), s);
+    const float y = clamped(x), y2 = y * y;   // all 0 or 1 beyond
+    const float s = logistic2(y * fmaf(kGeluA * kGeluB * kLog2E, y2, kGeluA * kLog2E));
+    *value = bounded(x) * s;
+    return fmaf(fmaf(-s, s, s) * y, fmaf(3.0f * kGeluA * kGeluB, y2, kGeluA), s);
   }
   if constexpr (ACT == MO_ACT_SILU) {
-    const float s = logistic(x);
-    *value = x == -INFINITY ? 0.0f : x * s;
-    const float y = fminf(fmaxf(x, -128.0f), 128.0f);
-    return x != x ? x : fmaf(y * s, 1.0f - s, s);
+    const float y = clamped(x);
+    const float s = logistic2(y * kLog2E);
+    *value = bounded(x) * s;
+    return fmaf(fmaf(-s, s, s), y, s);
   }
   *value = x;
   return 1.0f;

@@ -24,10 +24,14 @@ struct GemmTarget {
 
 struct GemmParams {
   CUtensorMap a[3], b[3];
+  CUtensorMap bs[3];             // pairs: b in boxes of 32 rows (64 columns where its rows run along k), for cut tiles
   GemmTarget t[3];
   int32_t count, segments;
   int32_t blocks;                // stages a segment
-  int32_t tiles;                 // of all targets
+  int32_t tiles;                 // of all targets; pairs: with the cut ones counted as their parts
+  int32_t whole;                 // pairs: tiles that are not cut, in front of the others
+  int32_t cut;                   // pairs: parts of the others, side by side: 1, 2 or 4
+  int32_t early;                 // narrow: the columns' operand may be read before the previous launch has ended
   int32_t act;
   const float* bias;
   Kept pre, pre2;
@@ -214,41 +218,39 @@ __device__ __forceinline__ void keep_chunk(const Kept& q, int align, int64_t row
   q.scales[row * nb + (col >> 5)] = uint8_t(s);
 }
 
-// A kept chunk's raw words, loaded ahead of their use: 8-bit codes in the first
-// eight and the scale, or bf16. Chunks of bf16 rows that are not whole or not
-// aligned are read element by element.
+// 16 kept columns' raw words, loaded ahead of their use: 8-bit codes in the first
+// four and the scale, or bf16. bf16 that is not a whole chunk or not aligned is
+// read element by element.
 struct RawChunk {
-  uint32_t w[16];
+  uint32_t w[8];
   uint32_t scale;
 };
 __device__ __forceinline__ void fetch_kept(const Kept& q, int align, int64_t row, int64_t col, int64_t n, RawChunk& raw) {
   if (q.dtype == MO_MX8) {
     const int64_t nb = (n + 31) / 32;
-    const uint8_t* o = static_cast<const uint8_t*>(q.data) + row * nb * 32 + col;
-    const uint4 a = reinterpret_cast<const uint4*>(o)[0], b = reinterpret_cast<const uint4*>(o)[1];
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(q.data) + row * nb * 32 + col);
     raw.w[0] = a.x, raw.w[1] = a.y, raw.w[2] = a.z, raw.w[3] = a.w;
-    raw.w[4] = b.x, raw.w[5] = b.y, raw.w[6] = b.z, raw.w[7] = b.w;
     raw.scale = q.scales[row * nb + (col >> 5)];
   } else {
     const uint16_t* o = static_cast<const uint16_t*>(q.data) + row * n + col;
-    if (align != 0 && col + 32 <= n) {
+    if (align != 0 && col + 16 <= n) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
         const uint4 a = reinterpret_cast<const uint4*>(o)[j];
         raw.w[4 * j] = a.x, raw.w[4 * j + 1] = a.y, raw.w[4 * j + 2] = a.z, raw.w[4 * j + 3] = a.w;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
+      for (int j = 0; j < 8; ++j)
         raw.w[j] = (col + 2 * j < n ? uint32_t(o[2 * j]) : 0u) | (col + 2 * j + 1 < n ? uint32_t(o[2 * j + 1]) << 16 : 0u);
     }
   }
 }
-__device__ __forceinline__ void kept_values(const Kept& q, const RawChunk& raw, float (&v)[32]) {
+__device__ __forceinline__ void kept_values(const Kept& q, const RawChunk& raw, float (&v)[16]) {
   if (q.dtype == MO_MX8) {
     const float up = mx8_up(raw.scale);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       float x[4];
       e4m3x4_values(raw.w[j], x);
 #pragma unroll
@@ -256,11 +258,18 @@ __device__ __forceinline__ void kept_values(const Kept& q, const RawChunk& raw, 
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < 8; ++j) {
       v[2 * j] = __uint_as_float(raw.w[j] << 16);
       v[2 * j + 1] = __uint_as_float(raw.w[j] & 0xFFFF0000u);
     }
   }
+}
+// 16 bf16 in one 32-byte store
+__device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  ptx::st_global_v8(p, w);
 }
 // One element of a kept tensor of rows of n.
 __device__ __forceinline__ float kept_at(const Kept& q, int64_t row, int64_t col, int64_t n) {

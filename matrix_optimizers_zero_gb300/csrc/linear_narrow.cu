@@ -132,33 +132,51 @@ __global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_co
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  ptx::griddep_launch_dependents();   // after the TMEM is held: the next kernel's blocks take theirs before they wait
-  ptx::griddep_wait();
 
+  // Weights that no launch of this call writes need not wait for the one before this: its blocks let
+  // this kernel come only after they have waited in their turn, when all earlier launches had ended.
   uint32_t n_issued = 0;
   bool mma_issued = false;
+  auto load_p = [&](int32_t kb, uint32_t fb, uint32_t sp) {
+    const int seg = kb >= p.blocks ? 1 : 0;
+    const int32_t at = (kb - seg * p.blocks) * kBlockK;
+#pragma unroll
+    for (int i = 0; i < kPanels<EPI>; ++i) {
+      const CUtensorMap* mp = &p.b[EPI == kEpiGated ? i : p.segments > 1 ? seg : q];
+      const uint32_t s = sp + uint32_t(i) * kPanel;
+      if (P_MN) {
+        ptx::tma_load_2d(s, mp, fb, tn * 128, at);
+        ptx::tma_load_2d(s + kBox, mp, fb, tn * 128 + 64, at);
+      } else {
+        ptx::tma_load_2d(s, mp, fb, at, tn * 128);
+      }
+    }
+  };
+  int32_t ahead = k0;   // stages whose columns' operand is under way already
+  if (p.early && warp == 0 && lane == 0)
+    for (; ahead < min(k1, k0 + kStgs); ++ahead) {
+      const uint32_t fb = full_bar(ahead - k0);
+      ptx::mbar_arrive_expect_tx(fb, kStg);
+      load_p(ahead, fb, base + uint32_t(ahead - k0) * kStg);
+    }
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();   // with the TMEM held: the next kernel's blocks take theirs before they wait
+
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t ph = 0;
       for (int32_t kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait_bounded(empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
+        // (stages that are under way were free: nothing may leave them half filled)
+        if (kb >= ahead && !mbar_wait_bounded(empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
         const int seg = kb >= p.blocks ? 1 : 0;
         const int32_t at = (kb - seg * p.blocks) * kBlockK;
         const int op = p.segments > 1 ? seg : q;
         const uint32_t fb = full_bar(stage);
-        ptx::mbar_arrive_expect_tx(fb, kStg);
         const uint32_t sp = base + uint32_t(stage) * kStg, sq = sp + kQ;
-#pragma unroll
-        for (int i = 0; i < kPanels<EPI>; ++i) {
-          const CUtensorMap* mp = &p.b[EPI == kEpiGated ? i : op];
-          const uint32_t s = sp + uint32_t(i) * kPanel;
-          if (P_MN) {
-            ptx::tma_load_2d(s, mp, fb, tn * 128, at);
-            ptx::tma_load_2d(s + kBox, mp, fb, tn * 128 + 64, at);
-          } else {
-            ptx::tma_load_2d(s, mp, fb, at, tn * 128);
-          }
+        if (kb >= ahead) {
+          ptx::mbar_arrive_expect_tx(fb, kStg);
+          load_p(kb, fb, sp);
         }
         if (Q_MN) {
           ptx::tma_load_2d(sq, &p.a[op], fb, tm * NT, at);

@@ -47,31 +47,37 @@ __device__ __forceinline__ void tmem_chunk(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The 32 rows from row0 on (lane l has row0 + l) and this warp's half of the
-// tile's columns, from TMEM column `tb` on.
+// The 32 rows from row0 on (lane l has row0 + l) of the `width` accumulator
+// columns from TMEM column `tb` on: chunks of 32 (or 16) columns, every other one
+// each half's. col0: the first column of the output.
 template <Epilogue EPI>
-__device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& t, int64_t row0, int32_t tn, int half, uint32_t tb,
-                                         float* turn) {
+__device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& t, int64_t row0, int64_t col0, int width, int half,
+                                         uint32_t tb, float* turn) {
   const int lane = int(threadIdx.x & 31);
   const int64_t row = row0 + lane;
   if constexpr (EPI == kEpiLinear) {
 #pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-      const int64_t col = int64_t(tn) * 256 + half * 128 + ch * 32;
+    for (int c = half * 32; c < width; c += 64) {
+      const int64_t col = col0 + c;
+      float bias[32];   // under way while the accumulator is read
+      const bool whole = col + 32 <= t.n;
+      if (p.bias != nullptr && whole) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 b = reinterpret_cast<const float4*>(p.bias + col)[j];
+          bias[4 * j] = b.x, bias[4 * j + 1] = b.y, bias[4 * j + 2] = b.z, bias[4 * j + 3] = b.w;
+        }
+      }
       float v[32];
-      tmem_chunk(tb + uint32_t(half * 128 + ch * 32), v);
+      tmem_chunk(tb + uint32_t(c), v);
       if (row0 >= t.m || col >= t.n) continue;
       if (p.bias != nullptr) {
-        if (col + 32 <= t.n) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 b = reinterpret_cast<const float4*>(p.bias + col)[j];
-            v[4 * j] += b.x, v[4 * j + 1] += b.y, v[4 * j + 2] += b.z, v[4 * j + 3] += b.w;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (col + i < t.n) v[i] += p.bias[col + i];
+        for (int i = 0; i < 32; ++i) {
+          if (whole)
+            v[i] += bias[i];
+          else if (col + i < t.n)
+            v[i] += p.bias[col + i];
         }
       }
       if (p.pre.data != nullptr) keep_chunk(p.pre, p.pre_align, row0, t.m, col, t.n, v, turn);
@@ -84,11 +90,11 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
     }
   } else if constexpr (EPI == kEpiGated) {
 #pragma unroll 1
-    for (int ch = 0; ch < 2; ++ch) {
-      const int64_t col = int64_t(tn) * 128 + half * 64 + ch * 32;
+    for (int c = half * 32; c < width / 2; c += 64) {
+      const int64_t col = col0 + c;
       float g[32], u[32];
-      tmem_chunk(tb + uint32_t(half * 64 + ch * 32), g);
-      tmem_chunk(tb + uint32_t(128 + half * 64 + ch * 32), u);
+      tmem_chunk(tb + uint32_t(c), g);
+      tmem_chunk(tb + uint32_t(width / 2 + c), u);
       if (row0 >= t.m || col >= t.n) continue;
       if (p.pre.data != nullptr) {
         keep_chunk(p.pre, p.pre_align, row0, t.m, col, t.n, g, turn);
@@ -102,24 +108,33 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       if (row < t.m) store32(static_cast<uint16_t*>(t.out) + row * t.ld + col, 32, g);
     }
   } else {
-#pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-      const int64_t col = int64_t(tn) * 256 + half * 128 + ch * 32;
-      const bool in = row < t.m && col < t.n;
-      RawChunk rg, ru;
-      if (in) {
+    // The next chunk's g and u are loaded while one is worked on.
+    RawChunk rg, ru;
+    auto fetch = [&](int c) {
+      const int64_t col = col0 + c;
+      if (row < t.m && col < t.n) {
         fetch_kept(p.pre, p.pre_align, row, col, t.n, rg);
         fetch_kept(p.pre2, p.pre_align, row, col, t.n, ru);
       }
-      float dh[32];
-      tmem_chunk(tb + uint32_t(half * 128 + ch * 32), dh);
-      if (!in) continue;
-      float g[32], u[32];
+    };
+    fetch(half * 16);
+#pragma unroll 1
+    for (int c = half * 16; c < width; c += 32) {
+      const int64_t col = col0 + c;
+      float g[16], u[16], dh[16];
       kept_values(p.pre, rg, g);
       kept_values(p.pre2, ru, u);
+      if (c + 32 < width) fetch(c + 32);
+      uint32_t r[16];
+      __syncwarp();
+      ptx::tmem_ld_32x32b_x16(tb + uint32_t(c), r);
+      ptx::tmem_ld_wait();
+      if (row >= t.m || col >= t.n) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dh[i] = __uint_as_float(r[i]);
       with_act(p.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
           float a;
           const float slope = act_slope<decltype(act)::value>(g[i], &a);
           g[i] = dh[i] * u[i] * slope;
@@ -128,11 +143,29 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
         }
       });
       const int64_t at = row * t.ld + col;
-      store32(static_cast<uint16_t*>(t.out) + at, 32, g);
-      store32(p.out2 + at, 32, dh);
-      store32(p.out3 + at, 32, u);
+      store16(static_cast<uint16_t*>(t.out) + at, g);
+      store16(p.out2 + at, dh);
+      store16(p.out3 + at, u);
     }
   }
+}
+
+// A tile of the launch: the first are 256 columns wide, the last ones cut into
+// p.cut parts.
+struct Tile {
+  int q;              // target
+  int32_t tm, tn;
+  int32_t width, sub;   // accumulator columns, part
+};
+__device__ __forceinline__ Tile tile_of(const GemmParams& p, int32_t i) {
+  Tile t;
+  const int32_t over = i - p.whole;
+  const int32_t tile = over < 0 ? i : p.whole + over / p.cut;
+  t.sub = over < 0 ? 0 : over % p.cut;
+  t.width = over < 0 ? 256 : 256 / p.cut;
+  t.q = target_of(p, tile);
+  tile_at(p.t[t.q], tile, t.tm, t.tn);
+  return t;
 }
 
 template <Epilogue EPI, bool A_MN, bool B_MN>
@@ -195,12 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
       int stage = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int32_t tile = first; ok && tile < p.tiles; tile += step) {
-        const int q = target_of(p, tile);
-        int32_t tm, tn;
-        tile_at(p.t[q], tile, tm, tn);
-        const int32_t ra = tm * 256 + int32_t(rank) * 128;
-        const int32_t rb = EPI == kEpiGated ? tn * 128 : tn * 256 + int32_t(rank) * 128;
+      for (int32_t i = first; ok && i < p.tiles; i += step) {
+        const Tile t = tile_of(p, i);
+        const int32_t ra = t.tm * 256 + int32_t(rank) * 128;
+        const int32_t half = t.width / 2;   // this CTA's rows of B
+        const int32_t rb = EPI == kEpiGated ? t.tn * 128 + t.sub * half : t.tn * 256 + t.sub * t.width + int32_t(rank) * half;
         for (int32_t kb = 0; kb < blocks; ++kb) {
           if (!mbar_wait_bounded(empty_bar(stage), ph ^ 1u, abort_flag, p.status, p.timeout_ns)) {
             ok = false;
@@ -208,10 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
           }
           const int seg = kb >= p.blocks ? 1 : 0;
           const int32_t k0 = (kb - seg * p.blocks) * kBlockK;
-          const CUtensorMap* ma = &p.a[p.segments > 1 ? seg : q];
-          const CUtensorMap* mb = &p.b[EPI == kEpiGated ? int(rank) : p.segments > 1 ? seg : q];
+          const int op = p.segments > 1 ? seg : t.q, opb = EPI == kEpiGated ? int(rank) : op;
+          const CUtensorMap* ma = &p.a[op];
           const uint32_t fb_local = full_bar(stage);
-          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * kStage);
+          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * (kHalf + uint32_t(half) * 128u));
           const uint32_t fb = ptx::mapa_shared(fb_local, 0);
           const uint32_t sa = base + uint32_t(stage) * kStage, sb = sa + kHalf;
           if (A_MN) {
@@ -221,10 +253,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
             ptx::tma_load_2d_pair(sa, ma, fb, k0, ra);
           }
           if (B_MN) {
+            const CUtensorMap* mb = &p.b[opb];
             ptx::tma_load_2d_pair(sb, mb, fb, rb, k0);
-            ptx::tma_load_2d_pair(sb + kBox, mb, fb, rb + 64, k0);
+            if (half == 128) ptx::tma_load_2d_pair(sb + kBox, mb, fb, rb + 64, k0);
+          } else if (half == 128) {
+            ptx::tma_load_2d_pair(sb, &p.b[opb], fb, k0, rb);
           } else {
-            ptx::tma_load_2d_pair(sb, mb, fb, k0, rb);
+            for (int32_t j = 0; j < half; j += 32) ptx::tma_load_2d_pair(sb + uint32_t(j) * 128u, &p.bs[opb], fb, k0, rb + j);
           }
           ++n_issued;
           if (++stage == kStages) {
@@ -237,14 +272,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ MMA issuer (even CTA)
-      constexpr uint32_t idesc = ptx::idesc_bf16_f32(256, 256, A_MN ? 1u : 0u, B_MN ? 1u : 0u);
       int stage = 0;
       uint32_t ph = 0;
       bool ok = true;
-      int32_t i = 0;
-      for (int32_t tile = first; ok && tile < p.tiles; tile += step, ++i) {
-        const int acc = i & 1;
-        if (!mbar_wait_bounded<true>(tempty_bar(acc), (uint32_t(i >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
+      int32_t n = 0;
+      for (int32_t i = first; ok && i < p.tiles; i += step, ++n) {
+        const int acc = n & 1;
+        const uint32_t width = i < p.whole ? 256u : 256u / uint32_t(p.cut);
+        const uint32_t idesc = ptx::idesc_bf16_f32(256, 0, A_MN ? 1u : 0u, B_MN ? 1u : 0u) | ((width >> 3) << 17);
+        if (!mbar_wait_bounded<true>(tempty_bar(acc), (uint32_t(n >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc) * 256u;
         for (int32_t kb = 0; kb < blocks; ++kb) {
@@ -279,18 +315,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
     const int quarter = warp & 3;
     const int half = (warp - 2) >> 2;
     float* turn = reinterpret_cast<float*>(smem_raw + (bars - raw) + kCtrl) + (warp - 2) * kTurn;
-    int32_t i = 0;
-    for (int32_t tile = first; tile < p.tiles; tile += step, ++i) {
-      const int acc = i & 1;
-      const GemmTarget& t = p.t[target_of(p, tile)];
-      int32_t tm, tn;
-      tile_at(t, tile, tm, tn);
-      bool ok = mbar_wait_bounded(tfull_bar(acc), uint32_t(i >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
+    int32_t n = 0;
+    for (int32_t i = first; i < p.tiles; i += step, ++n) {
+      const int acc = n & 1;
+      const Tile t = tile_of(p, i);
+      bool ok = mbar_wait_bounded(tfull_bar(acc), uint32_t(n >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       ptx::tc_fence_after();
-      const int64_t row0 = int64_t(tm) * 256 + int64_t(rank) * 128 + quarter * 32;
-      epilogue<EPI>(p, t, row0, tn, half, tmem + uint32_t(acc) * 256u + (uint32_t(quarter * 32) << 16), turn);
+      const int64_t row0 = int64_t(t.tm) * 256 + int64_t(rank) * 128 + quarter * 32;
+      const int64_t col0 = EPI == kEpiGated ? int64_t(t.tn) * 128 + t.sub * (t.width / 2) : int64_t(t.tn) * 256 + t.sub * t.width;
+      epilogue<EPI>(p, p.t[t.q], row0, col0, t.width, half, tmem + uint32_t(acc) * 256u + (uint32_t(quarter * 32) << 16), turn);
       // hand the accumulator back: its reads are complete (tcgen05.wait::ld) and fenced, and nothing
       // else of the tile has to be ordered inside the launch
       ptx::tc_fence_before();
@@ -317,12 +352,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
     if (leader && threadIdx.x == 0) {
       const uint32_t L = n_issued, P = peer_report[1];
       const uint32_t most = L > P ? L : P;
+      // stages of this pair's uncut tiles, which come first
+      const uint32_t wide = first < p.whole ? uint32_t((p.whole - first + step - 1) / step) * uint32_t(blocks) : 0u;
       for (uint32_t j = most > uint32_t(kStages) ? most - uint32_t(kStages) : 0u; j < most; ++j) {
         const int s = int(j % uint32_t(kStages));
+        const uint32_t bytes = kHalf + (j < wide ? kHalf : kHalf / uint32_t(p.cut));
         if (j >= L)
-          ptx::mbar_arrive_expect_tx(full_bar(s), kStage);   // only the peer's half is coming
+          ptx::mbar_arrive_expect_tx(full_bar(s), bytes);   // only the peer's half is coming
         else if (j >= P)
-          ptx::mbar_complete_tx(full_bar(s), kStage);        // the peer's half never will
+          ptx::mbar_complete_tx(full_bar(s), bytes);        // the peer's half never will
         mbar_wait_drain(full_bar(s), (j / uint32_t(kStages)) & 1u, p.timeout_ns);
       }
     }
@@ -354,7 +392,9 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
   const int n = std::max(q.count, q.segments);
   for (int i = 0; i < 3; ++i) {
     if (i < n && !encode_operand(&p.a[i], q.a[i], A_MN ? 64 : 128)) return cudaErrorInvalidValue;
-    if (i < (EPI == kEpiGated ? 2 : n) && !encode_operand(&p.b[i], q.b[i], B_MN ? 64 : 128)) return cudaErrorInvalidValue;
+    if (i < (EPI == kEpiGated ? 2 : n) &&
+        (!encode_operand(&p.b[i], q.b[i], B_MN ? 64 : 128) || (!B_MN && !encode_operand(&p.bs[i], q.b[i], 32))))
+      return cudaErrorInvalidValue;
   }
   int64_t tiles = 0;
   for (int i = 0; i < q.count; ++i) {
@@ -365,11 +405,16 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
     tiles += int64_t(t.tiles_m) * t.tiles_n;
   }
   if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
-  p.tiles = int32_t(tiles);
+  // The tiles of a last round that leaves half of the pairs idle, or three quarters, are cut into as
+  // many parts. (Parts of 64 columns not where B's rows run along k: its boxes are 64 wide a CTA.)
+  const int64_t pairs = sms / 2, last = tiles % pairs;
+  p.cut = last * 2 > pairs || last == 0 ? 1 : !B_MN && last * 4 <= pairs ? 4 : 2;
+  p.whole = int32_t(p.cut > 1 ? tiles - last : tiles);
+  p.tiles = int32_t(p.cut > 1 ? tiles + last * (p.cut - 1) : tiles);
   auto kern = linear_pair_kernel<EPI, A_MN, B_MN>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = unsigned(2 * std::min<int64_t>(sms / 2, tiles));
+  const unsigned grid = unsigned(2 * std::min<int64_t>(pairs, p.tiles));
   return launch_kernel(kern, dim3(grid), dim3(kThreads), kSmem, 2, true, stream, p);
 }
 
@@ -387,6 +432,17 @@ bool encode_operand(CUtensorMap* map, const Operand& o, uint32_t box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Few rows, or a long reduction and fewer tiles than half of the pairs: the reduction is split.
+bool is_narrow(const Product& q, int sms) {
+  int64_t pair_tiles = 0, rows = 0;
+  for (int i = 0; i < q.count; ++i) {
+    const Target& t = q.t[i];
+    pair_tiles += ((t.m + 255) / 256) * (q.epi == kEpiGated ? (t.n + 127) / 128 : (t.n + 255) / 256);
+    rows = std::max(rows, t.m);
+  }
+  return (rows <= 128 && !q.a_mn) || (pair_tiles * 2 < sms / 2 && (q.k + kBlockK - 1) / kBlockK * q.segments >= 16);
+}
+
 cudaError_t launch_product(const Product& q, int sms, int* status, cudaStream_t stream) {
   GemmParams p = {};
   p.count = q.count;
@@ -401,22 +457,19 @@ cudaError_t launch_product(const Product& q, int sms, int* status, cudaStream_t 
   p.status = status;
   p.timeout_ns = kDefaultTimeoutNs;
   auto align_of = [](uintptr_t bits) { return (bits & 31) == 0 ? 32 : (bits & 15) == 0 ? 16 : 0; };
-  int64_t pair_tiles = 0, rows = 0;
+  p.early = q.early;
   for (int i = 0; i < q.count; ++i) {
     const Target& t = q.t[i];
     uintptr_t bits = reinterpret_cast<uintptr_t>(t.out) | uintptr_t(t.ld * (t.out_bf16 ? 2 : 4));
     if (t.add != nullptr) bits |= reinterpret_cast<uintptr_t>(t.add) | uintptr_t(t.add_ld * (t.add_bf16 ? 2 : 4));
     p.t[i] = {t.out, t.add, t.m, t.n, t.ld, t.add_ld, 0, 0, 0, align_of(bits), t.out_bf16, t.add_bf16};
-    pair_tiles += ((t.m + 255) / 256) * (q.epi == kEpiGated ? (t.n + 127) / 128 : (t.n + 255) / 256);
-    rows = std::max(rows, t.m);
   }
   if (q.pre.data != nullptr) {
     uintptr_t bits = reinterpret_cast<uintptr_t>(q.pre.data) | reinterpret_cast<uintptr_t>(q.pre2.data);
     if (q.pre.dtype != MO_MX8) bits |= uintptr_t(q.t[0].n * 2);
     p.pre_align = align_of(bits);
   }
-  // Few rows, or a long reduction and fewer tiles than half of the pairs: the reduction is split.
-  if ((rows <= 128 && !q.a_mn) || (pair_tiles * 2 < sms / 2 && p.blocks * q.segments >= 16)) return launch_narrow(q, p, sms, stream);
+  if (is_narrow(q, sms)) return launch_narrow(q, p, sms, stream);
   if (q.epi == kEpiGated) return launch_pair<kEpiGated, false, false>(q, p, sms, stream);
   if (q.epi == kEpiGatedGrad) return launch_pair<kEpiGatedGrad, false, true>(q, p, sms, stream);
   if (q.a_mn) return launch_pair<kEpiLinear, true, true>(q, p, sms, stream);

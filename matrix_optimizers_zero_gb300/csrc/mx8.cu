@@ -19,33 +19,61 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ int64_t global_thread() { return int64_t(blockIdx.x) * kThreads + threadIdx.x; }
 
-// Four lanes a block of 32, eight elements a lane.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict__ x, int64_t groups, int64_t k, uint32_t nb,
+// Row and column of the first element of group g, where a row has `per_row`
+// groups of eight. 64-bit divisions take longer than the rest of a thread.
+__device__ __forceinline__ void place(int64_t g, uint32_t per_row, int64_t& row, int64_t& col) {
+  if (g >> 32 == 0) {
+    const uint32_t q = uint32_t(g) / per_row;
+    row = q;
+    col = int64_t(uint32_t(g) - q * per_row) * 8;
+  } else {
+    row = g / per_row;
+    col = (g - row * per_row) * 8;
+  }
+}
+
+constexpr int kQuantGroups = 4;   // groups of eight a thread, a block's threads apart: their loads are under way together
+
+// Four lanes a block of 32, eight elements a lane. FLAT: rows of whole blocks,
+// which need no row and column.
+template <typename T, bool FLAT>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict__ x, int64_t groups, int64_t k, uint32_t per_row,
                                                             uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int64_t g = global_thread();
-  const uint32_t per_row = nb * 4u;
-  const int64_t row = g / per_row;
-  const int64_t col = int64_t(g - row * per_row) * 8;
-  float v[8];
+  const int64_t g0 = int64_t(blockIdx.x) * (kThreads * kQuantGroups) + threadIdx.x;
+  float v[kQuantGroups][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  if (g < groups && col < k) load8(x + row * k + col, v);
-  float top = fabsf(v[0]);
+  for (int q = 0; q < kQuantGroups; ++q) {
+    const int64_t g = g0 + q * kThreads;
 #pragma unroll
-  for (int i = 1; i < 7; i += 2) top = top3(top, v[i], v[i + 1]);
-  top = top2(top, fabsf(v[7]));
-  top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-  top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-  if (g >= groups) return;
-  const uint32_t s = mx8_scale(top);
-  const float down = mx8_down(s);
+    for (int i = 0; i < 8; ++i) v[q][i] = 0.0f;
+    if (FLAT) {
+      if (g < groups) load8(x + g * 8, v[q]);
+    } else {
+      int64_t row, col;
+      place(g, per_row, row, col);
+      if (g < groups && col < k) load8(x + row * k + col, v[q]);
+    }
+  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= down;
-  *reinterpret_cast<uint2*>(codes + g * 8) = make_uint2(cvt_e4m3x4(v[0], v[1], v[2], v[3]), cvt_e4m3x4(v[4], v[5], v[6], v[7]));
-  if ((g & 3) == 0) scales[g >> 2] = uint8_t(s);
+  for (int q = 0; q < kQuantGroups; ++q) {
+    const int64_t g = g0 + q * kThreads;
+    float top = fabsf(v[q][0]);
+#pragma unroll
+    for (int i = 1; i < 7; i += 2) top = top3(top, v[q][i], v[q][i + 1]);
+    top = top2(top, fabsf(v[q][7]));
+    top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    if (g >= groups) continue;   // (whole groups of four lanes)
+    const uint32_t s = mx8_scale(top);
+    const float down = mx8_down(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[q][i] *= down;
+    *reinterpret_cast<uint2*>(codes + g * 8) =
+        make_uint2(cvt_e4m3x4(v[q][0], v[q][1], v[q][2], v[q][3]), cvt_e4m3x4(v[q][4], v[q][5], v[q][6], v[q][7]));
+    if ((g & 3) == 0) scales[g >> 2] = uint8_t(s);
+  }
 }
 
 // Rows that are not 16-byte aligned: a lane an element, a warp a block.
@@ -57,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) quantize_odd_kernel(const T* __restr
   const int lane = int(threadIdx.x & 31);
   const int64_t b = global_thread() >> 5;
   if (b >= blocks) return;
-  const int64_t row = b / nb, col = (b - row * nb) * 32 + lane;
+  const int64_t row = b >> 32 == 0 ? int64_t(uint32_t(b) / nb) : b / nb, col = (b - row * nb) * 32 + lane;
   const float v = col < k ? load1(x + row * k + col) : 0.0f;
   float top = fabsf(v);
 #pragma unroll
@@ -65,6 +93,40 @@ __global__ void __launch_bounds__(kThreads) quantize_odd_kernel(const T* __restr
   const uint32_t s = mx8_scale(top);
   codes[b * 32 + lane] = uint8_t(cvt_e4m3x2(v * mx8_down(s), 0.0f));
   if (lane == 0) scales[b] = uint8_t(s);
+}
+
+// Values of 8-bit codes into dense rows of whole blocks, eight a thread and group.
+template <typename O>
+__global__ void __launch_bounds__(kThreads) unpack_flat_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                               int64_t groups, O* __restrict__ out) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t g0 = int64_t(blockIdx.x) * (kThreads * kQuantGroups) + threadIdx.x;
+  uint2 w[kQuantGroups];
+  uint8_t s[kQuantGroups];
+#pragma unroll
+  for (int q = 0; q < kQuantGroups; ++q) {
+    const int64_t g = g0 + q * kThreads;
+    if (g < groups) {
+      w[q] = *reinterpret_cast<const uint2*>(codes + g * 8);
+      s[q] = scales[g >> 2];
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kQuantGroups; ++q) {
+    const int64_t g = g0 + q * kThreads;
+    if (g >= groups) break;
+    const float up = mx8_up(s[q]);
+    float a[4], b[4], v[8];
+    e4m3x4_values(w[q].x, a);
+    e4m3x4_values(w[q].y, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i] * up;
+      v[4 + i] = b[i] * up;
+    }
+    store8(out + g * 8, v);
+  }
 }
 
 // Values of 8-bit codes, or of bf16 rows, into rows of `ld` elements: eight
@@ -77,7 +139,8 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restr
   ptx::griddep_wait();
   const int64_t g = global_thread();
   if (g >= groups) return;
-  const int64_t row = g / per_row, col = (g - row * per_row) * 8;
+  int64_t row, col;
+  place(g, per_row, row, col);
   float v[8];
   if constexpr (MX8) {
     const uint32_t nb = uint32_t((k + 31) / 32);
@@ -116,71 +179,94 @@ __global__ void __launch_bounds__(kThreads) unpack_odd_kernel(const uint8_t* __r
   const int lane = int(threadIdx.x & 31);
   const int64_t b = global_thread() >> 5;
   if (b >= blocks) return;
-  const int64_t row = b / nb, col = (b - row * nb) * 32 + lane;
+  const int64_t row = b >> 32 == 0 ? int64_t(uint32_t(b) / nb) : b / nb, col = (b - row * nb) * 32 + lane;
   if (col < k) store1(out + row * k + col, e4m3_value(codes[b * 32 + lane]) * mx8_up(scales[b]));
 }
 
 // dz = dout act'(pre) and its column sums: a block takes 256 columns, eight a
 // thread, and `per` rows, eight at a time (one a warp); its warps' sums are
 // joined in order. A launch of strips x parts blocks.
-template <bool VEC, bool MX8, int ACT>
+constexpr int kRowsAhead = 4;   // of a warp, loaded together
+
+template <bool MX8, int ACT>
 __device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t row0, int64_t row1, int64_t col, float (&sum)[8]) {
   const int64_t n = p.rows;
+  if (col >= n) return;
   const uint32_t nb = uint32_t((n + 31) / 32);
-  for (int64_t r = row0 + (threadIdx.x >> 5); r < row1; r += 8) {
-    float d[8], z[8];
-    const uint16_t* src = p.dout + r * n;
-    if constexpr (VEC) {
-      if (col >= n) continue;
-      load8(src + col, d);
+  for (int64_t first = row0 + (threadIdx.x >> 5); first < row1; first += 8 * kRowsAhead) {
+    uint4 dout[kRowsAhead], pre[kRowsAhead];   // (pre: two words of 8-bit codes and the scale)
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      const int64_t r = first + 8 * u;
+      if (r >= row1) break;
+      dout[u] = *reinterpret_cast<const uint4*>(p.dout + r * n + col);
       if constexpr (ACT != MO_ACT_NONE) {
         if constexpr (MX8) {
           const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.pre.data) + r * nb * 32 + col);
-          const float up = mx8_up(p.pre.scales[r * nb + (col >> 5)]);
+          pre[u] = make_uint4(w.x, w.y, p.pre.scales[r * nb + (col >> 5)], 0u);
+        } else {
+          pre[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.pre.data) + r * n + col);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      const int64_t r = first + 8 * u;
+      if (r >= row1) break;
+      float d[8];
+      load8(reinterpret_cast<const uint16_t*>(&dout[u]), d);
+      if constexpr (ACT != MO_ACT_NONE) {
+        float z[8], value;
+        if constexpr (MX8) {
+          const float up = mx8_up(pre[u].z);
           float a[4], b[4];
-          e4m3x4_values(w.x, a);
-          e4m3x4_values(w.y, b);
+          e4m3x4_values(pre[u].x, a);
+          e4m3x4_values(pre[u].y, b);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             z[i] = a[i] * up;
             z[4 + i] = b[i] * up;
           }
         } else {
-          load8(static_cast<const uint16_t*>(p.pre.data) + r * n + col, z);
+          load8(reinterpret_cast<const uint16_t*>(&pre[u]), z);
         }
-      }
-    } else {   // columns a warp apart
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t c = col + 32 * i;
-        d[i] = c < n ? load1(src + c) : 0.0f;
-        if constexpr (ACT != MO_ACT_NONE) {
-          z[i] = 0.0f;
-          if (c < n) {
-            if constexpr (MX8)
-              z[i] = e4m3_value(static_cast<const uint8_t*>(p.pre.data)[r * nb * 32 + c]) * mx8_up(p.pre.scales[r * nb + (c >> 5)]);
-            else
-              z[i] = load1(static_cast<const uint16_t*>(p.pre.data) + r * n + c);
-          }
+        for (int i = 0; i < 8; ++i) d[i] *= act_slope<ACT>(z[i], &value);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += d[i];
+      if (p.dz != nullptr) store8(p.dz + r * p.ld + col, d);
+    }
+  }
+}
+
+// Rows that are not 16-byte aligned: a thread's eight columns are a warp apart.
+template <bool MX8, int ACT>
+__device__ __forceinline__ void act_grad_rows_odd(const ActGradParams& p, int64_t row0, int64_t row1, int64_t col, float (&sum)[8]) {
+  const int64_t n = p.rows;
+  const uint32_t nb = uint32_t((n + 31) / 32);
+  for (int64_t r = row0 + (threadIdx.x >> 5); r < row1; r += 8) {
+    float d[8], z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = col + 32 * i;
+      d[i] = c < n ? load1(p.dout + r * n + c) : 0.0f;
+      z[i] = 0.0f;
+      if constexpr (ACT != MO_ACT_NONE) {
+        if (c < n) {
+          if constexpr (MX8)
+            z[i] = e4m3_value(static_cast<const uint8_t*>(p.pre.data)[r * nb * 32 + c]) * mx8_up(p.pre.scales[r * nb + (c >> 5)]);
+          else
+            z[i] = load1(static_cast<const uint16_t*>(p.pre.data) + r * n + c);
         }
       }
     }
-    if constexpr (ACT != MO_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
       float value;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] *= act_slope<ACT>(z[i], &value);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] += d[i];
-    if (p.dz != nullptr) {
-      uint16_t* o = p.dz + r * p.ld;
-      if constexpr (VEC) {
-        store8(o + col, d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (col + 32 * i < n) store1(o + col + 32 * i, d[i]);
-      }
+      if constexpr (ACT != MO_ACT_NONE) d[i] *= act_slope<ACT>(z[i], &value);
+      sum[i] += d[i];
+      if (p.dz != nullptr && col + 32 * i < n) store1(p.dz + r * p.ld + col + 32 * i, d[i]);
     }
   }
 }
@@ -196,7 +282,13 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams 
   float sum[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
-  with_act(p.act, [&](auto act) { act_grad_rows<VEC, MX8, decltype(act)::value>(p, row0, row1, col, sum); });
+  with_act(p.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    if constexpr (VEC)
+      act_grad_rows<MX8, ACT>(p, row0, row1, col, sum);
+    else
+      act_grad_rows_odd<MX8, ACT>(p, row0, row1, col, sum);
+  });
   if (p.part == nullptr) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) sums[warp][VEC ? lane * 8 + i : lane + 32 * i] = sum[i];
@@ -210,29 +302,35 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams 
   }
 }
 
-// Column sums of part [parts, n]: a block takes 32 columns, a warp every eighth
-// row, and the eight sums are joined in order.
-__global__ void __launch_bounds__(kThreads) join_kernel(const float* __restrict__ part, int64_t parts, int64_t n, float* out,
-                                                        int accumulate) {
-  __shared__ float sums[8][32];
+// Column sums of part [parts, n]: a block takes 32 columns, each of its warps a
+// run of rows in order, and the warps' sums are joined in order.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const float* __restrict__ part, int64_t parts, int64_t n, float* out,
+                                                               int accumulate) {
+  __shared__ float sums[kJoinWarps][33];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
   const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+  const int64_t per = (parts + kJoinWarps - 1) / kJoinWarps, r1 = min((warp + 1) * per, parts);
   float t = 0.0f;
-  if (c < n)
-    for (int64_t r = warp; r < parts; r += 8) t += part[r * n + c];
+  if (c < n) {
+#pragma unroll 8
+    for (int64_t r = warp * per; r < r1; ++r) t += part[r * n + c];
+  }
   sums[warp][lane] = t;
   __syncthreads();
-  if (warp == 0 && c < n) {
-    t = 0.0f;
+  // warp w: column w, a lane for each run
+  t = sums[lane][warp];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += sums[w][lane];
-    out[c] = accumulate ? out[c] + t : t;
-  }
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  const int64_t col = int64_t(blockIdx.x) * 32 + warp;
+  if (lane == 0 && col < n) out[col] = accumulate ? out[col] + t : t;
 }
 
 unsigned blocks_of(int64_t threads) { return unsigned((threads + kThreads - 1) / kThreads); }
+
+unsigned quant_blocks(int64_t groups) { return unsigned((groups + kThreads * kQuantGroups - 1) / (kThreads * kQuantGroups)); }
 
 template <typename T>
 cudaError_t quantize_as(const T* x, int64_t rows, int64_t k, const Kept& q, cudaStream_t stream) {
@@ -240,8 +338,9 @@ cudaError_t quantize_as(const T* x, int64_t rows, int64_t k, const Kept& q, cuda
   uint8_t* codes = static_cast<uint8_t*>(q.data);
   if (k % 8 == 0) {
     const int64_t groups = rows * nb * 4;
-    return launch_kernel(quantize_kernel<T>, dim3(blocks_of(groups)), dim3(kThreads), 0, 1, true, stream, x, groups, k,
-                         uint32_t(nb), codes, q.scales);
+    auto kern = k % 32 == 0 ? quantize_kernel<T, true> : quantize_kernel<T, false>;
+    return launch_kernel(kern, dim3(quant_blocks(groups)), dim3(kThreads), 0, 1, true, stream, x, groups, k, uint32_t(nb * 4), codes,
+                         q.scales);
   }
   return launch_kernel(quantize_odd_kernel<T>, dim3(blocks_of(rows * nb * 32)), dim3(kThreads), 0, 1, true, stream, x, rows * nb, k,
                        uint32_t(nb), codes, q.scales);
@@ -250,15 +349,19 @@ cudaError_t quantize_as(const T* x, int64_t rows, int64_t k, const Kept& q, cuda
 template <typename O>
 cudaError_t unpack_as(const Kept& src, int64_t rows, int64_t k, O* out, int64_t ld, cudaStream_t stream) {
   const uint8_t* s = static_cast<const uint8_t*>(src.data);
+  const uint8_t* scales = src.scales;
+  if (src.dtype == MO_MX8 && ld == k && k % 32 == 0)
+    return launch_kernel(unpack_flat_kernel<O>, dim3(quant_blocks(rows * k / 8)), dim3(kThreads), 0, 1, true, stream, s, scales,
+                         rows * k / 8, out);
   if (ld % 8 == 0) {
     const int64_t per_row = (k + 7) / 8, groups = rows * per_row;
     auto kern = src.dtype == MO_MX8 ? unpack_kernel<true, O> : unpack_kernel<false, O>;
-    return launch_kernel(kern, dim3(blocks_of(groups)), dim3(kThreads), 0, 1, true, stream, s, static_cast<const uint8_t*>(src.scales),
-                         groups, k, uint32_t(per_row), out, ld);
+    return launch_kernel(kern, dim3(blocks_of(groups)), dim3(kThreads), 0, 1, true, stream, s, scales, groups, k, uint32_t(per_row), out,
+                         ld);
   }
   const int64_t nb = mx8_blocks(k);
-  return launch_kernel(unpack_odd_kernel<O>, dim3(blocks_of(rows * nb * 32)), dim3(kThreads), 0, 1, true, stream, s,
-                       static_cast<const uint8_t*>(src.scales), rows * nb, k, uint32_t(nb), out);
+  return launch_kernel(unpack_odd_kernel<O>, dim3(blocks_of(rows * nb * 32)), dim3(kThreads), 0, 1, true, stream, s, scales, rows * nb, k,
+                       uint32_t(nb), out);
 }
 
 }  // namespace
@@ -282,7 +385,7 @@ cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_join(const float* part, int64_t parts, int64_t n, float* out, bool accumulate, cudaStream_t stream) {
-  return launch_kernel(join_kernel, dim3(unsigned((n + 31) / 32)), dim3(kThreads), 0, 1, true, stream, part, parts, n, out,
+  return launch_kernel(join_kernel, dim3(unsigned((n + 31) / 32)), dim3(32 * kJoinWarps), 0, 1, true, stream, part, parts, n, out,
                        accumulate ? 1 : 0);
 }
 

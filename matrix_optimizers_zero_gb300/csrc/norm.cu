@@ -4,7 +4,7 @@
 //   s = x + residual,  r = 1 / sqrt(mean(s^2) + eps),  y = s r w
 //   g = dy w:  dx = r (g - s r mean(g s r)) + dres,  dw = sum over rows of dy s r
 //
-// A team of threads takes a row, keeps it in registers and reads it once: the
+// A team of threads takes a row, eight elements a thread, and reads it once: the
 // backward pass needs the two sums of s^2 and of g s, which one reduction
 // gives. A team of the backward pass goes from row to row and adds its part of
 // dw in registers; the teams' parts are joined in order, so results do not
@@ -50,36 +50,6 @@ __device__ __forceinline__ void load_row(const T* p, int64_t dim, int t, float (
     for (int i = 0; i < V; ++i) {
       const int64_t c = column<TEAM, VEC>(i, t);
       v[i] = c < dim ? load1(p + c) : 0.0f;
-    }
-  }
-}
-
-template <int TEAM, int V, bool VEC>
-__device__ __forceinline__ void load_row_mx8(const uint8_t* codes, const uint8_t* scales, int64_t dim, int t, float (&v)[V]) {
-  if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < V; i += 8) {
-      const int64_t c = column<TEAM, VEC>(i, t);
-      uint2 w = make_uint2(0u, 0u);
-      float up = 0.0f;
-      if (c < dim) {
-        w = *reinterpret_cast<const uint2*>(codes + c);
-        up = mx8_up(scales[c >> 5]);
-      }
-      float a[4], b[4];
-      e4m3x4_values(w.x, a);
-      e4m3x4_values(w.y, b);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[i + j] = a[j] * up;
-        v[i + 4 + j] = b[j] * up;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int64_t c = column<TEAM, VEC>(i, t);
-      v[i] = c < dim ? e4m3_value(codes[c]) * mx8_up(scales[c >> 5]) : 0.0f;
     }
   }
 }
@@ -202,14 +172,127 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_kernel(const NormParams p) 
   }
 }
 
+// A row as it lies in memory, loaded while the one before it is worked on.
+template <int V, bool VEC, typename T>
+struct RawRow {
+  using Word = typename std::conditional<VEC, uint4, T>::type;
+  static constexpr int kWords = VEC ? V * int(sizeof(T)) / 16 : V;
+  Word w[kWords];
+};
+template <int V, bool VEC>
+struct RawRow8 {
+  using Word = typename std::conditional<VEC, uint2, uint8_t>::type;
+  Word w[VEC ? V / 8 : V];
+  uint8_t scale[VEC ? V / 8 : V];
+};
+
 template <int TEAM, int V, bool VEC, typename T>
-__global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_kernel(const NormGradParams p) {
-  __shared__ float shared[64];
+__device__ __forceinline__ void fetch_row(const T* p, int64_t dim, int t, RawRow<V, VEC, T>& raw) {
+  if constexpr (VEC) {
+    constexpr int kPer = 8 * int(sizeof(T)) / 16;   // words of eight elements
+#pragma unroll
+    for (int i = 0; i < V; i += 8) {
+      const int64_t c = column<TEAM, VEC>(i, t);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        raw.w[i / 8 * kPer + j] = c < dim ? reinterpret_cast<const uint4*>(p + c)[j] : make_uint4(0u, 0u, 0u, 0u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int64_t c = column<TEAM, VEC>(i, t);
+      raw.w[i] = c < dim ? p[c] : T(0);
+    }
+  }
+}
+template <int TEAM, int V, bool VEC>
+__device__ __forceinline__ void fetch_row(const uint8_t* codes, const uint8_t* scales, int64_t dim, int t, RawRow8<V, VEC>& raw) {
+#pragma unroll
+  for (int i = 0; i < V; i += VEC ? 8 : 1) {
+    const int64_t c = column<TEAM, VEC>(i, t);
+    const int at = VEC ? i / 8 : i;
+    if constexpr (VEC)
+      raw.w[at] = c < dim ? *reinterpret_cast<const uint2*>(codes + c) : make_uint2(0u, 0u);
+    else
+      raw.w[at] = c < dim ? codes[c] : uint8_t(0);
+    raw.scale[at] = c < dim ? scales[c >> 5] : uint8_t(0);
+  }
+}
+
+template <int V, bool VEC, typename T>
+__device__ __forceinline__ void row_values(const RawRow<V, VEC, T>& raw, float (&v)[V]) {
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = load1(&raw.w[i]);
+  } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < V / 8; ++i) {
+      const uint32_t u[4] = {raw.w[i].x, raw.w[i].y, raw.w[i].z, raw.w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
+        v[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      v[4 * i] = __uint_as_float(raw.w[i].x);
+      v[4 * i + 1] = __uint_as_float(raw.w[i].y);
+      v[4 * i + 2] = __uint_as_float(raw.w[i].z);
+      v[4 * i + 3] = __uint_as_float(raw.w[i].w);
+    }
+  }
+}
+template <int V, bool VEC>
+__device__ __forceinline__ void row_values(const RawRow8<V, VEC>& raw, float (&v)[V]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < V / 8; ++i) {
+      const float up = mx8_up(raw.scale[i]);
+      float a[4], b[4];
+      e4m3x4_values(raw.w[i].x, a);
+      e4m3x4_values(raw.w[i].y, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * i + j] = a[j] * up;
+        v[8 * i + 4 + j] = b[j] * up;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = e4m3_value(raw.w[i]) * mx8_up(raw.scale[i]);
+  }
+}
+
+// The values are taken from the raw words again where they are used next, rather
+// than kept: the compiler may not take this row's words for those it has
+// converted already.
+template <typename Raw>
+__device__ __forceinline__ void forget(Raw& raw) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(raw.w);
+  if constexpr (sizeof(raw.w) % 4 == 0 && sizeof(raw.w[0]) >= 8) {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(raw.w) / 4); ++i) asm volatile("" : "+r"(w[i]));
+  }
+}
+
+// Blocks an SM, and so registers a thread: 1024 threads an SM where a row is 16
+// bytes a thread.
+template <int TEAM, bool VEC, typename T>
+constexpr int kGradBlocks = TEAM < 256 ? 4 : VEC && sizeof(T) == 2 ? 1024 / TEAM : TEAM > 512 ? 1 : 512 / TEAM;
+
+// The backward pass. A team has the next row's loads under way while it works on
+// one, and one barrier a row: the warps' sums go to one half of `shared` and the
+// next row's to the other.
+template <int TEAM, int V, bool VEC, typename T, bool MX8>
+__global__ void __launch_bounds__(kBlock<TEAM>, kGradBlocks<TEAM, VEC, T>) norm_grad_kernel(const NormGradParams p) {
+  __shared__ float2 shared[2][32];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   constexpr int kTeams = kBlock<TEAM> / TEAM;
-  const int t = int(threadIdx.x) % TEAM;
-  const int64_t team = int64_t(blockIdx.x) * kTeams + int(threadIdx.x) / TEAM;
+  const int t = int(threadIdx.x) % TEAM, lane = int(threadIdx.x & 31);
+  const int64_t team = int64_t(blockIdx.x) * kTeams + int(threadIdx.x) / TEAM, step = int64_t(gridDim.x) * kTeams;
   const int64_t nb = (p.dim + 31) / 32;
   float w[V], dw[V];
   if (p.weight != nullptr) {
@@ -220,23 +303,60 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_kernel(const NormGradP
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) dw[i] = 0.0f;
-  for (int64_t row = team; row < p.rows; row += int64_t(gridDim.x) * kTeams) {
+  struct Rows {
+    RawRow<V, VEC, T> dy, res;
+    typename std::conditional<MX8, RawRow8<V, VEC>, RawRow<V, VEC, T>>::type x;
+  };
+  Rows next;
+  auto fetch = [&](int64_t row) {
     const int64_t at = row * p.dim;
-    float s[V], dy[V];
-    load_row<TEAM, V, VEC>(static_cast<const T*>(p.dy) + at, p.dim, t, dy);
-    if (p.x.dtype == MO_MX8)
-      load_row_mx8<TEAM, V, VEC>(static_cast<const uint8_t*>(p.x.data) + row * nb * 32, p.x.scales + row * nb, p.dim, t, s);
+    fetch_row<TEAM, V, VEC>(static_cast<const T*>(p.dy) + at, p.dim, t, next.dy);
+    if constexpr (MX8)
+      fetch_row<TEAM, V, VEC>(static_cast<const uint8_t*>(p.x.data) + row * nb * 32, p.x.scales + row * nb, p.dim, t, next.x);
     else
-      load_row<TEAM, V, VEC>(static_cast<const T*>(p.x.data) + at, p.dim, t, s);
+      fetch_row<TEAM, V, VEC>(static_cast<const T*>(p.x.data) + at, p.dim, t, next.x);
+    if (p.dres != nullptr) fetch_row<TEAM, V, VEC>(static_cast<const T*>(p.dres) + at, p.dim, t, next.res);
+  };
+  if (team < p.rows) fetch(team);
+  int parity = 0;
+  for (int64_t row = team; row < p.rows; row += step, parity ^= 1) {
+    Rows cur = next;
+    if (row + step < p.rows) fetch(row + step);
     float squares = 0.0f, dot = 0.0f;
+    {
+      float s[V], dy[V];
+      row_values(cur.dy, dy);
+      row_values(cur.x, s);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      squares = fmaf(s[i], s[i], squares);
-      dot = fmaf(dy[i] * w[i], s[i], dot);
+      for (int i = 0; i < V; ++i) {
+        squares = fmaf(s[i], s[i], squares);
+        dot = fmaf(dy[i] * w[i], s[i], dot);
+      }
     }
-    team_sums<TEAM>(squares, dot, shared);
+    forget(cur.dy);
+    forget(cur.x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      squares += __shfl_xor_sync(0xFFFFFFFFu, squares, o);
+      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+    }
+    if constexpr (TEAM > 32) {
+      if (lane == 0) shared[parity][threadIdx.x >> 5] = make_float2(squares, dot);
+      __syncthreads();
+      const float2 v = shared[parity][lane % (TEAM / 32)];
+      squares = v.x;
+      dot = v.y;
+#pragma unroll
+      for (int o = TEAM / 64; o > 0; o >>= 1) {
+        squares += __shfl_xor_sync(0xFFFFFFFFu, squares, o);
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+      }
+    }
     const float r = inverse_rms(squares, p.dim, p.eps);
     const float m = dot * r / float(p.dim);   // mean(g s r)
+    float s[V], dy[V];
+    row_values(cur.dy, dy);
+    row_values(cur.x, s);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const float n = s[i] * r;
@@ -244,11 +364,11 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_kernel(const NormGradP
       dy[i] = r * fmaf(-n, m, dy[i] * w[i]);
     }
     if (p.dres != nullptr) {
-      load_row<TEAM, V, VEC>(static_cast<const T*>(p.dres) + at, p.dim, t, s);
+      row_values(cur.res, s);
 #pragma unroll
       for (int i = 0; i < V; ++i) dy[i] += s[i];
     }
-    store_row<TEAM, V, VEC>(static_cast<T*>(p.dx) + at, p.dim, t, dy);
+    store_row<TEAM, V, VEC>(static_cast<T*>(p.dx) + row * p.dim, p.dim, t, dy);
   }
   if (p.part != nullptr) store_row<TEAM, V, VEC>(p.part + team * p.dim, p.dim, t, dw);
 }
@@ -331,47 +451,37 @@ __global__ void __launch_bounds__(kLong) norm_grad_long_kernel(const NormGradPar
   }
 }
 
-// The teams that take rows of `dim` elements.
-struct Shape {
-  int team, values;   // 0: rows that no team holds
-};
-Shape shape_of(int64_t dim) {
-  if (dim <= 256) return {32, 8};
-  if (dim <= 1024) return {128, 8};
-  if (dim <= 2048) return {256, 8};
-  if (dim <= 4096) return {256, 16};
-  if (dim <= 8192) return {512, 16};
-  return {0, 0};
-}
-// Teams of the backward pass: 16 of a warp an SM, or blocks as follows, on 152
-// SMs (a number that does not depend on the device, as results must not).
+// Threads of the team that takes rows of `dim` elements, eight a thread; 0: rows
+// that no team holds.
+int team_of(int64_t dim) { return dim <= 256 ? 32 : dim <= 1024 ? 128 : dim <= 2048 ? 256 : dim <= 4096 ? 512 : dim <= 8192 ? 1024 : 0; }
+
+// Teams of the backward pass: 1024 threads an SM, on 152 SMs (a number that does
+// not depend on the device, as results must not).
 int64_t grad_teams(int64_t rows, int64_t dim) {
-  const int team = shape_of(dim).team;
-  return std::min<int64_t>(rows, 152 * (team == 32 ? 16 : team == 128 ? 6 : team == 256 ? 2 : team == 512 ? 1 : 2));
+  const int team = team_of(dim);
+  return std::min<int64_t>(rows, 152 * (team == 0 ? 2 : 1024 / team));
 }
 
 template <typename F>
-cudaError_t with_shape(int64_t dim, F&& f) {
+cudaError_t with_team(int64_t dim, F&& f) {
   const bool vec = dim % 8 == 0;
-  auto with = [&](auto team, auto values) {
-    constexpr int TEAM = decltype(team)::value, V = decltype(values)::value;
-    return vec ? f(Act<TEAM>(), Act<V>(), std::true_type()) : f(Act<TEAM>(), Act<V>(), std::false_type());
-  };
-  const Shape s = shape_of(dim);
-  if (s.team == 32) return with(Act<32>(), Act<8>());
-  if (s.team == 128) return with(Act<128>(), Act<8>());
-  if (s.team == 512) return with(Act<512>(), Act<16>());
-  return s.values == 8 ? with(Act<256>(), Act<8>()) : with(Act<256>(), Act<16>());
+  auto with = [&](auto team) { return vec ? f(team, std::true_type()) : f(team, std::false_type()); };
+  switch (team_of(dim)) {
+    case 32: return with(Act<32>());
+    case 128: return with(Act<128>());
+    case 256: return with(Act<256>());
+    case 512: return with(Act<512>());
+    default: return with(Act<1024>());
+  }
 }
 
 template <typename T>
 cudaError_t norm_as(const NormParams& p, cudaStream_t stream) {
-  if (shape_of(p.dim).team == 0)
+  if (team_of(p.dim) == 0)
     return launch_kernel(norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(kLong), 0, 1, true, stream, p);
-  return with_shape(p.dim, [&](auto team, auto values, auto vec) {
-    constexpr int TEAM = decltype(team)::value, V = decltype(values)::value;
-    constexpr int kTeams = kBlock<TEAM> / TEAM;
-    return launch_kernel(norm_kernel<TEAM, V, decltype(vec)::value, T>, dim3(unsigned((p.rows + kTeams - 1) / kTeams)),
+  return with_team(p.dim, [&](auto team, auto vec) {
+    constexpr int TEAM = decltype(team)::value, kTeams = kBlock<TEAM> / TEAM;
+    return launch_kernel(norm_kernel<TEAM, 8, decltype(vec)::value, T>, dim3(unsigned((p.rows + kTeams - 1) / kTeams)),
                          dim3(kBlock<TEAM>), 0, 1, true, stream, p);
   });
 }
@@ -379,20 +489,20 @@ cudaError_t norm_as(const NormParams& p, cudaStream_t stream) {
 template <typename T>
 cudaError_t norm_grad_as(const NormGradParams& p, cudaStream_t stream) {
   const int64_t teams = norm_parts(p.rows, p.dim);
-  if (shape_of(p.dim).team == 0)
+  if (team_of(p.dim) == 0)
     return launch_kernel(norm_grad_long_kernel<T>, dim3(unsigned(teams)), dim3(kLong), 0, 1, true, stream, p);
-  return with_shape(p.dim, [&](auto team, auto values, auto vec) {
-    constexpr int TEAM = decltype(team)::value, V = decltype(values)::value;
-    constexpr int kTeams = kBlock<TEAM> / TEAM;
-    return launch_kernel(norm_grad_kernel<TEAM, V, decltype(vec)::value, T>, dim3(unsigned(teams / kTeams)),
-                         dim3(kBlock<TEAM>), 0, 1, true, stream, p);
+  return with_team(p.dim, [&](auto team, auto vec) {
+    constexpr int TEAM = decltype(team)::value, kTeams = kBlock<TEAM> / TEAM;
+    constexpr bool VEC = decltype(vec)::value;
+    auto kern = p.x.dtype == MO_MX8 ? norm_grad_kernel<TEAM, 8, VEC, T, true> : norm_grad_kernel<TEAM, 8, VEC, T, false>;
+    return launch_kernel(kern, dim3(unsigned(teams / kTeams)), dim3(kBlock<TEAM>), 0, 1, true, stream, p);
   });
 }
 
 }  // namespace
 
 int64_t norm_parts(int64_t rows, int64_t dim) {
-  const int64_t teams = grad_teams(rows, dim), per = shape_of(dim).team == 32 ? kBlock<32> / 32 : 1;
+  const int64_t teams = grad_teams(rows, dim), per = team_of(dim) == 32 ? kBlock<32> / 32 : 1;
   return (teams + per - 1) / per * per;
 }
 
