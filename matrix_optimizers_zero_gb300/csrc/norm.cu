@@ -16,9 +16,12 @@
 #include "activation.cuh"
 #include "launch.cuh"
 #include "layer_kernels.h"
+#include "ptx_train.cuh"
 
 namespace mo {
 namespace {
+
+using ptx::F2;
 
 // A team of TEAM threads holds a row of at most TEAM V elements, V a thread:
 // eight neighbours of every 8 TEAM where rows are 16-byte aligned (VEC), one of
@@ -30,29 +33,6 @@ __device__ __forceinline__ int64_t column(int i, int t) {
 
 template <int TEAM>
 constexpr int kBlock = TEAM < 128 ? 128 : TEAM;
-
-template <int TEAM, int V, bool VEC, typename T>
-__device__ __forceinline__ void load_row(const T* p, int64_t dim, int t, float (&v)[V]) {
-  if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < V; i += 8) {
-      float (&w)[8] = *reinterpret_cast<float (*)[8]>(&v[i]);
-      const int64_t c = column<TEAM, VEC>(i, t);
-      if (c < dim) {
-        load8(p + c, w);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 0.0f;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int64_t c = column<TEAM, VEC>(i, t);
-      v[i] = c < dim ? load1(p + c) : 0.0f;
-    }
-  }
-}
 
 template <int TEAM, int V, bool VEC, typename T>
 __device__ __forceinline__ void store_row(T* p, int64_t dim, int t, const float (&v)[V]) {
@@ -96,281 +76,398 @@ __device__ __forceinline__ void store_row_mx8(uint8_t* codes, uint8_t* scales, i
   }
 }
 
-// Sums of a and b over a team; the order is fixed. `shared` holds 2 x 32
-// floats. (A team of a warp needs no shared memory; teams of more are a whole
-// block.)
+// 1 / sqrt(mean + eps), two units of 2^-23 off at most (rsqrtf)
+__device__ __forceinline__ float inverse_rms(float squares, float inv_dim, float eps) { return rsqrtf(fmaf(squares, inv_dim, eps)); }
+
+// Sums of a and b over a team, in a fixed order, with one barrier: a row's warps
+// leave theirs in one half of `shared`, the next row's in the other (parity). A
+// team of a warp needs neither; teams of more are a whole block. From the first
+// step on the upper half of a warp sums b and the lower a.
 template <int TEAM>
-__device__ __forceinline__ void team_sums(float& a, float& b, float* shared) {
+__device__ __forceinline__ float2 team_sums(float a, float b, float (&shared)[2][64], int parity) {
+  const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
+  const bool upper = lane >= 16;
+  float v = upper ? b : a;
+  v += __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-    b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-  }
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if constexpr (TEAM > 32) {
-    const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
-    if (lane == 0) {
-      shared[warp] = a;
-      shared[32 + warp] = b;
-    }
+    constexpr int kWarps = TEAM / 32;
+    if ((lane & 15) == 0) shared[parity][(upper ? kWarps : 0) + warp] = v;
     __syncthreads();
-    a = 0.0f;
-    b = 0.0f;
+    if constexpr (kWarps <= 16) {
+      v = shared[parity][(upper ? kWarps : 0) + lane % kWarps];
+    } else {
+      v = shared[parity][(upper ? 32 : 0) + (lane & 15)] + shared[parity][(upper ? 48 : 16) + (lane & 15)];
+    }
 #pragma unroll
-    for (int w = 0; w < TEAM / 32; ++w) {
-      a += shared[w];
-      b += shared[32 + w];
+    for (int o = (kWarps <= 16 ? kWarps : 16) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  }
+  return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
+}
+
+// ------------------------------------------------------------------ aligned rows
+//
+// A thread copies its eight elements of the rows to come into slots of its own in
+// shared memory (cp.async), up to three rows ahead, and reads them back when it
+// gets there: no barrier, no registers, and enough bytes under way. With one row
+// ahead in registers the backward pass of 16384 x 4096 took 101 us.
+//
+// Rows ahead where a row takes `slot` bytes a thread: 1024 threads' in 196 KB.
+constexpr int rows_ahead(int slot) { return 192 / slot - 1 < 3 ? 192 / slot - 1 : 3; }
+
+// Slots of BYTES bytes for each of THREADS threads and every row under way; 16
+// bytes of neighbouring threads lie side by side, so a warp's accesses meet all
+// banks.
+template <int BYTES, int THREADS>
+struct Slots {
+  static constexpr int kUnit = BYTES < 16 ? BYTES : 16;
+  static constexpr uint32_t kSlot = BYTES * THREADS;   // of one row
+  uint32_t base;   // this thread's first
+  __device__ __forceinline__ explicit Slots(uint32_t start) : base(start + threadIdx.x * kUnit) {}
+  __device__ __forceinline__ uint32_t at(uint32_t slot, int unit) const { return base + slot * kSlot + uint32_t(unit) * THREADS * kUnit; }
+  __device__ __forceinline__ void copy(uint32_t slot, const void* g) const {
+#pragma unroll
+    for (int i = 0; i < BYTES / kUnit; ++i) {
+      const uint8_t* p = static_cast<const uint8_t*>(g) + i * kUnit;
+      if constexpr (kUnit == 16)
+        ptx::cp_async16(at(slot, i), p);
+      else
+        ptx::cp_async8(at(slot, i), p);
     }
-    __syncthreads();
+  }
+};
+__device__ __forceinline__ void bf16_values(const uint4& w, F2 (&v)[4]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = ptx::f2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
+}
+template <int THREADS>
+__device__ __forceinline__ void slot_values(const Slots<16, THREADS>& s, uint32_t slot, float, F2 (&v)[4]) {   // bf16
+  bf16_values(ptx::ld_shared_v4(s.at(slot, 0)), v);
+}
+template <int THREADS>
+__device__ __forceinline__ void slot_values(const Slots<32, THREADS>& s, uint32_t slot, float, F2 (&v)[4]) {   // fp32
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 w = ptx::ld_shared_v4(s.at(slot, i));
+    v[2 * i] = ptx::f2(__uint_as_float(w.x), __uint_as_float(w.y));
+    v[2 * i + 1] = ptx::f2(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
+}
+template <int THREADS>
+__device__ __forceinline__ void slot_values(const Slots<8, THREADS>& s, uint32_t slot, float up, F2 (&v)[4]) {   // 8 bits
+  const uint2 w = ptx::ld_shared_v2(s.at(slot, 0));
+  const F2 u = ptx::f2(up);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float a[4];
+    e4m3x4_values(i == 0 ? w.x : w.y, a);
+    v[2 * i] = ptx::mul2(ptx::f2(a[0], a[1]), u);
+    v[2 * i + 1] = ptx::mul2(ptx::f2(a[2], a[3]), u);
+  }
+}
+__device__ __forceinline__ void unpair(const F2 (&v)[4], float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = ptx::parts(v[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* p, const F2 (&v)[4]) {
+  float f[8];
+  unpair(v, f);
+  store8(p, f);
+}
+
+template <typename T>
+constexpr int kNormSlot = 2 * 8 * int(sizeof(T));
+template <typename T>
+constexpr int kNormAhead = rows_ahead(kNormSlot<T>);
+template <typename T, bool MX8>
+constexpr int kGradSlot = 2 * 8 * int(sizeof(T)) + (MX8 ? 8 : 8 * int(sizeof(T)));
+template <typename T, bool MX8>
+constexpr int kGradAhead = rows_ahead(kGradSlot<T, MX8>);
+static_assert(kNormAhead<float> >= 1 && kGradAhead<float, true> >= 1 && kGradAhead<float, false> >= 1, "a row ahead");
+
+template <int TEAM, typename T>
+__global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_kernel(const NormParams p) {
+  extern __shared__ __align__(16) uint8_t slots[];
+  __shared__ float shared[2][64];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  constexpr int kTeams = kBlock<TEAM> / TEAM, kRow = 8 * int(sizeof(T)), kAhead = kNormAhead<T>;
+  const int t = int(threadIdx.x) % TEAM;
+  const int64_t team = int64_t(blockIdx.x) * kTeams + int(threadIdx.x) / TEAM, step = int64_t(gridDim.x) * kTeams;
+  const int64_t col = int64_t(t) * 8, nb = (p.dim + 31) / 32;
+  const bool in = col < p.dim;
+  const float inv_dim = 1.0f / float(p.dim);
+  const Slots<kRow, kBlock<TEAM>> xs(ptx::smem_addr(slots)), rs(ptx::smem_addr(slots) + (kAhead + 1) * xs.kSlot);
+  const T* x = static_cast<const T*>(p.x) + col;
+  const T* res = p.residual != nullptr ? static_cast<const T*>(p.residual) + col : nullptr;
+  auto fetch = [&](int64_t row, uint32_t slot) {
+    if (row < p.rows && in) {
+      xs.copy(slot, x + row * p.dim);
+      if (res != nullptr) rs.copy(slot, res + row * p.dim);
+    }
+    ptx::cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(team + i * step, uint32_t(i));
+  F2 w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = ptx::f2(1.0f);
+  if (p.weight != nullptr && in) {
+    float f[8];
+    load8(p.weight + col, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = ptx::f2(f[2 * i], f[2 * i + 1]);
+  }
+  uint32_t slot = 0;
+  int parity = 0;
+  for (int64_t row = team; row < p.rows; row += step, parity ^= 1) {
+    fetch(row + kAhead * step, slot == 0 ? kAhead : slot - 1);
+    ptx::cp_async_wait_but<kAhead>();
+    const int64_t at = row * p.dim + col;
+    F2 s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = ptx::f2(0.0f);
+    if (in) {
+      slot_values(xs, slot, 0.0f, s);
+      if (res != nullptr) {
+        F2 r[4];
+        slot_values(rs, slot, 0.0f, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = ptx::add2(s[i], r[i]);
+      }
+      if (p.sum != nullptr) store_pairs(static_cast<T*>(p.sum) + at, s);
+    }
+    slot = slot == kAhead ? 0 : slot + 1;
+    F2 squares = ptx::mul2(s[0], s[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) squares = ptx::fma2(s[i], s[i], squares);
+    const float2 half = ptx::parts(squares);
+    const F2 r = ptx::f2(inverse_rms(team_sums<TEAM>(half.x + half.y, 0.0f, shared, parity).x, inv_dim, p.eps));
+    // (a thread past dim holds zeros; where r is not finite they have to stay so)
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = ptx::mul2(ptx::mul2(s[i], r), w[i]);
+      if (p.out != nullptr) {
+        if (p.out_bf16)
+          store_pairs(static_cast<uint16_t*>(p.out) + at, s);
+        else
+          store_pairs(static_cast<float*>(p.out) + at, s);
+      }
+    }
+    if (p.out8.data != nullptr) {
+      float v[8];
+      unpair(s, v);
+      store_row_mx8<TEAM, 8, true>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, v);
+    }
   }
 }
 
-__device__ __forceinline__ float inverse_rms(float squares, int64_t dim, float eps) { return 1.0f / sqrtf(squares / float(dim) + eps); }
+template <int TEAM, typename T, bool MX8>
+__global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_grad_kernel(const NormGradParams p) {
+  extern __shared__ __align__(16) uint8_t slots[];
+  __shared__ float shared[2][64];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  constexpr int kTeams = kBlock<TEAM> / TEAM, kRow = 8 * int(sizeof(T)), kAhead = kGradAhead<T, MX8>;
+  const int t = int(threadIdx.x) % TEAM;
+  const int64_t team = int64_t(blockIdx.x) * kTeams + int(threadIdx.x) / TEAM, step = int64_t(gridDim.x) * kTeams;
+  const int64_t col = int64_t(t) * 8, nb = (p.dim + 31) / 32;
+  const bool in = col < p.dim;
+  const float inv_dim = 1.0f / float(p.dim);
+  const uint32_t start = ptx::smem_addr(slots);
+  const Slots<kRow, kBlock<TEAM>> ds(start), rs(start + (kAhead + 1) * ds.kSlot);
+  const Slots<MX8 ? 8 : kRow, kBlock<TEAM>> xs(start + 2 * (kAhead + 1) * ds.kSlot);
+  const T* dy_at = static_cast<const T*>(p.dy) + col;
+  const T* res_at = p.dres != nullptr ? static_cast<const T*>(p.dres) + col : nullptr;
+  auto fetch = [&](int64_t row, uint32_t slot) {
+    if (row < p.rows && in) {
+      ds.copy(slot, dy_at + row * p.dim);
+      if constexpr (MX8)
+        xs.copy(slot, static_cast<const uint8_t*>(p.x.data) + row * nb * 32 + col);
+      else
+        xs.copy(slot, static_cast<const T*>(p.x.data) + row * p.dim + col);
+      if (res_at != nullptr) rs.copy(slot, res_at + row * p.dim);
+    }
+    ptx::cp_async_commit();
+  };
+  // (a scale is one byte, too few for such a copy: one row ahead in a register)
+  auto scale_of = [&](int64_t row) { return MX8 && row < p.rows && in ? p.x.scales[row * nb + (col >> 5)] : uint8_t(0); };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(team + i * step, uint32_t(i));
+  uint8_t scale = scale_of(team);
+  F2 w[4], dw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = ptx::f2(1.0f), dw[i] = ptx::f2(0.0f);
+  if (p.weight != nullptr && in) {
+    float f[8];
+    load8(p.weight + col, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = ptx::f2(f[2 * i], f[2 * i + 1]);
+  }
+  uint32_t slot = 0;
+  int parity = 0;
+  for (int64_t row = team; row < p.rows; row += step, parity ^= 1) {
+    fetch(row + kAhead * step, slot == 0 ? kAhead : slot - 1);
+    ptx::cp_async_wait_but<kAhead>();
+    F2 s[4], dy[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = ptx::f2(0.0f), dy[i] = ptx::f2(0.0f);
+    if (in) {
+      slot_values(ds, slot, 0.0f, dy);
+      slot_values(xs, slot, MX8 ? mx8_up(scale) : 0.0f, s);
+    }
+    scale = scale_of(row + step);
+    F2 squares = ptx::mul2(s[0], s[0]), dot = ptx::mul2(ptx::mul2(dy[0], w[0]), s[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      squares = ptx::fma2(s[i], s[i], squares);
+      dot = ptx::fma2(ptx::mul2(dy[i], w[i]), s[i], dot);
+    }
+    const float2 hs = ptx::parts(squares), hd = ptx::parts(dot);
+    const float2 sums = team_sums<TEAM>(hs.x + hs.y, hd.x + hd.y, shared, parity);
+    const float r = inverse_rms(sums.x, inv_dim, p.eps);
+    if (in) {
+      const F2 r2 = ptx::f2(r), m2 = ptx::f2(-(sums.y * r * inv_dim));   // -mean(g s r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const F2 n = ptx::mul2(s[i], r2);
+        dw[i] = ptx::fma2(dy[i], n, dw[i]);
+        dy[i] = ptx::mul2(r2, ptx::fma2(n, m2, ptx::mul2(dy[i], w[i])));
+      }
+      if (res_at != nullptr) {
+        slot_values(rs, slot, 0.0f, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dy[i] = ptx::add2(dy[i], s[i]);
+      }
+      store_pairs(static_cast<T*>(p.dx) + row * p.dim + col, dy);
+    }
+    slot = slot == kAhead ? 0 : slot + 1;
+  }
+  if (p.part != nullptr && in) store_pairs(p.part + team * p.dim + col, dw);
+}
 
-template <int TEAM, int V, bool VEC, typename T>
-__global__ void __launch_bounds__(kBlock<TEAM>) norm_kernel(const NormParams p) {
-  __shared__ float shared[64];
+// ------------------------------------------------------------------ other rows
+//
+// Rows that are not 16-byte aligned: elements TEAM apart, eight a thread, one row
+// ahead in registers.
+template <int TEAM, typename T>
+__global__ void __launch_bounds__(kBlock<TEAM>) norm_odd_kernel(const NormParams p) {
+  __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   constexpr int kTeams = kBlock<TEAM> / TEAM;
   const int t = int(threadIdx.x) % TEAM;
   const int64_t row = int64_t(blockIdx.x) * kTeams + int(threadIdx.x) / TEAM;
   if (row >= p.rows) return;   // a whole warp, and a whole block where teams are more than one
-  const int64_t at = row * p.dim;
-  float s[V];
-  load_row<TEAM, V, VEC>(static_cast<const T*>(p.x) + at, p.dim, t, s);
-  if (p.residual != nullptr) {
-    float r[V];
-    load_row<TEAM, V, VEC>(static_cast<const T*>(p.residual) + at, p.dim, t, r);
+  const int64_t at = row * p.dim, nb = (p.dim + 31) / 32;
+  float s[8];
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] += r[i];
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = column<TEAM, false>(i, t);
+    s[i] = c < p.dim ? load1(static_cast<const T*>(p.x) + at + c) : 0.0f;
   }
-  if (p.sum != nullptr) store_row<TEAM, V, VEC>(static_cast<T*>(p.sum) + at, p.dim, t, s);
-  float squares = 0.0f, none = 0.0f;
+  if (p.residual != nullptr) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) squares = fmaf(s[i], s[i], squares);
-  team_sums<TEAM>(squares, none, shared);
-  const float r = inverse_rms(squares, p.dim, p.eps);
-  float w[V];
-  if (p.weight != nullptr) load_row<TEAM, V, VEC>(p.weight, p.dim, t, w);
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = column<TEAM, false>(i, t);
+      if (c < p.dim) s[i] += load1(static_cast<const T*>(p.residual) + at + c);
+    }
+  }
+  if (p.sum != nullptr) store_row<TEAM, 8, false>(static_cast<T*>(p.sum) + at, p.dim, t, s);
+  float squares = 0.0f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) s[i] = p.weight != nullptr ? s[i] * r * w[i] : s[i] * r;
+  for (int i = 0; i < 8; ++i) squares = fmaf(s[i], s[i], squares);
+  const float r = inverse_rms(team_sums<TEAM>(squares, 0.0f, shared, 0).x, 1.0f / float(p.dim), p.eps);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = column<TEAM, false>(i, t);
+    // (past dim 0, also where r is not finite)
+    s[i] = c >= p.dim ? 0.0f : p.weight != nullptr ? s[i] * r * p.weight[c] : s[i] * r;
+  }
   if (p.out != nullptr) {
     if (p.out_bf16)
-      store_row<TEAM, V, VEC>(static_cast<uint16_t*>(p.out) + at, p.dim, t, s);
+      store_row<TEAM, 8, false>(static_cast<uint16_t*>(p.out) + at, p.dim, t, s);
     else
-      store_row<TEAM, V, VEC>(static_cast<float*>(p.out) + at, p.dim, t, s);
+      store_row<TEAM, 8, false>(static_cast<float*>(p.out) + at, p.dim, t, s);
   }
-  if (p.out8.data != nullptr) {
-    const int64_t nb = (p.dim + 31) / 32;
-    // (elements past dim are not zeros where r is not finite)
-    if (column<TEAM, VEC>(V - 1, TEAM - 1) >= p.dim) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (column<TEAM, VEC>(i, t) >= p.dim) s[i] = 0.0f;
-    }
-    store_row_mx8<TEAM, V, VEC>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, s);
-  }
+  if (p.out8.data != nullptr)
+    store_row_mx8<TEAM, 8, false>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, s);
 }
 
-// A row as it lies in memory, loaded while the one before it is worked on.
-template <int V, bool VEC, typename T>
-struct RawRow {
-  using Word = typename std::conditional<VEC, uint4, T>::type;
-  static constexpr int kWords = VEC ? V * int(sizeof(T)) / 16 : V;
-  Word w[kWords];
-};
-template <int V, bool VEC>
-struct RawRow8 {
-  using Word = typename std::conditional<VEC, uint2, uint8_t>::type;
-  Word w[VEC ? V / 8 : V];
-  uint8_t scale[VEC ? V / 8 : V];
-};
-
-template <int TEAM, int V, bool VEC, typename T>
-__device__ __forceinline__ void fetch_row(const T* p, int64_t dim, int t, RawRow<V, VEC, T>& raw) {
-  if constexpr (VEC) {
-    constexpr int kPer = 8 * int(sizeof(T)) / 16;   // words of eight elements
-#pragma unroll
-    for (int i = 0; i < V; i += 8) {
-      const int64_t c = column<TEAM, VEC>(i, t);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        raw.w[i / 8 * kPer + j] = c < dim ? reinterpret_cast<const uint4*>(p + c)[j] : make_uint4(0u, 0u, 0u, 0u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int64_t c = column<TEAM, VEC>(i, t);
-      raw.w[i] = c < dim ? p[c] : T(0);
-    }
-  }
-}
-template <int TEAM, int V, bool VEC>
-__device__ __forceinline__ void fetch_row(const uint8_t* codes, const uint8_t* scales, int64_t dim, int t, RawRow8<V, VEC>& raw) {
-#pragma unroll
-  for (int i = 0; i < V; i += VEC ? 8 : 1) {
-    const int64_t c = column<TEAM, VEC>(i, t);
-    const int at = VEC ? i / 8 : i;
-    if constexpr (VEC)
-      raw.w[at] = c < dim ? *reinterpret_cast<const uint2*>(codes + c) : make_uint2(0u, 0u);
-    else
-      raw.w[at] = c < dim ? codes[c] : uint8_t(0);
-    raw.scale[at] = c < dim ? scales[c >> 5] : uint8_t(0);
-  }
-}
-
-template <int V, bool VEC, typename T>
-__device__ __forceinline__ void row_values(const RawRow<V, VEC, T>& raw, float (&v)[V]) {
-  if constexpr (!VEC) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = load1(&raw.w[i]);
-  } else if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int i = 0; i < V / 8; ++i) {
-      const uint32_t u[4] = {raw.w[i].x, raw.w[i].y, raw.w[i].z, raw.w[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
-        v[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      v[4 * i] = __uint_as_float(raw.w[i].x);
-      v[4 * i + 1] = __uint_as_float(raw.w[i].y);
-      v[4 * i + 2] = __uint_as_float(raw.w[i].z);
-      v[4 * i + 3] = __uint_as_float(raw.w[i].w);
-    }
-  }
-}
-template <int V, bool VEC>
-__device__ __forceinline__ void row_values(const RawRow8<V, VEC>& raw, float (&v)[V]) {
-  if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < V / 8; ++i) {
-      const float up = mx8_up(raw.scale[i]);
-      float a[4], b[4];
-      e4m3x4_values(raw.w[i].x, a);
-      e4m3x4_values(raw.w[i].y, b);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[8 * i + j] = a[j] * up;
-        v[8 * i + 4 + j] = b[j] * up;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = e4m3_value(raw.w[i]) * mx8_up(raw.scale[i]);
-  }
-}
-
-// The values are taken from the raw words again where they are used next, rather
-// than kept: the compiler may not take this row's words for those it has
-// converted already.
-template <typename Raw>
-__device__ __forceinline__ void forget(Raw& raw) {
-  uint32_t* w = reinterpret_cast<uint32_t*>(raw.w);
-  if constexpr (sizeof(raw.w) % 4 == 0 && sizeof(raw.w[0]) >= 8) {
-#pragma unroll
-    for (int i = 0; i < int(sizeof(raw.w) / 4); ++i) asm volatile("" : "+r"(w[i]));
-  }
-}
-
-// Blocks an SM, and so registers a thread: 1024 threads an SM where a row is 16
-// bytes a thread.
-template <int TEAM, bool VEC, typename T>
-constexpr int kGradBlocks = TEAM < 256 ? 4 : VEC && sizeof(T) == 2 ? 1024 / TEAM : TEAM > 512 ? 1 : 512 / TEAM;
-
-// The backward pass. A team has the next row's loads under way while it works on
-// one, and one barrier a row: the warps' sums go to one half of `shared` and the
-// next row's to the other.
-template <int TEAM, int V, bool VEC, typename T, bool MX8>
-__global__ void __launch_bounds__(kBlock<TEAM>, kGradBlocks<TEAM, VEC, T>) norm_grad_kernel(const NormGradParams p) {
-  __shared__ float2 shared[2][32];
+template <int TEAM, typename T, bool MX8>
+__global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const NormGradParams p) {
+  __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   constexpr int kTeams = kBlock<TEAM> / TEAM;
-  const int t = int(threadIdx.x) % TEAM, lane = int(threadIdx.x & 31);
+  const int t = int(threadIdx.x) % TEAM;
   const int64_t team = int64_t(blockIdx.x) * kTeams + int(threadIdx.x) / TEAM, step = int64_t(gridDim.x) * kTeams;
   const int64_t nb = (p.dim + 31) / 32;
-  float w[V], dw[V];
-  if (p.weight != nullptr) {
-    load_row<TEAM, V, VEC>(p.weight, p.dim, t, w);
-  } else {
+  float w[8], dw[8];
 #pragma unroll
-    for (int i = 0; i < V; ++i) w[i] = 1.0f;
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = column<TEAM, false>(i, t);
+    w[i] = p.weight != nullptr && c < p.dim ? p.weight[c] : 1.0f;
+    dw[i] = 0.0f;
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i) dw[i] = 0.0f;
-  struct Rows {
-    RawRow<V, VEC, T> dy, res;
-    typename std::conditional<MX8, RawRow8<V, VEC>, RawRow<V, VEC, T>>::type x;
-  };
-  Rows next;
+  const float inv_dim = 1.0f / float(p.dim);
+  T next_dy[8], next_res[8];
+  typename std::conditional<MX8, uint8_t, T>::type next_x[8];
+  uint8_t next_scale[8];
   auto fetch = [&](int64_t row) {
-    const int64_t at = row * p.dim;
-    fetch_row<TEAM, V, VEC>(static_cast<const T*>(p.dy) + at, p.dim, t, next.dy);
-    if constexpr (MX8)
-      fetch_row<TEAM, V, VEC>(static_cast<const uint8_t*>(p.x.data) + row * nb * 32, p.x.scales + row * nb, p.dim, t, next.x);
-    else
-      fetch_row<TEAM, V, VEC>(static_cast<const T*>(p.x.data) + at, p.dim, t, next.x);
-    if (p.dres != nullptr) fetch_row<TEAM, V, VEC>(static_cast<const T*>(p.dres) + at, p.dim, t, next.res);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = column<TEAM, false>(i, t), at = row * p.dim + c;
+      const bool in = c < p.dim;
+      next_dy[i] = in ? static_cast<const T*>(p.dy)[at] : T(0);
+      if constexpr (MX8) {
+        next_x[i] = in ? static_cast<const uint8_t*>(p.x.data)[row * nb * 32 + c] : uint8_t(0);
+        next_scale[i] = in ? p.x.scales[row * nb + (c >> 5)] : uint8_t(0);
+      } else {
+        next_x[i] = in ? static_cast<const T*>(p.x.data)[at] : T(0);
+      }
+      next_res[i] = in && p.dres != nullptr ? static_cast<const T*>(p.dres)[at] : T(0);
+    }
   };
   if (team < p.rows) fetch(team);
   int parity = 0;
   for (int64_t row = team; row < p.rows; row += step, parity ^= 1) {
-    Rows cur = next;
+    float s[8], dy[8], res[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dy[i] = load1(&next_dy[i]);
+      res[i] = load1(&next_res[i]);
+      if constexpr (MX8)
+        s[i] = e4m3_value(next_x[i]) * mx8_up(next_scale[i]);
+      else
+        s[i] = load1(&next_x[i]);
+    }
     if (row + step < p.rows) fetch(row + step);
     float squares = 0.0f, dot = 0.0f;
-    {
-      float s[V], dy[V];
-      row_values(cur.dy, dy);
-      row_values(cur.x, s);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        squares = fmaf(s[i], s[i], squares);
-        dot = fmaf(dy[i] * w[i], s[i], dot);
-      }
+    for (int i = 0; i < 8; ++i) {
+      squares = fmaf(s[i], s[i], squares);
+      dot = fmaf(dy[i] * w[i], s[i], dot);
     }
-    forget(cur.dy);
-    forget(cur.x);
+    const float2 sums = team_sums<TEAM>(squares, dot, shared, parity);
+    const float r = inverse_rms(sums.x, inv_dim, p.eps);
+    const float m = sums.y * r * inv_dim;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      squares += __shfl_xor_sync(0xFFFFFFFFu, squares, o);
-      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-    }
-    if constexpr (TEAM > 32) {
-      if (lane == 0) shared[parity][threadIdx.x >> 5] = make_float2(squares, dot);
-      __syncthreads();
-      const float2 v = shared[parity][lane % (TEAM / 32)];
-      squares = v.x;
-      dot = v.y;
-#pragma unroll
-      for (int o = TEAM / 64; o > 0; o >>= 1) {
-        squares += __shfl_xor_sync(0xFFFFFFFFu, squares, o);
-        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-      }
-    }
-    const float r = inverse_rms(squares, p.dim, p.eps);
-    const float m = dot * r / float(p.dim);   // mean(g s r)
-    float s[V], dy[V];
-    row_values(cur.dy, dy);
-    row_values(cur.x, s);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const float n = s[i] * r;
       dw[i] = fmaf(dy[i], n, dw[i]);
-      dy[i] = r * fmaf(-n, m, dy[i] * w[i]);
+      dy[i] = r * fmaf(-n, m, dy[i] * w[i]) + res[i];
     }
-    if (p.dres != nullptr) {
-      row_values(cur.res, s);
-#pragma unroll
-      for (int i = 0; i < V; ++i) dy[i] += s[i];
-    }
-    store_row<TEAM, V, VEC>(static_cast<T*>(p.dx) + row * p.dim, p.dim, t, dy);
+    store_row<TEAM, 8, false>(static_cast<T*>(p.dx) + row * p.dim, p.dim, t, dy);
   }
-  if (p.part != nullptr) store_row<TEAM, V, VEC>(p.part + team * p.dim, p.dim, t, dw);
+  if (p.part != nullptr) store_row<TEAM, 8, false>(p.part + team * p.dim, p.dim, t, dw);
 }
 
 // Rows that do not fit a team's registers: a block reads them twice, the second
@@ -379,19 +476,18 @@ constexpr int kLong = 512;
 
 template <typename T>
 __global__ void __launch_bounds__(kLong) norm_long_kernel(const NormParams p) {
-  __shared__ float shared[64];
+  __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t at = int64_t(blockIdx.x) * p.dim;
   const T* x = static_cast<const T*>(p.x) + at;
   const T* res = p.residual != nullptr ? static_cast<const T*>(p.residual) + at : nullptr;
-  float squares = 0.0f, none = 0.0f;
+  float squares = 0.0f;
   for (int64_t c = threadIdx.x; c < p.dim; c += kLong) {
     const float s = load1(x + c) + (res != nullptr ? load1(res + c) : 0.0f);
     squares = fmaf(s, s, squares);
   }
-  team_sums<kLong>(squares, none, shared);
-  const float r = inverse_rms(squares, p.dim, p.eps);
+  const float r = inverse_rms(team_sums<kLong>(squares, 0.0f, shared, 0).x, 1.0f / float(p.dim), p.eps);
   const int64_t nb = (p.dim + 31) / 32;
   uint8_t* codes = p.out8.data != nullptr ? static_cast<uint8_t*>(p.out8.data) + int64_t(blockIdx.x) * nb * 32 : nullptr;
   for (int64_t c = threadIdx.x; c < nb * 32; c += kLong) {   // whole warps
@@ -418,11 +514,13 @@ __global__ void __launch_bounds__(kLong) norm_long_kernel(const NormParams p) {
 
 template <typename T>
 __global__ void __launch_bounds__(kLong) norm_grad_long_kernel(const NormGradParams p) {
-  __shared__ float shared[64];
+  __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t nb = (p.dim + 31) / 32;
   float* part = p.part != nullptr ? p.part + int64_t(blockIdx.x) * p.dim : nullptr;
+  const float inv_dim = 1.0f / float(p.dim);
+  int parity = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int64_t at = row * p.dim;
     auto x_at = [&](int64_t c) {
@@ -438,9 +536,10 @@ __global__ void __launch_bounds__(kLong) norm_grad_long_kernel(const NormGradPar
       squares = fmaf(s, s, squares);
       dot = fmaf(load1(dy + c) * w_at(c), s, dot);
     }
-    team_sums<kLong>(squares, dot, shared);
-    const float r = inverse_rms(squares, p.dim, p.eps);
-    const float m = dot * r / float(p.dim);
+    const float2 sums = team_sums<kLong>(squares, dot, shared, parity);
+    parity ^= 1;
+    const float r = inverse_rms(sums.x, inv_dim, p.eps);
+    const float m = sums.y * r * inv_dim;
     for (int64_t c = threadIdx.x; c < p.dim; c += kLong) {   // a column is one thread's: no order to keep
       const float n = x_at(c) * r, d = load1(dy + c);
       if (part != nullptr) part[c] = row == int64_t(blockIdx.x) ? d * n : fmaf(d, n, part[c]);
@@ -464,14 +563,12 @@ int64_t grad_teams(int64_t rows, int64_t dim) {
 
 template <typename F>
 cudaError_t with_team(int64_t dim, F&& f) {
-  const bool vec = dim % 8 == 0;
-  auto with = [&](auto team) { return vec ? f(team, std::true_type()) : f(team, std::false_type()); };
   switch (team_of(dim)) {
-    case 32: return with(Act<32>());
-    case 128: return with(Act<128>());
-    case 256: return with(Act<256>());
-    case 512: return with(Act<512>());
-    default: return with(Act<1024>());
+    case 32: return f(Act<32>());
+    case 128: return f(Act<128>());
+    case 256: return f(Act<256>());
+    case 512: return f(Act<512>());
+    default: return f(Act<1024>());
   }
 }
 
@@ -479,23 +576,34 @@ template <typename T>
 cudaError_t norm_as(const NormParams& p, cudaStream_t stream) {
   if (team_of(p.dim) == 0)
     return launch_kernel(norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(kLong), 0, 1, true, stream, p);
-  return with_team(p.dim, [&](auto team, auto vec) {
+  return with_team(p.dim, [&](auto team) {
     constexpr int TEAM = decltype(team)::value, kTeams = kBlock<TEAM> / TEAM;
-    return launch_kernel(norm_kernel<TEAM, 8, decltype(vec)::value, T>, dim3(unsigned((p.rows + kTeams - 1) / kTeams)),
-                         dim3(kBlock<TEAM>), 0, 1, true, stream, p);
+    if (p.dim % 8 != 0)
+      return launch_kernel(norm_odd_kernel<TEAM, T>, dim3(unsigned((p.rows + kTeams - 1) / kTeams)), dim3(kBlock<TEAM>), 0, 1, true,
+                           stream, p);
+    constexpr size_t smem = size_t(kNormAhead<T> + 1) * kNormSlot<T> * kBlock<TEAM>;
+    auto kern = norm_kernel<TEAM, T>;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3(unsigned(norm_parts(p.rows, p.dim) / kTeams)), dim3(kBlock<TEAM>), smem, 1, true, stream, p);
   });
 }
 
-template <typename T>
+template <typename T, bool MX8>
 cudaError_t norm_grad_as(const NormGradParams& p, cudaStream_t stream) {
   const int64_t teams = norm_parts(p.rows, p.dim);
   if (team_of(p.dim) == 0)
     return launch_kernel(norm_grad_long_kernel<T>, dim3(unsigned(teams)), dim3(kLong), 0, 1, true, stream, p);
-  return with_team(p.dim, [&](auto team, auto vec) {
+  return with_team(p.dim, [&](auto team) {
     constexpr int TEAM = decltype(team)::value, kTeams = kBlock<TEAM> / TEAM;
-    constexpr bool VEC = decltype(vec)::value;
-    auto kern = p.x.dtype == MO_MX8 ? norm_grad_kernel<TEAM, 8, VEC, T, true> : norm_grad_kernel<TEAM, 8, VEC, T, false>;
-    return launch_kernel(kern, dim3(unsigned(teams / kTeams)), dim3(kBlock<TEAM>), 0, 1, true, stream, p);
+    const dim3 grid(unsigned(teams / kTeams));
+    if (p.dim % 8 != 0)
+      return launch_kernel(norm_grad_odd_kernel<TEAM, T, MX8>, grid, dim3(kBlock<TEAM>), 0, 1, true, stream, p);
+    constexpr size_t smem = size_t(kGradAhead<T, MX8> + 1) * kGradSlot<T, MX8> * kBlock<TEAM>;
+    auto kern = norm_grad_kernel<TEAM, T, MX8>;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, grid, dim3(kBlock<TEAM>), smem, 1, true, stream, p);
   });
 }
 
@@ -511,7 +619,8 @@ cudaError_t launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t stream)
 }
 
 cudaError_t launch_rms_norm_grad(const NormGradParams& p, bool bf16, cudaStream_t stream) {
-  return bf16 ? norm_grad_as<uint16_t>(p, stream) : norm_grad_as<float>(p, stream);
+  if (p.x.dtype == MO_MX8) return bf16 ? norm_grad_as<uint16_t, true>(p, stream) : norm_grad_as<float, true>(p, stream);
+  return bf16 ? norm_grad_as<uint16_t, false>(p, stream) : norm_grad_as<float, false>(p, stream);
 }
 
 }  // namespace mo
