@@ -1,22 +1,61 @@
 // Activations and their derivatives in fp32, and the 8-bit block format
 // (e4m3 codes, a power of two for each 32 elements of a row).
 //
+// Functions take one number or a pair (ptx::F2), which costs one instruction for
+// both wherever it is a product or a sum: an epilogue of 32768 elements a tile has
+// to end within the products of the next tile.
+//
 // Logistic functions go through 2^x and a reciprocal of the special function
 // unit (a few units of 2^-23, relative, over the range where the result is not 0
 // or 1 in fp32), without the scaling that subnormal arguments would need: they
 // give 1 and infinity here. gelu_tanh uses 0.5 (1 + tanh(u)) = 1 / (1 + e^(-2u)),
-// which loses nothing where tanh is near -1. gelu's normal distribution function
-// is erfcf's.
+// which loses nothing where tanh is near -1.
+//
+// gelu's normal distribution function: erfc(y) = (a1 t + ... + a5 t^5) e^(-y^2) with
+// t = 1 / (1 + p y), y >= 0 (Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26): within 1.5e-7, and within 0.3% of the value down to
+// erfc(4) = 1.5e-8, where the result is rounded to bf16 as a rule.
 #pragma once
 
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"
+#include "ptx_train.cuh"
 
 namespace mo {
 
-constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
-constexpr float kGeluB = 0.044715f;
+using ptx::F2;
+
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+using ptx::add2;
+using ptx::fma2;
+using ptx::mul2;
+
+// A number in both places
+template <typename N>
+__device__ __forceinline__ N both(float x) {
+  if constexpr (sizeof(N) == 8)
+    return ptx::f2(x);
+  else
+    return x;
+}
+// f of each
+template <typename F>
+__device__ __forceinline__ float each(float x, F&& f) { return f(x); }
+template <typename F>
+__device__ __forceinline__ F2 each(F2 x, F&& f) {
+  const float2 p = ptx::parts(x);
+  return ptx::f2(f(p.x), f(p.y));
+}
+template <typename F>
+__device__ __forceinline__ float each(float x, float y, F&& f) { return f(x, y); }
+template <typename F>
+__device__ __forceinline__ F2 each(F2 x, F2 y, F&& f) {
+  const float2 p = ptx::parts(x), q = ptx::parts(y);
+  return ptx::f2(f(p.x, q.x), f(p.y, q.y));
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -28,32 +67,12 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-constexpr float kLog2E = 1.4426950408889634f;
-
-// 1 / (1 + 2^-x): 0 where 2^-x is infinite
-__device__ __forceinline__ float logistic2(float x) { return reciprocal_fast(1.0f + exp2_fast(-x)); }
-
 // max(x, -3.4e38), NaN if x is: times 0, where it was -infinity, it gives -0
 __device__ __forceinline__ float bounded(float x) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(-3.402823466e38f));
   return r;
 }
-
-__device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(x * -0.70710678118654752f); }
-
-// act(x)
-template <int ACT>
-__device__ __forceinline__ float act_value(float x) {
-  if constexpr (ACT == MO_ACT_RELU) return x > 0.0f ? x : (x != x ? x : 0.0f);
-  if constexpr (ACT == MO_ACT_GELU) return bounded(x) * normal_cdf(x);
-  // the exponent is x (A + A B x^2) log2(e)
-  if constexpr (ACT == MO_ACT_GELU_TANH)
-    return bounded(x) * logistic2(x * fmaf(kGeluA * kGeluB * kLog2E, x * x, kGeluA * kLog2E));
-  if constexpr (ACT == MO_ACT_SILU) return bounded(x) * logistic2(x * kLog2E);
-  return x;
-}
-
 // x between -96 and 96, where what the slopes are made of is 0 or 1 to fp32 (or
 // below 2^-126); NaN if x is
 __device__ __forceinline__ float clamped(float x) {
@@ -62,34 +81,85 @@ __device__ __forceinline__ float clamped(float x) {
   return r;
 }
 
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+// 1 / (1 + 2^x): 0 where 2^x is infinite
+template <typename N>
+__device__ __forceinline__ N logistic_of(N x) {
+  return each(add2(each(x, exp2_fast), both<N>(1.0f)), reciprocal_fast);
+}
+
+// Phi(x), and e^(-x^2 / 2) in *bell
+template <typename N>
+__device__ __forceinline__ N normal_cdf(N x, N* bell) {
+  const N e = each(mul2(mul2(x, x), both<N>(-0.5f * kLog2E)), exp2_fast);
+  // 1 + p |x| / sqrt(2)
+  const N t = each(each(x, [](float v) { return fmaf(0.3275911f * 0.70710678f, fabsf(v), 1.0f); }), reciprocal_fast);
+  N q = fma2(t, both<N>(1.061405429f), both<N>(-1.453152027f));
+  q = fma2(t, q, both<N>(1.421413741f));
+  q = fma2(t, q, both<N>(-0.284496736f));
+  q = fma2(t, q, both<N>(0.254829592f));
+  const N half = mul2(mul2(mul2(t, both<N>(0.5f)), q), e);   // erfc(|x| / sqrt(2)) / 2
+  *bell = e;
+  return each(x, half, [](float v, float h) { return v >= 0.0f ? 1.0f - h : h; });
+}
+
+// act(x)
+template <int ACT, typename N>
+__device__ __forceinline__ N act_value(N x) {
+  if constexpr (ACT == MO_ACT_NONE) {
+    return x;
+  } else if constexpr (ACT == MO_ACT_RELU) {
+    return each(x, [](float v) {
+      float r;
+      asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+      return r;
+    });
+  } else {
+    const N y = each(x, bounded);
+    if constexpr (ACT == MO_ACT_GELU) {
+      N bell;
+      return mul2(y, normal_cdf(x, &bell));
+    } else if constexpr (ACT == MO_ACT_GELU_TANH) {
+      // the exponent is -x (A + A B x^2) log2(e)
+      const N u = mul2(x, fma2(mul2(x, x), both<N>(-kGeluA * kGeluB * kLog2E), both<N>(-kGeluA * kLog2E)));
+      return mul2(y, logistic_of(u));
+    } else {
+      return mul2(y, logistic_of(mul2(x, both<N>(-kLog2E))));
+    }
+  }
+}
+
 // act'(x), and act(x) in *value
-template <int ACT>
-__device__ __forceinline__ float act_slope(float x, float* value) {
-  if constexpr (ACT == MO_ACT_RELU) {
-    *value = x > 0.0f ? x : (x != x ? x : 0.0f);
-    return x > 0.0f ? 1.0f : (x != x ? x : 0.0f);
+template <int ACT, typename N>
+__device__ __forceinline__ N act_slope(N x, N* value) {
+  if constexpr (ACT == MO_ACT_NONE) {
+    *value = x;
+    return both<N>(1.0f);
+  } else if constexpr (ACT == MO_ACT_RELU) {
+    *value = act_value<ACT>(x);
+    return each(x, [](float v) { return v > 0.0f ? 1.0f : (v != v ? v : 0.0f); });
+  } else {
+    const N z = each(x, bounded), y = each(x, clamped);
+    if constexpr (ACT == MO_ACT_GELU) {
+      N bell;
+      const N c = normal_cdf(y, &bell);
+      *value = mul2(z, c);
+      return fma2(mul2(y, both<N>(0.3989422804f)), bell, c);   // (e^(-y^2 / 2) is 0 long before y is clamped)
+    } else if constexpr (ACT == MO_ACT_GELU_TANH) {
+      const N q = mul2(y, y);
+      const N s = logistic_of(mul2(y, fma2(q, both<N>(-kGeluA * kGeluB * kLog2E), both<N>(-kGeluA * kLog2E))));
+      *value = mul2(z, s);
+      const N d = mul2(s, fma2(s, both<N>(-1.0f), both<N>(1.0f)));   // s (1 - s)
+      return fma2(mul2(d, y), fma2(q, both<N>(3.0f * kGeluA * kGeluB), both<N>(kGeluA)), s);
+    } else {
+      const N s = logistic_of(mul2(y, both<N>(-kLog2E)));
+      *value = mul2(z, s);
+      return fma2(mul2(s, fma2(s, both<N>(-1.0f), both<N>(1.0f))), y, s);
+    }
   }
-  if constexpr (ACT == MO_ACT_GELU) {
-    const float c = normal_cdf(x);
-    *value = bounded(x) * c;
-    // x e^(-x^2 / 2) is 0 in fp32 from |x| = 15 on (and infinity times 0 is not a number)
-    const float t = fabsf(x) < 16.0f ? x * exp2_fast(-0.5f * kLog2E * x * x) : (x != x ? x : 0.0f);
-    return fmaf(0.3989422804014327f, t, c);
-  }
-  if constexpr (ACT == MO_ACT_GELU_TANH) {
-    const float y = clamped(x), y2 = y * y;   // all 0 or 1 beyond
-    const float s = logistic2(y * fmaf(kGeluA * kGeluB * kLog2E, y2, kGeluA * kLog2E));
-    *value = bounded(x) * s;
-    return fmaf(fmaf(-s, s, s) * y, fmaf(3.0f * kGeluA * kGeluB, y2, kGeluA), s);
-  }
-  if constexpr (ACT == MO_ACT_SILU) {
-    const float y = clamped(x);
-    const float s = logistic2(y * kLog2E);
-    *value = bounded(x) * s;
-    return fmaf(fmaf(-s, s, s), y, s);
-  }
-  *value = x;
-  return 1.0f;
 }
 
 // Calls f(Act<ACT>()) for a run-time activation.

@@ -129,6 +129,40 @@ __device__ __forceinline__ void store32(float* p, int align, const float (&v)[32
   }
 }
 
+// act of 32 (or 16) numbers, and times u
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 y = ptx::parts(act_value<ACT>(ptx::f2(v[i], v[i + 1])));
+    v[i] = y.x;
+    v[i + 1] = y.y;
+  }
+}
+template <int ACT, int N>
+__device__ __forceinline__ void gate_all(float (&g)[N], const float (&u)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 y = ptx::parts(ptx::mul2(act_value<ACT>(ptx::f2(g[i], g[i + 1])), ptx::f2(u[i], u[i + 1])));
+    g[i] = y.x;
+    g[i + 1] = y.y;
+  }
+}
+// dg, du and h of g, u and dh, in their places
+template <int ACT, int N>
+__device__ __forceinline__ void gate_grad_all(float (&g)[N], float (&u)[N], float (&dh)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const F2 u2 = ptx::f2(u[i], u[i + 1]), d2 = ptx::f2(dh[i], dh[i + 1]);
+    F2 a;
+    const F2 slope = act_slope<ACT>(ptx::f2(g[i], g[i + 1]), &a);
+    const float2 dg = ptx::parts(ptx::mul2(ptx::mul2(d2, u2), slope)), du = ptx::parts(ptx::mul2(d2, a)), h = ptx::parts(ptx::mul2(a, u2));
+    g[i] = dg.x, g[i + 1] = dg.y;
+    dh[i] = du.x, dh[i + 1] = du.y;
+    u[i] = h.x, u[i + 1] = h.y;
+  }
+}
+
 __device__ __forceinline__ void put(void* out, bool bf16, int64_t at, float v) {
   if (bf16)
     store1(static_cast<uint16_t*>(out) + at, v);
@@ -202,11 +236,14 @@ __device__ __forceinline__ void keep_chunk(const Kept& q, int align, int64_t row
   for (int i = 1; i < 31; i += 2) top = top3(top, v[i], v[i + 1]);
   top = top2(top, fabsf(v[31]));
   const uint32_t s = mx8_scale(top);
-  const float down = mx8_down(s);
+  const F2 down = ptx::f2(mx8_down(s));
   uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i] = cvt_e4m3x4(v[4 * i] * down, v[4 * i + 1] * down, v[4 * i + 2] * down, v[4 * i + 3] * down);
+  for (int i = 0; i < 8; ++i) {
+    const float2 a = ptx::parts(ptx::mul2(ptx::f2(v[4 * i], v[4 * i + 1]), down));
+    const float2 b = ptx::parts(ptx::mul2(ptx::f2(v[4 * i + 2], v[4 * i + 3]), down));
+    w[i] = cvt_e4m3x4(a.x, a.y, b.x, b.y);
+  }
   const int64_t nb = (n + 31) / 32;
   uint8_t* o = static_cast<uint8_t*>(q.data) + row * nb * 32 + col;
   if (align == 32) {

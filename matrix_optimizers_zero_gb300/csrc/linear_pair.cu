@@ -73,19 +73,20 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       if (row0 >= t.m || col >= t.n) continue;
       if (p.bias != nullptr) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (whole)
-            v[i] += bias[i];
-          else if (col + i < t.n)
-            v[i] += p.bias[col + i];
+        for (int i = 0; i < 32; i += 2) {
+          if (whole) {
+            const float2 y = ptx::parts(ptx::add2(ptx::f2(v[i], v[i + 1]), ptx::f2(bias[i], bias[i + 1])));
+            v[i] = y.x;
+            v[i + 1] = y.y;
+          } else {
+            if (col + i < t.n) v[i] += p.bias[col + i];
+            if (col + i + 1 < t.n) v[i + 1] += p.bias[col + i + 1];
+          }
         }
       }
       if (p.pre.data != nullptr) keep_chunk(p.pre, p.pre_align, row0, t.m, col, t.n, v, turn);
       if (p.act != MO_ACT_NONE)
-        with_act(p.act, [&](auto act) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
-        });
+        with_act(p.act, [&](auto act) { act_all<decltype(act)::value>(v); });
       store_chunk(t.out, t.out_bf16 != 0, t.ld, t.add, t.add_bf16 != 0, t.add_ld, t.align, row0, t.m, col, t.n, v, turn);
     }
   } else if constexpr (EPI == kEpiGated) {
@@ -100,10 +101,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
         keep_chunk(p.pre, p.pre_align, row0, t.m, col, t.n, g, turn);
         keep_chunk(p.pre2, p.pre_align, row0, t.m, col, t.n, u, turn);
       }
-      with_act(p.act, [&](auto act) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) g[i] = act_value<decltype(act)::value>(g[i]) * u[i];
-      });
+      with_act(p.act, [&](auto act) { gate_all<decltype(act)::value>(g, u); });
       // (a whole chunk: the rows of the workspace are padded)
       if (row < t.m) store32(static_cast<uint16_t*>(t.out) + row * t.ld + col, 32, g);
     }
@@ -132,16 +130,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       if (row >= t.m || col >= t.n) continue;
 #pragma unroll
       for (int i = 0; i < 16; ++i) dh[i] = __uint_as_float(r[i]);
-      with_act(p.act, [&](auto act) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a;
-          const float slope = act_slope<decltype(act)::value>(g[i], &a);
-          g[i] = dh[i] * u[i] * slope;
-          u[i] = a * u[i];
-          dh[i] = dh[i] * a;
-        }
-      });
+      with_act(p.act, [&](auto act) { gate_grad_all<decltype(act)::value>(g, u, dh); });
       const int64_t at = row * t.ld + col;
       store16(static_cast<uint16_t*>(t.out) + at, g);
       store16(p.out2 + at, dh);

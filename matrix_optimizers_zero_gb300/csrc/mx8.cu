@@ -216,7 +216,7 @@ __device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t ro
       float d[8];
       load8(reinterpret_cast<const uint16_t*>(&dout[u]), d);
       if constexpr (ACT != MO_ACT_NONE) {
-        float z[8], value;
+        float z[8];
         if constexpr (MX8) {
           const float up = mx8_up(pre[u].z);
           float a[4], b[4];
@@ -231,7 +231,12 @@ __device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t ro
           load8(reinterpret_cast<const uint16_t*>(&pre[u]), z);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= act_slope<ACT>(z[i], &value);
+        for (int i = 0; i < 8; i += 2) {
+          F2 value;
+          const float2 y = ptx::parts(ptx::mul2(ptx::f2(d[i], d[i + 1]), act_slope<ACT>(ptx::f2(z[i], z[i + 1]), &value)));
+          d[i] = y.x;
+          d[i + 1] = y.y;
+        }
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += d[i];

@@ -21,8 +21,6 @@
 namespace mo {
 namespace {
 
-using ptx::F2;
-
 // A team of TEAM threads holds a row of at most TEAM V elements, V a thread:
 // eight neighbours of every 8 TEAM where rows are 16-byte aligned (VEC), one of
 // every TEAM otherwise. Either way 32 elements of a block lie in one warp.
