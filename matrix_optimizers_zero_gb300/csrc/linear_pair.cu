@@ -8,7 +8,7 @@
 // 256 x 256 tiles on CTA pairs (cta_group::2), persistent, as the Newton-Schulz
 // products: warp 0 loads this CTA's 128-row halves of both operands by TMA
 // (128-byte swizzle) into six 32 KB stages, the even CTA's warp 1 issues the
-// instructions, warps 2-9 drain 128 lanes x 256 columns; two accumulators let a
+// instructions, warps 2-17 drain 128 lanes x 256 columns; two accumulators let a
 // tile's epilogue run under the next tile's products. Either operand's rows may
 // run along k (K-major) or along its own index (MN-major: the transposed
 // operands of the gradients, as they lie in memory).
@@ -19,6 +19,7 @@
 // both.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "launch.cuh"
@@ -27,14 +28,15 @@
 namespace mo {
 namespace {
 
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;   // four a quarter of the lanes
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kStages = 6;
+constexpr int kStages = 6;      // five where the epilogue turns chunks in shared memory (p.stages)
 constexpr uint32_t kHalf = 128 * kBlockK * 2;   // 16 KB: 128 rows of an operand
 constexpr uint32_t kStage = 2 * kHalf;
 constexpr uint32_t kBars = 2 * kStages + 5;
 constexpr uint32_t kCtrl = 256;
-constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kCtrl + size_t(kEpiWarps) * kTurn * 4;
+constexpr uint32_t kTurns = uint32_t(kEpiWarps) * kTurn * 4;
+constexpr size_t kSmem = 1024 + kCtrl + std::max(size_t(kStages) * kStage, size_t(kStages - 1) * kStage + kTurns);
 static_assert(8 * kBars + 16 <= kCtrl && kSmem <= 227 * 1024, "shared memory");
 
 // A chunk of 32 columns of an accumulator, a row a lane.
@@ -48,40 +50,33 @@ __device__ __forceinline__ void tmem_chunk(uint32_t taddr, float (&v)[32]) {
 }
 
 // The 32 rows from row0 on (lane l has row0 + l) of the `width` accumulator
-// columns from TMEM column `tb` on: chunks of 32 (or 16) columns, every other one
-// each half's. col0: the first column of the output.
+// columns from TMEM column `tb` on: chunks of 32 (or 16) columns, every fourth one
+// this warp's, from `part` on. col0: the first column of the output.
 template <Epilogue EPI>
-__device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& t, int64_t row0, int64_t col0, int width, int half,
+__device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& t, int64_t row0, int64_t col0, int width, int part,
                                          uint32_t tb, float* turn) {
   const int lane = int(threadIdx.x & 31);
   const int64_t row = row0 + lane;
   if constexpr (EPI == kEpiLinear) {
 #pragma unroll 1
-    for (int c = half * 32; c < width; c += 64) {
+    for (int c = part * 32; c < width; c += 128) {
       const int64_t col = col0 + c;
-      float bias[32];   // under way while the accumulator is read
-      const bool whole = col + 32 <= t.n;
-      if (p.bias != nullptr && whole) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 b = reinterpret_cast<const float4*>(p.bias + col)[j];
-          bias[4 * j] = b.x, bias[4 * j + 1] = b.y, bias[4 * j + 2] = b.z, bias[4 * j + 3] = b.w;
-        }
-      }
       float v[32];
       tmem_chunk(tb + uint32_t(c), v);
       if (row0 >= t.m || col >= t.n) continue;
       if (p.bias != nullptr) {
+        if (col + 32 <= t.n) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          if (whole) {
-            const float2 y = ptx::parts(ptx::add2(ptx::f2(v[i], v[i + 1]), ptx::f2(bias[i], bias[i + 1])));
-            v[i] = y.x;
-            v[i + 1] = y.y;
-          } else {
-            if (col + i < t.n) v[i] += p.bias[col + i];
-            if (col + i + 1 < t.n) v[i + 1] += p.bias[col + i + 1];
+          for (int j = 0; j < 8; ++j) {
+            const float4 b = reinterpret_cast<const float4*>(p.bias + col)[j];
+            const float2 lo = ptx::parts(ptx::add2(ptx::f2(v[4 * j], v[4 * j + 1]), ptx::f2(b.x, b.y)));
+            const float2 hi = ptx::parts(ptx::add2(ptx::f2(v[4 * j + 2], v[4 * j + 3]), ptx::f2(b.z, b.w)));
+            v[4 * j] = lo.x, v[4 * j + 1] = lo.y, v[4 * j + 2] = hi.x, v[4 * j + 3] = hi.y;
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (col + i < t.n) v[i] += p.bias[col + i];
         }
       }
       if (p.pre.data != nullptr) keep_chunk(p.pre, p.pre_align, row0, t.m, col, t.n, v, turn);
@@ -91,7 +86,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
     }
   } else if constexpr (EPI == kEpiGated) {
 #pragma unroll 1
-    for (int c = half * 32; c < width / 2; c += 64) {
+    for (int c = part * 32; c < width / 2; c += 128) {
       const int64_t col = col0 + c;
       float g[32], u[32];
       tmem_chunk(tb + uint32_t(c), g);
@@ -115,14 +110,14 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
         fetch_kept(p.pre2, p.pre_align, row, col, t.n, ru);
       }
     };
-    fetch(half * 16);
+    fetch(part * 16);
 #pragma unroll 1
-    for (int c = half * 16; c < width; c += 32) {
+    for (int c = part * 16; c < width; c += 64) {
       const int64_t col = col0 + c;
       float g[16], u[16], dh[16];
       kept_values(p.pre, rg, g);
       kept_values(p.pre2, ru, u);
-      if (c + 32 < width) fetch(c + 32);
+      if (c + 64 < width) fetch(c + 64);
       uint32_t r[16];
       __syncwarp();
       ptx::tmem_ld_32x32b_x16(tb + uint32_t(c), r);
@@ -162,7 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  const uint32_t bars = base + uint32_t(kStages) * kStage;
+  // stages (1024-byte aligned), or five of them and the chunks that are turned, then control
+  const uint32_t bars = base + uint32_t(kSmem - 1024 - kCtrl);
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kBars);
   uint32_t* tmem_slot = ctrl;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 1);
@@ -251,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
             for (int32_t j = 0; j < half; j += 32) ptx::tma_load_2d_pair(sb + uint32_t(j) * 128u, &p.bs[opb], fb, k0, rb + j);
           }
           ++n_issued;
-          if (++stage == kStages) {
+          if (++stage == p.stages) {
             stage = 0;
             ph ^= 1u;
           }
@@ -290,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
           }
           ptx::umma_commit_pair(empty_bar(stage), 0x3);
           mma_issued = true;
-          if (++stage == kStages) {
+          if (++stage == p.stages) {
             stage = 0;
             ph ^= 1u;
           }
@@ -302,8 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
-    float* turn = reinterpret_cast<float*>(smem_raw + (bars - raw) + kCtrl) + (warp - 2) * kTurn;
+    const int part = (warp - 2) >> 2;
+    // (the sixth stage's memory and what is behind it, where five are in use)
+    float* turn = reinterpret_cast<float*>(smem_raw + (base - raw) + (kStages - 1) * kStage) + (warp - 2) * kTurn;
     int32_t n = 0;
     for (int32_t i = first; i < p.tiles; i += step, ++n) {
       const int acc = n & 1;
@@ -314,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
       ptx::tc_fence_after();
       const int64_t row0 = int64_t(t.tm) * 256 + int64_t(rank) * 128 + quarter * 32;
       const int64_t col0 = EPI == kEpiGated ? int64_t(t.tn) * 128 + t.sub * (t.width / 2) : int64_t(t.tn) * 256 + t.sub * t.width;
-      epilogue<EPI>(p, p.t[t.q], row0, col0, t.width, half, tmem + uint32_t(acc) * 256u + (uint32_t(quarter * 32) << 16), turn);
+      epilogue<EPI>(p, p.t[t.q], row0, col0, t.width, part, tmem + uint32_t(acc) * 256u + (uint32_t(quarter * 32) << 16), turn);
       // hand the accumulator back: its reads are complete (tcgen05.wait::ld) and fenced, and nothing
       // else of the tile has to be ordered inside the launch
       ptx::tc_fence_before();
@@ -333,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
   if (*abort_flag != 0 || peer_report[0] != 0u) {
     // Nothing may still write into either CTA's memory when they exit: the even CTA waits for its
     // instructions, then settles every stage that either producer left in flight (all copies of both
-    // CTAs count their bytes on its full barriers; at most the last kStages can be in flight).
+    // CTAs count their bytes on its full barriers; at most the last p.stages can be in flight).
     if (leader && warp == 1 && lane == 0 && mma_issued) {
       ptx::umma_commit_pair(drain_bar, 0x1);
       mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
@@ -343,14 +340,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
       const uint32_t most = L > P ? L : P;
       // stages of this pair's uncut tiles, which come first
       const uint32_t wide = first < p.whole ? uint32_t((p.whole - first + step - 1) / step) * uint32_t(blocks) : 0u;
-      for (uint32_t j = most > uint32_t(kStages) ? most - uint32_t(kStages) : 0u; j < most; ++j) {
-        const int s = int(j % uint32_t(kStages));
+      const uint32_t stages = uint32_t(p.stages);
+      for (uint32_t j = most > stages ? most - stages : 0u; j < most; ++j) {
+        const int s = int(j % stages);
         const uint32_t bytes = kHalf + (j < wide ? kHalf : kHalf / uint32_t(p.cut));
         if (j >= L)
           ptx::mbar_arrive_expect_tx(full_bar(s), bytes);   // only the peer's half is coming
         else if (j >= P)
           ptx::mbar_complete_tx(full_bar(s), bytes);        // the peer's half never will
-        mbar_wait_drain(full_bar(s), (j / uint32_t(kStages)) & 1u, p.timeout_ns);
+        mbar_wait_drain(full_bar(s), (j / stages) & 1u, p.timeout_ns);
       }
     }
     ptx::cluster_sync();
@@ -397,6 +395,12 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
   // The tiles of a last round that leaves half of the pairs idle, or three quarters, are cut into as
   // many parts. (Parts of 64 columns not where B's rows run along k: its boxes are 64 wide a CTA.)
   const int64_t pairs = sms / 2, last = tiles % pairs;
+  // (whole chunks of aligned rows are stored as they are; the rows of the workspace are padded)
+  bool turned = false;
+  for (int i = 0; i < q.count; ++i)
+    turned |= EPI == kEpiLinear && (p.t[i].align == 0 || p.t[i].n % 32 != 0);
+  turned |= q.pre.data != nullptr && q.pre.dtype != MO_MX8 && EPI != kEpiGatedGrad && (p.pre_align == 0 || q.t[0].n % 32 != 0);
+  p.stages = turned ? kStages - 1 : kStages;
   p.cut = last * 2 > pairs || last == 0 ? 1 : !B_MN && last * 4 <= pairs ? 4 : 2;
   p.whole = int32_t(p.cut > 1 ? tiles - last : tiles);
   p.tiles = int32_t(p.cut > 1 ? tiles + last * (p.cut - 1) : tiles);
