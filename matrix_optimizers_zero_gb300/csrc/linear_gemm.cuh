@@ -24,7 +24,7 @@ struct GemmTarget {
 
 struct GemmParams {
   CUtensorMap a[3], b[3];
-  CUtensorMap bs[3];             // pairs: b in boxes of 32 rows (64 columns where its rows run along k), for cut tiles
+  CUtensorMap bs[3];             // pairs, K-major: b in boxes of 32 rows, for cut tiles
   GemmTarget t[3];
   int32_t count, segments;
   int32_t blocks;                // stages a segment

@@ -28,14 +28,15 @@
 namespace mo {
 namespace {
 
-constexpr int kEpiWarps = 16;   // four a quarter of the lanes
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+// Epilogue warps: two a quarter of the lanes, or four where the reduction is short
+// (see launch_pair).
+constexpr int kMostWarps = 16;
 constexpr int kStages = 6;      // five where the epilogue turns chunks in shared memory (p.stages)
 constexpr uint32_t kHalf = 128 * kBlockK * 2;   // 16 KB: 128 rows of an operand
 constexpr uint32_t kStage = 2 * kHalf;
 constexpr uint32_t kBars = 2 * kStages + 5;
 constexpr uint32_t kCtrl = 256;
-constexpr uint32_t kTurns = uint32_t(kEpiWarps) * kTurn * 4;
+constexpr uint32_t kTurns = uint32_t(kMostWarps) * kTurn * 4;
 constexpr size_t kSmem = 1024 + kCtrl + std::max(size_t(kStages) * kStage, size_t(kStages - 1) * kStage + kTurns);
 static_assert(8 * kBars + 16 <= kCtrl && kSmem <= 227 * 1024, "shared memory");
 
@@ -50,16 +51,16 @@ __device__ __forceinline__ void tmem_chunk(uint32_t taddr, float (&v)[32]) {
 }
 
 // The 32 rows from row0 on (lane l has row0 + l) of the `width` accumulator
-// columns from TMEM column `tb` on: chunks of 32 (or 16) columns, every fourth one
+// columns from TMEM column `tb` on: chunks of 32 (or 16) columns, every PARTSth one
 // this warp's, from `part` on. col0: the first column of the output.
-template <Epilogue EPI>
+template <Epilogue EPI, int PARTS>
 __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& t, int64_t row0, int64_t col0, int width, int part,
                                          uint32_t tb, float* turn) {
   const int lane = int(threadIdx.x & 31);
   const int64_t row = row0 + lane;
   if constexpr (EPI == kEpiLinear) {
 #pragma unroll 1
-    for (int c = part * 32; c < width; c += 128) {
+    for (int c = part * 32; c < width; c += 32 * PARTS) {
       const int64_t col = col0 + c;
       float v[32];
       tmem_chunk(tb + uint32_t(c), v);
@@ -86,7 +87,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
     }
   } else if constexpr (EPI == kEpiGated) {
 #pragma unroll 1
-    for (int c = part * 32; c < width / 2; c += 128) {
+    for (int c = part * 32; c < width / 2; c += 32 * PARTS) {
       const int64_t col = col0 + c;
       float g[32], u[32];
       tmem_chunk(tb + uint32_t(c), g);
@@ -112,12 +113,12 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
     };
     fetch(part * 16);
 #pragma unroll 1
-    for (int c = part * 16; c < width; c += 64) {
+    for (int c = part * 16; c < width; c += 16 * PARTS) {
       const int64_t col = col0 + c;
       float g[16], u[16], dh[16];
       kept_values(p.pre, rg, g);
       kept_values(p.pre2, ru, u);
-      if (c + 64 < width) fetch(c + 64);
+      if (c + 16 * PARTS < width) fetch(c + 16 * PARTS);
       uint32_t r[16];
       __syncwarp();
       ptx::tmem_ld_32x32b_x16(tb + uint32_t(c), r);
@@ -152,8 +153,8 @@ __device__ __forceinline__ Tile tile_of(const GemmParams& p, int32_t i) {
   return t;
 }
 
-template <Epilogue EPI, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_constant__ GemmParams p) {
+template <Epilogue EPI, bool A_MN, bool B_MN, int WARPS>
+__global__ void __launch_bounds__(64 + 32 * WARPS, 1) linear_pair_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(tfull_bar(s), 1);
-      ptx::mbar_init(tempty_bar(s), 2 * kEpiWarps);
+      ptx::mbar_init(tempty_bar(s), 2 * WARPS);
     }
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ MMA issuer (even CTA)
+      const uint32_t a_lo = ptx::desc_lo(base, A_MN ? kBox : 16u), b_lo = ptx::desc_lo(base + kHalf, B_MN ? kBox : 16u);
       int stage = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -275,15 +277,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sa = base + uint32_t(stage) * kStage, sb = sa + kHalf;
+          // K = 16 an instruction: 32 bytes of K-major rows, 16 rows of MN-major ones
+          const uint32_t at = uint32_t(stage) * (kStage / 16);
 #pragma unroll
-          for (int kk = 0; kk < kBlockK / 16; ++kk) {
-            const uint64_t ad = A_MN ? ptx::smem_desc_sw128(sa + uint32_t(kk) * 2048u, kBox, 1024u)
-                                     : ptx::smem_desc_sw128(sa + uint32_t(kk) * 32u, 16u, 1024u);
-            const uint64_t bd = B_MN ? ptx::smem_desc_sw128(sb + uint32_t(kk) * 2048u, kBox, 1024u)
-                                     : ptx::smem_desc_sw128(sb + uint32_t(kk) * 32u, 16u, 1024u);
-            ptx::umma_bf16_pair(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < kBlockK / 16; ++kk)
+            ptx::umma_bf16_pair_lo(d, a_lo + at + uint32_t(kk) * (A_MN ? 128u : 2u), b_lo + at + uint32_t(kk) * (B_MN ? 128u : 2u), idesc,
+                                   (kb | kk) != 0 ? 1u : 0u);
           ptx::umma_commit_pair(empty_bar(stage), 0x3);
           mma_issued = true;
           if (++stage == p.stages) {
@@ -311,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const __grid_c
       ptx::tc_fence_after();
       const int64_t row0 = int64_t(t.tm) * 256 + int64_t(rank) * 128 + quarter * 32;
       const int64_t col0 = EPI == kEpiGated ? int64_t(t.tn) * 128 + t.sub * (t.width / 2) : int64_t(t.tn) * 256 + t.sub * t.width;
-      epilogue<EPI>(p, p.t[t.q], row0, col0, t.width, part, tmem + uint32_t(acc) * 256u + (uint32_t(quarter * 32) << 16), turn);
+      epilogue<EPI, WARPS / 4>(p, p.t[t.q], row0, col0, t.width, part, tmem + uint32_t(acc) * 256u + (uint32_t(quarter * 32) << 16), turn);
       // hand the accumulator back: its reads are complete (tcgen05.wait::ld) and fenced, and nothing
       // else of the tile has to be ordered inside the launch
       ptx::tc_fence_before();
@@ -404,11 +403,15 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
   p.cut = last * 2 > pairs || last == 0 ? 1 : !B_MN && last * 4 <= pairs ? 4 : 2;
   p.whole = int32_t(p.cut > 1 ? tiles - last : tiles);
   p.tiles = int32_t(p.cut > 1 ? tiles + last * (p.cut - 1) : tiles);
-  auto kern = linear_pair_kernel<EPI, A_MN, B_MN>;
+  // Short reductions: with eight warps an epilogue takes longer than the products of a tile (8192 x 1280
+  // x 5120 with gelu and an 8-bit copy: 106 us, with sixteen 100). Long ones: the sixteen's waiting costs
+  // more than it gives (gated block 8192 x 4096 x 14336: 1775 and 1850 us).
+  const bool few = int64_t(p.blocks) * q.segments > 32;
+  auto kern = few ? linear_pair_kernel<EPI, A_MN, B_MN, 8> : linear_pair_kernel<EPI, A_MN, B_MN, kMostWarps>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem);
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(2 * std::min<int64_t>(pairs, p.tiles));
-  return launch_kernel(kern, dim3(grid), dim3(kThreads), kSmem, 2, true, stream, p);
+  return launch_kernel(kern, dim3(grid), dim3(64 + 32 * (few ? 8 : kMostWarps)), kSmem, 2, true, stream, p);
 }
 
 }  // namespace

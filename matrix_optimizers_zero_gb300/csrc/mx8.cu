@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) unpack_odd_kernel(const uint8_t* __r
 // dz = dout act'(pre) and its column sums: a block takes 256 columns, eight a
 // thread, and `per` rows, eight at a time (one a warp); its warps' sums are
 // joined in order. A launch of strips x parts blocks.
-constexpr int kRowsAhead = 4;   // of a warp, loaded together
+constexpr int kRowsAhead = 2;   // of a warp, loaded together
 
 template <bool MX8, int ACT>
 __device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t row0, int64_t row1, int64_t col, float (&sum)[8]) {
@@ -277,7 +277,7 @@ __device__ __forceinline__ void act_grad_rows_odd(const ActGradParams& p, int64_
 }
 
 template <bool VEC, bool MX8>
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams p) {
+__global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) act_grad_kernel(const ActGradParams p) {
   __shared__ float sums[8][256];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();

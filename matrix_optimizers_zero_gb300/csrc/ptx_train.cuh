@@ -32,6 +32,12 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) 
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
+// Upper half of the descriptor of a K-major operand of 128-byte rows
+// (smem_desc_sw128 with 1024 bytes between 8-row groups); the lower half is
+// the address / 16 with the unused leading dimension (1) above it.
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_sw128(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+
 // D (+)= (A sA)(B sB)^T over K = 64. kMx: a scale for 32 elements (e8m0),
 // otherwise for 16 (e4m3). The accumulator, and the A scales, are those of
 // each CTA's own rows; each CTA holds the B scales of all N columns. The
@@ -54,12 +60,6 @@ __device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint32_t a_lo, uint32_
   if (!kPair && !kMx) MO_UMMA_FP4("1", "mxf4nvf4", "4X");
 #undef MO_UMMA_FP4
 }
-
-// Upper half of the descriptor of a K-major operand of 128-byte rows
-// (smem_desc_sw128 with 1024 bytes between 8-row groups); the lower half is
-// the address / 16 with the unused leading dimension (1) above it.
-constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo_sw128(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 
 __device__ __forceinline__ uint32_t cluster_nctarank() {
   uint32_t r;
@@ -115,6 +115,19 @@ __device__ __forceinline__ void tmem_dealloc_one(uint32_t taddr, uint32_t ncols)
 }
 __device__ __forceinline__ void umma_commit_one(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// umma_bf16_pair with descriptors as their lower halves (the upper half
+// is the same for both majors): address / 16 and the leading dimension / 16 above
+// bit 16.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void umma_bf16_pair_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHiSw128), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // D (+)= A B^T over K = 16 with bf16 operands, one CTA.
