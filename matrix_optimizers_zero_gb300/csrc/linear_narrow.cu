@@ -2,8 +2,8 @@
 // multiplies 128 columns' operand by NT rows' over its part of the reduction,
 // and the CTAs of a cluster, which hold the parts of one tile, add their sums
 // through distributed shared memory in rank order. Accumulator lanes are
-// columns of the output, so a warp's 32 lanes store 32 neighbours of a row,
-// and are a block of an 8-bit tensor.
+// columns of the output; after the addition a lane has four neighbours of a row,
+// and eight lanes a block of an 8-bit tensor.
 //
 // With few rows a product is the reading of its weights, so K is split until
 // all SMs have loads under way.
@@ -24,9 +24,10 @@ template <Epilogue EPI>
 constexpr int kPanels = EPI == kEpiGated ? 2 : 1;   // gate and up
 template <Epilogue EPI, int NT>
 constexpr uint32_t kStage = kPanels<EPI> * kPanel + NT * kBlockK * 2;
-// Two CTAs an SM where the sums and enough stages fit.
+// Two CTAs an SM where the sums and enough stages fit; with gate and up one and
+// all its memory (one token of the 8B block: 63 -> 60 us).
 template <Epilogue EPI, int NT>
-constexpr int kStages = EPI == kEpiGated ? (NT == 16 ? 3 : NT == 64 ? 5 : 4) : (NT == 16 ? 6 : NT == 64 ? 4 : 3);
+constexpr int kStages = EPI == kEpiGated ? (NT == 16 ? 6 : NT == 64 ? 5 : 4) : (NT == 16 ? 6 : NT == 64 ? 4 : 3);
 template <Epilogue EPI, int NT>
 constexpr size_t kSmem = 1024 + size_t(kStages<EPI, NT>) * kStage<EPI, NT> + 160;
 template <Epilogue EPI, int NT>
@@ -37,48 +38,100 @@ static_assert(kFits<kEpiLinear, 16> && kFits<kEpiLinear, 64> && kFits<kEpiLinear
                   kFits<kEpiGated, 64> && kFits<kEpiGated, 128>,
               "sums in the stages' memory");
 
-// What follows the sums of one element; a warp has 32 neighbours of a row.
-template <Epilogue EPI>
-__device__ __forceinline__ void finish(const GemmParams& p, const GemmTarget& t, int64_t row, int64_t col, float x, float y) {
-  const bool in = col < t.n;
-  const int lane = int(threadIdx.x & 31);
-  auto keep = [&](const Kept& q, float v) {
-    if (q.dtype == MO_MX8) {
-      float top = in ? fabsf(v) : 0.0f;
+// Four neighbours of a row, the first at `at` of a multiple of 4; `live` of them
+// inside it. VEC: rows of a multiple of 4.
+__device__ __forceinline__ void put4(void* out, bool bf16, int64_t at, int live, bool vec, const float (&v)[4]) {
+  if (vec) {
+    if (live <= 0) return;
+    if (bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    return;
+  }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      const int64_t nb = (t.n + 31) / 32;
-      if (col - lane >= t.n) return;
-      const uint32_t s = mx8_scale(top);
-      static_cast<uint8_t*>(q.data)[row * nb * 32 + col] = uint8_t(cvt_e4m3x2(in ? v * mx8_down(s) : 0.0f, 0.0f));
-      if (lane == 0) q.scales[row * nb + (col >> 5)] = uint8_t(s);
-    } else if (in) {
-      store1(static_cast<uint16_t*>(q.data) + row * t.n + col, v);
+  for (int i = 0; i < 4; ++i)
+    if (i < live) put(out, bf16, at + i, v[i]);
+}
+__device__ __forceinline__ void get4(const void* p, bool bf16, int64_t at, int live, bool vec, float (&v)[4]) {
+  if (vec && live > 0) {
+    if (bf16) {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
     }
-  };
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = i < live ? get(p, bf16, at + i) : 0.0f;
+}
+
+// Kept values of four neighbours: in 8 bits eight lanes hold a block.
+__device__ __forceinline__ void keep4(const Kept& q, int64_t row, int64_t col, int64_t n, int live, bool vec, const float (&v)[4]) {
+  if (q.dtype != MO_MX8) {
+    put4(q.data, true, row * n + col, live, vec, v);
+    return;
+  }
+  float x[4], top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = i < live ? v[i] : 0.0f;
+    top = top2(top, fabsf(x[i]));
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const int64_t nb = (n + 31) / 32;
+  if ((col & ~int64_t(31)) >= n) return;
+  const uint32_t s = mx8_scale(top);
+  const float down = mx8_down(s);
+  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(q.data) + row * nb * 32 + col) =
+      cvt_e4m3x4(x[0] * down, x[1] * down, x[2] * down, x[3] * down);
+  if ((col & 31) == 0) q.scales[row * nb + (col >> 5)] = uint8_t(s);
+}
+
+// What follows the sums of four neighbours of a row; a warp has 128.
+template <Epilogue EPI>
+__device__ __forceinline__ void finish(const GemmParams& p, const GemmTarget& t, int64_t row, int64_t col, float (&x)[4], float (&y)[4]) {
+  const int live = int(max(int64_t(0), min(int64_t(4), t.n - col)));
+  const bool vec = (t.n & 3) == 0;
   if constexpr (EPI == kEpiLinear) {
-    if (p.bias != nullptr && in) x += p.bias[col];
-    if (p.pre.data != nullptr) keep(p.pre, x);
-    with_act(p.act, [&](auto act) { x = act_value<decltype(act)::value>(x); });
-    if (!in) return;
-    if (t.add != nullptr) x += get(t.add, t.add_bf16 != 0, row * t.add_ld + col);
-    put(t.out, t.out_bf16 != 0, row * t.ld + col, x);
+    if (p.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < live) x[i] += p.bias[col + i];
+    }
+    if (p.pre.data != nullptr) keep4(p.pre, row, col, t.n, live, vec, x);
+    with_act(p.act, [&](auto act) { act_all<decltype(act)::value>(x); });
+    if (t.add != nullptr) {
+      float a[4];
+      get4(t.add, t.add_bf16 != 0, row * t.add_ld + col, live, vec, a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] += a[i];
+    }
+    put4(t.out, t.out_bf16 != 0, row * t.ld + col, live, vec, x);
   } else if constexpr (EPI == kEpiGated) {
     if (p.pre.data != nullptr) {
-      keep(p.pre, x);
-      keep(p.pre2, y);
+      keep4(p.pre, row, col, t.n, live, vec, x);
+      keep4(p.pre2, row, col, t.n, live, vec, y);
     }
-    with_act(p.act, [&](auto act) { x = act_value<decltype(act)::value>(x) * y; });
-    if (in) store1(static_cast<uint16_t*>(t.out) + row * t.ld + col, x);
+    with_act(p.act, [&](auto act) { gate_all<decltype(act)::value>(x, y); });
+    put4(t.out, true, row * t.ld + col, live, vec, x);
   } else {
-    if (!in) return;
-    const float g = kept_at(p.pre, row, col, t.n), u = kept_at(p.pre2, row, col, t.n);
-    float a = 0.0f, slope = 0.0f;
-    with_act(p.act, [&](auto act) { slope = act_slope<decltype(act)::value>(g, &a); });
+    if (live <= 0) return;
+    float g[4], u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      g[i] = i < live ? kept_at(p.pre, row, col + i, t.n) : 0.0f;
+      u[i] = i < live ? kept_at(p.pre2, row, col + i, t.n) : 0.0f;
+    }
+    with_act(p.act, [&](auto act) { gate_grad_all<decltype(act)::value>(g, u, x); });
     const int64_t at = row * t.ld + col;
-    store1(static_cast<uint16_t*>(t.out) + at, x * u * slope);
-    store1(p.out2 + at, x * a);
-    store1(p.out3 + at, a * u);
+    put4(t.out, true, at, live, vec, g);
+    put4(p.out2, true, at, live, vec, x);
+    put4(p.out3, true, at, live, vec, u);
   }
 }
 
@@ -262,29 +315,29 @@ __global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_co
   }
   if (parts > 1) ptx::cluster_sync();   // every part's sums are in place
   {
-    // this CTA's share of the tile, 32 columns of a row a warp, parts added in rank order
+    // this CTA's share of the tile, a row a warp, four columns a lane, parts added in rank order
     const uint32_t sums_addr = ptx::smem_addr(sums);
-    const int64_t row0 = int64_t(tm) * NT, col0 = int64_t(tn) * 128;
-    const uint32_t units = uint32_t(min(int64_t(NT), t.m - row0)) * 4u;
-    for (uint32_t u = rank * kWarps + uint32_t(warp); u < units; u += parts * kWarps) {
-      const uint32_t j = u >> 2, c = (u & 3u) * 32u + uint32_t(lane);
-      float v[2] = {0.0f, 0.0f};
+    const int64_t row0 = int64_t(tm) * NT, col = int64_t(tn) * 128 + 4 * lane;
+    const uint32_t rows = uint32_t(min(int64_t(NT), t.m - row0));
+#pragma unroll 2
+    for (uint32_t j = rank * kWarps + uint32_t(warp); j < rows; j += parts * kWarps) {
+      float v[2][4];
 #pragma unroll
       for (int i = 0; i < kPanels<EPI>; ++i) {
-        const uint32_t at = (uint32_t(i) * NT + j) * kPitch + c;
-        if (parts == 1) {
-          v[i] = sums[at];
-        } else {
-          float x[8];
+        const uint32_t at = (uint32_t(i) * NT + j) * kPitch + 4u * uint32_t(lane);
+        float4 x[8];
 #pragma unroll
-          for (uint32_t s = 0; s < 8; ++s)
-            if (s < parts) x[s] = ptx::ld_shared_cluster_f32(ptx::mapa_shared(sums_addr + 4u * at, s));
+        for (uint32_t s = 0; s < 8; ++s)
+          if (s < parts)
+            x[s] = parts == 1 ? *reinterpret_cast<const float4*>(sums + at)
+                              : ptx::ld_shared_cluster_v4(ptx::mapa_shared(sums_addr + 4u * at, s));
+        float4 f = x[0];
 #pragma unroll
-          for (uint32_t s = 0; s < 8; ++s)
-            if (s < parts) v[i] += x[s];
-        }
+        for (uint32_t s = 1; s < 8; ++s)
+          if (s < parts) f.x += x[s].x, f.y += x[s].y, f.z += x[s].z, f.w += x[s].w;
+        v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
       }
-      finish<EPI>(p, t, row0 + j, col0 + c, v[0], v[1]);
+      finish<EPI>(p, t, row0 + j, col, v[0], v[kPanels<EPI> - 1]);
     }
   }
   if (parts > 1) ptx::cluster_sync();   // the peers have read this CTA's sums

@@ -141,9 +141,6 @@ __device__ __forceinline__ void umma_bf16_one(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
-  return __uint_as_float(ld_shared_cluster_u32(cluster_addr));
-}
 
 // TMA load into this CTA's shared memory, completion on its own mbarrier.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint32_t bar, int32_t x, int32_t y) {
