@@ -103,22 +103,32 @@ struct Launches {
   int status() const { return error == cudaSuccess ? MO_OK : report_cuda(error); }
 };
 
-// A bf16 operand [rows, cols] that TMA can read: rows of a multiple of 16
-// bytes, or else (and from 8 bits) laid out in the workspace.
+// The bf16 operands of a call's products as TMA can read them: rows of a multiple
+// of 16 bytes. Others, and those in 8 bits, are laid out in the workspace, all of
+// a launch's in one go.
 bool needs_copy(int64_t cols, int32_t dtype) { return dtype == MO_MX8 || cols % 8 != 0; }
 size_t copy_bytes(int64_t rows, int64_t cols) { return align256(size_t(rows) * size_t(padded(cols)) * 2); }
 
-Operand operand(const Kept& t, int64_t rows, int64_t cols, Workspace& ws, Launches& run, cudaStream_t stream) {
-  if (!needs_copy(cols, t.dtype)) return {t.data, rows, cols, cols};
-  void* copy = ws.take(size_t(rows) * size_t(padded(cols)) * 2);
-  if (run.error == cudaSuccess) run(mo::launch_unpack(t, rows, cols, copy, true, padded(cols), stream));
-  return {copy, rows, cols, padded(cols)};
-}
-Operand operand(const void* p, int64_t rows, int64_t cols, Workspace& ws, Launches& run, cudaStream_t stream) {
-  Kept t;
-  t.data = const_cast<void*>(p);
-  return operand(t, rows, cols, ws, run, stream);
-}
+struct Operands {
+  Workspace& ws;
+  mo::LayOut todo[3];
+  int n = 0;
+  Operand operator()(const Kept& t, int64_t rows, int64_t cols) {
+    if (!needs_copy(cols, t.dtype)) return {t.data, rows, cols, cols};
+    uint16_t* copy = static_cast<uint16_t*>(ws.take(size_t(rows) * size_t(padded(cols)) * 2));
+    todo[n++] = {t, rows, cols, copy, padded(cols)};
+    return {copy, rows, cols, padded(cols)};
+  }
+  Operand operator()(const void* p, int64_t rows, int64_t cols) {
+    Kept t;
+    t.data = const_cast<void*>(p);
+    return (*this)(t, rows, cols);
+  }
+  void lay_out(Launches& run, cudaStream_t stream) {
+    if (n > 0 && run.error == cudaSuccess) run(mo::launch_lay_out(todo, n, stream));
+    n = 0;
+  }
+};
 
 // Bytes of the partial sums of a product whose reduction is cut.
 size_t slice_bytes(int64_t k, int64_t m, int64_t n) { return k > kSlice ? align256(size_t(m) * size_t(n) * 4) : 0; }
@@ -255,7 +265,7 @@ int mx8_dequantize(const mo_tensor* q, int64_t rows, int64_t k, void* out, int32
   int* status = nullptr;
   if ((st = mo::current_device(&sms, &status)) != MO_OK) return st;
   Launches run;
-  run(mo::launch_unpack(from, rows, k, out, dtype == MO_BF16, k, stream));
+  run(mo::launch_unpack(from, rows, k, out, dtype == MO_BF16, stream));
   return run.status();
 }
 
@@ -392,8 +402,10 @@ int linear_forward(const mo_tensor* x, const void* w, int64_t tokens, int64_t co
   Workspace space{static_cast<uint8_t*>(ws)};
   Launches run;
   q.act = act;
-  q.a[0] = operand(xk, tokens, cols, space, run, stream);
-  q.b[0] = operand(w, rows, cols, space, run, stream);
+  Operands operand{space};
+  q.a[0] = operand(xk, tokens, cols);
+  q.b[0] = operand(w, rows, cols);
+  operand.lay_out(run, stream);
   q.t[0] = target(out, out_dtype, tokens, rows, residual);
   q.k = cols;
   q.bias = bias;
@@ -461,8 +473,10 @@ int linear_grad(const void* dout, const mo_tensor* x, const void* w, int64_t tok
   if (dbias != nullptr) g.part = static_cast<float*>(space.take(size_t(parts) * size_t(rows) * 4));
   if (g.dz != nullptr || g.part != nullptr) run(mo::launch_act_grad(g, stream));
   if (dbias != nullptr && run.error == cudaSuccess) run(mo::launch_join(g.part, parts, rows, dbias, accumulate != 0, stream));
-  const Operand xo = dw != nullptr ? operand(xk, tokens, cols, space, run, stream) : Operand{};
-  const Operand wo = dx != nullptr ? operand(w, rows, cols, space, run, stream) : Operand{};
+  Operands operand{space};
+  const Operand xo = dw != nullptr ? operand(xk, tokens, cols) : Operand{};
+  const Operand wo = dx != nullptr ? operand(w, rows, cols) : Operand{};
+  operand.lay_out(run, stream);
   float* part = reinterpret_cast<float*>(space.take(0));
   if (dx != nullptr) {
     mo::Product q;
@@ -530,15 +544,18 @@ int gated_ffn_forward(const mo_tensor* x, const void* w_gate, const void* w_up, 
   void* h = space.take(size_t(tokens) * size_t(ld) * 2);
   q.epi = mo::kEpiGated;
   q.act = act;
-  q.a[0] = operand(xk, tokens, dim, space, run, stream);
-  q.b[0] = operand(w_gate, inner, dim, space, run, stream);
-  q.b[1] = operand(w_up, inner, dim, space, run, stream);
+  Operands operand{space};
+  q.a[0] = operand(xk, tokens, dim);
+  q.b[0] = operand(w_gate, inner, dim);
+  q.b[1] = operand(w_up, inner, dim);
+  operand.lay_out(run, stream);
   q.t[0] = {h, nullptr, tokens, inner, ld, 0, 1, 0};
   q.k = dim;
   if (run.error == cudaSuccess) run(mo::launch_product(q, sms, status, stream));
   mo::Product down;
   down.a[0] = {h, tokens, inner, ld};
-  down.b[0] = operand(w_down, dim, inner, space, run, stream);
+  down.b[0] = operand(w_down, dim, inner);
+  operand.lay_out(run, stream);
   down.early = !needs_copy(inner, MO_BF16) && mo::is_narrow(q, sms);
   down.t[0] = target(out, out_dtype, tokens, dim, residual);
   down.k = inner;
@@ -603,12 +620,14 @@ int gated_ffn_grad(const void* dout, const mo_tensor* x, const mo_tensor* gate, 
   const int64_t ld = padded(inner);
   uint16_t* kept[3];   // dg, du, h
   for (uint16_t*& p : kept) p = static_cast<uint16_t*>(space.take(size_t(tokens) * size_t(ld) * 2));
-  const Operand d = operand(dout, tokens, dim, space, run, stream);
+  Operands operand{space};
+  const Operand d = operand(dout, tokens, dim);
   q.epi = mo::kEpiGatedGrad;
   q.act = act;
   q.b_mn = true;
   q.a[0] = d;
-  q.b[0] = operand(w_down, dim, inner, space, run, stream);
+  q.b[0] = operand(w_down, dim, inner);
+  operand.lay_out(run, stream);
   q.t[0] = {kept[0], nullptr, tokens, inner, ld, 0, 1, 0};
   q.out2 = kept[1];
   q.out3 = kept[2];
@@ -621,14 +640,16 @@ int gated_ffn_grad(const void* dout, const mo_tensor* x, const mo_tensor* gate, 
     const void* w[2] = {w_gate, w_up};
     for (int i = 0; i < 2; ++i) {
       s.a[i] = {kept[i], tokens, inner, ld};
-      s.b[i] = operand(w[i], inner, dim, space, run, stream);
+      s.b[i] = operand(w[i], inner, dim);
     }
+    operand.lay_out(run, stream);
     s.t[0] = target(dx, dx_dtype, tokens, dim);
     s.k = inner;
     if (run.error == cudaSuccess) run(mo::launch_product(s, sms, status, stream));
   }
   if (any_dw) {   // up to three products over the tokens, one launch
-    const Operand xo = need_x ? operand(xk, tokens, dim, space, run, stream) : Operand{};
+    const Operand xo = need_x ? operand(xk, tokens, dim) : Operand{};
+    operand.lay_out(run, stream);
     mo::Product s;
     s.a_mn = s.b_mn = true;
     s.count = 0;

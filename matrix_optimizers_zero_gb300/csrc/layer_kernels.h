@@ -28,8 +28,18 @@ inline int64_t padded(int64_t cols) { return (cols + 63) / 64 * 64; }
 // ---------------------------------------------------------------- 8-bit tensors
 // q = x in 8 bits.
 cudaError_t launch_mx8_quantize(const void* x, bool bf16, int64_t rows, int64_t k, const Kept& q, cudaStream_t stream);
-// out [rows, ld] (ld >= k) = the values of src: 8 bits, or bf16 in dense rows.
-cudaError_t launch_unpack(const Kept& src, int64_t rows, int64_t k, void* out, bool out_bf16, int64_t ld, cudaStream_t stream);
+// out [rows, k] = the values of the 8-bit src.
+cudaError_t launch_unpack(const Kept& src, int64_t rows, int64_t k, void* out, bool out_bf16, cudaStream_t stream);
+
+// Operands of products, 8 bits or bf16 [rows, cols], as bf16 in rows of `ld`
+// elements (a multiple of 8): up to three in one launch.
+struct LayOut {
+  Kept src;
+  int64_t rows, cols;
+  uint16_t* out;
+  int64_t ld;
+};
+cudaError_t launch_lay_out(const LayOut* t, int count, cudaStream_t stream);
 
 // dz [tokens, ld] = dout act'(pre), and part [parts, rows] its column sums over
 // `per` tokens each. dz null: no output; act 0: dz is dout.

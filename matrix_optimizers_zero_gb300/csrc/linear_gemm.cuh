@@ -31,7 +31,7 @@ struct GemmParams {
   int32_t tiles;                 // of all targets; pairs: with the cut ones counted as their parts
   int32_t whole;                 // pairs: tiles that are not cut, in front of the others
   int32_t cut;                   // pairs: parts of the others, side by side: 1, 2 or 4
-  int32_t stages;                // pairs: of shared memory
+  int32_t stages;                // of shared memory
   int32_t early;                 // narrow: the columns' operand may be read before the previous launch has ended
   int32_t act;
   const float* bias;

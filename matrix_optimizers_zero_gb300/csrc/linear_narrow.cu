@@ -9,6 +9,8 @@
 // all SMs have loads under way.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "launch.cuh"
 #include "linear_gemm.cuh"
 
@@ -24,16 +26,21 @@ template <Epilogue EPI>
 constexpr int kPanels = EPI == kEpiGated ? 2 : 1;   // gate and up
 template <Epilogue EPI, int NT>
 constexpr uint32_t kStage = kPanels<EPI> * kPanel + NT * kBlockK * 2;
-// Two CTAs an SM where the sums and enough stages fit; with gate and up one and
-// all its memory (one token of the 8B block: 63 -> 60 us).
+// Stages (p.stages): two CTAs an SM where the sums and enough of them fit; with gate
+// and up one CTA and all its memory (one token of the 8B block: 63 -> 60 us). Where
+// there are no more CTAs than SMs, each takes all memory too (100 x 14336 -> 4096: 30
+// -> 26 us).
+constexpr size_t kCtrl = 256;
 template <Epilogue EPI, int NT>
-constexpr int kStages = EPI == kEpiGated ? (NT == 16 ? 6 : NT == 64 ? 5 : 4) : (NT == 16 ? 6 : NT == 64 ? 4 : 3);
+constexpr int kDeep = std::min(12, int((227 * 1024 - 1024 - kCtrl) / kStage<EPI, NT>));
 template <Epilogue EPI, int NT>
-constexpr size_t kSmem = 1024 + size_t(kStages<EPI, NT>) * kStage<EPI, NT> + 160;
+constexpr int kStages = EPI == kEpiGated ? kDeep<EPI, NT> : (NT == 16 ? 6 : NT == 64 ? 4 : 3);
+template <Epilogue EPI, int NT>
+constexpr size_t smem_of(int stages) { return 1024 + size_t(stages) * kStage<EPI, NT> + kCtrl; }
 template <Epilogue EPI, int NT>
 constexpr uint32_t kCols = kPanels<EPI> * NT < 32 ? 32 : kPanels<EPI> * NT;   // of TMEM
 template <Epilogue EPI, int NT>
-constexpr bool kFits = kStages<EPI, NT> * kStage<EPI, NT> >= kPanels<EPI> * NT * kPitch * 4 && kSmem<EPI, NT> <= 227 * 1024;
+constexpr bool kFits = kStages<EPI, NT> * kStage<EPI, NT> >= kPanels<EPI> * NT * kPitch * 4 && smem_of<EPI, NT>(kDeep<EPI, NT>) <= 227 * 1024;
 static_assert(kFits<kEpiLinear, 16> && kFits<kEpiLinear, 64> && kFits<kEpiLinear, 128> && kFits<kEpiGated, 16> &&
                   kFits<kEpiGated, 64> && kFits<kEpiGated, 128>,
               "sums in the stages' memory");
@@ -141,21 +148,21 @@ __global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_co
   static_assert(!Q_MN || NT == 128, "whole boxes");
   extern __shared__ uint8_t smem_raw[];
   constexpr uint32_t kStg = kStage<EPI, NT>;
-  constexpr int kStgs = kStages<EPI, NT>;
+  const int stages = p.stages;
   constexpr uint32_t kQ = kPanels<EPI> * kPanel;   // of the rows' operand in a stage
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  const uint32_t bars = base + uint32_t(kStgs) * kStg;
-  constexpr uint32_t kBars = 2 * kStgs + 2;
-  static_assert(8 * kBars + 8 <= 160, "control block");
+  const uint32_t bars = base + uint32_t(stages) * kStg;
+  constexpr uint32_t kBars = 2 * kDeep<EPI, NT> + 2;
+  static_assert(8 * kBars + 8 <= kCtrl, "control block");
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kBars);
   uint32_t* tmem_slot = ctrl;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 1);
   float* sums = reinterpret_cast<float*>(smem_raw + (base - raw));
   auto full_bar = [&](int s) { return bars + 8u * uint32_t(s); };
-  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(kStgs + s); };
-  const uint32_t done_bar = bars + 8u * uint32_t(2 * kStgs);
-  const uint32_t drain_bar = bars + 8u * uint32_t(2 * kStgs + 1);
+  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(stages + s); };
+  const uint32_t done_bar = bars + 8u * uint32_t(2 * stages);
+  const uint32_t drain_bar = bars + 8u * uint32_t(2 * stages + 1);
 
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
   const uint32_t parts = gridDim.x / uint32_t(p.tiles);   // CTAs of a cluster
@@ -168,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_co
   const int32_t k0 = int32_t(blocks * rank / parts), k1 = int32_t(blocks * (rank + 1) / parts);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStgs; ++s) {
+    for (int s = 0; s < stages; ++s) {
       ptx::mbar_init(full_bar(s), 1);
       ptx::mbar_init(empty_bar(s), 1);
     }
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_co
   };
   int32_t ahead = k0;   // stages whose columns' operand is under way already
   if (p.early && warp == 0 && lane == 0)
-    for (; ahead < min(k1, k0 + kStgs); ++ahead) {
+    for (; ahead < min(k1, k0 + stages); ++ahead) {
       const uint32_t fb = full_bar(ahead - k0);
       ptx::mbar_arrive_expect_tx(fb, kStg);
       load_p(ahead, fb, base + uint32_t(ahead - k0) * kStg);
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_co
           ptx::tma_load_2d(sq, &p.a[op], fb, at, tm * NT);
         }
         ++n_issued;
-        if (++stage == kStgs) {
+        if (++stage == stages) {
           stage = 0;
           ph ^= 1u;
         }
@@ -271,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_co
         }
         ptx::umma_commit_one(empty_bar(stage));
         mma_issued = true;
-        if (++stage == kStgs) {
+        if (++stage == stages) {
           stage = 0;
           ph ^= 1u;
         }
@@ -309,8 +316,8 @@ __global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_co
       mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
     }
     if (threadIdx.x == 0)
-      for (uint32_t j = n_issued > uint32_t(kStgs) ? n_issued - uint32_t(kStgs) : 0u; j < n_issued; ++j)
-        mbar_wait_drain(full_bar(int(j % uint32_t(kStgs))), (j / uint32_t(kStgs)) & 1u, p.timeout_ns);
+      for (uint32_t n = uint32_t(stages), j = n_issued > n ? n_issued - n : 0u; j < n_issued; ++j)
+        mbar_wait_drain(full_bar(int(j % n)), (j / n) & 1u, p.timeout_ns);
     __syncthreads();
   }
   if (parts > 1) ptx::cluster_sync();   // every part's sums are in place
@@ -363,14 +370,15 @@ cudaError_t narrow_as(const Product& q, GemmParams& p, int sms, cudaStream_t str
   p.tiles = int32_t(tiles);
   // The reduction in as many parts as leave all clusters resident (clusters of 4 and 8 do not fill the
   // GPU's parts evenly: 72 of 76 and 30 of 38 fit on 152 SMs, two CTAs an SM) and four stages a CTA.
-  const int64_t per_sm = kSmem<EPI, NT> <= 113 * 1024 ? 2 : 1;
+  const int64_t per_sm = smem_of<EPI, NT>(kStages<EPI, NT>) <= 113 * 1024 ? 2 : 1;
   const int64_t most[4] = {0, sms * per_sm / 2, sms * per_sm * 45 / 200, sms * per_sm * 18 / 200};
   unsigned parts = 1;
   for (int i = 1; i < 4 && tiles <= most[i] && p.blocks * q.segments >= (4 << i); ++i) parts = 1u << i;
+  p.stages = tiles * parts <= sms ? kDeep<EPI, NT> : kStages<EPI, NT>;
   auto kern = linear_narrow_kernel<EPI, Q_MN, P_MN, NT>;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem<EPI, NT>);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem_of<EPI, NT>(kDeep<EPI, NT>));
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(unsigned(tiles * parts)), dim3(kThreads), kSmem<EPI, NT>, parts, true, stream, p);
+  return launch_kernel(kern, dim3(unsigned(tiles * parts)), dim3(kThreads), smem_of<EPI, NT>(p.stages), parts, true, stream, p);
 }
 
 template <Epilogue EPI, bool P_MN>

@@ -133,18 +133,14 @@ __global__ void __launch_bounds__(kThreads) unpack_flat_kernel(const uint8_t* __
 // elements a thread where the output's rows are 16-byte aligned. Elements past
 // k are not written.
 template <bool MX8, typename O>
-__global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restrict__ src, const uint8_t* __restrict__ scales,
-                                                          int64_t groups, int64_t k, uint32_t per_row, O* __restrict__ out, int64_t ld) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int64_t g = global_thread();
-  if (g >= groups) return;
+__device__ __forceinline__ void unpack_group(const void* src, const uint8_t* scales, int64_t g, int64_t k, uint32_t per_row, O* out,
+                                             int64_t ld) {
   int64_t row, col;
   place(g, per_row, row, col);
   float v[8];
   if constexpr (MX8) {
     const uint32_t nb = uint32_t((k + 31) / 32);
-    const uint2 w = *reinterpret_cast<const uint2*>(src + (row * nb * 32 + col));
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(src) + (row * nb * 32 + col));
     const float up = mx8_up(scales[row * nb + (col >> 5)]);
     float a[4], b[4];
     e4m3x4_values(w.x, a);
@@ -155,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restr
       v[4 + i] = b[i] * up;
     }
   } else {
-    const uint16_t* s = reinterpret_cast<const uint16_t*>(src) + row * k + col;
+    const uint16_t* s = static_cast<const uint16_t*>(src) + row * k + col;
     const int n = int(min(int64_t(8), k - col));
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < n ? load1(s + i) : 0.0f;
@@ -168,6 +164,34 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restr
     for (int i = 0; i < 8; ++i)
       if (col + i < k) store1(o + i, v[i]);
   }
+}
+
+template <typename O>
+__global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                          int64_t groups, int64_t k, uint32_t per_row, O* __restrict__ out, int64_t ld) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t g = global_thread();
+  if (g < groups) unpack_group<true>(codes, scales, g, k, per_row, out, ld);
+}
+
+// Up to three operands of products, one behind the other.
+struct LayOutParams {
+  LayOut t[3];
+  int64_t first[3];   // block
+};
+__global__ void __launch_bounds__(kThreads) lay_out_kernel(const LayOutParams p) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int i = int64_t(blockIdx.x) >= p.first[2] ? 2 : int64_t(blockIdx.x) >= p.first[1] ? 1 : 0;
+  const LayOut& t = p.t[i];
+  const int64_t g = (int64_t(blockIdx.x) - p.first[i]) * kThreads + threadIdx.x;
+  const uint32_t per_row = uint32_t((t.cols + 7) / 8);
+  if (g >= t.rows * per_row) return;
+  if (t.src.dtype == MO_MX8)
+    unpack_group<true>(t.src.data, t.src.scales, g, t.cols, per_row, t.out, t.ld);
+  else
+    unpack_group<false>(t.src.data, nullptr, g, t.cols, per_row, t.out, t.ld);
 }
 
 // 8-bit codes into rows that are not 16-byte aligned: a lane an element.
@@ -352,18 +376,15 @@ cudaError_t quantize_as(const T* x, int64_t rows, int64_t k, const Kept& q, cuda
 }
 
 template <typename O>
-cudaError_t unpack_as(const Kept& src, int64_t rows, int64_t k, O* out, int64_t ld, cudaStream_t stream) {
+cudaError_t unpack_as(const Kept& src, int64_t rows, int64_t k, O* out, cudaStream_t stream) {
   const uint8_t* s = static_cast<const uint8_t*>(src.data);
   const uint8_t* scales = src.scales;
-  if (src.dtype == MO_MX8 && ld == k && k % 32 == 0)
+  if (k % 32 == 0)
     return launch_kernel(unpack_flat_kernel<O>, dim3(quant_blocks(rows * k / 8)), dim3(kThreads), 0, 1, true, stream, s, scales,
                          rows * k / 8, out);
-  if (ld % 8 == 0) {
-    const int64_t per_row = (k + 7) / 8, groups = rows * per_row;
-    auto kern = src.dtype == MO_MX8 ? unpack_kernel<true, O> : unpack_kernel<false, O>;
-    return launch_kernel(kern, dim3(blocks_of(groups)), dim3(kThreads), 0, 1, true, stream, s, scales, groups, k, uint32_t(per_row), out,
-                         ld);
-  }
+  if (k % 8 == 0)
+    return launch_kernel(unpack_kernel<O>, dim3(blocks_of(rows * k / 8)), dim3(kThreads), 0, 1, true, stream, s, scales, rows * k / 8, k,
+                         uint32_t(k / 8), out, k);
   const int64_t nb = mx8_blocks(k);
   return launch_kernel(unpack_odd_kernel<O>, dim3(blocks_of(rows * nb * 32)), dim3(kThreads), 0, 1, true, stream, s, scales, rows * nb, k,
                        uint32_t(nb), out);
@@ -376,9 +397,22 @@ cudaError_t launch_mx8_quantize(const void* x, bool bf16, int64_t rows, int64_t 
               : quantize_as(static_cast<const float*>(x), rows, k, q, stream);
 }
 
-cudaError_t launch_unpack(const Kept& src, int64_t rows, int64_t k, void* out, bool out_bf16, int64_t ld, cudaStream_t stream) {
-  return out_bf16 ? unpack_as(src, rows, k, static_cast<uint16_t*>(out), ld, stream)
-                  : unpack_as(src, rows, k, static_cast<float*>(out), ld, stream);
+cudaError_t launch_unpack(const Kept& src, int64_t rows, int64_t k, void* out, bool out_bf16, cudaStream_t stream) {
+  return out_bf16 ? unpack_as(src, rows, k, static_cast<uint16_t*>(out), stream)
+                  : unpack_as(src, rows, k, static_cast<float*>(out), stream);
+}
+
+cudaError_t launch_lay_out(const LayOut* t, int count, cudaStream_t stream) {
+  if (count == 1 && t[0].src.dtype == MO_MX8 && t[0].ld == t[0].cols) return unpack_as(t[0].src, t[0].rows, t[0].cols, t[0].out, stream);
+  LayOutParams p = {};
+  int64_t blocks = 0;
+  for (int i = 0; i < 3; ++i) {
+    p.first[i] = i < count ? blocks : int64_t(1) << 62;
+    if (i >= count) continue;
+    p.t[i] = t[i];
+    blocks += blocks_of(t[i].rows * ((t[i].cols + 7) / 8));
+  }
+  return launch_kernel(lay_out_kernel, dim3(unsigned(blocks)), dim3(kThreads), 0, 1, true, stream, p);
 }
 
 cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream) {

@@ -31,7 +31,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _check, load_library
-from .train_ops import MO_BF16, MO_F32, _dense, _dtype, _stream_ptr
+from .train_ops import MO_BF16, MO_F32, _dense, _stream_ptr
 
 MO_MX8 = 2
 ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # mo_activation
@@ -72,90 +72,122 @@ class Mx8Tensor:
         if self.codes.get_device() != self.scales.get_device():
             raise ValueError("codes and scales must be on one device")
         self.rows, self.k = rows, k
+        self.device_index = self.codes.get_device()
         self.arg = MoTensor(self.codes.data_ptr(), self.scales.data_ptr(), MO_MX8)
 
     def numel(self) -> int:
         return self.rows * self.k
 
     def get_device(self) -> int:
-        return self.codes.get_device()
+        return self.device_index
 
 
-def _here(*tensors) -> None:
-    """All on the current device, which the library launches on."""
-    import torch
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError("tensors must be on the current device")
+# A call of one token takes a few microseconds on the GPU, and as many here: each
+# tensor is asked once for what is checked of it.
+
+_dtypes = None          # {torch dtype: mo_dtype}, from the first call on
+_current_device = None
+
+
+def _here() -> int:
+    """The current device, which the library launches on and all tensors must be on."""
+    global _dtypes, _current_device
+    if _dtypes is None:
+        import torch
+        _dtypes = {torch.float32: MO_F32, torch.bfloat16: MO_BF16}
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
+
+
+def _refuse(t, name: str, here: int, types: str):
+    if t.dtype not in _dtypes:
+        raise TypeError(f"{name} must be {types}")
+    if t.get_device() < 0 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    raise ValueError(f"{name} must be on the current device ({here})")
+
+
+def _plain(t, name: str, here: int):
+    """(pointer, type) of an fp32 or bf16 tensor."""
+    code = _dtypes.get(t.dtype)
+    if code is None or t.get_device() != here or not t.is_contiguous():
+        _refuse(t, name, here, "fp32 or bf16")
+    return t.data_ptr(), code
+
+
+def _typed(t, name: str, here: int, code: int, numel: int):
+    """Pointer of a tensor that must have a type and a size; None for none."""
+    if t is None:
+        return None
+    if _dtypes.get(t.dtype) != code:
+        raise TypeError(f"{name} must be {'bf16' if code == MO_BF16 else 'fp32'}")
+    if t.get_device() != here or not t.is_contiguous():
+        _refuse(t, name, here, "")
+    if t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements")
+    return t.data_ptr()
+
+
+def _matrix(t, shape, name: str, here: int):
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return _typed(t, name, here, MO_BF16, shape[0] * shape[1])
 
 
 def _rows(t, width: int, name: str) -> int:
     """Rows of a tensor whose rows have `width` elements."""
-    if (t.k if isinstance(t, Mx8Tensor) else t.shape[-1] if t.dim() else 0) != width:
-        raise ValueError(f"rows of {name} must have {width} elements")
-    return t.rows if isinstance(t, Mx8Tensor) else t.numel() // width
+    if isinstance(t, Mx8Tensor):
+        if t.k == width:
+            return t.rows
+    else:
+        shape = t.shape
+        if len(shape) and shape[-1] == width:
+            return shape[0] if len(shape) == 2 else t.numel() // width
+    raise ValueError(f"rows of {name} must have {width} elements")
 
 
-def _kept(t, name: str, f32: bool = False):
+def _kept(t, name: str, here: int, f32: bool = False):
     """mo_tensor of a plain or an 8-bit tensor."""
     if isinstance(t, Mx8Tensor):
+        if t.get_device() != here:
+            raise ValueError(f"{name} must be on the current device ({here})")
         return t.arg
-    code = _dtype(t, name)
+    ptr, code = _plain(t, name, here)
     if code == MO_F32 and not f32:
         raise TypeError(f"{name} must be bf16 or an Mx8Tensor")
-    return MoTensor(t.data_ptr(), None, code)
+    return MoTensor(ptr, None, code)
 
 
-def _matrix(t, rows: int, cols: int, name: str):
-    import torch
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bf16")
-    _dense(t, name)
-    if tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}]")
-    return t.data_ptr()
+def _kept_rows(t, width: int, rows: int, name: str, here: int, f32: bool = False):
+    """The same, of a tensor with so many rows."""
+    if _rows(t, width, name) != rows:
+        raise ValueError(f"{name} must have {rows} rows")
+    return _kept(t, name, here, f32)
 
 
-def _vector(t, n: int, name: str):
-    import torch
-    if t is None:
-        return None
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be fp32")
-    _dense(t, name)
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements")
-    return t.data_ptr()
-
-
-def _same(t, like, code: int, name: str):
-    if t is None:
-        return None
-    if _dtype(t, name) != code or t.numel() != like.numel():
-        raise ValueError(f"{name} must have the type and size of the tensor it goes with")
-    return t.data_ptr()
-
-
-def _result(t, rows: int, cols: int, name: str):
-    """Pointer and type of an output of rows * cols elements; (None, bf16) for none."""
+def _result(t, numel: int, name: str, here: int):
+    """Pointer and type of an output; (None, bf16) for none."""
     if t is None:
         return None, MO_BF16
-    code = _dtype(t, name)
-    if t.numel() != rows * cols:
-        raise ValueError(f"{name} must have {rows} x {cols} elements")
-    return t.data_ptr(), code
+    got = _plain(t, name, here)
+    if t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements")
+    return got
 
 
-def _scratch(t):
-    _dense(t, "workspace")
+def _scratch(t, name: str, here: int):
+    if t is None:
+        raise ValueError(f"a workspace is needed ({name})")
+    if t.get_device() != here or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _act(name):
-    if name not in ACTIVATIONS:
+    code = ACTIVATIONS.get(name)
+    if code is None:
         raise ValueError(f"activation must be one of {', '.join(str(k) for k in ACTIVATIONS)}")
-    return ACTIVATIONS[name]
+    return code
 
 
 def _ref(struct):
@@ -173,18 +205,20 @@ def _workspace(nbytes: int, device):
 
 def mx8_quantize(x, q: Mx8Tensor, stream=None) -> None:
     """q = x [rows, k], fp32 or bf16, in 8 bits."""
-    code = _dtype(x, "x")
+    here = _here()
+    arg = _kept(q, "q", here)
+    ptr, code = _plain(x, "x", here)
     if _rows(x, q.k, "x") != q.rows:
         raise ValueError("x and q must have equal sizes")
-    _here(x, q)
-    _check(load_library().mx8_quantize(x.data_ptr(), code, q.rows, q.k, ctypes.byref(q.arg), _stream_ptr(stream, x)), "mx8_quantize")
+    _check(load_library().mx8_quantize(ptr, code, q.rows, q.k, ctypes.byref(arg), _stream_ptr(stream, x)), "mx8_quantize")
 
 
 def mx8_dequantize(q: Mx8Tensor, out, stream=None) -> None:
     """out [rows, k], fp32 or bf16, = the values q stands for."""
-    ptr, code = _result(out, q.rows, q.k, "out")
-    _here(q, out)
-    _check(load_library().mx8_dequantize(ctypes.byref(q.arg), q.rows, q.k, ptr, code, _stream_ptr(stream, out)), "mx8_dequantize")
+    here = _here()
+    arg = _kept(q, "q", here)
+    ptr, code = _result(out, q.rows * q.k, "out", here)
+    _check(load_library().mx8_dequantize(ctypes.byref(arg), q.rows, q.k, ptr, code, _stream_ptr(stream, out)), "mx8_dequantize")
 
 
 # ---------------------------------------------------------------- norm
@@ -193,20 +227,24 @@ def rms_norm(x, out=None, weight=None, eps: float = 1e-6, residual=None, sum_out
     """y = s / sqrt(mean(s^2) + eps) * weight over the rows (the last dimension)
     of s = x + residual, into out (fp32 or bf16), out8 (an Mx8Tensor), or both;
     s into sum_out. sum_out and out may each be x or residual."""
-    code = _dtype(x, "x")
-    dim = x.shape[-1] if x.dim() else 0
+    here = _here()
+    ptr, code = _plain(x, "x", here)
+    shape, numel = x.shape, x.numel()
+    dim = shape[-1] if len(shape) else 0
     if dim == 0:
         raise ValueError("rows of x must have elements")
-    rows = x.numel() // dim
+    rows = numel // dim
     if out is None and out8 is None:
         raise ValueError("out or out8 must be given")
-    ptr, out_code = _result(out, rows, dim, "out")
-    if out8 is not None and (not isinstance(out8, Mx8Tensor) or (out8.rows, out8.k) != (rows, dim)):
-        raise ValueError(f"out8 must be an Mx8Tensor of [{rows}, {dim}]")
-    _here(x, out, weight, residual, sum_out, out8)
-    st = load_library().rms_norm(x.data_ptr(), _same(residual, x, code, "residual"), code, rows, dim, _vector(weight, dim, "weight"),
-                                 eps, _same(sum_out, x, code, "sum_out"), ptr, out_code,
-                                 None if out8 is None else ctypes.byref(out8.arg), _stream_ptr(stream, x))
+    out_ptr, out_code = _result(out, numel, "out", here)
+    arg8 = None
+    if out8 is not None:
+        if not isinstance(out8, Mx8Tensor) or (out8.rows, out8.k) != (rows, dim):
+            raise ValueError(f"out8 must be an Mx8Tensor of [{rows}, {dim}]")
+        arg8 = ctypes.byref(_kept(out8, "out8", here))
+    st = load_library().rms_norm(ptr, _typed(residual, "residual", here, code, numel), code, rows, dim,
+                                 _typed(weight, "weight", here, MO_F32, dim), eps, _typed(sum_out, "sum_out", here, code, numel), out_ptr,
+                                 out_code, arg8, _stream_ptr(stream, x))
     _check(st, "rms_norm")
 
 
@@ -224,23 +262,20 @@ def rms_norm_grad(dy, x, dx, weight=None, eps: float = 1e-6, dresidual=None, dwe
     """Gradients of rms_norm from dy and s, the rows it normalised (x: of dy's
     type, or an Mx8Tensor): dx (+ dresidual; it may be dy or dresidual) and the
     fp32 dweight, added to with accumulate, for which the workspace is needed."""
-    code = _dtype(dy, "dy")
-    dim = dy.shape[-1] if dy.dim() else 0
+    here = _here()
+    ptr, code = _plain(dy, "dy", here)
+    shape, numel = dy.shape, dy.numel()
+    dim = shape[-1] if len(shape) else 0
     if dim == 0:
         raise ValueError("rows of dy must have elements")
-    rows = dy.numel() // dim
-    if _rows(x, dim, "x") != rows:
-        raise ValueError("dy and x must have equal sizes")
-    arg = _kept(x, "x", f32=True)
+    rows = numel // dim
+    arg = _kept_rows(x, dim, rows, "x", here, f32=True)
     if arg.dtype not in (MO_MX8, code):
         raise TypeError("x must have the type of dy, or be an Mx8Tensor")
-    if dweight is not None and workspace is None:
-        raise ValueError("dweight needs a workspace (rms_norm_grad_workspace)")
-    ws, nbytes = _scratch(workspace) if workspace is not None else (None, 0)
-    _here(dy, x, dx, weight, dresidual, dweight, workspace)
-    st = load_library().rms_norm_grad(dy.data_ptr(), code, ctypes.byref(arg), rows, dim, _vector(weight, dim, "weight"), eps,
-                                      _same(dresidual, dy, code, "dresidual"), _same(dx, dy, code, "dx"),
-                                      _vector(dweight, dim, "dweight"), int(accumulate), ws, nbytes, _stream_ptr(stream, dy))
+    ws, nbytes = (None, 0) if dweight is None else _scratch(workspace, "rms_norm_grad_workspace", here)
+    st = load_library().rms_norm_grad(ptr, code, ctypes.byref(arg), rows, dim, _typed(weight, "weight", here, MO_F32, dim), eps,
+                                      _typed(dresidual, "dresidual", here, code, numel), _typed(dx, "dx", here, code, numel),
+                                      _typed(dweight, "dweight", here, MO_F32, dim), int(accumulate), ws, nbytes, _stream_ptr(stream, dy))
     _check(st, "rms_norm_grad")
 
 
@@ -260,23 +295,25 @@ def linear(x, w, out, bias=None, activation=None, residual=None, pre=None, works
     [tokens, cols], w bf16 [rows, cols], bias fp32, out (fp32 or bf16) and residual
     of one type (out may be residual). pre: bf16 or an Mx8Tensor [tokens, rows]
     that receives x w^T + bias for linear_grad."""
+    here = _here()
     act = _act(activation)
-    rows, cols = w.shape if w.dim() == 2 else (0, 0)
-    wp = _matrix(w, rows, cols, "w")
+    shape = w.shape
+    if len(shape) != 2:
+        raise ValueError("w must be [rows, cols]")
+    rows, cols = shape
+    wp = _matrix(w, shape, "w", here)
     tokens = _rows(x, cols, "x")
-    xk = _kept(x, "x")
-    ptr, code = _result(out, tokens, rows, "out")
-    pk = None if pre is None else _kept(pre, "pre")
-    if pre is not None and _rows(pre, rows, "pre") != tokens:
-        raise ValueError("pre must have a row for every token")
-    if pre is not None and not act:
-        raise ValueError("pre goes with an activation")
-    if workspace is None:
-        raise ValueError("a workspace is needed (linear_workspace)")
-    ws, nbytes = _scratch(workspace)
-    _here(x, w, out, bias, residual, pre, workspace)
-    st = load_library().linear_forward(ctypes.byref(xk), wp, tokens, cols, rows, _vector(bias, rows, "bias"), act,
-                                       _same(residual, out, code, "residual"), _ref(pk), ptr, code, ws, nbytes,
+    xk = _kept(x, "x", here)
+    numel = tokens * rows
+    ptr, code = _result(out, numel, "out", here)
+    pk = None
+    if pre is not None:
+        if not act:
+            raise ValueError("pre goes with an activation")
+        pk = ctypes.byref(_kept_rows(pre, rows, tokens, "pre", here))
+    ws, nbytes = _scratch(workspace, "linear_workspace", here)
+    st = load_library().linear_forward(ctypes.byref(xk), wp, tokens, cols, rows, _typed(bias, "bias", here, MO_F32, rows), act,
+                                       _typed(residual, "residual", here, code, numel), pk, ptr, code, ws, nbytes,
                                        _stream_ptr(stream, out))
     _check(st, "linear")
 
@@ -287,37 +324,30 @@ def linear_grad(dout, x, w, dx=None, dw=None, dbias=None, activation=None, pre=N
     bf16) and the fp32 dbias, whichever are given; dw and dbias are added to with
     accumulate. x may be None without dw, and an Mx8Tensor in place of the x that
     linear was given."""
+    here = _here()
     act = _act(activation)
-    rows, cols = w.shape if w.dim() == 2 else (0, 0)
-    wp = _matrix(w, rows, cols, "w")
+    shape = w.shape
+    if len(shape) != 2:
+        raise ValueError("w must be [rows, cols]")
+    rows, cols = shape
+    wp = _matrix(w, shape, "w", here)
     if dx is None and dw is None and dbias is None:
         raise ValueError("dx, dw or dbias must be given")
     tokens = _rows(dout, rows, "dout")
-    dk = _kept(dout, "dout")
-    if dk.dtype != MO_BF16:
-        raise TypeError("dout must be bf16")
-    if dw is not None and x is None:
-        raise ValueError("dw needs x")
+    dp = _typed(dout, "dout", here, MO_BF16, tokens * rows)
     xk = None
     if dw is not None:
-        if _rows(x, cols, "x") != tokens:
-            raise ValueError("dout and x must have a row for every token")
-        xk = _kept(x, "x")
+        if x is None:
+            raise ValueError("dw needs x")
+        xk = ctypes.byref(_kept_rows(x, cols, tokens, "x", here))
     if bool(act) != (pre is not None):
         raise ValueError("pre goes with an activation, and an activation with pre")
-    pk = None
-    if act:
-        if _rows(pre, rows, "pre") != tokens:
-            raise ValueError("pre must have a row for every token")
-        pk = _kept(pre, "pre")
-    dxp, dx_code = _result(dx, tokens, cols, "dx")
-    dwp, dw_code = _result(dw, rows, cols, "dw")
-    if workspace is None:
-        raise ValueError("a workspace is needed (linear_workspace)")
-    ws, nbytes = _scratch(workspace)
-    _here(dout, x if dw is not None else None, w, dx, dw, dbias, pre, workspace)
-    st = load_library().linear_grad(dk.data, _ref(xk), wp, tokens, cols, rows, act, _ref(pk), dxp, dx_code, dwp, dw_code,
-                                    _vector(dbias, rows, "dbias"), int(accumulate), ws, nbytes, _stream_ptr(stream, dout))
+    pk = ctypes.byref(_kept_rows(pre, rows, tokens, "pre", here)) if act else None
+    dxp, dx_code = _result(dx, tokens * cols, "dx", here)
+    dwp, dw_code = _result(dw, rows * cols, "dw", here)
+    ws, nbytes = _scratch(workspace, "linear_workspace", here)
+    st = load_library().linear_grad(dp, xk, wp, tokens, cols, rows, act, pk, dxp, dx_code, dwp, dw_code,
+                                    _typed(dbias, "dbias", here, MO_F32, rows), int(accumulate), ws, nbytes, _stream_ptr(stream, dout))
     _check(st, "linear_grad")
 
 
@@ -332,17 +362,19 @@ def gated_ffn_workspace(tokens: int, dim: int, inner: int, grad: bool = False, d
     return _workspace(mo_gated_ffn_workspace_bytes(tokens, dim, inner, grad), device)
 
 
-def _gated_weights(w_gate, w_up, w_down):
-    inner, dim = w_gate.shape if w_gate.dim() == 2 else (0, 0)
-    return dim, inner, (_matrix(w_gate, inner, dim, "w_gate"), _matrix(w_up, inner, dim, "w_up"), _matrix(w_down, dim, inner, "w_down"))
+def _gated_weights(w_gate, w_up, w_down, here: int):
+    shape = w_gate.shape
+    if len(shape) != 2:
+        raise ValueError("w_gate must be [inner, dim]")
+    inner, dim = shape
+    return dim, inner, (_matrix(w_gate, shape, "w_gate", here), _matrix(w_up, shape, "w_up", here),
+                        _matrix(w_down, (dim, inner), "w_down", here))
 
 
-def _gated_kept(gate, up, tokens: int, inner: int):
-    gk, uk = _kept(gate, "gate"), _kept(up, "up")
+def _gated_kept(gate, up, tokens: int, inner: int, here: int):
+    gk, uk = _kept_rows(gate, inner, tokens, "gate", here), _kept_rows(up, inner, tokens, "up", here)
     if gk.dtype != uk.dtype:
         raise TypeError("gate and up must be of one type")
-    if _rows(gate, inner, "gate") != tokens or _rows(up, inner, "up") != tokens:
-        raise ValueError("gate and up must have a row for every token")
     return gk, uk
 
 
@@ -352,20 +384,20 @@ def gated_ffn(x, w_gate, w_up, w_down, out, activation="silu", residual=None, ga
     Mx8Tensor [tokens, dim], bf16 weights [inner, dim] and [dim, inner], out (fp32
     or bf16) and residual of one type (out may be residual). gate and up: bf16 or
     Mx8Tensors [tokens, inner] that receive the two projections for gated_ffn_grad."""
+    here = _here()
     act = _act(activation)
-    dim, inner, w = _gated_weights(w_gate, w_up, w_down)
+    dim, inner, w = _gated_weights(w_gate, w_up, w_down, here)
     tokens = _rows(x, dim, "x")
-    xk = _kept(x, "x")
-    ptr, code = _result(out, tokens, dim, "out")
+    xk = _kept(x, "x", here)
+    numel = tokens * dim
+    ptr, code = _result(out, numel, "out", here)
     if (gate is None) != (up is None):
         raise ValueError("gate and up go together")
-    gk, uk = (None, None) if gate is None else _gated_kept(gate, up, tokens, inner)
-    if workspace is None:
-        raise ValueError("a workspace is needed (gated_ffn_workspace)")
-    ws, nbytes = _scratch(workspace)
-    _here(x, w_gate, w_up, w_down, out, residual, gate, up, workspace)
-    st = load_library().gated_ffn_forward(ctypes.byref(xk), *w, tokens, dim, inner, act, _same(residual, out, code, "residual"),
-                                          _ref(gk), _ref(uk), ptr, code, ws, nbytes, _stream_ptr(stream, out))
+    gk, uk = (None, None) if gate is None else _gated_kept(gate, up, tokens, inner, here)
+    ws, nbytes = _scratch(workspace, "gated_ffn_workspace", here)
+    st = load_library().gated_ffn_forward(ctypes.byref(xk), *w, tokens, dim, inner, act,
+                                          _typed(residual, "residual", here, code, numel), _ref(gk), _ref(uk), ptr, code, ws, nbytes,
+                                          _stream_ptr(stream, out))
     _check(st, "gated_ffn")
 
 
@@ -374,34 +406,26 @@ def gated_ffn_grad(dout, x, gate, up, w_gate, w_up, w_down, activation="silu", d
     """Gradients of gated_ffn from dout (bf16) and the kept gate and up: dx
     (fp32 or bf16) and those of the weights (of one type), whichever are given; the
     weights' are added to with accumulate. x may be None without dw_gate and dw_up."""
+    here = _here()
     act = _act(activation)
-    dim, inner, w = _gated_weights(w_gate, w_up, w_down)
+    dim, inner, w = _gated_weights(w_gate, w_up, w_down, here)
     tokens = _rows(dout, dim, "dout")
-    dk = _kept(dout, "dout")
-    if dk.dtype != MO_BF16:
-        raise TypeError("dout must be bf16")
-    grads = [_result(t, *s, n) for t, s, n in ((dw_gate, (inner, dim), "dw_gate"), (dw_up, (inner, dim), "dw_up"),
-                                               (dw_down, (dim, inner), "dw_down"))]
-    codes = {code for p, code in grads if p is not None}
+    dp = _typed(dout, "dout", here, MO_BF16, tokens * dim)
+    grads = [_result(t, inner * dim, n, here) for t, n in ((dw_gate, "dw_gate"), (dw_up, "dw_up"), (dw_down, "dw_down"))]
+    codes = {code for t, (_, code) in zip((dw_gate, dw_up, dw_down), grads) if t is not None}
     if len(codes) > 1:
         raise TypeError("the weights' gradients must be of one type")
     if dx is None and not codes:
         raise ValueError("dx or a weight's gradient must be given")
-    need_x = dw_gate is not None or dw_up is not None
-    if need_x and x is None:
-        raise ValueError("dw_gate and dw_up need x")
     xk = None
-    if need_x:
-        if _rows(x, dim, "x") != tokens:
-            raise ValueError("dout and x must have a row for every token")
-        xk = _kept(x, "x")
-    gk, uk = _gated_kept(gate, up, tokens, inner)
-    dxp, dx_code = _result(dx, tokens, dim, "dx")
-    if workspace is None:
-        raise ValueError("a workspace is needed (gated_ffn_workspace)")
-    ws, nbytes = _scratch(workspace)
-    _here(dout, x if need_x else None, gate, up, w_gate, w_up, w_down, dx, dw_gate, dw_up, dw_down, workspace)
-    st = load_library().gated_ffn_grad(dk.data, _ref(xk), ctypes.byref(gk), ctypes.byref(uk), *w, tokens, dim, inner, act, dxp,
-                                       dx_code, grads[0][0], grads[1][0], grads[2][0], codes.pop() if codes else MO_BF16,
-                                       int(accumulate), ws, nbytes, _stream_ptr(stream, dout))
+    if dw_gate is not None or dw_up is not None:
+        if x is None:
+            raise ValueError("dw_gate and dw_up need x")
+        xk = ctypes.byref(_kept_rows(x, dim, tokens, "x", here))
+    gk, uk = _gated_kept(gate, up, tokens, inner, here)
+    dxp, dx_code = _result(dx, tokens * dim, "dx", here)
+    ws, nbytes = _scratch(workspace, "gated_ffn_workspace", here)
+    st = load_library().gated_ffn_grad(dp, xk, ctypes.byref(gk), ctypes.byref(uk), *w, tokens, dim, inner, act, dxp, dx_code, grads[0][0],
+                                       grads[1][0], grads[2][0], codes.pop() if codes else MO_BF16, int(accumulate), ws, nbytes,
+                                       _stream_ptr(stream, dout))
     _check(st, "gated_ffn_grad")
