@@ -20,11 +20,13 @@ struct GemmTarget {
   int32_t tiles_m, tiles_n, tile0;
   int32_t align;                 // of the rows of out and add: 32, 16 or 0 (elements)
   int32_t out_bf16, add_bf16;
+  int32_t bulk;                  // pairs: out is stored by TMA
 };
 
 struct GemmParams {
   CUtensorMap a[3], b[3];
   CUtensorMap bs[3];             // pairs, K-major: b in boxes of 32 rows, for cut tiles
+  CUtensorMap so[3], sk[2];      // pairs: boxes of 32 rows of a chunk of the outputs, and of what is kept
   GemmTarget t[3];
   int32_t count, segments;
   int32_t blocks;                // stages a segment
@@ -37,6 +39,7 @@ struct GemmParams {
   const float* bias;
   Kept pre, pre2;
   int32_t pre_align;             // of bf16 rows, as above; of 8-bit codes 32 or 16
+  int32_t pre_bulk;              // pairs: they are stored by TMA
   uint16_t* out2;
   uint16_t* out3;
   int* status;
@@ -219,41 +222,63 @@ __device__ __forceinline__ void store_chunk(void* out, bool out_bf16, int64_t ld
   }
 }
 
-// Keeps a chunk, in 8 bits or in bf16.
-__device__ __forceinline__ void keep_chunk(const Kept& q, int align, int64_t row0, int64_t m, int64_t col, int64_t n,
-                                           const float (&v)[32], float* turn) {
-  if (q.dtype != MO_MX8) {
-    float x[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = v[i];
-    store_chunk(q.data, true, n, nullptr, false, 0, align, row0, m, col, n, x, turn);
-    return;
-  }
-  const int64_t row = row0 + int64_t(threadIdx.x & 31);
-  if (row >= m) return;
-  // (past n the sums are zeros, and so are the codes)
+// A chunk in 8 bits: codes and scale.
+__device__ __forceinline__ uint32_t mx8_chunk(const float (&v)[32], uint32_t (&w)[8]) {
   float top = fabsf(v[0]);
 #pragma unroll
   for (int i = 1; i < 31; i += 2) top = top3(top, v[i], v[i + 1]);
   top = top2(top, fabsf(v[31]));
   const uint32_t s = mx8_scale(top);
   const F2 down = ptx::f2(mx8_down(s));
-  uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 a = ptx::parts(ptx::mul2(ptx::f2(v[4 * i], v[4 * i + 1]), down));
     const float2 b = ptx::parts(ptx::mul2(ptx::f2(v[4 * i + 2], v[4 * i + 3]), down));
     w[i] = cvt_e4m3x4(a.x, a.y, b.x, b.y);
   }
-  const int64_t nb = (n + 31) / 32;
-  uint8_t* o = static_cast<uint8_t*>(q.data) + row * nb * 32 + col;
-  if (align == 32) {
-    ptx::st_global_v8(o, w);
-  } else {
-    reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  return s;
+}
+
+// A lane's row of a box of 32 rows, swizzled as the tensor map is: its 16-byte
+// pieces change places from row to row, so that the lanes meet all banks.
+template <int BYTES>
+__device__ __forceinline__ void put_row(uint32_t box, const uint32_t (&w)[BYTES / 4]) {
+  const uint32_t lane = threadIdx.x & 31u;
+  const uint32_t turn = BYTES == 64 ? (lane >> 1) & 3u : (lane >> 2) & 1u;
+#pragma unroll
+  for (uint32_t i = 0; i < BYTES / 16; ++i)
+    ptx::st_shared_v4(box + lane * BYTES + ((i ^ turn) * 16u), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+template <int N>
+__device__ __forceinline__ void put_bf16(uint32_t box, const float (&v)[N]) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  put_row<2 * N>(box, w);
+}
+
+// Keeps a chunk, in 8 bits or in bf16: into `box` for the copy that follows (bulk;
+// the scales go out at once), or as it is.
+__device__ __forceinline__ void keep_chunk(const Kept& q, bool bulk, int align, int64_t row0, int64_t m, int64_t col, int64_t n,
+                                           const float (&v)[32], uint32_t box, float* turn) {
+  if (q.dtype != MO_MX8) {
+    if (bulk) {
+      put_bf16(box, v);
+    } else {
+      float x[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = v[i];
+      store_chunk(q.data, true, n, nullptr, false, 0, align, row0, m, col, n, x, turn);
+      __syncwarp();
+    }
+    return;
   }
-  q.scales[row * nb + (col >> 5)] = uint8_t(s);
+  // (past n the sums are zeros, and so are the codes; their rows are 16-byte aligned, and always bulk)
+  uint32_t w[8];
+  const uint32_t s = mx8_chunk(v, w);
+  put_row<32>(box, w);
+  const int64_t row = row0 + int64_t(threadIdx.x & 31), nb = (n + 31) / 32;
+  if (row < m) q.scales[row * nb + (col >> 5)] = uint8_t(s);
 }
 
 // 16 kept columns' raw words, loaded ahead of their use: 8-bit codes in the first
@@ -301,13 +326,6 @@ __device__ __forceinline__ void kept_values(const Kept& q, const RawChunk& raw, 
       v[2 * j + 1] = __uint_as_float(raw.w[j] & 0xFFFF0000u);
     }
   }
-}
-// 16 bf16 in one 32-byte store
-__device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16]) {
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-  ptx::st_global_v8(p, w);
 }
 // One element of a kept tensor of rows of n.
 __device__ __forceinline__ float kept_at(const Kept& q, int64_t row, int64_t col, int64_t n) {

@@ -31,14 +31,17 @@ namespace {
 // Epilogue warps: two a quarter of the lanes, or four where the reduction is short
 // (see launch_pair).
 constexpr int kMostWarps = 16;
-constexpr int kStages = 6;      // five where the epilogue turns chunks in shared memory (p.stages)
 constexpr uint32_t kHalf = 128 * kBlockK * 2;   // 16 KB: 128 rows of an operand
 constexpr uint32_t kStage = 2 * kHalf;
-constexpr uint32_t kBars = 2 * kStages + 5;
+constexpr uint32_t kScratch = 4096;             // of an epilogue warp: what it stores by TMA, or turns
+template <int WARPS>
+constexpr int kStages = WARPS == kMostWarps ? 5 : 6;
+constexpr uint32_t kBars = 2 * 6 + 5;
 constexpr uint32_t kCtrl = 256;
-constexpr uint32_t kTurns = uint32_t(kMostWarps) * kTurn * 4;
-constexpr size_t kSmem = 1024 + kCtrl + std::max(size_t(kStages) * kStage, size_t(kStages - 1) * kStage + kTurns);
-static_assert(8 * kBars + 16 <= kCtrl && kSmem <= 227 * 1024, "shared memory");
+template <int WARPS>
+constexpr size_t kSmem = 1024 + size_t(kStages<WARPS>) * kStage + size_t(WARPS) * kScratch + kCtrl;
+static_assert(8 * kBars + 16 <= kCtrl && kSmem<8> <= 227 * 1024 && kSmem<kMostWarps> <= 227 * 1024 && kTurn * 4 <= kScratch,
+              "shared memory");
 
 // A chunk of 32 columns of an accumulator, a row a lane.
 __device__ __forceinline__ void tmem_chunk(uint32_t taddr, float (&v)[32]) {
@@ -53,11 +56,19 @@ __device__ __forceinline__ void tmem_chunk(uint32_t taddr, float (&v)[32]) {
 // The 32 rows from row0 on (lane l has row0 + l) of the `width` accumulator
 // columns from TMEM column `tb` on: chunks of 32 (or 16) columns, every PARTSth one
 // this warp's, from `part` on. col0: the first column of the output.
+//
+// What is written in bf16 or 8 bits goes through the warp's scratch and out by TMA
+// wherever its rows are 16-byte aligned: a store of a row a lane touches 32 lines an
+// instruction, and those are what the load-store unit counts.
 template <Epilogue EPI, int PARTS>
-__device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& t, int64_t row0, int64_t col0, int width, int part,
-                                         uint32_t tb, float* turn) {
+__device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& t, int q, int64_t row0, int64_t col0, int width, int part,
+                                         uint32_t tb, uint32_t scratch, float* turn) {
   const int lane = int(threadIdx.x & 31);
   const int64_t row = row0 + lane;
+  auto reuse = [&] {   // the scratch: its last copies have read it
+    if (lane == 0) ptx::bulk_wait_read();
+    __syncwarp();
+  };
   if constexpr (EPI == kEpiLinear) {
 #pragma unroll 1
     for (int c = part * 32; c < width; c += 32 * PARTS) {
@@ -65,6 +76,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       float v[32];
       tmem_chunk(tb + uint32_t(c), v);
       if (row0 >= t.m || col >= t.n) continue;
+      reuse();
       if (p.bias != nullptr) {
         if (col + 32 <= t.n) {
 #pragma unroll
@@ -80,10 +92,32 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
             if (col + i < t.n) v[i] += p.bias[col + i];
         }
       }
-      if (p.pre.data != nullptr) keep_chunk(p.pre, p.pre_align, row0, t.m, col, t.n, v, turn);
+      if (p.pre.data != nullptr) keep_chunk(p.pre, p.pre_bulk != 0, p.pre_align, row0, t.m, col, t.n, v, scratch + 2048, turn);
       if (p.act != MO_ACT_NONE)
         with_act(p.act, [&](auto act) { act_all<decltype(act)::value>(v); });
-      store_chunk(t.out, t.out_bf16 != 0, t.ld, t.add, t.add_bf16 != 0, t.add_ld, t.align, row0, t.m, col, t.n, v, turn);
+      if (t.bulk) {
+        if (t.add != nullptr && row < t.m) {   // (whole chunks)
+          float x[32];
+          if (t.add_bf16)
+            load32(static_cast<const uint16_t*>(t.add) + row * t.add_ld + col, t.align, x);
+          else
+            load32(static_cast<const float*>(t.add) + row * t.add_ld + col, t.align, x);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += x[i];
+        }
+        put_bf16(scratch, v);
+      }
+      ptx::fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (t.bulk) ptx::tma_store_2d(&p.so[q], scratch, int32_t(col), int32_t(row0));
+        if (p.pre_bulk) ptx::tma_store_2d(&p.sk[0], scratch + 2048, int32_t(col), int32_t(row0));
+        ptx::bulk_commit();
+      }
+      if (!t.bulk) {
+        reuse();   // (what is turned takes all of the scratch)
+        store_chunk(t.out, t.out_bf16 != 0, t.ld, t.add, t.add_bf16 != 0, t.add_ld, t.align, row0, t.m, col, t.n, v, turn);
+      }
     }
   } else if constexpr (EPI == kEpiGated) {
 #pragma unroll 1
@@ -93,17 +127,27 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       tmem_chunk(tb + uint32_t(c), g);
       tmem_chunk(tb + uint32_t(width / 2 + c), u);
       if (row0 >= t.m || col >= t.n) continue;
+      reuse();
       if (p.pre.data != nullptr) {
-        keep_chunk(p.pre, p.pre_align, row0, t.m, col, t.n, g, turn);
-        keep_chunk(p.pre2, p.pre_align, row0, t.m, col, t.n, u, turn);
+        keep_chunk(p.pre, p.pre_bulk != 0, p.pre_align, row0, t.m, col, t.n, g, scratch + 2048, turn);
+        keep_chunk(p.pre2, p.pre_bulk != 0, p.pre_align, row0, t.m, col, t.n, u, scratch + 3072, turn);
       }
       with_act(p.act, [&](auto act) { gate_all<decltype(act)::value>(g, u); });
-      // (a whole chunk: the rows of the workspace are padded)
-      if (row < t.m) store32(static_cast<uint16_t*>(t.out) + row * t.ld + col, 32, g);
+      put_bf16(scratch, g);
+      ptx::fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::tma_store_2d(&p.so[0], scratch, int32_t(col), int32_t(row0));
+        if (p.pre_bulk) {
+          ptx::tma_store_2d(&p.sk[0], scratch + 2048, int32_t(col), int32_t(row0));
+          ptx::tma_store_2d(&p.sk[1], scratch + 3072, int32_t(col), int32_t(row0));
+        }
+        ptx::bulk_commit();
+      }
     }
   } else {
     // The next chunk's g and u are loaded while one is worked on.
-    RawChunk rg, ru;
+    RawChunk rg = {}, ru = {};
     auto fetch = [&](int c) {
       const int64_t col = col0 + c;
       if (row < t.m && col < t.n) {
@@ -123,14 +167,21 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       __syncwarp();
       ptx::tmem_ld_32x32b_x16(tb + uint32_t(c), r);
       ptx::tmem_ld_wait();
-      if (row >= t.m || col >= t.n) continue;
+      if (row0 >= t.m || col >= t.n) continue;
+      reuse();
 #pragma unroll
       for (int i = 0; i < 16; ++i) dh[i] = __uint_as_float(r[i]);
       with_act(p.act, [&](auto act) { gate_grad_all<decltype(act)::value>(g, u, dh); });
-      const int64_t at = row * t.ld + col;
-      store16(static_cast<uint16_t*>(t.out) + at, g);
-      store16(p.out2 + at, dh);
-      store16(p.out3 + at, u);
+      put_bf16(scratch, g);
+      put_bf16(scratch + 1024, dh);
+      put_bf16(scratch + 2048, u);
+      ptx::fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) ptx::tma_store_2d(&p.so[i], scratch + uint32_t(i) * 1024u, int32_t(col), int32_t(row0));
+        ptx::bulk_commit();
+      }
     }
   }
 }
@@ -158,17 +209,18 @@ __global__ void __launch_bounds__(64 + 32 * WARPS, 1) linear_pair_kernel(const _
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  // stages (1024-byte aligned), or five of them and the chunks that are turned, then control
-  const uint32_t bars = base + uint32_t(kSmem - 1024 - kCtrl);
+  // stages (1024-byte aligned), the epilogue warps' scratch, control
+  constexpr int kStgs = kStages<WARPS>;
+  const uint32_t bars = base + uint32_t(kStgs) * kStage + uint32_t(WARPS) * kScratch;
   uint32_t* ctrl = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + 8 * kBars);
   uint32_t* tmem_slot = ctrl;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + 1);
   volatile uint32_t* peer_report = ctrl + 2;   // [0] the peer gave up, [1] stages its producer issued
   auto full_bar = [&](int s) { return bars + 8u * uint32_t(s); };
-  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(kStages + s); };
-  auto tfull_bar = [&](int s) { return bars + 8u * uint32_t(2 * kStages + s); };
-  auto tempty_bar = [&](int s) { return bars + 8u * uint32_t(2 * kStages + 2 + s); };
-  const uint32_t drain_bar = bars + 8u * uint32_t(2 * kStages + 4);
+  auto empty_bar = [&](int s) { return bars + 8u * uint32_t(kStgs + s); };
+  auto tfull_bar = [&](int s) { return bars + 8u * uint32_t(2 * kStgs + s); };
+  auto tempty_bar = [&](int s) { return bars + 8u * uint32_t(2 * kStgs + 2 + s); };
+  const uint32_t drain_bar = bars + 8u * uint32_t(2 * kStgs + 4);
 
   const int warp = int(threadIdx.x >> 5);
   const int lane = int(threadIdx.x & 31);
@@ -176,7 +228,7 @@ __global__ void __launch_bounds__(64 + 32 * WARPS, 1) linear_pair_kernel(const _
   const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kStgs; ++s) {
       ptx::mbar_init(full_bar(s), 1);
       ptx::mbar_init(empty_bar(s), 1);
     }
@@ -248,7 +300,7 @@ __global__ void __launch_bounds__(64 + 32 * WARPS, 1) linear_pair_kernel(const _
             for (int32_t j = 0; j < half; j += 32) ptx::tma_load_2d_pair(sb + uint32_t(j) * 128u, &p.bs[opb], fb, k0, rb + j);
           }
           ++n_issued;
-          if (++stage == p.stages) {
+          if (++stage == kStgs) {
             stage = 0;
             ph ^= 1u;
           }
@@ -285,7 +337,7 @@ __global__ void __launch_bounds__(64 + 32 * WARPS, 1) linear_pair_kernel(const _
                                    (kb | kk) != 0 ? 1u : 0u);
           ptx::umma_commit_pair(empty_bar(stage), 0x3);
           mma_issued = true;
-          if (++stage == p.stages) {
+          if (++stage == kStgs) {
             stage = 0;
             ph ^= 1u;
           }
@@ -298,8 +350,8 @@ __global__ void __launch_bounds__(64 + 32 * WARPS, 1) linear_pair_kernel(const _
     // -------------------------------------------------------------- epilogue (both CTAs)
     const int quarter = warp & 3;
     const int part = (warp - 2) >> 2;
-    // (the sixth stage's memory and what is behind it, where five are in use)
-    float* turn = reinterpret_cast<float*>(smem_raw + (base - raw) + (kStages - 1) * kStage) + (warp - 2) * kTurn;
+    const uint32_t scratch = base + uint32_t(kStgs) * kStage + uint32_t(warp - 2) * kScratch;
+    float* turn = reinterpret_cast<float*>(smem_raw + (scratch - raw));
     int32_t n = 0;
     for (int32_t i = first; i < p.tiles; i += step, ++n) {
       const int acc = n & 1;
@@ -310,13 +362,15 @@ __global__ void __launch_bounds__(64 + 32 * WARPS, 1) linear_pair_kernel(const _
       ptx::tc_fence_after();
       const int64_t row0 = int64_t(t.tm) * 256 + int64_t(rank) * 128 + quarter * 32;
       const int64_t col0 = EPI == kEpiGated ? int64_t(t.tn) * 128 + t.sub * (t.width / 2) : int64_t(t.tn) * 256 + t.sub * t.width;
-      epilogue<EPI, WARPS / 4>(p, p.t[t.q], row0, col0, t.width, part, tmem + uint32_t(acc) * 256u + (uint32_t(quarter * 32) << 16), turn);
+      epilogue<EPI, WARPS / 4>(p, p.t[t.q], t.q, row0, col0, t.width, part, tmem + uint32_t(acc) * 256u + (uint32_t(quarter * 32) << 16),
+                               scratch, turn);
       // hand the accumulator back: its reads are complete (tcgen05.wait::ld) and fenced, and nothing
       // else of the tile has to be ordered inside the launch
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_remote_relaxed(ptx::mapa_shared(tempty_bar(acc), 0));
     }
+    if (lane == 0) ptx::bulk_wait();
   }
 
   ptx::tc_fence_before();
@@ -329,7 +383,7 @@ __global__ void __launch_bounds__(64 + 32 * WARPS, 1) linear_pair_kernel(const _
   if (*abort_flag != 0 || peer_report[0] != 0u) {
     // Nothing may still write into either CTA's memory when they exit: the even CTA waits for its
     // instructions, then settles every stage that either producer left in flight (all copies of both
-    // CTAs count their bytes on its full barriers; at most the last p.stages can be in flight).
+    // CTAs count their bytes on its full barriers; at most the last kStgs can be in flight).
     if (leader && warp == 1 && lane == 0 && mma_issued) {
       ptx::umma_commit_pair(drain_bar, 0x1);
       mbar_wait_drain(drain_bar, 0u, p.timeout_ns);
@@ -339,7 +393,7 @@ __global__ void __launch_bounds__(64 + 32 * WARPS, 1) linear_pair_kernel(const _
       const uint32_t most = L > P ? L : P;
       // stages of this pair's uncut tiles, which come first
       const uint32_t wide = first < p.whole ? uint32_t((p.whole - first + step - 1) / step) * uint32_t(blocks) : 0u;
-      const uint32_t stages = uint32_t(p.stages);
+      constexpr uint32_t stages = uint32_t(kStgs);
       for (uint32_t j = most > stages ? most - stages : 0u; j < most; ++j) {
         const int s = int(j % stages);
         const uint32_t bytes = kHalf + (j < wide ? kHalf : kHalf / uint32_t(p.cut));
@@ -373,6 +427,19 @@ EncodeTiledFn tensor_map_encoder() {
   return fn;
 }
 
+// Boxes of 32 rows of `cols` columns of an output, swizzled as put_row has them.
+bool encode_box(CUtensorMap* map, void* p, int64_t rows, int64_t width, int64_t ld, int64_t size, uint32_t cols) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(width), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(ld * size)};
+  const cuuint32_t box[2] = {cols, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, cols * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <Epilogue EPI, bool A_MN, bool B_MN>
 cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t stream) {
   const int n = std::max(q.count, q.segments);
@@ -391,15 +458,30 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
     tiles += int64_t(t.tiles_m) * t.tiles_n;
   }
   if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
+  // What is stored by TMA: bf16 rows that are 16-byte aligned (added to, whole chunks only), the padded
+  // rows of the workspace, and 8-bit codes.
+  if (EPI == kEpiLinear) {
+    for (int i = 0; i < q.count; ++i) {
+      GemmTarget& t = p.t[i];
+      t.bulk = t.out_bf16 && t.align != 0 && (t.add == nullptr || t.n % 32 == 0);
+      if (t.bulk && !encode_box(&p.so[i], t.out, t.m, t.n, t.ld, 2, 32)) return cudaErrorInvalidValue;
+    }
+  } else {
+    void* outs[3] = {q.t[0].out, q.out2, q.out3};
+    for (int i = 0; i < (EPI == kEpiGated ? 1 : 3); ++i)
+      if (!encode_box(&p.so[i], outs[i], q.t[0].m, q.t[0].ld, q.t[0].ld, 2, EPI == kEpiGated ? 32 : 16)) return cudaErrorInvalidValue;
+  }
+  if (q.pre.data != nullptr && EPI != kEpiGatedGrad) {
+    const bool mx8 = q.pre.dtype == MO_MX8;
+    p.pre_bulk = mx8 || (EPI == kEpiLinear && p.pre_align != 0);
+    const int64_t k = q.t[0].n, pitch = mx8 ? mx8_blocks(k) * 32 : k;
+    const Kept* kept[2] = {&q.pre, &q.pre2};
+    for (int i = 0; p.pre_bulk && i < (EPI == kEpiGated ? 2 : 1); ++i)
+      if (!encode_box(&p.sk[i], kept[i]->data, q.t[0].m, mx8 ? pitch : k, pitch, mx8 ? 1 : 2, 32)) return cudaErrorInvalidValue;
+  }
   // The tiles of a last round that leaves half of the pairs idle, or three quarters, are cut into as
   // many parts. (Parts of 64 columns not where B's rows run along k: its boxes are 64 wide a CTA.)
   const int64_t pairs = sms / 2, last = tiles % pairs;
-  // (whole chunks of aligned rows are stored as they are; the rows of the workspace are padded)
-  bool turned = false;
-  for (int i = 0; i < q.count; ++i)
-    turned |= EPI == kEpiLinear && (p.t[i].align == 0 || p.t[i].n % 32 != 0);
-  turned |= q.pre.data != nullptr && q.pre.dtype != MO_MX8 && EPI != kEpiGatedGrad && (p.pre_align == 0 || q.t[0].n % 32 != 0);
-  p.stages = turned ? kStages - 1 : kStages;
   p.cut = last * 2 > pairs || last == 0 ? 1 : !B_MN && last * 4 <= pairs ? 4 : 2;
   p.whole = int32_t(p.cut > 1 ? tiles - last : tiles);
   p.tiles = int32_t(p.cut > 1 ? tiles + last * (p.cut - 1) : tiles);
@@ -408,10 +490,11 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
   // more than it gives (gated block 8192 x 4096 x 14336: 1775 and 1850 us).
   const bool few = int64_t(p.blocks) * q.segments > 32;
   auto kern = few ? linear_pair_kernel<EPI, A_MN, B_MN, 8> : linear_pair_kernel<EPI, A_MN, B_MN, kMostWarps>;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem);
+  const size_t smem = few ? kSmem<8> : kSmem<kMostWarps>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(2 * std::min<int64_t>(pairs, p.tiles));
-  return launch_kernel(kern, dim3(grid), dim3(64 + 32 * (few ? 8 : kMostWarps)), kSmem, 2, true, stream, p);
+  return launch_kernel(kern, dim3(grid), dim3(64 + 32 * (few ? 8 : kMostWarps)), smem, 2, true, stream, p);
 }
 
 }  // namespace

@@ -207,6 +207,23 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t saddr) {
   return v;
 }
 
+// ---------------------------------------------------------------- stores by TMA
+__device__ __forceinline__ void st_shared_v4(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Orders this thread's writes to shared memory before copies that are issued after
+// the next barrier.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// A box from shared memory to the tensor; elements outside it are not written.
+__device__ __forceinline__ void tma_store_2d(const void* map, uint32_t saddr, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(saddr), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// until this thread's copies have read their shared memory; until they are done
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // ---------------------------------------------------------------- pairs of fp32
 // Two fp32 numbers in a register pair: one instruction for both products, sums or
 // fused multiply-adds, each rounded as the single one is.
