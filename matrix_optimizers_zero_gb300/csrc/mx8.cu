@@ -76,23 +76,43 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict_
   }
 }
 
-// Rows that are not 16-byte aligned: a lane an element, a warp a block.
+// Rows that are not 16-byte aligned: a lane an element, a warp kOddBlocks blocks,
+// one behind the other, loaded together (1023 x 1283: 5.5 us, with one block 8.0).
+constexpr int kOddBlocks = 4;
+
+// f(q, block, row, first column) for the blocks from b0 on.
+template <typename F>
+__device__ __forceinline__ void each_odd(int64_t b0, int64_t blocks, uint32_t nb, F&& f) {
+  int64_t row = b0 >> 32 == 0 ? int64_t(uint32_t(b0) / nb) : b0 / nb, at = b0 - row * nb;
+#pragma unroll
+  for (int q = 0; q < kOddBlocks; ++q) {
+    if (b0 + q >= blocks) break;
+    f(q, b0 + q, row, at * 32);
+    if (++at == nb) at = 0, ++row;
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quantize_odd_kernel(const T* __restrict__ x, int64_t blocks, int64_t k, uint32_t nb,
                                                                 uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int lane = int(threadIdx.x & 31);
-  const int64_t b = global_thread() >> 5;
-  if (b >= blocks) return;
-  const int64_t row = b >> 32 == 0 ? int64_t(uint32_t(b) / nb) : b / nb, col = (b - row * nb) * 32 + lane;
-  const float v = col < k ? load1(x + row * k + col) : 0.0f;
-  float top = fabsf(v);
+  const int64_t b0 = (global_thread() >> 5) * kOddBlocks;
+  if (b0 >= blocks) return;
+  float v[kOddBlocks] = {};
+  each_odd(b0, blocks, nb, [&](int q, int64_t, int64_t row, int64_t col) {
+    if (col + lane < k) v[q] = load1(x + row * k + col + lane);
+  });
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  const uint32_t s = mx8_scale(top);
-  codes[b * 32 + lane] = uint8_t(cvt_e4m3x2(v * mx8_down(s), 0.0f));
-  if (lane == 0) scales[b] = uint8_t(s);
+  for (int q = 0; q < kOddBlocks; ++q) {
+    if (b0 + q >= blocks) break;
+    // (magnitudes are in order as their words are, and NaN is above infinity)
+    const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v[q]))));
+    const uint32_t s = mx8_scale(top);
+    codes[(b0 + q) * 32 + lane] = uint8_t(cvt_e4m3x2(v[q] * mx8_down(s), 0.0f));
+    if (lane == 0) scales[b0 + q] = uint8_t(s);
+  }
 }
 
 // Values of 8-bit codes into dense rows of whole blocks, eight a thread and group.
@@ -194,17 +214,23 @@ __global__ void __launch_bounds__(kThreads) lay_out_kernel(const LayOutParams p)
     unpack_group<false>(t.src.data, nullptr, g, t.cols, per_row, t.out, t.ld);
 }
 
-// 8-bit codes into rows that are not 16-byte aligned: a lane an element.
+// 8-bit codes into rows that are not 16-byte aligned: a lane an element, as above.
 template <typename O>
 __global__ void __launch_bounds__(kThreads) unpack_odd_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                               int64_t blocks, int64_t k, uint32_t nb, O* __restrict__ out) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int lane = int(threadIdx.x & 31);
-  const int64_t b = global_thread() >> 5;
-  if (b >= blocks) return;
-  const int64_t row = b >> 32 == 0 ? int64_t(uint32_t(b) / nb) : b / nb, col = (b - row * nb) * 32 + lane;
-  if (col < k) store1(out + row * k + col, e4m3_value(codes[b * 32 + lane]) * mx8_up(scales[b]));
+  const int64_t b0 = (global_thread() >> 5) * kOddBlocks;
+  if (b0 >= blocks) return;
+  uint8_t c[kOddBlocks], s[kOddBlocks];
+  each_odd(b0, blocks, nb, [&](int q, int64_t b, int64_t, int64_t) {
+    c[q] = codes[b * 32 + lane];
+    s[q] = scales[b];
+  });
+  each_odd(b0, blocks, nb, [&](int q, int64_t, int64_t row, int64_t col) {
+    if (col + lane < k) store1(out + row * k + col + lane, e4m3_value(c[q]) * mx8_up(s[q]));
+  });
 }
 
 // dz = dout act'(pre) and its column sums: a block takes 256 columns, eight a
@@ -361,6 +387,8 @@ unsigned blocks_of(int64_t threads) { return unsigned((threads + kThreads - 1) /
 
 unsigned quant_blocks(int64_t groups) { return unsigned((groups + kThreads * kQuantGroups - 1) / (kThreads * kQuantGroups)); }
 
+unsigned odd_blocks(int64_t blocks) { return blocks_of((blocks + kOddBlocks - 1) / kOddBlocks * 32); }
+
 template <typename T>
 cudaError_t quantize_as(const T* x, int64_t rows, int64_t k, const Kept& q, cudaStream_t stream) {
   const int64_t nb = mx8_blocks(k);
@@ -371,7 +399,7 @@ cudaError_t quantize_as(const T* x, int64_t rows, int64_t k, const Kept& q, cuda
     return launch_kernel(kern, dim3(quant_blocks(groups)), dim3(kThreads), 0, 1, true, stream, x, groups, k, uint32_t(nb * 4), codes,
                          q.scales);
   }
-  return launch_kernel(quantize_odd_kernel<T>, dim3(blocks_of(rows * nb * 32)), dim3(kThreads), 0, 1, true, stream, x, rows * nb, k,
+  return launch_kernel(quantize_odd_kernel<T>, dim3(odd_blocks(rows * nb)), dim3(kThreads), 0, 1, true, stream, x, rows * nb, k,
                        uint32_t(nb), codes, q.scales);
 }
 
@@ -386,7 +414,7 @@ cudaError_t unpack_as(const Kept& src, int64_t rows, int64_t k, O* out, cudaStre
     return launch_kernel(unpack_kernel<O>, dim3(blocks_of(rows * k / 8)), dim3(kThreads), 0, 1, true, stream, s, scales, rows * k / 8, k,
                          uint32_t(k / 8), out, k);
   const int64_t nb = mx8_blocks(k);
-  return launch_kernel(unpack_odd_kernel<O>, dim3(blocks_of(rows * nb * 32)), dim3(kThreads), 0, 1, true, stream, s, scales, rows * nb, k,
+  return launch_kernel(unpack_odd_kernel<O>, dim3(odd_blocks(rows * nb)), dim3(kThreads), 0, 1, true, stream, s, scales, rows * nb, k,
                        uint32_t(nb), out);
 }
 
