@@ -4,10 +4,11 @@ Bounds, element by element. A product's sum of K terms: each addition in fp32
 is off by at most 2^-23 of the magnitudes so far (truncation counted), so
 K 2^-23 of the sum of the terms' magnitudes. A rounding to a type: eps / 2 of
 the value. A logistic function: its exponent's argument is off by a few units
-of 2^-24 of itself and __expf by (2 + 1.2 |x|) 2^-23, so (8 + 4 |u|) 2^-23 of
-the value with u the argument; erfcf: 4 units, and 2 y^2 2^-23 for its rounded
-argument. What an error passes through multiplies it by at most its slope
-(|act'| <= 1.13)."""
+of 2^-24 of itself and the fast exponential by (2 + 1.2 |x|) 2^-23, so
+(8 + 4 |u|) 2^-23 of the value with u the argument. gelu's normal distribution is
+a published approximation (Abramowitz and Stegun 7.1.26): erfc within 1.5e-7, so
+0.75e-7 < 2^-23 times the argument, and 2 y^2 2^-23 for the exponent. What an
+error passes through multiplies it by at most its slope (|act'| <= 1.13)."""
 import numpy as np
 import pytest
 import torch
