@@ -17,8 +17,9 @@
 namespace mo {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kWarps = kThreads / 32;
+// Two warps load and multiply; eight (four for 16 rows) move the sums.
+template <int NT>
+constexpr int kThreads = NT == 16 ? 192 : 320;
 constexpr uint32_t kPanel = 128 * kBlockK * 2;   // 128 columns' operand
 constexpr uint32_t kPitch = 132;                 // of the fp32 sums [NT][128] in shared memory
 
@@ -144,10 +145,11 @@ __device__ __forceinline__ void finish(const GemmParams& p, const GemmTarget& t,
 
 // Q: the rows' operand (A of the product), P: the columns' (B).
 template <Epilogue EPI, bool Q_MN, bool P_MN, int NT>
-__global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __launch_bounds__(kThreads<NT>) linear_narrow_kernel(const __grid_constant__ GemmParams p) {
   static_assert(!Q_MN || NT == 128, "whole boxes");
   extern __shared__ uint8_t smem_raw[];
   constexpr uint32_t kStg = kStage<EPI, NT>;
+  constexpr int kWarps = kThreads<NT> / 32, kShares = (kWarps - 2) / 4;   // warps; of a quarter of the lanes
   const int stages = p.stages;
   constexpr uint32_t kQ = kPanels<EPI> * kPanel;   // of the rows' operand in a stage
   const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) linear_narrow_kernel(const __grid_co
 #pragma unroll 1
       for (int i = 0; i < kPanels<EPI>; ++i)
 #pragma unroll 1
-        for (int c = 0; c < rows; c += 16) {
+        for (int c = (warp - 2) / 4 * 16; c < rows; c += 16 * kShares) {
           uint32_t r[16];
           __syncwarp();
           ptx::tmem_ld_32x32b_x16(tmem + uint32_t(i * NT + c) + (uint32_t(quarter * 32) << 16), r);
@@ -378,7 +380,7 @@ cudaError_t narrow_as(const Product& q, GemmParams& p, int sms, cudaStream_t str
   auto kern = linear_narrow_kernel<EPI, Q_MN, P_MN, NT>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem_of<EPI, NT>(kDeep<EPI, NT>));
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(unsigned(tiles * parts)), dim3(kThreads), smem_of<EPI, NT>(p.stages), parts, true, stream, p);
+  return launch_kernel(kern, dim3(unsigned(tiles * parts)), dim3(kThreads<NT>), smem_of<EPI, NT>(p.stages), parts, true, stream, p);
 }
 
 template <Epilogue EPI, bool P_MN>

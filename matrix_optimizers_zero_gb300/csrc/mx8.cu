@@ -239,59 +239,75 @@ __global__ void __launch_bounds__(kThreads) unpack_odd_kernel(const uint8_t* __r
 constexpr int kRowsAhead = 2;   // of a warp, loaded together
 
 template <bool MX8, int ACT>
-__device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t row0, int64_t row1, int64_t col, float (&sum)[8]) {
+__device__ __forceinline__ void act_grad_rows(const ActGradParams& p, int64_t row0, int64_t row1, int64_t col, F2 (&sum)[4]) {
   const int64_t n = p.rows;
   if (col >= n) return;
-  const uint32_t nb = uint32_t((n + 31) / 32);
-  for (int64_t first = row0 + (threadIdx.x >> 5); first < row1; first += 8 * kRowsAhead) {
-    uint4 dout[kRowsAhead], pre[kRowsAhead];   // (pre: two words of 8-bit codes and the scale)
+  // Pointers to this lane's elements of the next row, and what a warp's next row is further on: two
+  // thirds of the time of a row are instructions.
+  const int64_t pitch = MX8 ? (n + 31) / 32 * 32 : n, first = row0 + (threadIdx.x >> 5);
+  const uint16_t* dout_at = p.dout + first * n + col;
+  const uint8_t* pre_at = static_cast<const uint8_t*>(p.pre.data) + (first * pitch + col) * (MX8 ? 1 : 2);
+  const uint8_t* scale_at = p.pre.scales + (first * pitch + col) / 32;
+  uint16_t* dz_at = p.dz + first * p.ld + col;
+  auto row = [&](const uint4& dout, const uint4& pre) {
+    const uint32_t w[4] = {dout.x, dout.y, dout.z, dout.w};
+    F2 d[4];
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      const int64_t r = first + 8 * u;
-      if (r >= row1) break;
-      dout[u] = *reinterpret_cast<const uint4*>(p.dout + r * n + col);
-      if constexpr (ACT != MO_ACT_NONE) {
-        if constexpr (MX8) {
-          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.pre.data) + r * nb * 32 + col);
-          pre[u] = make_uint4(w.x, w.y, p.pre.scales[r * nb + (col >> 5)], 0u);
-        } else {
-          pre[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.pre.data) + r * n + col);
+    for (int i = 0; i < 4; ++i) d[i] = ptx::f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    if constexpr (ACT != MO_ACT_NONE) {
+      F2 z[4];
+      if constexpr (MX8) {
+        const F2 up = ptx::f2(mx8_up(pre.z));
+        float a[4], b[4];
+        e4m3x4_values(pre.x, a);
+        e4m3x4_values(pre.y, b);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          z[i] = ptx::mul2(ptx::f2(a[2 * i], a[2 * i + 1]), up);
+          z[2 + i] = ptx::mul2(ptx::f2(b[2 * i], b[2 * i + 1]), up);
         }
-      }
-    }
+      } else {
+        const uint32_t v[4] = {pre.x, pre.y, pre.z, pre.w};
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      const int64_t r = first + 8 * u;
-      if (r >= row1) break;
-      float d[8];
-      load8(reinterpret_cast<const uint16_t*>(&dout[u]), d);
-      if constexpr (ACT != MO_ACT_NONE) {
-        float z[8];
-        if constexpr (MX8) {
-          const float up = mx8_up(pre[u].z);
-          float a[4], b[4];
-          e4m3x4_values(pre[u].x, a);
-          e4m3x4_values(pre[u].y, b);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            z[i] = a[i] * up;
-            z[4 + i] = b[i] * up;
-          }
-        } else {
-          load8(reinterpret_cast<const uint16_t*>(&pre[u]), z);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          F2 value;
-          const float2 y = ptx::parts(ptx::mul2(ptx::f2(d[i], d[i + 1]), act_slope<ACT>(ptx::f2(z[i], z[i + 1]), &value)));
-          d[i] = y.x;
-          d[i + 1] = y.y;
-        }
+        for (int i = 0; i < 4; ++i) z[i] = ptx::f2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += d[i];
-      if (p.dz != nullptr) store8(p.dz + r * p.ld + col, d);
+      for (int i = 0; i < 4; ++i) {
+        F2 value;
+        d[i] = ptx::mul2(d[i], act_slope<ACT>(z[i], &value));
+      }
     }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum[i] = ptx::add2(sum[i], d[i]);
+      const float2 y = ptx::parts(d[i]);
+      o[i] = pack_bf16x2(y.x, y.y);
+    }
+    if (p.dz != nullptr) *reinterpret_cast<uint4*>(dz_at) = make_uint4(o[0], o[1], o[2], o[3]);
+    dz_at += 8 * p.ld;
+  };
+  for (int64_t left = (row1 - first + 7) / 8; left > 0; left -= kRowsAhead) {
+    uint4 dout[kRowsAhead], pre[kRowsAhead] = {};   // (pre: two words of 8-bit codes and the scale)
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      if (u >= left) break;
+      dout[u] = *reinterpret_cast<const uint4*>(dout_at);
+      if constexpr (ACT != MO_ACT_NONE) {
+        if constexpr (MX8) {
+          const uint2 c = *reinterpret_cast<const uint2*>(pre_at);
+          pre[u] = make_uint4(c.x, c.y, *scale_at, 0u);
+          scale_at += pitch / 4;
+        } else {
+          pre[u] = *reinterpret_cast<const uint4*>(pre_at);
+        }
+        pre_at += 8 * pitch * (MX8 ? 1 : 2);
+      }
+      dout_at += 8 * n;
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u)
+      if (u < left) row(dout[u], pre[u]);
   }
 }
 
@@ -334,15 +350,20 @@ __global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) act_grad_kernel(const A
   const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
   const int64_t col = int64_t(blockIdx.x) * 256 + (VEC ? lane * 8 : lane);
   const int64_t row0 = int64_t(blockIdx.y) * p.per, row1 = min(row0 + p.per, p.tokens);
-  float sum[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+  float sum[8] = {};
   with_act(p.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
-    if constexpr (VEC)
-      act_grad_rows<MX8, ACT>(p, row0, row1, col, sum);
-    else
+    if constexpr (VEC) {
+      F2 pairs[4] = {ptx::f2(0.0f), ptx::f2(0.0f), ptx::f2(0.0f), ptx::f2(0.0f)};
+      act_grad_rows<MX8, ACT>(p, row0, row1, col, pairs);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 s = ptx::parts(pairs[i]);
+        sum[2 * i] = s.x, sum[2 * i + 1] = s.y;
+      }
+    } else {
       act_grad_rows_odd<MX8, ACT>(p, row0, row1, col, sum);
+    }
   });
   if (p.part == nullptr) return;
 #pragma unroll
