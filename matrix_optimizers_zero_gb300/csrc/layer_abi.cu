@@ -471,12 +471,13 @@ int linear_grad(const void* dout, const mo_tensor* x, const void* w, int64_t tok
   }
   const int64_t parts = (tokens + g.per - 1) / g.per;
   if (dbias != nullptr) g.part = static_cast<float*>(space.take(size_t(parts) * size_t(rows) * 4));
-  if (g.dz != nullptr || g.part != nullptr) run(mo::launch_act_grad(g, stream));
-  if (dbias != nullptr && run.error == cudaSuccess) run(mo::launch_join(g.part, parts, rows, dbias, accumulate != 0, stream));
   Operands operand{space};
   const Operand xo = dw != nullptr ? operand(xk, tokens, cols) : Operand{};
   const Operand wo = dx != nullptr ? operand(w, rows, cols) : Operand{};
+  g.early = operand.n > 0;
   operand.lay_out(run, stream);
+  if ((g.dz != nullptr || g.part != nullptr) && run.error == cudaSuccess) run(mo::launch_act_grad(g, stream));
+  if (dbias != nullptr && run.error == cudaSuccess) run(mo::launch_join(g.part, parts, rows, dbias, accumulate != 0, stream));
   float* part = reinterpret_cast<float*>(space.take(0));
   if (dx != nullptr) {
     mo::Product q;

@@ -51,6 +51,7 @@ struct ActGradParams {
   int64_t tokens, rows, ld;
   int64_t per;
   int32_t act;
+  int32_t early;   // directly behind launch_lay_out, and may run beside it
 };
 cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream);
 // out[i] (+)= the sum over part[0..parts)[i], in order.

@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(kThreads) quantize_odd_kernel(const T* __restr
 template <typename O>
 __global__ void __launch_bounds__(kThreads) unpack_flat_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                                int64_t groups, O* __restrict__ out) {
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();   // (after the wait: act_grad_kernel)
   const int64_t g0 = int64_t(blockIdx.x) * (kThreads * kQuantGroups) + threadIdx.x;
   uint2 w[kQuantGroups];
   uint8_t s[kQuantGroups];
@@ -189,8 +189,8 @@ __device__ __forceinline__ void unpack_group(const void* src, const uint8_t* sca
 template <typename O>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                           int64_t groups, int64_t k, uint32_t per_row, O* __restrict__ out, int64_t ld) {
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();   // (after the wait: act_grad_kernel)
   const int64_t g = global_thread();
   if (g < groups) unpack_group<true>(codes, scales, g, k, per_row, out, ld);
 }
@@ -201,8 +201,8 @@ struct LayOutParams {
   int64_t first[3];   // block
 };
 __global__ void __launch_bounds__(kThreads) lay_out_kernel(const LayOutParams p) {
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();   // (after the wait: act_grad_kernel)
   const int i = int64_t(blockIdx.x) >= p.first[2] ? 2 : int64_t(blockIdx.x) >= p.first[1] ? 1 : 0;
   const LayOut& t = p.t[i];
   const int64_t g = (int64_t(blockIdx.x) - p.first[i]) * kThreads + threadIdx.x;
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(kThreads) lay_out_kernel(const LayOutParams p)
 template <typename O>
 __global__ void __launch_bounds__(kThreads) unpack_odd_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                               int64_t blocks, int64_t k, uint32_t nb, O* __restrict__ out) {
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();   // (after the wait: act_grad_kernel)
   const int lane = int(threadIdx.x & 31);
   const int64_t b0 = (global_thread() >> 5) * kOddBlocks;
   if (b0 >= blocks) return;
@@ -346,7 +346,9 @@ template <bool VEC, bool MX8>
 __global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) act_grad_kernel(const ActGradParams p) {
   __shared__ float sums[8][256];
   ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
+  // early: behind a launch that lays out operands and writes nothing that is read here. Its blocks let this
+  // one come when they have waited, so what was before it has ended; and this one ends behind it.
+  if (!p.early) ptx::griddep_wait();
   const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
   const int64_t col = int64_t(blockIdx.x) * 256 + (VEC ? lane * 8 : lane);
   const int64_t row0 = int64_t(blockIdx.y) * p.per, row1 = min(row0 + p.per, p.tokens);
@@ -365,17 +367,19 @@ __global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) act_grad_kernel(const A
       act_grad_rows_odd<MX8, ACT>(p, row0, row1, col, sum);
     }
   });
-  if (p.part == nullptr) return;
+  if (p.part != nullptr) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[warp][VEC ? lane * 8 + i : lane + 32 * i] = sum[i];
-  __syncthreads();
-  const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (c < p.rows) {
-    float t = 0.0f;
+    for (int i = 0; i < 8; ++i) sums[warp][VEC ? lane * 8 + i : lane + 32 * i] = sum[i];
+    __syncthreads();
+    const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (c < p.rows) {
+      float t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
-    p.part[int64_t(blockIdx.y) * p.rows + c] = t;
+      for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
+      p.part[int64_t(blockIdx.y) * p.rows + c] = t;
+    }
   }
+  if (p.early) ptx::griddep_wait();
 }
 
 // Column sums of part [parts, n]: a block takes 32 columns, each of its warps a
