@@ -282,24 +282,27 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_grad_k
   const uint32_t start = ptx::smem_addr(slots);
   const Slots<kRow, kBlock<TEAM>> ds(start), rs(start + (kAhead + 1) * ds.kSlot);
   const Slots<MX8 ? 8 : kRow, kBlock<TEAM>> xs(start + 2 * (kAhead + 1) * ds.kSlot);
-  const T* dy_at = static_cast<const T*>(p.dy) + col;
-  const T* res_at = p.dres != nullptr ? static_cast<const T*>(p.dres) + col : nullptr;
-  auto fetch = [&](int64_t row, uint32_t slot) {
-    if (row < p.rows && in) {
-      ds.copy(slot, dy_at + row * p.dim);
+  // The rows that are left, this thread's elements of the first of them, and how far the next are (of 8-bit
+  // rows at8 and stride8): the instructions of a row take most of its time.
+  int left = team < p.rows ? int((p.rows - team + step - 1) / step) : 0;
+  int64_t at = team * p.dim + col, at8 = team * nb * 32 + col;
+  const int64_t stride = step * p.dim, stride8 = step * nb * 32;
+  auto fetch = [&](int ahead, uint32_t slot) {
+    if (left > ahead && in) {
+      ds.copy(slot, static_cast<const T*>(p.dy) + at + ahead * stride);
       if constexpr (MX8)
-        xs.copy(slot, static_cast<const uint8_t*>(p.x.data) + row * nb * 32 + col);
+        xs.copy(slot, static_cast<const uint8_t*>(p.x.data) + at8 + ahead * stride8);
       else
-        xs.copy(slot, static_cast<const T*>(p.x.data) + row * p.dim + col);
-      if (res_at != nullptr) rs.copy(slot, res_at + row * p.dim);
+        xs.copy(slot, static_cast<const T*>(p.x.data) + at + ahead * stride);
+      if (p.dres != nullptr) rs.copy(slot, static_cast<const T*>(p.dres) + at + ahead * stride);
     }
     ptx::cp_async_commit();
   };
   // (a scale is one byte, too few for such a copy: one row ahead in a register)
-  auto scale_of = [&](int64_t row) { return MX8 && row < p.rows && in ? p.x.scales[row * nb + (col >> 5)] : uint8_t(0); };
+  auto scale_of = [&](int ahead) { return MX8 && left > ahead && in ? p.x.scales[(at8 + ahead * stride8) >> 5] : uint8_t(0); };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch(team + i * step, uint32_t(i));
-  uint8_t scale = scale_of(team);
+  for (int i = 0; i < kAhead; ++i) fetch(i, uint32_t(i));
+  uint8_t scale = scale_of(0);
   F2 w[4], dw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = ptx::f2(1.0f), dw[i] = ptx::f2(0.0f);
@@ -311,8 +314,8 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_grad_k
   }
   uint32_t slot = 0;
   int parity = 0;
-  for (int64_t row = team; row < p.rows; row += step, parity ^= 1) {
-    fetch(row + kAhead * step, slot == 0 ? kAhead : slot - 1);
+  for (; left > 0; --left, at += stride, at8 += stride8, parity ^= 1) {
+    fetch(kAhead, slot == 0 ? kAhead : slot - 1);
     ptx::cp_async_wait_but<kAhead>();
     F2 s[4], dy[4];
 #pragma unroll
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_grad_k
       slot_values(ds, slot, 0.0f, dy);
       slot_values(xs, slot, MX8 ? mx8_up(scale) : 0.0f, s);
     }
-    scale = scale_of(row + step);
+    scale = scale_of(1);
     F2 squares = ptx::mul2(s[0], s[0]), dot = ptx::mul2(ptx::mul2(dy[0], w[0]), s[0]);
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
@@ -339,12 +342,12 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_grad_k
         dw[i] = ptx::fma2(dy[i], n, dw[i]);
         dy[i] = ptx::mul2(r2, ptx::fma2(n, m2, ptx::mul2(dy[i], w[i])));
       }
-      if (res_at != nullptr) {
+      if (p.dres != nullptr) {
         slot_values(rs, slot, 0.0f, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) dy[i] = ptx::add2(dy[i], s[i]);
       }
-      store_pairs(static_cast<T*>(p.dx) + row * p.dim + col, dy);
+      store_pairs(static_cast<T*>(p.dx) + at, dy);
     }
     slot = slot == kAhead ? 0 : slot + 1;
   }
