@@ -22,7 +22,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libmo.so")
 SOURCES = ["plan.cpp", "planner.cpp", "abi.cu", "elementwise.cu", "ns_gemm.cu", "static_ws.cu",
            "train_abi.cu", "embed.cu", "fp4_quant.cu", "fp4_gemm.cu",
-           "layer_abi.cu", "mx8.cu", "norm.cu", "linear_pair.cu", "linear_narrow.cu"]
+           "layer_abi.cu", "mx8.cu", "norm.cu", "linear_pair.cu", "linear_narrow.cu", "linear_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -557,7 +557,7 @@ int gated_ffn_forward(const mo_tensor* x, const void* w_gate, const void* w_up, 
   down.a[0] = {h, tokens, inner, ld};
   down.b[0] = operand(w_down, dim, inner);
   operand.lay_out(run, stream);
-  down.early = !needs_copy(inner, MO_BF16) && mo::is_narrow(q, sms);
+  down.early = !needs_copy(inner, MO_BF16) && (mo::is_few(q, sms) || mo::is_narrow(q, sms));
   down.t[0] = target(out, out_dtype, tokens, dim, residual);
   down.k = inner;
   if (run.error == cudaSuccess) run(mo::launch_product(down, sms, status, stream));

@@ -132,11 +132,12 @@ struct Product {
   Kept pre, pre2;
   uint16_t* out2 = nullptr;          // kEpiGatedGrad, pitch t[0].ld
   uint16_t* out3 = nullptr;
-  // b may be read while the previous launch runs: that launch is a product for which is_narrow holds,
-  // and does not write b
+  // b may be read while the previous launch runs: that launch is a product for which is_narrow or is_few
+  // holds, and does not write b
   bool early = false;
 };
-// Whether a product goes to the kernel for few rows.
+// Whether a product goes to the kernel for one or two rows, and otherwise to the one for few.
+bool is_few(const Product& q, int sms);
 bool is_narrow(const Product& q, int sms);
 cudaError_t launch_product(const Product& p, int sms, int* status, cudaStream_t stream);
 

@@ -338,6 +338,7 @@ __device__ __forceinline__ float kept_at(const Kept& q, int64_t row, int64_t col
 
 // Few rows: tiles of 128 columns, the reduction split over clusters.
 cudaError_t launch_narrow(const Product& q, GemmParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_few(const Product& q, int sms, cudaStream_t stream);
 bool encode_operand(CUtensorMap* map, const Operand& o, uint32_t box_rows);
 
 }  // namespace mo

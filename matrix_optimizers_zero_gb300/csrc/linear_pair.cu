@@ -524,6 +524,7 @@ bool is_narrow(const Product& q, int sms) {
 }
 
 cudaError_t launch_product(const Product& q, int sms, int* status, cudaStream_t stream) {
+  if (is_few(q, sms)) return launch_few(q, sms, stream);
   GemmParams p = {};
   p.count = q.count;
   p.segments = q.segments;

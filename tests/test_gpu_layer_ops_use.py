@@ -66,6 +66,23 @@ def test_gated_ffn_grad_tiles(t, d, f, activation, save, mx8, dtype, accumulate)
     base.test_gated_ffn_grad(t, d, f, activation, save, mx8, dtype, accumulate)
 
 
+# One and two rows, which have a kernel of their own where nothing is kept: reductions that end inside a
+# warp's pieces, columns past every warp's first, the longest rows it takes and longer ones.
+
+@pytest.mark.parametrize("t,k,n", [(1, 8, 5), (2, 264, 4863), (1, 256, 4864), (2, 256, 4865), (1, 512, 9999), (2, 520, 4870), (1, 4096, 33),
+                                   (2, 28672, 40), (1, 57344, 17), (2, 28680, 16), (1, 57352, 16), (3, 1280, 100), (1, 1283, 90)])
+@pytest.mark.parametrize("activation,bias,residual,mx8,out", [(None, False, False, False, BF16), ("silu", True, True, True, F32),
+                                                              ("gelu", False, True, False, BF16)])
+def test_one_and_two_rows(t, k, n, activation, bias, residual, mx8, out):
+    base.test_linear(t, k, n, activation, bias, residual, None, mx8, out)
+
+
+@pytest.mark.parametrize("t,d,f", [(1, 8, 16), (2, 264, 4880), (1, 520, 9728), (2, 1280, 1003), (2, 1003, 1288), (1, 512, 5000), (2, 64, 30000)])
+@pytest.mark.parametrize("activation,residual,mx8,out", [("silu", True, False, BF16), ("gelu_tanh", False, True, F32)])
+def test_gated_block_of_one_and_two_rows(t, d, f, activation, residual, mx8, out):
+    base.test_gated_ffn(t, d, f, activation, residual, None, mx8, out)
+
+
 # ---------------------------------------------------------------- sums that are cut, offsets past 32 bits
 
 @pytest.mark.parametrize("t,k,n,accumulate", [(40000, 24, 40, True), (70001, 33, 17, False), (32769, 8, 8, True)])
@@ -192,7 +209,7 @@ class Guarded:
             assert (buf[:self.PAD] == 0xA5).all() and (buf[self.PAD + nbytes:] == 0xA5).all()
 
 
-@pytest.mark.parametrize("t,d,f", [(1, 33, 47), (3, 40, 72), (130, 200, 301), (777, 515, 1003), (2300, 520, 1153), (2311, 1096, 1160)])
+@pytest.mark.parametrize("t,d,f", [(1, 33, 47), (1, 512, 520), (2, 40, 72), (3, 40, 72), (130, 200, 301), (777, 515, 1003), (2300, 520, 1153), (2311, 1096, 1160)])
 def test_buffers_end_where_the_call_ends(t, d, f):
     g = Guarded()
     bf = lambda *s: g(torch.zeros(s, dtype=BF16, device=dev()))   # noqa: E731
@@ -210,11 +227,13 @@ def test_buffers_end_where_the_call_ends(t, d, f):
     for out in (bf(t, f), fp(t, f)):
         mo.linear(x, wg, out, bias=fp(f), activation="silu", residual=out, pre=bf(t, f), workspace=small)
         mo.linear(n8, wg, out, bias=fp(f), activation="gelu", pre=u8, workspace=small)
+        mo.linear(x, wg, out, workspace=small)
     dout = bf(t, f)
     mo.linear_grad(dout, n8, wg, dx=bf(t, d), dw=fp(f, d), dbias=fp(f), activation="silu", pre=u8, workspace=big)
     mo.linear_grad(dout, x, wg, dx=fp(t, d), dw=bf(f, d), dbias=fp(f), workspace=big)
     small, big = ws(mo.mo_gated_ffn_workspace_bytes(t, d, f)), ws(mo.mo_gated_ffn_workspace_bytes(t, d, f, grad=True))
     mo.gated_ffn(n8, wg, wu, wd, s, residual=s, gate=g8, up=u8, workspace=small)
+    mo.gated_ffn(x, wg, wu, wd, fp(t, d), workspace=small)
     gate, up = bf(t, f), bf(t, f)
     mo.gated_ffn(x, wg, wu, wd, fp(t, d), gate=gate, up=up, workspace=small)
     for pair in ((g8, u8), (gate, up)):
@@ -299,13 +318,15 @@ class Step:
         self.sum, self.out, self.dn, self.dx, self.dw = e(self.s), e(self.s), e(self.s), e(self.s), e(self.w)
         self.h, self.z8, self.y, self.db = torch.empty(t, f, dtype=BF16, device=dev()), empty8(t, f), e(self.s), torch.empty(f, device=dev())
         self.grads = [e(m) for m in self.mats]
-        self.g1 = e(self.mats[0])
+        self.g1, self.served, self.logits = e(self.mats[0]), e(self.s), e(self.h)
 
     def run(self, stream=None):
         k = dict(stream=stream)
         mo.rms_norm(self.x, weight=self.w, residual=self.s, sum_out=self.sum, out8=self.n8, **k)
         mo.mx8_quantize(self.sum, self.s8, **k)
         mo.gated_ffn(self.n8, *self.mats, self.out, residual=self.sum, gate=self.g8, up=self.u8, workspace=self.ws, **k)
+        mo.gated_ffn(self.x, *self.mats, self.served, workspace=self.ws, **k)
+        mo.linear(self.served, self.mats[0], self.logits, workspace=self.ws, **k)
         mo.linear(self.out, self.mats[0], self.h, bias=self.b, activation="gelu", pre=self.z8, workspace=self.ws, **k)
         mo.linear_grad(self.h, self.out, self.mats[0], dx=self.y, dw=self.g1, dbias=self.db, activation="gelu", pre=self.z8, workspace=self.ws, **k)
         mo.gated_ffn_grad(self.ds, self.n8, self.g8, self.u8, *self.mats, dx=self.dn, dw_gate=self.grads[0], dw_up=self.grads[1],
@@ -313,7 +334,7 @@ class Step:
         mo.rms_norm_grad(self.dn, self.s8, self.dx, weight=self.w, dresidual=self.ds, dweight=self.dw, workspace=self.norm_ws, **k)
 
     def results(self):
-        return [self.sum, self.out, self.h, self.y, self.g1, self.db, self.dn, self.dx, self.dw, *self.grads,
+        return [self.sum, self.out, self.h, self.y, self.g1, self.db, self.dn, self.dx, self.dw, self.served, self.logits, *self.grads,
                 *(v for q in (self.n8, self.s8, self.g8, self.u8, self.z8) for v in (q.codes, q.scales))]
 
     def spoil(self):
@@ -333,7 +354,7 @@ def same(a, b):
     return all(torch.equal(x.view(U8), y.view(U8)) for x, y in zip(a, b))
 
 
-SIZES = [(1, 64, 96), (37, 200, 301), (513, 256, 704), (2304, 1032, 1160)]
+SIZES = [(1, 64, 96), (2, 520, 1000), (37, 200, 301), (513, 256, 704), (2304, 1032, 1160)]
 
 
 @pytest.mark.parametrize("t,d,f", SIZES)
