@@ -129,9 +129,14 @@ def _typed(t, name: str, here: int, code: int, numel: int):
 
 
 def _matrix(t, shape, name: str, here: int):
+    """Pointer of a bf16 matrix of a shape."""
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
-    return _typed(t, name, here, MO_BF16, shape[0] * shape[1])
+    if _dtypes.get(t.dtype) != MO_BF16:
+        raise TypeError(f"{name} must be bf16")
+    if t.get_device() != here or not t.is_contiguous():
+        _refuse(t, name, here, "")
+    return t.data_ptr()
 
 
 def _rows(t, width: int, name: str) -> int:
@@ -149,13 +154,15 @@ def _rows(t, width: int, name: str) -> int:
 def _kept(t, name: str, here: int, f32: bool = False):
     """mo_tensor of a plain or an 8-bit tensor."""
     if isinstance(t, Mx8Tensor):
-        if t.get_device() != here:
+        if t.device_index != here:
             raise ValueError(f"{name} must be on the current device ({here})")
         return t.arg
-    ptr, code = _plain(t, name, here)
-    if code == MO_F32 and not f32:
+    code = _dtypes.get(t.dtype)
+    if code != MO_BF16 and not (f32 and code == MO_F32):
         raise TypeError(f"{name} must be bf16 or an Mx8Tensor")
-    return MoTensor(ptr, None, code)
+    if t.get_device() != here or not t.is_contiguous():
+        _refuse(t, name, here, "")
+    return MoTensor(t.data_ptr(), None, code)
 
 
 def _kept_rows(t, width: int, rows: int, name: str, here: int, f32: bool = False):
@@ -180,11 +187,11 @@ def _scratch(t, name: str, here: int):
         raise ValueError(f"a workspace is needed ({name})")
     if t.get_device() != here or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def _act(name):
-    code = ACTIVATIONS.get(name)
+    code = ACTIVATIONS.get(name)   # (0: none)
     if code is None:
         raise ValueError(f"activation must be one of {', '.join(str(k) for k in ACTIVATIONS)}")
     return code

@@ -21,8 +21,9 @@ class Tensor:
     def numel(self):
         return self.shape.numel()
 
-    def element_size(self):
-        return self.dtype.itemsize
+    @property
+    def nbytes(self):
+        return self.numel() * self.dtype.itemsize
 
     def data_ptr(self):
         return 4096
