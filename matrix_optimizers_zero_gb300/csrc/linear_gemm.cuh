@@ -260,7 +260,7 @@ __device__ __forceinline__ void put_bf16(uint32_t box, const float (&v)[N]) {
 // Keeps a chunk, in 8 bits or in bf16: into `box` for the copy that follows (bulk;
 // the scales go out at once), or as it is.
 __device__ __forceinline__ void keep_chunk(const Kept& q, bool bulk, int align, int64_t row0, int64_t m, int64_t col, int64_t n,
-                                           const float (&v)[32], uint32_t box, float* turn) {
+                                           float (&v)[32], uint32_t box, float* turn) {
   if (q.dtype != MO_MX8) {
     if (bulk) {
       put_bf16(box, v);
@@ -273,7 +273,13 @@ __device__ __forceinline__ void keep_chunk(const Kept& q, bool bulk, int align, 
     }
     return;
   }
-  // (past n the sums are zeros, and so are the codes; their rows are 16-byte aligned, and always bulk)
+  // (rows of codes are 16-byte aligned, and always bulk; past n a sum is 0, or NaN where its row's operand
+  // is not finite)
+  if (col + 32 > n) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col + i >= n) v[i] = 0.0f;
+  }
   uint32_t w[8];
   const uint32_t s = mx8_chunk(v, w);
   put_row<32>(box, w);

@@ -276,6 +276,22 @@ def test_a_token_that_is_no_number_stays_alone(t, d, f, bad):
     assert torch.isnan(got[1][2][3]).all() and torch.isnan(got[1][4][3]).all()
 
 
+@pytest.mark.parametrize("t,d,f", [(6, 40, 72), (2400, 64, 2300)])
+def test_padding_is_zeros_beside_values_that_are_no_numbers(t, d, f):
+    x = data(t, d)
+    x[3, 5] = float("inf")
+    w, z8, out = data(f, d, seed=1), empty8(t, f), torch.empty(t, f, dtype=BF16, device=dev())
+    mo.linear(x, w, out, activation="silu", pre=z8, workspace=mo.linear_workspace(t, d, f))
+    g8, u8, y = empty8(t, f), empty8(t, f), torch.empty(t, d, dtype=BF16, device=dev())
+    mo.gated_ffn(x, w, w, data(d, f, seed=2), y, gate=g8, up=u8, workspace=mo.gated_ffn_workspace(t, d, f))
+    n8 = empty8(t, d)
+    mo.rms_norm(x, out8=n8)
+    clean()
+    for q in (z8, g8, u8, n8):
+        assert (q.codes[:, q.k:] == 0).all() and (q.scales[3] == 255).any()
+        assert (q.scales[[i for i in range(t) if i != 3]] != 255).all()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_a_block_that_is_no_number_stays_alone(bad):
     x = data(4, 100)
