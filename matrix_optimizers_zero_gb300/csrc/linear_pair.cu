@@ -491,11 +491,18 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
   p.cut = last * 2 > pairs || last == 0 ? 1 : !B_MN && last * 4 <= pairs ? 4 : 2;
   p.whole = int32_t(p.cut > 1 ? tiles - last : tiles);
   p.tiles = int32_t(p.cut > 1 ? tiles + last * (p.cut - 1) : tiles);
-  // Short reductions: with eight warps an epilogue takes longer than the products of a tile (8192 x 1280
-  // x 5120 with gelu and an 8-bit copy: 106 us, with sixteen 100). Long ones: the sixteen's waiting costs
-  // more than it gives (gated block 8192 x 4096 x 14336: 1775 and 1850 us).
-  const bool few = int64_t(p.blocks) * q.segments > 32;
-  auto kern = few ? linear_pair_kernel<EPI, A_MN, B_MN, 8> : linear_pair_kernel<EPI, A_MN, B_MN, kMostWarps>;
+  // Short reductions: with eight warps an epilogue takes longer than the products of a tile (8192 tokens,
+  // gelu_tanh and an 8-bit copy, 768 -> 3200: 48 us, with sixteen 37; 1280 -> 5120: 75 and 70). Long ones:
+  // the sixteen's waiting and the stage they cost are more than they give (1600 -> 6400: 107 and 109; 2048
+  // -> 8192: 168 and 176; gated block 8192 x 4096 x 14336: 1775 and 1850). Where sums only go out in bf16 it
+  // turns earlier (768 -> 3200: 28 and 28; 1280 -> 5120: 57 and 60). Gate and up take more registers than
+  // sixteen warps have (8192 x 1024 x 2816, both kept: 93, with sixteen 107); their gradients do not (131
+  // with sixteen, 134 with eight).
+  constexpr int kMost = EPI == kEpiGated ? 8 : kMostWarps;
+  bool light = EPI == kEpiLinear && q.act == MO_ACT_NONE && q.pre.data == nullptr;
+  for (int i = 0; i < q.count; ++i) light = light && p.t[i].bulk && p.t[i].add == nullptr;
+  const bool few = kMost == 8 || int64_t(p.blocks) * q.segments > (EPI == kEpiGatedGrad ? 32 : light ? 12 : 24);
+  auto kern = few ? linear_pair_kernel<EPI, A_MN, B_MN, 8> : linear_pair_kernel<EPI, A_MN, B_MN, kMost>;
   const size_t smem = few ? kSmem<8> : kSmem<kMostWarps>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
