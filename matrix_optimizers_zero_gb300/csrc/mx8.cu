@@ -76,42 +76,47 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict_
   }
 }
 
-// Rows that are not 16-byte aligned: a lane an element, a warp kOddBlocks blocks,
-// one behind the other, loaded together (1023 x 1283: 5.5 us, with one block 8.0).
-constexpr int kOddBlocks = 4;
+// Rows that are not 16-byte aligned: four neighbours a lane, element by element,
+// eight lanes a block, kOddBlocks blocks a lane, loaded together. (An element a lane
+// pays for the scale of its block each time: 16384 x 4097 bf16 143 us, so 63.)
+constexpr int kOddBlocks = 2;
 
-// f(q, block, row, first column) for the blocks from b0 on.
+// f(q, block, row, first column) for a lane's blocks: a warp's lie side by side.
 template <typename F>
 __device__ __forceinline__ void each_odd(int64_t b0, int64_t blocks, uint32_t nb, F&& f) {
-  int64_t row = b0 >> 32 == 0 ? int64_t(uint32_t(b0) / nb) : b0 / nb, at = b0 - row * nb;
+  int64_t row = b0 >> 32 == 0 ? int64_t(uint32_t(b0) / nb) : b0 / nb;
+  int64_t at = b0 - row * nb;
 #pragma unroll
   for (int q = 0; q < kOddBlocks; ++q) {
-    if (b0 + q >= blocks) break;
-    f(q, b0 + q, row, at * 32);
-    if (++at == nb) at = 0, ++row;
+    if (b0 + 4 * q < blocks) f(q, b0 + 4 * q, row, at * 32 + (threadIdx.x & 7u) * 4u);
+    for (at += 4; at >= nb; at -= nb) ++row;
   }
 }
+__device__ __forceinline__ int64_t first_odd() { return (global_thread() >> 5) * (4 * kOddBlocks) + ((threadIdx.x & 31u) >> 3); }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quantize_odd_kernel(const T* __restrict__ x, int64_t blocks, int64_t k, uint32_t nb,
                                                                 uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int lane = int(threadIdx.x & 31);
-  const int64_t b0 = (global_thread() >> 5) * kOddBlocks;
-  if (b0 >= blocks) return;
-  float v[kOddBlocks] = {};
+  const int64_t b0 = first_odd();
+  float v[kOddBlocks][4] = {};
   each_odd(b0, blocks, nb, [&](int q, int64_t, int64_t row, int64_t col) {
-    if (col + lane < k) v[q] = load1(x + row * k + col + lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i < k) v[q][i] = load1(x + row * k + col + i);
   });
 #pragma unroll
   for (int q = 0; q < kOddBlocks; ++q) {
-    if (b0 + q >= blocks) break;
-    // (magnitudes are in order as their words are, and NaN is above infinity)
-    const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v[q]))));
-    const uint32_t s = mx8_scale(top);
-    codes[(b0 + q) * 32 + lane] = uint8_t(cvt_e4m3x2(v[q] * mx8_down(s), 0.0f));
-    if (lane == 0) scales[b0 + q] = uint8_t(s);
+    float top = top2(top3(fabsf(v[q][0]), v[q][1], v[q][2]), fabsf(v[q][3]));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const int64_t b = b0 + 4 * q;
+    if (b >= blocks) continue;   // (whole groups of eight lanes)
+    const uint32_t s = mx8_scale(top), sub = threadIdx.x & 7u;
+    const float down = mx8_down(s);
+    reinterpret_cast<uint32_t*>(codes)[b * 8 + sub] = cvt_e4m3x4(v[q][0] * down, v[q][1] * down, v[q][2] * down, v[q][3] * down);
+    if (sub == 0) scales[b] = uint8_t(s);
   }
 }
 
@@ -214,22 +219,29 @@ __global__ void __launch_bounds__(kThreads) lay_out_kernel(const LayOutParams p)
     unpack_group<false>(t.src.data, nullptr, g, t.cols, per_row, t.out, t.ld);
 }
 
-// 8-bit codes into rows that are not 16-byte aligned: a lane an element, as above.
+// 8-bit codes into rows that are not 16-byte aligned, as above.
 template <typename O>
 __global__ void __launch_bounds__(kThreads) unpack_odd_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                               int64_t blocks, int64_t k, uint32_t nb, O* __restrict__ out) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();   // (after the wait: act_grad_kernel)
-  const int lane = int(threadIdx.x & 31);
-  const int64_t b0 = (global_thread() >> 5) * kOddBlocks;
-  if (b0 >= blocks) return;
-  uint8_t c[kOddBlocks], s[kOddBlocks];
-  each_odd(b0, blocks, nb, [&](int q, int64_t b, int64_t, int64_t) {
-    c[q] = codes[b * 32 + lane];
+  const int64_t b0 = first_odd();
+  uint32_t c[kOddBlocks] = {};
+  uint8_t s[kOddBlocks] = {};
+#pragma unroll
+  for (int q = 0; q < kOddBlocks; ++q) {
+    const int64_t b = b0 + 4 * q;
+    if (b >= blocks) break;
+    c[q] = reinterpret_cast<const uint32_t*>(codes)[b * 8 + (threadIdx.x & 7u)];
     s[q] = scales[b];
-  });
+  }
   each_odd(b0, blocks, nb, [&](int q, int64_t, int64_t row, int64_t col) {
-    if (col + lane < k) store1(out + row * k + col + lane, e4m3_value(c[q]) * mx8_up(s[q]));
+    float v[4];
+    e4m3x4_values(c[q], v);
+    const float up = mx8_up(s[q]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i < k) store1(out + row * k + col + i, v[i] * up);
   });
 }
 
@@ -412,7 +424,7 @@ unsigned blocks_of(int64_t threads) { return unsigned((threads + kThreads - 1) /
 
 unsigned quant_blocks(int64_t groups) { return unsigned((groups + kThreads * kQuantGroups - 1) / (kThreads * kQuantGroups)); }
 
-unsigned odd_blocks(int64_t blocks) { return blocks_of((blocks + kOddBlocks - 1) / kOddBlocks * 32); }
+unsigned odd_blocks(int64_t blocks) { return blocks_of((blocks + 4 * kOddBlocks - 1) / (4 * kOddBlocks) * 32); }
 
 template <typename T>
 cudaError_t quantize_as(const T* x, int64_t rows, int64_t k, const Kept& q, cudaStream_t stream) {
