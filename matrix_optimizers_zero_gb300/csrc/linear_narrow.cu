@@ -370,13 +370,16 @@ cudaError_t narrow_as(const Product& q, GemmParams& p, int sms, cudaStream_t str
     tiles += int64_t(t.tiles_m) * t.tiles_n;
   }
   p.tiles = int32_t(tiles);
-  // The reduction in as many parts as leave all clusters resident (clusters of 4 and 8 do not fill the
-  // GPU's parts evenly: 72 of 76 and 30 of 38 fit on 152 SMs, two CTAs an SM) and four stages a CTA.
+  // The reduction in as many parts as leave all clusters resident and four stages a CTA. Clusters of 4 and 8
+  // do not fill the GPU's parts evenly: with a CTA an SM (all its memory), 36 and 15 of 38 and 19 fit on 152
+  // SMs, with two twice as many. One cluster more than fit takes another round (512 x 512 over 4096 in 16
+  // clusters of 8: 15.8 us, two CTAs an SM 8).
   const int64_t per_sm = smem_of<EPI, NT>(kStages<EPI, NT>) <= 113 * 1024 ? 2 : 1;
-  const int64_t most[4] = {0, sms * per_sm / 2, sms * per_sm * 45 / 200, sms * per_sm * 18 / 200};
+  const int64_t fit[4] = {sms, sms / 2, sms * 45 / 200, sms * 18 / 200};
   unsigned parts = 1;
-  for (int i = 1; i < 4 && tiles <= most[i] && p.blocks * q.segments >= (4 << i); ++i) parts = 1u << i;
-  p.stages = tiles * parts <= sms ? kDeep<EPI, NT> : kStages<EPI, NT>;
+  int log = 0;
+  for (int i = 1; i < 4 && tiles <= fit[i] * per_sm && p.blocks * q.segments >= (4 << i); ++i) parts = 1u << i, log = i;
+  p.stages = tiles <= fit[log] ? kDeep<EPI, NT> : kStages<EPI, NT>;
   auto kern = linear_narrow_kernel<EPI, Q_MN, P_MN, NT>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem_of<EPI, NT>(kDeep<EPI, NT>));
   if (e != cudaSuccess) return e;

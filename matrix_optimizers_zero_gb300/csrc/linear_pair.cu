@@ -524,8 +524,10 @@ bool encode_operand(CUtensorMap* map, const Operand& o, uint32_t box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Few rows, or a long reduction and fewer tiles than half of the pairs: the reduction is split. (128
-// rows: 4096 -> 14336 29 us by the other kernel and 27 by pairs, which have 56 tiles.)
+// Few rows, or few tiles and a reduction that is worth splitting: 16 blocks of 64 for each, and twice the
+// tiles where they are more (us by pairs and by the other kernel: 1 to 8 tiles over 512 6 and 8, over 1024 7 and
+// 7, over 2048 11 and 7 to 9; 16 tiles over 1024 8 and 10, over 2048 12 and 11; 32 over 2048 13 and 14, over
+// 8192 37 and 34).
 bool is_narrow(const Product& q, int sms) {
   int64_t pair_tiles = 0, rows = 0;
   for (int i = 0; i < q.count; ++i) {
@@ -533,7 +535,8 @@ bool is_narrow(const Product& q, int sms) {
     pair_tiles += ((t.m + 255) / 256) * (q.epi == kEpiGated ? (t.n + 127) / 128 : (t.n + 255) / 256);
     rows = std::max(rows, t.m);
   }
-  return (rows <= 64 && !q.a_mn) || (pair_tiles * 2 < sms / 2 && (q.k + kBlockK - 1) / kBlockK * q.segments >= 16);
+  const int64_t blocks = (q.k + kBlockK - 1) / kBlockK * q.segments;
+  return (rows <= 64 && !q.a_mn) || (pair_tiles * 2 < sms / 2 && blocks >= std::max<int64_t>(16, 2 * pair_tiles));
 }
 
 cudaError_t launch_product(const Product& q, int sms, int* status, cudaStream_t stream) {
