@@ -66,6 +66,30 @@ def test_gated_ffn_grad_tiles(t, d, f, activation, save, mx8, dtype, accumulate)
     base.test_gated_ffn_grad(t, d, f, activation, save, mx8, dtype, accumulate)
 
 
+# Reductions that are split: clusters of 2, 4 and 8, one and two CTAs an SM, every operand order.
+
+@pytest.mark.parametrize("t,k,n,activation,bias,residual,pre,mx8,out", [
+    (500, 2112, 520, "silu", True, True, "bf16", False, BF16), (300, 4100, 1000, None, False, True, None, False, F32),
+    (1000, 1604, 700, "gelu_tanh", True, False, "mx8", False, BF16), (1300, 4200, 1100, "relu", False, False, "mx8", False, F32),
+    (72, 8200, 2050, None, True, True, None, False, BF16), (128, 1100, 1030, "silu", False, False, "mx8", False, BF16)])
+def test_linear_splits(t, k, n, activation, bias, residual, pre, mx8, out):
+    base.test_linear(t, k, n, activation, bias, residual, pre, mx8, out)
+
+
+@pytest.mark.parametrize("t,k,n,activation,pre,mx8,dtype,accumulate", [
+    (2100, 500, 520, "silu", "bf16", False, BF16, True), (4100, 300, 1001, None, None, False, F32, True),
+    (140, 1030, 4200, "relu", "bf16", False, BF16, False)])
+def test_linear_grad_splits(t, k, n, activation, pre, mx8, dtype, accumulate):
+    base.test_linear_grad(t, k, n, activation, pre, mx8, dtype, accumulate)
+
+
+@pytest.mark.parametrize("t,d,f", [(200, 2112, 700), (130, 1100, 1500), (90, 4104, 264)])
+def test_gated_ffn_splits(t, d, f):
+    base.test_gated_ffn(t, d, f, "silu", True, "mx8", False, BF16)
+    base.test_gated_ffn(t, d, f, "gelu_tanh", False, "bf16", False, F32)
+    base.test_gated_ffn_grad(t, d, f, "silu", "bf16", False, BF16, True)
+
+
 # One and two rows, which have a kernel of their own where nothing is kept: reductions that end inside a
 # warp's pieces, columns past every warp's first, the longest rows it takes and longer ones.
 
