@@ -447,8 +447,9 @@ int mx8_dequantize(const mo_tensor* q, int64_t rows, int64_t k, void* out, int32
  *   y = s / sqrt(mean(s^2) + eps) * weight
  * x, residual (or NULL) and sum (s is stored there; or NULL) have `dtype`; y
  * goes to out (`out_dtype`), to out8 in 8 bits, or to both; either may be NULL.
- * weight is fp32 [dim], or NULL for ones. s is not rounded in between. sum and
- * out may each be x or residual itself. rows up to 2^30, dim up to 2^22. */
+ * weight is fp32 [dim], or NULL for ones. s is not rounded in between; s^2 is
+ * summed in fp32, and a row whose sum is infinite there gives zeros. sum and out
+ * may each be x or residual itself. rows up to 2^30, dim up to 2^22. */
 int rms_norm(const void* x, const void* residual, int32_t dtype, int64_t rows, int64_t dim, const float* weight, float eps,
              void* sum, void* out, int32_t out_dtype, const mo_tensor* out8, cudaStream_t stream);
 

@@ -555,6 +555,127 @@ __global__ void __launch_bounds__(kLong) norm_grad_long_kernel(const NormGradPar
   }
 }
 
+// The same where rows are 16-byte aligned: eight neighbours a thread.
+constexpr int kLongStep = kLong * 8;
+
+template <typename T>
+__device__ __forceinline__ void sum8(const T* x, const T* res, float (&s)[8]) {
+  load8(x, s);
+  if (res != nullptr) {
+    float r[8];
+    load8(res, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += r[i];
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLong) norm_long_vec_kernel(const NormParams p) {
+  __shared__ float shared[2][64];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t at = int64_t(blockIdx.x) * p.dim, nb = (p.dim + 31) / 32;
+  const T* x = static_cast<const T*>(p.x) + at;
+  const T* res = p.residual != nullptr ? static_cast<const T*>(p.residual) + at : nullptr;
+  float squares = 0.0f;
+#pragma unroll 2
+  for (int64_t c = threadIdx.x * 8; c < p.dim; c += kLongStep) {
+    float s[8];
+    sum8(x + c, res != nullptr ? res + c : nullptr, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) squares = fmaf(s[i], s[i], squares);
+  }
+  const float r = inverse_rms(team_sums<kLong>(squares, 0.0f, shared, 0).x, 1.0f / float(p.dim), p.eps);
+  for (int64_t first = 0; first < nb * 32; first += kLongStep) {   // (whole warps: a block of 32 is four lanes)
+    const int64_t c = first + threadIdx.x * 8;
+    float y[8] = {};
+    if (c < p.dim) {
+      sum8(x + c, res != nullptr ? res + c : nullptr, y);
+      if (p.sum != nullptr) store8(static_cast<T*>(p.sum) + at + c, y);
+      float w[8];
+      if (p.weight != nullptr) load8(p.weight + c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = p.weight != nullptr ? y[i] * r * w[i] : y[i] * r;
+      if (p.out != nullptr) {
+        if (p.out_bf16)
+          store8(static_cast<uint16_t*>(p.out) + at + c, y);
+        else
+          store8(static_cast<float*>(p.out) + at + c, y);
+      }
+    }
+    if (p.out8.data != nullptr)
+      store_row_mx8<kLong, 8, true>(static_cast<uint8_t*>(p.out8.data) + int64_t(blockIdx.x) * nb * 32 + first,
+                                    p.out8.scales + int64_t(blockIdx.x) * nb + (first >> 5), nb * 32 - first, int(threadIdx.x), y);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLong) norm_grad_long_vec_kernel(const NormGradParams p) {
+  __shared__ float shared[2][64];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t nb = (p.dim + 31) / 32;
+  float* part = p.part != nullptr ? p.part + int64_t(blockIdx.x) * p.dim : nullptr;
+  const float inv_dim = 1.0f / float(p.dim);
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t at = row * p.dim;
+    const T* dy = static_cast<const T*>(p.dy) + at;
+    // x, dy and g = dy w of eight columns
+    auto fetch = [&](int64_t c, float (&s)[8], float (&d)[8], float (&g)[8]) {
+      if (p.x.dtype == MO_MX8) {
+        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x.data) + row * nb * 32 + c);
+        const float up = mx8_up(p.x.scales[row * nb + (c >> 5)]);
+        e4m3x4_values(q.x, *reinterpret_cast<float (*)[4]>(&s[0]));
+        e4m3x4_values(q.y, *reinterpret_cast<float (*)[4]>(&s[4]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] *= up;
+      } else {
+        load8(static_cast<const T*>(p.x.data) + at + c, s);
+      }
+      load8(dy + c, d);
+      if (p.weight != nullptr) load8(p.weight + c, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = p.weight != nullptr ? d[i] * g[i] : d[i];
+    };
+    float squares = 0.0f, dot = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < p.dim; c += kLongStep) {
+      float s[8], d[8], g[8];
+      fetch(c, s, d, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        squares = fmaf(s[i], s[i], squares);
+        dot = fmaf(g[i], s[i], dot);
+      }
+    }
+    const float2 sums = team_sums<kLong>(squares, dot, shared, parity);
+    parity ^= 1;
+    const float r = inverse_rms(sums.x, inv_dim, p.eps);
+    const float m = sums.y * r * inv_dim;
+    for (int64_t c = threadIdx.x * 8; c < p.dim; c += kLongStep) {   // a column is one thread's: no order to keep
+      float s[8], d[8], g[8];
+      fetch(c, s, d, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] *= r;
+      if (part != nullptr) {
+        float q[8] = {};
+        if (row != int64_t(blockIdx.x)) load8(part + c, q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = fmaf(d[i], s[i], q[i]);
+        store8(part + c, q);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = r * fmaf(-s[i], m, g[i]);
+      if (p.dres != nullptr) {
+        load8(static_cast<const T*>(p.dres) + at + c, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] += g[i];
+      }
+      store8(static_cast<T*>(p.dx) + at + c, d);
+    }
+  }
+}
+
 // Threads of the team that takes rows of `dim` elements, eight a thread; 0: rows
 // that no team holds.
 int team_of(int64_t dim) { return dim <= 256 ? 32 : dim <= 1024 ? 128 : dim <= 2048 ? 256 : dim <= 4096 ? 512 : dim <= 8192 ? 1024 : 0; }
@@ -580,7 +701,7 @@ cudaError_t with_team(int64_t dim, F&& f) {
 template <typename T>
 cudaError_t norm_as(const NormParams& p, cudaStream_t stream) {
   if (team_of(p.dim) == 0)
-    return launch_kernel(norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(kLong), 0, 1, true, stream, p);
+    return launch_kernel(p.dim % 8 == 0 ? norm_long_vec_kernel<T> : norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(kLong), 0, 1, true, stream, p);
   return with_team(p.dim, [&](auto team) {
     constexpr int TEAM = decltype(team)::value, kTeams = kBlock<TEAM> / TEAM;
     if (p.dim % 8 != 0)
@@ -598,7 +719,7 @@ template <typename T, bool MX8>
 cudaError_t norm_grad_as(const NormGradParams& p, cudaStream_t stream) {
   const int64_t teams = norm_parts(p.rows, p.dim);
   if (team_of(p.dim) == 0)
-    return launch_kernel(norm_grad_long_kernel<T>, dim3(unsigned(teams)), dim3(kLong), 0, 1, true, stream, p);
+    return launch_kernel(p.dim % 8 == 0 ? norm_grad_long_vec_kernel<T> : norm_grad_long_kernel<T>, dim3(unsigned(teams)), dim3(kLong), 0, 1, true, stream, p);
   return with_team(p.dim, [&](auto team) {
     constexpr int TEAM = decltype(team)::value, kTeams = kBlock<TEAM> / TEAM;
     const dim3 grid(unsigned(teams / kTeams));

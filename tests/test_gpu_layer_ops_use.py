@@ -107,6 +107,21 @@ def test_gated_block_of_one_and_two_rows(t, d, f, activation, residual, mx8, out
     base.test_gated_ffn(t, d, f, activation, residual, None, mx8, out)
 
 
+# Rows that no team of threads holds, aligned and not; more of them than blocks, so that a block's rows add up.
+
+@pytest.mark.parametrize("dim", [8193, 8200, 12288, 16392, 40001])
+@pytest.mark.parametrize("dtype,out,residual,mx8", [(BF16, BF16, True, True), (F32, None, False, True)])
+def test_long_rows(dim, dtype, out, residual, mx8):
+    base.test_norm(dim, dtype, out, residual, mx8)
+    base.test_norm_in_place(dim, dtype)
+
+
+@pytest.mark.parametrize("rows,dim", [(3, 16392), (700, 8200), (650, 8195)])
+@pytest.mark.parametrize("dtype,mx8", [(BF16, True), (BF16, False), (F32, True)])
+def test_gradients_of_long_rows(rows, dim, dtype, mx8):
+    base.test_norm_grad(rows, dim, dtype, mx8, True, rows == 700)
+
+
 # ---------------------------------------------------------------- sums that are cut, offsets past 32 bits
 
 @pytest.mark.parametrize("t,k,n,accumulate", [(40000, 24, 40, True), (70001, 33, 17, False), (32769, 8, 8, True)])
