@@ -375,9 +375,9 @@ cudaError_t narrow_as(const Product& q, GemmParams& p, int sms, cudaStream_t str
   // The reduction in as many parts as leave all clusters resident and four stages a CTA. Clusters of 4 and 8
   // do not fill the GPU's parts evenly: with a CTA an SM (all its memory), 36 and 15 of 38 and 19 fit on 152
   // SMs, with two twice as many. One cluster more than fit takes another round (512 x 512 over 4096 in 16
-  // clusters of 8: 15.8 us, two CTAs an SM 8).
+  // clusters of 8: 15.8 us, with two CTAs an SM 10.3).
   const int64_t per_sm = smem_of<EPI, NT>(kStages<EPI, NT>) <= 113 * 1024 ? 2 : 1;
-  const int64_t fit[4] = {sms, sms / 2, sms * 45 / 200, sms * 18 / 200};
+  const int64_t fit[4] = {sms, sms / 2, sms * 47 / 200, sms * 18 / 200};
   unsigned parts = 1;
   int log = 0;
   for (int i = 1; i < 4 && tiles <= fit[i] * per_sm && p.blocks * q.segments >= (4 << i); ++i) parts = 1u << i, log = i;

@@ -524,19 +524,23 @@ bool encode_operand(CUtensorMap* map, const Operand& o, uint32_t box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Few rows, or few tiles and a reduction that is worth splitting: 16 blocks of 64 for each, and twice the
-// tiles where they are more (us by pairs and by the other kernel: 1 to 8 tiles over 512 6 and 8, over 1024 7 and
-// 7, over 2048 11 and 7 to 9; 16 tiles over 1024 8 and 10, over 2048 12 and 11; 32 over 2048 13 and 14, over
-// 8192 37 and 34).
+// Few rows, or few tiles and a reduction that is worth splitting: 16 blocks of 64, and half of the other
+// kernel's tiles where they are more (us by pairs and by the other kernel: 512 x 512 over 512 6 and 8, over
+// 1024 7 and 7, over 2048 11 and 9; 1024 x 1024 over 1024 8 and 10, over 2048 12 and 11; 1024 x 2048 over
+// 2048 13 and 14, over 8192 37 and 34). Rows that are not 16-byte aligned take pairs longer to store: 777 x
+// 515 over 1024 9 and 8, with a residual 15 and 9.
 bool is_narrow(const Product& q, int sms) {
-  int64_t pair_tiles = 0, rows = 0;
+  int64_t pair_tiles = 0, tiles = 0, rows = 0;
+  bool odd = false;
   for (int i = 0; i < q.count; ++i) {
     const Target& t = q.t[i];
     pair_tiles += ((t.m + 255) / 256) * (q.epi == kEpiGated ? (t.n + 127) / 128 : (t.n + 255) / 256);
+    tiles += ((t.m + 127) / 128) * ((t.n + 127) / 128);
     rows = std::max(rows, t.m);
+    odd = odd || t.ld % (t.out_bf16 ? 8 : 4) != 0;
   }
   const int64_t blocks = (q.k + kBlockK - 1) / kBlockK * q.segments;
-  return (rows <= 64 && !q.a_mn) || (pair_tiles * 2 < sms / 2 && blocks >= std::max<int64_t>(16, 2 * pair_tiles));
+  return (rows <= 64 && !q.a_mn) || (pair_tiles * 2 < sms / 2 && blocks >= std::max<int64_t>(16, odd ? 0 : tiles / 2));
 }
 
 cudaError_t launch_product(const Product& q, int sms, int* status, cudaStream_t stream) {
