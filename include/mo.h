@@ -413,7 +413,8 @@ int fp4_product(const mo_fp4* a, const mo_fp4* b, void* out, int32_t dtype, cuda
  * everything around them in their epilogues, 8-bit activation checkpoints.
  * Weights and activations of products are bf16, sums fp32; what is kept for
  * the backward pass is bf16 or 8 bits. No call needs another's workspace or
- * state; a workspace may be shared by calls in stream order. */
+ * state; a workspace may be shared by calls in stream order, and one made for
+ * more tokens (rows of the norm) serves calls of fewer. */
 
 /* A tensor [rows, k] of a call, in one of
  *   MO_F32, MO_BF16   data: the elements, dense; scales NULL

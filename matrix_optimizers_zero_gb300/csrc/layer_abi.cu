@@ -190,12 +190,12 @@ int ffn_shape(int64_t tokens, int64_t dim, int64_t inner) {
   return tokens > 0 && most > kMaxElems / tokens ? MO_ERR_BAD_SHAPE : MO_OK;
 }
 
+// (No less for more tokens: a workspace of the largest batch serves the others.)
 size_t linear_bytes(int64_t tokens, int64_t cols, int64_t rows, bool grad) {
   size_t b = copy_bytes(tokens, cols) + (cols % 8 != 0 ? copy_bytes(rows, cols) : 0);
   if (grad) {
     b += copy_bytes(tokens, rows);   // dz
-    const int64_t per = mo::act_grad_per(tokens, rows);
-    b += align256(size_t((tokens + per - 1) / per) * size_t(rows) * 4);
+    b += align256(size_t(mo::act_grad_room(tokens, rows)) * size_t(rows) * 4);
     b += std::max(slice_bytes(tokens, rows, cols), slice_bytes(rows, tokens, cols));
   }
   return std::max<size_t>(b, 256);

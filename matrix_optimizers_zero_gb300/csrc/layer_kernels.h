@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "mo.h"
@@ -57,14 +58,18 @@ cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream);
 // out[i] (+)= the sum over part[0..parts)[i], in order.
 cudaError_t launch_join(const float* part, int64_t parts, int64_t n, float* out, bool accumulate, cudaStream_t stream);
 
-// Tokens that a block of launch_act_grad takes: at most 608 parts (four blocks
-// an SM at 152, a number that does not depend on the device), a multiple of 8
-// each. A block is 256 columns wide, so few parts do for wide rows.
+// Parts of launch_act_grad at most: 608 blocks (four an SM at 152, a number that
+// does not depend on the device). A block is 256 columns wide, so few parts do for
+// wide rows.
+inline int64_t act_grad_most(int64_t rows) { return std::max<int64_t>(1, 608 / ((rows + 255) / 256)); }
+// Tokens that a block takes, a multiple of 8.
 inline int64_t act_grad_per(int64_t tokens, int64_t rows) {
-  const int64_t strips = (rows + 255) / 256;
-  const int64_t parts = std::max<int64_t>(1, 608 / strips);
+  const int64_t parts = act_grad_most(rows);
   return std::max<int64_t>(8, ((tokens + parts - 1) / parts + 7) / 8 * 8);
 }
+// Parts that `tokens` or fewer need: more than `tokens` make where their blocks have
+// just grown (4865 tokens of 256 columns: 305 parts, 4864: 608).
+inline int64_t act_grad_room(int64_t tokens, int64_t rows) { return std::min((tokens + 7) / 8, act_grad_most(rows)); }
 
 // ---------------------------------------------------------------- norm
 struct NormParams {
