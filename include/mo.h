@@ -474,7 +474,7 @@ enum mo_activation { MO_ACT_NONE = 0, MO_ACT_RELU = 1, MO_ACT_GELU = 2, MO_ACT_G
 /* z = x w^T + bias, out = act(z) + residual, in one launch.
  *   x [tokens, cols] bf16 or 8 bits; w bf16 [rows, cols]; bias fp32 [rows] or
  *   NULL; residual (or NULL) and out [tokens, rows] of `out_dtype`, out may be
- *   residual itself; pre (or NULL; with an activation only): receives z
+ *   residual itself (unless that is x too: x is read by all tiles); pre (or NULL; with an activation only): receives z
  *   [tokens, rows] for the backward pass, in bf16 or 8 bits
  * tokens up to 2^30, cols up to 2^16, rows up to 2^22. ws: device scratch of
  * mo_linear_workspace_bytes(.., 0) bytes, 256-byte aligned: 8-bit operands, and
@@ -502,7 +502,7 @@ int linear_grad(const void* dout, const mo_tensor* x, const void* w, int64_t tok
  * is in the workspace).
  *   x [tokens, dim] bf16 or 8 bits; w_gate, w_up bf16 [inner, dim], w_down bf16
  *   [dim, inner]; residual (or NULL) and out [tokens, dim] of `out_dtype`, out
- *   may be residual itself; gate, up (both or neither, of one type): receive g
+ *   may be residual itself, also where that is x; gate, up (both or neither, of one type): receive g
  *   and u [tokens, inner] for the backward pass, in bf16 or 8 bits
  * tokens up to 2^30, dim up to 2^16, inner up to 2^15. */
 size_t mo_gated_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t inner, int32_t grad);

@@ -36,28 +36,33 @@ int matrix_shape(int64_t rows, int64_t k) {
 }
 
 // Memory that a call touches; a range that is written may overlap no other, but
-// be one that it was given to replace.
+// be one that it was given to replace. Operands of a product are read whole, by
+// tiles that write other places: the product's output replaces none of them,
+// whatever else was given at the same address.
 struct Range {
   const void* p;
   size_t bytes;
-  bool written;
+  bool written, operand;
   const void* in_place[2];   // ranges that may begin at the same place
 };
 struct Ranges {
   Range r[24];
   int n = 0;
-  void add(const void* p, size_t bytes, bool written, const void* same0 = nullptr, const void* same1 = nullptr) {
-    if (p != nullptr && bytes > 0) r[n++] = {p, bytes, written, {same0, same1}};
+  void add(const void* p, size_t bytes, bool written, bool operand, const void* same0 = nullptr, const void* same1 = nullptr) {
+    if (p != nullptr && bytes > 0) r[n++] = {p, bytes, written, operand, {same0, same1}};
   }
-  void reads(const void* p, size_t bytes) { add(p, bytes, false); }
-  void writes(const void* p, size_t bytes, const void* same0 = nullptr, const void* same1 = nullptr) { add(p, bytes, true, same0, same1); }
-  void kept(const mo_tensor* t, int64_t rows, int64_t k, bool written) {
+  void reads(const void* p, size_t bytes) { add(p, bytes, false, false); }
+  void operand(const void* p, size_t bytes) { add(p, bytes, false, true); }
+  void writes(const void* p, size_t bytes, const void* same0 = nullptr, const void* same1 = nullptr) {
+    add(p, bytes, true, false, same0, same1);
+  }
+  void kept(const mo_tensor* t, int64_t rows, int64_t k, bool written, bool operand = false) {
     if (t == nullptr) return;
     if (t->dtype == MO_MX8) {
-      add(t->data, size_t(rows) * size_t(mo::mx8_blocks(k)) * 32, written);
-      add(t->scales, size_t(rows) * size_t(mo::mx8_blocks(k)), written);
+      add(t->data, size_t(rows) * size_t(mo::mx8_blocks(k)) * 32, written, operand);
+      add(t->scales, size_t(rows) * size_t(mo::mx8_blocks(k)), written, operand);
     } else {
-      add(t->data, size_t(rows) * size_t(k) * bytes_of(t->dtype), written);
+      add(t->data, size_t(rows) * size_t(k) * bytes_of(t->dtype), written, operand);
     }
   }
   int check() const {
@@ -66,7 +71,7 @@ struct Ranges {
         if (i == j || !r[i].written) continue;
         const uintptr_t x = reinterpret_cast<uintptr_t>(r[i].p), y = reinterpret_cast<uintptr_t>(r[j].p);
         if (!(x < y + r[j].bytes && y < x + r[i].bytes)) continue;
-        const bool same = x == y && r[i].bytes == r[j].bytes && !r[j].written && (r[i].in_place[0] == r[j].p || r[i].in_place[1] == r[j].p);
+        const bool same = x == y && r[i].bytes == r[j].bytes && !r[j].written && !r[j].operand && (r[i].in_place[0] == r[j].p || r[i].in_place[1] == r[j].p);
         if (!same) return MO_ERR_OVERLAP;
       }
     return MO_OK;
@@ -388,8 +393,8 @@ int linear_forward(const mo_tensor* x, const void* w, int64_t tokens, int64_t co
   const size_t need = linear_bytes(tokens, cols, rows, false), out_bytes = size_t(tokens) * size_t(rows) * bytes_of(out_dtype);
   if (ws_bytes < need) return MO_ERR_WORKSPACE_TOO_SMALL;
   Ranges mem;
-  mem.kept(x, tokens, cols, false);
-  mem.reads(w, size_t(rows) * size_t(cols) * 2);
+  mem.kept(x, tokens, cols, false, true);
+  mem.operand(w, size_t(rows) * size_t(cols) * 2);
   mem.reads(bias, size_t(rows) * 4);
   mem.reads(residual, out_bytes);
   mem.kept(pre, tokens, rows, true);
@@ -528,8 +533,8 @@ int gated_ffn_forward(const mo_tensor* x, const void* w_gate, const void* w_up, 
   const size_t need = ffn_bytes(tokens, dim, inner, false), out_bytes = size_t(tokens) * size_t(dim) * bytes_of(out_dtype);
   if (ws_bytes < need) return MO_ERR_WORKSPACE_TOO_SMALL;
   Ranges mem;
-  mem.kept(x, tokens, dim, false);
-  for (const void* p : {w_gate, w_up, w_down}) mem.reads(p, size_t(inner) * size_t(dim) * 2);
+  mem.kept(x, tokens, dim, false);   // (out may replace it as the residual: the launch that writes out does not read x)
+  for (const void* p : {w_gate, w_up, w_down}) mem.operand(p, size_t(inner) * size_t(dim) * 2);
   mem.reads(residual, out_bytes);
   mem.kept(gate, tokens, inner, true);
   mem.kept(up, tokens, inner, true);

@@ -300,7 +300,7 @@ def linear_workspace(tokens: int, cols: int, rows: int, grad: bool = False, devi
 def linear(x, w, out, bias=None, activation=None, residual=None, pre=None, workspace=None, stream=None) -> None:
     """out = act(x w^T + bias) + residual, in one launch: x bf16 or an Mx8Tensor
     [tokens, cols], w bf16 [rows, cols], bias fp32, out (fp32 or bf16) and residual
-    of one type (out may be residual). pre: bf16 or an Mx8Tensor [tokens, rows]
+    of one type (out may be residual, but not x). pre: bf16 or an Mx8Tensor [tokens, rows]
     that receives x w^T + bias for linear_grad."""
     here = _here()
     act = _act(activation)
@@ -389,7 +389,7 @@ def gated_ffn(x, w_gate, w_up, w_down, out, activation="silu", residual=None, ga
               stream=None) -> None:
     """out = (act(x w_gate^T) * (x w_up^T)) w_down^T + residual: x bf16 or an
     Mx8Tensor [tokens, dim], bf16 weights [inner, dim] and [dim, inner], out (fp32
-    or bf16) and residual of one type (out may be residual). gate and up: bf16 or
+    or bf16) and residual of one type (out may be residual, and both x). gate and up: bf16 or
     Mx8Tensors [tokens, inner] that receive the two projections for gated_ffn_grad."""
     here = _here()
     act = _act(activation)

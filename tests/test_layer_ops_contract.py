@@ -1,9 +1,26 @@
 """What callers of the feed-forward operators rely on beyond a single call's
 values (no GPU needed)."""
+import ctypes
+
 import pytest
+import torch
 
 import matrix_optimizers_zero_gb300 as mo
 from matrix_optimizers_zero_gb300 import build as mo_build
+from matrix_optimizers_zero_gb300.layer_ops import MoTensor
+
+NULL, SHAPE, ALIGN, PARAM, WS, OVERLAP = -1, -2, -3, -4, -5, -6
+F32, BF16, MX8 = 0, 1, 2
+A, B, C, D, E, F = (0x100000000 * k for k in range(1, 7))   # far apart, aligned, never read
+BIG = 1 << 30
+
+
+def ten(data):
+    return MoTensor(data, None, BF16)
+
+
+def ref(t):
+    return ctypes.byref(t)
 
 
 @pytest.fixture(scope="module")
@@ -44,3 +61,41 @@ def test_a_gradient_workspace_serves_the_forward_pass(lib, tokens, cols, rows):
     assert mo.mo_linear_workspace_bytes(tokens, cols, rows, grad=True) >= mo.mo_linear_workspace_bytes(tokens, cols, rows)
     dim, inner = cols, min(rows, 32768)
     assert mo.mo_gated_ffn_workspace_bytes(tokens, dim, inner, grad=True) >= mo.mo_gated_ffn_workspace_bytes(tokens, dim, inner)
+
+
+# ---------------------------------------------------------------- in place
+
+@pytest.mark.parametrize("act", [0, 4])
+@pytest.mark.parametrize("t,k,n,kw", [
+    (8, 64, 64, dict(x=ten(A), res=A, out=A)),            # s += s w^T: other tiles read s
+    (8, 63, 63, dict(x=ten(A), res=A, out=A)),
+    (64, 64, 32, dict(w=A, res=A, out=A)),                # 64 tokens of 32 are as long as the weight
+    (300, 1000, 1000, dict(x=ten(A), res=A, out=A)),
+])
+def test_a_product_does_not_replace_its_operands(lib, t, k, n, kw, act):
+    a = dict(dict(x=ten(B), w=C, res=None, out=D), **kw)
+    got = lib.linear_forward(ref(a["x"]), a["w"], t, k, n, None, act, a["res"], None, a["out"], BF16, E, BIG, None)
+    assert got == OVERLAP
+
+
+@pytest.mark.parametrize("w", ["wg", "wu", "wd"])
+def test_a_gated_block_does_not_replace_its_weights(lib, w):
+    a = dict(dict(wg=B, wu=C, wd=D), **{w: A})
+    t, d, f = 96, 64, 96                                  # 96 tokens of 64 are as long as a weight
+    assert lib.gated_ffn_forward(ref(ten(E)), a["wg"], a["wu"], a["wd"], t, d, f, 4, A, None, None, A, BF16, F, BIG, None) == OVERLAP
+
+
+def test_in_place_calls_pass_the_checks(lib):
+    """What is read and written by the same threads, or by different launches, is no overlap: these calls go on
+    to the device."""
+    def passes(st):
+        assert st not in (NULL, SHAPE, ALIGN, PARAM, WS, OVERLAP), st
+
+    if torch.cuda.is_available():
+        pytest.skip("addresses that nothing stands behind")
+    passes(lib.linear_forward(ref(ten(A)), B, 8, 64, 32, None, 0, C, None, C, BF16, D, BIG, None))
+    passes(lib.gated_ffn_forward(ref(ten(A)), B, C, D, 8, 64, 96, 4, E, None, None, E, BF16, F, BIG, None))
+    passes(lib.gated_ffn_forward(ref(ten(A)), B, C, D, 8, 64, 96, 4, A, None, None, A, BF16, F, BIG, None))
+    passes(lib.rms_norm(A, B, BF16, 4, 40, C, 1e-6, B, A, BF16, None, None))
+    passes(lib.rms_norm_grad(A, BF16, ref(ten(B)), 4, 40, C, 1e-6, D, A, E, 0, F, BIG, None))
+    passes(lib.rms_norm_grad(A, BF16, ref(ten(B)), 4, 40, C, 1e-6, D, D, E, 0, F, BIG, None))
