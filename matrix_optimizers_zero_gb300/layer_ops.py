@@ -94,8 +94,8 @@ def _here() -> int:
     global _dtypes, _current_device
     if _dtypes is None:
         import torch
-        _dtypes = {torch.float32: MO_F32, torch.bfloat16: MO_BF16}
         _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _dtypes = {torch.float32: MO_F32, torch.bfloat16: MO_BF16}   # last: another thread that sees it finds both
     return _current_device()
 
 

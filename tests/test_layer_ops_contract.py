@@ -1,12 +1,14 @@
 """What callers of the feed-forward operators rely on beyond a single call's
 values (no GPU needed)."""
 import ctypes
+import threading
 
 import pytest
 import torch
 
 import matrix_optimizers_zero_gb300 as mo
 from matrix_optimizers_zero_gb300 import build as mo_build
+from matrix_optimizers_zero_gb300 import layer_ops
 from matrix_optimizers_zero_gb300.layer_ops import MoTensor
 
 NULL, SHAPE, ALIGN, PARAM, WS, OVERLAP = -1, -2, -3, -4, -5, -6
@@ -99,3 +101,24 @@ def test_in_place_calls_pass_the_checks(lib):
     passes(lib.rms_norm(A, B, BF16, 4, 40, C, 1e-6, B, A, BF16, None, None))
     passes(lib.rms_norm_grad(A, BF16, ref(ten(B)), 4, 40, C, 1e-6, D, A, E, 0, F, BIG, None))
     passes(lib.rms_norm_grad(A, BF16, ref(ten(B)), 4, 40, C, 1e-6, D, D, E, 0, F, BIG, None))
+
+
+# ---------------------------------------------------------------- threads
+
+def test_a_second_thread_may_make_its_first_call_beside_the_first(monkeypatch):
+    """What a call looks up once is complete for every thread that finds it: the second thread comes while the
+    first one is looking up."""
+    monkeypatch.setattr(layer_ops, "_dtypes", None)
+    monkeypatch.setattr(layer_ops, "_current_device", None)
+    seen, inside = [], []
+
+    def lookup(obj, name, *default):
+        if not inside:
+            inside.append(True)
+            t = threading.Thread(target=lambda: seen.append(layer_ops._here()))
+            t.start()
+            t.join()
+        return lambda: 5
+
+    monkeypatch.setattr(layer_ops, "getattr", lookup, raising=False)
+    assert layer_ops._here() == 5 and seen == [5]
