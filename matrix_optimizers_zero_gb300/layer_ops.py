@@ -29,6 +29,7 @@ adamw_tail_step. A GPT-2 style block is two calls of `linear`:
 from __future__ import annotations
 
 import ctypes
+import math
 
 from . import _check, load_library
 from .train_ops import MO_BF16, MO_F32, _dense, _stream_ptr
@@ -115,16 +116,30 @@ def _plain(t, name: str, here: int):
     return t.data_ptr(), code
 
 
-def _typed(t, name: str, here: int, code: int, numel: int):
-    """Pointer of a tensor that must have a type and a size; None for none."""
+def _sized(t, shape, name: str):
+    """Refuses a tensor of another size than `shape`, or one that lies as the transposed matrix does. Views of
+    the same rows ([batch, tokens, heads, width of a head] or all in one dimension) are as good as
+    [tokens, width]."""
+    numel, ends, at = math.prod(shape), {1}, 1
+    if t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements")
+    for n in t.shape:
+        at *= n
+        ends.add(at)
+    if len(shape) > 1 and shape[-1] in ends and numel // max(shape[-1], 1) not in ends:
+        raise ValueError(f"{name} must be {list(shape)}, not its transpose")
+
+
+def _typed(t, name: str, here: int, code: int, shape):
+    """Pointer of a tensor that must have a type and a shape; None for none."""
     if t is None:
         return None
     if _dtypes.get(t.dtype) != code:
         raise TypeError(f"{name} must be {'bf16' if code == MO_BF16 else 'fp32'}")
     if t.get_device() != here or not t.is_contiguous():
         _refuse(t, name, here, "")
-    if t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} elements")
+    if t.shape != shape:
+        _sized(t, shape, name)
     return t.data_ptr()
 
 
@@ -172,13 +187,13 @@ def _kept_rows(t, width: int, rows: int, name: str, here: int, f32: bool = False
     return _kept(t, name, here, f32)
 
 
-def _result(t, numel: int, name: str, here: int):
+def _result(t, shape, name: str, here: int):
     """Pointer and type of an output; (None, bf16) for none."""
     if t is None:
         return None, MO_BF16
     got = _plain(t, name, here)
-    if t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} elements")
+    if t.shape != shape:
+        _sized(t, shape, name)
     return got
 
 
@@ -224,7 +239,7 @@ def mx8_dequantize(q: Mx8Tensor, out, stream=None) -> None:
     """out [rows, k], fp32 or bf16, = the values q stands for."""
     here = _here()
     arg = _kept(q, "q", here)
-    ptr, code = _result(out, q.rows * q.k, "out", here)
+    ptr, code = _result(out, (q.rows, q.k), "out", here)
     _check(load_library().mx8_dequantize(ctypes.byref(arg), q.rows, q.k, ptr, code, _stream_ptr(stream, out)), "mx8_dequantize")
 
 
@@ -243,14 +258,14 @@ def rms_norm(x, out=None, weight=None, eps: float = 1e-6, residual=None, sum_out
     rows = numel // dim
     if out is None and out8 is None:
         raise ValueError("out or out8 must be given")
-    out_ptr, out_code = _result(out, numel, "out", here)
+    out_ptr, out_code = _result(out, shape, "out", here)
     arg8 = None
     if out8 is not None:
         if not isinstance(out8, Mx8Tensor) or (out8.rows, out8.k) != (rows, dim):
             raise ValueError(f"out8 must be an Mx8Tensor of [{rows}, {dim}]")
         arg8 = ctypes.byref(_kept(out8, "out8", here))
-    st = load_library().rms_norm(ptr, _typed(residual, "residual", here, code, numel), code, rows, dim,
-                                 _typed(weight, "weight", here, MO_F32, dim), eps, _typed(sum_out, "sum_out", here, code, numel), out_ptr,
+    st = load_library().rms_norm(ptr, _typed(residual, "residual", here, code, shape), code, rows, dim,
+                                 _typed(weight, "weight", here, MO_F32, (dim,)), eps, _typed(sum_out, "sum_out", here, code, shape), out_ptr,
                                  out_code, arg8, _stream_ptr(stream, x))
     _check(st, "rms_norm")
 
@@ -280,9 +295,9 @@ def rms_norm_grad(dy, x, dx, weight=None, eps: float = 1e-6, dresidual=None, dwe
     if arg.dtype not in (MO_MX8, code):
         raise TypeError("x must have the type of dy, or be an Mx8Tensor")
     ws, nbytes = (None, 0) if dweight is None else _scratch(workspace, "rms_norm_grad_workspace", here)
-    st = load_library().rms_norm_grad(ptr, code, ctypes.byref(arg), rows, dim, _typed(weight, "weight", here, MO_F32, dim), eps,
-                                      _typed(dresidual, "dresidual", here, code, numel), _typed(dx, "dx", here, code, numel),
-                                      _typed(dweight, "dweight", here, MO_F32, dim), int(accumulate), ws, nbytes, _stream_ptr(stream, dy))
+    st = load_library().rms_norm_grad(ptr, code, ctypes.byref(arg), rows, dim, _typed(weight, "weight", here, MO_F32, (dim,)), eps,
+                                      _typed(dresidual, "dresidual", here, code, shape), _typed(dx, "dx", here, code, shape),
+                                      _typed(dweight, "dweight", here, MO_F32, (dim,)), int(accumulate), ws, nbytes, _stream_ptr(stream, dy))
     _check(st, "rms_norm_grad")
 
 
@@ -311,16 +326,16 @@ def linear(x, w, out, bias=None, activation=None, residual=None, pre=None, works
     wp = _matrix(w, shape, "w", here)
     tokens = _rows(x, cols, "x")
     xk = _kept(x, "x", here)
-    numel = tokens * rows
-    ptr, code = _result(out, numel, "out", here)
+    out_shape = tokens, rows
+    ptr, code = _result(out, out_shape, "out", here)
     pk = None
     if pre is not None:
         if not act:
             raise ValueError("pre goes with an activation")
         pk = ctypes.byref(_kept_rows(pre, rows, tokens, "pre", here))
     ws, nbytes = _scratch(workspace, "linear_workspace", here)
-    st = load_library().linear_forward(ctypes.byref(xk), wp, tokens, cols, rows, _typed(bias, "bias", here, MO_F32, rows), act,
-                                       _typed(residual, "residual", here, code, numel), pk, ptr, code, ws, nbytes,
+    st = load_library().linear_forward(ctypes.byref(xk), wp, tokens, cols, rows, _typed(bias, "bias", here, MO_F32, (rows,)), act,
+                                       _typed(residual, "residual", here, code, out_shape), pk, ptr, code, ws, nbytes,
                                        _stream_ptr(stream, out))
     _check(st, "linear")
 
@@ -341,7 +356,7 @@ def linear_grad(dout, x, w, dx=None, dw=None, dbias=None, activation=None, pre=N
     if dx is None and dw is None and dbias is None:
         raise ValueError("dx, dw or dbias must be given")
     tokens = _rows(dout, rows, "dout")
-    dp = _typed(dout, "dout", here, MO_BF16, tokens * rows)
+    dp = _typed(dout, "dout", here, MO_BF16, (tokens, rows))
     xk = None
     if dw is not None:
         if x is None:
@@ -350,11 +365,11 @@ def linear_grad(dout, x, w, dx=None, dw=None, dbias=None, activation=None, pre=N
     if bool(act) != (pre is not None):
         raise ValueError("pre goes with an activation, and an activation with pre")
     pk = ctypes.byref(_kept_rows(pre, rows, tokens, "pre", here)) if act else None
-    dxp, dx_code = _result(dx, tokens * cols, "dx", here)
-    dwp, dw_code = _result(dw, rows * cols, "dw", here)
+    dxp, dx_code = _result(dx, (tokens, cols), "dx", here)
+    dwp, dw_code = _result(dw, shape, "dw", here)
     ws, nbytes = _scratch(workspace, "linear_workspace", here)
     st = load_library().linear_grad(dp, xk, wp, tokens, cols, rows, act, pk, dxp, dx_code, dwp, dw_code,
-                                    _typed(dbias, "dbias", here, MO_F32, rows), int(accumulate), ws, nbytes, _stream_ptr(stream, dout))
+                                    _typed(dbias, "dbias", here, MO_F32, (rows,)), int(accumulate), ws, nbytes, _stream_ptr(stream, dout))
     _check(st, "linear_grad")
 
 
@@ -396,14 +411,14 @@ def gated_ffn(x, w_gate, w_up, w_down, out, activation="silu", residual=None, ga
     dim, inner, w = _gated_weights(w_gate, w_up, w_down, here)
     tokens = _rows(x, dim, "x")
     xk = _kept(x, "x", here)
-    numel = tokens * dim
-    ptr, code = _result(out, numel, "out", here)
+    out_shape = tokens, dim
+    ptr, code = _result(out, out_shape, "out", here)
     if (gate is None) != (up is None):
         raise ValueError("gate and up go together")
     gk, uk = (None, None) if gate is None else _gated_kept(gate, up, tokens, inner, here)
     ws, nbytes = _scratch(workspace, "gated_ffn_workspace", here)
     st = load_library().gated_ffn_forward(ctypes.byref(xk), *w, tokens, dim, inner, act,
-                                          _typed(residual, "residual", here, code, numel), _ref(gk), _ref(uk), ptr, code, ws, nbytes,
+                                          _typed(residual, "residual", here, code, out_shape), _ref(gk), _ref(uk), ptr, code, ws, nbytes,
                                           _stream_ptr(stream, out))
     _check(st, "gated_ffn")
 
@@ -417,8 +432,8 @@ def gated_ffn_grad(dout, x, gate, up, w_gate, w_up, w_down, activation="silu", d
     act = _act(activation)
     dim, inner, w = _gated_weights(w_gate, w_up, w_down, here)
     tokens = _rows(dout, dim, "dout")
-    dp = _typed(dout, "dout", here, MO_BF16, tokens * dim)
-    grads = [_result(t, inner * dim, n, here) for t, n in ((dw_gate, "dw_gate"), (dw_up, "dw_up"), (dw_down, "dw_down"))]
+    dp = _typed(dout, "dout", here, MO_BF16, (tokens, dim))
+    grads = [_result(t, s, n, here) for t, s, n in ((dw_gate, (inner, dim), "dw_gate"), (dw_up, (inner, dim), "dw_up"), (dw_down, (dim, inner), "dw_down"))]
     codes = {code for t, (_, code) in zip((dw_gate, dw_up, dw_down), grads) if t is not None}
     if len(codes) > 1:
         raise TypeError("the weights' gradients must be of one type")
@@ -430,7 +445,7 @@ def gated_ffn_grad(dout, x, gate, up, w_gate, w_up, w_down, activation="silu", d
             raise ValueError("dw_gate and dw_up need x")
         xk = ctypes.byref(_kept_rows(x, dim, tokens, "x", here))
     gk, uk = _gated_kept(gate, up, tokens, inner, here)
-    dxp, dx_code = _result(dx, tokens * dim, "dx", here)
+    dxp, dx_code = _result(dx, (tokens, dim), "dx", here)
     ws, nbytes = _scratch(workspace, "gated_ffn_workspace", here)
     st = load_library().gated_ffn_grad(dp, xk, ctypes.byref(gk), ctypes.byref(uk), *w, tokens, dim, inner, act, dxp, dx_code, grads[0][0],
                                        grads[1][0], grads[2][0], codes.pop() if codes else MO_BF16, int(accumulate), ws, nbytes,

@@ -7,9 +7,11 @@ import pytest
 import torch
 
 import matrix_optimizers_zero_gb300 as mo
+import test_layer_ops_binding as b
 from matrix_optimizers_zero_gb300 import build as mo_build
 from matrix_optimizers_zero_gb300 import layer_ops
 from matrix_optimizers_zero_gb300.layer_ops import MoTensor
+from test_layer_ops_binding import library  # noqa: F401  (a fixture)
 
 NULL, SHAPE, ALIGN, PARAM, WS, OVERLAP = -1, -2, -3, -4, -5, -6
 F32, BF16, MX8 = 0, 1, 2
@@ -122,3 +124,43 @@ def test_a_second_thread_may_make_its_first_call_beside_the_first(monkeypatch):
 
     monkeypatch.setattr(layer_ops, "getattr", lookup, raising=False)
     assert layer_ops._here() == 5 and seen == [5]
+
+
+# ---------------------------------------------------------------- layouts
+
+LAYOUTS = {   # argument -> its shape [rows, width], for every matrix that the binding checks by type and size
+    "mx8_dequantize": {"out": (6, 40)}, "rms_norm": {"out": (6, 40), "residual": (6, 40), "sum_out": (6, 40)},
+    "rms_norm_grad": {"dx": (6, 40), "dresidual": (6, 40)}, "linear": {"out": (6, 72), "residual": (6, 72)},
+    "linear_grad": {"dx": (6, 40), "dw": (72, 40)}, "gated_ffn": {"out": (6, 40), "residual": (6, 40)},
+    "gated_ffn_grad": {"dx": (6, 40), "dw_gate": (72, 40), "dw_up": (72, 40), "dw_down": (40, 72)}}
+ARGS = [(name, arg) for name, args in LAYOUTS.items() for arg in args]
+
+
+@pytest.mark.parametrize("name,arg", ARGS)
+def test_refuses_matrices_that_lie_the_other_way(library, name, arg):
+    f, kw = b.calls()[name]
+    rows, width = LAYOUTS[name][arg]
+    assert tuple(kw[arg].shape) == (rows, width)
+    for shape in ((width, rows), (1, width, rows), (width, 2, rows // 2), (width // 2, 2, rows)):
+        kw[arg] = b.Tensor(shape, kw[arg].dtype)
+        with pytest.raises(ValueError, match="transpose"):
+            f(**kw)
+    assert not library.calls
+
+
+@pytest.mark.parametrize("name,arg", ARGS)
+def test_takes_views_of_the_same_rows(library, name, arg):
+    f, kw = b.calls()[name]
+    rows, width = LAYOUTS[name][arg]
+    shapes = [(2, rows // 2, width), (1, rows, 1, width), (rows * width,), (1, rows * width), (rows, 4, width // 4), (2, rows // 2, 4, width // 4),
+              (rows * 4, width // 4)]
+    for shape in shapes:
+        kw[arg] = b.Tensor(shape, kw[arg].dtype)
+        f(**kw)
+    assert len(library.calls) == len(shapes)
+
+
+def test_square_and_single_rows_have_no_other_way(library):
+    for t, d in ((40, 40), (1, 40), (40, 1)):
+        mo.rms_norm(b.Tensor((t, d)), b.Tensor((t, d)), residual=b.Tensor((d, t) if t == d or t == 1 else (t, d)))
+    assert len(library.calls) == 3
