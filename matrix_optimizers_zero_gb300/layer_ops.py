@@ -61,20 +61,29 @@ class Mx8Tensor:
             raise ValueError("rows must be 0 to 2^30 and k 1 to 2^22, with at most 2^37 elements")
         device = device or torch.device("cuda")
         blocks = -(-k // 32)
-        got = []
-        for t, width, name in ((codes, 32 * blocks, "codes"), (scales, blocks, "scales")):
-            if t is None:
-                t = torch.empty((rows, width), dtype=torch.uint8, device=device)
-            if t.dtype != torch.uint8 or t.numel() != rows * width:
-                raise ValueError(f"{name} must be {rows * width} uint8 elements")
+        self.rows, self.k = rows, k
+        self.codes, self.scales = (torch.empty((rows, width), dtype=torch.uint8, device=device) if t is None else t
+                                   for t, width in ((codes, 32 * blocks), (scales, blocks)))
+        self._look()
+
+    def _look(self):
+        """Checks the storage and takes its addresses."""
+        import torch
+        blocks = -(-self.k // 32)
+        for t, width, name in ((self.codes, 32 * blocks, "codes"), (self.scales, blocks, "scales")):
+            if t.dtype != torch.uint8 or t.numel() != self.rows * width:
+                raise ValueError(f"{name} must be {self.rows * width} uint8 elements")
             _dense(t, name)
-            got.append(t)
-        self.codes, self.scales = got
         if self.codes.get_device() != self.scales.get_device():
             raise ValueError("codes and scales must be on one device")
-        self.rows, self.k = rows, k
         self.device_index = self.codes.get_device()
         self.arg = MoTensor(self.codes.data_ptr(), self.scales.data_ptr(), MO_MX8)
+
+    def address(self) -> MoTensor:
+        """mo_tensor of the storage where it is now: codes or scales may have been replaced or moved."""
+        if self.codes.data_ptr() != (self.arg.data or 0) or self.scales.data_ptr() != (self.arg.scales or 0):
+            self._look()
+        return self.arg
 
     def numel(self) -> int:
         return self.rows * self.k
@@ -169,9 +178,10 @@ def _rows(t, width: int, name: str) -> int:
 def _kept(t, name: str, here: int, f32: bool = False):
     """mo_tensor of a plain or an 8-bit tensor."""
     if isinstance(t, Mx8Tensor):
+        arg = t.address()
         if t.device_index != here:
             raise ValueError(f"{name} must be on the current device ({here})")
-        return t.arg
+        return arg
     code = _dtypes.get(t.dtype)
     if code != MO_BF16 and not (f32 and code == MO_F32):
         raise TypeError(f"{name} must be bf16 or an Mx8Tensor")

@@ -164,3 +164,38 @@ def test_square_and_single_rows_have_no_other_way(library):
     for t, d in ((40, 40), (1, 40), (40, 1)):
         mo.rms_norm(b.Tensor((t, d)), b.Tensor((t, d)), residual=b.Tensor((d, t) if t == d or t == 1 else (t, d)))
     assert len(library.calls) == 3
+
+
+# ---------------------------------------------------------------- storage that moves
+
+class At(b.Tensor):
+    """A stand-in for a CUDA tensor at an address."""
+
+    def __init__(self, shape, at, dtype=torch.uint8, device=0):
+        super().__init__(shape, dtype, device)
+        self.at = at
+
+    def data_ptr(self):
+        return self.at
+
+
+def test_an_8_bit_tensor_is_where_its_storage_is(library):
+    q = mo.Mx8Tensor(6, 40, codes=At((6, 64), 4096), scales=At((6, 2), 8192))
+    x = b.Tensor((6, 40))
+
+    def call():
+        mo.mx8_quantize(x, q)
+        got = library.calls[-1][1][4]._obj      # (what byref was given)
+        return got.data, got.scales
+
+    assert call() == (4096, 8192)
+    q.codes.at = 1 << 20                        # t.data = another, or a resized storage
+    assert call() == (1 << 20, 8192)
+    q.scales = At((6, 2), 1 << 21)
+    assert call() == (1 << 20, 1 << 21)
+    n = len(library.calls)
+    for bad in (At((6, 32), 1 << 22), At((6, 64), 1 << 22, torch.int8), At((6, 64), 1 << 22, device=1), At((6, 64), 1 << 22, device=-1)):
+        q.codes = bad
+        with pytest.raises(ValueError):
+            mo.mx8_quantize(x, q)
+    assert len(library.calls) == n
