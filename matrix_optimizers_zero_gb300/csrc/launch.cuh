@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cstdint>
 #include <utility>
 
 namespace mo {
@@ -37,21 +38,28 @@ inline cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, dim3 block,
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-// Raises a kernel's limit of dynamic shared memory, once a device.
+// Raises a kernel's limit of dynamic shared memory, once a device and thread: a
+// table by the kernel's address, with room for all kernels of the library
+// on eight devices. What finds no place is raised at every call.
 inline cudaError_t allow_smem(const void* kern, size_t bytes) {
   struct Seen {
     const void* kern;
     int device;
   };
-  static thread_local Seen seen[64];
-  static thread_local int count = 0;
+  constexpr uint32_t kPlaces = 1024, kTries = 64;
+  static thread_local Seen seen[kPlaces];
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  for (int i = 0; i < count; ++i)
-    if (seen[i].kern == kern && seen[i].device == device) return cudaSuccess;
+  const uint32_t first = uint32_t((uint64_t(reinterpret_cast<uintptr_t>(kern)) >> 4) * 0x9E3779B1u >> 16) + uint32_t(device) * 97u;
+  Seen* place = nullptr;
+  for (uint32_t i = 0; i < kTries && place == nullptr; ++i) {
+    Seen& s = seen[(first + i) % kPlaces];
+    if (s.kern == kern && s.device == device) return cudaSuccess;
+    if (s.kern == nullptr) place = &s;
+  }
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-  if (e == cudaSuccess && count < 64) seen[count++] = {kern, device};
+  if (e == cudaSuccess && place != nullptr) *place = {kern, device};
   return e;
 }
 
