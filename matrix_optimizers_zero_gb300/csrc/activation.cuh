@@ -11,10 +11,13 @@
 // give 1 and infinity here. gelu_tanh uses 0.5 (1 + tanh(u)) = 1 / (1 + e^(-2u)),
 // which loses nothing where tanh is near -1.
 //
-// gelu's normal distribution function: erfc(y) = (a1 t + ... + a5 t^5) e^(-y^2) with
-// t = 1 / (1 + p y), y >= 0 (Abramowitz and Stegun, Handbook of Mathematical
-// Functions, 7.1.26): within 1.5e-7, and within 0.3% of the value down to
-// erfc(4) = 1.5e-8, where the result is rounded to bf16 as a rule.
+// gelu's normal distribution function: Phi(-x) = e^(-x^2 / 2) R(x), x >= 0, where
+// R(x) = Phi(-x) e^(x^2 / 2) falls from 1/2 as 1 / x does. R is t times a polynomial of
+// degree 7 in t = 1 / (1 + 0.3 x), fitted here to R in double precision for the least
+// relative error on [0, 14] (weighted least squares, the weights raised where the error
+// is largest): 1.6e-7 with the coefficients below. So gelu keeps its relative accuracy in
+// the left tail, down to where e^(-x^2 / 2) is 0 in fp32. (Abramowitz and Stegun 7.1.26,
+// which is as exact beside 1, is 5e-5 of the value off at -3 and 1e-2 at -8.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -95,15 +98,17 @@ __device__ __forceinline__ N logistic_of(N x) {
 template <typename N>
 __device__ __forceinline__ N normal_cdf(N x, N* bell) {
   const N e = each(mul2(mul2(x, x), both<N>(-0.5f * kLog2E)), exp2_fast);
-  // 1 + p |x| / sqrt(2)
-  const N t = each(each(x, [](float v) { return fmaf(0.3275911f * 0.70710678f, fabsf(v), 1.0f); }), reciprocal_fast);
-  N q = fma2(t, both<N>(1.061405429f), both<N>(-1.453152027f));
-  q = fma2(t, q, both<N>(1.421413741f));
-  q = fma2(t, q, both<N>(-0.284496736f));
-  q = fma2(t, q, both<N>(0.254829592f));
-  const N half = mul2(mul2(mul2(t, both<N>(0.5f)), q), e);   // erfc(|x| / sqrt(2)) / 2
+  const N t = each(each(x, [](float v) { return fmaf(0.3f, fabsf(v), 1.0f); }), reciprocal_fast);
+  N q = fma2(t, both<N>(0.035674572f), both<N>(-0.15720221f));
+  q = fma2(t, q, both<N>(0.206352f));
+  q = fma2(t, q, both<N>(-0.053682234f));
+  q = fma2(t, q, both<N>(0.12856087f));
+  q = fma2(t, q, both<N>(0.099913724f));
+  q = fma2(t, q, both<N>(0.12075392f));
+  q = fma2(t, q, both<N>(0.1196293f));
+  const N tail = mul2(mul2(t, q), e);   // Phi(-|x|)
   *bell = e;
-  return each(x, half, [](float v, float h) { return v >= 0.0f ? 1.0f - h : h; });
+  return each(x, tail, [](float v, float h) { return v >= 0.0f ? 1.0f - h : h; });
 }
 
 // act(x)
