@@ -448,20 +448,21 @@ int mx8_dequantize(const mo_tensor* q, int64_t rows, int64_t k, void* out, int32
  *   y = s / sqrt(mean(s^2) + eps) * weight
  * x, residual (or NULL) and sum (s is stored there; or NULL) have `dtype`; y
  * goes to out (`out_dtype`), to out8 in 8 bits, or to both; either may be NULL.
- * weight is fp32 [dim], or NULL for ones. s is not rounded in between; s^2 is
- * summed in fp32, and a row whose sum is infinite there gives zeros. sum and out
- * may each be x or residual itself. rows up to 2^30, dim up to 2^22. */
+ * weight is fp32 [dim], or NULL for ones. s is not rounded in between. Rows of
+ * any size that the type holds are normalised: where their squares leave fp32's
+ * range, they are scaled by a power of two first. sum and out may each be x or
+ * residual itself. rows up to 2^30, dim up to 2^22. */
 int rms_norm(const void* x, const void* residual, int32_t dtype, int64_t rows, int64_t dim, const float* weight, float eps,
              void* sum, void* out, int32_t out_dtype, const mo_tensor* out8, cudaStream_t stream);
 
 /* Gradients of rms_norm in s and in the weight, from dy and s itself (x: of
  * dy's type, or 8 bits). With r = 1 / sqrt(mean(s^2) + eps), n = s r, g = dy weight:
  *   dx = r (g - n mean(g n)) + dresidual,   dweight (+)= sum over rows of dy n
- * dresidual (the gradient that passes the norm by) and dweight may be NULL; dx
- * may be dy or dresidual itself. With accumulate = 1 dweight, the fp32 g of
- * adamw_tail_step, is added to. Sums over rows are taken in a fixed order. ws:
- * mo_rms_norm_grad_workspace_bytes() bytes, 256-byte aligned (not used without
- * dweight). */
+ * for rows of s and of dy of any size, as above. dresidual (the gradient that
+ * passes the norm by) and dweight may be NULL; dx may be dy or dresidual itself.
+ * With accumulate = 1 dweight, the fp32 g of adamw_tail_step, is added to. Sums
+ * over rows are taken in a fixed order. ws: mo_rms_norm_grad_workspace_bytes()
+ * bytes, 256-byte aligned (not used without dweight). */
 size_t mo_rms_norm_grad_workspace_bytes(int64_t rows, int64_t dim);
 int rms_norm_grad(const void* dy, int32_t dtype, const mo_tensor* x, int64_t rows, int64_t dim, const float* weight,
                   float eps, const void* dresidual, void* dx, float* dweight, int32_t accumulate, void* ws,

@@ -74,8 +74,19 @@ __device__ __forceinline__ void store_row_mx8(uint8_t* codes, uint8_t* scales, i
   }
 }
 
-// 1 / sqrt(mean + eps), two units of 2^-23 off at most (rsqrtf)
-__device__ __forceinline__ float inverse_rms(float squares, float inv_dim, float eps) { return rsqrtf(fmaf(squares, inv_dim, eps)); }
+// mean + eps where squares and products in fp32 say all: above what is lost where a
+// square is below 2^-126, and finite. Others are computed again from scaled rows.
+__device__ __forceinline__ bool usual(float mean_eps) { return mean_eps >= 0x1p-80f && mean_eps <= 3.402823466e38f; }
+// (m: mean(g n); the same for the products of the backward pass)
+__device__ __forceinline__ bool usual(float mean_eps, float m) { return usual(mean_eps) && fabsf(m) <= 0x1p100f; }
+
+// 1 / sqrt(x), two units of 2^-23 off at most; infinite below 2^-126, which `usual` and
+// scaled rows leave to rows of zeros (eps 0)
+__device__ __forceinline__ float inverse_sqrt(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // Sums of a and b over a team, in a fixed order, with one barrier: a row's warps
 // leave theirs in one half of `shared`, the next row's in the other (parity). A
@@ -102,6 +113,94 @@ __device__ __forceinline__ float2 team_sums(float a, float b, float (&shared)[2]
     for (int o = (kWarps <= 16 ? kWarps : 16) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   }
   return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
+}
+
+// Maxima of a and b over a team, likewise (a and b not negative; NaN does not count).
+template <int TEAM>
+__device__ __forceinline__ float2 team_max(float a, float b, float (&shared)[2][64], int parity) {
+  const int lane = int(threadIdx.x & 31), warp = int(threadIdx.x >> 5);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    b = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
+  }
+  if constexpr (TEAM > 32) {
+    constexpr int kWarps = TEAM / 32;
+    if (lane == 0) shared[parity][warp] = a, shared[parity][32 + warp] = b;
+    __syncthreads();
+    a = shared[parity][lane % kWarps];
+    b = shared[parity][32 + lane % kWarps];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+      a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+      b = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
+    }
+  }
+  return make_float2(a, b);
+}
+
+// ------------------------------------------------------------------ rows out of range
+//
+// A row whose squares (or products with the gradient) leave fp32's range is scaled by
+// a power of two, which loses nothing: with t = s 2^-e and the largest |t| (or the
+// square root of eps) in [1, 4), r' = 1 / sqrt(mean(t^2) + eps 2^-2e) gives n = t r' = s r.
+//
+// The team's first sums have used one half of `shared` (parity); its maxima take the
+// other, and the second sums the first again: between two uses of a half lies a barrier.
+
+// The exponent of a magnitude, -126 to 126; 0 of 0 and of what is not finite.
+__device__ __forceinline__ int exponent_of(float top) {
+  const int e = int(__float_as_uint(top) >> 23);
+  return top == 0.0f || e == 255 ? 0 : min(max(e, 1), 253) - 127;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }   // e: -126 to 127
+
+// s becomes t; r'.
+template <int TEAM>
+__device__ __forceinline__ float scaled_row(float (&s)[8], float inv_dim, float eps, float (&shared)[2][64], int parity) {
+  float top = 0.0f, squares = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(s[i]));
+  top = team_max<TEAM>(top, 0.0f, shared, parity ^ 1).x;
+  const float down = power_of_two(-exponent_of(fmaxf(top, sqrtf(eps))));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s[i] *= down;
+    squares = fmaf(s[i], s[i], squares);
+  }
+  return inverse_sqrt(fmaf(team_sums<TEAM>(squares, 0.0f, shared, parity).x, inv_dim, eps * down * down));
+}
+
+// s becomes n and w the gradient r (g - n mean(g n)); dy is scaled by its own power
+// of two on the way.
+template <int TEAM>
+__device__ __forceinline__ void scaled_grad_row(float (&s)[8], const float (&dy)[8], float (&w)[8], float inv_dim, float eps,
+                                                float (&shared)[2][64], int parity) {
+  float top_s = 0.0f, top_d = 0.0f, squares = 0.0f, dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    top_s = fmaxf(top_s, fabsf(s[i]));
+    top_d = fmaxf(top_d, fabsf(dy[i]));
+  }
+  const float2 top = team_max<TEAM>(top_s, top_d, shared, parity ^ 1);
+  const int es = exponent_of(fmaxf(top.x, sqrtf(eps))), ed = exponent_of(top.y);
+  const float down_s = power_of_two(-es), down_d = power_of_two(-ed);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s[i] *= down_s;
+    w[i] *= dy[i] * down_d;
+    squares = fmaf(s[i], s[i], squares);
+    dot = fmaf(w[i], s[i], dot);
+  }
+  const float2 sums = team_sums<TEAM>(squares, dot, shared, parity);
+  const float r = inverse_sqrt(fmaf(sums.x, inv_dim, eps * down_s * down_s)), m = sums.y * r * inv_dim;
+  const int c = ed - es;   // (in two steps: up to 2^252)
+  const float c0 = power_of_two(c / 2), c1 = power_of_two(c - c / 2);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s[i] *= r;
+    w[i] = r * fmaf(-s[i], m, w[i]) * c0 * c1;
+  }
 }
 
 // ------------------------------------------------------------------ aligned rows
@@ -177,6 +276,10 @@ __device__ __forceinline__ void unpair(const F2 (&v)[4], float (&f)[8]) {
     f[2 * i + 1] = p.y;
   }
 }
+__device__ __forceinline__ void pair(const float (&f)[8], F2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = ptx::f2(f[2 * i], f[2 * i + 1]);
+}
 template <typename T>
 __device__ __forceinline__ void store_pairs(T* p, const F2 (&v)[4]) {
   float f[8];
@@ -194,8 +297,42 @@ template <typename T, bool MX8>
 constexpr int kGradAhead = rows_ahead(kGradSlot<T, MX8>);
 static_assert(kNormAhead<float> >= 1 && kGradAhead<float, true> >= 1 && kGradAhead<float, false> >= 1, "a row ahead");
 
+// A row out of range, once more from its slots.
 template <int TEAM, typename T>
-__global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_kernel(const NormParams p) {
+__device__ __noinline__ void scaled_slot_row(const NormParams& p, int64_t row, uint32_t xs_at, uint32_t rs_at, float (&shared)[2][64], int parity) {
+  const int t = int(threadIdx.x) % TEAM;
+  const int64_t col = int64_t(t) * 8, nb = (p.dim + 31) / 32, at = row * p.dim + col;
+  const bool in = col < p.dim;
+  const Slots<8 * int(sizeof(T)), kBlock<TEAM>> xs(xs_at), rs(rs_at);
+  float f[8] = {};
+  if (in) {
+    F2 s[4];
+    slot_values(xs, 0, 0.0f, s);
+    if (p.residual != nullptr) {
+      F2 r[4];
+      slot_values(rs, 0, 0.0f, r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = ptx::add2(s[i], r[i]);
+    }
+    unpair(s, f);
+  }
+  const float r = scaled_row<TEAM>(f, 1.0f / float(p.dim), p.eps, shared, parity);
+  if (in) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] * r * (p.weight != nullptr ? p.weight[col + i] : 1.0f);
+    if (p.out != nullptr) {
+      if (p.out_bf16)
+        store8(static_cast<uint16_t*>(p.out) + at, f);
+      else
+        store8(static_cast<float*>(p.out) + at, f);
+    }
+  }
+  if (p.out8.data != nullptr)
+    store_row_mx8<TEAM, 8, true>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, f);
+}
+
+template <int TEAM, typename T>
+__global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t slots[];
   __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
@@ -206,7 +343,8 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_kernel
   const int64_t col = int64_t(t) * 8, nb = (p.dim + 31) / 32;
   const bool in = col < p.dim;
   const float inv_dim = 1.0f / float(p.dim);
-  const Slots<kRow, kBlock<TEAM>> xs(ptx::smem_addr(slots)), rs(ptx::smem_addr(slots) + (kAhead + 1) * xs.kSlot);
+  const uint32_t start = ptx::smem_addr(slots);
+  const Slots<kRow, kBlock<TEAM>> xs(start), rs(start + (kAhead + 1) * xs.kSlot);
   const T* x = static_cast<const T*>(p.x) + col;
   const T* res = p.residual != nullptr ? static_cast<const T*>(p.residual) + col : nullptr;
   auto fetch = [&](int64_t row, uint32_t slot) {
@@ -232,7 +370,6 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_kernel
   for (int64_t row = team; row < p.rows; row += step, parity ^= 1) {
     fetch(row + kAhead * step, slot == 0 ? kAhead : slot - 1);
     ptx::cp_async_wait_but<kAhead>();
-    const int64_t at = row * p.dim + col;
     F2 s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = ptx::f2(0.0f);
@@ -244,14 +381,15 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_kernel
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = ptx::add2(s[i], r[i]);
       }
-      if (p.sum != nullptr) store_pairs(static_cast<T*>(p.sum) + at, s);
+      if (p.sum != nullptr) store_pairs(static_cast<T*>(p.sum) + row * p.dim + col, s);
     }
-    slot = slot == kAhead ? 0 : slot + 1;
     F2 squares = ptx::mul2(s[0], s[0]);
 #pragma unroll
     for (int i = 1; i < 4; ++i) squares = ptx::fma2(s[i], s[i], squares);
     const float2 half = ptx::parts(squares);
-    const F2 r = ptx::f2(inverse_rms(team_sums<TEAM>(half.x + half.y, 0.0f, shared, parity).x, inv_dim, p.eps));
+    const float mean = fmaf(team_sums<TEAM>(half.x + half.y, 0.0f, shared, parity).x, inv_dim, p.eps);
+    const int64_t at = row * p.dim + col;
+    const F2 r = ptx::f2(inverse_sqrt(mean));
     // (a thread past dim holds zeros; where r is not finite they have to stay so)
     if (in) {
 #pragma unroll
@@ -268,6 +406,9 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_kernel
       unpair(s, v);
       store_row_mx8<TEAM, 8, true>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, v);
     }
+    if (!usual(mean))   // once more, from the slots: behind the row, where the check holds nothing up
+      scaled_slot_row<TEAM, T>(p, row, start + slot * xs.kSlot, start + (kAhead + 1 + slot) * xs.kSlot, shared, parity);
+    slot = slot == kAhead ? 0 : slot + 1;
   }
 }
 
@@ -337,21 +478,46 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_grad_k
     }
     const float2 hs = ptx::parts(squares), hd = ptx::parts(dot);
     const float2 sums = team_sums<TEAM>(hs.x + hs.y, hd.x + hd.y, shared, parity);
-    const float r = inverse_rms(sums.x, inv_dim, p.eps);
-    if (in) {
-      const F2 r2 = ptx::f2(r), m2 = ptx::f2(-(sums.y * r * inv_dim));   // -mean(g s r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const F2 n = ptx::mul2(s[i], r2);
-        dw[i] = ptx::fma2(dy[i], n, dw[i]);
-        dy[i] = ptx::mul2(r2, ptx::fma2(n, m2, ptx::mul2(dy[i], w[i])));
-      }
+    const float mean = fmaf(sums.x, inv_dim, p.eps);
+    float r = inverse_sqrt(mean), m = sums.y * r * inv_dim;   // m: mean(g s r)
+    const bool fits = usual(mean, m);
+    if (!fits) r = m = 0.0f;   // (adds nothing to dw)
+    auto put = [&] {           // dy is the norm's gradient
       if (p.dres != nullptr) {
         slot_values(rs, slot, 0.0f, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) dy[i] = ptx::add2(dy[i], s[i]);
       }
       store_pairs(static_cast<T*>(p.dx) + at, dy);
+    };
+    if (in) {
+      const F2 r2 = ptx::f2(r), m2 = ptx::f2(-m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const F2 n = ptx::mul2(s[i], r2);
+        dw[i] = ptx::fma2(dy[i], n, dw[i]);
+        dy[i] = ptx::mul2(r2, ptx::fma2(n, m2, ptx::mul2(dy[i], w[i])));
+      }
+      put();
+    }
+    if (!fits) {   // once more, from the slots: behind the row, where the check holds nothing up
+      float fs[8] = {}, fd[8] = {}, fw[8];
+      if (in) {
+        slot_values(ds, slot, 0.0f, dy);
+        slot_values(xs, slot, MX8 ? mx8_up(p.x.scales[at8 >> 5]) : 0.0f, s);
+        unpair(s, fs);
+        unpair(dy, fd);
+      }
+      unpair(w, fw);
+      scaled_grad_row<TEAM>(fs, fd, fw, inv_dim, p.eps, shared, parity);
+      if (in) {
+        F2 n[4];
+        pair(fs, n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw[i] = ptx::fma2(dy[i], n[i], dw[i]);
+        pair(fw, dy);
+        put();
+      }
     }
     slot = slot == kAhead ? 0 : slot + 1;
   }
@@ -362,6 +528,31 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_grad_k
 //
 // Rows that are not 16-byte aligned: elements TEAM apart, eight a thread, one row
 // ahead in registers.
+// (2^-e, r') of a row out of range, from memory
+template <int TEAM, typename T>
+__device__ __noinline__ float2 scaled_odd_row(const T* x, const T* res, int64_t dim, float eps, float (&shared)[2][64]) {
+  float top = 0.0f, squares = 0.0f;
+#pragma unroll 1
+  for (int64_t c = int(threadIdx.x) % TEAM; c < dim; c += TEAM)
+    top = fmaxf(top, fabsf(load1(x + c) + (res != nullptr ? load1(res + c) : 0.0f)));
+  top = team_max<TEAM>(top, 0.0f, shared, 1).x;
+  const float down = power_of_two(-exponent_of(fmaxf(top, sqrtf(eps))));
+#pragma unroll 1
+  for (int64_t c = int(threadIdx.x) % TEAM; c < dim; c += TEAM) {
+    const float t = (load1(x + c) + (res != nullptr ? load1(res + c) : 0.0f)) * down;
+    squares = fmaf(t, t, squares);
+  }
+  const float mean = fmaf(team_sums<TEAM>(squares, 0.0f, shared, 0).x, 1.0f / float(dim), eps * down * down);
+  return make_float2(down, inverse_sqrt(mean));
+}
+
+template <typename T>
+__device__ __forceinline__ float kept_value(const Kept& x, int64_t row, int64_t dim, int64_t c) {
+  const int64_t nb = (dim + 31) / 32;
+  if (x.dtype == MO_MX8) return e4m3_value(static_cast<const uint8_t*>(x.data)[row * nb * 32 + c]) * mx8_up(x.scales[row * nb + (c >> 5)]);
+  return load1(static_cast<const T*>(x.data) + row * dim + c);
+}
+
 template <int TEAM, typename T>
 __global__ void __launch_bounds__(kBlock<TEAM>) norm_odd_kernel(const NormParams p) {
   __shared__ float shared[2][64];
@@ -385,16 +576,21 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_odd_kernel(const NormParams
       if (c < p.dim) s[i] += load1(static_cast<const T*>(p.residual) + at + c);
     }
   }
-  if (p.sum != nullptr) store_row<TEAM, 8, false>(static_cast<T*>(p.sum) + at, p.dim, t, s);
   float squares = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) squares = fmaf(s[i], s[i], squares);
-  const float r = inverse_rms(team_sums<TEAM>(squares, 0.0f, shared, 0).x, 1.0f / float(p.dim), p.eps);
+  const float mean = fmaf(team_sums<TEAM>(squares, 0.0f, shared, 0).x, 1.0f / float(p.dim), p.eps);
+  float2 k = make_float2(1.0f, inverse_sqrt(mean));
+  if (!usual(mean))
+    k = scaled_odd_row<TEAM>(static_cast<const T*>(p.x) + at, p.residual != nullptr ? static_cast<const T*>(p.residual) + at : nullptr,
+                             p.dim, p.eps, shared);
+  if (p.sum != nullptr) store_row<TEAM, 8, false>(static_cast<T*>(p.sum) + at, p.dim, t, s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t c = column<TEAM, false>(i, t);
     // (past dim 0, also where r is not finite)
-    s[i] = c >= p.dim ? 0.0f : p.weight != nullptr ? s[i] * r * p.weight[c] : s[i] * r;
+    const float n = s[i] * k.x * k.y;
+    s[i] = c >= p.dim ? 0.0f : p.weight != nullptr ? n * p.weight[c] : n;
   }
   if (p.out != nullptr) {
     if (p.out_bf16)
@@ -406,8 +602,39 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_odd_kernel(const NormParams
     store_row_mx8<TEAM, 8, false>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, s);
 }
 
+// dx of a row if it is out of range, from memory; its dy n is added to `part` (null: not
+// wanted), of which a thread adds to its own columns.
+template <int TEAM, typename T>
+__device__ __noinline__ void scaled_odd_grad(const NormGradParams& p, int64_t row, float* part, float (&shared)[2][64], int parity) {
+  const int t = int(threadIdx.x) % TEAM;
+  const float inv_dim = 1.0f / float(p.dim);
+  float s[8], dy[8], g[8], squares = 0.0f, dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = column<TEAM, false>(i, t);
+    const bool in = c < p.dim;
+    s[i] = in ? kept_value<T>(p.x, row, p.dim, c) : 0.0f;
+    dy[i] = in ? load1(static_cast<const T*>(p.dy) + row * p.dim + c) : 0.0f;
+    g[i] = p.weight != nullptr && in ? p.weight[c] : 1.0f;
+    squares = fmaf(s[i], s[i], squares);   // (as the row was judged: the same bits)
+    dot = fmaf(dy[i] * g[i], s[i], dot);
+  }
+  const float2 sums = team_sums<TEAM>(squares, dot, shared, parity);
+  const float mean = fmaf(sums.x, inv_dim, p.eps);
+  if (usual(mean, sums.y * inverse_sqrt(mean) * inv_dim)) return;
+  scaled_grad_row<TEAM>(s, dy, g, inv_dim, p.eps, shared, parity);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = column<TEAM, false>(i, t);
+    if (c >= p.dim) continue;
+    if (part != nullptr) part[c] = fmaf(dy[i], s[i], part[c]);
+    if (p.dres != nullptr) g[i] += load1(static_cast<const T*>(p.dres) + row * p.dim + c);
+    store1(static_cast<T*>(p.dx) + row * p.dim + c, g[i]);
+  }
+}
+
 template <int TEAM, typename T, bool MX8>
-__global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const NormGradParams p) {
+__global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const __grid_constant__ NormGradParams p) {
   __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -442,6 +669,7 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const NormG
     }
   };
   if (team < p.rows) fetch(team);
+  bool again = false;   // there are rows out of range
   int parity = 0;
   for (int64_t row = team; row < p.rows; row += step, parity ^= 1) {
     float s[8], dy[8], res[8];
@@ -462,17 +690,23 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const NormG
       dot = fmaf(dy[i] * w[i], s[i], dot);
     }
     const float2 sums = team_sums<TEAM>(squares, dot, shared, parity);
-    const float r = inverse_rms(sums.x, inv_dim, p.eps);
-    const float m = sums.y * r * inv_dim;
+    const float mean = fmaf(sums.x, inv_dim, p.eps);
+    float r = inverse_sqrt(mean), m = sums.y * r * inv_dim;
+    const bool fits = usual(mean, m);
+    if (!fits) r = m = 0.0f;   // (adds nothing to dw, and is not stored: dx may be dy)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float n = s[i] * r;
       dw[i] = fmaf(dy[i], n, dw[i]);
       dy[i] = r * fmaf(-n, m, dy[i] * w[i]) + res[i];
     }
-    store_row<TEAM, 8, false>(static_cast<T*>(p.dx) + row * p.dim, p.dim, t, dy);
+    if (fits) store_row<TEAM, 8, false>(static_cast<T*>(p.dx) + row * p.dim, p.dim, t, dy);
+    again = again || !fits;
   }
-  if (p.part != nullptr) store_row<TEAM, 8, false>(p.part + team * p.dim, p.dim, t, dw);
+  float* part = p.part != nullptr ? p.part + team * p.dim : nullptr;
+  if (part != nullptr) store_row<TEAM, 8, false>(part, p.dim, t, dw);
+  if (again)
+    for (int64_t row = team; row < p.rows; row += step, parity ^= 1) scaled_odd_grad<TEAM, T>(p, row, part, shared, parity);
 }
 
 // Rows that do not fit a team's registers: a block reads them twice, the second
@@ -480,7 +714,7 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const NormG
 constexpr int kLong = 512;
 
 template <typename T>
-__global__ void __launch_bounds__(kLong) norm_long_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kLong, 3) norm_long_kernel(const NormParams p) {
   __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -492,13 +726,15 @@ __global__ void __launch_bounds__(kLong) norm_long_kernel(const NormParams p) {
     const float s = load1(x + c) + (res != nullptr ? load1(res + c) : 0.0f);
     squares = fmaf(s, s, squares);
   }
-  const float r = inverse_rms(team_sums<kLong>(squares, 0.0f, shared, 0).x, 1.0f / float(p.dim), p.eps);
+  const float mean = fmaf(team_sums<kLong>(squares, 0.0f, shared, 0).x, 1.0f / float(p.dim), p.eps);
+  float2 k = make_float2(1.0f, inverse_sqrt(mean));
+  if (!usual(mean)) k = scaled_odd_row<kLong>(x, res, p.dim, p.eps, shared);
   const int64_t nb = (p.dim + 31) / 32;
   uint8_t* codes = p.out8.data != nullptr ? static_cast<uint8_t*>(p.out8.data) + int64_t(blockIdx.x) * nb * 32 : nullptr;
   for (int64_t c = threadIdx.x; c < nb * 32; c += kLong) {   // whole warps
     const bool in = c < p.dim;
     const float s = in ? load1(x + c) + (res != nullptr ? load1(res + c) : 0.0f) : 0.0f;
-    const float y = !in ? 0.0f : p.weight != nullptr ? s * r * p.weight[c] : s * r;
+    const float n = s * k.x * k.y, y = !in ? 0.0f : p.weight != nullptr ? n * p.weight[c] : n;
     if (in && p.sum != nullptr) store1(static_cast<T*>(p.sum) + at + c, s);
     if (in && p.out != nullptr) {
       if (p.out_bf16)
@@ -510,48 +746,87 @@ __global__ void __launch_bounds__(kLong) norm_long_kernel(const NormParams p) {
       float top = fabsf(y);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = top2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      const uint32_t k = mx8_scale(top);
-      codes[c] = uint8_t(cvt_e4m3x2(y * mx8_down(k), 0.0f));
-      if ((c & 31) == 0) p.out8.scales[int64_t(blockIdx.x) * nb + (c >> 5)] = uint8_t(k);
+      const uint32_t e = mx8_scale(top);
+      codes[c] = uint8_t(cvt_e4m3x2(y * mx8_down(e), 0.0f));
+      if ((c & 31) == 0) p.out8.scales[int64_t(blockIdx.x) * nb + (c >> 5)] = uint8_t(e);
     }
   }
 }
 
+// A row's gradient, element by element: n = s down r, dx = r (dy down_d w - n m) c0 c1;
+// dy n is added to `from` (null: nothing to add to) and left in `to` (null: not wanted).
+struct LongGrad {
+  float down = 1.0f, r, down_d = 1.0f, m, c0 = 1.0f, c1 = 1.0f;
+};
+template <typename T, int UNROLL>
+__device__ __forceinline__ void put_long_grad(const NormGradParams& p, int64_t row, const LongGrad& l, const float* from, float* to) {
+  const int64_t at = row * p.dim;
+#pragma unroll UNROLL
+  for (int64_t c = threadIdx.x; c < p.dim; c += kLong) {   // a column is one thread's: no order to keep
+    const float n = kept_value<T>(p.x, row, p.dim, c) * l.down * l.r, d = load1(static_cast<const T*>(p.dy) + at + c);
+    if (to != nullptr) to[c] = from == nullptr ? d * n : fmaf(d, n, from[c]);
+    float v = l.r * fmaf(-n, l.m, d * l.down_d * (p.weight != nullptr ? p.weight[c] : 1.0f)) * l.c0 * l.c1;
+    if (p.dres != nullptr) v += load1(static_cast<const T*>(p.dres) + at + c);
+    store1(static_cast<T*>(p.dx) + at + c, v);
+  }
+}
 template <typename T>
-__global__ void __launch_bounds__(kLong) norm_grad_long_kernel(const NormGradParams p) {
+__device__ __noinline__ void scaled_long_grad(const NormGradParams& p, int64_t row, float (&shared)[2][64], int parity, const float* from,
+                                              float* to) {
+  const T* dy = static_cast<const T*>(p.dy) + row * p.dim;
+  LongGrad l;
+  float top_s = 0.0f, top_d = 0.0f, squares = 0.0f, dot = 0.0f;
+#pragma unroll 1
+  for (int64_t c = threadIdx.x; c < p.dim; c += kLong) {
+    top_s = fmaxf(top_s, fabsf(kept_value<T>(p.x, row, p.dim, c)));
+    top_d = fmaxf(top_d, fabsf(load1(dy + c)));
+  }
+  const float2 top = team_max<kLong>(top_s, top_d, shared, parity ^ 1);
+  const int es = exponent_of(fmaxf(top.x, sqrtf(p.eps))), ed = exponent_of(top.y);
+  l.down = power_of_two(-es);
+  l.down_d = power_of_two(-ed);
+#pragma unroll 1
+  for (int64_t c = threadIdx.x; c < p.dim; c += kLong) {
+    const float t = kept_value<T>(p.x, row, p.dim, c) * l.down;
+    squares = fmaf(t, t, squares);
+    dot = fmaf(load1(dy + c) * l.down_d * (p.weight != nullptr ? p.weight[c] : 1.0f), t, dot);
+  }
+  const float2 sums = team_sums<kLong>(squares, dot, shared, parity);
+  const float inv_dim = 1.0f / float(p.dim);
+  l.r = inverse_sqrt(fmaf(sums.x, inv_dim, p.eps * l.down * l.down));
+  l.m = sums.y * l.r * inv_dim;
+  l.c0 = power_of_two((ed - es) / 2);
+  l.c1 = power_of_two(ed - es - (ed - es) / 2);
+  put_long_grad<T, 1>(p, row, l, from, to);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLong) norm_grad_long_kernel(const __grid_constant__ NormGradParams p) {
   __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int64_t nb = (p.dim + 31) / 32;
   float* part = p.part != nullptr ? p.part + int64_t(blockIdx.x) * p.dim : nullptr;
   const float inv_dim = 1.0f / float(p.dim);
   int parity = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const int64_t at = row * p.dim;
-    auto x_at = [&](int64_t c) {
-      if (p.x.dtype == MO_MX8)
-        return e4m3_value(static_cast<const uint8_t*>(p.x.data)[row * nb * 32 + c]) * mx8_up(p.x.scales[row * nb + (c >> 5)]);
-      return load1(static_cast<const T*>(p.x.data) + at + c);
-    };
-    auto w_at = [&](int64_t c) { return p.weight != nullptr ? p.weight[c] : 1.0f; };
-    const T* dy = static_cast<const T*>(p.dy) + at;
+    const T* dy = static_cast<const T*>(p.dy) + row * p.dim;
     float squares = 0.0f, dot = 0.0f;
     for (int64_t c = threadIdx.x; c < p.dim; c += kLong) {
-      const float s = x_at(c);
+      const float s = kept_value<T>(p.x, row, p.dim, c);
       squares = fmaf(s, s, squares);
-      dot = fmaf(load1(dy + c) * w_at(c), s, dot);
+      dot = fmaf(load1(dy + c) * (p.weight != nullptr ? p.weight[c] : 1.0f), s, dot);
     }
     const float2 sums = team_sums<kLong>(squares, dot, shared, parity);
+    const float mean = fmaf(sums.x, inv_dim, p.eps);
+    const float* from = row == int64_t(blockIdx.x) ? nullptr : part;
+    LongGrad l;
+    l.r = inverse_sqrt(mean);
+    l.m = sums.y * l.r * inv_dim;
+    if (usual(mean, l.m))
+      put_long_grad<T, 4>(p, row, l, from, part);
+    else
+      scaled_long_grad<T>(p, row, shared, parity, from, part);
     parity ^= 1;
-    const float r = inverse_rms(sums.x, inv_dim, p.eps);
-    const float m = sums.y * r * inv_dim;
-    for (int64_t c = threadIdx.x; c < p.dim; c += kLong) {   // a column is one thread's: no order to keep
-      const float n = x_at(c) * r, d = load1(dy + c);
-      if (part != nullptr) part[c] = row == int64_t(blockIdx.x) ? d * n : fmaf(d, n, part[c]);
-      float v = r * fmaf(-n, m, d * w_at(c));
-      if (p.dres != nullptr) v += load1(static_cast<const T*>(p.dres) + at + c);
-      store1(static_cast<T*>(p.dx) + at + c, v);
-    }
   }
 }
 
@@ -569,33 +844,57 @@ __device__ __forceinline__ void sum8(const T* x, const T* res, float (&s)[8]) {
   }
 }
 
+// The sum of squares in two ranges, without a branch: of s 2^-75 (finite for 2^22
+// numbers below 2^128, and accurate for a mean square from 2^24 on) and of s 2^40 (for
+// less than that: its sum stays below 2^126; and down to 2^-206, where any eps but 0 is
+// all that counts). Code for rows out of range would take registers from the others:
+// 8192 x 12288 bf16 75 us with neither, 81 with this, 97 to 130 with that. eps > 0;
+// other calls go to the kernel above.
+constexpr float kHigh = 0x1p-75f, kLow = 0x1p40f;
+// (f, r): n = s f r, where f is 1 if r is a normal number by itself
+__device__ __forceinline__ float2 two_ranges(float2 sums, float inv_dim, float eps) {
+  const bool low = sums.y <= 0x1p126f && eps <= 0x1p40f;
+  const float f = low ? kLow : kHigh, r = inverse_sqrt(fmaf(low ? sums.y : sums.x, inv_dim, eps * f * f));
+  return f * r >= 0x1p-126f ? make_float2(1.0f, f * r) : make_float2(f, r);
+}
+
+// (Four blocks an SM: 32 registers a thread, so columns are counted in 32 bits.)
 template <typename T>
-__global__ void __launch_bounds__(kLong) norm_long_vec_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kLong, 4) norm_long_vec_kernel(const NormParams p) {
   __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int64_t at = int64_t(blockIdx.x) * p.dim, nb = (p.dim + 31) / 32;
+  const int dim = int(p.dim), padded = (dim + 31) / 32 * 32;
+  const int64_t at = int64_t(blockIdx.x) * dim;
   const T* x = static_cast<const T*>(p.x) + at;
   const T* res = p.residual != nullptr ? static_cast<const T*>(p.residual) + at : nullptr;
-  float squares = 0.0f;
+  F2 high = ptx::f2(0.0f), low = ptx::f2(0.0f);
 #pragma unroll 2
-  for (int64_t c = threadIdx.x * 8; c < p.dim; c += kLongStep) {
+  for (int c = threadIdx.x * 8; c < dim; c += kLongStep) {
     float s[8];
     sum8(x + c, res != nullptr ? res + c : nullptr, s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) squares = fmaf(s[i], s[i], squares);
+    for (int i = 0; i < 8; i += 2) {
+      const F2 v = ptx::f2(s[i], s[i + 1]), h = ptx::mul2(v, ptx::f2(kHigh)), l = ptx::mul2(v, ptx::f2(kLow));
+      high = ptx::fma2(h, h, high);
+      low = ptx::fma2(l, l, low);
+    }
   }
-  const float r = inverse_rms(team_sums<kLong>(squares, 0.0f, shared, 0).x, 1.0f / float(p.dim), p.eps);
-  for (int64_t first = 0; first < nb * 32; first += kLongStep) {   // (whole warps: a block of 32 is four lanes)
-    const int64_t c = first + threadIdx.x * 8;
+  const float2 h = ptx::parts(high), l = ptx::parts(low);
+  const float2 k = two_ranges(team_sums<kLong>(h.x + h.y, l.x + l.y, shared, 0), 1.0f / float(p.dim), p.eps);
+  for (int first = 0; first < padded; first += kLongStep) {   // (whole warps: a block of 32 is four lanes)
+    const int c = first + threadIdx.x * 8;
     float y[8] = {};
-    if (c < p.dim) {
+    if (c < dim) {
       sum8(x + c, res != nullptr ? res + c : nullptr, y);
       if (p.sum != nullptr) store8(static_cast<T*>(p.sum) + at + c, y);
       float w[8];
       if (p.weight != nullptr) load8(p.weight + c, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = p.weight != nullptr ? y[i] * r * w[i] : y[i] * r;
+      for (int i = 0; i < 8; ++i) {
+        const float n = y[i] * k.x * k.y;
+        y[i] = p.weight != nullptr ? n * w[i] : n;
+      }
       if (p.out != nullptr) {
         if (p.out_bf16)
           store8(static_cast<uint16_t*>(p.out) + at + c, y);
@@ -603,9 +902,10 @@ __global__ void __launch_bounds__(kLong) norm_long_vec_kernel(const NormParams p
           store8(static_cast<float*>(p.out) + at + c, y);
       }
     }
-    if (p.out8.data != nullptr)
-      store_row_mx8<kLong, 8, true>(static_cast<uint8_t*>(p.out8.data) + int64_t(blockIdx.x) * nb * 32 + first,
-                                    p.out8.scales + int64_t(blockIdx.x) * nb + (first >> 5), nb * 32 - first, int(threadIdx.x), y);
+    if (p.out8.data != nullptr) {
+      const int64_t q = int64_t(blockIdx.x) * padded + first;
+      store_row_mx8<kLong, 8, true>(static_cast<uint8_t*>(p.out8.data) + q, p.out8.scales + (q >> 5), padded - first, int(threadIdx.x), y);
+    }
   }
 }
 
@@ -614,7 +914,7 @@ __global__ void __launch_bounds__(kLong) norm_long_vec_kernel(const NormParams p
 constexpr int64_t kLongShared = 100 * 1024;
 
 template <typename T, bool SHARED>
-__global__ void __launch_bounds__(kLong) norm_grad_long_vec_kernel(const NormGradParams p) {
+__global__ void __launch_bounds__(kLong) norm_grad_long_vec_kernel(const __grid_constant__ NormGradParams p) {
   extern __shared__ __align__(16) uint8_t slots[];
   __shared__ float shared[2][64];
   ptx::griddep_launch_dependents();
@@ -655,9 +955,14 @@ __global__ void __launch_bounds__(kLong) norm_grad_long_vec_kernel(const NormGra
       }
     }
     const float2 sums = team_sums<kLong>(squares, dot, shared, parity);
+    const float mean = fmaf(sums.x, inv_dim, p.eps), r = inverse_sqrt(mean), m = sums.y * r * inv_dim;
+    if (!usual(mean, m)) {
+      scaled_long_grad<T>(p, row, shared, parity, row != int64_t(blockIdx.x) ? sum : nullptr,
+                          part == nullptr ? nullptr : SHARED && row + gridDim.x < p.rows ? sum : part);
+      parity ^= 1;
+      continue;
+    }
     parity ^= 1;
-    const float r = inverse_rms(sums.x, inv_dim, p.eps);
-    const float m = sums.y * r * inv_dim;
     for (int64_t c = threadIdx.x * 8; c < p.dim; c += kLongStep) {   // a column is one thread's: no order to keep
       float s[8], d[8], g[8];
       fetch(c, s, d, g);
@@ -707,7 +1012,8 @@ cudaError_t with_team(int64_t dim, F&& f) {
 template <typename T>
 cudaError_t norm_as(const NormParams& p, cudaStream_t stream) {
   if (team_of(p.dim) == 0)
-    return launch_kernel(p.dim % 8 == 0 ? norm_long_vec_kernel<T> : norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(kLong), 0, 1, true, stream, p);
+    return launch_kernel(p.dim % 8 == 0 && p.eps > 0.0f ? norm_long_vec_kernel<T> : norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(kLong),
+                         0, 1, true, stream, p);
   return with_team(p.dim, [&](auto team) {
     constexpr int TEAM = decltype(team)::value, kTeams = kBlock<TEAM> / TEAM;
     if (p.dim % 8 != 0)

@@ -8,7 +8,7 @@ import matrix_optimizers_zero_gb300 as mo
 import test_gpu_layer_ops as base
 from gpu_util import f64
 from oracle import layer_ops as ol
-from test_gpu_layer_ops import BF16, clean, dev, empty8
+from test_gpu_layer_ops import BF16, F32, ROUND, clean, data, dev, empty8, norm_tol, packed, within, within8
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,110 @@ def test_slopes_keep_their_relative_accuracy(name):
     live = size > 1e-35
     tol = (4 * 2.0 ** -23 + 2 * relative(v, name)) * size
     assert (np.abs(f64(db) - want) <= tol)[live].all(), (np.abs(f64(db) - want) / tol)[live].max()
+
+
+# ---------------------------------------------------------------- norms at both ends of fp32's range
+
+# Sizes of a row and of its gradient: squares that overflow, that are 0, and products of the two that do; rows of
+# ordinary size lie between them, in the same blocks.
+SCALES = [(1.0, 1.0), (1e20, 1.0), (1.0, 1e-20), (1e-23, 1.0), (1e38, 1e38), (1.0, 1.0), (3e18, 1e30), (1e-38, 1e-6), (1e10, 1e32), (1e-20, 1e-25),
+          (1e30, 1e-5), (1e-30, 1e-10), (1.0, 1e35)]
+NORM_DIMS = [7, 48, 256, 257, 1000, 1001, 2048, 4096, 4099, 8192, 8200, 9001]
+
+
+def scaled(rows, dim, which, dtype, seed):
+    """Numbers of both signs, between half and twice their row's size."""
+    g = torch.Generator().manual_seed(seed + dim)
+    u = (torch.rand(rows, dim, generator=g) * 1.5 + 0.5) * torch.where(torch.rand(rows, dim, generator=g) < 0.5, -1.0, 1.0)
+    size = torch.tensor([SCALES[i % len(SCALES)][which] for i in range(rows)], dtype=torch.float64)
+    return (u.double() * size[:, None]).to(dtype).to(dev())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", NORM_DIMS)
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-35, 1e7, 1e30])
+def test_norm_of_rows_of_every_size(dim, dtype, eps):
+    rows = 2 * len(SCALES) + 1
+    x, r, w = scaled(rows, dim, 0, dtype, 1), scaled(rows, dim, 0, dtype, 2) * 0.125, data(dim, dtype=F32, seed=3)
+    eps = float(np.float32(eps))
+    for residual in (None, r):
+        o, q = torch.empty(rows, dim, device=dev()), empty8(rows, dim)
+        mo.rms_norm(x, o, weight=w, eps=eps, residual=residual, out8=q)
+        clean()
+        want, _ = ol.rms_norm(f64(x), f64(w), eps, None if residual is None else f64(r))
+        # (s is rounded to fp32; scaling is exact but for what is 2^-126 of the row's largest)
+        tol = norm_tol(want) + 2 * 2.0 ** -24 * np.abs(want)
+        within(o, want, tol + ROUND[F32] * np.abs(want), "out")
+        within8(q, want, tol, "out8")
+
+
+@pytest.mark.parametrize("dtype,mx8", [(F32, False), (BF16, False), (F32, True), (BF16, True)])
+@pytest.mark.parametrize("dim", NORM_DIMS)
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e30])
+def test_norm_gradient_of_rows_of_every_size(dim, dtype, mx8, eps):
+    rows = 2 * len(SCALES) + 1
+    norm_gradient_case(rows, dim, dtype, mx8, float(np.float32(eps)))
+
+
+@pytest.mark.parametrize("rows,dim", [(700, 4096), (650, 1001), (700, 8200), (640, 8193), (5000, 40)])
+def test_norm_gradient_of_more_rows_than_blocks(rows, dim):
+    """A block takes ordinary rows and others in turn."""
+    norm_gradient_case(rows, dim, F32, False, 0.0)
+
+
+def norm_gradient_case(rows, dim, dtype, mx8, eps):
+    x, dy, w = scaled(rows, dim, 0, dtype, 1), scaled(rows, dim, 1, dtype, 2), data(dim, dtype=F32, seed=3)
+    w = torch.sign(w) * (w.abs() + 0.1).clamp(max=4)
+    q, xv = packed(x) if mx8 else (x, f64(x))
+    dx, dw = torch.empty_like(dy), torch.empty(dim, device=dev())
+    mo.rms_norm_grad(dy, q, dx, weight=w, eps=eps, dweight=dw, workspace=mo.rms_norm_grad_workspace(rows, dim))
+    clean()
+    dyv, wv = f64(dy), f64(w)
+    want, _ = ol.rms_norm_grad(dyv, xv, wv, eps)
+    r = 1 / np.sqrt(np.mean(xv * xv, 1, keepdims=True) + eps)
+    mag = r * (np.abs(dyv * wv) + np.abs(xv * r) * np.mean(np.abs(dyv * wv * xv * r), 1, keepdims=True))
+    # where the gradient itself leaves the type, or terms of it leave fp32, nothing is asked
+    live = (mag < 1e38).all(1)
+    assert live.sum() >= rows * 3 // 4
+    tol = 240 * 2.0 ** -24 * mag
+    within(f64(dx)[live], want[live], (tol + ROUND[dtype] * (np.abs(want) + tol))[live], "dx")
+    # dweight: the rows' terms differ by 60 orders of magnitude; their sum is held by the largest. Columns whose
+    # magnitudes add up to more than fp32 holds (several rows of 1e38) may be infinite
+    n = np.abs(dyv * xv * r)
+    fits = n.sum(0) < 3.4e38
+    within(f64(dw)[fits], (dyv * xv * r).sum(0)[fits], (rows + 80) * 2.0 ** -24 * n.sum(0)[fits], "dweight")
+    if dtype == F32 and not mx8:   # without them every column fits
+        keep = np.flatnonzero(np.abs(dyv).max(1) < 1e37)
+        part = mo.rms_norm_grad_workspace(len(keep), dim)
+        mo.rms_norm_grad(dy[keep].contiguous(), x[keep].contiguous(), torch.empty(len(keep), dim, device=dev()), weight=w, eps=eps, dweight=dw,
+                         workspace=part)
+        clean()
+        within(dw, (dyv * xv * r)[keep].sum(0), (rows + 80) * 2.0 ** -24 * n[keep].sum(0), "dweight of the others")
+    if dtype == F32 and not mx8:   # each row alone gives the same, whatever its neighbours are
+        for i in range(min(rows, len(SCALES))):
+            if live[i]:
+                one = torch.empty(1, dim, device=dev())
+                mo.rms_norm_grad(dy[i:i + 1].clone(), x[i:i + 1].clone(), one, weight=w, eps=eps)
+                assert torch.equal(one[0], dx[i]), i
+
+
+def test_rows_of_zeros_and_no_numbers_stay_what_they_were():
+    """Rows that scaling says nothing of: zeros give zeros where eps is not 0, and infinities stay in their row."""
+    for dim in (48, 1001, 4096, 8200, 9001):
+        x, w = data(5, dim, dtype=F32), data(dim, dtype=F32, seed=1)
+        alone = torch.empty_like(x)
+        mo.rms_norm(x, alone, weight=w, eps=0.0)
+        x[1] = 0
+        x[2, 3] = float("inf")
+        x[3, 5] = float("nan")
+        o, dx = torch.empty_like(x), torch.empty_like(x)
+        for eps in (1e-6, 1e-38):
+            mo.rms_norm(x, o, weight=w, eps=eps)
+            mo.rms_norm_grad(torch.ones_like(x), x, dx, weight=w, eps=eps)
+            clean()
+            assert not o[1].any() and torch.isfinite(dx[1]).all()
+            assert torch.isnan(o[2, 3]) and torch.isnan(o[3]).all()
+            assert torch.isfinite(o[[0, 4]]).all() and torch.isfinite(dx[[0, 4]]).all() and not torch.isfinite(dx[3]).any()
+        mo.rms_norm(x, o, weight=w, eps=0.0)
+        clean()
+        assert torch.equal(o[[0, 4]], alone[[0, 4]])
