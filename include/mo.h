@@ -411,10 +411,11 @@ int fp4_product(const mo_fp4* a, const mo_fp4* b, void* out, int32_t dtype, cuda
 
 /* ---- the feed-forward half of a transformer layer: norm, products with
  * everything around them in their epilogues, 8-bit activation checkpoints.
- * Weights and activations of products are bf16, sums fp32; what is kept for
- * the backward pass is bf16 or 8 bits. No call needs another's workspace or
- * state; a workspace may be shared by calls in stream order, and one made for
- * more tokens (rows of the norm) serves calls of fewer. */
+ * Weights and activations of products are bf16, sums fp32, of more than 32768
+ * products in slices of as many at most; what is kept for the backward pass is
+ * bf16 or 8 bits. No call needs another's workspace or state; a workspace may be
+ * shared by calls in stream order, and one made for more tokens (rows of the
+ * norm) serves calls of fewer. */
 
 /* A tensor [rows, k] of a call, in one of
  *   MO_F32, MO_BF16   data: the elements, dense; scales NULL
@@ -491,9 +492,8 @@ int linear_forward(const mo_tensor* x, const void* w, int64_t tokens, int64_t co
  * dx [tokens, cols], dw [rows, cols] in their types, dbias fp32 [rows]; each
  * may be NULL, and x and w where nothing needs them. (The residual's gradient
  * is dout.) dz is rounded to bf16 for the products, not for dbias. With
- * accumulate = 1 dw and dbias are added to. Sums over more than 32768 tokens
- * (or, for dx, rows) are taken in slices of as many, joined in fp32. ws:
- * mo_linear_workspace_bytes(.., 1) bytes, 256-byte aligned. */
+ * accumulate = 1 dw and dbias are added to. ws: mo_linear_workspace_bytes(.., 1)
+ * bytes, 256-byte aligned. */
 int linear_grad(const void* dout, const mo_tensor* x, const void* w, int64_t tokens, int64_t cols, int64_t rows,
                 int32_t act, const mo_tensor* pre, void* dx, int32_t dx_dtype, void* dw, int32_t dw_dtype, float* dbias,
                 int32_t accumulate, void* ws, size_t ws_bytes, cudaStream_t stream);

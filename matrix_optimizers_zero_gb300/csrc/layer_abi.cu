@@ -19,10 +19,11 @@ using mo::report_cuda;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxWidth = int64_t(1) << 22;
 constexpr int64_t kMaxElems = int64_t(1) << 37;
-constexpr int64_t kMaxReduction = int64_t(1) << 16;   // of one accumulation
-// Longer sums over tokens or rows are taken in slices of as many: over one very
-// long reduction the tensor core's accumulator loses products far below the
-// running sum (as the Newton-Schulz Gram products do).
+constexpr int64_t kMaxReduction = int64_t(1) << 16;   // columns that a forward product sums over
+// Longer sums are taken in slices of as many, joined in fp32: the tensor core's
+// accumulator cuts what is added off below the running sum, and the loss grows with the
+// number of additions (numbers of one sign, relative to the sum: 1.6e-4 over 32768
+// products, 3.4e-4 over 65536, in two slices 1.6e-4).
 constexpr int64_t kSlice = 32768;
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
@@ -138,6 +139,54 @@ struct Operands {
 // Bytes of the partial sums of a product whose reduction is cut.
 size_t slice_bytes(int64_t k, int64_t m, int64_t n) { return k > kSlice ? align256(size_t(m) * size_t(n) * 4) : 0; }
 
+// An operand's part along the reduction: its rows, or (whole 128-byte lines in, so
+// aligned as the operand is) its columns.
+void cut(Operand& o, bool mn, int64_t k0, int64_t k) {
+  if (mn) {
+    o.p = static_cast<const uint16_t*>(o.p) + k0 * o.ld;
+    o.rows = k;
+  } else {
+    o.p = static_cast<const uint16_t*>(o.p) + k0;
+    o.cols = k;
+  }
+}
+
+// Bytes of the sums that a product with an epilogue starts from where its reduction is
+// cut: of `count` sums [m, n].
+size_t start_bytes(int64_t k, int64_t m, int64_t n, int count) {
+  return k > kSlice ? size_t(count) * align256(size_t(m) * size_t(padded(n)) * 4) : 0;
+}
+
+// Cuts a product's reduction where one accumulation would be too long: the slices but
+// the last are summed in fp32 in `part`, each on top of the last one's, and q is left
+// with the last slice, which starts from there.
+void slice_ahead(mo::Product& q, float* part, int sms, int* status, Launches& run, cudaStream_t stream) {
+  if (mo::longest_sum(q, sms) <= kSlice) return;
+  const mo::Target whole = q.t[0];
+  const int64_t ld = padded(whole.n);
+  mo::Product s;
+  s.a_mn = q.a_mn;
+  s.b_mn = q.b_mn;
+  s.count = q.epi == mo::kEpiGated ? 2 : 1;
+  s.k = kSlice;
+  int64_t k0 = 0;
+  for (; q.k - k0 > kSlice && run.error == cudaSuccess; k0 += kSlice) {
+    for (int i = 0; i < s.count; ++i) {
+      float* sums = part + i * (align256(size_t(whole.m) * size_t(ld) * 4) / 4);
+      s.a[i] = q.a[0];
+      s.b[i] = q.b[i];
+      cut(s.a[i], q.a_mn, k0, kSlice);
+      cut(s.b[i], q.b_mn, k0, kSlice);
+      s.t[i] = {sums, k0 > 0 ? sums : nullptr, whole.m, whole.n, ld, ld, 0, 0};
+      q.start[i] = sums;
+    }
+    run(mo::launch_product(s, sms, status, stream));
+  }
+  q.k -= k0;
+  cut(q.a[0], q.a_mn, k0, q.k);
+  for (int i = 0; i < s.count; ++i) cut(q.b[i], q.b_mn, k0, q.k);
+}
+
 // A product without activation whose reduction runs over the rows of both
 // operands (or, without a_mn, of the second alone), in slices where it is long:
 // the first slices' sums go to `part` in fp32, each on top of the last one's.
@@ -150,17 +199,8 @@ void sliced_product(const mo::Product& whole, float* part, int sms, int* status,
     float* sums = part;
     for (int i = 0; i < q.count; ++i) {
       if (slices > 1) {
-        auto cut_rows = [&](Operand& o) {
-          o.p = static_cast<const uint16_t*>(o.p) + k0 * o.ld;
-          o.rows = q.k;
-        };
-        cut_rows(q.b[i]);
-        if (q.a_mn) {
-          cut_rows(q.a[i]);
-        } else {
-          q.a[i].p = static_cast<const uint16_t*>(q.a[i].p) + k0;
-          q.a[i].cols = q.k;
-        }
+        cut(q.a[i], q.a_mn, k0, q.k);
+        cut(q.b[i], true, k0, q.k);
         mo::Target& t = q.t[i];
         if (s > 0) t.add = sums, t.add_ld = t.n, t.add_bf16 = 0;
         if (s + 1 < slices) t.out = sums, t.ld = t.n, t.out_bf16 = 0;
@@ -197,7 +237,7 @@ int ffn_shape(int64_t tokens, int64_t dim, int64_t inner) {
 
 // (No less for more tokens: a workspace of the largest batch serves the others.)
 size_t linear_bytes(int64_t tokens, int64_t cols, int64_t rows, bool grad) {
-  size_t b = copy_bytes(tokens, cols) + (cols % 8 != 0 ? copy_bytes(rows, cols) : 0);
+  size_t b = copy_bytes(tokens, cols) + (cols % 8 != 0 ? copy_bytes(rows, cols) : 0) + start_bytes(cols, tokens, rows, 1);
   if (grad) {
     b += copy_bytes(tokens, rows);   // dz
     b += align256(size_t(mo::act_grad_room(tokens, rows)) * size_t(rows) * 4);
@@ -210,12 +250,13 @@ size_t ffn_bytes(int64_t tokens, int64_t dim, int64_t inner, bool grad) {
   size_t b = copy_bytes(tokens, dim) + copy_bytes(tokens, inner);   // x, h
   if (dim % 8 != 0) b += 2 * copy_bytes(inner, dim);
   if (inner % 8 != 0) b += copy_bytes(dim, inner);
+  size_t sums = start_bytes(dim, tokens, inner, 2);   // of one launch at a time
   if (grad) {
+    sums = std::max({sums, slice_bytes(2 * inner, tokens, dim), 3 * slice_bytes(tokens, inner, dim)});
     b += 2 * copy_bytes(tokens, inner);   // dg, du
     if (dim % 8 != 0) b += copy_bytes(tokens, dim);   // dout
-    b += 3 * slice_bytes(tokens, inner, dim);
   }
-  return std::max<size_t>(b, 256);
+  return std::max<size_t>(b + sums, 256);
 }
 
 }  // namespace
@@ -414,6 +455,7 @@ int linear_forward(const mo_tensor* x, const void* w, int64_t tokens, int64_t co
   q.t[0] = target(out, out_dtype, tokens, rows, residual);
   q.k = cols;
   q.bias = bias;
+  slice_ahead(q, static_cast<float*>(space.take(0)), sms, status, run, stream);
   if (run.error == cudaSuccess) run(mo::launch_product(q, sms, status, stream));
   return run.status();
 }
@@ -557,6 +599,7 @@ int gated_ffn_forward(const mo_tensor* x, const void* w_gate, const void* w_up, 
   operand.lay_out(run, stream);
   q.t[0] = {h, nullptr, tokens, inner, ld, 0, 1, 0};
   q.k = dim;
+  slice_ahead(q, static_cast<float*>(space.take(0)), sms, status, run, stream);
   if (run.error == cudaSuccess) run(mo::launch_product(q, sms, status, stream));
   mo::Product down;
   down.a[0] = {h, tokens, inner, ld};
@@ -638,6 +681,7 @@ int gated_ffn_grad(const void* dout, const mo_tensor* x, const mo_tensor* gate, 
   q.out2 = kept[1];
   q.out3 = kept[2];
   q.k = dim;
+  slice_ahead(q, static_cast<float*>(space.take(0)), sms, status, run, stream);
   if (run.error == cudaSuccess) run(mo::launch_product(q, sms, status, stream));
   if (dx != nullptr) {
     mo::Product s;
@@ -651,6 +695,15 @@ int gated_ffn_grad(const void* dout, const mo_tensor* x, const mo_tensor* gate, 
     operand.lay_out(run, stream);
     s.t[0] = target(dx, dx_dtype, tokens, dim);
     s.k = inner;
+    if (mo::longest_sum(s, sms) > kSlice) {   // one after the other, joined in fp32
+      float* sums = static_cast<float*>(space.take(0));
+      s.segments = 1;
+      s.t[0] = target(sums, MO_F32, tokens, dim);
+      if (run.error == cudaSuccess) run(mo::launch_product(s, sms, status, stream));
+      s.a[0] = s.a[1];
+      s.b[0] = s.b[1];
+      s.t[0] = {dx, sums, tokens, dim, dim, dim, dx_dtype == MO_BF16, 0};
+    }
     if (run.error == cudaSuccess) run(mo::launch_product(s, sms, status, stream));
   }
   if (any_dw) {   // up to three products over the tokens, one launch

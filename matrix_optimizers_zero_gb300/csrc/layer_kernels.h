@@ -135,12 +135,16 @@ struct Product {
   int64_t k = 0;
   const float* bias = nullptr;
   Kept pre, pre2;
+  // sums so far, fp32 [m, padded(n)], which the product's are added to (kEpiGated: gate's and up's); one target
+  const float* start[2] = {nullptr, nullptr};
   uint16_t* out2 = nullptr;          // kEpiGatedGrad, pitch t[0].ld
   uint16_t* out3 = nullptr;
   // b may be read while the previous launch runs: that launch is a product for which is_narrow or is_few
   // holds, and does not write b
   bool early = false;
 };
+// The most products that one accumulator of the tensor cores takes (0: the product does not use them).
+int64_t longest_sum(const Product& q, int sms);
 // Whether a product goes to the kernel for one or two rows, and otherwise to the one for few.
 bool is_few(const Product& q, int sms);
 bool is_narrow(const Product& q, int sms);

@@ -147,7 +147,7 @@ auto kernel_for(int64_t rows) {
 // the other kernel; 256 -> 4096: 2.5 and 3.6; 512 -> 50304: 12.2 and 13.4).
 bool is_few(const Product& q, int sms) {
   const Target& t = q.t[0];
-  return t.m <= 2 && q.count == 1 && q.segments == 1 && !q.a_mn && !q.b_mn && q.epi != kEpiGatedGrad && q.pre.data == nullptr &&
+  return t.m <= 2 && q.count == 1 && q.segments == 1 && !q.a_mn && !q.b_mn && q.epi != kEpiGatedGrad && q.pre.data == nullptr && q.start[0] == nullptr &&
          q.k % 8 == 0 && t.m * q.k * 2 <= kRowBytes && (q.k >= 512 || t.n <= int64_t(kBlocks) * kWarps * sms);
 }
 

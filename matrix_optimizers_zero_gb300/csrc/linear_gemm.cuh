@@ -37,6 +37,8 @@ struct GemmParams {
   int32_t early;                 // narrow: the columns' operand may be read before the previous launch has ended
   int32_t act;
   const float* bias;
+  const float* start[2];         // sums so far, or null
+  int64_t start_ld;
   Kept pre, pre2;
   int32_t pre_align;             // of bf16 rows, as above; of 8-bit codes 32 or 16
   int32_t pre_bulk;              // pairs: they are stored by TMA
@@ -342,7 +344,18 @@ __device__ __forceinline__ float kept_at(const Kept& q, int64_t row, int64_t col
   return load1(static_cast<const uint16_t*>(q.data) + row * n + col);
 }
 
+// The sums so far of N columns of a row, added; rows of a multiple of 64, so all of them are there.
+template <int N>
+__device__ __forceinline__ void add_start(const float* p, float (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N / 4; ++j) {
+    const float4 x = reinterpret_cast<const float4*>(p)[j];
+    v[4 * j] += x.x, v[4 * j + 1] += x.y, v[4 * j + 2] += x.z, v[4 * j + 3] += x.w;
+  }
+}
+
 // Few rows: tiles of 128 columns, the reduction split over clusters.
+int64_t narrow_parts(const Product& q, int sms);   // of the reduction
 cudaError_t launch_narrow(const Product& q, GemmParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_few(const Product& q, int sms, cudaStream_t stream);
 bool encode_operand(CUtensorMap* map, const Operand& o, uint32_t box_rows);

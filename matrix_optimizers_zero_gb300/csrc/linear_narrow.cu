@@ -107,6 +107,10 @@ template <Epilogue EPI>
 __device__ __forceinline__ void finish(const GemmParams& p, const GemmTarget& t, int64_t row, int64_t col, float (&x)[4], float (&y)[4]) {
   const int live = int(max(int64_t(0), min(int64_t(4), t.n - col)));
   const bool vec = (t.n & 3) == 0;
+  if (p.start[0] != nullptr && live > 0) {
+    add_start(p.start[0] + row * p.start_ld + col, x);
+    if (EPI == kEpiGated) add_start(p.start[1] + row * p.start_ld + col, y);
+  }
   if constexpr (EPI == kEpiLinear) {
     if (p.bias != nullptr) {
 #pragma unroll
@@ -356,6 +360,24 @@ __global__ void __launch_bounds__(kThreads<NT>) linear_narrow_kernel(const __gri
   if (warp == 1) ptx::tmem_dealloc_one(tmem, kCols<EPI, NT>);
 }
 
+// The reduction in as many parts (2^log) as leave all clusters resident and four stages a CTA. Clusters of 4
+// and 8 do not fill the GPU's parts evenly: with a CTA an SM (all its memory), 36 and 15 of 38 and 19 fit on
+// 152 SMs, with two twice as many. One cluster more than fit takes another round (512 x 512 over 4096 in 16
+// clusters of 8: 15.8 us, with two CTAs an SM 10.3).
+template <Epilogue EPI, int NT>
+struct Split {
+  int64_t tiles = 0;
+  int log = 0;
+  bool deep;   // one CTA an SM, with all its memory
+  Split(const Product& q, int sms) {
+    for (int i = 0; i < q.count; ++i) tiles += (q.t[i].m + NT - 1) / NT * ((q.t[i].n + 127) / 128);
+    const int64_t per_sm = smem_of<EPI, NT>(kStages<EPI, NT>) <= 113 * 1024 ? 2 : 1;
+    const int64_t fit[4] = {sms, sms / 2, sms * 47 / 200, sms * 18 / 200}, blocks = (q.k + kBlockK - 1) / kBlockK * q.segments;
+    for (int i = 1; i < 4 && tiles <= fit[i] * per_sm && blocks >= (4 << i); ++i) log = i;
+    deep = tiles <= fit[log];
+  }
+};
+
 template <Epilogue EPI, bool Q_MN, bool P_MN, int NT>
 cudaError_t narrow_as(const Product& q, GemmParams& p, int sms, cudaStream_t stream) {
   const int n = std::max(q.count, q.segments);
@@ -372,36 +394,45 @@ cudaError_t narrow_as(const Product& q, GemmParams& p, int sms, cudaStream_t str
     tiles += int64_t(t.tiles_m) * t.tiles_n;
   }
   p.tiles = int32_t(tiles);
-  // The reduction in as many parts as leave all clusters resident and four stages a CTA. Clusters of 4 and 8
-  // do not fill the GPU's parts evenly: with a CTA an SM (all its memory), 36 and 15 of 38 and 19 fit on 152
-  // SMs, with two twice as many. One cluster more than fit takes another round (512 x 512 over 4096 in 16
-  // clusters of 8: 15.8 us, with two CTAs an SM 10.3).
-  const int64_t per_sm = smem_of<EPI, NT>(kStages<EPI, NT>) <= 113 * 1024 ? 2 : 1;
-  const int64_t fit[4] = {sms, sms / 2, sms * 47 / 200, sms * 18 / 200};
-  unsigned parts = 1;
-  int log = 0;
-  for (int i = 1; i < 4 && tiles <= fit[i] * per_sm && p.blocks * q.segments >= (4 << i); ++i) parts = 1u << i, log = i;
-  p.stages = tiles <= fit[log] ? kDeep<EPI, NT> : kStages<EPI, NT>;
+  const Split<EPI, NT> split(q, sms);
+  const unsigned parts = 1u << split.log;
+  p.stages = split.deep ? kDeep<EPI, NT> : kStages<EPI, NT>;
   auto kern = linear_narrow_kernel<EPI, Q_MN, P_MN, NT>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem_of<EPI, NT>(kDeep<EPI, NT>));
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(unsigned(tiles * parts)), dim3(kThreads<NT>), smem_of<EPI, NT>(p.stages), parts, true, stream, p);
 }
 
-template <Epilogue EPI, bool P_MN>
-cudaError_t narrow_rows(const Product& q, GemmParams& p, int sms, cudaStream_t stream) {
-  if (q.t[0].m <= 16) return narrow_as<EPI, false, P_MN, 16>(q, p, sms, stream);
-  if (q.t[0].m <= 64) return narrow_as<EPI, false, P_MN, 64>(q, p, sms, stream);
-  return narrow_as<EPI, false, P_MN, 128>(q, p, sms, stream);
+// f(variant) for the kernel that a product takes.
+template <Epilogue EPI, bool Q_MN, bool P_MN, int NT>
+struct Variant {
+  static int64_t parts(const Product& q, int sms) { return int64_t(1) << Split<EPI, NT>(q, sms).log; }
+  static cudaError_t launch(const Product& q, GemmParams& p, int sms, cudaStream_t stream) {
+    return narrow_as<EPI, Q_MN, P_MN, NT>(q, p, sms, stream);
+  }
+};
+template <Epilogue EPI, bool P_MN, typename F>
+auto with_rows(const Product& q, F&& f) {
+  if (q.t[0].m <= 16) return f(Variant<EPI, false, P_MN, 16>());
+  if (q.t[0].m <= 64) return f(Variant<EPI, false, P_MN, 64>());
+  return f(Variant<EPI, false, P_MN, 128>());
+}
+template <typename F>
+auto with_variant(const Product& q, F&& f) {
+  if (q.epi == kEpiGated) return with_rows<kEpiGated, false>(q, f);
+  if (q.epi == kEpiGatedGrad) return with_rows<kEpiGatedGrad, true>(q, f);
+  if (q.a_mn) return f(Variant<kEpiLinear, true, true, 128>());
+  return q.b_mn ? with_rows<kEpiLinear, true>(q, f) : with_rows<kEpiLinear, false>(q, f);
 }
 
 }  // namespace
 
+int64_t narrow_parts(const Product& q, int sms) {
+  return with_variant(q, [&](auto v) { return decltype(v)::parts(q, sms); });
+}
+
 cudaError_t launch_narrow(const Product& q, GemmParams& p, int sms, cudaStream_t stream) {
-  if (q.epi == kEpiGated) return narrow_rows<kEpiGated, false>(q, p, sms, stream);
-  if (q.epi == kEpiGatedGrad) return narrow_rows<kEpiGatedGrad, true>(q, p, sms, stream);
-  if (q.a_mn) return narrow_as<kEpiLinear, true, true, 128>(q, p, sms, stream);
-  return q.b_mn ? narrow_rows<kEpiLinear, true>(q, p, sms, stream) : narrow_rows<kEpiLinear, false>(q, p, sms, stream);
+  return with_variant(q, [&](auto v) { return decltype(v)::launch(q, p, sms, stream); });
 }
 
 }  // namespace mo

@@ -82,6 +82,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       float v[32];
       tmem_chunk(tb + uint32_t(c), v);
       if (row0 >= t.m || col >= t.n) continue;
+      if (PARTS == 2 && p.start[0] != nullptr && row < t.m) add_start(p.start[0] + row * p.start_ld + col, v);
       reuse();
       if (p.bias != nullptr) {
         if (col + 32 <= t.n) {
@@ -133,6 +134,10 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       tmem_chunk(tb + uint32_t(c), g);
       tmem_chunk(tb + uint32_t(width / 2 + c), u);
       if (row0 >= t.m || col >= t.n) continue;
+      if (p.start[0] != nullptr && row < t.m) {
+        add_start(p.start[0] + row * p.start_ld + col, g);
+        add_start(p.start[1] + row * p.start_ld + col, u);
+      }
       reuse();
       if (p.pre.data != nullptr) {
         keep_chunk(p.pre, p.pre_bulk != 0, p.pre_align, row0, t.m, col, t.n, g, scratch + 2048, turn);
@@ -177,6 +182,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       reuse();
 #pragma unroll
       for (int i = 0; i < 16; ++i) dh[i] = __uint_as_float(r[i]);
+      if (PARTS == 2 && p.start[0] != nullptr && row < t.m) add_start(p.start[0] + row * p.start_ld + col, dh);
       with_act(p.act, [&](auto act) { gate_grad_all<decltype(act)::value>(g, u, dh); });
       put_bf16(scratch, g);
       put_bf16(scratch + 1024, dh);
@@ -501,7 +507,8 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
   constexpr int kMost = EPI == kEpiGated ? 8 : kMostWarps;
   bool light = EPI == kEpiLinear && q.act == MO_ACT_NONE && q.pre.data == nullptr;
   for (int i = 0; i < q.count; ++i) light = light && p.t[i].bulk && p.t[i].add == nullptr;
-  const bool few = kMost == 8 || int64_t(p.blocks) * q.segments > (EPI == kEpiGatedGrad ? 32 : light ? 12 : 24);
+  // (Sums so far belong to reductions that are longer still: eight warps.)
+  const bool few = kMost == 8 || q.start[0] != nullptr || int64_t(p.blocks) * q.segments > (EPI == kEpiGatedGrad ? 32 : light ? 12 : 24);
   auto kern = few ? linear_pair_kernel<EPI, A_MN, B_MN, 8> : linear_pair_kernel<EPI, A_MN, B_MN, kMost>;
   const size_t smem = few ? kSmem<8> : kSmem<kMostWarps>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
@@ -543,6 +550,12 @@ bool is_narrow(const Product& q, int sms) {
   return (rows <= 64 && !q.a_mn) || (pair_tiles * 2 < sms / 2 && blocks >= std::max<int64_t>(16, odd ? 0 : tiles / 2));
 }
 
+int64_t longest_sum(const Product& q, int sms) {
+  if (is_few(q, sms)) return 0;
+  const int64_t blocks = (q.k + kBlockK - 1) / kBlockK * q.segments, parts = is_narrow(q, sms) ? narrow_parts(q, sms) : 1;
+  return (blocks + parts - 1) / parts * kBlockK;
+}
+
 cudaError_t launch_product(const Product& q, int sms, int* status, cudaStream_t stream) {
   if (is_few(q, sms)) return launch_few(q, sms, stream);
   GemmParams p = {};
@@ -551,6 +564,9 @@ cudaError_t launch_product(const Product& q, int sms, int* status, cudaStream_t 
   p.blocks = int32_t((q.k + kBlockK - 1) / kBlockK);
   p.act = q.act;
   p.bias = q.bias;
+  p.start[0] = q.start[0];
+  p.start[1] = q.start[1];
+  p.start_ld = padded(q.t[0].n);
   p.pre = q.pre;
   p.pre2 = q.pre2;
   p.out2 = q.out2;

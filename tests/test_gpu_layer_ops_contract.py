@@ -199,3 +199,124 @@ def test_rows_of_zeros_and_no_numbers_stay_what_they_were():
         mo.rms_norm(x, o, weight=w, eps=0.0)
         clean()
         assert torch.equal(o[[0, 4]], alone[[0, 4]])
+
+
+# ---------------------------------------------------------------- long reductions
+
+SLICE = 32768
+
+
+def large(*shape, dtype=BF16, seed=0, std=1.0):
+    """data, made on the GPU."""
+    g = torch.Generator(dev()).manual_seed(seed + sum(shape))
+    return (torch.randn(shape, generator=g, device=dev()) * std).to(dtype)
+
+
+def positive(*shape, seed=0, std=1.0):
+    return (large(*shape, seed=seed, std=std).abs() + std / 2).to(BF16)
+
+
+# CTA pairs (more than 38 tiles of 256), clusters that are too many to split the reduction, and the kernels that
+# split it by themselves (few columns; one row).
+@pytest.mark.parametrize("t,k,n", [(520, 65536, 4900), (520, 40001, 4900), (64, 40000, 20004), (12, 33000, 20001), (300, 65536, 256), (1, 65536, 300)])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_long_forward_sums_are_joined_in_fp32(t, k, n, out):
+    """No accumulation is longer than 32768 products: the call gives the bits of a call for each slice, the second
+    on top of the first. (The split kernels' own slices are shorter; theirs is the bound alone.)"""
+    x, w, b = positive(t, k), positive(n, k, seed=1, std=k ** -0.5), large(n, dtype=F32, seed=2)
+    o = torch.empty(t, n, dtype=out, device=dev())
+    mo.linear(x, w, o, bias=b, workspace=mo.linear_workspace(t, k, n))
+    first, two = torch.empty(t, n, device=dev()), torch.empty(t, n, device=dev())
+    x0, x1, w0, w1 = (v.contiguous() for v in (x[:, :SLICE], x[:, SLICE:], w[:, :SLICE], w[:, SLICE:]))
+    ws = mo.linear_workspace(t, SLICE, n)
+    mo.linear(x0, w0, first, workspace=ws)
+    mo.linear(x1, w1, two, residual=first, workspace=mo.linear_workspace(t, k - SLICE, n))
+    clean()
+    if t > 1 and n > 300:
+        assert torch.equal(o, (two + b).to(out))
+    # terms of one sign: an addition of 16 products cuts off at most 2^-22 of the sum so far, which is half of the
+    # last one on average
+    rows = slice(0, min(t, 64))
+    want = f64(x[rows].double() @ w.double().T + b.double())
+    size = f64(x[rows].double() @ w.double().T)
+    tol = (SLICE / 16 + 4) * 2.0 ** -23 * size + 2.0 ** -23 * np.abs(want)
+    within(f64(o[rows]), want, tol + ROUND[out] * (np.abs(want) + tol))
+
+
+@pytest.mark.parametrize("t,k,n", [(520, 40000, 4864), (64, 40001, 19500)])
+def test_long_forward_sums_with_activation_and_copies(t, k, n):
+    """What follows the sum follows the joined one."""
+    x, w, b, r = large(t, k), large(n, k, seed=1, std=k ** -0.5), large(n, dtype=F32, seed=2), large(t, n, dtype=F32, seed=3)
+    ws = mo.linear_workspace(t, k, n)
+    z, pre, z8, o = torch.empty(t, n, dtype=BF16, device=dev()), torch.empty(t, n, dtype=BF16, device=dev()), empty8(t, n), torch.empty(t, n, device=dev())
+    mo.linear(x, w, z, bias=b, workspace=ws)
+    mo.linear(x, w, o, bias=b, activation="relu", residual=r, pre=pre, workspace=ws)
+    clean()
+    assert torch.equal(z, pre)
+    wide = torch.empty(t, n, device=dev())
+    mo.linear(x, w, wide, bias=b, workspace=ws)
+    assert torch.equal(o, torch.relu(wide) + r)
+    mo.linear(x, w, r, bias=b, activation="relu", residual=r, pre=z8, workspace=ws)
+    q = empty8(t, n)
+    mo.mx8_quantize(wide, q)
+    clean()
+    assert torch.equal(r, o) and torch.equal(q.codes, z8.codes) and torch.equal(q.scales, z8.scales)
+
+
+@pytest.mark.parametrize("t,d,f", [(520, 33000, 2500), (48, 40000, 9999), (70, 33001, 300)])
+def test_gated_block_of_long_rows(t, d, f):
+    """gate and up are the sums that linear gives, and the backward pass's dh is taken in slices too."""
+    x, wg, wu, wd = large(t, d), large(f, d, seed=1, std=d ** -0.5), large(f, d, seed=2, std=d ** -0.5), large(d, f, seed=3, std=f ** -0.5)
+    gate, up, o = torch.empty(t, f, dtype=BF16, device=dev()), torch.empty(t, f, dtype=BF16, device=dev()), torch.empty(t, d, device=dev())
+    ws = mo.gated_ffn_workspace(t, d, f, grad=True)
+    mo.gated_ffn(x, wg, wu, wd, o, gate=gate, up=up, workspace=ws)
+    clean()
+    D = torch.float64
+    g, u = x.to(D) @ wg.to(D).T, x.to(D) @ wu.to(D).T
+    size = [x.to(D).abs() @ v.to(D).abs().T for v in (wg, wu)]
+    for got, want, s in ((gate, g, size[0]), (up, u, size[1])):
+        tol = f64((d / 16 + 4) * 2.0 ** -23 * s)
+        within(got, f64(want), tol + ROUND[BF16] * (np.abs(f64(want)) + tol))
+    # backward from the kept values, as they are
+    dout = large(t, d, seed=5)
+    dw = [torch.empty(v.shape, device=dev()) for v in (wg, wu, wd)]
+    dx = torch.empty(t, d, device=dev())
+    mo.gated_ffn_grad(dout, x, gate, up, wg, wu, wd, activation="relu", dx=dx, dw_gate=dw[0], dw_up=dw[1], dw_down=dw[2], workspace=ws)
+    clean()
+    gv, uv, dv = gate.to(D), up.to(D), dout.to(D)
+    dh, edh = dv @ wd.to(D), (d / 16 + 4) * 2.0 ** -23 * (dv.abs() @ wd.to(D).abs())
+    on = (gv > 0).to(D)
+    dg, du = dh * uv * on, dh * gv * on
+    eg, eu = edh * (uv * on).abs(), edh * (gv * on).abs()
+    R = ROUND[BF16] + 2.0 ** -22
+    eg, eu = eg + R * (dg.abs() + eg), eu + R * (du.abs() + eu)
+    e = eg @ wg.to(D).abs() + eu @ wu.to(D).abs() + (2 * f / 16 + 8) * 2.0 ** -23 * ((dg.abs() + eg) @ wg.to(D).abs() + (du.abs() + eu) @ wu.to(D).abs())
+    want = dg @ wg.to(D) + du @ wu.to(D)
+    within(dx, f64(want), f64(e + 2.0 ** -23 * want.abs()), "dx")
+    for got, m, em in ((dw[0], dg, eg), (dw[1], du, eu)):
+        want = m.T @ x.to(D)
+        e = em.T @ x.to(D).abs() + (t / 16 + 4) * 2.0 ** -23 * ((m.abs() + em).T @ x.to(D).abs())
+        within(got, f64(want), f64(e + 2.0 ** -23 * want.abs()), "dw")
+
+
+@pytest.mark.parametrize("t,d,f", [(520, 4900, 32768), (520, 4864, 20001), (64, 20004, 32768), (300, 256, 32768), (3, 33, 32768)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gated_input_gradient_of_a_wide_block(t, d, f, dtype):
+    """Both halves of dx together are longer than one accumulation may be."""
+    dout, gate, up = positive(t, d, seed=5), positive(t, f, seed=6), positive(t, f, seed=7)
+    wg, wu, wd = positive(f, d, seed=1, std=f ** -0.5), positive(f, d, seed=2, std=f ** -0.5), positive(d, f, seed=3, std=d ** -0.5)
+    dx = torch.empty(t, d, dtype=dtype, device=dev())
+    ws = mo.gated_ffn_workspace(t, d, f, grad=True)
+    ws.fill_(0xFF)
+    mo.gated_ffn_grad(dout, None, gate, up, wg, wu, wd, activation=None, dx=dx, workspace=ws)
+    clean()
+    D = torch.float64
+    rows = slice(0, min(t, 64))
+    dh = dout[rows].to(D) @ wd.to(D)
+    edh = (d / 16 + 4) * 2.0 ** -23 * dh
+    a, b = dh * up[rows].to(D), dh * gate[rows].to(D)
+    ea, eb = ((ROUND[BF16] + 2.0 ** -22) * (v + e) + e for v, e in ((a, edh * up[rows].to(D)), (b, edh * gate[rows].to(D))))
+    want = a @ wg.to(D) + b @ wu.to(D)
+    # roundings of a and b go either way; they are a sixteenth of their bound together (a sum of thousands): all of it is allowed
+    e = ea @ wg.to(D) + eb @ wu.to(D) + (SLICE / 16 + 8) * 2.0 ** -23 * 1.01 * want
+    within(f64(dx[rows]), f64(want), f64(e + ROUND[dtype] * (want + e)))
