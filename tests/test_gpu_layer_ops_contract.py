@@ -179,6 +179,37 @@ def norm_gradient_case(rows, dim, dtype, mx8, eps):
                 assert torch.equal(one[0], dx[i]), i
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,dim", [(27, d) for d in NORM_DIMS] + [(700, 4096), (650, 1001), (700, 8200), (640, 8193)])
+def test_norms_of_rows_of_every_size_in_place(rows, dim, dtype):
+    """What replaces its input has the bits of what does not, and so has a gradient that another is added to."""
+    x, r, w = scaled(rows, dim, 0, dtype, 1), scaled(rows, dim, 0, dtype, 2) * 0.125, data(dim, dtype=F32, seed=3)
+    out, total = torch.empty_like(x), torch.empty_like(x)
+    q8, p8 = empty8(rows, dim), empty8(rows, dim)
+    mo.rms_norm(x, out, weight=w, eps=0.0, residual=r, sum_out=total, out8=q8)
+    a, b = x.clone(), r.clone()
+    mo.rms_norm(a, a, weight=w, eps=0.0, residual=b, sum_out=b, out8=p8)
+    clean()
+    assert torch.equal(a, out) and torch.equal(b, total) and torch.equal(q8.codes, p8.codes) and torch.equal(q8.scales, p8.scales)
+    assert torch.equal(total, (x.float() + r.float()).to(dtype))
+    dy, ws = scaled(rows, dim, 1, dtype, 4), mo.rms_norm_grad_workspace(rows, dim)
+    plain, dx, dw, dv = torch.empty_like(x), torch.empty_like(x), torch.empty(dim, device=dev()), torch.empty(dim, device=dev())
+    mo.rms_norm_grad(dy, x, plain, weight=w, eps=0.0, dweight=dw, workspace=ws)
+    dres = (plain.float() * 0.5).nan_to_num(0, 0, 0).to(dtype)      # of each row's own size
+    mo.rms_norm_grad(dy, x, dx, weight=w, eps=0.0, dresidual=dres, dweight=dv, workspace=ws)
+    clean()
+    assert torch.equal(dw.view(torch.int32), dv.view(torch.int32))
+    live = torch.isfinite(plain) & (plain.abs() < 1e38) & (plain.abs() > 1e-36)
+    got, want = f64(dx)[live.cpu().numpy()], (f64(plain) + f64(dres))[live.cpu().numpy()]
+    # plain is rounded to its type; dx is not before dres is added
+    assert (np.abs(got - want) <= (2 * ROUND[dtype] + 2.0 ** -22) * np.abs(f64(plain) * 1.5)[live.cpu().numpy()]).all()
+    for same in (dy, dres):
+        again = same.clone()
+        mo.rms_norm_grad(again if same is dy else dy, x, again, weight=w, eps=0.0, dresidual=again if same is dres else dres, dweight=dv, workspace=ws)
+        clean()
+        assert torch.equal(again.view(torch.uint8), dx.view(torch.uint8)) and torch.equal(dw.view(torch.int32), dv.view(torch.int32))
+
+
 def test_rows_of_zeros_and_no_numbers_stay_what_they_were():
     """Rows that scaling says nothing of: zeros give zeros where eps is not 0, and infinities stay in their row."""
     for dim in (48, 1001, 4096, 8200, 9001):
