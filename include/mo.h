@@ -473,11 +473,13 @@ int rms_norm_grad(const void* dy, int32_t dtype, const mo_tensor* x, int64_t row
  * 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))). */
 enum mo_activation { MO_ACT_NONE = 0, MO_ACT_RELU = 1, MO_ACT_GELU = 2, MO_ACT_GELU_TANH = 3, MO_ACT_SILU = 4 };
 
-/* z = x w^T + bias, out = act(z) + residual, in one launch.
+/* z = x w^T + bias, out = act(z) + residual, in one launch (one more where x or w
+ * is laid out first, and one for each 32768 columns beyond the first).
  *   x [tokens, cols] bf16 or 8 bits; w bf16 [rows, cols]; bias fp32 [rows] or
  *   NULL; residual (or NULL) and out [tokens, rows] of `out_dtype`, out may be
- *   residual itself (unless that is x too: x is read by all tiles); pre (or NULL; with an activation only): receives z
- *   [tokens, rows] for the backward pass, in bf16 or 8 bits
+ *   residual itself (unless that is x too: x is read by all tiles); pre (or
+ *   NULL; with an activation only): receives z [tokens, rows] for the backward
+ *   pass, in bf16 or 8 bits
  * tokens up to 2^30, cols up to 2^16, rows up to 2^22. ws: device scratch of
  * mo_linear_workspace_bytes(.., 0) bytes, 256-byte aligned: 8-bit operands, and
  * operands whose rows are no multiple of 8, are laid out there first. */
@@ -500,7 +502,8 @@ int linear_grad(const void* dout, const mo_tensor* x, const void* w, int64_t tok
 
 /* Gated feed-forward block: g = x w_gate^T, u = x w_up^T, h = act(g) u,
  * out = h w_down^T + residual, in two launches (g, u and h in one; h, in bf16,
- * is in the workspace).
+ * is in the workspace), and those that linear_forward has in addition: one where x,
+ * w_gate and w_up are laid out, one for w_down.
  *   x [tokens, dim] bf16 or 8 bits; w_gate, w_up bf16 [inner, dim], w_down bf16
  *   [dim, inner]; residual (or NULL) and out [tokens, dim] of `out_dtype`, out
  *   may be residual itself, also where that is x; gate, up (both or neither, of one type): receive g

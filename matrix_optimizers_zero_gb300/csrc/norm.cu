@@ -21,7 +21,7 @@
 namespace mo {
 namespace {
 
-// A team of TEAM threads holds a row of at most TEAM V elements, V a thread:
+// A team of TEAM threads holds a row of at most 8 TEAM elements, eight a thread:
 // eight neighbours of every 8 TEAM where rows are 16-byte aligned (VEC), one of
 // every TEAM otherwise. Either way 32 elements of a block lie in one warp.
 template <int TEAM, bool VEC>
@@ -32,25 +32,22 @@ __device__ __forceinline__ int64_t column(int i, int t) {
 template <int TEAM>
 constexpr int kBlock = TEAM < 128 ? 128 : TEAM;
 
-template <int TEAM, int V, bool VEC, typename T>
-__device__ __forceinline__ void store_row(T* p, int64_t dim, int t, const float (&v)[V]) {
+// Elements TEAM apart.
+template <int TEAM, typename T>
+__device__ __forceinline__ void store_row(T* p, int64_t dim, int t, const float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < V; i += VEC ? 8 : 1) {
-    const int64_t c = column<TEAM, VEC>(i, t);
-    if (c >= dim) continue;
-    if constexpr (VEC)
-      store8(p + c, *reinterpret_cast<const float (*)[8]>(&v[i]));
-    else
-      store1(p + c, v[i]);
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = column<TEAM, false>(i, t);
+    if (c < dim) store1(p + c, v[i]);
   }
 }
 
 // A row in 8 bits. All threads of a warp come here together; elements past dim
 // are zeros, and the codes of the last block past it too.
-template <int TEAM, int V, bool VEC>
-__device__ __forceinline__ void store_row_mx8(uint8_t* codes, uint8_t* scales, int64_t end, int t, const float (&v)[V]) {
+template <int TEAM, bool VEC>
+__device__ __forceinline__ void store_row_mx8(uint8_t* codes, uint8_t* scales, int64_t end, int t, const float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < V; i += VEC ? 8 : 1) {
+  for (int i = 0; i < 8; i += VEC ? 8 : 1) {
     const int64_t c = column<TEAM, VEC>(i, t);
     float top = fabsf(v[i]);
     if constexpr (VEC) {
@@ -328,7 +325,7 @@ __device__ __noinline__ void scaled_slot_row(const NormParams& p, int64_t row, u
     }
   }
   if (p.out8.data != nullptr)
-    store_row_mx8<TEAM, 8, true>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, f);
+    store_row_mx8<TEAM, true>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, f);
 }
 
 template <int TEAM, typename T>
@@ -404,7 +401,7 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_kernel
     if (p.out8.data != nullptr) {
       float v[8];
       unpair(s, v);
-      store_row_mx8<TEAM, 8, true>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, v);
+      store_row_mx8<TEAM, true>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, v);
     }
     if (!usual(mean))   // once more, from the slots: behind the row, where the check holds nothing up
       scaled_slot_row<TEAM, T>(p, row, start + slot * xs.kSlot, start + (kAhead + 1 + slot) * xs.kSlot, shared, parity);
@@ -584,7 +581,7 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_odd_kernel(const NormParams
   if (!usual(mean))
     k = scaled_odd_row<TEAM>(static_cast<const T*>(p.x) + at, p.residual != nullptr ? static_cast<const T*>(p.residual) + at : nullptr,
                              p.dim, p.eps, shared);
-  if (p.sum != nullptr) store_row<TEAM, 8, false>(static_cast<T*>(p.sum) + at, p.dim, t, s);
+  if (p.sum != nullptr) store_row<TEAM>(static_cast<T*>(p.sum) + at, p.dim, t, s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t c = column<TEAM, false>(i, t);
@@ -594,12 +591,12 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_odd_kernel(const NormParams
   }
   if (p.out != nullptr) {
     if (p.out_bf16)
-      store_row<TEAM, 8, false>(static_cast<uint16_t*>(p.out) + at, p.dim, t, s);
+      store_row<TEAM>(static_cast<uint16_t*>(p.out) + at, p.dim, t, s);
     else
-      store_row<TEAM, 8, false>(static_cast<float*>(p.out) + at, p.dim, t, s);
+      store_row<TEAM>(static_cast<float*>(p.out) + at, p.dim, t, s);
   }
   if (p.out8.data != nullptr)
-    store_row_mx8<TEAM, 8, false>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, s);
+    store_row_mx8<TEAM, false>(static_cast<uint8_t*>(p.out8.data) + row * nb * 32, p.out8.scales + row * nb, nb * 32, t, s);
 }
 
 // dx of a row if it is out of range, from memory; its dy n is added to `part` (null: not
@@ -700,11 +697,11 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const __gri
       dw[i] = fmaf(dy[i], n, dw[i]);
       dy[i] = r * fmaf(-n, m, dy[i] * w[i]) + res[i];
     }
-    if (fits) store_row<TEAM, 8, false>(static_cast<T*>(p.dx) + row * p.dim, p.dim, t, dy);
+    if (fits) store_row<TEAM>(static_cast<T*>(p.dx) + row * p.dim, p.dim, t, dy);
     again = again || !fits;
   }
   float* part = p.part != nullptr ? p.part + team * p.dim : nullptr;
-  if (part != nullptr) store_row<TEAM, 8, false>(part, p.dim, t, dw);
+  if (part != nullptr) store_row<TEAM>(part, p.dim, t, dw);
   if (again)
     for (int64_t row = team; row < p.rows; row += step, parity ^= 1) scaled_odd_grad<TEAM, T>(p, row, part, shared, parity);
 }
@@ -904,7 +901,7 @@ __global__ void __launch_bounds__(kLong, 4) norm_long_vec_kernel(const NormParam
     }
     if (p.out8.data != nullptr) {
       const int64_t q = int64_t(blockIdx.x) * padded + first;
-      store_row_mx8<kLong, 8, true>(static_cast<uint8_t*>(p.out8.data) + q, p.out8.scales + (q >> 5), padded - first, int(threadIdx.x), y);
+      store_row_mx8<kLong, true>(static_cast<uint8_t*>(p.out8.data) + q, p.out8.scales + (q >> 5), padded - first, int(threadIdx.x), y);
     }
   }
 }

@@ -323,10 +323,11 @@ def linear_workspace(tokens: int, cols: int, rows: int, grad: bool = False, devi
 
 
 def linear(x, w, out, bias=None, activation=None, residual=None, pre=None, workspace=None, stream=None) -> None:
-    """out = act(x w^T + bias) + residual, in one launch: x bf16 or an Mx8Tensor
-    [tokens, cols], w bf16 [rows, cols], bias fp32, out (fp32 or bf16) and residual
-    of one type (out may be residual, but not x). pre: bf16 or an Mx8Tensor [tokens, rows]
-    that receives x w^T + bias for linear_grad."""
+    """out = act(x w^T + bias) + residual: x bf16 or an Mx8Tensor [tokens, cols],
+    w bf16 [rows, cols], bias fp32, out (fp32 or bf16) and residual of one type (out
+    may be residual, but not x). pre: bf16 or an Mx8Tensor [tokens, rows] that
+    receives x w^T + bias for linear_grad. One launch, and one more where x is in 8
+    bits or cols is no multiple of 8."""
     here = _here()
     act = _act(activation)
     shape = w.shape
