@@ -15,8 +15,10 @@
 //
 // Where it stands: 8192 x 1280 x 5120 with gelu_tanh and an 8-bit copy 72 us (1.49
 // PFLOP/s, 68% of the tensor pipe's cycles), the gradients of the same 73 and 74 us
-// (83% and 76%; a last round of 8 and of 24 tiles on 76 pairs, and L2), the gated
-// block of 8192 x 4096 x 14336 930 and 500 us at the power cap.
+// (83% and 76%; a last round of 8 and of 24 tiles on 76 pairs, and L2). The gated block
+// of 8192 x 4096 x 14336: gate and up 930 us and down 500 in runs of milliseconds (96 and
+// 97% of the tensor pipe's cycles), 1080 and 570 in runs of seconds, where the power cap
+// lowers the clock.
 //
 // kEpiGated: the even CTA's half of B is 128 rows of the gate weight, the odd
 // CTA's the same rows of the up weight. Both CTAs' accumulators then hold g in
@@ -144,7 +146,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
         keep_chunk(p.pre2, p.pre_bulk != 0, p.pre_align, row0, t.m, col, t.n, u, scratch + 2048 + kCodes, turn);
       }
       with_act(p.act, [&](auto act) { gate_all<decltype(act)::value>(g, u); });
-      put_bf16(scratch, g);
+      put_bf16(scratch, g);   // h in bf16, as the next product's operand
       ptx::fence_async_shared();
       __syncwarp();
       if (lane == 0) {
@@ -184,7 +186,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, const GemmTarget& 
       for (int i = 0; i < 16; ++i) dh[i] = __uint_as_float(r[i]);
       if (PARTS == 2 && p.start[0] != nullptr && row < t.m) add_start(p.start[0] + row * p.start_ld + col, dh);
       with_act(p.act, [&](auto act) { gate_grad_all<decltype(act)::value>(g, u, dh); });
-      put_bf16(scratch, g);
+      put_bf16(scratch, g);   // dg, du and h in bf16, as the next products' operands
       put_bf16(scratch + 1024, dh);
       put_bf16(scratch + 2048, u);
       ptx::fence_async_shared();
@@ -492,7 +494,10 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
       if (!encode_box(&p.sk[i], kept[i]->data, q.t[0].m, mx8 ? pitch : k, pitch, mx8 ? 1 : 2, 32)) return cudaErrorInvalidValue;
   }
   // The tiles of a last round that leaves half of the pairs idle, or three quarters, are cut into as
-  // many parts. (Parts of 64 columns not where B's rows run along k: its boxes are 64 wide a CTA.)
+  // many parts (us in quarters and in halves: 4096 x 1280 -> 5120 31.3 and 32.1, 2560 x 4096 -> 4096 53.9
+  // and 55.9, 2560 x 1280 -> 4096 20.0 and 21.3; gate and up of 2048 x 8192 -> 2560 110 and 112, of 2048 x
+  // 4096 -> 5120 96 and 95). Parts of 64 columns not where B's rows run along the output's columns: its
+  // boxes are 64 wide a CTA.
   const int64_t pairs = sms / 2, last = tiles % pairs;
   p.cut = last * 2 > pairs || last == 0 ? 1 : !B_MN && last * 4 <= pairs ? 4 : 2;
   p.whole = int32_t(p.cut > 1 ? tiles - last : tiles);
@@ -501,7 +506,8 @@ cudaError_t launch_pair(const Product& q, GemmParams& p, int sms, cudaStream_t s
   // gelu_tanh and an 8-bit copy, 768 -> 3200: 48 us, with sixteen 37; 1280 -> 5120: 75 and 70). Long ones:
   // the sixteen's waiting and the stage they cost are more than they give (1600 -> 6400: 107 and 109; 2048
   // -> 8192: 168 and 176; gated block 8192 x 4096 x 14336: 1775 and 1850). Where sums only go out in bf16 it
-  // turns earlier (768 -> 3200: 28 and 28; 1280 -> 5120: 57 and 60). Gate and up take more registers than
+  // turns earlier (768 -> 3200: 28 and 28; 1280 -> 5120: 57 and 60). (The gated block's figures here include the decoding
+  // of its checkpoints.) Gate and up take more registers than
   // sixteen warps have (8192 x 1024 x 2816, both kept: 93, with sixteen 107); their gradients do not (131
   // with sixteen, 134 with eight).
   constexpr int kMost = EPI == kEpiGated ? 8 : kMostWarps;
@@ -531,11 +537,14 @@ bool encode_operand(CUtensorMap* map, const Operand& o, uint32_t box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Few rows, or few tiles and a reduction that is worth splitting: 16 blocks of 64, and half of the other
-// kernel's tiles where they are more (us by pairs and by the other kernel: 512 x 512 over 512 6 and 8, over
-// 1024 7 and 7, over 2048 11 and 9; 1024 x 1024 over 1024 8 and 10, over 2048 12 and 11; 1024 x 2048 over
-// 2048 13 and 14, over 8192 37 and 34). Rows that are not 16-byte aligned take pairs longer to store: 777 x
-// 515 over 1024 9 and 8, with a residual 15 and 9.
+// Up to 64 rows, or few tiles and a reduction that is worth splitting: 16 blocks of 64, and half of the other
+// kernel's tiles where they are more. In us by pairs and by the other kernel:
+//   gated block of 4096 x 14336: 65 tokens 71 and 69, 100 73 and 73, 128 74 and 74, 129 80 and 98, 256 82 and 106
+//   128 tokens 4096 -> 14336 28 and 28 (65: 27 and 25), 768 -> 16384 11 and 13, 1280 -> 50304 29 and 43
+//   512 x 512 over 512 6 and 8, over 1024 7 and 7, over 2048 11 and 9; 1024 x 1024 over 1024 8 and 10, over 2048
+//   12 and 11; 1024 x 2048 over 2048 13 and 14, over 8192 37 and 34
+// Rows that are not 16-byte aligned take pairs longer to store: 777 x 515 over 1024 9 and 8, with a residual 15
+// and 9.
 bool is_narrow(const Product& q, int sms) {
   int64_t pair_tiles = 0, tiles = 0, rows = 0;
   bool odd = false;

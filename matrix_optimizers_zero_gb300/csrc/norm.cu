@@ -207,9 +207,9 @@ __device__ __forceinline__ void scaled_grad_row(float (&s)[8], const float (&dy)
 // gets there: no barrier, no registers, and enough bytes under way. With one row
 // ahead in registers the backward pass of 16384 x 4096 took 101 us.
 //
-// 16384 x 4096 bf16 with a residual, the sum and an 8-bit result: 71 us, 6.6 TB/s,
+// 16384 x 4096 bf16 with a residual, the sum and an 8-bit result: 72 us, 6.5 TB/s,
 // bound by memory. Backward from 8-bit rows with dres and dw: 77 us and 6 for the
-// join, 72% of issue slots and 68% of DRAM's rate.
+// join, 71% of issue slots and 68% of DRAM's rate.
 //
 // Rows ahead where a row takes `slot` bytes a thread: 1024 threads' in 196 KB.
 constexpr int rows_ahead(int slot) { return 192 / slot - 1 < 3 ? 192 / slot - 1 : 3; }
@@ -523,8 +523,11 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_grad_k
 
 // ------------------------------------------------------------------ other rows
 //
-// Rows that are not 16-byte aligned: elements TEAM apart, eight a thread, one row
-// ahead in registers.
+// Rows that are not 16-byte aligned: elements TEAM apart, eight a thread, in the
+// backward pass one row ahead in registers. Far from memory's rate, for its loads and
+// stores of single elements: 16384 x 4097 bf16 154 us (40 of bytes), with residual, sum
+// and 8-bit result 307 (71), its gradient 447 (59), from 8-bit rows with dres and dw 671
+// (69).
 // (2^-e, r') of a row out of range, from memory
 template <int TEAM, typename T>
 __device__ __noinline__ float2 scaled_odd_row(const T* x, const T* res, int64_t dim, float eps, float (&shared)[2][64]) {
@@ -707,7 +710,9 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const __gri
 }
 
 // Rows that do not fit a team's registers: a block reads them twice, the second
-// time from L2.
+// time from L2 or nearer. 8192 x 12288 bf16 81 us (59 of bytes), with residual, sum and
+// 8-bit result 114 (89), its gradient 168 (89), from 8-bit rows with dres and dw 242 (104):
+// two passes with nothing loaded ahead, and dw through shared memory once a row.
 constexpr int kLong = 512;
 
 template <typename T>
@@ -989,7 +994,7 @@ __global__ void __launch_bounds__(kLong) norm_grad_long_vec_kernel(const __grid_
 int team_of(int64_t dim) { return dim <= 256 ? 32 : dim <= 1024 ? 128 : dim <= 2048 ? 256 : dim <= 4096 ? 512 : dim <= 8192 ? 1024 : 0; }
 
 // Teams of the backward pass: 1024 threads an SM, on 152 SMs (a number that does
-// not depend on the device, as results must not).
+// not depend on the device, so that the sums' order does not either).
 int64_t grad_teams(int64_t rows, int64_t dim) {
   const int team = team_of(dim);
   return std::min<int64_t>(rows, 152 * (team == 0 ? 2 : 1024 / team));
