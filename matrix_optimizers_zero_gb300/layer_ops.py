@@ -77,11 +77,12 @@ class Mx8Tensor:
         if self.codes.get_device() != self.scales.get_device():
             raise ValueError("codes and scales must be on one device")
         self.device_index = self.codes.get_device()
-        self.arg = MoTensor(self.codes.data_ptr(), self.scales.data_ptr(), MO_MX8)
+        self.at, self.scales_at = self.codes.data_ptr(), self.scales.data_ptr()
+        self.arg = MoTensor(self.at, self.scales_at, MO_MX8)
 
     def address(self) -> MoTensor:
         """mo_tensor of the storage where it is now: codes or scales may have been replaced or moved."""
-        if self.codes.data_ptr() != (self.arg.data or 0) or self.scales.data_ptr() != (self.arg.scales or 0):
+        if self.codes.data_ptr() != self.at or self.scales.data_ptr() != self.scales_at:
             self._look()
         return self.arg
 
