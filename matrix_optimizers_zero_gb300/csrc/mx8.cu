@@ -351,8 +351,9 @@ __device__ __forceinline__ void act_grad_rows_odd(const ActGradParams& p, int64_
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float value;
-      if constexpr (ACT != MO_ACT_NONE) d[i] *= act_slope<ACT>(z[i], &value);
-      sum[i] += d[i];
+      // (one rounding each, as in the pairs above: with and without dz the sums are the same)
+      if constexpr (ACT != MO_ACT_NONE) d[i] = __fmul_rn(d[i], act_slope<ACT>(z[i], &value));
+      sum[i] = __fadd_rn(sum[i], d[i]);
       if (p.dz != nullptr && col + 32 * i < n) store1(p.dz + r * p.ld + col + 32 * i, d[i]);
     }
   }

@@ -616,7 +616,7 @@ __device__ __noinline__ void scaled_odd_grad(const NormGradParams& p, int64_t ro
     s[i] = in ? kept_value<T>(p.x, row, p.dim, c) : 0.0f;
     dy[i] = in ? load1(static_cast<const T*>(p.dy) + row * p.dim + c) : 0.0f;
     g[i] = p.weight != nullptr && in ? p.weight[c] : 1.0f;
-    squares = fmaf(s[i], s[i], squares);   // (as the row was judged: the same bits)
+    squares = fmaf(s[i], s[i], squares);   // (in the kernel's order: the same bits)
     dot = fmaf(dy[i] * g[i], s[i], dot);
   }
   const float2 sums = team_sums<TEAM>(squares, dot, shared, parity);

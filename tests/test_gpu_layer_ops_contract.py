@@ -351,3 +351,23 @@ def test_gated_input_gradient_of_a_wide_block(t, d, f, dtype):
     # roundings of a and b go either way; they are a sixteenth of their bound together (a sum of thousands): all of it is allowed
     e = ea @ wg.to(D) + eb @ wu.to(D) + (SLICE / 16 + 8) * 2.0 ** -23 * 1.01 * want
     within(f64(dx[rows]), f64(want), f64(e + ROUND[dtype] * (want + e)))
+
+
+# ---------------------------------------------------------------- one output at a time
+
+@pytest.mark.parametrize("t,k,n,activation,pre", [(512, 2, 3082, "silu", "bf16"), (973, 312, 2421, "gelu_tanh", "bf16"), (2560, 8, 2346, "gelu", "mx8"),
+                                                  (600, 8, 2344, "gelu", "bf16")])
+def test_a_bias_gradient_does_not_depend_on_what_else_is_wanted(t, k, n, activation, pre):
+    """Several rows a warp, of widths that are and are no multiples of 8."""
+    x, w, dout, z = data(t, k), data(n, k, seed=1, std=k ** -0.5), data(t, n, seed=5), data(t, n, seed=6, std=1.5)
+    if pre == "mx8":
+        q = empty8(t, n)
+        mo.mx8_quantize(z, q)
+        z = q
+    ws = mo.linear_workspace(t, k, n, grad=True)
+    got = []
+    for more in (dict(), dict(dx=torch.empty(t, k, device=dev())), dict(dw=torch.empty(n, k, device=dev()))):
+        got.append(torch.empty(n, device=dev()))
+        mo.linear_grad(dout, x, w, dbias=got[-1], activation=activation, pre=z, workspace=ws, **more)
+    clean()
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
