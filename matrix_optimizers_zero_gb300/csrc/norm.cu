@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kBlock<TEAM>, 1024 / kBlock<TEAM>) norm_grad_k
 // Rows that are not 16-byte aligned: elements TEAM apart, eight a thread, in the
 // backward pass one row ahead in registers. Far from memory's rate, for its loads and
 // stores of single elements: 16384 x 4097 bf16 154 us (40 of bytes), with residual, sum
-// and 8-bit result 307 (71), its gradient 447 (59), from 8-bit rows with dres and dw 671
+// and 8-bit result 307 (71), its gradient 445 (59), from 8-bit rows with dres and dw 566
 // (69).
 // (2^-e, r') of a row out of range, from memory
 template <int TEAM, typename T>
@@ -640,7 +640,8 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const __gri
   ptx::griddep_wait();
   constexpr int kTeams = kBlock<TEAM> / TEAM;
   const int t = int(threadIdx.x) % TEAM;
-  const int64_t team = int64_t(blockIdx.x) * kTeams + int(threadIdx.x) / TEAM, step = int64_t(gridDim.x) * kTeams;
+  const int team = int(blockIdx.x) * kTeams + int(threadIdx.x) / TEAM, step = int(gridDim.x) * kTeams;
+  const int rows = int(p.rows);   // (2^30 at most; 64-bit counters cost registers that rows are kept in)
   const int64_t nb = (p.dim + 31) / 32;
   float w[8], dw[8];
 #pragma unroll
@@ -671,7 +672,7 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const __gri
   if (team < p.rows) fetch(team);
   bool again = false;   // there are rows out of range
   int parity = 0;
-  for (int64_t row = team; row < p.rows; row += step, parity ^= 1) {
+  for (int row = team; row < rows; row += step, parity ^= 1) {
     float s[8], dy[8], res[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const __gri
       else
         s[i] = load1(&next_x[i]);
     }
-    if (row + step < p.rows) fetch(row + step);
+    if (row + step < rows) fetch(row + step);
     float squares = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -692,18 +693,17 @@ __global__ void __launch_bounds__(kBlock<TEAM>) norm_grad_odd_kernel(const __gri
     const float2 sums = team_sums<TEAM>(squares, dot, shared, parity);
     const float mean = fmaf(sums.x, inv_dim, p.eps);
     float r = inverse_sqrt(mean), m = sums.y * r * inv_dim;
-    const bool fits = usual(mean, m);
-    if (!fits) r = m = 0.0f;   // (adds nothing to dw, and is not stored: dx may be dy)
+    if (!usual(mean, m)) r = m = 0.0f;   // (adds nothing to dw, and is not stored: dx may be dy)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float n = s[i] * r;
       dw[i] = fmaf(dy[i], n, dw[i]);
       dy[i] = r * fmaf(-n, m, dy[i] * w[i]) + res[i];
     }
-    if (fits) store_row<TEAM>(static_cast<T*>(p.dx) + row * p.dim, p.dim, t, dy);
-    again = again || !fits;
+    if (r != 0.0f) store_row<TEAM>(static_cast<T*>(p.dx) + int64_t(row) * p.dim, p.dim, t, dy);
+    again = again || r == 0.0f;
   }
-  float* part = p.part != nullptr ? p.part + team * p.dim : nullptr;
+  float* part = p.part != nullptr ? p.part + int64_t(team) * p.dim : nullptr;
   if (part != nullptr) store_row<TEAM>(part, p.dim, t, dw);
   if (again)
     for (int64_t row = team; row < p.rows; row += step, parity ^= 1) scaled_odd_grad<TEAM, T>(p, row, part, shared, parity);
