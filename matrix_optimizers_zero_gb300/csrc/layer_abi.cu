@@ -38,8 +38,8 @@ int matrix_shape(int64_t rows, int64_t k) {
 
 // Memory that a call touches; a range that is written may overlap no other, but
 // be one that it was given to replace. Operands of a product are read whole, by
-// tiles that write other places: the product's output replaces none of them,
-// whatever else was given at the same address.
+// tiles that write other places, and a norm's weight is read by every row: an output
+// replaces none of them, whatever else was given at the same address.
 struct Range {
   const void* p;
   size_t bytes;
@@ -332,7 +332,7 @@ int rms_norm(const void* x, const void* residual, int32_t dtype, int64_t rows, i
   Ranges mem;
   mem.reads(x, n * bytes_of(dtype));
   mem.reads(residual, n * bytes_of(dtype));
-  mem.reads(weight, size_t(dim) * 4);
+  mem.operand(weight, size_t(dim) * 4);
   mem.writes(sum, n * bytes_of(dtype), x, residual);
   mem.writes(out, n * bytes_of(out_dtype), x, residual);
   mem.kept(out8, rows, dim, true);
@@ -389,7 +389,7 @@ int rms_norm_grad(const void* dy, int32_t dtype, const mo_tensor* x, int64_t row
   Ranges mem;
   mem.reads(dy, n);
   mem.kept(x, rows, dim, false);
-  mem.reads(weight, size_t(dim) * 4);
+  mem.operand(weight, size_t(dim) * 4);
   mem.reads(dresidual, n);
   mem.writes(dx, n, dy, dresidual);
   mem.writes(dweight, size_t(dim) * 4);

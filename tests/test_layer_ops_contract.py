@@ -89,6 +89,14 @@ def test_a_gated_block_does_not_replace_its_weights(lib, w):
     assert lib.gated_ffn_forward(ref(ten(E)), a["wg"], a["wu"], a["wd"], t, d, f, 4, A, None, None, A, BF16, F, BIG, None) == OVERLAP
 
 
+def test_a_norm_does_not_replace_its_weight(lib):
+    """One row of fp32 is as long as the weight."""
+    assert lib.rms_norm(A, None, F32, 1, 40, A, 1e-6, None, A, F32, None, None) == OVERLAP
+    assert lib.rms_norm(A, B, F32, 1, 40, B, 1e-6, B, C, F32, None, None) == OVERLAP
+    x = MoTensor(B, None, F32)
+    assert lib.rms_norm_grad(A, F32, ref(x), 1, 40, A, 1e-6, None, A, None, 0, None, 0, None) == OVERLAP
+
+
 def test_in_place_calls_pass_the_checks(lib):
     """What is read and written by the same threads, or by different launches, is no overlap: these calls go on
     to the device."""
